@@ -431,3 +431,9 @@ def selftest_bounded_wait(arrive, device=None, stream=None):
     tsv_selftest_bounded_wait(handle(dev.index), arrive, st, ns, stream)
     torch.cuda.synchronize(dev)
     return int(st.item()), ns.item() * 1e-9
+
+
+# The paged 8-bit cache (include/tsv_paged.h).
+from .paged import (PAGED_EXPORTED, PagedCache, paged_append, paged_commit, paged_tree_attention,  # noqa: E402,F401
+                    paged_tree_attention_workspace, rope, rope_frequencies)
+from . import paged  # noqa: E402,F401

@@ -13,24 +13,6 @@
 
 using namespace tsv;
 
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
-                                  const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                                  const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-struct tsv_handle_s {
-  int device;
-  int num_sms;
-  EncodeTiledFn encode;
-  bool tc_attr_set[2];    // rows-on-lanes kernel (tile pairs), D = 64, 128
-  bool tc1_attr_set[2];   // rows-on-lanes kernel (one tile), D = 64, 128
-  bool keys_attr_set[2];  // keys-on-lanes kernel, D = 64, 128
-  bool mss_attr_set;      // MSS kernel's shared-memory limit
-  size_t mss_staged_limit;
-  int mss_max_clusters[kMssClusterSizes];  // resident MSS clusters of each size
-  uint32_t verify_overlap;  // tsv_set_verify_overlap: TSV_OVERLAP_* flags
-};
-
 namespace {
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
@@ -322,6 +304,7 @@ tsv_status tsv_create(tsv_handle* out, int device) {
   h->mss_attr_set = false;
   h->mss_staged_limit = 0;
   h->verify_overlap = 0u;
+  h->paged_attr_mask = h->append_attr_mask = 0u;
   *out = h;
   return TSV_OK;
 }

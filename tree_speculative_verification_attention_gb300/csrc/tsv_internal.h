@@ -8,6 +8,29 @@
 #include <stdint.h>
 
 #include "../../include/tsv.h"
+#include "../../include/tsv_paged.h"
+
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                  const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                  const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+constexpr int kMssClusterSizeEntries = 9;  // entries of the resident-cluster table (sizes 0..8)
+
+struct tsv_handle_s {
+  int device;
+  int num_sms;
+  EncodeTiledFn encode;
+  bool tc_attr_set[2];    // rows-on-lanes kernel (tile pairs), D = 64, 128
+  bool tc1_attr_set[2];   // rows-on-lanes kernel (one tile), D = 64, 128
+  bool keys_attr_set[2];  // keys-on-lanes kernel, D = 64, 128
+  bool mss_attr_set;      // MSS kernel's shared-memory limit
+  size_t mss_staged_limit;
+  int mss_max_clusters[kMssClusterSizeEntries];  // resident MSS clusters of each size
+  uint32_t verify_overlap;  // tsv_set_verify_overlap: TSV_OVERLAP_* flags
+  uint32_t paged_attr_mask;   // paged attention kernels whose attributes are set, one bit per (D, tile rows)
+  uint32_t append_attr_mask;  // paged append kernels, one bit per (type, D)
+};
 
 namespace tsv {
 
@@ -167,7 +190,7 @@ inline size_t greedy_workspace_bytes(int32_t B, int32_t N) {
 // kMssBesideFull start beside it (two-warp CTAs that fit next to an attention
 // CTA, or the full-size CTAs on SMs it leaves free) and complete after it.
 // `room`: the full-size CTAs leave registers for a greedy CTA beside each.
-constexpr int kMssClusterSizes = 9;  // entries of the resident-cluster table (sizes 0..8)
+constexpr int kMssClusterSizes = kMssClusterSizeEntries;
 constexpr int kMssBesideCompact = 1, kMssBesideFull = 2;
 // Largest cluster of the full-size CTAs beside a running kernel: a cluster
 // needs that many idle SMs in one GPC, which a running grid seldom leaves
@@ -207,5 +230,64 @@ cudaError_t launch_kv_commit(uint8_t* k, uint8_t* v, int64_t sb, int64_t sl, int
                              const int32_t* node_offsets, const int32_t* path,
                              const int32_t* accept_len, int32_t* new_len, int32_t* status,
                              cudaStream_t st);
+
+// Rotary positions (tsv_rope).
+struct RopeArgs {
+  const void* x;
+  void* y;
+  int64_t xs_n, xs_h, ys_n, ys_h;  // elements
+  int32_t N, H, D, rot;
+  const int32_t* positions;
+  const double* inv_freq;
+  float amplitude;
+  int32_t interleaved, inverse;
+};
+cudaError_t launch_rope(const RopeArgs& a, bool bf16, int num_sms, cudaStream_t st);
+
+// New rows of a paged cache (tsv_paged_append and tsv_paged_commit).
+struct PagedWriteArgs {
+  tsv_paged_cache cache;
+  tsv_page_table table;       // pages written
+  const int32_t* start;       // [B] rows kept in front of the new ones, NULL: 0
+  const int32_t* offsets;     // [B+1] rows of k / v (append) or of path (commit)
+  int32_t B, N, max_rows;     // max_rows: new rows of one request at most
+  int32_t head_loop;          // head groups that one CTA takes in turn
+  int32_t* status;
+  // append
+  const void* k;
+  const void* v;
+  int64_t ks_n, ks_h, vs_n, vs_h;
+  const int32_t* positions;
+  const double* inv_freq;     // NULL: no rotation
+  int32_t rot, interleaved;
+  float amplitude;
+  // commit
+  tsv_page_table tree_table;  // pages read
+  const int32_t* path;
+  const int32_t* accept_len;
+  int32_t* new_len;
+};
+size_t paged_append_smem_bytes(int32_t page_size, int32_t rot);
+constexpr int kPagedWriteWarps = 8;  // a warp takes 16 rows of one (page, head)
+cudaError_t paged_append_set_attributes(bool bf16, int32_t D);
+cudaError_t launch_paged_append(const PagedWriteArgs& a, bool bf16, cudaStream_t st);
+cudaError_t launch_paged_commit(const PagedWriteArgs& a, cudaStream_t st);
+
+// Tree attention over a paged cache.
+struct PagedAttnArgs {
+  const void* q;
+  int64_t qs_n, qs_h;
+  tsv_paged_cache cache;
+  tsv_page_table table;
+  tsv_page_table tree_table;  // ids_d NULL: no tree keys
+  const int32_t* prefix_len;
+  const int32_t* offsets;
+  const uint32_t* anc;
+  void* out;
+  int32_t* status;
+  int32_t B, N, max_nodes, Hq, G;
+  float scale;
+};
+cudaError_t launch_paged_attention_simt(const PagedAttnArgs& a, bool bf16, cudaStream_t st);
 
 }  // namespace tsv
