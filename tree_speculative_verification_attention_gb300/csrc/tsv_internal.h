@@ -288,6 +288,23 @@ struct PagedAttnArgs {
   int32_t B, N, max_nodes, Hq, G;
   float scale;
 };
+// Tensor-core kernel: row tiles of R = 16, 32 or 64 query rows; its workspace
+// holds one completion counter per CTA, then two partial results per CTA (O
+// [R][D], then maxima and sums [2][R]).
+inline int32_t paged_attn_rows(int64_t rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
+struct PagedAttnLayout {
+  size_t part_o, part_ml, total;
+};
+inline PagedAttnLayout paged_attn_layout(int grid, int32_t R, int32_t D) {
+  PagedAttnLayout l;
+  l.part_o = ((size_t)grid * 4 + 255) & ~(size_t)255;
+  l.part_ml = l.part_o + (size_t)grid * 2 * R * D * 4;
+  l.total = l.part_ml + (size_t)grid * 2 * 2 * R * 4;
+  return l;
+}
+cudaError_t paged_attention_set_attributes(int32_t D, int32_t R);
+cudaError_t launch_paged_attention(const CUtensorMap& tk, const CUtensorMap& tv, const PagedAttnArgs& a, int32_t R, int grid,
+                                   void* ws, cudaStream_t st);
 cudaError_t launch_paged_attention_simt(const PagedAttnArgs& a, bool bf16, cudaStream_t st);
 
 }  // namespace tsv

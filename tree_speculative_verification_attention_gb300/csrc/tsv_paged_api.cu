@@ -74,6 +74,20 @@ tsv_status check_attention(tsv_handle h, tsv_dtype dtype, const tsv_paged_cache*
   return TSV_OK;
 }
 
+// One KV head's rows of a page as a box of a 4-D map (D, Hkv, rows, pages).
+tsv_status encode_pages(tsv_handle h, CUtensorMap* map, const void* base, const tsv_paged_cache& c) {
+  const cuuint64_t dims[4] = {(cuuint64_t)c.D, (cuuint64_t)c.Hkv, (cuuint64_t)c.page_size, (cuuint64_t)c.num_pages};
+  const cuuint64_t strides[3] = {(cuuint64_t)c.stride_head, (cuuint64_t)c.stride_row, (cuuint64_t)c.stride_page};
+  const cuuint32_t box[4] = {(cuuint32_t)c.D, 1, (cuuint32_t)c.page_size, 1};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  const CUresult r = h->encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(base), dims, strides, box, estr,
+                               CU_TENSOR_MAP_INTERLEAVE_NONE, c.D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? TSV_OK : TSV_ERR_INVALID_ARG;
+}
+
+bool paged_uses_tc(tsv_dtype dtype, uint32_t flags) { return dtype == TSV_BF16 && !(flags & TSV_ATTN_SIMT); }
+
 // Head groups that one CTA of an append or commit takes in turn: as many as
 // leave 4 CTAs per SM.  A CTA computes its page's angles once, so fewer, longer
 // CTAs save work as soon as the grid fills the machine.
@@ -210,7 +224,8 @@ tsv_status tsv_paged_tree_attention_workspace_size(tsv_handle h, tsv_dtype dtype
   if (!bytes) return TSV_ERR_INVALID_ARG;
   const tsv_status st = check_attention(h, dtype, cache, &c, B, max_nodes, Hq, flags);
   if (st != TSV_OK) return st;
-  *bytes = 0;
+  const int32_t R = paged_attn_rows((int64_t)max_nodes * (Hq / c.Hkv));
+  *bytes = paged_uses_tc(dtype, flags) ? paged_attn_layout(h->num_sms, R, c.D).total : 0;
   return TSV_OK;
 }
 
@@ -233,8 +248,11 @@ tsv_status tsv_paged_tree_attention(tsv_handle h, tsv_dtype dtype, const void* q
   if (N > 0 && (!q_d || !out_d || !aligned16(out_d) || !rows_aligned(q_d, q_stride_n, q_stride_h, esz)))
     return TSV_ERR_INVALID_ARG;
   if ((int64_t)N * Hq > INT32_MAX) return TSV_ERR_UNSUPPORTED;
-  (void)workspace_d;
-  (void)workspace_bytes;
+  const bool use_tc = paged_uses_tc(dtype, flags);
+  const int32_t R = paged_attn_rows((int64_t)max_nodes * (Hq / a.cache.Hkv));
+  if (use_tc && (!workspace_d || !aligned16(workspace_d) ||
+                 workspace_bytes < paged_attn_layout(h->num_sms, R, a.cache.D).total))
+    return TSV_ERR_INVALID_ARG;
   const DeviceScope scope(h->device);
   if (!scope.ok) return TSV_ERR_CUDA;
   a.q = q_d;
@@ -253,6 +271,18 @@ tsv_status tsv_paged_tree_attention(tsv_handle h, tsv_dtype dtype, const void* q
   a.Hq = Hq;
   a.G = Hq / a.cache.Hkv;
   a.scale = scale == 0.f ? 1.f / sqrtf((float)a.cache.D) : scale;
+  if (use_tc) {
+    CUtensorMap tk, tv;
+    st = encode_pages(h, &tk, a.cache.k_d, a.cache);
+    if (st == TSV_OK) st = encode_pages(h, &tv, a.cache.v_d, a.cache);
+    if (st != TSV_OK) return st;
+    const uint32_t bit = 1u << ((R == 16 ? 0 : R == 32 ? 1 : 2) + (a.cache.D == 128 ? 3 : 0));
+    if (!(h->paged_attr_mask & bit)) {
+      if (paged_attention_set_attributes(a.cache.D, R) != cudaSuccess) return TSV_ERR_CUDA;
+      h->paged_attr_mask |= bit;
+    }
+    return cuda_status(launch_paged_attention(tk, tv, a, R, h->num_sms, workspace_d, static_cast<cudaStream_t>(stream)));
+  }
   return cuda_status(launch_paged_attention_simt(a, dtype == TSV_BF16, static_cast<cudaStream_t>(stream)));
 }
 

@@ -1,0 +1,992 @@
+// tsv_paged_attention.cu — tree attention over a paged 8-bit cache on the
+// tensor cores, keys on the TMEM lanes.
+//
+//   S^T = K Q^T       M = 128 keys, N = rows, K = D      (A = K tile, B = Q tile)
+//   O^T = V^T P^T     M = 128 (d), N = 2 x rows, K = 128 keys (A = V tile, M-major)
+//
+// Both products run on the e4m3 codes themselves, straight from the bytes that
+// TMA brings in: nothing is widened on the way, so a 128-key block of one head
+// costs 32 KB of shared memory and of HBM traffic, which is the bound while a
+// KV head has few query rows.  The operands that are not e4m3 are split:
+//   q = (hi + lo) 2^-k   two e4m3 terms under a power of two per row (the
+//                        row's largest value lands in [128, 256)): a bf16's 8
+//                        bits exactly down to 2^-17 of the row's largest.
+//                        Both terms accumulate into the same S.
+//   p = (hi + lo / 16) / 256   relative to the block's own largest score of
+//                        the row: 8 bits down to 2^-14 of it, never off by more
+//                        than 2^-22 of it.  hi and lo sit side by side on
+//                        the N axis of one MMA and are added in fp32.
+// That the reference maximum is the block's own (not a running one) keeps
+// those bounds whatever the earlier blocks held; O of a block is brought to
+// the running maximum in fp32 registers, which also keeps long sums out of the
+// tensor core's accumulator.  The scale of a key's page multiplies S, and the
+// scale of its V page, relative to the block's largest, multiplies P.
+//
+// Work.  The 128-key blocks of all (request, KV head, row tile) groups form one
+// list, cut into equal ranges, one per CTA (one CTA per SM): every SM gets the
+// same number of blocks whatever the lengths, which the kernel reads from the
+// device.  A group that a cut goes through leaves fp32 partials in the
+// workspace, and the last of its CTAs to arrive joins them in a fixed order.
+//
+// Roles (16 warps): two softmax warpgroups taking alternate blocks (warps 0-3
+// and 4-7; a thread owns a key), the accumulating warpgroup (8-11; a thread
+// owns a d), the TMA producer (12: page ids and scales are looked up two
+// blocks ahead), the MMA issuer (13), and two warps that prepare the next
+// unit's Q tiles and tree mask (14, 15).
+//
+// Tail and tree blocks: V rows past the last key are zeroed in shared memory
+// and NaN codes of tree rows are taken out of the product and put back only
+// into the rows that see them, so that 0 x NaN reaches nobody.
+#include "tsv_attention_common.cuh"
+#include "tsv_paged_common.cuh"
+
+namespace tsv {
+
+namespace {
+
+constexpr int kPThreads = 512;
+constexpr int kPProducerWarp = 12, kPMmaWarp = 13, kPPrepWarp = 14;
+constexpr int kPBlock = 128;      // keys of a block
+constexpr int kBarSoft = 1;       // and 2: one per softmax warpgroup
+constexpr int kBarAcc = 3, kBarPrep = 4;
+
+template <int D, int R>
+struct PCfg {
+  static constexpr int kRowBytes = D;                       // one key, one head
+  static constexpr int kTile = kPBlock * D;                 // K tile
+  static constexpr int kVTile = kPBlock * 128;              // 128 d; the upper half stays zero when D = 64
+  static constexpr int kStage = kTile + kVTile;
+  static constexpr int kStages = D == 128 ? 4 : 6;
+  static constexpr int kQ = R * D;                          // one term of a Q tile
+  static constexpr int kOffStage = 0;
+  static constexpr int kOffP = kOffStage + kStages * kStage;       // [2][128 keys][128 B]
+  static constexpr int kOffQ = kOffP + 2 * kPBlock * 128;          // [2][hi, lo]
+  static constexpr int kOffDesc = kOffQ + 4 * kQ;                  // u32 [2][256 keys][2]: rows that see the tree key
+  static constexpr int kOffPoison = kOffDesc + 2 * 256 * 8;        // u64 [2][128 d]: rows that see a NaN there
+  static constexpr int kOffCum = kOffPoison + 2 * 128 * 8;         // i64 [TSV_MAX_BATCH + 1]
+  static constexpr int kOffReq = kOffCum + 8 * (TSV_MAX_BATCH + 2);  // int4 [TSV_MAX_BATCH]: off, n, P, blocks
+  static constexpr int kOffFr = kOffReq + 16 * TSV_MAX_BATCH;      // f32 [2][R]: score factor of a row
+  static constexpr int kOffRow = kOffFr + 8 * R;                   // i32 [2][R]: output row
+  static constexpr int kOffWmax = kOffRow + 8 * R;                 // f32 [8 warps][R]
+  static constexpr int kOffM = kOffWmax + 32 * R;                  // f32 [2][R]: a block's largest scores
+  static constexpr int kOffAl = kOffM + 8 * R;                     // f32 [2][R]
+  static constexpr int kOffBe = kOffAl + 8 * R;                    // f32 [2][R]
+  static constexpr int kOffAB = kOffBe + 8 * R;                    // f32 [2][2][R]: accumulating group's factors
+  static constexpr int kOffL = kOffAB + 16 * R;                    // f32 [2][8 warps][R]
+  static constexpr int kOffMw = kOffL + 64 * R;                    // f32 [2][2][R]
+  static constexpr int kOffFin = kOffMw + 16 * R;                  // f32 [2][R]: sums of a unit
+  static constexpr int kOffScale = kOffFin + 8 * R;                // f32 [stages][K 8, V 8]
+  static constexpr int kOffSv = kOffScale + kStages * 64;          // f32 [2]
+  static constexpr int kOffBar = (kOffSv + 8 + 7) & ~7;
+  // kv_full[S], kv_empty[S], s_full[2], p_full[2], o_full[2], o_free[2], q_full[2], unit_free[2], l_full[2], mma_done
+  static constexpr int kBars = 2 * kStages + 15;
+  static constexpr int kOffMisc = kOffBar + 8 * kBars;
+  static constexpr int kSmem = kOffMisc + 64 + 1024;
+  static constexpr uint32_t kCols = R == 64 ? 512 : R == 32 ? 256 : 128;  // S0 S1 (R each) O0 O1 (2 R each)
+  static_assert(kSmem <= 227 * 1024, "shared memory");
+  static_assert(kStage % 1024 == 0 && kQ % 512 == 0 && kOffQ % 1024 == 0, "swizzle atoms");
+};
+
+// Swizzled position of 16-byte chunk c of row r in a tile of ROW-byte rows.
+template <int ROW>
+__device__ __forceinline__ uint32_t swz(int r, int c) {
+  return ROW == 128 ? (uint32_t)(r * 128 + ((c ^ (r & 7)) << 4)) : (uint32_t)(r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
+}
+
+__device__ __forceinline__ void umma_e4m3(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                          uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// Instruction descriptor of kind::f8f6f4: e4m3 A and B (format 0), fp32 D.
+__device__ __forceinline__ uint32_t idesc_e4m3(int M, int N, int a_mn, int b_mn) {
+  return (1u << 4) | ((uint32_t)a_mn << 15) | ((uint32_t)b_mn << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+// Descriptor of a tile with 128- or 64-byte rows, swizzled over its rows' width.
+template <int ROW>
+__device__ __forceinline__ uint64_t sdesc_row(uint32_t saddr, uint32_t lbo) {
+  uint64_t d = sdesc_sw128(saddr, lbo, 8 * ROW);
+  if (ROW == 64) d = (d & ~(7ull << 61)) | (4ull << 61);
+  return d;
+}
+
+__device__ __forceinline__ void mbar_expect_tx(uint64_t* bar, uint32_t bytes) {
+  asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes) : "memory");
+}
+
+// 16 lanes x 256 bits, repeated over R columns: thread t holds, of lanes t / 4
+// and t / 4 + 8, columns 8 i + 2 (t % 4) and the next, in v[4 i ..] (two of the
+// first lane, two of the second).
+template <int R>
+__device__ __forceinline__ void tmem_ld_16x256(uint32_t taddr, float (&v)[R / 2]) {
+  uint32_t r[R / 2];
+  if constexpr (R == 16) {
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr) : "memory");
+  } else if constexpr (R == 32) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr) : "memory");
+  } else {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x8.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr) : "memory");
+  }
+  asm volatile("tcgen05.wait::ld.sync.aligned;\n" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < R / 2; ++i) {
+    asm volatile("" : "+r"(r[i])::"memory");  // no use before the wait
+    v[i] = __uint_as_float(r[i]);
+  }
+}
+
+// One unit of a CTA's range: blocks j .. j1 - 1 of a (request, KV head, row
+// tile) group of T blocks, nmain of them over prefix rows.  gx is the place of
+// the group's block 0 in the list of all blocks.
+struct PUnit {
+  int b, g, tile, tiles, off, n, P, nmain, T, j, j1;
+  int64_t gx;
+  bool valid;
+  __device__ __forceinline__ bool whole() const { return j == 0 && j1 == T; }
+};
+
+struct PList {
+  const int64_t* cum;
+  const int4* req;
+  int B, G, Hkv, R;
+  bool tree;
+  int64_t x1;  // end of this CTA's range
+
+  __device__ __forceinline__ void request(PUnit& u) const {
+    const int4 q = req[u.b];
+    u.off = q.x;
+    u.n = q.y;
+    u.P = q.z;
+    u.T = q.w;
+    u.nmain = (u.P + kPBlock - 1) / kPBlock;
+    u.tiles = (u.n * G + R - 1) / R;
+  }
+  __device__ __forceinline__ PUnit first(int64_t x0) const {
+    PUnit u{};
+    u.valid = x0 < x1;
+    if (!u.valid) return u;
+    while (cum[u.b + 1] <= x0) ++u.b;
+    request(u);
+    const int64_t rel = x0 - cum[u.b];
+    const int group = (int)(rel / u.T);
+    u.j = (int)(rel - (int64_t)group * u.T);
+    u.g = group / u.tiles;
+    u.tile = group - u.g * u.tiles;
+    u.gx = x0 - u.j;
+    u.j1 = (int)min((int64_t)u.T, x1 - u.gx);
+    return u;
+  }
+  __device__ __forceinline__ void next(PUnit& u) const {
+    u.gx += u.T;
+    u.valid = u.gx < x1;
+    if (!u.valid) return;
+    if (++u.tile == u.tiles) {
+      u.tile = 0;
+      if (++u.g == Hkv) {
+        u.g = 0;
+        do ++u.b;
+        while (cum[u.b + 1] == cum[u.b]);
+        request(u);
+      }
+    }
+    u.j = 0;
+    u.j1 = (int)min((int64_t)u.T, x1 - u.gx);
+  }
+};
+
+// A wait that ran out (or saw another role's) leaves the thread `dead`: it goes
+// through the motions without waiting, so that named barriers stay complete.
+#define TSV_PWAIT(bar, parity)                                             \
+  do {                                                                     \
+    if (!dead && !mbar_wait((bar), (uint32_t)(parity) & 1u, abort_v)) dead = true; \
+    __syncwarp();                                                          \
+  } while (0)
+
+template <int D, int R>
+__global__ void __launch_bounds__(kPThreads, 1)
+    paged_attn_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
+                      const __grid_constant__ PagedAttnArgs a, int32_t* __restrict__ counters,
+                      float* __restrict__ part_o, float* __restrict__ part_ml) {
+  using C = PCfg<D, R>;
+  constexpr int S = C::kStages;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sStage = smem + C::kOffStage;
+  uint8_t* sP = smem + C::kOffP;
+  uint8_t* sQ = smem + C::kOffQ;
+  uint32_t* sDesc = reinterpret_cast<uint32_t*>(smem + C::kOffDesc);
+  unsigned long long* sPoison = reinterpret_cast<unsigned long long*>(smem + C::kOffPoison);
+  int64_t* sCum = reinterpret_cast<int64_t*>(smem + C::kOffCum);
+  int4* sReq = reinterpret_cast<int4*>(smem + C::kOffReq);
+  float* sFr = reinterpret_cast<float*>(smem + C::kOffFr);
+  int32_t* sRow = reinterpret_cast<int32_t*>(smem + C::kOffRow);
+  float* sWmax = reinterpret_cast<float*>(smem + C::kOffWmax);
+  float* sM = reinterpret_cast<float*>(smem + C::kOffM);
+  float* sAl = reinterpret_cast<float*>(smem + C::kOffAl);
+  float* sBe = reinterpret_cast<float*>(smem + C::kOffBe);
+  float* sAB = reinterpret_cast<float*>(smem + C::kOffAB);
+  float* sL = reinterpret_cast<float*>(smem + C::kOffL);
+  float* sMw = reinterpret_cast<float*>(smem + C::kOffMw);
+  float* sFin = reinterpret_cast<float*>(smem + C::kOffFin);
+  float* sScale = reinterpret_cast<float*>(smem + C::kOffScale);
+  float* sSv = reinterpret_cast<float*>(smem + C::kOffSv);
+  uint64_t* kv_full = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
+  uint64_t* kv_empty = kv_full + S;
+  uint64_t* s_full = kv_empty + S;
+  uint64_t* p_full = s_full + 2;
+  uint64_t* o_full = p_full + 2;
+  uint64_t* o_free = o_full + 2;
+  uint64_t* q_full = o_free + 2;
+  uint64_t* unit_free = q_full + 2;
+  uint64_t* l_full = unit_free + 2;
+  uint64_t* mma_done = l_full + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
+  int* abort_flag = reinterpret_cast<int*>(smem + C::kOffMisc + 4);
+  int* sPoisoned = reinterpret_cast<int*>(smem + C::kOffMisc + 8);   // [2]
+  int* sJoin = reinterpret_cast<int*>(smem + C::kOffMisc + 16);
+  int64_t* sTot = reinterpret_cast<int64_t*>(smem + C::kOffMisc + 24);  // [4]
+  volatile int* abort_v = abort_flag;
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int ps = a.cache.page_size;
+  const bool tree = a.tree_table.ids_d != nullptr;
+  bool dead = false;
+
+  if (tid == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(&kv_full[s], 1);
+      mbar_init(&kv_empty[s], 1);
+    }
+    for (int x = 0; x < 2; ++x) {
+      mbar_init(&s_full[x], 1);
+      mbar_init(&p_full[x], 128);
+      mbar_init(&o_full[x], 1);
+      mbar_init(&o_free[x], 128);
+      mbar_init(&q_full[x], 64);
+      mbar_init(&unit_free[x], 128);
+      mbar_init(&l_full[x], 256);
+    }
+    mbar_init(mma_done, 1);
+    *abort_flag = 0;
+    sPoisoned[0] = sPoisoned[1] = 0;
+    mbar_fence_init();
+  }
+  if (warp == kPMmaWarp) {
+    tmem_alloc(tmem_slot, C::kCols);
+    tmem_relinquish();
+  }
+  if (warp == kPProducerWarp && lane == 0) {
+    tma_prefetch_desc(&tmap_k);
+    tma_prefetch_desc(&tmap_v);
+  }
+  if (D == 64) {  // the upper half of every V stage stays zero
+    for (int i = tid; i < S * (C::kVTile / 2 / 16); i += kPThreads) {
+      const int st = i / (C::kVTile / 2 / 16), o = i % (C::kVTile / 2 / 16);
+      reinterpret_cast<uint4*>(sStage + st * C::kStage + C::kTile + C::kVTile / 2)[o] = make_uint4(0u, 0u, 0u, 0u);
+    }
+    fence_proxy_async_smem();
+  }
+  if (tid < 256) sPoison[tid] = 0ull;
+  pdl_wait();  // the previous kernel's results are visible from here on
+  pdl_trigger();
+
+  // The list of blocks: request b holds T_b x Hkv x tiles of them.  A request
+  // with nothing to see still gets one (empty) block, which writes its zeros.
+  if (tid < TSV_MAX_BATCH) {
+    int64_t w = 0;
+    PagedRequest r;
+    if (tid < a.B && paged_request(a, tid, &r) && r.n > 0) {
+      const int T = max(1, (r.P + kPBlock - 1) / kPBlock + (tree ? (r.n + kPBlock - 1) / kPBlock : 0));
+      w = (int64_t)T * a.cache.Hkv * ((r.n * a.G + R - 1) / R);
+      sReq[tid] = make_int4(r.off, r.n, r.P, T);
+    }
+    int64_t sum = w;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, sum, o);
+      if (lane >= o) sum += y;
+    }
+    if (lane == 31) sTot[warp] = sum;
+    sCum[tid + 1] = sum;
+    if (tid == 0) sCum[0] = 0;
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (tid < TSV_MAX_BATCH) {
+    int64_t before = 0;
+    for (int w = 0; w < warp; ++w) before += sTot[w];
+    sCum[tid + 1] += before;
+  }
+  __syncthreads();
+  const uint32_t tmem = *tmem_slot;
+  const int64_t W = sCum[TSV_MAX_BATCH];
+  const int64_t ctas = min((int64_t)gridDim.x, W);  // that have work
+  const int64_t x0 = (int)blockIdx.x < ctas ? (int64_t)blockIdx.x * W / ctas : W;
+  PList list{sCum, sReq, a.B, a.G, a.cache.Hkv, R, tree, (int)blockIdx.x < ctas ? ((int64_t)blockIdx.x + 1) * W / ctas : W};
+
+  if (warp == kPProducerWarp) {
+    // ------------------------------------------------------------ producer
+    // Block t is issued while the page scales of block t + 1 and the page ids
+    // of block t + 2 are on their way.
+    const int per = kPBlock / ps;  // pages of a block
+    struct Look {
+      PUnit u;
+      int id;
+      float ks, vs;
+    };
+    auto block_pages = [&](const PUnit& u) {  // pages of block u.j that hold keys
+      const int keys = u.j < u.nmain ? u.P - u.j * kPBlock : tree ? u.n - (u.j - u.nmain) * kPBlock : 0;
+      return (min(keys, kPBlock) + ps - 1) / ps;
+    };
+    auto look_id = [&](Look& k) {
+      k.id = -1;
+      if (!k.u.valid || lane >= block_pages(k.u)) return;
+      const bool main = k.u.j < k.u.nmain;
+      const tsv_page_table& t = main ? a.table : a.tree_table;
+      k.id = __ldg(t.ids_d + (int64_t)k.u.b * t.stride + (main ? k.u.j : k.u.j - k.u.nmain) * per + lane);
+    };
+    auto look_scale = [&](Look& k) {
+      k.ks = k.vs = 0.f;
+      if (k.u.valid && (uint32_t)k.id < (uint32_t)a.cache.num_pages) {
+        k.ks = __ldg(a.cache.k_scale_d + (int64_t)k.id * a.cache.Hkv + k.u.g);
+        k.vs = __ldg(a.cache.v_scale_d + (int64_t)k.id * a.cache.Hkv + k.u.g);
+      }
+    };
+    auto advance = [&](Look& k) {
+      if (k.u.valid && ++k.u.j >= k.u.j1) list.next(k.u);
+    };
+    Look c0, c1, c2;
+    c0.u = list.first(x0);
+    look_id(c0);
+    c1.u = c0.u;
+    advance(c1);
+    look_id(c1);
+    look_scale(c0);
+    int t = 0, st = 0, ph = 0;
+    for (; c0.u.valid; ++t) {
+      c2.u = c1.u;
+      advance(c2);
+      look_id(c2);
+      if (t >= S) TSV_PWAIT(&kv_empty[st], ph ^ 1);
+      if (__any_sync(0xffffffffu, dead || *abort_v)) break;
+      const int pages = block_pages(c0.u);
+      uint8_t* kt = sStage + st * C::kStage;
+      uint8_t* vt = kt + C::kTile;
+      if (lane == 0 && pages > 0) mbar_expect_tx(&kv_full[st], 2u * (uint32_t)(pages * ps * D));
+      __syncwarp();
+      if (lane < pages) {
+        // Pages that several row tiles read stay in L2.
+        const uint64_t pol = c0.u.tiles > 1 ? l2_policy_evict_last() : l2_policy_evict_first();
+        tma_load_4d(kt + lane * ps * D, &tmap_k, &kv_full[st], 0, c0.u.g, 0, c0.id, pol);
+        tma_load_4d(vt + lane * ps * D, &tmap_v, &kv_full[st], 0, c0.u.g, 0, c0.id, pol);
+      }
+      look_scale(c1);
+      if (lane < 8) {
+        sScale[st * 16 + lane] = c0.ks;
+        sScale[st * 16 + 8 + lane] = c0.vs;
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&kv_full[st]);
+      if (++st == S) {
+        st = 0;
+        ph ^= 1;
+      }
+      c0 = c1;
+      c1 = c2;
+    }
+    // Every copy has landed before the CTA leaves (whatever the other roles did).
+    for (int x = (t > S ? t - S : 0); x < t; ++x) mbar_wait(&kv_full[x % S], (x / S) & 1, nullptr);
+  } else if (warp == kPMmaWarp) {
+    // ------------------------------------------------------------ MMA issuer
+    if (lane == 0) {
+      const uint32_t sa = smem_u32(sStage), qa = smem_u32(sQ), pa = smem_u32(sP);
+      const uint64_t dK0 = sdesc_row<D>(sa, 16);
+      const uint64_t dQ0 = sdesc_row<D>(qa, 16);
+      const uint64_t dV0 = sdesc_row<D>(sa + C::kTile, kPBlock * 64);
+      const uint64_t dP0 = sdesc_row<128>(pa, kPBlock * 128);
+      const uint32_t idS = idesc_e4m3(kPBlock, R, 0, 0);
+      const uint32_t idO = idesc_e4m3(128, 2 * R, 1, 1);
+      struct Cursor {
+        PUnit u;
+        int t, st, ph, k;  // block and unit counts of this CTA
+        bool first;
+      };
+      auto step = [&](Cursor& c) {
+        ++c.t;
+        if (++c.st == S) {
+          c.st = 0;
+          c.ph ^= 1;
+        }
+        c.first = false;
+        if (++c.u.j >= c.u.j1) {
+          list.next(c.u);
+          ++c.k;
+          c.first = true;
+        }
+      };
+      Cursor xs{list.first(x0), 0, 0, 0, 0, true};
+      Cursor xp = xs;
+      uint64_t t_idle = 0;
+      uint32_t idle = 0;
+      while (xp.u.valid) {
+        bool did = false;
+        if (xs.u.valid && xs.t <= xp.t + 1 && (!xs.first || mbar_test_wait(&q_full[xs.k & 1], (xs.k >> 1) & 1)) &&
+            mbar_test_wait(&kv_full[xs.st], xs.ph)) {
+          tc_fence_after();
+          const uint64_t dk = dK0 + (uint64_t)(xs.st * (C::kStage >> 4));
+          const uint64_t dq = dQ0 + (uint64_t)((xs.k & 1) * (2 * C::kQ >> 4));
+          const uint32_t dst = tmem + (uint32_t)((xs.t & 1) * R);
+#pragma unroll
+          for (int term = 0; term < 2; ++term)
+#pragma unroll
+            for (int kk = 0; kk < D / 32; ++kk)
+              umma_e4m3(dst, dk + kk * 2, dq + term * (C::kQ >> 4) + kk * 2, idS, term + kk > 0 ? 1u : 0u);
+          umma_commit(&s_full[xs.t & 1]);
+          step(xs);
+          did = true;
+        }
+        if (xp.t < xs.t && mbar_test_wait(&p_full[xp.t & 1], (xp.t >> 1) & 1)) {
+          tc_fence_after();
+          const uint64_t dv = dV0 + (uint64_t)(xp.st * (C::kStage >> 4));
+          const uint64_t dp = dP0 + (uint64_t)((xp.t & 1) * (kPBlock * 128 >> 4));
+          const uint32_t dst = tmem + (uint32_t)(2 * R + (xp.t & 1) * 2 * R);
+#pragma unroll
+          for (int kk = 0; kk < kPBlock / 32; ++kk)
+            umma_e4m3(dst, dv + kk * (32 * D >> 4), dp + kk * (32 * 128 >> 4), idO, kk > 0 ? 1u : 0u);
+          umma_commit(&o_full[xp.t & 1]);
+          umma_commit(&kv_empty[xp.st]);
+          step(xp);
+          did = true;
+        }
+        if (did) {
+          t_idle = 0;
+          idle = 0;
+        } else if ((++idle & 1023u) == 0) {
+          const uint64_t now = global_timer_ns();
+          if (t_idle == 0) t_idle = now;
+          if (*abort_v || now - t_idle > kWaitLimitNs) {
+            *abort_v = 1;
+            break;
+          }
+        }
+      }
+      umma_commit(mma_done);
+      mbar_wait(mma_done, 0, nullptr);
+    }
+  } else if (warp >= kPPrepWarp) {
+    // ------------------------------------------------------------ Q tiles and tree masks
+    const int q = warp - kPPrepWarp;   // this warp's half of the rows
+    constexpr int E = D / 32;          // elements of a row per lane
+    int k = 0;
+    for (PUnit u = list.first(x0); u.valid; list.next(u), ++k) {
+      const int buf = k & 1;
+      if (k >= 2) TSV_PWAIT(&unit_free[buf], (k >> 1) - 1);
+      if (__any_sync(0xffffffffu, dead)) break;
+      const int row0 = u.tile * R;
+      const int rows = min(R, u.n * a.G - row0);
+      // Row r of the tile: node (row0 + r) / G, query head g G + (row0 + r) % G.
+      {
+        const int r = q * 32 + lane;
+        if (r < R) {
+          const int gr = row0 + r, node = gr / a.G;
+          sRow[buf * R + r] = r < rows ? (u.off + node) * a.Hq + u.g * a.G + (gr - node * a.G) : -1;
+        }
+      }
+      __syncwarp();
+      uint8_t* hi = sQ + buf * 2 * C::kQ;
+      uint8_t* lo = hi + C::kQ;
+      constexpr int kBatch = 8;
+      for (int r0 = q * 32; r0 < min(R, q * 32 + 32); r0 += kBatch) {
+        float x[kBatch][E];
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+          const int r = r0 + i;
+#pragma unroll
+          for (int e = 0; e < E; ++e) x[i][e] = 0.f;
+          if (r < rows) {
+            const int row = sRow[buf * R + r];
+            const int node = row / a.Hq;
+            const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.q) + (int64_t)node * a.qs_n +
+                                       (int64_t)(row - node * a.Hq) * a.qs_h + lane * E;
+            if constexpr (E == 4) {
+              const uint2 w = __ldg(reinterpret_cast<const uint2*>(src));
+              x[i][0] = __uint_as_float(w.x << 16);
+              x[i][1] = __uint_as_float(w.x & 0xFFFF0000u);
+              x[i][2] = __uint_as_float(w.y << 16);
+              x[i][3] = __uint_as_float(w.y & 0xFFFF0000u);
+            } else {
+              const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(src));
+              x[i][0] = __uint_as_float(w << 16);
+              x[i][1] = __uint_as_float(w & 0xFFFF0000u);
+            }
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+          const int r = r0 + i;
+          uint32_t top = 0u;
+#pragma unroll
+          for (int e = 0; e < E; ++e) top = max(top, __float_as_uint(x[i][e]) & 0x7FFFFFFFu);
+          top = __reduce_max_sync(0xffffffffu, top);
+          const bool fine = top < 0x7F800000u;  // no infinity, no NaN in the row
+          // The largest value moves to [128, 256): exponent 134 as biased.
+          const int up = top == 0u ? 0 : max(-120, min(120, 134 - (int)(top >> 23)));
+          const float mul = __uint_as_float((uint32_t)(127 + up) << 23);
+          if (lane == 0) sFr[buf * R + r] = __uint_as_float((uint32_t)(127 - up) << 23) * (a.scale * 1.4426950408889634f);
+          uint32_t wh = 0u, wl = 0u;
+#pragma unroll
+          for (int e = 0; e < E; e += 2) {
+            // A row with an infinity or a NaN is NaN throughout (its scores are).
+            const float y0 = fine ? x[i][e] * mul : NAN, y1 = fine ? x[i][e + 1] * mul : NAN;
+            const uint32_t h2 = e4m3x2(y0, y1), f2 = f16x2_of_e4m3x2(h2);
+            wh |= h2 << (8 * e);
+            wl |= e4m3x2(y0 - f16_lo(f2), y1 - f16_hi(f2)) << (8 * e);
+          }
+          const uint32_t at = swz<D>(r, lane * E / 16) + (lane * E) % 16;
+          if constexpr (E == 4) {
+            *reinterpret_cast<uint32_t*>(hi + at) = wh;
+            *reinterpret_cast<uint32_t*>(lo + at) = wl;
+          } else {
+            *reinterpret_cast<uint16_t*>(hi + at) = (uint16_t)wh;
+            *reinterpret_cast<uint16_t*>(lo + at) = (uint16_t)wl;
+          }
+        }
+      }
+      // Rows that see tree key j, 32 rows a warp: word q of sDesc[buf][j].
+      if (tree && u.j1 > u.nmain) {
+        const int r = q * 32 + lane;
+        const bool on = r < rows;
+        const int node = on ? (row0 + r) / a.G : 0;
+        for (int w = 0; w < (u.n + 31) / 32; ++w) {
+          uint32_t bits = 0u;
+          if (on) {
+            const int left = node + 1 - 32 * w;
+            bits = a.anc ? __ldg(a.anc + (int64_t)(u.off + node) * TSV_ANC_WORDS + w)
+                         : (left >= 32 ? 0xFFFFFFFFu : left > 0 ? (1u << left) - 1u : 0u);
+          }
+          uint32_t mine = 0u;
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            const uint32_t m = __ballot_sync(0xffffffffu, (bits >> i) & 1u);
+            if (lane == i) mine = m;
+          }
+          sDesc[(buf * 256 + w * 32 + lane) * 2 + q] = mine;
+        }
+      }
+      fence_proxy_async_smem();
+      mbar_arrive(&q_full[buf]);
+    }
+    // Every request's lengths and page ids are checked by one CTA.
+    for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
+      PagedRequest r;
+      bool bad = !paged_request(a, b, &r);
+      if (!bad) bad = paged_bad_page(a, b, r, tid - 32 * kPPrepWarp, 64);
+      bad = named_bar_or(kBarPrep, 64, bad);
+      if (tid == 32 * kPPrepWarp) a.status[b] = bad ? TSV_ERR_INVALID_ARG : TSV_OK;
+    }
+  } else if (warp < 8) {
+    // ------------------------------------------------------------ softmax: a thread owns a key
+    const int wg = warp >> 2, lg = warp & 3;
+    const int kt = tid & 127;                  // thread of the group = key lane
+    const uint32_t lane_base = (uint32_t)(lg * 32) << 16;
+    const uint32_t s_col = tmem + lane_base + (uint32_t)(wg * R);
+    uint8_t* prow = sP + wg * (kPBlock * 128);
+    float* fr_w = sWmax + (wg * 4) * R;
+    int t = 0, st = 0, ph = 0, k = 0;
+    for (PUnit u = list.first(x0); u.valid; list.next(u), ++k) {
+      const int buf = k & 1;
+      float lsum[R];
+#pragma unroll
+      for (int i = 0; i < R; ++i) lsum[i] = 0.f;
+      float mw = -INFINITY;  // thread r < R: largest score of row r over this group's blocks of the unit
+      bool have_q = false;
+      for (int j = u.j; j < u.j1; ++j, ++t) {
+        const int stage = st, phase = ph;
+        if (++st == S) {
+          st = 0;
+          ph ^= 1;
+        }
+        if ((t & 1) != wg) continue;
+        if (!have_q) {
+          TSV_PWAIT(&q_full[buf], k >> 1);
+          have_q = true;
+        }
+        TSV_PWAIT(&kv_full[stage], phase);
+        TSV_PWAIT(&s_full[wg], t >> 1);
+        tc_fence_after();
+        const bool main = j < u.nmain;
+        const int base = (main ? j : j - u.nmain) * kPBlock;
+        const int valid = max(0, min(kPBlock, (main ? u.P : tree ? u.n : 0) - base));
+        const bool all = main && valid == kPBlock;  // every row sees every key
+        const float* ksc = sScale + stage * 16;
+        const float fk = ksc[kt / ps];
+        float svmax = 0.f;
+        for (int i = 0; i < kPBlock / ps; ++i) svmax = fmaxf(svmax, ksc[8 + i]);
+        const float svr = svmax > 0.f ? 256.f * (ksc[8 + kt / ps] / svmax) : 0.f;
+        // Rows that see a key, one bit each.
+        auto sees = [&](int key) -> uint64_t {
+          if (key >= valid) return 0ull;
+          if (main) return ~0ull;
+          const uint32_t* w = sDesc + (buf * 256 + base + key) * 2;
+          return (uint64_t)w[0] | (R > 32 ? (uint64_t)w[1] << 32 : 0ull);
+        };
+
+        // Largest score of every row over the warp's 32 keys, in the 16x256b
+        // layout: 4 keys of 2 columns in 8 a thread, then three halving
+        // exchanges over the 8 thread rows.
+        {
+          float best[R / 4];
+#pragma unroll
+          for (int i = 0; i < R / 4; ++i) best[i] = -INFINITY;
+#pragma unroll
+          for (int hh = 0; hh < 2; ++hh) {
+            float v[R / 2];
+            tmem_ld_16x256<R>(s_col + ((uint32_t)(hh * 16) << 16), v);
+            const int key = lg * 32 + hh * 16 + (lane >> 2);
+            if (!all) {
+              const uint64_t va = sees(key) >> (2 * (lane & 3)), vb = sees(key + 8) >> (2 * (lane & 3));
+#pragma unroll
+              for (int i = 0; i < R / 8; ++i)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                  if (!((va >> (8 * i + c)) & 1ull)) v[4 * i + c] = -INFINITY;
+                  if (!((vb >> (8 * i + c)) & 1ull)) v[4 * i + 2 + c] = -INFINITY;
+                }
+            }
+            const float f = ksc[key / ps];
+#pragma unroll
+            for (int i = 0; i < R / 8; ++i)
+#pragma unroll
+              for (int c = 0; c < 2; ++c)
+                best[2 * i + c] = fmaxf(best[2 * i + c], fmaxf(v[4 * i + c], v[4 * i + 2 + c]) * f);
+          }
+          // best[2 i + c] is column 8 i + 2 (lane % 4) + c.
+          constexpr int N0 = R / 4;
+#pragma unroll
+          for (int s = 0; s < 3; ++s) {
+            const int half = (N0 >> s) / 2;  // values kept
+            const int bit = 16 >> s;
+            const bool up = lane & bit;
+            if (half >= 1) {
+#pragma unroll
+              for (int i = 0; i < (half > 0 ? half : 1); ++i) {
+                const float send = up ? best[i] : best[i + half];
+                const float keep = up ? best[i + half] : best[i];
+                best[i] = fmaxf(keep, __shfl_xor_sync(0xffffffffu, send, bit));
+              }
+            } else {
+              best[0] = fmaxf(best[0], __shfl_xor_sync(0xffffffffu, best[0], bit));
+            }
+          }
+          // Which columns this thread is left with: the halvings picked index
+          // bits from the top down.
+          constexpr int kLeft = N0 >= 8 ? N0 / 8 : 1;
+          int at = 0;
+          {
+            int half = N0 / 2;
+            if (half >= 1) at += (lane & 16) ? half : 0;
+            half >>= 1;
+            if (half >= 1) at += (lane & 8) ? half : 0;
+            half >>= 1;
+            if (half >= 1) at += (lane & 4) ? half : 0;
+          }
+#pragma unroll
+          for (int i = 0; i < kLeft; ++i) {
+            const int idx = at + i;
+            fr_w[lg * R + (idx >> 1) * 8 + 2 * (lane & 3) + (idx & 1)] = best[i];
+          }
+        }
+        // The accumulating group has read this buffer's last block (its
+        // maxima and O), which also means that P of that block has been used.
+        if (t >= 2) TSV_PWAIT(&o_free[wg], (t >> 1) - 1);
+        named_bar_sync(kBarSoft + wg, 128);
+        bool moved = false;
+        if (kt < R) {
+          float m = fmaxf(fmaxf(fr_w[kt], fr_w[R + kt]), fmaxf(fr_w[2 * R + kt], fr_w[3 * R + kt])) * sFr[buf * R + kt];
+          if (!(m > -INFINITY)) m = -INFINITY;  // nothing seen, or NaN scores only
+          const float mn = fmaxf(mw, m);
+          sM[wg * R + kt] = m;
+          sBe[wg * R + kt] = m == -INFINITY ? 1.f : fast_exp2(m - mn);  // no maximum: P is 0 or NaN
+          const float al = mw == -INFINITY ? 0.f : fast_exp2(mw - mn);
+          sAl[wg * R + kt] = mn == -INFINITY ? 1.f : al;
+          moved = mn != mw;
+          mw = mn;
+        }
+        if (kt == 0) sSv[wg] = svmax * (1.f / 256.f);
+        if (named_bar_or(kBarSoft + wg, 128, moved)) {
+#pragma unroll
+          for (int i = 0; i < R; ++i) lsum[i] *= sAl[wg * R + i];
+        }
+        const uint64_t vis = all ? ~0ull : sees(kt);
+#pragma unroll
+        for (int c0 = 0; c0 < R; c0 += 16) {
+          float sv[16];
+          tmem_ld16(s_col + c0, sv);
+          uint32_t hi[4], lo[4];
+#pragma unroll
+          for (int q4 = 0; q4 < 4; ++q4) {
+            const float4 m4 = *reinterpret_cast<const float4*>(sM + wg * R + c0 + 4 * q4);
+            const float4 f4 = *reinterpret_cast<const float4*>(sFr + buf * R + c0 + 4 * q4);
+            const float4 b4 = *reinterpret_cast<const float4*>(sBe + wg * R + c0 + 4 * q4);
+            const float m[4] = {m4.x, m4.y, m4.z, m4.w}, f[4] = {f4.x, f4.y, f4.z, f4.w}, be[4] = {b4.x, b4.y, b4.z, b4.w};
+            float p[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int r = c0 + 4 * q4 + e;
+              // The same products as in the maximum: x <= 0 up to m's own rounding.
+              const float x = fmaf(sv[4 * q4 + e] * fk, f[e], m[e] == -INFINITY ? 0.f : -m[e]);
+              p[e] = fast_exp2(x);
+              if (!all && !((vis >> r) & 1ull)) p[e] = 0.f;
+              lsum[r] = fmaf(p[e], be[e], lsum[r]);
+              p[e] *= svr;
+            }
+            // Two e4m3 terms: hi, and 16 x what it leaves (exact in fp16).
+            uint32_t h01 = e4m3x2(p[0], p[1]), h23 = e4m3x2(p[2], p[3]);
+            const uint32_t g01 = f16x2_of_e4m3x2(h01), g23 = f16x2_of_e4m3x2(h23);
+            const uint32_t l01 = e4m3x2((p[0] - f16_lo(g01)) * 16.f, (p[1] - f16_hi(g01)) * 16.f);
+            const uint32_t l23 = e4m3x2((p[2] - f16_lo(g23)) * 16.f, (p[3] - f16_hi(g23)) * 16.f);
+            hi[q4] = h01 | (h23 << 16);
+            lo[q4] = l01 | (l23 << 16);
+          }
+          *reinterpret_cast<uint4*>(prow + swz<128>(kt, c0 / 16)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+          *reinterpret_cast<uint4*>(prow + swz<128>(kt, (R + c0) / 16)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        }
+        if (!all) {
+          uint8_t* vrow = sStage + stage * C::kStage + C::kTile + kt * D;
+          if (kt >= valid) {  // whatever the row holds
+#pragma unroll
+            for (int c = 0; c < D / 16; ++c) reinterpret_cast<uint4*>(vrow)[c] = make_uint4(0u, 0u, 0u, 0u);
+          } else if (!main) {
+            for (int c = 0; c < D / 4; ++c) {
+              const uint32_t w = reinterpret_cast<const uint32_t*>(vrow)[c];
+              uint32_t nan = ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+              if (nan == 0u) continue;
+              reinterpret_cast<uint32_t*>(vrow)[c] = w & ~((nan >> 7) * 0xFFu);
+              const int chunk = D == 128 ? (c >> 2) ^ (kt & 7) : (c >> 2) ^ ((kt >> 1) & 3);
+              for (; nan; nan &= nan - 1)
+                atomicOr(sPoison + buf * 128 + chunk * 16 + (c & 3) * 4 + ((__ffs(nan) - 1) >> 3), (unsigned long long)vis);
+              sPoisoned[buf] = 1;
+            }
+          }
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        mbar_arrive(&p_full[wg]);
+      }
+      // Sums of P over the warp's keys (transposed reduction), and their reference.
+      if (k >= 2) TSV_PWAIT(&unit_free[buf], (k >> 1) - 1);
+      {
+        constexpr int kLeft = R >= 32 ? R / 32 : 1;
+#pragma unroll
+        for (int s = 0; s < 5; ++s) {
+          const int half = (R >> s) / 2;
+          const int bit = 16 >> s;
+          const bool up = lane & bit;
+          if (half >= 1) {
+#pragma unroll
+            for (int i = 0; i < (half > 0 ? half : 1); ++i) {
+              const float send = up ? lsum[i] : lsum[i + half];
+              const float keep = up ? lsum[i + half] : lsum[i];
+              lsum[i] = keep + __shfl_xor_sync(0xffffffffu, send, bit);
+            }
+          } else {
+            lsum[0] += __shfl_xor_sync(0xffffffffu, lsum[0], bit);
+          }
+        }
+        const int first = R >= 32 ? lane * kLeft : lane >> 1;  // the halvings picked the row's bits from the top
+#pragma unroll
+        for (int i = 0; i < kLeft; ++i) sL[(buf * 8 + warp) * R + first + i] = lsum[i];
+        if (kt < R) sMw[(buf * 2 + wg) * R + kt] = mw;
+      }
+      mbar_arrive(&l_full[buf]);
+    }
+  } else {
+    // ------------------------------------------------------------ accumulation: a thread owns a d
+    const int d = tid & 127, lg = warp & 3;
+    const uint32_t lane_base = (uint32_t)(lg * 32) << 16;
+    const bool live = d < D;
+    int t = 0, k = 0;
+    for (PUnit u = list.first(x0); u.valid; list.next(u), ++k) {
+      const int buf = k & 1;
+      float acc[R];
+#pragma unroll
+      for (int i = 0; i < R; ++i) acc[i] = 0.f;
+      float mt = -INFINITY;  // thread r < R: running maximum of row r
+      TSV_PWAIT(&q_full[buf], k >> 1);  // the unit's output rows
+      for (int j = u.j; j < u.j1; ++j, ++t) {
+        const int x = t & 1;
+        TSV_PWAIT(&p_full[x], t >> 1);
+        float* ab = sAB + x * 2 * R;
+        if (d < R) {
+          const float m = sM[x * R + d];
+          const float mn = fmaxf(mt, m);
+          ab[d] = mn == -INFINITY ? 1.f : mt == -INFINITY ? 0.f : fast_exp2(mt - mn);
+          // A block without a maximum holds P against 0 (only NaN scores, or nothing seen: P = 0).
+          ab[R + d] = sSv[x] * (m == -INFINITY ? 1.f : fast_exp2(m - mn));
+          mt = mn;
+        }
+        named_bar_sync(kBarAcc, 128);
+        TSV_PWAIT(&o_full[x], t >> 1);
+        tc_fence_after();
+        const uint32_t o_col = tmem + lane_base + (uint32_t)(2 * R + x * 2 * R);
+#pragma unroll
+        for (int c0 = 0; c0 < R; c0 += 16) {
+          float h[16], l[16];
+          tmem_ld16(o_col + c0, h);
+          tmem_ld16(o_col + R + c0, l);
+#pragma unroll
+          for (int q4 = 0; q4 < 4; ++q4) {
+            const float4 al = *reinterpret_cast<const float4*>(ab + c0 + 4 * q4);
+            const float4 be = *reinterpret_cast<const float4*>(ab + R + c0 + 4 * q4);
+            const float av[4] = {al.x, al.y, al.z, al.w}, bv[4] = {be.x, be.y, be.z, be.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int r = c0 + 4 * q4 + e;
+              acc[r] = fmaf(fmaf(l[4 * q4 + e], 0.0625f, h[4 * q4 + e]), bv[e], acc[r] * av[e]);
+            }
+          }
+        }
+        tc_fence_before();
+        mbar_arrive(&o_free[x]);
+      }
+      // The unit is done: denominators, then its rows or its partials.
+      TSV_PWAIT(&l_full[buf], k >> 1);
+      float* fin = sFin + buf * R;
+      if (d < R) {
+        float l = 0.f;
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+          const float mw = sMw[(buf * 2 + w) * R + d];
+          const float* lw = sL + (buf * 8 + 4 * w) * R + d;
+          const float sum = (lw[0] + lw[R]) + (lw[2 * R] + lw[3 * R]);
+          l += mw == -INFINITY ? sum : sum * fast_exp2(mw - mt);
+        }
+        fin[d] = l;
+      }
+      if (sPoisoned[buf]) {
+        const unsigned long long rows = sPoison[buf * 128 + d];
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+          if ((rows >> r) & 1ull) acc[r] = NAN;
+        sPoison[buf * 128 + d] = 0ull;
+      }
+      const bool stop = named_bar_or(kBarAcc, 128, dead);  // the same in every thread
+      if (d == 0) sPoisoned[buf] = 0;
+      const int rows = min(R, u.n * a.G - u.tile * R);
+      __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out);
+      if (u.whole()) {
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+          if (r < rows && live) {
+            const float l = fin[r];
+            out[(int64_t)sRow[buf * R + r] * D + d] = __float2bfloat16_rn(l == 0.f ? 0.f : acc[r] / l);
+          }
+      } else if (!stop) {
+        const int slot = 2 * (int)blockIdx.x + (k == 0 ? 0 : 1);
+        float* po = part_o + (int64_t)slot * R * D;
+        float* pm = part_ml + (int64_t)slot * 2 * R;
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+          if (r < rows && live) po[r * D + d] = acc[r];
+        if (d < R) {
+          pm[d] = mt;
+          pm[R + d] = fin[d];
+        }
+        // CTAs cf .. cl share the group; the last to arrive joins.
+        __threadfence();
+        const int cf = (int)(((u.gx + 1) * ctas - 1) / W), cl = (int)(((u.gx + u.T) * ctas - 1) / W);
+        named_bar_sync(kBarAcc, 128);
+        if (d == 0) {
+          const int n = atom_add_acq_rel_gpu(counters + cf, 1);
+          const bool last = n == cl - cf;
+          if (last) counters[cf] = 0;
+          *sJoin = last ? 1 : 0;
+        }
+        named_bar_sync(kBarAcc, 128);
+        if (*sJoin) {
+          __threadfence();
+          for (int r = 0; r < rows; ++r) {
+            float top = -INFINITY, sum = 0.f, o = 0.f;
+            for (int c = cf; c <= cl; ++c) {
+              const int s = 2 * c + ((int64_t)c * W / ctas >= u.gx ? 0 : 1);
+              top = fmaxf(top, __ldcg(part_ml + (int64_t)s * 2 * R + r));
+            }
+            for (int c = cf; c <= cl; ++c) {
+              const int s = 2 * c + ((int64_t)c * W / ctas >= u.gx ? 0 : 1);
+              const float m = __ldcg(part_ml + (int64_t)s * 2 * R + r);
+              const float w = m == -INFINITY ? 1.f : fast_exp2(m - top);
+              sum += w * __ldcg(part_ml + (int64_t)s * 2 * R + R + r);
+              if (live) o += w * __ldcg(part_o + ((int64_t)s * R + r) * D + d);
+            }
+            if (live) out[(int64_t)sRow[buf * R + r] * D + d] = __float2bfloat16_rn(sum == 0.f ? 0.f : o / sum);
+          }
+        }
+      }
+      mbar_arrive(&unit_free[buf]);
+    }
+  }
+
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (tid == 0 && *abort_v)
+    for (PUnit u = list.first(x0); u.valid; list.next(u)) a.status[u.b] = TSV_ERR_TIMEOUT;
+  if (warp == kPMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::kCols);
+  }
+}
+
+template <int D, int R>
+cudaError_t launch_typed(const CUtensorMap& tk, const CUtensorMap& tv, const PagedAttnArgs& a, int grid, void* ws,
+                         cudaStream_t st) {
+  char* w = static_cast<char*>(ws);
+  const PagedAttnLayout lay = paged_attn_layout(grid, R, D);
+  return launch_pdl(paged_attn_kernel<D, R>, dim3(grid), dim3(kPThreads), (size_t)PCfg<D, R>::kSmem, st, 0u, tk, tv, a,
+                    reinterpret_cast<int32_t*>(w), reinterpret_cast<float*>(w + lay.part_o),
+                    reinterpret_cast<float*>(w + lay.part_ml));
+}
+
+template <int D, int R>
+cudaError_t set_typed() {
+  return cudaFuncSetAttribute(paged_attn_kernel<D, R>, cudaFuncAttributeMaxDynamicSharedMemorySize, PCfg<D, R>::kSmem);
+}
+
+}  // namespace
+
+cudaError_t paged_attention_set_attributes(int32_t D, int32_t R) {
+  if (D == 64) return R == 16 ? set_typed<64, 16>() : R == 32 ? set_typed<64, 32>() : set_typed<64, 64>();
+  return R == 16 ? set_typed<128, 16>() : R == 32 ? set_typed<128, 32>() : set_typed<128, 64>();
+}
+
+cudaError_t launch_paged_attention(const CUtensorMap& tk, const CUtensorMap& tv, const PagedAttnArgs& a, int32_t R, int grid,
+                                   void* ws, cudaStream_t st) {
+  if (a.cache.D == 64)
+    return R == 16   ? launch_typed<64, 16>(tk, tv, a, grid, ws, st)
+           : R == 32 ? launch_typed<64, 32>(tk, tv, a, grid, ws, st)
+                     : launch_typed<64, 64>(tk, tv, a, grid, ws, st);
+  return R == 16   ? launch_typed<128, 16>(tk, tv, a, grid, ws, st)
+         : R == 32 ? launch_typed<128, 32>(tk, tv, a, grid, ws, st)
+                   : launch_typed<128, 64>(tk, tv, a, grid, ws, st);
+}
+
+}  // namespace tsv
