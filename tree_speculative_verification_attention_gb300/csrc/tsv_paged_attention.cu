@@ -2,7 +2,7 @@
 // tensor cores, keys on the TMEM lanes.
 //
 //   S^T = K Q^T       M = 128 keys, N = rows, K = D      (A = K tile, B = Q tile)
-//   O^T = V^T P^T     M = 128 (d), N = 2 x rows, K = 128 keys (A = V tile, M-major)
+//   O^T = V^T P^T     M = 128 (d), N = rows, K = 128 keys (A = V tile, M-major)
 //
 // Both products run on the e4m3 codes themselves, straight from the bytes that
 // TMA brings in: nothing is widened on the way, so a 128-key block of one head
@@ -11,11 +11,10 @@
 //   q = (hi + lo) 2^-k   two e4m3 terms under a power of two per row (the
 //                        row's largest value lands in [128, 256)): a bf16's 8
 //                        bits exactly down to 2^-17 of the row's largest.
-//                        Both terms accumulate into the same S.
-//   p = (hi + lo / 16) / 256   relative to the block's own largest score of
-//                        the row: 8 bits down to 2^-14 of it, never off by more
-//                        than 2^-22 of it.  hi and lo sit side by side on
-//                        the N axis of one MMA and are added in fp32.
+//   p = (hi + lo) / 256  relative to the block's own largest score of the
+//                        row: 8 bits down to 2^-10 of it, never off by more
+//                        than 2^-18 of it (128 keys: 2^-11 of the block).
+// Both terms of either accumulate into the same S or O.
 // That the reference maximum is the block's own (not a running one) keeps
 // those bounds whatever the earlier blocks held; O of a block is brought to
 // the running maximum in fp32 registers, which also keeps long sums out of the
@@ -28,11 +27,14 @@
 // device.  A group that a cut goes through leaves fp32 partials in the
 // workspace, and the last of its CTAs to arrive joins them in a fixed order.
 //
-// Roles (16 warps): two softmax warpgroups taking alternate blocks (warps 0-3
-// and 4-7; a thread owns a key), the accumulating warpgroup (8-11; a thread
-// owns a d), the TMA producer (12: page ids and scales are looked up two
-// blocks ahead), the MMA issuer (13), and two warps that prepare the next
-// unit's Q tiles and tree mask (14, 15).
+// Roles (16 warps): two softmax warpgroups (warps 0-3 and 4-7; a thread owns a
+// key), which take alternate blocks, or, with 64 rows, 32 rows of every block
+// each; the accumulating warpgroup (8-11; a thread owns a d); the TMA producer
+// (12: page ids and scales are looked up a warp's worth ahead); the MMA issuer
+// (13); and two warps that prepare the next unit's Q tiles and tree mask (14,
+// 15).  What a role needs from the rows (maxima, factors) is worked out by
+// each of its warps for itself: a block costs a softmax group one barrier and
+// the accumulating group none.
 //
 // Tail and tree blocks: V rows past the last key are zeroed in shared memory
 // and NaN codes of tree rows are taken out of the product and put back only
@@ -52,7 +54,6 @@ constexpr int kBarAcc = 3, kBarPrep = 4;
 
 template <int D, int R>
 struct PCfg {
-  static constexpr int kRowBytes = D;                       // one key, one head
   static constexpr int kTile = kPBlock * D;                 // K tile
   static constexpr int kVTile = kPBlock * 128;              // 128 d; the upper half stays zero when D = 64
   static constexpr int kStage = kTile + kVTile;
@@ -67,22 +68,23 @@ struct PCfg {
   static constexpr int kOffReq = kOffCum + 8 * (TSV_MAX_BATCH + 2);  // int4 [TSV_MAX_BATCH]: off, n, P, blocks
   static constexpr int kOffFr = kOffReq + 16 * TSV_MAX_BATCH;      // f32 [2][R]: score factor of a row
   static constexpr int kOffRow = kOffFr + 8 * R;                   // i32 [2][R]: output row
-  static constexpr int kOffWmax = kOffRow + 8 * R;                 // f32 [8 warps][R]
-  static constexpr int kOffM = kOffWmax + 32 * R;                  // f32 [2][R]: a block's largest scores
-  static constexpr int kOffAl = kOffM + 8 * R;                     // f32 [2][R]
-  static constexpr int kOffBe = kOffAl + 8 * R;                    // f32 [2][R]
-  static constexpr int kOffAB = kOffBe + 8 * R;                    // f32 [2][2][R]: accumulating group's factors
-  static constexpr int kOffL = kOffAB + 16 * R;                    // f32 [2][8 warps][R]
-  static constexpr int kOffMw = kOffL + 64 * R;                    // f32 [2][2][R]
-  static constexpr int kOffFin = kOffMw + 16 * R;                  // f32 [2][R]: sums of a unit
-  static constexpr int kOffScale = kOffFin + 8 * R;                // f32 [stages][K 8, V 8]
-  static constexpr int kOffSv = kOffScale + kStages * 64;          // f32 [2]
+  static constexpr int RW = R < 32 ? R : 32;                       // rows of one softmax group
+  static constexpr bool kCols = R == 64;                           // the groups split the rows, not the blocks
+  static constexpr int kOffWmax = kOffRow + 8 * R;                 // f32 [2 groups][2][4 warps][RW]
+  static constexpr int kOffPw = kOffWmax + 64 * RW;                // f32 [8 warps][3][RW]: -maxima, sum factors, rescale
+  static constexpr int kOffM = kOffPw + 96 * RW;                   // f32 [2][R]: a block's largest scores
+  static constexpr int kOffAB = kOffM + 8 * R;                     // f32 [4 warps][2][R]: accumulation factors
+  static constexpr int kOffL = kOffAB + 32 * R;                    // f32 [2][8 warps][RW]
+  static constexpr int kOffMw = kOffL + 64 * RW;                   // f32 [2][2 groups][RW]
+  static constexpr int kOffFin = kOffMw + 16 * RW;                 // f32 [2][R]: sums of a unit
+  static constexpr int kOffScale = kOffFin + 8 * R;                // f32 [stages][20]: (K, V) of 8 pages, V's largest
+  static constexpr int kOffSv = kOffScale + kStages * 80;          // f32 [2]
   static constexpr int kOffBar = (kOffSv + 8 + 7) & ~7;
   // kv_full[S], kv_empty[S], s_full[2], p_full[2], o_full[2], o_free[2], q_full[2], unit_free[2], l_full[2], mma_done
   static constexpr int kBars = 2 * kStages + 15;
   static constexpr int kOffMisc = kOffBar + 8 * kBars;
   static constexpr int kSmem = kOffMisc + 64 + 1024;
-  static constexpr uint32_t kCols = R == 64 ? 512 : R == 32 ? 256 : 128;  // S0 S1 (R each) O0 O1 (2 R each)
+  static constexpr uint32_t kTmem = R == 64 ? 256 : R == 32 ? 128 : 64;  // S0 S1 O0 O1, R each
   static_assert(kSmem <= 227 * 1024, "shared memory");
   static_assert(kStage % 1024 == 0 && kQ % 512 == 0 && kOffQ % 1024 == 0, "swizzle atoms");
 };
@@ -120,37 +122,50 @@ __device__ __forceinline__ void mbar_expect_tx(uint64_t* bar, uint32_t bytes) {
 
 // 16 lanes x 256 bits, repeated over R columns: thread t holds, of lanes t / 4
 // and t / 4 + 8, columns 8 i + 2 (t % 4) and the next, in v[4 i ..] (two of the
-// first lane, two of the second).
-template <int R>
-__device__ __forceinline__ void tmem_ld_16x256(uint32_t taddr, float (&v)[R / 2]) {
-  uint32_t r[R / 2];
-  if constexpr (R == 16) {
-    asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-                 : "r"(taddr) : "memory");
-  } else if constexpr (R == 32) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-        : "r"(taddr) : "memory");
-  } else {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.16x256b.x8.b32 "
-        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
-          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-        : "r"(taddr) : "memory");
-  }
+// first lane, two of the second).  Does not wait.
+__device__ __forceinline__ void tmem_ld_16x256(uint32_t taddr, uint32_t (&v)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n"
+               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+               : "r"(taddr)
+               : "memory");
+}
+__device__ __forceinline__ void tmem_ld_16x256(uint32_t taddr, uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+        "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+      : "r"(taddr)
+      : "memory");
+}
+
+// Waits for this thread's TMEM loads and ties registers to the wait.
+template <int N>
+__device__ __forceinline__ void tmem_wait_tie(uint32_t (&v)[N]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;\n" ::: "memory");
 #pragma unroll
-  for (int i = 0; i < R / 2; ++i) {
-    asm volatile("" : "+r"(r[i])::"memory");  // no use before the wait
-    v[i] = __uint_as_float(r[i]);
-  }
+  for (int i = 0; i < N; ++i) asm volatile("" : "+r"(v[i])::"memory");
+}
+template <int N>
+__device__ __forceinline__ void tmem_tie(uint32_t (&v)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) asm volatile("" : "+r"(v[i])::"memory");
+}
+
+// 32 lanes x 32 bits, 16 consecutive columns per thread; does not wait.
+__device__ __forceinline__ void tmem_ld16_nowait(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+
+__device__ __forceinline__ uint64_t fmul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
 }
 
 // One unit of a CTA's range: blocks j .. j1 - 1 of a (request, KV head, row
@@ -239,9 +254,8 @@ __global__ void __launch_bounds__(kPThreads, 1)
   float* sFr = reinterpret_cast<float*>(smem + C::kOffFr);
   int32_t* sRow = reinterpret_cast<int32_t*>(smem + C::kOffRow);
   float* sWmax = reinterpret_cast<float*>(smem + C::kOffWmax);
+  float* sPw = reinterpret_cast<float*>(smem + C::kOffPw);
   float* sM = reinterpret_cast<float*>(smem + C::kOffM);
-  float* sAl = reinterpret_cast<float*>(smem + C::kOffAl);
-  float* sBe = reinterpret_cast<float*>(smem + C::kOffBe);
   float* sAB = reinterpret_cast<float*>(smem + C::kOffAB);
   float* sL = reinterpret_cast<float*>(smem + C::kOffL);
   float* sMw = reinterpret_cast<float*>(smem + C::kOffMw);
@@ -266,7 +280,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
   volatile int* abort_v = abort_flag;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int ps = a.cache.page_size;
+  const int lps = __ffs(a.cache.page_size) - 1;  // pages are powers of two
   const bool tree = a.tree_table.ids_d != nullptr;
   bool dead = false;
 
@@ -277,7 +291,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
     }
     for (int x = 0; x < 2; ++x) {
       mbar_init(&s_full[x], 1);
-      mbar_init(&p_full[x], 128);
+      mbar_init(&p_full[x], C::kCols ? 256 : 128);
       mbar_init(&o_full[x], 1);
       mbar_init(&o_free[x], 128);
       mbar_init(&q_full[x], 64);
@@ -290,7 +304,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
     mbar_fence_init();
   }
   if (warp == kPMmaWarp) {
-    tmem_alloc(tmem_slot, C::kCols);
+    tmem_alloc(tmem_slot, C::kTmem);
     tmem_relinquish();
   }
   if (warp == kPProducerWarp && lane == 0) {
@@ -345,73 +359,91 @@ __global__ void __launch_bounds__(kPThreads, 1)
 
   if (warp == kPProducerWarp) {
     // ------------------------------------------------------------ producer
-    // Block t is issued while the page scales of block t + 1 and the page ids
-    // of block t + 2 are on their way.
-    const int per = kPBlock / ps;  // pages of a block
+    // The lanes stand for the pages of the next 32 / per blocks, per pages to
+    // a block: lane i holds page i % per of block i / per of its chunk.  Page ids
+    // of the next chunk are loaded as a chunk begins, their scales after its
+    // first block.
+    const int per = kPBlock >> lps, chunk = 32 >> (7 - lps);  // pages of a block, blocks of a chunk
+    const int mine = lane >> (7 - lps), pg = lane & (per - 1);
     struct Look {
       PUnit u;
-      int id;
-      float ks, vs;
+      int id, pages;  // of the block; id -1: no keys in this lane's page
     };
-    auto block_pages = [&](const PUnit& u) {  // pages of block u.j that hold keys
-      const int keys = u.j < u.nmain ? u.P - u.j * kPBlock : tree ? u.n - (u.j - u.nmain) * kPBlock : 0;
-      return (min(keys, kPBlock) + ps - 1) / ps;
+    auto advance = [&](PUnit& u, int blocks) {
+      while (u.valid && blocks > 0) {
+        const int left = u.j1 - u.j;
+        if (blocks < left) {
+          u.j += blocks;
+          return;
+        }
+        blocks -= left;
+        list.next(u);
+      }
     };
     auto look_id = [&](Look& k) {
       k.id = -1;
-      if (!k.u.valid || lane >= block_pages(k.u)) return;
+      k.pages = 0;
+      if (!k.u.valid) return;
       const bool main = k.u.j < k.u.nmain;
+      const int block = main ? k.u.j : k.u.j - k.u.nmain;
+      const int keys = (main ? k.u.P : tree ? k.u.n : 0) - block * kPBlock;
+      k.pages = (max(0, min(keys, kPBlock)) + (1 << lps) - 1) >> lps;
       const tsv_page_table& t = main ? a.table : a.tree_table;
-      k.id = __ldg(t.ids_d + (int64_t)k.u.b * t.stride + (main ? k.u.j : k.u.j - k.u.nmain) * per + lane);
+      if (pg < k.pages) k.id = __ldg(t.ids_d + (int64_t)k.u.b * t.stride + block * per + pg);
     };
-    auto look_scale = [&](Look& k) {
-      k.ks = k.vs = 0.f;
+    auto look_scale = [&](const Look& k, float& ks, float& vs) {
+      ks = vs = 0.f;
       if (k.u.valid && (uint32_t)k.id < (uint32_t)a.cache.num_pages) {
-        k.ks = __ldg(a.cache.k_scale_d + (int64_t)k.id * a.cache.Hkv + k.u.g);
-        k.vs = __ldg(a.cache.v_scale_d + (int64_t)k.id * a.cache.Hkv + k.u.g);
+        ks = __ldg(a.cache.k_scale_d + (int64_t)k.id * a.cache.Hkv + k.u.g);
+        vs = __ldg(a.cache.v_scale_d + (int64_t)k.id * a.cache.Hkv + k.u.g);
       }
     };
-    auto advance = [&](Look& k) {
-      if (k.u.valid && ++k.u.j >= k.u.j1) list.next(k.u);
-    };
-    Look c0, c1, c2;
+    Look c0, c1;
+    float ks0, vs0, ks1 = 0.f, vs1 = 0.f;
     c0.u = list.first(x0);
+    advance(c0.u, mine);
     look_id(c0);
-    c1.u = c0.u;
-    advance(c1);
-    look_id(c1);
-    look_scale(c0);
+    look_scale(c0, ks0, vs0);
+    const int blocks = (int)(list.x1 - x0);
     int t = 0, st = 0, ph = 0;
-    for (; c0.u.valid; ++t) {
-      c2.u = c1.u;
-      advance(c2);
-      look_id(c2);
-      if (t >= S) TSV_PWAIT(&kv_empty[st], ph ^ 1);
+    while (t < blocks) {
+      c1.u = c0.u;
+      advance(c1.u, chunk);
+      look_id(c1);
+      for (int i = 0; i < chunk && t < blocks; ++i, ++t) {
+        if (t >= S) TSV_PWAIT(&kv_empty[st], ph ^ 1);
+        if (__any_sync(0xffffffffu, dead || *abort_v)) break;
+        const bool turn = mine == i;
+        if (turn && pg == 0 && c0.pages > 0) mbar_expect_tx(&kv_full[st], 2u * (uint32_t)((c0.pages << lps) * D));
+        __syncwarp();
+        if (turn && pg < c0.pages) {
+          // Pages that several row tiles read stay in L2.
+          const uint64_t pol = c0.u.tiles > 1 ? l2_policy_evict_last() : l2_policy_evict_first();
+          uint8_t* kt = sStage + st * C::kStage + (pg << lps) * D;
+          tma_load_4d(kt, &tmap_k, &kv_full[st], 0, c0.u.g, 0, c0.id, pol);
+          tma_load_4d(kt + C::kTile, &tmap_v, &kv_full[st], 0, c0.u.g, 0, c0.id, pol);
+        }
+        if (i == 0) look_scale(c1, ks1, vs1);
+        // V's scale relative to the block's largest goes to P, with its 256.
+        float top = vs0;
+        for (int o = per >> 1; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        if (turn) {
+          float* sc = sScale + st * 20;
+          sc[2 * pg] = ks0;
+          sc[2 * pg + 1] = top > 0.f ? __fdividef(vs0, top) * 256.f : 0.f;
+          if (pg == 0) sc[16] = top * (1.f / 256.f);
+        }
+        __syncwarp();
+        if (turn && pg == 0) mbar_arrive(&kv_full[st]);
+        if (++st == S) {
+          st = 0;
+          ph ^= 1;
+        }
+      }
       if (__any_sync(0xffffffffu, dead || *abort_v)) break;
-      const int pages = block_pages(c0.u);
-      uint8_t* kt = sStage + st * C::kStage;
-      uint8_t* vt = kt + C::kTile;
-      if (lane == 0 && pages > 0) mbar_expect_tx(&kv_full[st], 2u * (uint32_t)(pages * ps * D));
-      __syncwarp();
-      if (lane < pages) {
-        // Pages that several row tiles read stay in L2.
-        const uint64_t pol = c0.u.tiles > 1 ? l2_policy_evict_last() : l2_policy_evict_first();
-        tma_load_4d(kt + lane * ps * D, &tmap_k, &kv_full[st], 0, c0.u.g, 0, c0.id, pol);
-        tma_load_4d(vt + lane * ps * D, &tmap_v, &kv_full[st], 0, c0.u.g, 0, c0.id, pol);
-      }
-      look_scale(c1);
-      if (lane < 8) {
-        sScale[st * 16 + lane] = c0.ks;
-        sScale[st * 16 + 8 + lane] = c0.vs;
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&kv_full[st]);
-      if (++st == S) {
-        st = 0;
-        ph ^= 1;
-      }
       c0 = c1;
-      c1 = c2;
+      ks0 = ks1;
+      vs0 = vs1;
     }
     // Every copy has landed before the CTA leaves (whatever the other roles did).
     for (int x = (t > S ? t - S : 0); x < t; ++x) mbar_wait(&kv_full[x % S], (x / S) & 1, nullptr);
@@ -424,7 +456,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
       const uint64_t dV0 = sdesc_row<D>(sa + C::kTile, kPBlock * 64);
       const uint64_t dP0 = sdesc_row<128>(pa, kPBlock * 128);
       const uint32_t idS = idesc_e4m3(kPBlock, R, 0, 0);
-      const uint32_t idO = idesc_e4m3(128, 2 * R, 1, 1);
+      const uint32_t idO = idesc_e4m3(128, R, 1, 1);
       struct Cursor {
         PUnit u;
         int t, st, ph, k;  // block and unit counts of this CTA
@@ -468,10 +500,12 @@ __global__ void __launch_bounds__(kPThreads, 1)
           tc_fence_after();
           const uint64_t dv = dV0 + (uint64_t)(xp.st * (C::kStage >> 4));
           const uint64_t dp = dP0 + (uint64_t)((xp.t & 1) * (kPBlock * 128 >> 4));
-          const uint32_t dst = tmem + (uint32_t)(2 * R + (xp.t & 1) * 2 * R);
+          const uint32_t dst = tmem + (uint32_t)(2 * R + (xp.t & 1) * R);
 #pragma unroll
-          for (int kk = 0; kk < kPBlock / 32; ++kk)
-            umma_e4m3(dst, dv + kk * (32 * D >> 4), dp + kk * (32 * 128 >> 4), idO, kk > 0 ? 1u : 0u);
+          for (int term = 0; term < 2; ++term)
+#pragma unroll
+            for (int kk = 0; kk < kPBlock / 32; ++kk)
+              umma_e4m3(dst, dv + kk * (32 * D >> 4), dp + term * (R >> 4) + kk * (32 * 128 >> 4), idO, term + kk > 0 ? 1u : 0u);
           umma_commit(&o_full[xp.t & 1]);
           umma_commit(&kv_empty[xp.st]);
           step(xp);
@@ -494,8 +528,10 @@ __global__ void __launch_bounds__(kPThreads, 1)
     }
   } else if (warp >= kPPrepWarp) {
     // ------------------------------------------------------------ Q tiles and tree masks
-    const int q = warp - kPPrepWarp;   // this warp's half of the rows
-    constexpr int E = D / 32;          // elements of a row per lane
+    const int q = warp - kPPrepWarp;
+    constexpr int E = D / 32;                    // elements of a row per lane
+    constexpr int kMine = R / 2;                 // rows of this warp: kMine q ..
+    constexpr int kBatch = kMine < 16 ? kMine : 16;  // loaded together
     int k = 0;
     for (PUnit u = list.first(x0); u.valid; list.next(u), ++k) {
       const int buf = k & 1;
@@ -504,48 +540,41 @@ __global__ void __launch_bounds__(kPThreads, 1)
       const int row0 = u.tile * R;
       const int rows = min(R, u.n * a.G - row0);
       // Row r of the tile: node (row0 + r) / G, query head g G + (row0 + r) % G.
-      {
-        const int r = q * 32 + lane;
-        if (r < R) {
-          const int gr = row0 + r, node = gr / a.G;
-          sRow[buf * R + r] = r < rows ? (u.off + node) * a.Hq + u.g * a.G + (gr - node * a.G) : -1;
-        }
+      // Lane i knows row kMine q + i.
+      int64_t at_q = 0;
+      if (lane < kMine) {
+        const int r = kMine * q + lane;
+        const int gr = row0 + r, node = gr / a.G, head = u.g * a.G + (gr - node * a.G);
+        sRow[buf * R + r] = r < rows ? (u.off + node) * a.Hq + head : -1;
+        if (r < rows) at_q = (int64_t)(u.off + node) * a.qs_n + (int64_t)head * a.qs_h;
       }
-      __syncwarp();
       uint8_t* hi = sQ + buf * 2 * C::kQ;
       uint8_t* lo = hi + C::kQ;
-      constexpr int kBatch = 8;
-      for (int r0 = q * 32; r0 < min(R, q * 32 + 32); r0 += kBatch) {
-        float x[kBatch][E];
+#pragma unroll 1
+      for (int r0 = 0; r0 < kMine; r0 += kBatch) {
+        uint32_t raw[kBatch][E / 2];
 #pragma unroll
         for (int i = 0; i < kBatch; ++i) {
-          const int r = r0 + i;
+          const int64_t at = __shfl_sync(0xffffffffu, at_q, r0 + i);
 #pragma unroll
-          for (int e = 0; e < E; ++e) x[i][e] = 0.f;
-          if (r < rows) {
-            const int row = sRow[buf * R + r];
-            const int node = row / a.Hq;
-            const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.q) + (int64_t)node * a.qs_n +
-                                       (int64_t)(row - node * a.Hq) * a.qs_h + lane * E;
+          for (int e = 0; e < E / 2; ++e) raw[i][e] = 0u;
+          if (kMine * q + r0 + i < rows) {
+            const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.q) + at + lane * E;
             if constexpr (E == 4) {
               const uint2 w = __ldg(reinterpret_cast<const uint2*>(src));
-              x[i][0] = __uint_as_float(w.x << 16);
-              x[i][1] = __uint_as_float(w.x & 0xFFFF0000u);
-              x[i][2] = __uint_as_float(w.y << 16);
-              x[i][3] = __uint_as_float(w.y & 0xFFFF0000u);
+              raw[i][0] = w.x;
+              raw[i][1] = w.y;
             } else {
-              const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(src));
-              x[i][0] = __uint_as_float(w << 16);
-              x[i][1] = __uint_as_float(w & 0xFFFF0000u);
+              raw[i][0] = __ldg(reinterpret_cast<const uint32_t*>(src));
             }
           }
         }
 #pragma unroll
         for (int i = 0; i < kBatch; ++i) {
-          const int r = r0 + i;
+          const int r = kMine * q + r0 + i;
           uint32_t top = 0u;
 #pragma unroll
-          for (int e = 0; e < E; ++e) top = max(top, __float_as_uint(x[i][e]) & 0x7FFFFFFFu);
+          for (int e = 0; e < E / 2; ++e) top = max(top, max((raw[i][e] << 16) & 0x7FFF0000u, raw[i][e] & 0x7FFF0000u));
           top = __reduce_max_sync(0xffffffffu, top);
           const bool fine = top < 0x7F800000u;  // no infinity, no NaN in the row
           // The largest value moves to [128, 256): exponent 134 as biased.
@@ -554,12 +583,13 @@ __global__ void __launch_bounds__(kPThreads, 1)
           if (lane == 0) sFr[buf * R + r] = __uint_as_float((uint32_t)(127 - up) << 23) * (a.scale * 1.4426950408889634f);
           uint32_t wh = 0u, wl = 0u;
 #pragma unroll
-          for (int e = 0; e < E; e += 2) {
+          for (int e = 0; e < E / 2; ++e) {
             // A row with an infinity or a NaN is NaN throughout (its scores are).
-            const float y0 = fine ? x[i][e] * mul : NAN, y1 = fine ? x[i][e + 1] * mul : NAN;
+            const float y0 = fine ? __uint_as_float(raw[i][e] << 16) * mul : NAN;
+            const float y1 = fine ? __uint_as_float(raw[i][e] & 0xFFFF0000u) * mul : NAN;
             const uint32_t h2 = e4m3x2(y0, y1), f2 = f16x2_of_e4m3x2(h2);
-            wh |= h2 << (8 * e);
-            wl |= e4m3x2(y0 - f16_lo(f2), y1 - f16_hi(f2)) << (8 * e);
+            wh |= h2 << (16 * e);
+            wl |= e4m3x2(y0 - f16_lo(f2), y1 - f16_hi(f2)) << (16 * e);
           }
           const uint32_t at = swz<D>(r, lane * E / 16) + (lane * E) % 16;
           if constexpr (E == 4) {
@@ -605,82 +635,83 @@ __global__ void __launch_bounds__(kPThreads, 1)
     }
   } else if (warp < 8) {
     // ------------------------------------------------------------ softmax: a thread owns a key
+    constexpr int RW = C::RW;
+    constexpr bool kCols = C::kCols;
     const int wg = warp >> 2, lg = warp & 3;
+    const int col0 = kCols ? wg * 32 : 0;      // this group's rows of the tile
     const int kt = tid & 127;                  // thread of the group = key lane
     const uint32_t lane_base = (uint32_t)(lg * 32) << 16;
-    const uint32_t s_col = tmem + lane_base + (uint32_t)(wg * R);
-    uint8_t* prow = sP + wg * (kPBlock * 128);
-    float* fr_w = sWmax + (wg * 4) * R;
-    int t = 0, st = 0, ph = 0, k = 0;
+    float* pw = sPw + warp * 3 * RW;
+    int t = 0, st = 0, ph = 0, k = 0, nth = 0;
     for (PUnit u = list.first(x0); u.valid; list.next(u), ++k) {
       const int buf = k & 1;
-      float lsum[R];
+      float lsum[RW];
 #pragma unroll
-      for (int i = 0; i < R; ++i) lsum[i] = 0.f;
-      float mw = -INFINITY;  // thread r < R: largest score of row r over this group's blocks of the unit
-      bool have_q = false;
+      for (int i = 0; i < RW; ++i) lsum[i] = 0.f;
+      float mw = -INFINITY;  // lane r < RW: largest score of row r over this group's blocks of the unit
+      TSV_PWAIT(&q_full[buf], k >> 1);
+      const float fr = lane < RW ? sFr[buf * R + col0 + lane] : 0.f;
       for (int j = u.j; j < u.j1; ++j, ++t) {
         const int stage = st, phase = ph;
         if (++st == S) {
           st = 0;
           ph ^= 1;
         }
-        if ((t & 1) != wg) continue;
-        if (!have_q) {
-          TSV_PWAIT(&q_full[buf], k >> 1);
-          have_q = true;
-        }
-        TSV_PWAIT(&kv_full[stage], phase);
-        TSV_PWAIT(&s_full[wg], t >> 1);
-        tc_fence_after();
+        if (!kCols && (t & 1) != wg) continue;
+        const int x = t & 1;
+        const uint32_t s_col = tmem + lane_base + (uint32_t)(x * R + col0);
         const bool main = j < u.nmain;
         const int base = (main ? j : j - u.nmain) * kPBlock;
         const int valid = max(0, min(kPBlock, (main ? u.P : tree ? u.n : 0) - base));
         const bool all = main && valid == kPBlock;  // every row sees every key
-        const float* ksc = sScale + stage * 16;
-        const float fk = ksc[kt / ps];
-        float svmax = 0.f;
-        for (int i = 0; i < kPBlock / ps; ++i) svmax = fmaxf(svmax, ksc[8 + i]);
-        const float svr = svmax > 0.f ? 256.f * (ksc[8 + kt / ps] / svmax) : 0.f;
-        // Rows that see a key, one bit each.
-        auto sees = [&](int key) -> uint64_t {
-          if (key >= valid) return 0ull;
-          if (main) return ~0ull;
-          const uint32_t* w = sDesc + (buf * 256 + base + key) * 2;
-          return (uint64_t)w[0] | (R > 32 ? (uint64_t)w[1] << 32 : 0ull);
+        // Rows (of this group) that see a key, one bit each.
+        auto sees = [&](int key) -> uint32_t {
+          if (key >= valid) return 0u;
+          if (main) return 0xFFFFFFFFu;
+          return sDesc[(buf * 256 + base + key) * 2 + (kCols ? wg : 0)];
         };
+        float* wmax = sWmax + ((wg * 2 + (nth & 1)) * 4) * RW;
+        ++nth;
+        TSV_PWAIT(&s_full[x], t >> 1);
+        tc_fence_after();
+        uint32_t sa[RW / 2], sb[RW / 2];  // the warp's keys 0-15 and 16-31
+        tmem_ld_16x256(s_col, sa);
+        tmem_ld_16x256(s_col + (16u << 16), sb);
+        TSV_PWAIT(&kv_full[stage], phase);
+        const float2* sc = reinterpret_cast<const float2*>(sScale + stage * 20);
+        const float fa = sc[(lg * 32) >> lps].x, fb = sc[(lg * 32 + 16) >> lps].x;
+        const float2 mine = sc[kt >> lps];  // K's scale; 256 x V's, relative to the block's largest
+        const uint32_t vis = all ? 0xFFFFFFFFu : sees(kt);
+        tmem_wait_tie(sa);
+        tmem_tie(sb);
 
-        // Largest score of every row over the warp's 32 keys, in the 16x256b
-        // layout: 4 keys of 2 columns in 8 a thread, then three halving
-        // exchanges over the 8 thread rows.
+        // Largest score of every row over the warp's 32 keys: 4 keys of 2
+        // columns in 8 a thread, then three halving exchanges over the 8
+        // thread rows.  best[2 i + c] is column 8 i + 2 (lane % 4) + c.
         {
-          float best[R / 4];
+          constexpr int N0 = RW / 4;
+          float best[N0];
+          if (!all) {
+            const int key = lg * 32 + (lane >> 2);
+            const int sh = 2 * (lane & 3);
+            const uint32_t v0 = sees(key) >> sh, v1 = sees(key + 8) >> sh, v2 = sees(key + 16) >> sh, v3 = sees(key + 24) >> sh;
 #pragma unroll
-          for (int i = 0; i < R / 4; ++i) best[i] = -INFINITY;
+            for (int i = 0; i < RW / 8; ++i)
 #pragma unroll
-          for (int hh = 0; hh < 2; ++hh) {
-            float v[R / 2];
-            tmem_ld_16x256<R>(s_col + ((uint32_t)(hh * 16) << 16), v);
-            const int key = lg * 32 + hh * 16 + (lane >> 2);
-            if (!all) {
-              const uint64_t va = sees(key) >> (2 * (lane & 3)), vb = sees(key + 8) >> (2 * (lane & 3));
-#pragma unroll
-              for (int i = 0; i < R / 8; ++i)
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                  if (!((va >> (8 * i + c)) & 1ull)) v[4 * i + c] = -INFINITY;
-                  if (!((vb >> (8 * i + c)) & 1ull)) v[4 * i + 2 + c] = -INFINITY;
-                }
-            }
-            const float f = ksc[key / ps];
-#pragma unroll
-            for (int i = 0; i < R / 8; ++i)
-#pragma unroll
-              for (int c = 0; c < 2; ++c)
-                best[2 * i + c] = fmaxf(best[2 * i + c], fmaxf(v[4 * i + c], v[4 * i + 2 + c]) * f);
+              for (int c = 0; c < 2; ++c) {
+                if (!((v0 >> (8 * i + c)) & 1u)) sa[4 * i + c] = 0xFF800000u;
+                if (!((v1 >> (8 * i + c)) & 1u)) sa[4 * i + 2 + c] = 0xFF800000u;
+                if (!((v2 >> (8 * i + c)) & 1u)) sb[4 * i + c] = 0xFF800000u;
+                if (!((v3 >> (8 * i + c)) & 1u)) sb[4 * i + 2 + c] = 0xFF800000u;
+              }
           }
-          // best[2 i + c] is column 8 i + 2 (lane % 4) + c.
-          constexpr int N0 = R / 4;
+#pragma unroll
+          for (int i = 0; i < RW / 8; ++i)
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+              best[2 * i + c] = fmaxf(fmaxf(__uint_as_float(sa[4 * i + c]), __uint_as_float(sa[4 * i + 2 + c])) * fa,
+                                      fmaxf(__uint_as_float(sb[4 * i + c]), __uint_as_float(sb[4 * i + 2 + c])) * fb);
+          int at = 0;  // first index that this thread is left with: the halvings pick its bits from the top
 #pragma unroll
           for (int s = 0; s < 3; ++s) {
             const int half = (N0 >> s) / 2;  // values kept
@@ -693,89 +724,98 @@ __global__ void __launch_bounds__(kPThreads, 1)
                 const float keep = up ? best[i + half] : best[i];
                 best[i] = fmaxf(keep, __shfl_xor_sync(0xffffffffu, send, bit));
               }
+              at += up ? half : 0;
             } else {
               best[0] = fmaxf(best[0], __shfl_xor_sync(0xffffffffu, best[0], bit));
             }
           }
-          // Which columns this thread is left with: the halvings picked index
-          // bits from the top down.
-          constexpr int kLeft = N0 >= 8 ? N0 / 8 : 1;
-          int at = 0;
-          {
-            int half = N0 / 2;
-            if (half >= 1) at += (lane & 16) ? half : 0;
-            half >>= 1;
-            if (half >= 1) at += (lane & 8) ? half : 0;
-            half >>= 1;
-            if (half >= 1) at += (lane & 4) ? half : 0;
-          }
-#pragma unroll
-          for (int i = 0; i < kLeft; ++i) {
-            const int idx = at + i;
-            fr_w[lg * R + (idx >> 1) * 8 + 2 * (lane & 3) + (idx & 1)] = best[i];
-          }
+          wmax[lg * RW + (at >> 1) * 8 + 2 * (lane & 3) + (at & 1)] = best[0];
         }
-        // The accumulating group has read this buffer's last block (its
-        // maxima and O), which also means that P of that block has been used.
-        if (t >= 2) TSV_PWAIT(&o_free[wg], (t >> 1) - 1);
+        uint32_t sv2[2][16];  // this chunk of 16 rows and the next
+        tmem_ld16_nowait(s_col, sv2[0]);
         named_bar_sync(kBarSoft + wg, 128);
+        // Every warp works out the rows' maxima and factors for itself.
         bool moved = false;
-        if (kt < R) {
-          float m = fmaxf(fmaxf(fr_w[kt], fr_w[R + kt]), fmaxf(fr_w[2 * R + kt], fr_w[3 * R + kt])) * sFr[buf * R + kt];
-          if (!(m > -INFINITY)) m = -INFINITY;  // nothing seen, or NaN scores only
+        if (lane < RW) {
+          float m = fmaxf(fmaxf(wmax[lane], wmax[RW + lane]), fmaxf(wmax[2 * RW + lane], wmax[3 * RW + lane])) * fr;
+          if (!(m > -INFINITY)) m = -INFINITY;  // nothing seen, or NaN scores only: P is 0 or NaN
           const float mn = fmaxf(mw, m);
-          sM[wg * R + kt] = m;
-          sBe[wg * R + kt] = m == -INFINITY ? 1.f : fast_exp2(m - mn);  // no maximum: P is 0 or NaN
-          const float al = mw == -INFINITY ? 0.f : fast_exp2(mw - mn);
-          sAl[wg * R + kt] = mn == -INFINITY ? 1.f : al;
+          pw[lane] = m == -INFINITY ? 0.f : -m;
+          pw[RW + lane] = m == -INFINITY ? 1.f : fast_exp2(m - mn);
+          pw[2 * RW + lane] = mn == -INFINITY ? 1.f : mw == -INFINITY ? 0.f : fast_exp2(mw - mn);
           moved = mn != mw;
           mw = mn;
+          // The accumulating group's copy goes out once that group has read
+          // this buffer's last block (its maxima and O, hence P has been used).
+          if (lg == 0) {
+            if (t >= 2 && !dead && !mbar_wait(&o_free[x], ((t >> 1) - 1) & 1, abort_v)) dead = true;
+            sM[x * R + col0 + lane] = m;
+            if (lane == 0 && col0 == 0) sSv[x] = sScale[stage * 20 + 16];
+          }
         }
-        if (kt == 0) sSv[wg] = svmax * (1.f / 256.f);
-        if (named_bar_or(kBarSoft + wg, 128, moved)) {
+        __syncwarp();
+        if (t >= 2) TSV_PWAIT(&o_free[x], (t >> 1) - 1);
+        if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll
-          for (int i = 0; i < R; ++i) lsum[i] *= sAl[wg * R + i];
+          for (int i = 0; i < RW; i += 4) {
+            const float4 al = *reinterpret_cast<const float4*>(pw + 2 * RW + i);
+            lsum[i] *= al.x;
+            lsum[i + 1] *= al.y;
+            lsum[i + 2] *= al.z;
+            lsum[i + 3] *= al.w;
+          }
         }
-        const uint64_t vis = all ? ~0ull : sees(kt);
+        uint8_t* ptile = sP + x * (kPBlock * 128);
+        const uint64_t fk2 = f2_pack(mine.x, mine.x), fv2 = f2_pack(mine.y, mine.y);
 #pragma unroll
-        for (int c0 = 0; c0 < R; c0 += 16) {
-          float sv[16];
-          tmem_ld16(s_col + c0, sv);
+        for (int c0 = 0; c0 < RW; c0 += 16) {
+          uint32_t(&sv)[16] = sv2[(c0 >> 4) & 1];
+          tmem_wait_tie(sv);
+          if (c0 + 16 < RW) tmem_ld16_nowait(s_col + c0 + 16, sv2[((c0 >> 4) + 1) & 1]);
           uint32_t hi[4], lo[4];
 #pragma unroll
           for (int q4 = 0; q4 < 4; ++q4) {
-            const float4 m4 = *reinterpret_cast<const float4*>(sM + wg * R + c0 + 4 * q4);
-            const float4 f4 = *reinterpret_cast<const float4*>(sFr + buf * R + c0 + 4 * q4);
-            const float4 b4 = *reinterpret_cast<const float4*>(sBe + wg * R + c0 + 4 * q4);
-            const float m[4] = {m4.x, m4.y, m4.z, m4.w}, f[4] = {f4.x, f4.y, f4.z, f4.w}, be[4] = {b4.x, b4.y, b4.z, b4.w};
-            float p[4];
+            const ulonglong2 m4 = *reinterpret_cast<const ulonglong2*>(pw + c0 + 4 * q4);
+            const ulonglong2 b4 = *reinterpret_cast<const ulonglong2*>(pw + RW + c0 + 4 * q4);
+            const ulonglong2 f4 = *reinterpret_cast<const ulonglong2*>(sFr + buf * R + col0 + c0 + 4 * q4);
+            uint32_t hw = 0u, lw = 0u;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int r = c0 + 4 * q4 + e;
+            for (int pr = 0; pr < 2; ++pr) {
+              const int r = c0 + 4 * q4 + 2 * pr;
+              const uint64_t s2 = (uint64_t)sv[4 * q4 + 2 * pr] | ((uint64_t)sv[4 * q4 + 2 * pr + 1] << 32);
               // The same products as in the maximum: x <= 0 up to m's own rounding.
-              const float x = fmaf(sv[4 * q4 + e] * fk, f[e], m[e] == -INFINITY ? 0.f : -m[e]);
-              p[e] = fast_exp2(x);
-              if (!all && !((vis >> r) & 1ull)) p[e] = 0.f;
-              lsum[r] = fmaf(p[e], be[e], lsum[r]);
-              p[e] *= svr;
+              const uint64_t x2 = ffma2(fmul2(s2, fk2), pr ? f4.y : f4.x, pr ? m4.y : m4.x);
+              float p0 = fast_exp2(f2_lo(x2)), p1 = fast_exp2(f2_hi(x2));
+              if (!all) {
+                if (!((vis >> r) & 1u)) p0 = 0.f;
+                if (!((vis >> (r + 1)) & 1u)) p1 = 0.f;
+              }
+              uint64_t p2 = f2_pack(p0, p1);
+              const uint64_t l2 = ffma2(p2, pr ? b4.y : b4.x, f2_pack(lsum[r], lsum[r + 1]));
+              lsum[r] = f2_lo(l2);
+              lsum[r + 1] = f2_hi(l2);
+              p2 = fmul2(p2, fv2);
+              p0 = f2_lo(p2);
+              p1 = f2_hi(p2);
+              const uint32_t h2 = e4m3x2(p0, p1), g2 = f16x2_of_e4m3x2(h2);
+              hw |= h2 << (16 * pr);
+              lw |= e4m3x2(p0 - f16_lo(g2), p1 - f16_hi(g2)) << (16 * pr);
             }
-            // Two e4m3 terms: hi, and 16 x what it leaves (exact in fp16).
-            uint32_t h01 = e4m3x2(p[0], p[1]), h23 = e4m3x2(p[2], p[3]);
-            const uint32_t g01 = f16x2_of_e4m3x2(h01), g23 = f16x2_of_e4m3x2(h23);
-            const uint32_t l01 = e4m3x2((p[0] - f16_lo(g01)) * 16.f, (p[1] - f16_hi(g01)) * 16.f);
-            const uint32_t l23 = e4m3x2((p[2] - f16_lo(g23)) * 16.f, (p[3] - f16_hi(g23)) * 16.f);
-            hi[q4] = h01 | (h23 << 16);
-            lo[q4] = l01 | (l23 << 16);
+            hi[q4] = hw;
+            lo[q4] = lw;
           }
-          *reinterpret_cast<uint4*>(prow + swz<128>(kt, c0 / 16)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-          *reinterpret_cast<uint4*>(prow + swz<128>(kt, (R + c0) / 16)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+          *reinterpret_cast<uint4*>(ptile + swz<128>(kt, (col0 + c0) / 16)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+          *reinterpret_cast<uint4*>(ptile + swz<128>(kt, (R + col0 + c0) / 16)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
         }
-        if (!all) {
+        if (!all && (!kCols || wg == 0)) {
           uint8_t* vrow = sStage + stage * C::kStage + C::kTile + kt * D;
           if (kt >= valid) {  // whatever the row holds
 #pragma unroll
             for (int c = 0; c < D / 16; ++c) reinterpret_cast<uint4*>(vrow)[c] = make_uint4(0u, 0u, 0u, 0u);
           } else if (!main) {
+            const uint32_t* see = sDesc + (buf * 256 + base + kt) * 2;
+            const unsigned long long rows = (unsigned long long)see[0] | (R > 32 ? (unsigned long long)see[1] << 32 : 0ull);
+#pragma unroll 1
             for (int c = 0; c < D / 4; ++c) {
               const uint32_t w = reinterpret_cast<const uint32_t*>(vrow)[c];
               uint32_t nan = ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
@@ -783,22 +823,22 @@ __global__ void __launch_bounds__(kPThreads, 1)
               reinterpret_cast<uint32_t*>(vrow)[c] = w & ~((nan >> 7) * 0xFFu);
               const int chunk = D == 128 ? (c >> 2) ^ (kt & 7) : (c >> 2) ^ ((kt >> 1) & 3);
               for (; nan; nan &= nan - 1)
-                atomicOr(sPoison + buf * 128 + chunk * 16 + (c & 3) * 4 + ((__ffs(nan) - 1) >> 3), (unsigned long long)vis);
+                atomicOr(sPoison + buf * 128 + chunk * 16 + (c & 3) * 4 + ((__ffs(nan) - 1) >> 3), rows);
               sPoisoned[buf] = 1;
             }
           }
         }
         fence_proxy_async_smem();
         tc_fence_before();
-        mbar_arrive(&p_full[wg]);
+        mbar_arrive(&p_full[x]);
       }
       // Sums of P over the warp's keys (transposed reduction), and their reference.
       if (k >= 2) TSV_PWAIT(&unit_free[buf], (k >> 1) - 1);
       {
-        constexpr int kLeft = R >= 32 ? R / 32 : 1;
+        int first = 0;  // row that this thread is left with
 #pragma unroll
         for (int s = 0; s < 5; ++s) {
-          const int half = (R >> s) / 2;
+          const int half = (RW >> s) / 2;
           const int bit = 16 >> s;
           const bool up = lane & bit;
           if (half >= 1) {
@@ -808,14 +848,13 @@ __global__ void __launch_bounds__(kPThreads, 1)
               const float keep = up ? lsum[i + half] : lsum[i];
               lsum[i] = keep + __shfl_xor_sync(0xffffffffu, send, bit);
             }
+            first += up ? half : 0;
           } else {
             lsum[0] += __shfl_xor_sync(0xffffffffu, lsum[0], bit);
           }
         }
-        const int first = R >= 32 ? lane * kLeft : lane >> 1;  // the halvings picked the row's bits from the top
-#pragma unroll
-        for (int i = 0; i < kLeft; ++i) sL[(buf * 8 + warp) * R + first + i] = lsum[i];
-        if (kt < R) sMw[(buf * 2 + wg) * R + kt] = mw;
+        sL[(buf * 8 + warp) * RW + first] = lsum[0];
+        if (lg == 0 && lane < RW) sMw[(buf * 2 + wg) * RW + lane] = mw;
       }
       mbar_arrive(&l_full[buf]);
     }
@@ -827,42 +866,58 @@ __global__ void __launch_bounds__(kPThreads, 1)
     int t = 0, k = 0;
     for (PUnit u = list.first(x0); u.valid; list.next(u), ++k) {
       const int buf = k & 1;
-      float acc[R];
+      uint64_t acc[R / 2];  // rows 2 i and 2 i + 1
 #pragma unroll
-      for (int i = 0; i < R; ++i) acc[i] = 0.f;
-      float mt = -INFINITY;  // thread r < R: running maximum of row r
+      for (int i = 0; i < R / 2; ++i) acc[i] = 0ull;
+      constexpr int kPer = (R + 31) / 32;  // rows of a lane: lane, lane + 32
+      float mt[kPer];                      // their running maxima (each warp keeps its own copy)
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) mt[i] = -INFINITY;
+      float* ab = sAB + lg * 2 * R;        // this warp's factors: rescale, weight of the block
       TSV_PWAIT(&q_full[buf], k >> 1);  // the unit's output rows
       for (int j = u.j; j < u.j1; ++j, ++t) {
         const int x = t & 1;
         TSV_PWAIT(&p_full[x], t >> 1);
-        float* ab = sAB + x * 2 * R;
-        if (d < R) {
-          const float m = sM[x * R + d];
-          const float mn = fmaxf(mt, m);
-          ab[d] = mn == -INFINITY ? 1.f : mt == -INFINITY ? 0.f : fast_exp2(mt - mn);
-          // A block without a maximum holds P against 0 (only NaN scores, or nothing seen: P = 0).
-          ab[R + d] = sSv[x] * (m == -INFINITY ? 1.f : fast_exp2(m - mn));
-          mt = mn;
+        const float sv = sSv[x];
+        bool moved = false;
+        __syncwarp();  // the last block's factors have been read
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+          const int r = lane + 32 * i;
+          if (r < R) {
+            const float m = sM[x * R + r];
+            const float mn = fmaxf(mt[i], m);
+            ab[r] = mn == -INFINITY ? 1.f : mt[i] == -INFINITY ? 0.f : fast_exp2(mt[i] - mn);
+            ab[R + r] = sv * (m == -INFINITY ? 1.f : fast_exp2(m - mn));  // no maximum: P is 0 or NaN
+            moved = moved || mn != mt[i];
+            mt[i] = mn;
+          }
         }
-        named_bar_sync(kBarAcc, 128);
+        __syncwarp();
+        if (__any_sync(0xffffffffu, moved)) {
+#pragma unroll
+          for (int i = 0; i < R / 2; i += 2) {
+            const ulonglong2 al = *reinterpret_cast<const ulonglong2*>(ab + 2 * i);
+            acc[i] = fmul2(acc[i], al.x);
+            acc[i + 1] = fmul2(acc[i + 1], al.y);
+          }
+        }
         TSV_PWAIT(&o_full[x], t >> 1);
         tc_fence_after();
-        const uint32_t o_col = tmem + lane_base + (uint32_t)(2 * R + x * 2 * R);
+        const uint32_t o_col = tmem + lane_base + (uint32_t)(2 * R + x * R);
+        uint32_t h2[2][16];
+        tmem_ld16_nowait(o_col, h2[0]);
 #pragma unroll
         for (int c0 = 0; c0 < R; c0 += 16) {
-          float h[16], l[16];
-          tmem_ld16(o_col + c0, h);
-          tmem_ld16(o_col + R + c0, l);
+          uint32_t(&h)[16] = h2[(c0 >> 4) & 1];
+          tmem_wait_tie(h);
+          if (c0 + 16 < R) tmem_ld16_nowait(o_col + c0 + 16, h2[((c0 >> 4) + 1) & 1]);
 #pragma unroll
-          for (int q4 = 0; q4 < 4; ++q4) {
-            const float4 al = *reinterpret_cast<const float4*>(ab + c0 + 4 * q4);
-            const float4 be = *reinterpret_cast<const float4*>(ab + R + c0 + 4 * q4);
-            const float av[4] = {al.x, al.y, al.z, al.w}, bv[4] = {be.x, be.y, be.z, be.w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int r = c0 + 4 * q4 + e;
-              acc[r] = fmaf(fmaf(l[4 * q4 + e], 0.0625f, h[4 * q4 + e]), bv[e], acc[r] * av[e]);
-            }
+          for (int i = 0; i < 8; i += 2) {
+            const ulonglong2 be = *reinterpret_cast<const ulonglong2*>(ab + R + c0 + 2 * i);
+            const int q = c0 / 2 + i;
+            acc[q] = ffma2((uint64_t)h[2 * i] | ((uint64_t)h[2 * i + 1] << 32), be.x, acc[q]);
+            acc[q + 1] = ffma2((uint64_t)h[2 * i + 2] | ((uint64_t)h[2 * i + 3] << 32), be.y, acc[q + 1]);
           }
         }
         tc_fence_before();
@@ -871,22 +926,30 @@ __global__ void __launch_bounds__(kPThreads, 1)
       // The unit is done: denominators, then its rows or its partials.
       TSV_PWAIT(&l_full[buf], k >> 1);
       float* fin = sFin + buf * R;
-      if (d < R) {
-        float l = 0.f;
+      if (lg == 0) {
 #pragma unroll
-        for (int w = 0; w < 2; ++w) {
-          const float mw = sMw[(buf * 2 + w) * R + d];
-          const float* lw = sL + (buf * 8 + 4 * w) * R + d;
-          const float sum = (lw[0] + lw[R]) + (lw[2 * R] + lw[3 * R]);
-          l += mw == -INFINITY ? sum : sum * fast_exp2(mw - mt);
+        for (int i = 0; i < kPer; ++i) {
+          const int r = lane + 32 * i;
+          if (r >= R) continue;
+          float l = 0.f;
+#pragma unroll
+          for (int w = 0; w < 2; ++w) {
+            if (C::kCols && w != i) continue;  // the group that had the row
+            const int rr = C::kCols ? lane : r;
+            const float mw = sMw[(buf * 2 + w) * C::RW + rr];
+            const float* lw = sL + (buf * 8 + 4 * w) * C::RW + rr;
+            const float sum = (lw[0] + lw[C::RW]) + (lw[2 * C::RW] + lw[3 * C::RW]);
+            l += mw == -INFINITY ? sum : sum * fast_exp2(mw - mt[i]);
+          }
+          fin[r] = l;
         }
-        fin[d] = l;
       }
+      float* of = reinterpret_cast<float*>(acc);
       if (sPoisoned[buf]) {
         const unsigned long long rows = sPoison[buf * 128 + d];
 #pragma unroll
         for (int r = 0; r < R; ++r)
-          if ((rows >> r) & 1ull) acc[r] = NAN;
+          if ((rows >> r) & 1ull) of[r] = NAN;
         sPoison[buf * 128 + d] = 0ull;
       }
       const bool stop = named_bar_or(kBarAcc, 128, dead);  // the same in every thread
@@ -898,7 +961,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
         for (int r = 0; r < R; ++r)
           if (r < rows && live) {
             const float l = fin[r];
-            out[(int64_t)sRow[buf * R + r] * D + d] = __float2bfloat16_rn(l == 0.f ? 0.f : acc[r] / l);
+            out[(int64_t)sRow[buf * R + r] * D + d] = __float2bfloat16_rn(l == 0.f ? 0.f : of[r] / l);
           }
       } else if (!stop) {
         const int slot = 2 * (int)blockIdx.x + (k == 0 ? 0 : 1);
@@ -906,11 +969,13 @@ __global__ void __launch_bounds__(kPThreads, 1)
         float* pm = part_ml + (int64_t)slot * 2 * R;
 #pragma unroll
         for (int r = 0; r < R; ++r)
-          if (r < rows && live) po[r * D + d] = acc[r];
-        if (d < R) {
-          pm[d] = mt;
-          pm[R + d] = fin[d];
+          if (r < rows && live) po[r * D + d] = of[r];
+        if (lg == 0) {
+#pragma unroll
+          for (int i = 0; i < kPer; ++i)
+            if (lane + 32 * i < R) pm[lane + 32 * i] = mt[i];
         }
+        if (d < R) pm[R + d] = fin[d];
         // CTAs cf .. cl share the group; the last to arrive joins.
         __threadfence();
         const int cf = (int)(((u.gx + 1) * ctas - 1) / W), cl = (int)(((u.gx + u.T) * ctas - 1) / W);
@@ -924,20 +989,63 @@ __global__ void __launch_bounds__(kPThreads, 1)
         named_bar_sync(kBarAcc, 128);
         if (*sJoin) {
           __threadfence();
-          for (int r = 0; r < rows; ++r) {
-            float top = -INFINITY, sum = 0.f, o = 0.f;
-            for (int c = cf; c <= cl; ++c) {
-              const int s = 2 * c + ((int64_t)c * W / ctas >= u.gx ? 0 : 1);
-              top = fmaxf(top, __ldcg(part_ml + (int64_t)s * 2 * R + r));
+          // A warp takes 4 rows at a time, a lane 16 bytes of each; the CTAs'
+          // partials are brought to a running maximum in order, two in flight.
+          constexpr int RB = 4, CB = 2, L4 = D / 4;  // lanes of a row: D / 4
+          const int lane_row = lane / L4, d4 = (lane % L4) * 4;
+          constexpr int kRowsPerWarp = 32 / L4;
+          for (int r0 = lg * RB * kRowsPerWarp; r0 < rows; r0 += 4 * RB * kRowsPerWarp) {
+            float top[RB], sum[RB];
+            float4 o[RB];
+#pragma unroll
+            for (int i = 0; i < RB; ++i) {
+              top[i] = -INFINITY;
+              sum[i] = 0.f;
+              o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
             }
-            for (int c = cf; c <= cl; ++c) {
-              const int s = 2 * c + ((int64_t)c * W / ctas >= u.gx ? 0 : 1);
-              const float m = __ldcg(part_ml + (int64_t)s * 2 * R + r);
-              const float w = m == -INFINITY ? 1.f : fast_exp2(m - top);
-              sum += w * __ldcg(part_ml + (int64_t)s * 2 * R + R + r);
-              if (live) o += w * __ldcg(part_o + ((int64_t)s * R + r) * D + d);
+            for (int c0 = cf; c0 <= cl; c0 += CB) {
+              float m[CB][RB], l[CB][RB];
+              float4 v[CB][RB];
+#pragma unroll
+              for (int x = 0; x < CB; ++x) {
+                const int c = c0 + x;
+                const int64_t s = 2 * c + ((int64_t)c * W / ctas >= u.gx ? 0 : 1);
+#pragma unroll
+                for (int i = 0; i < RB; ++i) {
+                  const int r = r0 + i * kRowsPerWarp + lane_row;
+                  m[x][i] = -INFINITY;
+                  l[x][i] = 0.f;
+                  v[x][i] = make_float4(0.f, 0.f, 0.f, 0.f);
+                  if (c <= cl && r < rows) {
+                    m[x][i] = __ldcg(part_ml + s * 2 * R + r);
+                    l[x][i] = __ldcg(part_ml + s * 2 * R + R + r);
+                    v[x][i] = __ldcg(reinterpret_cast<const float4*>(part_o + (s * R + r) * D + d4));
+                  }
+                }
+              }
+#pragma unroll
+              for (int x = 0; x < CB; ++x)
+#pragma unroll
+                for (int i = 0; i < RB; ++i) {
+                  const float t2 = fmaxf(top[i], m[x][i]);
+                  const float f = top[i] == -INFINITY ? 1.f : fast_exp2(top[i] - t2);  // nothing yet: all zero (or NaN)
+                  const float w = m[x][i] == -INFINITY ? 1.f : fast_exp2(m[x][i] - t2);
+                  top[i] = t2;
+                  sum[i] = sum[i] * f + l[x][i] * w;
+                  o[i].x = o[i].x * f + v[x][i].x * w;
+                  o[i].y = o[i].y * f + v[x][i].y * w;
+                  o[i].z = o[i].z * f + v[x][i].z * w;
+                  o[i].w = o[i].w * f + v[x][i].w * w;
+                }
             }
-            if (live) out[(int64_t)sRow[buf * R + r] * D + d] = __float2bfloat16_rn(sum == 0.f ? 0.f : o / sum);
+#pragma unroll
+            for (int i = 0; i < RB; ++i) {
+              const int r = r0 + i * kRowsPerWarp + lane_row;
+              if (r >= rows) continue;
+              const float inv = sum[i] == 0.f ? 0.f : 1.f / sum[i];
+              *reinterpret_cast<uint2*>(out + (int64_t)sRow[buf * R + r] * D + d4) =
+                  make_uint2(pack_bf16x2(o[i].x * inv, o[i].y * inv), pack_bf16x2(o[i].z * inv, o[i].w * inv));
+            }
           }
         }
       }
@@ -952,7 +1060,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
     for (PUnit u = list.first(x0); u.valid; list.next(u)) a.status[u.b] = TSV_ERR_TIMEOUT;
   if (warp == kPMmaWarp) {
     tc_fence_after();
-    tmem_dealloc(tmem, C::kCols);
+    tmem_dealloc(tmem, C::kTmem);
   }
 }
 
