@@ -738,6 +738,32 @@ def test_calls_on_a_given_stream(tsv):
     assert torch.equal(out, want) and (st == 0).all() and x.shape == b.q.shape
 
 
+LONG = [  # page, Hq, Hkv, D, tree, B, prefix, nodes: dozens of key blocks for every SM
+    (16, 16, 16, 128, True, 16, 2500, 9), (128, 64, 8, 128, True, 2, 9000, 20), (64, 64, 8, 64, False, 30, 3000, 1),
+    (32, 96, 24, 64, True, 12, 1700, 8), (32, 32, 32, 128, True, 7, 1900, 64), (16, 8, 2, 128, True, 1, 40000, 7),
+]
+
+
+@pytest.mark.parametrize("case", LONG, ids=lambda c: "-".join(str(x) for x in c))
+def test_attention_over_many_blocks(tsv, case):
+    """Long and ragged batches, the tensor cores' result against the CUDA cores' (which the tests above hold to 64 bits)."""
+    page, Hq, Hkv, D, tree, B, P, n = case
+    rng = np.random.default_rng(P)
+    lens = [(int(rng.integers(P // 2, P + 1)), int(rng.integers(1, n + 1))) for _ in range(B)]
+    b = Batch(tsv, rng, lens, Hq, Hkv, D, page, tree=tree)
+    ws = tsv.paged_tree_attention_workspace(b.q, b.cache, B, max(x for _, x in lens))
+    for _ in range(3):  # a workspace used again and again
+        out, st = b.run(tsv, workspace=ws)
+    ref, st2 = b.run(tsv, flags=1)
+    assert (st == 0).all() and (st2 == 0).all()
+    norm = ref.float().norm()
+    assert (out.float() - ref.float()).norm() <= 6e-3 * norm  # two roundings to bf16 and weights of 8 bits
+    # A value is off by at most 2^-8 + 2^-11 of the weighted sum over |v| and half a step of the result on either side;
+    # both sums are at most the largest |v|.
+    top = float((b.cache.v.float().abs().amax() * b.cache.v_scale.amax()))
+    assert (out.float() - ref.float()).abs().max().item() <= (2.0 ** -8 + 2.0 ** -11 + 2 * 2.0 ** -8) * top
+
+
 @pytest.mark.parametrize("kind", KINDS, ids=lambda k: k[0])
 def test_attention_is_repeatable(tsv, kind):
     b = Batch(tsv, np.random.default_rng(61), [(3000, 20), (1, 1), (700, 64)], 8, 2, 128, 64, dtype=kind[1])

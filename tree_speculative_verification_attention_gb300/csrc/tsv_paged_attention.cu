@@ -2,7 +2,7 @@
 // tensor cores, keys on the TMEM lanes.
 //
 //   S^T = K Q^T       M = 128 keys, N = rows, K = D      (A = K tile, B = Q tile)
-//   O^T = V^T P^T     M = 128 (d), N = rows, K = 128 keys (A = V tile, M-major)
+//   O^T = V^T P^T     M = 128 (d), N = 2 x rows, K = 128 keys (A = V tile, M-major)
 //
 // Both products run on the e4m3 codes themselves, straight from the bytes that
 // TMA brings in: nothing is widened on the way, so a 128-key block of one head
@@ -14,7 +14,9 @@
 //   p = (hi + lo) / 256  relative to the block's own largest score of the
 //                        row: 8 bits down to 2^-10 of it, never off by more
 //                        than 2^-18 of it (128 keys: 2^-11 of the block).
-// Both terms of either accumulate into the same S or O.
+// The terms of q accumulate into the same S; those of p lie side by side on the
+// N axis of one MMA (an MMA of this shape takes its issue time, not its N) and
+// are added in fp32.
 // That the reference maximum is the block's own (not a running one) keeps
 // those bounds whatever the earlier blocks held; O of a block is brought to
 // the running maximum in fp32 registers, which also keeps long sums out of the
@@ -27,12 +29,15 @@
 // device.  A group that a cut goes through leaves fp32 partials in the
 // workspace, and the last of its CTAs to arrive joins them in a fixed order.
 //
-// Roles (16 warps): two softmax warpgroups (warps 0-3 and 4-7; a thread owns a
+// Roles (20 warps): two softmax warpgroups (warps 0-3 and 4-7; a thread owns a
 // key), which take alternate blocks, or, with 64 rows, 32 rows of every block
-// each; the accumulating warpgroup (8-11; a thread owns a d); the TMA producer
-// (12: page ids and scales are looked up a warp's worth ahead); the MMA issuer
-// (13); and two warps that prepare the next unit's Q tiles and tree mask (14,
-// 15).  What a role needs from the rows (maxima, factors) is worked out by
+// each; the accumulating warpgroup (8-11; a thread owns a d); the producers of
+// K and of V (12, 13: page ids and scales are looked up a warp's worth ahead;
+// a page is one TMA box, and a warp issues one in about 100 cycles); the
+// issuers of S and of O (14, 15); and four warps that prepare the next unit's Q
+// tiles and tree mask (16-19).  The register file is split by role.
+//
+// What a role needs from the rows (maxima, factors) is worked out by
 // each of its warps for itself: a block costs a softmax group one barrier and
 // the accumulating group none.
 //
@@ -46,22 +51,27 @@ namespace tsv {
 
 namespace {
 
-constexpr int kPThreads = 512;
-constexpr int kPProducerWarp = 12, kPMmaWarp = 13, kPPrepWarp = 14;
+constexpr int kPThreads = 640;
+constexpr int kPProducerWarp = 12, kPSWarp = 14, kPOWarp = 15, kPPrepWarp = 16;  // K, V producers: 12, 13
+// Registers a thread: 640 x 96 at launch = 256 x 120 + 128 x 112 + 256 x 64.
+constexpr int kPRegs = 96, kPSoftRegs = 120, kPAccRegs = 112, kPRestRegs = 64;
+static_assert(256 * kPSoftRegs + 128 * kPAccRegs + 256 * kPRestRegs <= kPThreads * kPRegs, "register split");
 constexpr int kPBlock = 128;      // keys of a block
 constexpr int kBarSoft = 1;       // and 2: one per softmax warpgroup
-constexpr int kBarAcc = 3, kBarPrep = 4;
+constexpr int kBarAcc = 3;
 
 template <int D, int R>
 struct PCfg {
   static constexpr int kTile = kPBlock * D;                 // K tile
   static constexpr int kVTile = kPBlock * 128;              // 128 d; the upper half stays zero when D = 64
-  static constexpr int kStage = kTile + kVTile;
-  static constexpr int kStages = D == 128 ? 4 : 6;
+  static constexpr int kStages = D == 64 ? 6 : R == 64 ? 4 : 5;
   static constexpr int kQ = R * D;                          // one term of a Q tile
-  static constexpr int kOffStage = 0;
-  static constexpr int kOffP = kOffStage + kStages * kStage;       // [2][128 keys][128 B]
-  static constexpr int kOffQ = kOffP + 2 * kPBlock * 128;          // [2][hi, lo]
+  static constexpr int kOffK = 0;                                  // K ring
+  static constexpr int kOffV = kOffK + kStages * kTile;            // V ring
+  static constexpr int kPRow = R == 64 ? 128 : 64;                 // bytes of a key's P: hi of every row, lo of every row
+  static constexpr int kPTile = kPBlock * kPRow;
+  static constexpr int kOffP = kOffV + kStages * kVTile;           // [2]
+  static constexpr int kOffQ = kOffP + 2 * kPTile;                 // [2][hi, lo]
   static constexpr int kOffDesc = kOffQ + 4 * kQ;                  // u32 [2][256 keys][2]: rows that see the tree key
   static constexpr int kOffPoison = kOffDesc + 2 * 256 * 8;        // u64 [2][128 d]: rows that see a NaN there
   static constexpr int kOffCum = kOffPoison + 2 * 128 * 8;         // i64 [TSV_MAX_BATCH + 1]
@@ -72,21 +82,21 @@ struct PCfg {
   static constexpr bool kCols = R == 64;                           // the groups split the rows, not the blocks
   static constexpr int kOffWmax = kOffRow + 8 * R;                 // f32 [2 groups][2][4 warps][RW]
   static constexpr int kOffPw = kOffWmax + 64 * RW;                // f32 [8 warps][3][RW]: -maxima, sum factors, rescale
-  static constexpr int kOffM = kOffPw + 96 * RW;                   // f32 [2][R]: a block's largest scores
-  static constexpr int kOffAB = kOffM + 8 * R;                     // f32 [4 warps][2][R]: accumulation factors
+  static constexpr int kOffM = kOffPw + 96 * RW;                   // f32 [4][R]: a block's largest scores
+  static constexpr int kOffAB = kOffM + 16 * R;                     // f32 [4 warps][2][R]: accumulation factors
   static constexpr int kOffL = kOffAB + 32 * R;                    // f32 [2][8 warps][RW]
   static constexpr int kOffMw = kOffL + 64 * RW;                   // f32 [2][2 groups][RW]
   static constexpr int kOffFin = kOffMw + 16 * RW;                 // f32 [2][R]: sums of a unit
   static constexpr int kOffScale = kOffFin + 8 * R;                // f32 [stages][20]: (K, V) of 8 pages, V's largest
-  static constexpr int kOffSv = kOffScale + kStages * 80;          // f32 [2]
-  static constexpr int kOffBar = (kOffSv + 8 + 7) & ~7;
-  // kv_full[S], kv_empty[S], s_full[2], p_full[2], o_full[2], o_free[2], q_full[2], unit_free[2], l_full[2], mma_done
-  static constexpr int kBars = 2 * kStages + 15;
+  static constexpr int kOffSv = kOffScale + kStages * 80;               // f32 [4]
+  static constexpr int kOffBar = kOffSv + 16;
+  // k_full[S], k_empty[S], v_full[S], v_empty[S], s_full[4], p_full[4], o_full[2], o_free[2], q_full[2], unit_free[2], l_full[2], mma_done[2]
+  static constexpr int kBars = 4 * kStages + 20;
   static constexpr int kOffMisc = kOffBar + 8 * kBars;
   static constexpr int kSmem = kOffMisc + 64 + 1024;
-  static constexpr uint32_t kTmem = R == 64 ? 256 : R == 32 ? 128 : 64;  // S0 S1 O0 O1, R each
+  static constexpr uint32_t kTmem = 8 * R;  // S0 .. S3 (R each), O0, O1 (2 R each)
   static_assert(kSmem <= 227 * 1024, "shared memory");
-  static_assert(kStage % 1024 == 0 && kQ % 512 == 0 && kOffQ % 1024 == 0, "swizzle atoms");
+  static_assert(kTile % 1024 == 0 && kQ % 512 == 0 && kOffQ % 1024 == 0, "swizzle atoms");
 };
 
 // Swizzled position of 16-byte chunk c of row r in a tile of ROW-byte rows.
@@ -114,6 +124,26 @@ __device__ __forceinline__ uint64_t sdesc_row(uint32_t saddr, uint32_t lbo) {
   uint64_t d = sdesc_sw128(saddr, lbo, 8 * ROW);
   if (ROW == 64) d = (d & ~(7ull << 61)) | (4ull << 61);
   return d;
+}
+
+template <int N>
+__device__ __forceinline__ void setmaxnreg_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void setmaxnreg_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// One lane of the (whole) warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(p));
+  return p != 0;
 }
 
 __device__ __forceinline__ void mbar_expect_tx(uint64_t* bar, uint32_t bytes) {
@@ -244,7 +274,8 @@ __global__ void __launch_bounds__(kPThreads, 1)
   constexpr int S = C::kStages;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* sStage = smem + C::kOffStage;
+  uint8_t* sK = smem + C::kOffK;
+  uint8_t* sV = smem + C::kOffV;
   uint8_t* sP = smem + C::kOffP;
   uint8_t* sQ = smem + C::kOffQ;
   uint32_t* sDesc = reinterpret_cast<uint32_t*>(smem + C::kOffDesc);
@@ -262,11 +293,13 @@ __global__ void __launch_bounds__(kPThreads, 1)
   float* sFin = reinterpret_cast<float*>(smem + C::kOffFin);
   float* sScale = reinterpret_cast<float*>(smem + C::kOffScale);
   float* sSv = reinterpret_cast<float*>(smem + C::kOffSv);
-  uint64_t* kv_full = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
-  uint64_t* kv_empty = kv_full + S;
-  uint64_t* s_full = kv_empty + S;
-  uint64_t* p_full = s_full + 2;
-  uint64_t* o_full = p_full + 2;
+  uint64_t* k_full = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
+  uint64_t* k_empty = k_full + S;
+  uint64_t* v_full = k_empty + S;
+  uint64_t* v_empty = v_full + S;
+  uint64_t* s_full = v_empty + S;
+  uint64_t* p_full = s_full + 4;
+  uint64_t* o_full = p_full + 4;
   uint64_t* o_free = o_full + 2;
   uint64_t* q_full = o_free + 2;
   uint64_t* unit_free = q_full + 2;
@@ -286,24 +319,29 @@ __global__ void __launch_bounds__(kPThreads, 1)
 
   if (tid == 0) {
     for (int s = 0; s < S; ++s) {
-      mbar_init(&kv_full[s], 1);
-      mbar_init(&kv_empty[s], 1);
+      mbar_init(&k_full[s], 1);
+      mbar_init(&k_empty[s], 1);
+      mbar_init(&v_full[s], 1);
+      mbar_init(&v_empty[s], 1);
     }
-    for (int x = 0; x < 2; ++x) {
+    for (int x = 0; x < 4; ++x) {
       mbar_init(&s_full[x], 1);
       mbar_init(&p_full[x], C::kCols ? 256 : 128);
+    }
+    for (int x = 0; x < 2; ++x) {
       mbar_init(&o_full[x], 1);
       mbar_init(&o_free[x], 128);
-      mbar_init(&q_full[x], 64);
+      mbar_init(&q_full[x], 128);
       mbar_init(&unit_free[x], 128);
       mbar_init(&l_full[x], 256);
     }
-    mbar_init(mma_done, 1);
+    mbar_init(&mma_done[0], 1);
+    mbar_init(&mma_done[1], 1);
     *abort_flag = 0;
     sPoisoned[0] = sPoisoned[1] = 0;
     mbar_fence_init();
   }
-  if (warp == kPMmaWarp) {
+  if (warp == kPSWarp) {
     tmem_alloc(tmem_slot, C::kTmem);
     tmem_relinquish();
   }
@@ -314,7 +352,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
   if (D == 64) {  // the upper half of every V stage stays zero
     for (int i = tid; i < S * (C::kVTile / 2 / 16); i += kPThreads) {
       const int st = i / (C::kVTile / 2 / 16), o = i % (C::kVTile / 2 / 16);
-      reinterpret_cast<uint4*>(sStage + st * C::kStage + C::kTile + C::kVTile / 2)[o] = make_uint4(0u, 0u, 0u, 0u);
+      reinterpret_cast<uint4*>(sV + st * C::kVTile + C::kVTile / 2)[o] = make_uint4(0u, 0u, 0u, 0u);
     }
     fence_proxy_async_smem();
   }
@@ -357,8 +395,15 @@ __global__ void __launch_bounds__(kPThreads, 1)
   const int64_t x0 = (int)blockIdx.x < ctas ? (int64_t)blockIdx.x * W / ctas : W;
   PList list{sCum, sReq, a.B, a.G, a.cache.Hkv, R, tree, (int)blockIdx.x < ctas ? ((int64_t)blockIdx.x + 1) * W / ctas : W};
 
-  if (warp == kPProducerWarp) {
-    // ------------------------------------------------------------ producer
+  if (warp == kPProducerWarp || warp == kPProducerWarp + 1) {
+    // ------------------------------------------------------------ producers of K and of V
+    setmaxnreg_dec<kPRestRegs>();
+    const bool is_v = warp != kPProducerWarp;
+    const CUtensorMap* tmap = is_v ? &tmap_v : &tmap_k;
+    uint64_t* full = is_v ? v_full : k_full;
+    uint64_t* empty = is_v ? v_empty : k_empty;
+    uint8_t* ring = is_v ? sV : sK;
+    const int tile = is_v ? C::kVTile : C::kTile;
     // The lanes stand for the pages of the next 32 / per blocks, per pages to
     // a block: lane i holds page i % per of block i / per of its chunk.  Page ids
     // of the next chunk are loaded as a chunk begins, their scales after its
@@ -366,75 +411,77 @@ __global__ void __launch_bounds__(kPThreads, 1)
     const int per = kPBlock >> lps, chunk = 32 >> (7 - lps);  // pages of a block, blocks of a chunk
     const int mine = lane >> (7 - lps), pg = lane & (per - 1);
     struct Look {
-      PUnit u;
-      int id, pages;  // of the block; id -1: no keys in this lane's page
+      int id, pages, g, tiles;  // id -1: no keys in this lane's page
     };
-    auto advance = [&](PUnit& u, int blocks) {
-      while (u.valid && blocks > 0) {
+    PUnit u = list.first(x0);  // the unit and block of this lane's page
+    auto advance = [&](int n) {
+      while (u.valid && n > 0) {
         const int left = u.j1 - u.j;
-        if (blocks < left) {
-          u.j += blocks;
+        if (n < left) {
+          u.j += n;
           return;
         }
-        blocks -= left;
+        n -= left;
         list.next(u);
       }
     };
     auto look_id = [&](Look& k) {
       k.id = -1;
       k.pages = 0;
-      if (!k.u.valid) return;
-      const bool main = k.u.j < k.u.nmain;
-      const int block = main ? k.u.j : k.u.j - k.u.nmain;
-      const int keys = (main ? k.u.P : tree ? k.u.n : 0) - block * kPBlock;
+      k.g = u.g;
+      k.tiles = u.tiles;
+      if (!u.valid) return;
+      const bool main = u.j < u.nmain;
+      const int block = main ? u.j : u.j - u.nmain;
+      const int keys = (main ? u.P : tree ? u.n : 0) - block * kPBlock;
       k.pages = (max(0, min(keys, kPBlock)) + (1 << lps) - 1) >> lps;
-      const tsv_page_table& t = main ? a.table : a.tree_table;
-      if (pg < k.pages) k.id = __ldg(t.ids_d + (int64_t)k.u.b * t.stride + block * per + pg);
+      const tsv_page_table& pt = main ? a.table : a.tree_table;
+      if (pg < k.pages) k.id = __ldg(pt.ids_d + (int64_t)u.b * pt.stride + block * per + pg);
     };
-    auto look_scale = [&](const Look& k, float& ks, float& vs) {
-      ks = vs = 0.f;
-      if (k.u.valid && (uint32_t)k.id < (uint32_t)a.cache.num_pages) {
-        ks = __ldg(a.cache.k_scale_d + (int64_t)k.id * a.cache.Hkv + k.u.g);
-        vs = __ldg(a.cache.v_scale_d + (int64_t)k.id * a.cache.Hkv + k.u.g);
+    // V's producer brings both scales: V's tile is held until the block is done,
+    // so whoever waits for it sees this phase of its barrier (K's goes on).
+    auto look_scale = [&](const Look& k) {
+      float2 s = make_float2(0.f, 0.f);
+      if (is_v && (uint32_t)k.id < (uint32_t)a.cache.num_pages) {
+        const int64_t at = (int64_t)k.id * a.cache.Hkv + k.g;
+        s = make_float2(__ldg(a.cache.k_scale_d + at), __ldg(a.cache.v_scale_d + at));
       }
+      return s;
     };
     Look c0, c1;
-    float ks0, vs0, ks1 = 0.f, vs1 = 0.f;
-    c0.u = list.first(x0);
-    advance(c0.u, mine);
+    advance(mine);
     look_id(c0);
-    look_scale(c0, ks0, vs0);
-    const int blocks = (int)(list.x1 - x0);
+    float2 sc0 = look_scale(c0), sc1 = make_float2(0.f, 0.f);
+    const int blocks = __shfl_sync(0xffffffffu, (int)(list.x1 - x0), 0);
     int t = 0, st = 0, ph = 0;
     while (t < blocks) {
-      c1.u = c0.u;
-      advance(c1.u, chunk);
+      advance(chunk);
       look_id(c1);
+      float top = sc0.y;  // the block's largest scale of V
+      for (int o = per >> 1; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      // V's scale relative to the block's largest goes to P, with its 256.
+      sc0.y = top > 0.f ? __fdividef(sc0.y, top) * 256.f : 0.f;
       for (int i = 0; i < chunk && t < blocks; ++i, ++t) {
-        if (t >= S) TSV_PWAIT(&kv_empty[st], ph ^ 1);
+        if (t >= S) TSV_PWAIT(&empty[st], ph ^ 1);
         if (__any_sync(0xffffffffu, dead || *abort_v)) break;
-        const bool turn = mine == i;
-        if (turn && pg == 0 && c0.pages > 0) mbar_expect_tx(&kv_full[st], 2u * (uint32_t)((c0.pages << lps) * D));
-        __syncwarp();
-        if (turn && pg < c0.pages) {
-          // Pages that several row tiles read stay in L2.
-          const uint64_t pol = c0.u.tiles > 1 ? l2_policy_evict_last() : l2_policy_evict_first();
-          uint8_t* kt = sStage + st * C::kStage + (pg << lps) * D;
-          tma_load_4d(kt, &tmap_k, &kv_full[st], 0, c0.u.g, 0, c0.id, pol);
-          tma_load_4d(kt + C::kTile, &tmap_v, &kv_full[st], 0, c0.u.g, 0, c0.id, pol);
+        const int src = i << (7 - lps);
+        const int pages = __shfl_sync(0xffffffffu, c0.pages, src);
+        const int g = __shfl_sync(0xffffffffu, c0.g, src);
+        // Pages that several row tiles read stay in L2.
+        const uint64_t pol = __shfl_sync(0xffffffffu, c0.tiles, src) > 1 ? l2_policy_evict_last() : l2_policy_evict_first();
+        if (pages > 0 && elect_one()) mbar_expect_tx(&full[st], (uint32_t)((pages << lps) * D));
+        for (int p = 0; p < pages; ++p) {
+          const int id = __shfl_sync(0xffffffffu, c0.id, src + p);
+          if (elect_one()) tma_load_4d(ring + st * tile + (p << lps) * D, tmap, &full[st], 0, g, 0, id, pol);
         }
-        if (i == 0) look_scale(c1, ks1, vs1);
-        // V's scale relative to the block's largest goes to P, with its 256.
-        float top = vs0;
-        for (int o = per >> 1; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        if (turn) {
+        if (i == 0) sc1 = look_scale(c1);
+        if (is_v && mine == i) {
           float* sc = sScale + st * 20;
-          sc[2 * pg] = ks0;
-          sc[2 * pg + 1] = top > 0.f ? __fdividef(vs0, top) * 256.f : 0.f;
+          *reinterpret_cast<float2*>(sc + 2 * pg) = sc0;
           if (pg == 0) sc[16] = top * (1.f / 256.f);
         }
         __syncwarp();
-        if (turn && pg == 0) mbar_arrive(&kv_full[st]);
+        if (elect_one()) mbar_arrive(&full[st]);
         if (++st == S) {
           st = 0;
           ph ^= 1;
@@ -442,96 +489,92 @@ __global__ void __launch_bounds__(kPThreads, 1)
       }
       if (__any_sync(0xffffffffu, dead || *abort_v)) break;
       c0 = c1;
-      ks0 = ks1;
-      vs0 = vs1;
+      sc0 = sc1;
     }
     // Every copy has landed before the CTA leaves (whatever the other roles did).
-    for (int x = (t > S ? t - S : 0); x < t; ++x) mbar_wait(&kv_full[x % S], (x / S) & 1, nullptr);
-  } else if (warp == kPMmaWarp) {
-    // ------------------------------------------------------------ MMA issuer
-    if (lane == 0) {
-      const uint32_t sa = smem_u32(sStage), qa = smem_u32(sQ), pa = smem_u32(sP);
-      const uint64_t dK0 = sdesc_row<D>(sa, 16);
-      const uint64_t dQ0 = sdesc_row<D>(qa, 16);
-      const uint64_t dV0 = sdesc_row<D>(sa + C::kTile, kPBlock * 64);
-      const uint64_t dP0 = sdesc_row<128>(pa, kPBlock * 128);
-      const uint32_t idS = idesc_e4m3(kPBlock, R, 0, 0);
-      const uint32_t idO = idesc_e4m3(128, R, 1, 1);
-      struct Cursor {
-        PUnit u;
-        int t, st, ph, k;  // block and unit counts of this CTA
-        bool first;
-      };
-      auto step = [&](Cursor& c) {
-        ++c.t;
-        if (++c.st == S) {
-          c.st = 0;
-          c.ph ^= 1;
-        }
-        c.first = false;
-        if (++c.u.j >= c.u.j1) {
-          list.next(c.u);
-          ++c.k;
-          c.first = true;
-        }
-      };
-      Cursor xs{list.first(x0), 0, 0, 0, 0, true};
-      Cursor xp = xs;
-      uint64_t t_idle = 0;
-      uint32_t idle = 0;
-      while (xp.u.valid) {
-        bool did = false;
-        if (xs.u.valid && xs.t <= xp.t + 1 && (!xs.first || mbar_test_wait(&q_full[xs.k & 1], (xs.k >> 1) & 1)) &&
-            mbar_test_wait(&kv_full[xs.st], xs.ph)) {
-          tc_fence_after();
-          const uint64_t dk = dK0 + (uint64_t)(xs.st * (C::kStage >> 4));
-          const uint64_t dq = dQ0 + (uint64_t)((xs.k & 1) * (2 * C::kQ >> 4));
-          const uint32_t dst = tmem + (uint32_t)((xs.t & 1) * R);
+    for (int x = (t > S ? t - S : 0); x < t; ++x) mbar_wait(&full[x % S], (x / S) & 1, nullptr);
+  } else if (warp == kPSWarp) {
+    // ------------------------------------------------------------ issuer of S
+    setmaxnreg_dec<kPRestRegs>();
+    // S(t) needs its unit's Q, the block's K, and its buffer: the softmax of
+    // block t - 4 has read it.
+    const uint64_t dK0 = sdesc_row<D>(smem_u32(sK), 16);
+    const uint64_t dQ0 = sdesc_row<D>(smem_u32(sQ), 16);
+    const uint32_t idS = idesc_e4m3(kPBlock, R, 0, 0);
+    int t = 0, st = 0, ph = 0, k = 0;
+    for (PUnit u = list.first(x0); u.valid; list.next(u), ++k) {
+      TSV_PWAIT(&q_full[k & 1], k >> 1);
+      const uint64_t dq = dQ0 + (uint64_t)((k & 1) * (2 * C::kQ >> 4));
+      const int blocks = __shfl_sync(0xffffffffu, u.j1 - u.j, 0);
+      for (int i = 0; i < blocks; ++i, ++t) {
+        TSV_PWAIT(&k_full[st], ph);
+        if (t >= 4) TSV_PWAIT(&p_full[t & 3], (t >> 2) - 1);
+        if (__any_sync(0xffffffffu, dead)) break;
+        tc_fence_after();
+        if (elect_one()) {
+          const uint64_t dk = dK0 + (uint64_t)(st * (C::kTile >> 4));
+          const uint32_t dst = tmem + (uint32_t)((t & 3) * R);
 #pragma unroll
           for (int term = 0; term < 2; ++term)
 #pragma unroll
             for (int kk = 0; kk < D / 32; ++kk)
               umma_e4m3(dst, dk + kk * 2, dq + term * (C::kQ >> 4) + kk * 2, idS, term + kk > 0 ? 1u : 0u);
-          umma_commit(&s_full[xs.t & 1]);
-          step(xs);
-          did = true;
+          umma_commit(&s_full[t & 3]);
+          umma_commit(&k_empty[st]);
         }
-        if (xp.t < xs.t && mbar_test_wait(&p_full[xp.t & 1], (xp.t >> 1) & 1)) {
-          tc_fence_after();
-          const uint64_t dv = dV0 + (uint64_t)(xp.st * (C::kStage >> 4));
-          const uint64_t dp = dP0 + (uint64_t)((xp.t & 1) * (kPBlock * 128 >> 4));
-          const uint32_t dst = tmem + (uint32_t)(2 * R + (xp.t & 1) * R);
-#pragma unroll
-          for (int term = 0; term < 2; ++term)
-#pragma unroll
-            for (int kk = 0; kk < kPBlock / 32; ++kk)
-              umma_e4m3(dst, dv + kk * (32 * D >> 4), dp + term * (R >> 4) + kk * (32 * 128 >> 4), idO, term + kk > 0 ? 1u : 0u);
-          umma_commit(&o_full[xp.t & 1]);
-          umma_commit(&kv_empty[xp.st]);
-          step(xp);
-          did = true;
-        }
-        if (did) {
-          t_idle = 0;
-          idle = 0;
-        } else if ((++idle & 1023u) == 0) {
-          const uint64_t now = global_timer_ns();
-          if (t_idle == 0) t_idle = now;
-          if (*abort_v || now - t_idle > kWaitLimitNs) {
-            *abort_v = 1;
-            break;
-          }
+        __syncwarp();
+        if (++st == S) {
+          st = 0;
+          ph ^= 1;
         }
       }
-      umma_commit(mma_done);
-      mbar_wait(mma_done, 0, nullptr);
+      if (__any_sync(0xffffffffu, dead)) break;
     }
+    if (elect_one()) umma_commit(&mma_done[0]);
+    __syncwarp();
+    mbar_wait(&mma_done[0], 0, nullptr);
+  } else if (warp == kPOWarp) {
+    // ------------------------------------------------------------ issuer of O
+    setmaxnreg_dec<kPRestRegs>();
+    // O(t) needs P of the block and its own buffer: the accumulating group has
+    // read block t - 2.
+    const uint64_t dV0 = sdesc_row<D>(smem_u32(sV), kPBlock * 64);
+    const uint64_t dP0 = sdesc_row<C::kPRow>(smem_u32(sP), kPBlock * 128);
+    const uint32_t idO = idesc_e4m3(128, 2 * R, 1, 1);
+    const int blocks = __shfl_sync(0xffffffffu, (int)(list.x1 - x0), 0);
+    int st = 0, ph = 0;
+    for (int t = 0; t < blocks; ++t) {
+      TSV_PWAIT(&v_full[st], ph);
+      if (t >= 2) TSV_PWAIT(&o_free[t & 1], (t >> 1) - 1);
+      TSV_PWAIT(&p_full[t & 3], t >> 2);
+      if (__any_sync(0xffffffffu, dead)) break;
+      tc_fence_after();
+      if (elect_one()) {
+        const uint64_t dv = dV0 + (uint64_t)(st * (C::kVTile >> 4));
+        const uint64_t dp = dP0 + (uint64_t)((t & 1) * (C::kPTile >> 4));
+        const uint32_t dst = tmem + (uint32_t)(4 * R + (t & 1) * 2 * R);
+#pragma unroll
+        for (int kk = 0; kk < kPBlock / 32; ++kk)
+          umma_e4m3(dst, dv + kk * (32 * D >> 4), dp + kk * (32 * C::kPRow >> 4), idO, kk > 0 ? 1u : 0u);
+        umma_commit(&o_full[t & 1]);
+        umma_commit(&v_empty[st]);
+      }
+      __syncwarp();
+      if (++st == S) {
+        st = 0;
+        ph ^= 1;
+      }
+    }
+    if (elect_one()) umma_commit(&mma_done[1]);
+    __syncwarp();
+    mbar_wait(&mma_done[1], 0, nullptr);
   } else if (warp >= kPPrepWarp) {
     // ------------------------------------------------------------ Q tiles and tree masks
+    setmaxnreg_dec<kPRestRegs>();
     const int q = warp - kPPrepWarp;
-    constexpr int E = D / 32;                    // elements of a row per lane
-    constexpr int kMine = R / 2;                 // rows of this warp: kMine q ..
-    constexpr int kBatch = kMine < 16 ? kMine : 16;  // loaded together
+    constexpr int E = D / 32;        // elements of a row per lane
+    constexpr int kMine = R / 4;     // rows of this warp, r_lo ..
+    const int r_lo = kMine * q;
     int k = 0;
     for (PUnit u = list.first(x0); u.valid; list.next(u), ++k) {
       const int buf = k & 1;
@@ -540,101 +583,102 @@ __global__ void __launch_bounds__(kPThreads, 1)
       const int row0 = u.tile * R;
       const int rows = min(R, u.n * a.G - row0);
       // Row r of the tile: node (row0 + r) / G, query head g G + (row0 + r) % G.
-      // Lane i knows row kMine q + i.
+      // Lane i knows row r_lo + i.
       int64_t at_q = 0;
+      const bool on = lane < kMine && r_lo + lane < rows;
       if (lane < kMine) {
-        const int r = kMine * q + lane;
-        const int gr = row0 + r, node = gr / a.G, head = u.g * a.G + (gr - node * a.G);
-        sRow[buf * R + r] = r < rows ? (u.off + node) * a.Hq + head : -1;
-        if (r < rows) at_q = (int64_t)(u.off + node) * a.qs_n + (int64_t)head * a.qs_h;
+        const int r = r_lo + lane;
+        const int gr = row0 + r;
+        const int node = gr / a.G;
+        const int head = u.g * a.G + (gr - node * a.G);
+        sRow[buf * R + r] = on ? (u.off + node) * a.Hq + head : -1;
+        if (on) at_q = (int64_t)(u.off + node) * a.qs_n + (int64_t)head * a.qs_h;
       }
       uint8_t* hi = sQ + buf * 2 * C::kQ;
       uint8_t* lo = hi + C::kQ;
-#pragma unroll 1
-      for (int r0 = 0; r0 < kMine; r0 += kBatch) {
-        uint32_t raw[kBatch][E / 2];
+      uint32_t raw[kMine][E / 2];
 #pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-          const int64_t at = __shfl_sync(0xffffffffu, at_q, r0 + i);
+      for (int i = 0; i < kMine; ++i) {
+        const int64_t at = __shfl_sync(0xffffffffu, at_q, i);
 #pragma unroll
-          for (int e = 0; e < E / 2; ++e) raw[i][e] = 0u;
-          if (kMine * q + r0 + i < rows) {
-            const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.q) + at + lane * E;
-            if constexpr (E == 4) {
-              const uint2 w = __ldg(reinterpret_cast<const uint2*>(src));
-              raw[i][0] = w.x;
-              raw[i][1] = w.y;
-            } else {
-              raw[i][0] = __ldg(reinterpret_cast<const uint32_t*>(src));
-            }
-          }
-        }
-#pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-          const int r = kMine * q + r0 + i;
-          uint32_t top = 0u;
-#pragma unroll
-          for (int e = 0; e < E / 2; ++e) top = max(top, max((raw[i][e] << 16) & 0x7FFF0000u, raw[i][e] & 0x7FFF0000u));
-          top = __reduce_max_sync(0xffffffffu, top);
-          const bool fine = top < 0x7F800000u;  // no infinity, no NaN in the row
-          // The largest value moves to [128, 256): exponent 134 as biased.
-          const int up = top == 0u ? 0 : max(-120, min(120, 134 - (int)(top >> 23)));
-          const float mul = __uint_as_float((uint32_t)(127 + up) << 23);
-          if (lane == 0) sFr[buf * R + r] = __uint_as_float((uint32_t)(127 - up) << 23) * (a.scale * 1.4426950408889634f);
-          uint32_t wh = 0u, wl = 0u;
-#pragma unroll
-          for (int e = 0; e < E / 2; ++e) {
-            // A row with an infinity or a NaN is NaN throughout (its scores are).
-            const float y0 = fine ? __uint_as_float(raw[i][e] << 16) * mul : NAN;
-            const float y1 = fine ? __uint_as_float(raw[i][e] & 0xFFFF0000u) * mul : NAN;
-            const uint32_t h2 = e4m3x2(y0, y1), f2 = f16x2_of_e4m3x2(h2);
-            wh |= h2 << (16 * e);
-            wl |= e4m3x2(y0 - f16_lo(f2), y1 - f16_hi(f2)) << (16 * e);
-          }
-          const uint32_t at = swz<D>(r, lane * E / 16) + (lane * E) % 16;
+        for (int e = 0; e < E / 2; ++e) raw[i][e] = 0u;
+        if (r_lo + i < rows) {
+          const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.q) + at + lane * E;
           if constexpr (E == 4) {
-            *reinterpret_cast<uint32_t*>(hi + at) = wh;
-            *reinterpret_cast<uint32_t*>(lo + at) = wl;
+            const uint2 w = __ldg(reinterpret_cast<const uint2*>(src));
+            raw[i][0] = w.x;
+            raw[i][1] = w.y;
           } else {
-            *reinterpret_cast<uint16_t*>(hi + at) = (uint16_t)wh;
-            *reinterpret_cast<uint16_t*>(lo + at) = (uint16_t)wl;
+            raw[i][0] = __ldg(reinterpret_cast<const uint32_t*>(src));
           }
         }
       }
-      // Rows that see tree key j, 32 rows a warp: word q of sDesc[buf][j].
-      if (tree && u.j1 > u.nmain) {
+#pragma unroll
+      for (int i = 0; i < kMine; ++i) {
+        const int r = r_lo + i;
+        uint32_t top = 0u;
+#pragma unroll
+        for (int e = 0; e < E / 2; ++e) top = max(top, max((raw[i][e] << 16) & 0x7FFF0000u, raw[i][e] & 0x7FFF0000u));
+        top = __reduce_max_sync(0xffffffffu, top);
+        const bool fine = top < 0x7F800000u;  // no infinity, no NaN in the row
+        // The largest value moves to [128, 256): exponent 134 as biased.
+        const int up = top == 0u ? 0 : max(-120, min(120, 134 - (int)(top >> 23)));
+        const float mul = __uint_as_float((uint32_t)(127 + up) << 23);
+        if (lane == 0) sFr[buf * R + r] = __uint_as_float((uint32_t)(127 - up) << 23) * (a.scale * 1.4426950408889634f);
+        uint32_t wh = 0u, wl = 0u;
+#pragma unroll
+        for (int e = 0; e < E / 2; ++e) {
+          // A row with an infinity or a NaN is NaN throughout (its scores are).
+          const float y0 = fine ? __uint_as_float(raw[i][e] << 16) * mul : NAN;
+          const float y1 = fine ? __uint_as_float(raw[i][e] & 0xFFFF0000u) * mul : NAN;
+          const uint32_t h2 = e4m3x2(y0, y1), f2 = f16x2_of_e4m3x2(h2);
+          wh |= h2 << (16 * e);
+          wl |= e4m3x2(y0 - f16_lo(f2), y1 - f16_hi(f2)) << (16 * e);
+        }
+        const uint32_t at = swz<D>(r, lane * E / 16) + (lane * E) % 16;
+        if constexpr (E == 4) {
+          *reinterpret_cast<uint32_t*>(hi + at) = wh;
+          *reinterpret_cast<uint32_t*>(lo + at) = wl;
+        } else {
+          *reinterpret_cast<uint16_t*>(hi + at) = (uint16_t)wh;
+          *reinterpret_cast<uint16_t*>(lo + at) = (uint16_t)wl;
+        }
+      }
+      // Rows that see tree key j: word q of sDesc[buf][j] holds rows 32 q .. (two warps).
+      if (tree && u.j1 > u.nmain && q < 2) {
         const int r = q * 32 + lane;
-        const bool on = r < rows;
-        const int node = on ? (row0 + r) / a.G : 0;
+        const bool has = r < rows;
+        const int i0 = has ? (row0 + r) / a.G : 0;  // the row's node
         for (int w = 0; w < (u.n + 31) / 32; ++w) {
           uint32_t bits = 0u;
-          if (on) {
-            const int left = node + 1 - 32 * w;
-            bits = a.anc ? __ldg(a.anc + (int64_t)(u.off + node) * TSV_ANC_WORDS + w)
+          if (has) {
+            const int left = i0 + 1 - 32 * w;
+            bits = a.anc ? __ldg(a.anc + (int64_t)(u.off + i0) * TSV_ANC_WORDS + w)
                          : (left >= 32 ? 0xFFFFFFFFu : left > 0 ? (1u << left) - 1u : 0u);
           }
-          uint32_t mine = 0u;
+          uint32_t see = 0u;
 #pragma unroll
           for (int i = 0; i < 32; ++i) {
             const uint32_t m = __ballot_sync(0xffffffffu, (bits >> i) & 1u);
-            if (lane == i) mine = m;
+            if (lane == i) see = m;
           }
-          sDesc[(buf * 256 + w * 32 + lane) * 2 + q] = mine;
+          sDesc[(buf * 256 + w * 32 + lane) * 2 + q] = see;
         }
       }
       fence_proxy_async_smem();
       mbar_arrive(&q_full[buf]);
     }
     // Every request's lengths and page ids are checked by one CTA.
-    for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
+    for (int b = blockIdx.x; q == 0 && b < a.B; b += gridDim.x) {
       PagedRequest r;
       bool bad = !paged_request(a, b, &r);
-      if (!bad) bad = paged_bad_page(a, b, r, tid - 32 * kPPrepWarp, 64);
-      bad = named_bar_or(kBarPrep, 64, bad);
-      if (tid == 32 * kPPrepWarp) a.status[b] = bad ? TSV_ERR_INVALID_ARG : TSV_OK;
+      if (!bad) bad = paged_bad_page(a, b, r, lane, 32);
+      bad = __any_sync(0xffffffffu, bad);
+      if (lane == 0) a.status[b] = bad ? TSV_ERR_INVALID_ARG : TSV_OK;
     }
   } else if (warp < 8) {
     // ------------------------------------------------------------ softmax: a thread owns a key
+    setmaxnreg_inc<kPSoftRegs>();
     constexpr int RW = C::RW;
     constexpr bool kCols = C::kCols;
     const int wg = warp >> 2, lg = warp & 3;
@@ -658,8 +702,8 @@ __global__ void __launch_bounds__(kPThreads, 1)
           ph ^= 1;
         }
         if (!kCols && (t & 1) != wg) continue;
-        const int x = t & 1;
-        const uint32_t s_col = tmem + lane_base + (uint32_t)(x * R + col0);
+        const int x = t & 1, x4 = t & 3;
+        const uint32_t s_col = tmem + lane_base + (uint32_t)(x4 * R + col0);
         const bool main = j < u.nmain;
         const int base = (main ? j : j - u.nmain) * kPBlock;
         const int valid = max(0, min(kPBlock, (main ? u.P : tree ? u.n : 0) - base));
@@ -672,12 +716,12 @@ __global__ void __launch_bounds__(kPThreads, 1)
         };
         float* wmax = sWmax + ((wg * 2 + (nth & 1)) * 4) * RW;
         ++nth;
-        TSV_PWAIT(&s_full[x], t >> 1);
+        TSV_PWAIT(&s_full[x4], t >> 2);
         tc_fence_after();
         uint32_t sa[RW / 2], sb[RW / 2];  // the warp's keys 0-15 and 16-31
         tmem_ld_16x256(s_col, sa);
         tmem_ld_16x256(s_col + (16u << 16), sb);
-        TSV_PWAIT(&kv_full[stage], phase);
+        TSV_PWAIT(&v_full[stage], phase);
         const float2* sc = reinterpret_cast<const float2*>(sScale + stage * 20);
         const float fa = sc[(lg * 32) >> lps].x, fb = sc[(lg * 32 + 16) >> lps].x;
         const float2 mine = sc[kt >> lps];  // K's scale; 256 x V's, relative to the block's largest
@@ -736,8 +780,9 @@ __global__ void __launch_bounds__(kPThreads, 1)
         named_bar_sync(kBarSoft + wg, 128);
         // Every warp works out the rows' maxima and factors for itself.
         bool moved = false;
+        float m = 0.f;
         if (lane < RW) {
-          float m = fmaxf(fmaxf(wmax[lane], wmax[RW + lane]), fmaxf(wmax[2 * RW + lane], wmax[3 * RW + lane])) * fr;
+          m = fmaxf(fmaxf(wmax[lane], wmax[RW + lane]), fmaxf(wmax[2 * RW + lane], wmax[3 * RW + lane])) * fr;
           if (!(m > -INFINITY)) m = -INFINITY;  // nothing seen, or NaN scores only: P is 0 or NaN
           const float mn = fmaxf(mw, m);
           pw[lane] = m == -INFINITY ? 0.f : -m;
@@ -745,16 +790,16 @@ __global__ void __launch_bounds__(kPThreads, 1)
           pw[2 * RW + lane] = mn == -INFINITY ? 1.f : mw == -INFINITY ? 0.f : fast_exp2(mw - mn);
           moved = mn != mw;
           mw = mn;
-          // The accumulating group's copy goes out once that group has read
-          // this buffer's last block (its maxima and O, hence P has been used).
-          if (lg == 0) {
-            if (t >= 2 && !dead && !mbar_wait(&o_free[x], ((t >> 1) - 1) & 1, abort_v)) dead = true;
-            sM[x * R + col0 + lane] = m;
-            if (lane == 0 && col0 == 0) sSv[x] = sScale[stage * 20 + 16];
-          }
         }
         __syncwarp();
-        if (t >= 2) TSV_PWAIT(&o_free[x], (t >> 1) - 1);
+        // P's buffer is free once PV of the block before last is done.  That PV
+        // waited for the accumulating group to be through with block t - 4,
+        // so the group's copies of the maxima (4 deep) are free too.
+        if (t >= 2) TSV_PWAIT(&o_full[x], (t >> 1) - 1);
+        if (lg == 0 && lane < RW) {
+          sM[x4 * R + col0 + lane] = m;
+          if (lane == 0 && col0 == 0) sSv[x4] = sScale[stage * 20 + 16];
+        }
         if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll
           for (int i = 0; i < RW; i += 4) {
@@ -765,7 +810,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
             lsum[i + 3] *= al.w;
           }
         }
-        uint8_t* ptile = sP + x * (kPBlock * 128);
+        uint8_t* ptile = sP + x * C::kPTile;
         const uint64_t fk2 = f2_pack(mine.x, mine.x), fv2 = f2_pack(mine.y, mine.y);
 #pragma unroll
         for (int c0 = 0; c0 < RW; c0 += 16) {
@@ -804,19 +849,27 @@ __global__ void __launch_bounds__(kPThreads, 1)
             hi[q4] = hw;
             lo[q4] = lw;
           }
-          *reinterpret_cast<uint4*>(ptile + swz<128>(kt, (col0 + c0) / 16)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-          *reinterpret_cast<uint4*>(ptile + swz<128>(kt, (R + col0 + c0) / 16)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+          *reinterpret_cast<uint4*>(ptile + swz<C::kPRow>(kt, (col0 + c0) / 16)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+          *reinterpret_cast<uint4*>(ptile + swz<C::kPRow>(kt, (R + col0 + c0) / 16)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
         }
         if (!all && (!kCols || wg == 0)) {
-          uint8_t* vrow = sStage + stage * C::kStage + C::kTile + kt * D;
+          uint8_t* vrow = sV + stage * C::kVTile + kt * D;
           if (kt >= valid) {  // whatever the row holds
 #pragma unroll
             for (int c = 0; c < D / 16; ++c) reinterpret_cast<uint4*>(vrow)[c] = make_uint4(0u, 0u, 0u, 0u);
           } else if (!main) {
+            uint32_t any = 0u;
+#pragma unroll
+            for (int c = 0; c < D / 16; ++c) {
+              const uint4 w = reinterpret_cast<const uint4*>(vrow)[c];
+              any |= ((w.x & 0x7F7F7F7Fu) + 0x01010101u) | ((w.y & 0x7F7F7F7Fu) + 0x01010101u) |
+                     ((w.z & 0x7F7F7F7Fu) + 0x01010101u) | ((w.w & 0x7F7F7F7Fu) + 0x01010101u);
+            }
+            any &= 0x80808080u;
             const uint32_t* see = sDesc + (buf * 256 + base + kt) * 2;
             const unsigned long long rows = (unsigned long long)see[0] | (R > 32 ? (unsigned long long)see[1] << 32 : 0ull);
 #pragma unroll 1
-            for (int c = 0; c < D / 4; ++c) {
+            for (int c = 0; any && c < D / 4; ++c) {
               const uint32_t w = reinterpret_cast<const uint32_t*>(vrow)[c];
               uint32_t nan = ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
               if (nan == 0u) continue;
@@ -830,7 +883,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
         }
         fence_proxy_async_smem();
         tc_fence_before();
-        mbar_arrive(&p_full[x]);
+        mbar_arrive(&p_full[x4]);
       }
       // Sums of P over the warp's keys (transposed reduction), and their reference.
       if (k >= 2) TSV_PWAIT(&unit_free[buf], (k >> 1) - 1);
@@ -860,6 +913,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
     }
   } else {
     // ------------------------------------------------------------ accumulation: a thread owns a d
+    setmaxnreg_inc<kPAccRegs>();
     const int d = tid & 127, lg = warp & 3;
     const uint32_t lane_base = (uint32_t)(lg * 32) << 16;
     const bool live = d < D;
@@ -876,16 +930,16 @@ __global__ void __launch_bounds__(kPThreads, 1)
       float* ab = sAB + lg * 2 * R;        // this warp's factors: rescale, weight of the block
       TSV_PWAIT(&q_full[buf], k >> 1);  // the unit's output rows
       for (int j = u.j; j < u.j1; ++j, ++t) {
-        const int x = t & 1;
-        TSV_PWAIT(&p_full[x], t >> 1);
-        const float sv = sSv[x];
+        const int x = t & 1, x4 = t & 3;
+        TSV_PWAIT(&p_full[x4], t >> 2);
+        const float sv = sSv[x4];
         bool moved = false;
         __syncwarp();  // the last block's factors have been read
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
           const int r = lane + 32 * i;
           if (r < R) {
-            const float m = sM[x * R + r];
+            const float m = sM[x4 * R + r];
             const float mn = fmaxf(mt[i], m);
             ab[r] = mn == -INFINITY ? 1.f : mt[i] == -INFINITY ? 0.f : fast_exp2(mt[i] - mn);
             ab[R + r] = sv * (m == -INFINITY ? 1.f : fast_exp2(m - mn));  // no maximum: P is 0 or NaN
@@ -904,20 +958,30 @@ __global__ void __launch_bounds__(kPThreads, 1)
         }
         TSV_PWAIT(&o_full[x], t >> 1);
         tc_fence_after();
-        const uint32_t o_col = tmem + lane_base + (uint32_t)(2 * R + x * R);
-        uint32_t h2[2][16];
+        const uint32_t o_col = tmem + lane_base + (uint32_t)(4 * R + x * 2 * R);
+        uint32_t h2[2][16], l2[2][16];  // hi and lo of this chunk of 16 rows and the next
         tmem_ld16_nowait(o_col, h2[0]);
+        tmem_ld16_nowait(o_col + R, l2[0]);
 #pragma unroll
         for (int c0 = 0; c0 < R; c0 += 16) {
           uint32_t(&h)[16] = h2[(c0 >> 4) & 1];
+          uint32_t(&l)[16] = l2[(c0 >> 4) & 1];
           tmem_wait_tie(h);
-          if (c0 + 16 < R) tmem_ld16_nowait(o_col + c0 + 16, h2[((c0 >> 4) + 1) & 1]);
+          tmem_tie(l);
+          if (c0 + 16 < R) {
+            tmem_ld16_nowait(o_col + c0 + 16, h2[((c0 >> 4) + 1) & 1]);
+            tmem_ld16_nowait(o_col + R + c0 + 16, l2[((c0 >> 4) + 1) & 1]);
+          }
 #pragma unroll
           for (int i = 0; i < 8; i += 2) {
             const ulonglong2 be = *reinterpret_cast<const ulonglong2*>(ab + R + c0 + 2 * i);
             const int q = c0 / 2 + i;
-            acc[q] = ffma2((uint64_t)h[2 * i] | ((uint64_t)h[2 * i + 1] << 32), be.x, acc[q]);
-            acc[q + 1] = ffma2((uint64_t)h[2 * i + 2] | ((uint64_t)h[2 * i + 3] << 32), be.y, acc[q + 1]);
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+              const uint64_t sum = fadd2((uint64_t)h[2 * (i + y)] | ((uint64_t)h[2 * (i + y) + 1] << 32),
+                                         (uint64_t)l[2 * (i + y)] | ((uint64_t)l[2 * (i + y) + 1] << 32));
+              acc[q + y] = ffma2(sum, y ? be.y : be.x, acc[q + y]);
+            }
           }
         }
         tc_fence_before();
@@ -1058,7 +1122,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
   __syncthreads();
   if (tid == 0 && *abort_v)
     for (PUnit u = list.first(x0); u.valid; list.next(u)) a.status[u.b] = TSV_ERR_TIMEOUT;
-  if (warp == kPMmaWarp) {
+  if (warp == kPSWarp) {
     tc_fence_after();
     tmem_dealloc(tmem, C::kTmem);
   }
@@ -1076,6 +1140,11 @@ cudaError_t launch_typed(const CUtensorMap& tk, const CUtensorMap& tv, const Pag
 
 template <int D, int R>
 cudaError_t set_typed() {
+  // The register split draws on what the block is launched with.
+  cudaFuncAttributes attr;
+  const cudaError_t e = cudaFuncGetAttributes(&attr, paged_attn_kernel<D, R>);
+  if (e != cudaSuccess) return e;
+  if (attr.numRegs < kPRegs) return cudaErrorInvalidConfiguration;
   return cudaFuncSetAttribute(paged_attn_kernel<D, R>, cudaFuncAttributeMaxDynamicSharedMemorySize, PCfg<D, R>::kSmem);
 }
 
