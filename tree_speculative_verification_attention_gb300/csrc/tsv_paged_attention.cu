@@ -28,23 +28,30 @@
 // same number of blocks whatever the lengths, which the kernel reads from the
 // device.  A group that a cut goes through leaves fp32 partials in the
 // workspace, and the last of its CTAs to arrive joins them in a fixed order.
+// Inside a CTA two blocks make a step: one exchange of maxima, one O and one
+// round of barriers for 256 keys.  With few rows the bound is not the bytes but
+// the instructions around them (a warp's chain of dependent steps runs at 6 to
+// 7 cycles an instruction, a third of it waiting for instruction fetches), so
+// what a step costs once matters most.
 //
 // Roles (20 warps): two softmax warpgroups (warps 0-3 and 4-7; a thread owns a
-// key), which take alternate blocks, or, with 64 rows, 32 rows of every block
-// each; the accumulating warpgroup (8-11; a thread owns a d); the producers of
-// K and of V (12, 13: page ids and scales are looked up a warp's worth ahead;
-// a page is one TMA box, and a warp issues one in about 100 cycles); the
-// issuers of S and of O (14, 15); and four warps that prepare the next unit's Q
-// tiles and tree mask (16-19).  The register file is split by role.
-//
-// What a role needs from the rows (maxima, factors) is worked out by
-// each of its warps for itself: a block costs a softmax group one barrier and
-// the accumulating group none.
+// key of each block), which take alternate steps, or, with 64 rows, 32 rows of
+// every step each; the accumulating warpgroup (8-11; a thread owns a d); the
+// producers (12, 13 of K, 14, 15 of V, each pair taking alternate blocks: page
+// ids and scales are looked up a warp's worth ahead, a page is one TMA box, and
+// a box costs its warp about 100 cycles); the issuers of S and of O (16, 17);
+// and two warps that prepare the next unit's Q tiles and tree mask (18, 19). 
+// What
+// a role needs from the rows (maxima, factors) is worked out by each of its
+// warps for itself: a step costs a softmax group one barrier and the
+// accumulating group none.  The register file is split by role.
 //
 // Tail and tree blocks: V rows past the last key are zeroed in shared memory
 // and NaN codes of tree rows are taken out of the product and put back only
 // into the rows that see them, so that 0 x NaN reaches nobody.
 #include "tsv_attention_common.cuh"
+#include <type_traits>
+
 #include "tsv_paged_common.cuh"
 
 namespace tsv {
@@ -52,7 +59,7 @@ namespace tsv {
 namespace {
 
 constexpr int kPThreads = 640;
-constexpr int kPProducerWarp = 12, kPSWarp = 14, kPOWarp = 15, kPPrepWarp = 16;  // K, V producers: 12, 13
+constexpr int kPProducerWarp = 12, kPSWarp = 16, kPOWarp = 17, kPPrepWarp = 18;
 // Registers a thread: 640 x 96 at launch = 256 x 120 + 128 x 112 + 256 x 64.
 constexpr int kPRegs = 96, kPSoftRegs = 120, kPAccRegs = 112, kPRestRegs = 64;
 static_assert(256 * kPSoftRegs + 128 * kPAccRegs + 256 * kPRestRegs <= kPThreads * kPRegs, "register split");
@@ -64,14 +71,19 @@ template <int D, int R>
 struct PCfg {
   static constexpr int kTile = kPBlock * D;                 // K tile
   static constexpr int kVTile = kPBlock * 128;              // 128 d; the upper half stays zero when D = 64
-  static constexpr int kStages = D == 64 ? 6 : R == 64 ? 4 : 5;
+  // K tiles go as soon as S is there; V tiles wait for their step's P, so more
+  // of them are needed for the same bytes in flight.
+  static constexpr int kKStages = D == 64 ? 6 : R == 64 ? 3 : 4;
+  static constexpr int kVStages = R == 16 ? 6 : 5;
+  static constexpr int kPB = R == 64 ? 1 : 2;               // P buffers (of two blocks)
+  static constexpr int kNS = R == 64 ? 2 : 4;               // S buffers (of two blocks)
   static constexpr int kQ = R * D;                          // one term of a Q tile
   static constexpr int kOffK = 0;                                  // K ring
-  static constexpr int kOffV = kOffK + kStages * kTile;            // V ring
+  static constexpr int kOffV = kOffK + kKStages * kTile;           // V ring
   static constexpr int kPRow = R == 64 ? 128 : 64;                 // bytes of a key's P: hi of every row, lo of every row
   static constexpr int kPTile = kPBlock * kPRow;
-  static constexpr int kOffP = kOffV + kStages * kVTile;           // [2]
-  static constexpr int kOffQ = kOffP + 2 * kPTile;                 // [2][hi, lo]
+  static constexpr int kOffP = kOffV + kVStages * kVTile;          // [kPB][2 blocks]
+  static constexpr int kOffQ = kOffP + 2 * kPB * kPTile;                 // [2][hi, lo]
   static constexpr int kOffDesc = kOffQ + 4 * kQ;                  // u32 [2][256 keys][2]: rows that see the tree key
   static constexpr int kOffPoison = kOffDesc + 2 * 256 * 8;        // u64 [2][128 d]: rows that see a NaN there
   static constexpr int kOffCum = kOffPoison + 2 * 128 * 8;         // i64 [TSV_MAX_BATCH + 1]
@@ -87,14 +99,17 @@ struct PCfg {
   static constexpr int kOffL = kOffAB + 32 * R;                    // f32 [2][8 warps][RW]
   static constexpr int kOffMw = kOffL + 64 * RW;                   // f32 [2][2 groups][RW]
   static constexpr int kOffFin = kOffMw + 16 * RW;                 // f32 [2][R]: sums of a unit
-  static constexpr int kOffScale = kOffFin + 8 * R;                // f32 [stages][20]: (K, V) of 8 pages, V's largest
-  static constexpr int kOffSv = kOffScale + kStages * 80;               // f32 [4]
+  static constexpr int kOffUnit = kOffFin + 8 * R;                 // PUnit [2]
+  static constexpr int kOffScale = kOffUnit + 128;                 // f32 [V stages][20]: (K, V) of 8 pages, V's largest
+  static constexpr int kOffSv = kOffScale + kVStages * 80;         // f32 [4]
   static constexpr int kOffBar = kOffSv + 16;
-  // k_full[S], k_empty[S], v_full[S], v_empty[S], s_full[4], p_full[4], o_full[2], o_free[2], q_full[2], unit_free[2], l_full[2], mma_done[2]
-  static constexpr int kBars = 4 * kStages + 20;
+  // k_full, k_empty, v_full, v_empty, sc_full (per stage), s_full[4], p_full[4], o_full[2], o_free[2], q_full[2], unit_free[2],
+  // l_full[2], mma_done[2]
+  static constexpr int kBars = 2 * kKStages + 3 * kVStages + 20;
   static constexpr int kOffMisc = kOffBar + 8 * kBars;
   static constexpr int kSmem = kOffMisc + 64 + 1024;
-  static constexpr uint32_t kTmem = 8 * R;  // S0 .. S3 (R each), O0, O1 (2 R each)
+  static constexpr int kO = kNS * 2 * R;                           // first column of O: S is [kNS][2 blocks][R], O [2][2 R]
+  static constexpr uint32_t kTmem = R == 16 ? 256 : 512;
   static_assert(kSmem <= 227 * 1024, "shared memory");
   static_assert(kTile % 1024 == 0 && kQ % 512 == 0 && kOffQ % 1024 == 0, "swizzle atoms");
 };
@@ -105,14 +120,21 @@ __device__ __forceinline__ uint32_t swz(int r, int c) {
   return ROW == 128 ? (uint32_t)(r * 128 + ((c ^ (r & 7)) << 4)) : (uint32_t)(r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
 }
 
+// Issued by the whole warp: the one lane with `lead` set issues the MMA.
 __device__ __forceinline__ void umma_e4m3(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
-                                          uint32_t accumulate) {
+                                          uint32_t accumulate, uint32_t lead) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
+      "{\n\t.reg .pred p, q;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d_tmem),
-      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(lead)
       : "memory");
+}
+// A value that is the same in every lane, in a uniform register.
+__device__ __forceinline__ uint32_t uniform(uint32_t x) { return __reduce_or_sync(0xffffffffu, x); }
+__device__ __forceinline__ uint64_t desc_at(uint64_t base, uint32_t low) {
+  return (base & 0xFFFFFFFF00000000ull) | low;
 }
 // Instruction descriptor of kind::f8f6f4: e4m3 A and B (format 0), fp32 D.
 __device__ __forceinline__ uint32_t idesc_e4m3(int M, int N, int a_mn, int b_mn) {
@@ -144,6 +166,19 @@ __device__ __forceinline__ bool elect_one() {
       "selp.u32 %0, 1, 0, p;\n\t}\n"
       : "=r"(p));
   return p != 0;
+}
+
+// tma_load_4d of one KV head's rows of a page, issued by the lane with `lead`
+// set (the whole warp calls it, so the operands stay uniform).
+__device__ __forceinline__ void tma_load_page(uint32_t dst, const CUtensorMap* tmap, uint32_t bar, uint32_t head, uint32_t page,
+                                              uint64_t policy, bool lead) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "setp.ne.b32 q, %7, 0;\n\t"
+      "@q cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%2, %3, %2, %4}], [%5], %6;\n\t}\n" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(0), "r"(head), "r"(page), "r"(bar), "l"(policy), "r"((uint32_t)lead)
+      : "memory");
 }
 
 __device__ __forceinline__ void mbar_expect_tx(uint64_t* bar, uint32_t bytes) {
@@ -192,6 +227,14 @@ __device__ __forceinline__ void tmem_ld16_nowait(uint32_t taddr, uint32_t (&r)[1
       : "memory");
 }
 
+// The same with 8 columns.
+__device__ __forceinline__ void tmem_ld8_nowait(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr)
+               : "memory");
+}
+
 __device__ __forceinline__ uint64_t fmul2(uint64_t a, uint64_t b) {
   uint64_t d;
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
@@ -201,10 +244,9 @@ __device__ __forceinline__ uint64_t fmul2(uint64_t a, uint64_t b) {
 // One unit of a CTA's range: blocks j .. j1 - 1 of a (request, KV head, row
 // tile) group of T blocks, nmain of them over prefix rows.  gx is the place of
 // the group's block 0 in the list of all blocks.
-struct PUnit {
-  int b, g, tile, tiles, off, n, P, nmain, T, j, j1;
+struct alignas(16) PUnit {
+  int b, g, tile, tiles, off, n, P, nmain, T, j, j1, valid;
   int64_t gx;
-  bool valid;
   __device__ __forceinline__ bool whole() const { return j == 0 && j1 == T; }
 };
 
@@ -257,13 +299,41 @@ struct PList {
   }
 };
 
-// A wait that ran out (or saw another role's) leaves the thread `dead`: it goes
+// A wait that ran out (or saw another role's) leaves the warp `dead`: it goes
 // through the motions without waiting, so that named barriers stay complete.
-#define TSV_PWAIT(bar, parity)                                             \
-  do {                                                                     \
-    if (!dead && !mbar_wait((bar), (uint32_t)(parity) & 1u, abort_v)) dead = true; \
-    __syncwarp();                                                          \
-  } while (0)
+__device__ __forceinline__ bool mbar_try_long(uint32_t at, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 100000;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(ok)
+      : "r"(at), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ void pwait(uint64_t* bar, uint32_t parity, volatile int* abort, bool& dead) {
+  const uint32_t at = smem_u32(bar);
+  uint64_t t0 = 0;
+#pragma unroll 1
+  while (!mbar_try_long(at, parity & 1u)) {
+    if (dead || *abort) {
+      dead = true;
+      break;
+    }
+    const uint64_t now = global_timer_ns();
+    if (t0 == 0) t0 = now;
+    if (now - t0 > kWaitLimitNs) *abort = 1;
+  }
+  __syncwarp();
+}
+// Arrives for the whole warp, or, once it is dead, not at all: arrivals of a
+// warp are added up, and a phase with fewer of them left than a later warp
+// brings would be a fault.
+__device__ __forceinline__ void parrive(uint64_t* bar, bool dead) {
+  if (!__any_sync(0xffffffffu, dead)) mbar_arrive(bar);
+}
+#define TSV_PWAIT(bar, parity) pwait((bar), (uint32_t)(parity), abort_v, dead)
 
 template <int D, int R>
 __global__ void __launch_bounds__(kPThreads, 1)
@@ -271,7 +341,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
                       const __grid_constant__ PagedAttnArgs a, int32_t* __restrict__ counters,
                       float* __restrict__ part_o, float* __restrict__ part_ml) {
   using C = PCfg<D, R>;
-  constexpr int S = C::kStages;
+  constexpr int SK = C::kKStages, SV = C::kVStages, NS = C::kNS;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sK = smem + C::kOffK;
@@ -291,13 +361,15 @@ __global__ void __launch_bounds__(kPThreads, 1)
   float* sL = reinterpret_cast<float*>(smem + C::kOffL);
   float* sMw = reinterpret_cast<float*>(smem + C::kOffMw);
   float* sFin = reinterpret_cast<float*>(smem + C::kOffFin);
+  PUnit* sUnit = reinterpret_cast<PUnit*>(smem + C::kOffUnit);
   float* sScale = reinterpret_cast<float*>(smem + C::kOffScale);
   float* sSv = reinterpret_cast<float*>(smem + C::kOffSv);
   uint64_t* k_full = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
-  uint64_t* k_empty = k_full + S;
-  uint64_t* v_full = k_empty + S;
-  uint64_t* v_empty = v_full + S;
-  uint64_t* s_full = v_empty + S;
+  uint64_t* k_empty = k_full + SK;
+  uint64_t* v_full = k_empty + SK;
+  uint64_t* v_empty = v_full + SV;
+  uint64_t* sc_full = v_empty + SV;  // a block's scales are in
+  uint64_t* s_full = sc_full + SV;
   uint64_t* p_full = s_full + 4;
   uint64_t* o_full = p_full + 4;
   uint64_t* o_free = o_full + 2;
@@ -318,11 +390,14 @@ __global__ void __launch_bounds__(kPThreads, 1)
   bool dead = false;
 
   if (tid == 0) {
-    for (int s = 0; s < S; ++s) {
+    for (int s = 0; s < SK; ++s) {
       mbar_init(&k_full[s], 1);
       mbar_init(&k_empty[s], 1);
+    }
+    for (int s = 0; s < SV; ++s) {
       mbar_init(&v_full[s], 1);
       mbar_init(&v_empty[s], 1);
+      mbar_init(&sc_full[s], 1);
     }
     for (int x = 0; x < 4; ++x) {
       mbar_init(&s_full[x], 1);
@@ -331,7 +406,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
     for (int x = 0; x < 2; ++x) {
       mbar_init(&o_full[x], 1);
       mbar_init(&o_free[x], 128);
-      mbar_init(&q_full[x], 128);
+      mbar_init(&q_full[x], 64);
       mbar_init(&unit_free[x], 128);
       mbar_init(&l_full[x], 256);
     }
@@ -350,7 +425,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
     tma_prefetch_desc(&tmap_v);
   }
   if (D == 64) {  // the upper half of every V stage stays zero
-    for (int i = tid; i < S * (C::kVTile / 2 / 16); i += kPThreads) {
+    for (int i = tid; i < SV * (C::kVTile / 2 / 16); i += kPThreads) {
       const int st = i / (C::kVTile / 2 / 16), o = i % (C::kVTile / 2 / 16);
       reinterpret_cast<uint4*>(sV + st * C::kVTile + C::kVTile / 2)[o] = make_uint4(0u, 0u, 0u, 0u);
     }
@@ -395,15 +470,16 @@ __global__ void __launch_bounds__(kPThreads, 1)
   const int64_t x0 = (int)blockIdx.x < ctas ? (int64_t)blockIdx.x * W / ctas : W;
   PList list{sCum, sReq, a.B, a.G, a.cache.Hkv, R, tree, (int)blockIdx.x < ctas ? ((int64_t)blockIdx.x + 1) * W / ctas : W};
 
-  if (warp == kPProducerWarp || warp == kPProducerWarp + 1) {
+  if (warp >= kPProducerWarp && warp < kPSWarp) {
     // ------------------------------------------------------------ producers of K and of V
     setmaxnreg_dec<kPRestRegs>();
-    const bool is_v = warp != kPProducerWarp;
+    const bool is_v = warp >= kPProducerWarp + 2;
+    const int odd = warp & 1;  // this warp's blocks
     const CUtensorMap* tmap = is_v ? &tmap_v : &tmap_k;
     uint64_t* full = is_v ? v_full : k_full;
     uint64_t* empty = is_v ? v_empty : k_empty;
     uint8_t* ring = is_v ? sV : sK;
-    const int tile = is_v ? C::kVTile : C::kTile;
+    const int tile = is_v ? C::kVTile : C::kTile, stages = is_v ? SV : SK;
     // The lanes stand for the pages of the next 32 / per blocks, per pages to
     // a block: lane i holds page i % per of block i / per of its chunk.  Page ids
     // of the next chunk are loaded as a chunk begins, their scales after its
@@ -438,8 +514,8 @@ __global__ void __launch_bounds__(kPThreads, 1)
       const tsv_page_table& pt = main ? a.table : a.tree_table;
       if (pg < k.pages) k.id = __ldg(pt.ids_d + (int64_t)u.b * pt.stride + block * per + pg);
     };
-    // V's producer brings both scales: V's tile is held until the block is done,
-    // so whoever waits for it sees this phase of its barrier (K's goes on).
+    // V's producer brings both scales: V's stage is held until the block is done,
+    // so whoever waits for them sees this phase of their barrier (K's goes on).
     auto look_scale = [&](const Look& k) {
       float2 s = make_float2(0.f, 0.f);
       if (is_v && (uint32_t)k.id < (uint32_t)a.cache.num_pages) {
@@ -453,82 +529,94 @@ __global__ void __launch_bounds__(kPThreads, 1)
     look_id(c0);
     float2 sc0 = look_scale(c0), sc1 = make_float2(0.f, 0.f);
     const int blocks = __shfl_sync(0xffffffffu, (int)(list.x1 - x0), 0);
-    int t = 0, st = 0, ph = 0;
+    int t = 0, st = odd, ph = 0;  // of this warp's next block: ring stage and phase
     while (t < blocks) {
       advance(chunk);
       look_id(c1);
       float top = sc0.y;  // the block's largest scale of V
       for (int o = per >> 1; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-      // V's scale relative to the block's largest goes to P, with its 256.
-      sc0.y = top > 0.f ? __fdividef(sc0.y, top) * 256.f : 0.f;
-      for (int i = 0; i < chunk && t < blocks; ++i, ++t) {
-        if (t >= S) TSV_PWAIT(&empty[st], ph ^ 1);
+      for (int i = odd; i < chunk && t + i < blocks; i += 2) {  // this warp's blocks of the chunk
+        if (t + i >= stages) TSV_PWAIT(&empty[st], ph ^ 1);
         if (__any_sync(0xffffffffu, dead || *abort_v)) break;
         const int src = i << (7 - lps);
-        const int pages = __shfl_sync(0xffffffffu, c0.pages, src);
-        const int g = __shfl_sync(0xffffffffu, c0.g, src);
-        // Pages that several row tiles read stay in L2.
-        const uint64_t pol = __shfl_sync(0xffffffffu, c0.tiles, src) > 1 ? l2_policy_evict_last() : l2_policy_evict_first();
-        if (pages > 0 && elect_one()) mbar_expect_tx(&full[st], (uint32_t)((pages << lps) * D));
-        for (int p = 0; p < pages; ++p) {
-          const int id = __shfl_sync(0xffffffffu, c0.id, src + p);
-          if (elect_one()) tma_load_4d(ring + st * tile + (p << lps) * D, tmap, &full[st], 0, g, 0, id, pol);
+        const bool mine_now = mine == i;
+        // Pages, whether several row tiles read them (then they stay in L2), head.
+        const uint32_t what = uniform(mine_now ? (uint32_t)c0.pages | (c0.tiles > 1 ? 0x100u : 0u) | ((uint32_t)c0.g << 16) : 0u);
+        const uint32_t pages = what & 0xFFu, g = what >> 16;
+        const uint64_t pol = (what & 0x100u) ? l2_policy_evict_last() : l2_policy_evict_first();
+        const uint32_t at = smem_u32(ring) + (uint32_t)(st * tile), bar = smem_u32(&full[st]);
+        const bool lead = elect_one();
+        if (pages > 0 && lead) mbar_expect_tx(&full[st], (uint32_t)((pages << lps) * D));
+        for (uint32_t p = 0; p < pages; ++p) {
+          const uint32_t id = __shfl_sync(0xffffffffu, (uint32_t)c0.id, src + (int)p);
+          tma_load_page(at + (p << lps) * D, tmap, bar, g, id, pol, lead);
         }
-        if (i == 0) sc1 = look_scale(c1);
-        if (is_v && mine == i) {
+        if (is_v && mine_now) {
           float* sc = sScale + st * 20;
           *reinterpret_cast<float2*>(sc + 2 * pg) = sc0;
-          if (pg == 0) sc[16] = top * (1.f / 256.f);
+          if (pg == 0) sc[16] = top;
         }
         __syncwarp();
-        if (elect_one()) mbar_arrive(&full[st]);
-        if (++st == S) {
-          st = 0;
+        if (lead) {
+          mbar_arrive(&full[st]);
+          if (is_v) mbar_arrive(&sc_full[st]);
+        }
+        st += 2;
+        if (st >= stages) {
+          st -= stages;
           ph ^= 1;
         }
       }
+      t += chunk;
+      sc1 = look_scale(c1);
       if (__any_sync(0xffffffffu, dead || *abort_v)) break;
       c0 = c1;
       sc0 = sc1;
     }
     // Every copy has landed before the CTA leaves (whatever the other roles did).
-    for (int x = (t > S ? t - S : 0); x < t; ++x) mbar_wait(&full[x % S], (x / S) & 1, nullptr);
+    for (int x = max(0, blocks - stages); x < blocks; ++x)
+      if ((x & 1) == odd) mbar_wait(&full[x % stages], (x / stages) & 1, nullptr);
   } else if (warp == kPSWarp) {
     // ------------------------------------------------------------ issuer of S
     setmaxnreg_dec<kPRestRegs>();
-    // S(t) needs its unit's Q, the block's K, and its buffer: the softmax of
-    // block t - 4 has read it.
+    // S of step t needs its unit's Q, the blocks' K, and its buffer: the softmax
+    // of step t - NS has read it.
     const uint64_t dK0 = sdesc_row<D>(smem_u32(sK), 16);
     const uint64_t dQ0 = sdesc_row<D>(smem_u32(sQ), 16);
     const uint32_t idS = idesc_e4m3(kPBlock, R, 0, 0);
-    int t = 0, st = 0, ph = 0, k = 0;
-    for (PUnit u = list.first(x0); u.valid; list.next(u), ++k) {
+    int t = 0, st = 0, ph = 0;
+    for (int k = 0; !dead; ++k) {
       TSV_PWAIT(&q_full[k & 1], k >> 1);
-      const uint64_t dq = dQ0 + (uint64_t)((k & 1) * (2 * C::kQ >> 4));
-      const int blocks = __shfl_sync(0xffffffffu, u.j1 - u.j, 0);
-      for (int i = 0; i < blocks; ++i, ++t) {
+      const PUnit& u = sUnit[k & 1];
+      const int blocks = __shfl_sync(0xffffffffu, u.valid ? u.j1 - u.j : 0, 0);
+      if (blocks == 0) break;
+      const uint32_t dq = (uint32_t)dQ0 + (uint32_t)((k & 1) * (2 * C::kQ >> 4));
+      for (int i = 0; i < blocks; ++i) {
+        if ((i & 1) == 0 && t >= NS) TSV_PWAIT(&p_full[(t - NS) & 3], (t - NS) >> 2);
         TSV_PWAIT(&k_full[st], ph);
-        if (t >= 4) TSV_PWAIT(&p_full[t & 3], (t >> 2) - 1);
         if (__any_sync(0xffffffffu, dead)) break;
         tc_fence_after();
-        if (elect_one()) {
-          const uint64_t dk = dK0 + (uint64_t)(st * (C::kTile >> 4));
-          const uint32_t dst = tmem + (uint32_t)((t & 3) * R);
+        const bool last = (i & 1) || i + 1 == blocks;
+        const bool lead = elect_one();
+        const uint32_t dk = (uint32_t)dK0 + (uint32_t)(st * (C::kTile >> 4));
+        const uint32_t dst = tmem + (uint32_t)((t % NS) * 2 * R + (i & 1) * R);
 #pragma unroll
-          for (int term = 0; term < 2; ++term)
+        for (int term = 0; term < 2; ++term)
 #pragma unroll
-            for (int kk = 0; kk < D / 32; ++kk)
-              umma_e4m3(dst, dk + kk * 2, dq + term * (C::kQ >> 4) + kk * 2, idS, term + kk > 0 ? 1u : 0u);
-          umma_commit(&s_full[t & 3]);
+          for (int kk = 0; kk < D / 32; ++kk)
+            umma_e4m3(dst, desc_at(dK0, dk + kk * 2), desc_at(dQ0, dq + term * (C::kQ >> 4) + kk * 2), idS, term + kk > 0 ? 1u : 0u, lead);
+        if (lead) {
           umma_commit(&k_empty[st]);
+          if (last) umma_commit(&s_full[t & 3]);
         }
         __syncwarp();
-        if (++st == S) {
+        if (last) ++t;
+        if (++st == SK) {
           st = 0;
           ph ^= 1;
         }
       }
-      if (__any_sync(0xffffffffu, dead)) break;
+      dead = __any_sync(0xffffffffu, dead);
     }
     if (elect_one()) umma_commit(&mma_done[0]);
     __syncwarp();
@@ -536,34 +624,46 @@ __global__ void __launch_bounds__(kPThreads, 1)
   } else if (warp == kPOWarp) {
     // ------------------------------------------------------------ issuer of O
     setmaxnreg_dec<kPRestRegs>();
-    // O(t) needs P of the block and its own buffer: the accumulating group has
-    // read block t - 2.
+    // O of step t needs P, the blocks' V and its own buffer: the accumulating
+    // group has read step t - 2.
     const uint64_t dV0 = sdesc_row<D>(smem_u32(sV), kPBlock * 64);
     const uint64_t dP0 = sdesc_row<C::kPRow>(smem_u32(sP), kPBlock * 128);
     const uint32_t idO = idesc_e4m3(128, 2 * R, 1, 1);
-    const int blocks = __shfl_sync(0xffffffffu, (int)(list.x1 - x0), 0);
-    int st = 0, ph = 0;
-    for (int t = 0; t < blocks; ++t) {
-      TSV_PWAIT(&v_full[st], ph);
-      if (t >= 2) TSV_PWAIT(&o_free[t & 1], (t >> 1) - 1);
-      TSV_PWAIT(&p_full[t & 3], t >> 2);
-      if (__any_sync(0xffffffffu, dead)) break;
-      tc_fence_after();
-      if (elect_one()) {
-        const uint64_t dv = dV0 + (uint64_t)(st * (C::kVTile >> 4));
-        const uint64_t dp = dP0 + (uint64_t)((t & 1) * (C::kPTile >> 4));
-        const uint32_t dst = tmem + (uint32_t)(4 * R + (t & 1) * 2 * R);
+    int t = 0, st = 0, ph = 0;
+    for (int k = 0; !dead; ++k) {
+      TSV_PWAIT(&q_full[k & 1], k >> 1);
+      const PUnit& u = sUnit[k & 1];
+      const int blocks = __shfl_sync(0xffffffffu, u.valid ? u.j1 - u.j : 0, 0);
+      if (blocks == 0) break;
+      for (int i = 0; i < blocks; ++i) {
+        if ((i & 1) == 0) {
+          if (t >= 2) TSV_PWAIT(&o_free[t & 1], (t >> 1) - 1);
+          TSV_PWAIT(&p_full[t & 3], t >> 2);
+        }
+        TSV_PWAIT(&v_full[st], ph);
+        if (__any_sync(0xffffffffu, dead)) break;
+        tc_fence_after();
+        const bool last = (i & 1) || i + 1 == blocks;
+        const bool lead = elect_one();
+        const uint32_t dv = (uint32_t)dV0 + (uint32_t)(st * (C::kVTile >> 4));
+        const uint32_t dp = (uint32_t)dP0 + (uint32_t)(((t % C::kPB) * 2 + (i & 1)) * (C::kPTile >> 4));
+        const uint32_t dst = tmem + (uint32_t)(C::kO + (t & 1) * 2 * R);
+        const uint32_t more = (uint32_t)(i & 1);
 #pragma unroll
         for (int kk = 0; kk < kPBlock / 32; ++kk)
-          umma_e4m3(dst, dv + kk * (32 * D >> 4), dp + kk * (32 * C::kPRow >> 4), idO, kk > 0 ? 1u : 0u);
-        umma_commit(&o_full[t & 1]);
-        umma_commit(&v_empty[st]);
+          umma_e4m3(dst, desc_at(dV0, dv + kk * (32 * D >> 4)), desc_at(dP0, dp + kk * (32 * C::kPRow >> 4)), idO, kk > 0 ? 1u : more, lead);
+        if (lead) {
+          umma_commit(&v_empty[st]);
+          if (last) umma_commit(&o_full[t & 1]);
+        }
+        __syncwarp();
+        if (last) ++t;
+        if (++st == SV) {
+          st = 0;
+          ph ^= 1;
+        }
       }
-      __syncwarp();
-      if (++st == S) {
-        st = 0;
-        ph ^= 1;
-      }
+      dead = __any_sync(0xffffffffu, dead);
     }
     if (elect_one()) umma_commit(&mma_done[1]);
     __syncwarp();
@@ -573,13 +673,19 @@ __global__ void __launch_bounds__(kPThreads, 1)
     setmaxnreg_dec<kPRestRegs>();
     const int q = warp - kPPrepWarp;
     constexpr int E = D / 32;        // elements of a row per lane
-    constexpr int kMine = R / 4;     // rows of this warp, r_lo ..
+    constexpr int kMine = R / 2;     // rows of this warp, r_lo ..
+    constexpr int kBatch = 8;        // loaded together
     const int r_lo = kMine * q;
-    int k = 0;
-    for (PUnit u = list.first(x0); u.valid; list.next(u), ++k) {
+    PUnit u = list.first(x0);
+    for (int k = 0;; ++k) {
       const int buf = k & 1;
       if (k >= 2) TSV_PWAIT(&unit_free[buf], (k >> 1) - 1);
       if (__any_sync(0xffffffffu, dead)) break;
+      if (q == 0 && lane == 0) sUnit[buf] = u;  // what the other roles walk by
+      if (!u.valid) {
+        parrive(&q_full[buf], dead);
+        break;
+      }
       const int row0 = u.tile * R;
       const int rows = min(R, u.n * a.G - row0);
       // Row r of the tile: node (row0 + r) / G, query head g G + (row0 + r) % G.
@@ -596,56 +702,59 @@ __global__ void __launch_bounds__(kPThreads, 1)
       }
       uint8_t* hi = sQ + buf * 2 * C::kQ;
       uint8_t* lo = hi + C::kQ;
-      uint32_t raw[kMine][E / 2];
+#pragma unroll 1
+      for (int r0 = 0; r0 < kMine; r0 += kBatch) {
+        uint32_t raw[kBatch][E / 2];
 #pragma unroll
-      for (int i = 0; i < kMine; ++i) {
-        const int64_t at = __shfl_sync(0xffffffffu, at_q, i);
+        for (int i = 0; i < kBatch; ++i) {
+          const int64_t at = __shfl_sync(0xffffffffu, at_q, r0 + i);
 #pragma unroll
-        for (int e = 0; e < E / 2; ++e) raw[i][e] = 0u;
-        if (r_lo + i < rows) {
-          const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.q) + at + lane * E;
+          for (int e = 0; e < E / 2; ++e) raw[i][e] = 0u;
+          if (r_lo + r0 + i < rows) {
+            const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.q) + at + lane * E;
+            if constexpr (E == 4) {
+              const uint2 w = __ldg(reinterpret_cast<const uint2*>(src));
+              raw[i][0] = w.x;
+              raw[i][1] = w.y;
+            } else {
+              raw[i][0] = __ldg(reinterpret_cast<const uint32_t*>(src));
+            }
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+          const int r = r_lo + r0 + i;
+          uint32_t top = 0u;
+#pragma unroll
+          for (int e = 0; e < E / 2; ++e) top = max(top, max((raw[i][e] << 16) & 0x7FFF0000u, raw[i][e] & 0x7FFF0000u));
+          top = __reduce_max_sync(0xffffffffu, top);
+          const bool fine = top < 0x7F800000u;  // no infinity, no NaN in the row
+          // The largest value moves to [128, 256): exponent 134 as biased.
+          const int up = top == 0u ? 0 : max(-120, min(120, 134 - (int)(top >> 23)));
+          const float mul = __uint_as_float((uint32_t)(127 + up) << 23);
+          if (lane == 0) sFr[buf * R + r] = __uint_as_float((uint32_t)(127 - up) << 23) * (a.scale * 1.4426950408889634f);
+          uint32_t wh = 0u, wl = 0u;
+#pragma unroll
+          for (int e = 0; e < E / 2; ++e) {
+            // A row with an infinity or a NaN is NaN throughout (its scores are).
+            const float y0 = fine ? __uint_as_float(raw[i][e] << 16) * mul : NAN;
+            const float y1 = fine ? __uint_as_float(raw[i][e] & 0xFFFF0000u) * mul : NAN;
+            const uint32_t h2 = e4m3x2(y0, y1), f2 = f16x2_of_e4m3x2(h2);
+            wh |= h2 << (16 * e);
+            wl |= e4m3x2(y0 - f16_lo(f2), y1 - f16_hi(f2)) << (16 * e);
+          }
+          const uint32_t at = swz<D>(r, lane * E / 16) + (lane * E) % 16;
           if constexpr (E == 4) {
-            const uint2 w = __ldg(reinterpret_cast<const uint2*>(src));
-            raw[i][0] = w.x;
-            raw[i][1] = w.y;
+            *reinterpret_cast<uint32_t*>(hi + at) = wh;
+            *reinterpret_cast<uint32_t*>(lo + at) = wl;
           } else {
-            raw[i][0] = __ldg(reinterpret_cast<const uint32_t*>(src));
+            *reinterpret_cast<uint16_t*>(hi + at) = (uint16_t)wh;
+            *reinterpret_cast<uint16_t*>(lo + at) = (uint16_t)wl;
           }
         }
       }
-#pragma unroll
-      for (int i = 0; i < kMine; ++i) {
-        const int r = r_lo + i;
-        uint32_t top = 0u;
-#pragma unroll
-        for (int e = 0; e < E / 2; ++e) top = max(top, max((raw[i][e] << 16) & 0x7FFF0000u, raw[i][e] & 0x7FFF0000u));
-        top = __reduce_max_sync(0xffffffffu, top);
-        const bool fine = top < 0x7F800000u;  // no infinity, no NaN in the row
-        // The largest value moves to [128, 256): exponent 134 as biased.
-        const int up = top == 0u ? 0 : max(-120, min(120, 134 - (int)(top >> 23)));
-        const float mul = __uint_as_float((uint32_t)(127 + up) << 23);
-        if (lane == 0) sFr[buf * R + r] = __uint_as_float((uint32_t)(127 - up) << 23) * (a.scale * 1.4426950408889634f);
-        uint32_t wh = 0u, wl = 0u;
-#pragma unroll
-        for (int e = 0; e < E / 2; ++e) {
-          // A row with an infinity or a NaN is NaN throughout (its scores are).
-          const float y0 = fine ? __uint_as_float(raw[i][e] << 16) * mul : NAN;
-          const float y1 = fine ? __uint_as_float(raw[i][e] & 0xFFFF0000u) * mul : NAN;
-          const uint32_t h2 = e4m3x2(y0, y1), f2 = f16x2_of_e4m3x2(h2);
-          wh |= h2 << (16 * e);
-          wl |= e4m3x2(y0 - f16_lo(f2), y1 - f16_hi(f2)) << (16 * e);
-        }
-        const uint32_t at = swz<D>(r, lane * E / 16) + (lane * E) % 16;
-        if constexpr (E == 4) {
-          *reinterpret_cast<uint32_t*>(hi + at) = wh;
-          *reinterpret_cast<uint32_t*>(lo + at) = wl;
-        } else {
-          *reinterpret_cast<uint16_t*>(hi + at) = (uint16_t)wh;
-          *reinterpret_cast<uint16_t*>(lo + at) = (uint16_t)wl;
-        }
-      }
       // Rows that see tree key j: word q of sDesc[buf][j] holds rows 32 q .. (two warps).
-      if (tree && u.j1 > u.nmain && q < 2) {
+      if (tree && u.j1 > u.nmain) {
         const int r = q * 32 + lane;
         const bool has = r < rows;
         const int i0 = has ? (row0 + r) / a.G : 0;  // the row's node
@@ -666,7 +775,8 @@ __global__ void __launch_bounds__(kPThreads, 1)
         }
       }
       fence_proxy_async_smem();
-      mbar_arrive(&q_full[buf]);
+      parrive(&q_full[buf], dead);
+      list.next(u);
     }
     // Every request's lengths and page ids are checked by one CTA.
     for (int b = blockIdx.x; q == 0 && b < a.B; b += gridDim.x) {
@@ -686,204 +796,233 @@ __global__ void __launch_bounds__(kPThreads, 1)
     const int kt = tid & 127;                  // thread of the group = key lane
     const uint32_t lane_base = (uint32_t)(lg * 32) << 16;
     float* pw = sPw + warp * 3 * RW;
-    int t = 0, st = 0, ph = 0, k = 0, nth = 0;
-    for (PUnit u = list.first(x0); u.valid; list.next(u), ++k) {
+    int t = 0, st = 0, ph = 0, nth = 0;
+    for (int k = 0;; ++k) {
       const int buf = k & 1;
+      TSV_PWAIT(&q_full[buf], k >> 1);
+      if (named_bar_or(kBarSoft + wg, 128, dead)) break;  // the same in every thread of the group
+      const int u_j = sUnit[buf].j, u_j1 = sUnit[buf].j1, u_P = sUnit[buf].P, u_n = sUnit[buf].n, nmain = sUnit[buf].nmain;
+      if (!sUnit[buf].valid) break;
       float lsum[RW];
 #pragma unroll
       for (int i = 0; i < RW; ++i) lsum[i] = 0.f;
       float mw = -INFINITY;  // lane r < RW: largest score of row r over this group's blocks of the unit
-      TSV_PWAIT(&q_full[buf], k >> 1);
       const float fr = lane < RW ? sFr[buf * R + col0 + lane] : 0.f;
-      for (int j = u.j; j < u.j1; ++j, ++t) {
-        const int stage = st, phase = ph;
-        if (++st == S) {
-          st = 0;
-          ph ^= 1;
-        }
+      for (int j = u_j; j < u_j1; j += 2, ++t) {
+        const int halves = min(2, u_j1 - j);
+        const int st0 = st, ph0 = ph;
+        for (int h = 0; h < halves; ++h)
+          if (++st == SV) {
+            st = 0;
+            ph ^= 1;
+          }
         if (!kCols && (t & 1) != wg) continue;
-        const int x = t & 1, x4 = t & 3;
-        const uint32_t s_col = tmem + lane_base + (uint32_t)(x4 * R + col0);
-        const bool main = j < u.nmain;
-        const int base = (main ? j : j - u.nmain) * kPBlock;
-        const int valid = max(0, min(kPBlock, (main ? u.P : tree ? u.n : 0) - base));
-        const bool all = main && valid == kPBlock;  // every row sees every key
-        // Rows (of this group) that see a key, one bit each.
-        auto sees = [&](int key) -> uint32_t {
-          if (key >= valid) return 0u;
-          if (main) return 0xFFFFFFFFu;
-          return sDesc[(buf * 256 + base + key) * 2 + (kCols ? wg : 0)];
+        const int st1 = st0 + 1 == SV ? 0 : st0 + 1, ph1 = st0 + 1 == SV ? ph0 ^ 1 : ph0;
+        const uint32_t s_col = tmem + lane_base + (uint32_t)((t % NS) * 2 * R + col0);
+        // Keys of block j + h: its first row, how many are valid, tree or prefix.
+        auto block_base = [&](int h) { return (j + h < nmain ? j + h : j + h - nmain) * kPBlock; };
+        auto block_valid = [&](int h) {
+          return h >= halves ? 0 : max(0, min(kPBlock, (j + h < nmain ? u_P : tree ? u_n : 0) - block_base(h)));
         };
-        float* wmax = sWmax + ((wg * 2 + (nth & 1)) * 4) * RW;
+        const bool all = j + 2 <= u_j1 && (j + 2) * kPBlock <= u_P;  // two blocks that every row sees throughout
         ++nth;
-        TSV_PWAIT(&s_full[x4], t >> 2);
+        TSV_PWAIT(&s_full[t & 3], t >> 2);
         tc_fence_after();
-        uint32_t sa[RW / 2], sb[RW / 2];  // the warp's keys 0-15 and 16-31
-        tmem_ld_16x256(s_col, sa);
-        tmem_ld_16x256(s_col + (16u << 16), sb);
-        TSV_PWAIT(&v_full[stage], phase);
-        const float2* sc = reinterpret_cast<const float2*>(sScale + stage * 20);
-        const float fa = sc[(lg * 32) >> lps].x, fb = sc[(lg * 32 + 16) >> lps].x;
-        const float2 mine = sc[kt >> lps];  // K's scale; 256 x V's, relative to the block's largest
-        const uint32_t vis = all ? 0xFFFFFFFFu : sees(kt);
-        tmem_wait_tie(sa);
-        tmem_tie(sb);
 
-        // Largest score of every row over the warp's 32 keys: 4 keys of 2
-        // columns in 8 a thread, then three halving exchanges over the 8
-        // thread rows.  best[2 i + c] is column 8 i + 2 (lane % 4) + c.
-        {
+        auto step = [&](auto all_c) {
+          constexpr bool ALL = decltype(all_c)::value;
+          const int nh = ALL ? 2 : halves;
+          // Rows (of this group) that see a key, one bit each.
+          auto sees = [&](int h, int key) -> uint32_t {
+            if (key >= block_valid(h)) return 0u;
+            if (j + h < nmain) return 0xFFFFFFFFu;
+            return sDesc[(buf * 256 + block_base(h) + key) * 2 + (kCols ? wg : 0)];
+          };
+          // Largest score of every row over the warp's 64 keys: of 16 keys a
+          // thread holds 2 in 2 columns of 8; then three halving exchanges over
+          // the 8 thread rows.  best[2 i + c] is column 8 i + 2 (lane % 4) + c.
           constexpr int N0 = RW / 4;
           float best[N0];
-          if (!all) {
-            const int key = lg * 32 + (lane >> 2);
-            const int sh = 2 * (lane & 3);
-            const uint32_t v0 = sees(key) >> sh, v1 = sees(key + 8) >> sh, v2 = sees(key + 16) >> sh, v3 = sees(key + 24) >> sh;
+#pragma unroll
+          for (int i = 0; i < N0; ++i) best[i] = -INFINITY;
+#pragma unroll 1
+          for (int h = 0; h < nh; ++h) {
+            uint32_t sa[RW / 2], sb[RW / 2];  // the warp's keys 0-15 and 16-31
+            tmem_ld_16x256(s_col + h * R, sa);
+            tmem_ld_16x256(s_col + h * R + (16u << 16), sb);
+            TSV_PWAIT(&sc_full[h ? st1 : st0], h ? ph1 : ph0);
+            const float2* sc = reinterpret_cast<const float2*>(sScale + (h ? st1 : st0) * 20);
+            const float fa = sc[(lg * 32) >> lps].x, fb = sc[(lg * 32 + 16) >> lps].x;
+            tmem_wait_tie(sa);
+            tmem_tie(sb);
+            if (!ALL) {
+              const int key = lg * 32 + (lane >> 2);
+              const int sh = 2 * (lane & 3);
+              const uint32_t v0 = sees(h, key) >> sh, v1 = sees(h, key + 8) >> sh;
+              const uint32_t v2 = sees(h, key + 16) >> sh, v3 = sees(h, key + 24) >> sh;
+#pragma unroll
+              for (int i = 0; i < RW / 8; ++i)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                  if (!((v0 >> (8 * i + c)) & 1u)) sa[4 * i + c] = 0xFF800000u;
+                  if (!((v1 >> (8 * i + c)) & 1u)) sa[4 * i + 2 + c] = 0xFF800000u;
+                  if (!((v2 >> (8 * i + c)) & 1u)) sb[4 * i + c] = 0xFF800000u;
+                  if (!((v3 >> (8 * i + c)) & 1u)) sb[4 * i + 2 + c] = 0xFF800000u;
+                }
+            }
 #pragma unroll
             for (int i = 0; i < RW / 8; ++i)
 #pragma unroll
               for (int c = 0; c < 2; ++c) {
-                if (!((v0 >> (8 * i + c)) & 1u)) sa[4 * i + c] = 0xFF800000u;
-                if (!((v1 >> (8 * i + c)) & 1u)) sa[4 * i + 2 + c] = 0xFF800000u;
-                if (!((v2 >> (8 * i + c)) & 1u)) sb[4 * i + c] = 0xFF800000u;
-                if (!((v3 >> (8 * i + c)) & 1u)) sb[4 * i + 2 + c] = 0xFF800000u;
-              }
-          }
-#pragma unroll
-          for (int i = 0; i < RW / 8; ++i)
-#pragma unroll
-            for (int c = 0; c < 2; ++c)
-              best[2 * i + c] = fmaxf(fmaxf(__uint_as_float(sa[4 * i + c]), __uint_as_float(sa[4 * i + 2 + c])) * fa,
+                const float x = fmaxf(fmaxf(__uint_as_float(sa[4 * i + c]), __uint_as_float(sa[4 * i + 2 + c])) * fa,
                                       fmaxf(__uint_as_float(sb[4 * i + c]), __uint_as_float(sb[4 * i + 2 + c])) * fb);
-          int at = 0;  // first index that this thread is left with: the halvings pick its bits from the top
-#pragma unroll
-          for (int s = 0; s < 3; ++s) {
-            const int half = (N0 >> s) / 2;  // values kept
-            const int bit = 16 >> s;
-            const bool up = lane & bit;
-            if (half >= 1) {
-#pragma unroll
-              for (int i = 0; i < (half > 0 ? half : 1); ++i) {
-                const float send = up ? best[i] : best[i + half];
-                const float keep = up ? best[i + half] : best[i];
-                best[i] = fmaxf(keep, __shfl_xor_sync(0xffffffffu, send, bit));
+                best[2 * i + c] = fmaxf(best[2 * i + c], x);
               }
-              at += up ? half : 0;
-            } else {
-              best[0] = fmaxf(best[0], __shfl_xor_sync(0xffffffffu, best[0], bit));
-            }
           }
-          wmax[lg * RW + (at >> 1) * 8 + 2 * (lane & 3) + (at & 1)] = best[0];
-        }
-        uint32_t sv2[2][16];  // this chunk of 16 rows and the next
-        tmem_ld16_nowait(s_col, sv2[0]);
-        named_bar_sync(kBarSoft + wg, 128);
-        // Every warp works out the rows' maxima and factors for itself.
-        bool moved = false;
-        float m = 0.f;
-        if (lane < RW) {
-          m = fmaxf(fmaxf(wmax[lane], wmax[RW + lane]), fmaxf(wmax[2 * RW + lane], wmax[3 * RW + lane])) * fr;
-          if (!(m > -INFINITY)) m = -INFINITY;  // nothing seen, or NaN scores only: P is 0 or NaN
-          const float mn = fmaxf(mw, m);
-          pw[lane] = m == -INFINITY ? 0.f : -m;
-          pw[RW + lane] = m == -INFINITY ? 1.f : fast_exp2(m - mn);
-          pw[2 * RW + lane] = mn == -INFINITY ? 1.f : mw == -INFINITY ? 0.f : fast_exp2(mw - mn);
-          moved = mn != mw;
-          mw = mn;
-        }
-        __syncwarp();
-        // P's buffer is free once PV of the block before last is done.  That PV
-        // waited for the accumulating group to be through with block t - 4,
-        // so the group's copies of the maxima (4 deep) are free too.
-        if (t >= 2) TSV_PWAIT(&o_full[x], (t >> 1) - 1);
-        if (lg == 0 && lane < RW) {
-          sM[x4 * R + col0 + lane] = m;
-          if (lane == 0 && col0 == 0) sSv[x4] = sScale[stage * 20 + 16];
-        }
-        if (__any_sync(0xffffffffu, moved)) {
+          float* wmax = sWmax + ((wg * 2 + (nth & 1)) * 4) * RW;
+          {
+            int at = 0;  // first index that this thread is left with: the halvings pick its bits from the top
 #pragma unroll
-          for (int i = 0; i < RW; i += 4) {
-            const float4 al = *reinterpret_cast<const float4*>(pw + 2 * RW + i);
-            lsum[i] *= al.x;
-            lsum[i + 1] *= al.y;
-            lsum[i + 2] *= al.z;
-            lsum[i + 3] *= al.w;
-          }
-        }
-        uint8_t* ptile = sP + x * C::kPTile;
-        const uint64_t fk2 = f2_pack(mine.x, mine.x), fv2 = f2_pack(mine.y, mine.y);
+            for (int s = 0; s < 3; ++s) {
+              const int half = (N0 >> s) / 2;  // values kept
+              const int bit = 16 >> s;
+              const bool up = lane & bit;
+              if (half >= 1) {
 #pragma unroll
-        for (int c0 = 0; c0 < RW; c0 += 16) {
-          uint32_t(&sv)[16] = sv2[(c0 >> 4) & 1];
-          tmem_wait_tie(sv);
-          if (c0 + 16 < RW) tmem_ld16_nowait(s_col + c0 + 16, sv2[((c0 >> 4) + 1) & 1]);
-          uint32_t hi[4], lo[4];
-#pragma unroll
-          for (int q4 = 0; q4 < 4; ++q4) {
-            const ulonglong2 m4 = *reinterpret_cast<const ulonglong2*>(pw + c0 + 4 * q4);
-            const ulonglong2 b4 = *reinterpret_cast<const ulonglong2*>(pw + RW + c0 + 4 * q4);
-            const ulonglong2 f4 = *reinterpret_cast<const ulonglong2*>(sFr + buf * R + col0 + c0 + 4 * q4);
-            uint32_t hw = 0u, lw = 0u;
-#pragma unroll
-            for (int pr = 0; pr < 2; ++pr) {
-              const int r = c0 + 4 * q4 + 2 * pr;
-              const uint64_t s2 = (uint64_t)sv[4 * q4 + 2 * pr] | ((uint64_t)sv[4 * q4 + 2 * pr + 1] << 32);
-              // The same products as in the maximum: x <= 0 up to m's own rounding.
-              const uint64_t x2 = ffma2(fmul2(s2, fk2), pr ? f4.y : f4.x, pr ? m4.y : m4.x);
-              float p0 = fast_exp2(f2_lo(x2)), p1 = fast_exp2(f2_hi(x2));
-              if (!all) {
-                if (!((vis >> r) & 1u)) p0 = 0.f;
-                if (!((vis >> (r + 1)) & 1u)) p1 = 0.f;
+                for (int i = 0; i < (half > 0 ? half : 1); ++i) {
+                  const float send = up ? best[i] : best[i + half];
+                  const float keep = up ? best[i + half] : best[i];
+                  best[i] = fmaxf(keep, __shfl_xor_sync(0xffffffffu, send, bit));
+                }
+                at += up ? half : 0;
+              } else {
+                best[0] = fmaxf(best[0], __shfl_xor_sync(0xffffffffu, best[0], bit));
               }
-              uint64_t p2 = f2_pack(p0, p1);
-              const uint64_t l2 = ffma2(p2, pr ? b4.y : b4.x, f2_pack(lsum[r], lsum[r + 1]));
-              lsum[r] = f2_lo(l2);
-              lsum[r + 1] = f2_hi(l2);
-              p2 = fmul2(p2, fv2);
-              p0 = f2_lo(p2);
-              p1 = f2_hi(p2);
-              const uint32_t h2 = e4m3x2(p0, p1), g2 = f16x2_of_e4m3x2(h2);
-              hw |= h2 << (16 * pr);
-              lw |= e4m3x2(p0 - f16_lo(g2), p1 - f16_hi(g2)) << (16 * pr);
             }
-            hi[q4] = hw;
-            lo[q4] = lw;
+            wmax[lg * RW + (at >> 1) * 8 + 2 * (lane & 3) + (at & 1)] = best[0];
           }
-          *reinterpret_cast<uint4*>(ptile + swz<C::kPRow>(kt, (col0 + c0) / 16)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-          *reinterpret_cast<uint4*>(ptile + swz<C::kPRow>(kt, (R + col0 + c0) / 16)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-        }
-        if (!all && (!kCols || wg == 0)) {
-          uint8_t* vrow = sV + stage * C::kVTile + kt * D;
-          if (kt >= valid) {  // whatever the row holds
+          // V's scales, relative to the step's largest, go to P with its 256.
+          const float top0 = sScale[st0 * 20 + 16];
+          const float top = nh == 2 ? fmaxf(top0, sScale[st1 * 20 + 16]) : top0;
+          const float inv_top = top > 0.f ? __fdividef(256.f, top) : 0.f;
+          named_bar_sync(kBarSoft + wg, 128);
+          // Every warp works out the rows' maxima and factors for itself.
+          float m = 0.f;
+          bool moved = false;
+          if (lane < RW) {
+            m = fmaxf(fmaxf(wmax[lane], wmax[RW + lane]), fmaxf(wmax[2 * RW + lane], wmax[3 * RW + lane])) * fr;
+            if (!(m > -INFINITY)) m = -INFINITY;  // nothing seen, or NaN scores only: P is 0 or NaN
+            const float mn = fmaxf(mw, m);
+            pw[lane] = m == -INFINITY ? 0.f : -m;
+            pw[RW + lane] = m == -INFINITY ? 1.f : fast_exp2(m - mn);
+            pw[2 * RW + lane] = mn == -INFINITY ? 1.f : mw == -INFINITY ? 0.f : fast_exp2(mw - mn);
+            moved = mn != mw;
+            mw = mn;
+          }
+          __syncwarp();
+          // P's buffer is free once O of the step kPB before is there.  That
+          // waited for the accumulating group to be through with a step at least
+          // 3 back, so the group's copies of the maxima (4 deep) are free too.
+          if (t >= C::kPB) TSV_PWAIT(&o_full[(t - C::kPB) & 1], (t - C::kPB) >> 1);
+          if (lg == 0 && lane < RW) {
+            sM[(t & 3) * R + col0 + lane] = m;
+            if (lane == 0 && col0 == 0) sSv[t & 3] = top * (1.f / 256.f);
+          }
+          if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll
-            for (int c = 0; c < D / 16; ++c) reinterpret_cast<uint4*>(vrow)[c] = make_uint4(0u, 0u, 0u, 0u);
-          } else if (!main) {
-            uint32_t any = 0u;
-#pragma unroll
-            for (int c = 0; c < D / 16; ++c) {
-              const uint4 w = reinterpret_cast<const uint4*>(vrow)[c];
-              any |= ((w.x & 0x7F7F7F7Fu) + 0x01010101u) | ((w.y & 0x7F7F7F7Fu) + 0x01010101u) |
-                     ((w.z & 0x7F7F7F7Fu) + 0x01010101u) | ((w.w & 0x7F7F7F7Fu) + 0x01010101u);
+            for (int i = 0; i < RW; i += 4) {
+              const float4 al = *reinterpret_cast<const float4*>(pw + 2 * RW + i);
+              lsum[i] *= al.x;
+              lsum[i + 1] *= al.y;
+              lsum[i + 2] *= al.z;
+              lsum[i + 3] *= al.w;
             }
-            any &= 0x80808080u;
-            const uint32_t* see = sDesc + (buf * 256 + base + kt) * 2;
-            const unsigned long long rows = (unsigned long long)see[0] | (R > 32 ? (unsigned long long)see[1] << 32 : 0ull);
+          }
 #pragma unroll 1
-            for (int c = 0; any && c < D / 4; ++c) {
-              const uint32_t w = reinterpret_cast<const uint32_t*>(vrow)[c];
-              uint32_t nan = ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
-              if (nan == 0u) continue;
-              reinterpret_cast<uint32_t*>(vrow)[c] = w & ~((nan >> 7) * 0xFFu);
-              const int chunk = D == 128 ? (c >> 2) ^ (kt & 7) : (c >> 2) ^ ((kt >> 1) & 3);
-              for (; nan; nan &= nan - 1)
-                atomicOr(sPoison + buf * 128 + chunk * 16 + (c & 3) * 4 + ((__ffs(nan) - 1) >> 3), rows);
-              sPoisoned[buf] = 1;
+          for (int h = 0; h < nh; ++h) {  // rolled, here and above: the loop's code is fetched once for both blocks
+            uint32_t sv2[2][16];  // this chunk of 16 rows and the next
+            tmem_ld16_nowait(s_col + h * R, sv2[0]);
+            const float2 mine = reinterpret_cast<const float2*>(sScale + (h ? st1 : st0) * 20)[kt >> lps];
+            const uint32_t vis = ALL ? 0u : sees(h, kt);
+            uint8_t* ptile = sP + ((t % C::kPB) * 2 + h) * C::kPTile;
+            const uint64_t fk2 = f2_pack(mine.x, mine.x), fv2 = f2_pack(mine.y * inv_top, mine.y * inv_top);
+#pragma unroll
+            for (int c0 = 0; c0 < RW; c0 += 16) {
+              uint32_t(&sv)[16] = sv2[(c0 >> 4) & 1];
+              tmem_wait_tie(sv);
+              if (c0 + 16 < RW) tmem_ld16_nowait(s_col + h * R + c0 + 16, sv2[((c0 >> 4) + 1) & 1]);
+              uint32_t hi[4], lo[4];
+#pragma unroll
+              for (int q4 = 0; q4 < 4; ++q4) {
+                const ulonglong2 m4 = *reinterpret_cast<const ulonglong2*>(pw + c0 + 4 * q4);
+                const ulonglong2 b4 = *reinterpret_cast<const ulonglong2*>(pw + RW + c0 + 4 * q4);
+                const ulonglong2 f4 = *reinterpret_cast<const ulonglong2*>(sFr + buf * R + col0 + c0 + 4 * q4);
+                uint32_t hw = 0u, lw = 0u;
+#pragma unroll
+                for (int pr = 0; pr < 2; ++pr) {
+                  const int r = c0 + 4 * q4 + 2 * pr;
+                  const uint64_t s2 = (uint64_t)sv[4 * q4 + 2 * pr] | ((uint64_t)sv[4 * q4 + 2 * pr + 1] << 32);
+                  // The same products as in the maximum: x <= 0 up to m's own rounding.
+                  const uint64_t x2 = ffma2(fmul2(s2, fk2), pr ? f4.y : f4.x, pr ? m4.y : m4.x);
+                  float p0 = fast_exp2(f2_lo(x2)), p1 = fast_exp2(f2_hi(x2));
+                  if (!ALL) {
+                    if (!((vis >> r) & 1u)) p0 = 0.f;
+                    if (!((vis >> (r + 1)) & 1u)) p1 = 0.f;
+                  }
+                  uint64_t p2 = f2_pack(p0, p1);
+                  const uint64_t l2 = ffma2(p2, pr ? b4.y : b4.x, f2_pack(lsum[r], lsum[r + 1]));
+                  lsum[r] = f2_lo(l2);
+                  lsum[r + 1] = f2_hi(l2);
+                  p2 = fmul2(p2, fv2);
+                  p0 = f2_lo(p2);
+                  p1 = f2_hi(p2);
+                  const uint32_t h2 = e4m3x2(p0, p1), g2 = f16x2_of_e4m3x2(h2);
+                  hw |= h2 << (16 * pr);
+                  lw |= e4m3x2(p0 - f16_lo(g2), p1 - f16_hi(g2)) << (16 * pr);
+                }
+                hi[q4] = hw;
+                lo[q4] = lw;
+              }
+              *reinterpret_cast<uint4*>(ptile + swz<C::kPRow>(kt, (col0 + c0) / 16)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+              *reinterpret_cast<uint4*>(ptile + swz<C::kPRow>(kt, (R + col0 + c0) / 16)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            }
+            if (!ALL && (!kCols || wg == 0)) {
+              uint8_t* vrow = sV + (h ? st1 : st0) * C::kVTile + kt * D;
+              TSV_PWAIT(&v_full[h ? st1 : st0], h ? ph1 : ph0);
+              if (kt >= block_valid(h)) {  // whatever the row holds
+#pragma unroll
+                for (int c = 0; c < D / 16; ++c) reinterpret_cast<uint4*>(vrow)[c] = make_uint4(0u, 0u, 0u, 0u);
+              } else if (j + h >= nmain) {
+                uint32_t any = 0u;
+#pragma unroll
+                for (int c = 0; c < D / 16; ++c) {
+                  const uint4 w = reinterpret_cast<const uint4*>(vrow)[c];
+                  any |= ((w.x & 0x7F7F7F7Fu) + 0x01010101u) | ((w.y & 0x7F7F7F7Fu) + 0x01010101u) |
+                         ((w.z & 0x7F7F7F7Fu) + 0x01010101u) | ((w.w & 0x7F7F7F7Fu) + 0x01010101u);
+                }
+                any &= 0x80808080u;
+                const uint32_t* see = sDesc + (buf * 256 + block_base(h) + kt) * 2;
+                const unsigned long long rows = (unsigned long long)see[0] | (R > 32 ? (unsigned long long)see[1] << 32 : 0ull);
+#pragma unroll 1
+                for (int c = 0; any && c < D / 4; ++c) {
+                  const uint32_t w = reinterpret_cast<const uint32_t*>(vrow)[c];
+                  uint32_t nan = ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+                  if (nan == 0u) continue;
+                  reinterpret_cast<uint32_t*>(vrow)[c] = w & ~((nan >> 7) * 0xFFu);
+                  const int chunk = D == 128 ? (c >> 2) ^ (kt & 7) : (c >> 2) ^ ((kt >> 1) & 3);
+                  for (; nan; nan &= nan - 1)
+                    atomicOr(sPoison + buf * 128 + chunk * 16 + (c & 3) * 4 + ((__ffs(nan) - 1) >> 3), rows);
+                  sPoisoned[buf] = 1;
+                }
+              }
             }
           }
-        }
+        };
+        if (all) step(std::true_type{});
+        else step(std::false_type{});
         fence_proxy_async_smem();
         tc_fence_before();
-        mbar_arrive(&p_full[x4]);
+        parrive(&p_full[t & 3], dead);
       }
       // Sums of P over the warp's keys (transposed reduction), and their reference.
       if (k >= 2) TSV_PWAIT(&unit_free[buf], (k >> 1) - 1);
@@ -909,7 +1048,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
         sL[(buf * 8 + warp) * RW + first] = lsum[0];
         if (lg == 0 && lane < RW) sMw[(buf * 2 + wg) * RW + lane] = mw;
       }
-      mbar_arrive(&l_full[buf]);
+      parrive(&l_full[buf], dead);
     }
   } else {
     // ------------------------------------------------------------ accumulation: a thread owns a d
@@ -917,9 +1056,14 @@ __global__ void __launch_bounds__(kPThreads, 1)
     const int d = tid & 127, lg = warp & 3;
     const uint32_t lane_base = (uint32_t)(lg * 32) << 16;
     const bool live = d < D;
-    int t = 0, k = 0;
-    for (PUnit u = list.first(x0); u.valid; list.next(u), ++k) {
+    int t = 0;
+    for (int k = 0;; ++k) {
       const int buf = k & 1;
+      TSV_PWAIT(&q_full[buf], k >> 1);
+      if (named_bar_or(kBarAcc, 128, dead)) break;  // the same in every thread of the group
+      const PUnit& u = sUnit[buf];
+      if (!u.valid) break;
+      const int u_j = u.j, u_j1 = u.j1;
       uint64_t acc[R / 2];  // rows 2 i and 2 i + 1
 #pragma unroll
       for (int i = 0; i < R / 2; ++i) acc[i] = 0ull;
@@ -928,8 +1072,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
 #pragma unroll
       for (int i = 0; i < kPer; ++i) mt[i] = -INFINITY;
       float* ab = sAB + lg * 2 * R;        // this warp's factors: rescale, weight of the block
-      TSV_PWAIT(&q_full[buf], k >> 1);  // the unit's output rows
-      for (int j = u.j; j < u.j1; ++j, ++t) {
+      for (int j = u_j; j < u_j1; j += 2, ++t) {
         const int x = t & 1, x4 = t & 3;
         TSV_PWAIT(&p_full[x4], t >> 2);
         const float sv = sSv[x4];
@@ -958,22 +1101,22 @@ __global__ void __launch_bounds__(kPThreads, 1)
         }
         TSV_PWAIT(&o_full[x], t >> 1);
         tc_fence_after();
-        const uint32_t o_col = tmem + lane_base + (uint32_t)(4 * R + x * 2 * R);
-        uint32_t h2[2][16], l2[2][16];  // hi and lo of this chunk of 16 rows and the next
-        tmem_ld16_nowait(o_col, h2[0]);
-        tmem_ld16_nowait(o_col + R, l2[0]);
+        const uint32_t o_col = tmem + lane_base + (uint32_t)(C::kO + x * 2 * R);
+        uint32_t h2[2][8], l2[2][8];  // hi and lo of this chunk of 8 rows and the next
+        tmem_ld8_nowait(o_col, h2[0]);
+        tmem_ld8_nowait(o_col + R, l2[0]);
 #pragma unroll
-        for (int c0 = 0; c0 < R; c0 += 16) {
-          uint32_t(&h)[16] = h2[(c0 >> 4) & 1];
-          uint32_t(&l)[16] = l2[(c0 >> 4) & 1];
+        for (int c0 = 0; c0 < R; c0 += 8) {
+          uint32_t(&h)[8] = h2[(c0 >> 3) & 1];
+          uint32_t(&l)[8] = l2[(c0 >> 3) & 1];
           tmem_wait_tie(h);
           tmem_tie(l);
-          if (c0 + 16 < R) {
-            tmem_ld16_nowait(o_col + c0 + 16, h2[((c0 >> 4) + 1) & 1]);
-            tmem_ld16_nowait(o_col + R + c0 + 16, l2[((c0 >> 4) + 1) & 1]);
+          if (c0 + 8 < R) {
+            tmem_ld8_nowait(o_col + c0 + 8, h2[((c0 >> 3) + 1) & 1]);
+            tmem_ld8_nowait(o_col + R + c0 + 8, l2[((c0 >> 3) + 1) & 1]);
           }
 #pragma unroll
-          for (int i = 0; i < 8; i += 2) {
+          for (int i = 0; i < 4; i += 2) {
             const ulonglong2 be = *reinterpret_cast<const ulonglong2*>(ab + R + c0 + 2 * i);
             const int q = c0 / 2 + i;
 #pragma unroll
@@ -985,7 +1128,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
           }
         }
         tc_fence_before();
-        mbar_arrive(&o_free[x]);
+        parrive(&o_free[x], dead);
       }
       // The unit is done: denominators, then its rows or its partials.
       TSV_PWAIT(&l_full[buf], k >> 1);
@@ -1055,6 +1198,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
           __threadfence();
           // A warp takes 4 rows at a time, a lane 16 bytes of each; the CTAs'
           // partials are brought to a running maximum in order, two in flight.
+          const int first_slot = (int64_t)cf * W / ctas >= u.gx ? 0 : 1;  // the group is its first unit, or its last
           constexpr int RB = 4, CB = 2, L4 = D / 4;  // lanes of a row: D / 4
           const int lane_row = lane / L4, d4 = (lane % L4) * 4;
           constexpr int kRowsPerWarp = 32 / L4;
@@ -1073,7 +1217,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
 #pragma unroll
               for (int x = 0; x < CB; ++x) {
                 const int c = c0 + x;
-                const int64_t s = 2 * c + ((int64_t)c * W / ctas >= u.gx ? 0 : 1);
+                const int64_t s = 2 * c + (c == cf ? first_slot : 0);
 #pragma unroll
                 for (int i = 0; i < RB; ++i) {
                   const int r = r0 + i * kRowsPerWarp + lane_row;
@@ -1113,7 +1257,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
           }
         }
       }
-      mbar_arrive(&unit_free[buf]);
+      parrive(&unit_free[buf], dead);
     }
   }
 
