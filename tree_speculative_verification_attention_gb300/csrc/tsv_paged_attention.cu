@@ -65,7 +65,7 @@ constexpr int kPRegs = 96, kPSoftRegs = 120, kPAccRegs = 112, kPRestRegs = 64;
 static_assert(256 * kPSoftRegs + 128 * kPAccRegs + 256 * kPRestRegs <= kPThreads * kPRegs, "register split");
 constexpr int kPBlock = 128;      // keys of a block
 constexpr int kBarSoft = 1;       // and 2: one per softmax warpgroup
-constexpr int kBarAcc = 3;
+constexpr int kBarAcc = 3, kBarFirst = 4;
 
 template <int D, int R>
 struct PCfg {
@@ -100,12 +100,13 @@ struct PCfg {
   static constexpr int kOffMw = kOffL + 64 * RW;                   // f32 [2][2 groups][RW]
   static constexpr int kOffFin = kOffMw + 16 * RW;                 // f32 [2][R]: sums of a unit
   static constexpr int kOffUnit = kOffFin + 8 * R;                 // PUnit [2]
-  static constexpr int kOffScale = kOffUnit + 128;                 // f32 [V stages][20]: (K, V) of 8 pages, V's largest
+  static constexpr int kOffFirst = kOffUnit + 128;                 // PUnit, then i64 [4]: x0, x1, blocks, CTAs
+  static constexpr int kOffScale = kOffFirst + 96;                 // f32 [V stages][20]: (K, V) of 8 pages, V's largest
   static constexpr int kOffSv = kOffScale + kVStages * 80;         // f32 [4]
   static constexpr int kOffBar = kOffSv + 16;
   // k_full, k_empty, v_full, v_empty, sc_full (per stage), s_full[4], p_full[4], o_full[2], o_free[2], q_full[2], unit_free[2],
-  // l_full[2], mma_done[2]
-  static constexpr int kBars = 2 * kKStages + 3 * kVStages + 20;
+  // l_full[2], d_full[2], mma_done[2]
+  static constexpr int kBars = 2 * kKStages + 3 * kVStages + 22;
   static constexpr int kOffMisc = kOffBar + 8 * kBars;
   static constexpr int kSmem = kOffMisc + 64 + 1024;
   static constexpr int kO = kNS * 2 * R;                           // first column of O: S is [kNS][2 blocks][R], O [2][2 R]
@@ -266,14 +267,17 @@ struct PList {
     u.nmain = (u.P + kPBlock - 1) / kPBlock;
     u.tiles = (u.n * G + R - 1) / R;
   }
+  // The unit at x0 < x1 (called by a whole warp).
   __device__ __forceinline__ PUnit first(int64_t x0) const {
     PUnit u{};
     u.valid = x0 < x1;
     if (!u.valid) return u;
-    while (cum[u.b + 1] <= x0) ++u.b;
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int q = 0; q < TSV_MAX_BATCH / 32; ++q) u.b += __popc(__ballot_sync(0xffffffffu, cum[32 * q + lane + 1] <= x0));
     request(u);
     const int64_t rel = x0 - cum[u.b];
-    const int group = (int)(rel / u.T);
+    const int group = rel <= 0xFFFFFFFFll ? (int)((uint32_t)rel / (uint32_t)u.T) : (int)(rel / u.T);
     u.j = (int)(rel - (int64_t)group * u.T);
     u.g = group / u.tiles;
     u.tile = group - u.g * u.tiles;
@@ -362,6 +366,8 @@ __global__ void __launch_bounds__(kPThreads, 1)
   float* sMw = reinterpret_cast<float*>(smem + C::kOffMw);
   float* sFin = reinterpret_cast<float*>(smem + C::kOffFin);
   PUnit* sUnit = reinterpret_cast<PUnit*>(smem + C::kOffUnit);
+  PUnit* sFirst = reinterpret_cast<PUnit*>(smem + C::kOffFirst);
+  int64_t* sRange = reinterpret_cast<int64_t*>(smem + C::kOffFirst + 64);
   float* sScale = reinterpret_cast<float*>(smem + C::kOffScale);
   float* sSv = reinterpret_cast<float*>(smem + C::kOffSv);
   uint64_t* k_full = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
@@ -376,12 +382,12 @@ __global__ void __launch_bounds__(kPThreads, 1)
   uint64_t* q_full = o_free + 2;
   uint64_t* unit_free = q_full + 2;
   uint64_t* l_full = unit_free + 2;
-  uint64_t* mma_done = l_full + 2;
+  uint64_t* d_full = l_full + 2;  // a unit's tree mask is in
+  uint64_t* mma_done = d_full + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
   int* abort_flag = reinterpret_cast<int*>(smem + C::kOffMisc + 4);
   int* sPoisoned = reinterpret_cast<int*>(smem + C::kOffMisc + 8);   // [2]
   int* sJoin = reinterpret_cast<int*>(smem + C::kOffMisc + 16);
-  int64_t* sTot = reinterpret_cast<int64_t*>(smem + C::kOffMisc + 24);  // [4]
   volatile int* abort_v = abort_flag;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -407,6 +413,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
       mbar_init(&o_full[x], 1);
       mbar_init(&o_free[x], 128);
       mbar_init(&q_full[x], 64);
+      mbar_init(&d_full[x], 64);
       mbar_init(&unit_free[x], 128);
       mbar_init(&l_full[x], 256);
     }
@@ -437,38 +444,140 @@ __global__ void __launch_bounds__(kPThreads, 1)
 
   // The list of blocks: request b holds T_b x Hkv x tiles of them.  A request
   // with nothing to see still gets one (empty) block, which writes its zeros.
-  if (tid < TSV_MAX_BATCH) {
-    int64_t w = 0;
-    PagedRequest r;
-    if (tid < a.B && paged_request(a, tid, &r) && r.n > 0) {
-      const int T = max(1, (r.P + kPBlock - 1) / kPBlock + (tree ? (r.n + kPBlock - 1) / kPBlock : 0));
-      w = (int64_t)T * a.cache.Hkv * ((r.n * a.G + R - 1) / R);
-      sReq[tid] = make_int4(r.off, r.n, r.P, T);
-    }
-    int64_t sum = w;
+  // One warp works it out, and the CTA's range and first unit.
+  if (warp == 0) {
+    int64_t before = 0;
+    if (lane == 0) sCum[0] = 0;
+#pragma unroll 1
+    for (int b0 = 0; b0 < TSV_MAX_BATCH; b0 += 32) {
+      const int b = b0 + lane;
+      int64_t upto = 0;
+      if (b0 < a.B) {
+        PagedRequest r;
+        if (b < a.B && paged_request(a, b, &r) && r.n > 0) {
+          const int T = max(1, (r.P + kPBlock - 1) / kPBlock + (tree ? (r.n + kPBlock - 1) / kPBlock : 0));
+          upto = (int64_t)T * a.cache.Hkv * ((r.n * a.G + R - 1) / R);
+          sReq[b] = make_int4(r.off, r.n, r.P, T);
+        }
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t y = __shfl_up_sync(0xffffffffu, sum, o);
-      if (lane >= o) sum += y;
+        for (int o = 1; o < 32; o <<= 1) {
+          const int64_t y = __shfl_up_sync(0xffffffffu, upto, o);
+          if (lane >= o) upto += y;
+        }
+      }
+      sCum[b + 1] = before + upto;
+      before += __shfl_sync(0xffffffffu, upto, 31);
     }
-    if (lane == 31) sTot[warp] = sum;
-    sCum[tid + 1] = sum;
-    if (tid == 0) sCum[0] = 0;
+    __syncwarp();
+    const int64_t W = before, ctas = min((int64_t)gridDim.x, W);
+    int64_t x0 = W, x1 = W;
+    if ((int)blockIdx.x < ctas) {
+      if (W < (1 << 22)) {  // 32-bit products and quotients (at most 1024 CTAs)
+        x0 = (uint32_t)blockIdx.x * (uint32_t)W / (uint32_t)ctas;
+        x1 = ((uint32_t)blockIdx.x + 1u) * (uint32_t)W / (uint32_t)ctas;
+      } else {
+        x0 = (int64_t)blockIdx.x * W / ctas;
+        x1 = ((int64_t)blockIdx.x + 1) * W / ctas;
+      }
+    }
+    const PList mine{sCum, sReq, a.B, a.G, a.cache.Hkv, R, tree, x1};
+    const PUnit u = mine.first(x0);
+    if (lane == 0) {
+      *sFirst = u;
+      sRange[0] = x0;
+      sRange[1] = x1;
+      sRange[2] = W;
+      sRange[3] = ctas;
+    }
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (tid < TSV_MAX_BATCH) {
-    int64_t before = 0;
-    for (int w = 0; w < warp; ++w) before += sTot[w];
-    sCum[tid + 1] += before;
-  }
-  __syncthreads();
   const uint32_t tmem = *tmem_slot;
-  const int64_t W = sCum[TSV_MAX_BATCH];
-  const int64_t ctas = min((int64_t)gridDim.x, W);  // that have work
-  const int64_t x0 = (int)blockIdx.x < ctas ? (int64_t)blockIdx.x * W / ctas : W;
-  PList list{sCum, sReq, a.B, a.G, a.cache.Hkv, R, tree, (int)blockIdx.x < ctas ? ((int64_t)blockIdx.x + 1) * W / ctas : W};
+  const PList list{sCum, sReq, a.B, a.G, a.cache.Hkv, R, tree, sRange[1]};
+
+  // Rows r_lo .. r_lo + count - 1 of a unit's tile (one warp): their output
+  // rows, score factors and two e4m3 terms.
+  auto prep_rows = [&](const PUnit& u, int buf, int r_lo, int count) {
+    constexpr int E = D / 32;  // elements of a row per lane
+    constexpr int kBatch = 8;  // rows loaded together
+    const int row0 = u.tile * R;
+    const int rows = min(R, u.n * a.G - row0);
+    // Row r of the tile: node (row0 + r) / G, query head g G + (row0 + r) % G.
+    // Lane i knows row r_lo + i.
+    int64_t at_q = 0;
+    if (lane < count) {
+      const int r = r_lo + lane;
+      const int gr = row0 + r;
+      const int node = gr / a.G;
+      const int head = u.g * a.G + (gr - node * a.G);
+      sRow[buf * R + r] = r < rows ? (u.off + node) * a.Hq + head : -1;
+      if (r < rows) at_q = (int64_t)(u.off + node) * a.qs_n + (int64_t)head * a.qs_h;
+    }
+    uint8_t* hi = sQ + buf * 2 * C::kQ;
+    uint8_t* lo = hi + C::kQ;
+#pragma unroll 1
+    for (int r0 = 0; r0 < count; r0 += kBatch) {
+      uint32_t raw[kBatch][E / 2];
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        if (r0 + i >= count) break;
+        const int64_t at = __shfl_sync(0xffffffffu, at_q, r0 + i);
+#pragma unroll
+        for (int e = 0; e < E / 2; ++e) raw[i][e] = 0u;
+        if (r_lo + r0 + i < rows) {
+          const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.q) + at + lane * E;
+          if constexpr (E == 4) {
+            const uint2 w = __ldg(reinterpret_cast<const uint2*>(src));
+            raw[i][0] = w.x;
+            raw[i][1] = w.y;
+          } else {
+            raw[i][0] = __ldg(reinterpret_cast<const uint32_t*>(src));
+          }
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        if (r0 + i >= count) break;
+        const int r = r_lo + r0 + i;
+        uint32_t top = 0u;
+#pragma unroll
+        for (int e = 0; e < E / 2; ++e) top = max(top, max((raw[i][e] << 16) & 0x7FFF0000u, raw[i][e] & 0x7FFF0000u));
+        top = __reduce_max_sync(0xffffffffu, top);
+        const bool fine = top < 0x7F800000u;  // no infinity, no NaN in the row
+        // The largest value moves to [128, 256): exponent 134 as biased.
+        const int up = top == 0u ? 0 : max(-120, min(120, 134 - (int)(top >> 23)));
+        const float mul = __uint_as_float((uint32_t)(127 + up) << 23);
+        if (lane == 0) sFr[buf * R + r] = __uint_as_float((uint32_t)(127 - up) << 23) * (a.scale * 1.4426950408889634f);
+        uint32_t wh = 0u, wl = 0u;
+#pragma unroll
+        for (int e = 0; e < E / 2; ++e) {
+          // A row with an infinity or a NaN is NaN throughout (its scores are).
+          const float y0 = fine ? __uint_as_float(raw[i][e] << 16) * mul : NAN;
+          const float y1 = fine ? __uint_as_float(raw[i][e] & 0xFFFF0000u) * mul : NAN;
+          const uint32_t h2 = e4m3x2(y0, y1), f2 = f16x2_of_e4m3x2(h2);
+          wh |= h2 << (16 * e);
+          wl |= e4m3x2(y0 - f16_lo(f2), y1 - f16_hi(f2)) << (16 * e);
+        }
+        const uint32_t at = swz<D>(r, lane * E / 16) + (lane * E) % 16;
+        if constexpr (E == 4) {
+          *reinterpret_cast<uint32_t*>(hi + at) = wh;
+          *reinterpret_cast<uint32_t*>(lo + at) = wl;
+        } else {
+          *reinterpret_cast<uint16_t*>(hi + at) = (uint16_t)wh;
+          *reinterpret_cast<uint16_t*>(lo + at) = (uint16_t)wl;
+        }
+      }
+    }
+    fence_proxy_async_smem();
+  };
+  // The first unit's rows: every warp but the producers, which start the
+  // copies meanwhile.
+  if (sFirst->valid && (warp < kPProducerWarp || warp >= kPSWarp)) {
+    const int w = warp < kPProducerWarp ? warp : warp - 4;
+    prep_rows(*sFirst, 0, w * (R / 16), R / 16);
+    named_bar_sync(kBarFirst, 512);
+  }
 
   if (warp >= kPProducerWarp && warp < kPSWarp) {
     // ------------------------------------------------------------ producers of K and of V
@@ -489,7 +598,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
     struct Look {
       int id, pages, g, tiles;  // id -1: no keys in this lane's page
     };
-    PUnit u = list.first(x0);  // the unit and block of this lane's page
+    PUnit u = *sFirst;  // the unit and block of this lane's page
     auto advance = [&](int n) {
       while (u.valid && n > 0) {
         const int left = u.j1 - u.j;
@@ -528,13 +637,10 @@ __global__ void __launch_bounds__(kPThreads, 1)
     advance(mine);
     look_id(c0);
     float2 sc0 = look_scale(c0), sc1 = make_float2(0.f, 0.f);
-    const int blocks = __shfl_sync(0xffffffffu, (int)(list.x1 - x0), 0);
+    const int blocks = __shfl_sync(0xffffffffu, (int)(sRange[1] - sRange[0]), 0);
     int t = 0, st = odd, ph = 0;  // of this warp's next block: ring stage and phase
     while (t < blocks) {
-      advance(chunk);
-      look_id(c1);
-      float top = sc0.y;  // the block's largest scale of V
-      for (int o = per >> 1; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      float top = 0.f;  // the block's largest scale of V
       for (int i = odd; i < chunk && t + i < blocks; i += 2) {  // this warp's blocks of the chunk
         if (t + i >= stages) TSV_PWAIT(&empty[st], ph ^ 1);
         if (__any_sync(0xffffffffu, dead || *abort_v)) break;
@@ -551,6 +657,10 @@ __global__ void __launch_bounds__(kPThreads, 1)
           const uint32_t id = __shfl_sync(0xffffffffu, (uint32_t)c0.id, src + (int)p);
           tma_load_page(at + (p << lps) * D, tmap, bar, g, id, pol, lead);
         }
+        if (is_v && i == odd) {  // (the copies of the first block go before the wait for its scales)
+          top = sc0.y;
+          for (int o = per >> 1; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        }
         if (is_v && mine_now) {
           float* sc = sScale + st * 20;
           *reinterpret_cast<float2*>(sc + 2 * pg) = sc0;
@@ -566,9 +676,17 @@ __global__ void __launch_bounds__(kPThreads, 1)
           st -= stages;
           ph ^= 1;
         }
+        // The next chunk's ids go out after this chunk's first block, its scales
+        // after the second.
+        if (i == odd) {
+          advance(chunk);
+          look_id(c1);
+        } else if (i == odd + 2) {
+          sc1 = look_scale(c1);
+        }
       }
+      if (t + odd >= blocks) break;  // (this warp has no block in this chunk, the last)
       t += chunk;
-      sc1 = look_scale(c1);
       if (__any_sync(0xffffffffu, dead || *abort_v)) break;
       c0 = c1;
       sc0 = sc1;
@@ -635,6 +753,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
       const PUnit& u = sUnit[k & 1];
       const int blocks = __shfl_sync(0xffffffffu, u.valid ? u.j1 - u.j : 0, 0);
       if (blocks == 0) break;
+      const int u_j = u.j, u_P = u.P, u_n = u.n, nmain = u.nmain;
       for (int i = 0; i < blocks; ++i) {
         if ((i & 1) == 0) {
           if (t >= 2) TSV_PWAIT(&o_free[t & 1], (t >> 1) - 1);
@@ -649,8 +768,12 @@ __global__ void __launch_bounds__(kPThreads, 1)
         const uint32_t dp = (uint32_t)dP0 + (uint32_t)(((t % C::kPB) * 2 + (i & 1)) * (C::kPTile >> 4));
         const uint32_t dst = tmem + (uint32_t)(C::kO + (t & 1) * 2 * R);
         const uint32_t more = (uint32_t)(i & 1);
+        // The last blocks of the prefix and of the tree: only the 32-key slices
+        // that hold keys (one at least, so that O is written).
+        const int block = u_j + i;
+        const int keys = (block < nmain ? u_P - block * kPBlock : tree ? u_n - (block - nmain) * kPBlock : 0);
 #pragma unroll
-        for (int kk = 0; kk < kPBlock / 32; ++kk)
+        for (int kk = 0; kk < kPBlock / 32; ++kk) if (kk == 0 || 32 * kk < keys)
           umma_e4m3(dst, desc_at(dV0, dv + kk * (32 * D >> 4)), desc_at(dP0, dp + kk * (32 * C::kPRow >> 4)), idO, kk > 0 ? 1u : more, lead);
         if (lead) {
           umma_commit(&v_empty[st]);
@@ -672,11 +795,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
     // ------------------------------------------------------------ Q tiles and tree masks
     setmaxnreg_dec<kPRestRegs>();
     const int q = warp - kPPrepWarp;
-    constexpr int E = D / 32;        // elements of a row per lane
-    constexpr int kMine = R / 2;     // rows of this warp, r_lo ..
-    constexpr int kBatch = 8;        // loaded together
-    const int r_lo = kMine * q;
-    PUnit u = list.first(x0);
+    PUnit u = *sFirst;
     for (int k = 0;; ++k) {
       const int buf = k & 1;
       if (k >= 2) TSV_PWAIT(&unit_free[buf], (k >> 1) - 1);
@@ -686,78 +805,13 @@ __global__ void __launch_bounds__(kPThreads, 1)
         parrive(&q_full[buf], dead);
         break;
       }
-      const int row0 = u.tile * R;
-      const int rows = min(R, u.n * a.G - row0);
-      // Row r of the tile: node (row0 + r) / G, query head g G + (row0 + r) % G.
-      // Lane i knows row r_lo + i.
-      int64_t at_q = 0;
-      const bool on = lane < kMine && r_lo + lane < rows;
-      if (lane < kMine) {
-        const int r = r_lo + lane;
-        const int gr = row0 + r;
-        const int node = gr / a.G;
-        const int head = u.g * a.G + (gr - node * a.G);
-        sRow[buf * R + r] = on ? (u.off + node) * a.Hq + head : -1;
-        if (on) at_q = (int64_t)(u.off + node) * a.qs_n + (int64_t)head * a.qs_h;
-      }
-      uint8_t* hi = sQ + buf * 2 * C::kQ;
-      uint8_t* lo = hi + C::kQ;
-#pragma unroll 1
-      for (int r0 = 0; r0 < kMine; r0 += kBatch) {
-        uint32_t raw[kBatch][E / 2];
-#pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-          const int64_t at = __shfl_sync(0xffffffffu, at_q, r0 + i);
-#pragma unroll
-          for (int e = 0; e < E / 2; ++e) raw[i][e] = 0u;
-          if (r_lo + r0 + i < rows) {
-            const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.q) + at + lane * E;
-            if constexpr (E == 4) {
-              const uint2 w = __ldg(reinterpret_cast<const uint2*>(src));
-              raw[i][0] = w.x;
-              raw[i][1] = w.y;
-            } else {
-              raw[i][0] = __ldg(reinterpret_cast<const uint32_t*>(src));
-            }
-          }
-        }
-#pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-          const int r = r_lo + r0 + i;
-          uint32_t top = 0u;
-#pragma unroll
-          for (int e = 0; e < E / 2; ++e) top = max(top, max((raw[i][e] << 16) & 0x7FFF0000u, raw[i][e] & 0x7FFF0000u));
-          top = __reduce_max_sync(0xffffffffu, top);
-          const bool fine = top < 0x7F800000u;  // no infinity, no NaN in the row
-          // The largest value moves to [128, 256): exponent 134 as biased.
-          const int up = top == 0u ? 0 : max(-120, min(120, 134 - (int)(top >> 23)));
-          const float mul = __uint_as_float((uint32_t)(127 + up) << 23);
-          if (lane == 0) sFr[buf * R + r] = __uint_as_float((uint32_t)(127 - up) << 23) * (a.scale * 1.4426950408889634f);
-          uint32_t wh = 0u, wl = 0u;
-#pragma unroll
-          for (int e = 0; e < E / 2; ++e) {
-            // A row with an infinity or a NaN is NaN throughout (its scores are).
-            const float y0 = fine ? __uint_as_float(raw[i][e] << 16) * mul : NAN;
-            const float y1 = fine ? __uint_as_float(raw[i][e] & 0xFFFF0000u) * mul : NAN;
-            const uint32_t h2 = e4m3x2(y0, y1), f2 = f16x2_of_e4m3x2(h2);
-            wh |= h2 << (16 * e);
-            wl |= e4m3x2(y0 - f16_lo(f2), y1 - f16_hi(f2)) << (16 * e);
-          }
-          const uint32_t at = swz<D>(r, lane * E / 16) + (lane * E) % 16;
-          if constexpr (E == 4) {
-            *reinterpret_cast<uint32_t*>(hi + at) = wh;
-            *reinterpret_cast<uint32_t*>(lo + at) = wl;
-          } else {
-            *reinterpret_cast<uint16_t*>(hi + at) = (uint16_t)wh;
-            *reinterpret_cast<uint16_t*>(lo + at) = (uint16_t)wl;
-          }
-        }
-      }
+      if (k > 0) prep_rows(u, buf, q * (R / 2), R / 2);
+      parrive(&q_full[buf], dead);
       // Rows that see tree key j: word q of sDesc[buf][j] holds rows 32 q .. (two warps).
       if (tree && u.j1 > u.nmain) {
         const int r = q * 32 + lane;
-        const bool has = r < rows;
-        const int i0 = has ? (row0 + r) / a.G : 0;  // the row's node
+        const bool has = r < min(R, u.n * a.G - u.tile * R);
+        const int i0 = has ? (u.tile * R + r) / a.G : 0;  // the row's node
         for (int w = 0; w < (u.n + 31) / 32; ++w) {
           uint32_t bits = 0u;
           if (has) {
@@ -766,7 +820,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
                          : (left >= 32 ? 0xFFFFFFFFu : left > 0 ? (1u << left) - 1u : 0u);
           }
           uint32_t see = 0u;
-#pragma unroll
+#pragma unroll 4
           for (int i = 0; i < 32; ++i) {
             const uint32_t m = __ballot_sync(0xffffffffu, (bits >> i) & 1u);
             if (lane == i) see = m;
@@ -774,8 +828,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
           sDesc[(buf * 256 + w * 32 + lane) * 2 + q] = see;
         }
       }
-      fence_proxy_async_smem();
-      parrive(&q_full[buf], dead);
+      parrive(&d_full[buf], dead);
       list.next(u);
     }
     // Every request's lengths and page ids are checked by one CTA.
@@ -831,6 +884,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
 
         auto step = [&](auto all_c) {
           constexpr bool ALL = decltype(all_c)::value;
+          if (!ALL && j + halves > nmain) TSV_PWAIT(&d_full[buf], k >> 1);
           const int nh = ALL ? 2 : halves;
           // Rows (of this group) that see a key, one bit each.
           auto sees = [&](int h, int key) -> uint32_t {
@@ -940,6 +994,9 @@ __global__ void __launch_bounds__(kPThreads, 1)
           }
 #pragma unroll 1
           for (int h = 0; h < nh; ++h) {  // rolled, here and above: the loop's code is fetched once for both blocks
+            // O reads the 32-key slices that hold keys (and the first): the
+            // other warps have no P to write.
+            if (!ALL && lg > 0 && lg * 32 >= block_valid(h)) continue;
             uint32_t sv2[2][16];  // this chunk of 16 rows and the next
             tmem_ld16_nowait(s_col + h * R, sv2[0]);
             const float2 mine = reinterpret_cast<const float2*>(sScale + (h ? st1 : st0) * 20)[kt >> lps];
@@ -991,12 +1048,13 @@ __global__ void __launch_bounds__(kPThreads, 1)
               TSV_PWAIT(&v_full[h ? st1 : st0], h ? ph1 : ph0);
               if (kt >= block_valid(h)) {  // whatever the row holds
 #pragma unroll
-                for (int c = 0; c < D / 16; ++c) reinterpret_cast<uint4*>(vrow)[c] = make_uint4(0u, 0u, 0u, 0u);
+                for (int c = 0; c < D / 16; ++c)  // (a lane starts at its own chunk: no bank conflicts)
+                  reinterpret_cast<uint4*>(vrow)[(c + kt) % (D / 16)] = make_uint4(0u, 0u, 0u, 0u);
               } else if (j + h >= nmain) {
                 uint32_t any = 0u;
 #pragma unroll
                 for (int c = 0; c < D / 16; ++c) {
-                  const uint4 w = reinterpret_cast<const uint4*>(vrow)[c];
+                  const uint4 w = reinterpret_cast<const uint4*>(vrow)[(c + kt) % (D / 16)];
                   any |= ((w.x & 0x7F7F7F7Fu) + 0x01010101u) | ((w.y & 0x7F7F7F7Fu) + 0x01010101u) |
                          ((w.z & 0x7F7F7F7Fu) + 0x01010101u) | ((w.w & 0x7F7F7F7Fu) + 0x01010101u);
                 }
@@ -1148,7 +1206,8 @@ __global__ void __launch_bounds__(kPThreads, 1)
             const float sum = (lw[0] + lw[C::RW]) + (lw[2 * C::RW] + lw[3 * C::RW]);
             l += mw == -INFINITY ? sum : sum * fast_exp2(mw - mt[i]);
           }
-          fin[r] = l;
+          // A whole group needs the reciprocal (0 for a row that sees nothing).
+          fin[r] = !u.whole() ? l : l == 0.f ? 0.f : 1.f / l;
         }
       }
       float* of = reinterpret_cast<float*>(acc);
@@ -1164,12 +1223,10 @@ __global__ void __launch_bounds__(kPThreads, 1)
       const int rows = min(R, u.n * a.G - u.tile * R);
       __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out);
       if (u.whole()) {
+        __nv_bfloat16* od = out + d;
 #pragma unroll
         for (int r = 0; r < R; ++r)
-          if (r < rows && live) {
-            const float l = fin[r];
-            out[(int64_t)sRow[buf * R + r] * D + d] = __float2bfloat16_rn(l == 0.f ? 0.f : of[r] / l);
-          }
+          if (r < rows && live) od[(int64_t)sRow[buf * R + r] * D] = __float2bfloat16_rn(of[r] * fin[r]);
       } else if (!stop) {
         const int slot = 2 * (int)blockIdx.x + (k == 0 ? 0 : 1);
         float* po = part_o + (int64_t)slot * R * D;
@@ -1184,7 +1241,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
         }
         if (d < R) pm[R + d] = fin[d];
         // CTAs cf .. cl share the group; the last to arrive joins.
-        __threadfence();
+        const int64_t W = sRange[2], ctas = sRange[3];
         const int cf = (int)(((u.gx + 1) * ctas - 1) / W), cl = (int)(((u.gx + u.T) * ctas - 1) / W);
         named_bar_sync(kBarAcc, 128);
         if (d == 0) {
@@ -1195,11 +1252,10 @@ __global__ void __launch_bounds__(kPThreads, 1)
         }
         named_bar_sync(kBarAcc, 128);
         if (*sJoin) {
-          __threadfence();
-          // A warp takes 4 rows at a time, a lane 16 bytes of each; the CTAs'
-          // partials are brought to a running maximum in order, two in flight.
+          // A warp takes 2 rows at a time, a lane 16 bytes of each; the CTAs'
+          // partials are brought to a running maximum in order, five in flight.
           const int first_slot = (int64_t)cf * W / ctas >= u.gx ? 0 : 1;  // the group is its first unit, or its last
-          constexpr int RB = 4, CB = 2, L4 = D / 4;  // lanes of a row: D / 4
+          constexpr int RB = 2, CB = 5, L4 = D / 4;  // lanes of a row: D / 4
           const int lane_row = lane / L4, d4 = (lane % L4) * 4;
           constexpr int kRowsPerWarp = 32 / L4;
           for (int r0 = lg * RB * kRowsPerWarp; r0 < rows; r0 += 4 * RB * kRowsPerWarp) {
@@ -1265,7 +1321,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
   tc_fence_before();
   __syncthreads();
   if (tid == 0 && *abort_v)
-    for (PUnit u = list.first(x0); u.valid; list.next(u)) a.status[u.b] = TSV_ERR_TIMEOUT;
+    for (PUnit u = *sFirst; u.valid; list.next(u)) a.status[u.b] = TSV_ERR_TIMEOUT;
   if (warp == kPSWarp) {
     tc_fence_after();
     tmem_dealloc(tmem, C::kTmem);

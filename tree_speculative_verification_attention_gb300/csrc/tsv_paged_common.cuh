@@ -100,9 +100,9 @@ struct PagedRequest {
 };
 __device__ __forceinline__ bool paged_request(const PagedAttnArgs& a, int b, PagedRequest* r) {
   const int ps = a.cache.page_size;
-  r->off = a.offsets[b];
-  const int end = a.offsets[b + 1];
-  r->P = a.prefix_len[b];
+  r->off = __ldg(a.offsets + b);
+  const int end = __ldg(a.offsets + b + 1);
+  r->P = __ldg(a.prefix_len + b);
   r->n = end - r->off;
   return r->off >= 0 && end >= r->off && end <= a.N && r->n <= a.max_nodes && r->P >= 0 &&
          (int64_t)r->P <= (int64_t)a.table.pages * ps &&
