@@ -93,7 +93,12 @@ def _call(paged, name, **kw):
     for k in kw:
         assert k in args, k
     args.update(kw)
-    return getattr(paged._lib, name)(*args.values())
+    return _raw(paged, name, *args.values())
+
+
+def _raw(paged, name, *args):
+    """The C function, structures by their address."""
+    return getattr(paged._lib, name)(*[paged._at(x) if isinstance(x, ctypes.Structure) else x for x in args])
 
 
 BAD = {
@@ -129,7 +134,7 @@ def test_bad_caches_and_tables_are_refused(paged, name):
         if name != "tsv_paged_append":
             assert _call(paged, name, tree=_table(paged, **kw)) == 1, kw
     dtype = [] if name == "tsv_paged_commit" else [1]
-    assert getattr(paged._lib, name)(H, *dtype, *_nulls(paged, name)) == 1
+    assert _raw(paged, name, H, *dtype, *_nulls(paged, name)) == 1
 
 
 def _nulls(paged, name):
@@ -151,7 +156,7 @@ def test_good_arguments_reach_the_device(paged):
 
 def test_workspace_size_refusals(paged):
     n = ctypes.c_size_t(7)
-    f = paged._lib.tsv_paged_tree_attention_workspace_size
+    f = lambda *a: _raw(paged, "tsv_paged_tree_attention_workspace_size", *a)  # noqa: E731
     c = _cache(paged)
     assert f(None, 1, c, 1, 1, 4, 0, ctypes.byref(n)) == 1
     assert f(H, 1, c, 1, 1, 4, 0, None) == 1

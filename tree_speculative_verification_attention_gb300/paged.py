@@ -14,7 +14,7 @@ import ctypes
 
 import torch
 
-from . import (TSV_ATTN_DEFAULT, TSV_BF16, TSV_F32, TSV_MAX_NODES, _check, _lib, _ptr, _workspace, handle)
+from . import TSV_ATTN_DEFAULT, TSV_BF16, TSV_F32, TSV_MAX_NODES, _HANDLES, _check, _lib, _ptr, _workspace, handle
 
 PAGED_EXPORTED = (
     "tsv_rope_frequencies", "tsv_rope", "tsv_paged_append", "tsv_paged_tree_attention_workspace_size",
@@ -44,7 +44,8 @@ class CPageTable(ctypes.Structure):
 def _declare():
     vp, i32, i64, u32, f32, f64, sz = (ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_uint32,
                                        ctypes.c_float, ctypes.c_double, ctypes.c_size_t)
-    cache, table, e = ctypes.POINTER(CPagedCache), ctypes.POINTER(CPageTable), ctypes.c_int
+    cache = table = vp  # structures go by their address: the quickest argument to convert
+    e = ctypes.c_int
     sig = {
         "tsv_rope_frequencies": [i32, f64, e, f64, f64, f64, f64, ctypes.POINTER(f64), ctypes.POINTER(f32)],
         "tsv_rope": [vp, e, vp, i64, i64, vp, i64, i64, i32, i32, i32, vp, vp, i32, f32, u32, vp],
@@ -61,6 +62,11 @@ def _declare():
 
 
 _declare()
+
+
+def _at(struct):
+    """The address of a structure (None: NULL)."""
+    return None if struct is None else ctypes.addressof(struct)
 
 
 # ----------------------------------------------------------------- C ABI mirror
@@ -84,7 +90,7 @@ def tsv_rope(h, dtype_code, x, x_stride_n, x_stride_h, y, y_stride_n, y_stride_h
 def tsv_paged_append(h, dtype_code, cache, table, start, k, k_stride_n, k_stride_h, v, v_stride_n, v_stride_h,
                      row_offsets, B, N, max_rows, positions, inv_freq, rotary_dim, amplitude, flags, status, stream):
     """cache: CPagedCache, table: CPageTable."""
-    _check(_lib.tsv_paged_append(h, dtype_code, cache, table, _ptr(start), _ptr(k), k_stride_n, k_stride_h, _ptr(v),
+    _check(_lib.tsv_paged_append(h, dtype_code, _at(cache), _at(table), _ptr(start), _ptr(k), k_stride_n, k_stride_h, _ptr(v),
                                  v_stride_n, v_stride_h, _ptr(row_offsets), B, N, max_rows, _ptr(positions),
                                  _ptr(inv_freq), rotary_dim, amplitude, flags, _ptr(status), stream),
            "tsv_paged_append")
@@ -92,7 +98,7 @@ def tsv_paged_append(h, dtype_code, cache, table, start, k, k_stride_n, k_stride
 
 def tsv_paged_tree_attention_workspace_size(h, dtype_code, cache, B, max_nodes, Hq, flags=TSV_ATTN_DEFAULT) -> int:
     out = ctypes.c_size_t()
-    _check(_lib.tsv_paged_tree_attention_workspace_size(h, dtype_code, cache, int(B), int(max_nodes), int(Hq), int(flags),
+    _check(_lib.tsv_paged_tree_attention_workspace_size(h, dtype_code, _at(cache), int(B), int(max_nodes), int(Hq), int(flags),
                                                         ctypes.byref(out)), "tsv_paged_tree_attention_workspace_size")
     return out.value
 
@@ -101,15 +107,15 @@ def tsv_paged_tree_attention(h, dtype_code, q, q_stride_n, q_stride_h, cache, ta
                              node_offsets, anc, out, B, N, max_nodes, Hq, scale, workspace, workspace_bytes, status,
                              flags, stream):
     """tree_table: CPageTable or None."""
-    _check(_lib.tsv_paged_tree_attention(h, dtype_code, _ptr(q), q_stride_n, q_stride_h, cache, table, _ptr(prefix_len),
-                                         tree_table, _ptr(node_offsets), _ptr(anc), _ptr(out), B, N, max_nodes, Hq,
+    _check(_lib.tsv_paged_tree_attention(h, dtype_code, _ptr(q), q_stride_n, q_stride_h, _at(cache), _at(table),
+                                         _ptr(prefix_len), _at(tree_table), _ptr(node_offsets), _ptr(anc), _ptr(out), B, N, max_nodes, Hq,
                                          scale, _ptr(workspace), workspace_bytes, _ptr(status), flags, stream),
            "tsv_paged_tree_attention")
 
 
 def tsv_paged_commit(h, cache, table, tree_table, prefix_len, node_offsets, path, accept_len, B, N, max_nodes, new_len,
                      status, stream):
-    _check(_lib.tsv_paged_commit(h, cache, table, tree_table, _ptr(prefix_len), _ptr(node_offsets), _ptr(path),
+    _check(_lib.tsv_paged_commit(h, _at(cache), _at(table), _at(tree_table), _ptr(prefix_len), _ptr(node_offsets), _ptr(path),
                                  _ptr(accept_len), B, N, max_nodes, _ptr(new_len), _ptr(status), stream),
            "tsv_paged_commit")
 
@@ -117,10 +123,13 @@ def tsv_paged_commit(h, cache, table, tree_table, prefix_len, node_offsets, path
 # ----------------------------------------------------------------- convenience layer
 
 
-def _on(stream, dev):
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _on(stream, index):
     """The raw stream to launch on."""
     if stream is None:
-        return torch.cuda.current_stream(dev).cuda_stream
+        return _raw_stream(index)
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
@@ -132,12 +141,19 @@ def _allocating(stream, dev):
     return torch.cuda.stream(s)
 
 
+_CODES = {torch.bfloat16: TSV_BF16, torch.float32: TSV_F32}
+_INT = torch.int32
+
+
 def _code(dt):
-    if dt == torch.bfloat16:
-        return TSV_BF16
-    if dt == torch.float32:
-        return TSV_F32
-    raise TypeError("the paged cache's operators take bfloat16 or float32 rows, got %s" % dt)
+    code = _CODES.get(dt)
+    if code is None:
+        raise TypeError("the paged cache's operators take bfloat16 or float32 rows, got %s" % dt)
+    return code
+
+
+def _handle(index):
+    return _HANDLES.get(index) or handle(index)
 
 
 def _want(ok, what):
@@ -145,23 +161,31 @@ def _want(ok, what):
         raise ValueError(what)
 
 
-def _ints(name, t, size, dev):
-    """An int32 vector of `size` values on the call's device."""
-    if t.dtype != torch.int32 or t.device != dev or t.dim() != 1 or t.shape[0] != size or not t.is_contiguous():
-        raise ValueError("%s: a contiguous int32 tensor of %d values on %s is wanted" % (name, size, dev))
+def _ints(name, t, size, index):
+    """The address of an int32 vector of `size` values on the call's device."""
+    if t.dtype is not _INT or t.get_device() != index or t.dim() != 1 or t.numel() != size or not t.is_contiguous():
+        raise ValueError("%s: a contiguous int32 tensor of %d values on cuda:%d is wanted" % (name, size, index))
+    return t.data_ptr()
 
 
-def _table(name, t, B, dev):
-    if t.dtype != torch.int32 or t.device != dev or t.dim() != 2 or t.shape[0] != B or (t.shape[1] > 1 and t.stride(1) != 1):
-        raise ValueError("%s: an int32 tensor [%d, pages] on %s is wanted" % (name, B, dev))
-    return CPageTable(t.data_ptr(), t.stride(0), t.shape[1])
+def _table(name, t, B, index):
+    if t.dtype is not _INT or t.get_device() != index or t.dim() != 2:
+        raise ValueError("%s: an int32 tensor [%d, pages] on cuda:%d is wanted" % (name, B, index))
+    rows, pages = t.shape
+    stride, inner = t.stride()
+    if rows != B or (pages > 1 and inner != 1):
+        raise ValueError("%s: an int32 tensor [%d, pages] on cuda:%d is wanted" % (name, B, index))
+    return CPageTable(t.data_ptr(), stride, pages)
 
 
-def _heads(name, t, dev, D=None):
-    """Rows of heads [N, H, D] with the elements of a head next to each other."""
-    if t.device != dev or t.dim() != 3 or (t.stride(2) != 1 and t.shape[2] > 1 and t.numel()) or (D is not None and t.shape[2] != D):
-        raise ValueError("%s: rows of heads [N, H, %s] on %s with contiguous heads are wanted"
-                         % (name, "D" if D is None else D, dev))
+def _heads(name, t, index, D=None):
+    """Shape and strides of rows of heads [N, H, D] with the elements of a head next to each other."""
+    if t.get_device() != index or t.dim() != 3:
+        raise ValueError("%s: rows of heads [N, H, D] on cuda:%d are wanted" % (name, index))
+    shape, strides = t.shape, t.stride()
+    if (strides[2] != 1 and shape[2] > 1 and t.numel()) or (D is not None and shape[2] != D):
+        raise ValueError("%s: rows of heads [N, H, %s] with contiguous heads are wanted" % (name, "D" if D is None else D))
+    return shape, strides
 
 
 def rope_frequencies(rotary_dim, base=10000.0, scaling="none", factor=1.0, trained=0.0, low=1.0, high=32.0, device=None):
@@ -175,10 +199,10 @@ def rope_frequencies(rotary_dim, base=10000.0, scaling="none", factor=1.0, train
     return torch.tensor(f, dtype=torch.float64, device=device), amplitude
 
 
-def _freqs(inv_freq, dev, D):
-    if inv_freq.dtype != torch.float64 or inv_freq.device != dev or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
-        raise ValueError("inv_freq: a contiguous float64 vector on %s is wanted" % dev)
-    rot = 2 * inv_freq.shape[0]
+def _freqs(inv_freq, index, D):
+    if inv_freq.dtype is not torch.float64 or inv_freq.get_device() != index or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
+        raise ValueError("inv_freq: a contiguous float64 vector on cuda:%d is wanted" % index)
+    rot = 2 * inv_freq.numel()
     _want(2 <= rot <= D, "inv_freq: 1 to D / 2 frequencies are wanted")
     return rot
 
@@ -186,20 +210,23 @@ def _freqs(inv_freq, dev, D):
 def rope(x, positions, inv_freq, interleaved=False, inverse=False, amplitude=1.0, out=None, stream=None):
     """Rotates the first 2 * len(inv_freq) elements of every head of x [N, H, D] by its row's position; `inverse` turns
     back (the gradient of the rotation).  `out` may be x (in place).  Returns out."""
-    dev = x.device
-    _heads("x", x, dev)
-    N, H, D = x.shape
-    _ints("positions", positions, N, dev)
-    rot = _freqs(inv_freq, dev, D)
+    index = x.get_device()
+    shape, xs = _heads("x", x, index)
+    _want(index >= 0, "x: a CUDA tensor is wanted")
+    N, H, D = shape
+    pos = _ints("positions", positions, N, index)
+    rot = _freqs(inv_freq, index, D)
+    code = _code(x.dtype)
     if out is None:
-        with _allocating(stream, dev):
-            out = torch.empty((N, H, D), dtype=x.dtype, device=dev)
+        with _allocating(stream, x.device):
+            out = torch.empty((N, H, D), dtype=x.dtype, device=x.device)
+        ys = out.stride()
     else:
-        _heads("out", out, dev, D)
-        _want(out.shape == x.shape and out.dtype == x.dtype, "out: x's shape and type are wanted")
+        oshape, ys = _heads("out", out, index)
+        _want(oshape == shape and out.dtype is x.dtype, "out: x's shape and type are wanted")
     flags = (TSV_ROPE_INTERLEAVED if interleaved else 0) | (TSV_ROPE_INVERSE if inverse else 0)
-    tsv_rope(handle(dev.index), _code(x.dtype), x, x.stride(0), x.stride(1), out, out.stride(0), out.stride(1), N, H, D,
-             positions, inv_freq, rot, float(amplitude), flags, _on(stream, dev))
+    _check(_lib.tsv_rope(_handle(index), code, x.data_ptr(), xs[0], xs[1], out.data_ptr(), ys[0], ys[1], N, H, D, pos,
+                         inv_freq.data_ptr(), rot, amplitude, flags, _on(stream, index)), "tsv_rope")
     return out
 
 
@@ -220,8 +247,10 @@ class PagedCache:
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self.num_pages, self.page_size, self.Hkv, self.D = k.shape
         self.device = k.device
+        self.index = k.get_device()
         self.c = CPagedCache(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), k.stride(0), k.stride(1),
                              k.stride(2), *k.shape)
+        self.at = ctypes.addressof(self.c)
 
     @classmethod
     def empty(cls, num_pages, page_size, Hkv, D, device="cuda", head_major=True):
@@ -241,29 +270,29 @@ def paged_append(cache, page_table, k, v, row_offsets, start=None, positions=Non
     """Writes rows row_offsets[b] .. row_offsets[b+1]-1 of k and v [N, Hkv, D] as rows start[b] .. of request b's pages
     (start None: from row 0), K rotated by `positions` when inv_freq is given; see tsv_paged_append for the scales.
     `max_rows`: the most new rows of one request (default N).  Returns status [B]."""
-    dev = cache.device
+    index = cache.index
     B = row_offsets.shape[0] - 1
-    _heads("k", k, dev, cache.D)
-    _heads("v", v, dev, cache.D)
-    N = k.shape[0]
-    _want(k.shape[1] == cache.Hkv and v.shape == k.shape and v.dtype == k.dtype, "k and v: [N, Hkv, D] of one type are wanted")
-    _ints("row_offsets", row_offsets, B + 1, dev)
-    rot = 0
+    shape, ks = _heads("k", k, index, cache.D)
+    vshape, vs = _heads("v", v, index)
+    N = shape[0]
+    _want(shape[1] == cache.Hkv and vshape == shape and v.dtype is k.dtype, "k and v: [N, Hkv, D] of one type are wanted")
+    offs = _ints("row_offsets", row_offsets, B + 1, index)
+    rot, pos, freq = 0, None, None
     if inv_freq is not None:
-        rot = _freqs(inv_freq, dev, cache.D)
+        rot, freq = _freqs(inv_freq, index, cache.D), inv_freq.data_ptr()
         _want(positions is not None, "positions are wanted with inv_freq")
-        _ints("positions", positions, N, dev)
-    if start is not None:
-        _ints("start", start, B, dev)
+        pos = _ints("positions", positions, N, index)
+    first = None if start is None else _ints("start", start, B, index)
+    table = _table("page_table", page_table, B, index)
+    code = _code(k.dtype)
     if status is None:
-        with _allocating(stream, dev):
-            status = torch.empty(B, dtype=torch.int32, device=dev)
-    else:
-        _ints("status", status, B, dev)
-    tsv_paged_append(handle(dev.index), _code(k.dtype), cache.c, _table("page_table", page_table, B, dev), start, k,
-                     k.stride(0), k.stride(1), v, v.stride(0), v.stride(1), row_offsets, B, N,
-                     N if max_rows is None else int(max_rows), positions if rot else None, inv_freq, rot, float(amplitude),
-                     TSV_ROPE_INTERLEAVED if interleaved else 0, status, _on(stream, dev))
+        with _allocating(stream, cache.device):
+            status = torch.empty(B, dtype=_INT, device=cache.device)
+    st = _ints("status", status, B, index)
+    _check(_lib.tsv_paged_append(_handle(index), code, cache.at, ctypes.addressof(table), first, k.data_ptr(), ks[0], ks[1],
+                                 v.data_ptr(), vs[0], vs[1], offs, B, N, N if max_rows is None else max_rows, pos, freq, rot,
+                                 amplitude, TSV_ROPE_INTERLEAVED if interleaved else 0, st, _on(stream, index)),
+           "tsv_paged_append")
     return status
 
 
@@ -278,35 +307,40 @@ def paged_tree_attention(q, cache, page_table, prefix_len, node_offsets, tree_ta
     """Tree attention over the paged cache: q [N, Hq, D] -> out [N, Hq, D] and status [B].  prefix_len, node_offsets and
     both page tables are device tensors; anc [N, 8] comes from tree_prepare (None: a chain of new tokens); tree_table
     None: the nodes see the prefix alone.  `max_nodes`: the most nodes of one request (default min(N, 256))."""
-    dev = cache.device
+    index = cache.index
     B = node_offsets.shape[0] - 1
-    _heads("q", q, dev, cache.D)
-    N, Hq, D = q.shape
-    _ints("prefix_len", prefix_len, B, dev)
-    _ints("node_offsets", node_offsets, B + 1, dev)
+    shape, qs = _heads("q", q, index, cache.D)
+    N, Hq, D = shape
+    plen = _ints("prefix_len", prefix_len, B, index)
+    offs = _ints("node_offsets", node_offsets, B + 1, index)
+    words = None
     if anc is not None:
-        _want(anc.dtype == torch.int32 and anc.device == dev and anc.shape == (N, 8) and anc.is_contiguous(),
+        _want(anc.dtype is _INT and anc.get_device() == index and anc.shape == (N, 8) and anc.is_contiguous(),
               "anc: the contiguous int32 [N, 8] of tree_prepare is wanted")
+        words = anc.data_ptr()
     if max_nodes is None:
         max_nodes = max(1, min(N, TSV_MAX_NODES))
-    h = handle(dev.index)
-    code = _code(q.dtype)
-    with _allocating(stream, dev):
-        if out is None:
-            out = torch.empty((N, Hq, D), dtype=q.dtype, device=dev)
-        else:
-            _want(out.shape == q.shape and out.dtype == q.dtype and out.is_contiguous() and out.device == dev,
-                  "out: a contiguous tensor of q's shape and type is wanted")
-        if status is None:
-            status = torch.empty(B, dtype=torch.int32, device=dev)
-        else:
-            _ints("status", status, B, dev)
-        if workspace is None:
-            workspace = _workspace(tsv_paged_tree_attention_workspace_size(h, code, cache.c, B, max_nodes, Hq, flags), dev)
-    tsv_paged_tree_attention(h, code, q, q.stride(0), q.stride(1), cache.c, _table("page_table", page_table, B, dev),
-                             prefix_len, None if tree_table is None else _table("tree_table", tree_table, B, dev),
-                             node_offsets, anc, out, B, N, int(max_nodes), Hq, float(scale), workspace, workspace.numel(),
-                             status, int(flags), _on(stream, dev))
+    main = _table("page_table", page_table, B, index)
+    tree = None if tree_table is None else _table("tree_table", tree_table, B, index)
+    h, code = _handle(index), _code(q.dtype)
+    if out is None or status is None or workspace is None:
+        with _allocating(stream, cache.device):
+            if out is None:
+                out = torch.empty((N, Hq, D), dtype=q.dtype, device=cache.device)
+            if status is None:
+                status = torch.empty(B, dtype=_INT, device=cache.device)
+            if workspace is None:
+                workspace = _workspace(tsv_paged_tree_attention_workspace_size(h, code, cache.c, B, max_nodes, Hq, flags),
+                                       cache.device)
+    _want(out.shape == shape and out.dtype is q.dtype and out.is_contiguous() and out.get_device() == index,
+          "out: a contiguous tensor of q's shape and type is wanted")
+    _want(workspace.get_device() == index and workspace.is_contiguous(), "workspace: a contiguous tensor beside the cache is wanted")
+    st = _ints("status", status, B, index)
+    _check(_lib.tsv_paged_tree_attention(h, code, q.data_ptr(), qs[0], qs[1], cache.at, ctypes.addressof(main), plen,
+                                         None if tree is None else ctypes.addressof(tree), offs, words, out.data_ptr(), B, N,
+                                         max_nodes, Hq, scale, workspace.data_ptr(),
+                                         workspace.numel() * workspace.element_size(), st, flags, _on(stream, index)),
+           "tsv_paged_tree_attention")
     return out, status
 
 
@@ -314,22 +348,20 @@ def paged_commit(cache, page_table, tree_table, prefix_len, node_offsets, path, 
                  out=None):
     """Appends the accepted path's rows of the tree pages to the prefix pages: row prefix_len[b] + k takes tree row
     path[k].  Returns dict(new_len, status)."""
-    dev = cache.device
+    index = cache.index
     B = node_offsets.shape[0] - 1
     N = path.shape[0]
-    _ints("prefix_len", prefix_len, B, dev)
-    _ints("node_offsets", node_offsets, B + 1, dev)
-    _ints("path", path, N, dev)
-    _ints("accept_len", accept_len, B, dev)
+    plen = _ints("prefix_len", prefix_len, B, index)
+    offs = _ints("node_offsets", node_offsets, B + 1, index)
+    way = _ints("path", path, N, index)
+    acc = _ints("accept_len", accept_len, B, index)
+    main, tree = _table("page_table", page_table, B, index), _table("tree_table", tree_table, B, index)
     if out is None:
-        with _allocating(stream, dev):
-            out = dict(new_len=torch.empty(B, dtype=torch.int32, device=dev),
-                       status=torch.empty(B, dtype=torch.int32, device=dev))
-    else:
-        _ints("new_len", out["new_len"], B, dev)
-        _ints("status", out["status"], B, dev)
-    tsv_paged_commit(handle(dev.index), cache.c, _table("page_table", page_table, B, dev),
-                     _table("tree_table", tree_table, B, dev), prefix_len, node_offsets, path, accept_len, B, N,
-                     max(1, min(N, TSV_MAX_NODES)) if max_nodes is None else int(max_nodes), out["new_len"], out["status"],
-                     _on(stream, dev))
+        with _allocating(stream, cache.device):
+            out = dict(new_len=torch.empty(B, dtype=_INT, device=cache.device),
+                       status=torch.empty(B, dtype=_INT, device=cache.device))
+    new, st = _ints("new_len", out["new_len"], B, index), _ints("status", out["status"], B, index)
+    _check(_lib.tsv_paged_commit(_handle(index), cache.at, ctypes.addressof(main), ctypes.addressof(tree), plen, offs, way, acc,
+                                 B, N, max(1, min(N, TSV_MAX_NODES)) if max_nodes is None else max_nodes, new, st,
+                                 _on(stream, index)), "tsv_paged_commit")
     return out
