@@ -305,6 +305,11 @@ struct PList {
 
 // A wait that ran out (or saw another role's) leaves the warp `dead`: it goes
 // through the motions without waiting, so that named barriers stay complete.
+// The hardware holds a waiting thread for up to 4 us a try (with the hint;
+// measured), so that waiting warps do not take the working ones' issue slots;
+// 2^18 tries are about a second.  Short on purpose: an SM sub-partition keeps
+// about 2000 instructions at hand, and the roles' loops have to share them.
+constexpr uint32_t kWaitTries = 1u << 18;
 __device__ __forceinline__ bool mbar_try_long(uint32_t at, uint32_t parity) {
   uint32_t ok;
   asm volatile(
@@ -318,17 +323,13 @@ __device__ __forceinline__ bool mbar_try_long(uint32_t at, uint32_t parity) {
 }
 __device__ __forceinline__ void pwait(uint64_t* bar, uint32_t parity, volatile int* abort, bool& dead) {
   const uint32_t at = smem_u32(bar);
-  uint64_t t0 = 0;
 #pragma unroll 1
-  while (!mbar_try_long(at, parity & 1u)) {
-    if (dead || *abort) {
+  for (uint32_t n = 0; !mbar_try_long(at, parity & 1u); ++n)
+    if (dead || *abort || n == kWaitTries) {
+      *abort = 1;
       dead = true;
       break;
     }
-    const uint64_t now = global_timer_ns();
-    if (t0 == 0) t0 = now;
-    if (now - t0 > kWaitLimitNs) *abort = 1;
-  }
   __syncwarp();
 }
 // Arrives for the whole warp, or, once it is dead, not at all: arrivals of a
@@ -633,17 +634,21 @@ __global__ void __launch_bounds__(kPThreads, 1)
       }
       return s;
     };
-    Look c0, c1;
-    advance(mine);
-    look_id(c0);
-    float2 sc0 = look_scale(c0), sc1 = make_float2(0.f, 0.f);
+    Look c0{-1, 0, 0, 0}, c1;
+    float2 sc0 = make_float2(0.f, 0.f), sc1 = sc0;
+    float top = 0.f;  // of the lane's block: V's largest scale
     const int blocks = __shfl_sync(0xffffffffu, (int)(sRange[1] - sRange[0]), 0);
-    int t = 0, st = odd, ph = 0;  // of this warp's next block: ring stage and phase
-    while (t < blocks) {
-      float top = 0.f;  // the block's largest scale of V
-      for (int i = odd; i < chunk && t + i < blocks; i += 2) {  // this warp's blocks of the chunk
+    int st = odd, ph = 0;  // of this warp's next block: ring stage and phase
+    // Chunk t is issued (c0) while the ids of the next one (c1) are looked up,
+    // at its first block, and its scales, at its second.
+#pragma unroll 1
+    for (int t = -chunk;; t += chunk) {
+      advance(t < 0 ? mine : chunk);
+      look_id(c1);
+#pragma unroll 1
+      for (int i = odd; t >= 0 && i < chunk && t + i < blocks; i += 2) {  // this warp's blocks of the chunk
         if (t + i >= stages) TSV_PWAIT(&empty[st], ph ^ 1);
-        if (__any_sync(0xffffffffu, dead || *abort_v)) break;
+        if (__any_sync(0xffffffffu, dead)) break;
         const int src = i << (7 - lps);
         const bool mine_now = mine == i;
         // Pages, whether several row tiles read them (then they stay in L2), head.
@@ -653,6 +658,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
         const uint32_t at = smem_u32(ring) + (uint32_t)(st * tile), bar = smem_u32(&full[st]);
         const bool lead = elect_one();
         if (pages > 0 && lead) mbar_expect_tx(&full[st], (uint32_t)((pages << lps) * D));
+#pragma unroll 1
         for (uint32_t p = 0; p < pages; ++p) {
           const uint32_t id = __shfl_sync(0xffffffffu, (uint32_t)c0.id, src + (int)p);
           tma_load_page(at + (p << lps) * D, tmap, bar, g, id, pol, lead);
@@ -676,18 +682,10 @@ __global__ void __launch_bounds__(kPThreads, 1)
           st -= stages;
           ph ^= 1;
         }
-        // The next chunk's ids go out after this chunk's first block, its scales
-        // after the second.
-        if (i == odd) {
-          advance(chunk);
-          look_id(c1);
-        } else if (i == odd + 2) {
-          sc1 = look_scale(c1);
-        }
+        if (i == odd + 2) sc1 = look_scale(c1);
       }
-      if (t + odd >= blocks) break;  // (this warp has no block in this chunk, the last)
-      t += chunk;
-      if (__any_sync(0xffffffffu, dead || *abort_v)) break;
+      if (__any_sync(0xffffffffu, dead) || t + chunk >= blocks) break;
+      if (t < 0) sc1 = look_scale(c1);
       c0 = c1;
       sc0 = sc1;
     }
@@ -820,7 +818,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
                          : (left >= 32 ? 0xFFFFFFFFu : left > 0 ? (1u << left) - 1u : 0u);
           }
           uint32_t see = 0u;
-#pragma unroll 4
+#pragma unroll 1
           for (int i = 0; i < 32; ++i) {
             const uint32_t m = __ballot_sync(0xffffffffu, (bits >> i) & 1u);
             if (lane == i) see = m;
