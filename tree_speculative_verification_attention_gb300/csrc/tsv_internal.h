@@ -268,10 +268,19 @@ struct PagedWriteArgs {
   int32_t* new_len;
 };
 size_t paged_append_smem_bytes(int32_t page_size, int32_t rot);
-constexpr int kPagedWriteWarps = 8;  // a warp takes 16 rows of one (page, head)
+constexpr int kPagedWriteMaxWarps = 32;
+constexpr int paged_write_rows(int32_t D) { return 512 / D; }  // rows of one (page, head) that a warp takes
+// Warps of a CTA, a whole page of one head at least, and the heads they hold.
+inline int paged_write_warps(int32_t page_size, int32_t D) {
+  const int page = page_size / paged_write_rows(D);
+  return page > 8 ? page : 8;
+}
+inline int paged_write_heads(int32_t page_size, int32_t D) {
+  return paged_write_warps(page_size, D) * paged_write_rows(D) / page_size;
+}
 cudaError_t paged_append_set_attributes(bool bf16, int32_t D);
-cudaError_t launch_paged_append(const PagedWriteArgs& a, bool bf16, cudaStream_t st);
-cudaError_t launch_paged_commit(const PagedWriteArgs& a, cudaStream_t st);
+cudaError_t launch_paged_append(const PagedWriteArgs& a, bool bf16, int num_sms, cudaStream_t st);
+cudaError_t launch_paged_commit(const PagedWriteArgs& a, int num_sms, cudaStream_t st);
 
 // Tree attention over a paged cache.
 struct PagedAttnArgs {

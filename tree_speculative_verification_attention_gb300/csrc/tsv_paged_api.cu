@@ -88,14 +88,16 @@ tsv_status encode_pages(tsv_handle h, CUtensorMap* map, const void* base, const 
 
 bool paged_uses_tc(tsv_dtype dtype, uint32_t flags) { return dtype == TSV_BF16 && !(flags & TSV_ATTN_SIMT); }
 
-// Head groups that one CTA of an append or commit takes in turn: as many as
-// leave 4 CTAs per SM.  A CTA computes its page's angles once, so fewer, longer
-// CTAs save work as soon as the grid fills the machine.
+// Head groups that one CTA of an append takes in turn: as many as leave every
+// SM its 32 warps.  A CTA computes its page's angles once and loads the next
+// group's rows under the current one's arithmetic, so fewer, longer CTAs save
+// work as soon as the grid fills the machine.
 int32_t head_loop(const PagedWriteArgs& a, int64_t rows, int num_sms) {
-  const int hp = kPagedWriteWarps / (a.cache.page_size / 16);
-  const int64_t groups = cdiv(a.cache.Hkv, hp);
+  const int64_t groups = cdiv(a.cache.Hkv, paged_write_heads(a.cache.page_size, a.cache.D));
   const int64_t pages = cdiv(rows, a.cache.page_size) + a.B / 2;
-  return (int32_t)std::max<int64_t>(1, std::min(groups, pages * groups / (4 * (int64_t)num_sms)));
+  const int64_t warps = pages * groups * paged_write_warps(a.cache.page_size, a.cache.D);
+  const int64_t loop = std::max<int64_t>(1, std::min(groups, warps / (32 * (int64_t)num_sms)));
+  return (int32_t)cdiv(groups, cdiv(groups, loop));  // the same number for each CTA
 }
 
 }  // namespace
@@ -214,7 +216,7 @@ tsv_status tsv_paged_append(tsv_handle h, tsv_dtype dtype, const tsv_paged_cache
     if (paged_append_set_attributes(dtype == TSV_BF16, a.cache.D) != cudaSuccess) return TSV_ERR_CUDA;
     h->append_attr_mask |= bit;
   }
-  return cuda_status(launch_paged_append(a, dtype == TSV_BF16, static_cast<cudaStream_t>(stream)));
+  return cuda_status(launch_paged_append(a, dtype == TSV_BF16, h->num_sms, static_cast<cudaStream_t>(stream)));
 }
 
 tsv_status tsv_paged_tree_attention_workspace_size(tsv_handle h, tsv_dtype dtype, const tsv_paged_cache* cache,
@@ -313,7 +315,7 @@ tsv_status tsv_paged_commit(tsv_handle h, const tsv_paged_cache* cache, const ts
   a.accept_len = accept_len_d;
   a.new_len = new_len_d;
   a.head_loop = 1;
-  return cuda_status(launch_paged_commit(a, static_cast<cudaStream_t>(stream)));
+  return cuda_status(launch_paged_commit(a, h->num_sms, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -7,12 +7,14 @@
 //   code              = e4m3(value / scale), nearest even
 //
 // A scale needs every new row of its page before the first code can be
-// written, so the unit of work is one (page, head): 16 rows per warp, a whole
-// page in 1 to 8 warps, its values held in registers between the maximum and
+// written, so the unit of work is one (page, head): 512 values per
+// warp (4 or 8 rows), a whole page in 2 to 32 warps, its values held in registers between the maximum and
 // the rounding - each value is read from HBM once and each code written once,
-// which is the bound.  A CTA takes one page for 128 / page_size heads at a
-// time and walks `head_loop` such groups: the angles of the page's rows are
-// the same for every head and are computed once per CTA.
+// which is the bound.  A CTA takes one page for `hp` heads at a time and walks
+// `head_loop` such groups: the angles of the page's rows are the same for every
+// head and are computed once per CTA, while its first rows are on their way.
+// One row part a lane rather than two or four: 64 registers hold it, so 32
+// warps share an SM and one's loads run under another's rounding.
 //
 // A lane owns 16 values of a row as two chunks of 8: adjacent chunks, or, for
 // the half layout, a chunk and its partner rotary_dim / 2 elements on, so that
@@ -24,8 +26,6 @@
 namespace tsv {
 
 namespace {
-
-constexpr int kWriteThreads = 32 * kPagedWriteWarps;
 
 struct FromCodes {};  // source type of the commit kernel
 
@@ -83,6 +83,26 @@ __device__ __forceinline__ float warp_max(float v) {
   return v;
 }
 
+// The largest finite |x|.  A maximum leaves NaN out by itself; only an infinity
+// needs the second look.
+__device__ __forceinline__ float finite_amax(const float (&x)[16]) {
+  float m = 0.f;
+#pragma unroll
+  for (int e = 0; e < 16; ++e) m = fmaxf(m, fabsf(x[e]));
+  if (m == INFINITY) {
+    m = 0.f;
+    for (int e = 0; e < 16; ++e) m = fmaxf(m, finite_abs(x[e]));
+  }
+  return m;
+}
+
+// The table of angles: rows of `width` floats, their 16-byte blocks 2i and
+// 2i + 1 swapped in the upper half of every 64 floats, so that eight lanes that
+// read the first (or second) blocks of eight neighbouring pairs meet 32
+// different banks.
+__host__ __device__ constexpr int angle_width(int half) { return (half + 7) & ~7; }
+__device__ __forceinline__ int angle_at(int f) { return f ^ ((f >> 3) & 4); }
+
 template <typename T>
 __device__ __forceinline__ float scalar_f32(T v);
 template <>
@@ -91,18 +111,18 @@ template <>
 __device__ __forceinline__ float scalar_f32<__nv_bfloat16>(__nv_bfloat16 v) { return __bfloat162float(v); }
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kWriteThreads) paged_write_kernel(const PagedWriteArgs a) {
+__global__ void __launch_bounds__(32 * kPagedWriteMaxWarps) paged_write_kernel(const PagedWriteArgs a) {
   constexpr bool kCommit = sizeof(Chunk<T>) == sizeof(uint2);
-  constexpr int LPR = D / 16;        // lanes of a row
-  constexpr int RPP = 32 / LPR;      // rows of a warp at a time
-  constexpr int PASSES = 16 / RPP;   // for its 16 rows
+  constexpr int LPR = D / 16;                      // lanes of a row
+  constexpr int ROWS = paged_write_rows(D);        // rows of a warp
+  static_assert(LPR * ROWS == 32, "a lane holds a part of one row");
   pdl_trigger();
   pdl_wait();  // the previous kernel's results are visible from here on
-  extern __shared__ float angles[];  // cosines [page_size][half], then sines
-  __shared__ float amax[2][kPagedWriteWarps];
-  __shared__ int32_t spath[TSV_MAX_NODES];
+  extern __shared__ float4 angle_table[];  // cosines [page_size][width], then sines
+  __shared__ float amax[2][2][kPagedWriteMaxWarps];
+  __shared__ int32_t spath[kCommit ? TSV_MAX_NODES : 1];
 
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, threads = blockDim.x, warp = tid >> 5, lane = tid & 31;
   const int b = blockIdx.y;
   const tsv_paged_cache& C = a.cache;
   const int ps = C.page_size;
@@ -118,13 +138,13 @@ __global__ void __launch_bounds__(kWriteThreads) paged_write_kernel(const PagedW
   const int last = bad || n == 0 ? first - 1 : (start + n - 1) / ps;
   const int32_t* ids = a.table.ids_d + (int64_t)b * a.table.stride;
   if (!bad) {
-    for (int i = first + tid; i <= last; i += kWriteThreads) {
+    for (int i = first + tid; i <= last; i += threads) {
       const int id = ids[i];
       if (id < 0 || id >= C.num_pages) bad = true;
     }
     if constexpr (kCommit) {
       const int32_t* tids = a.tree_table.ids_d + (int64_t)b * a.tree_table.stride;
-      for (int i = tid; i < n; i += kWriteThreads) {
+      for (int i = tid; i < n; i += threads) {
         const int x = a.path[off + i];
         const int before = i == 0 ? -1 : a.path[off + i - 1];
         int id = -1;
@@ -134,39 +154,16 @@ __global__ void __launch_bounds__(kWriteThreads) paged_write_kernel(const PagedW
       }
     }
   }
-  bad = __syncthreads_or(bad);
-  if (blockIdx.x == 0 && blockIdx.z == 0 && tid == 0) {
-    a.status[b] = bad ? TSV_ERR_INVALID_ARG : TSV_OK;
-    if (kCommit && a.new_len) a.new_len[b] = bad ? -1 : start + n;
-  }
-  const int pi = first + blockIdx.x;
-  if (bad || pi > last) return;
-  const int row0 = pi * ps - start;              // new row held by the page's row 0 (negative: kept rows)
-  const int kept = max(-row0, 0), end = min(ps, n - row0);  // new rows: page rows kept .. end - 1
-  const int64_t page = ids[pi];
 
   const bool turn = !kCommit && a.inv_freq != nullptr;
   const int half = a.rot >> 1;
-  const float* ct = angles;
-  const float* st = angles + ps * half;
-  if (turn) {
-    const int per = kWriteThreads / half, f = tid % half;
-    if (tid < per * half) {
-      const uint64_t w = rope_turns(a.inv_freq[f]);
-      for (int r = kept + tid / half; r < end; r += per) {
-        float c, s;
-        rope_cos_sin(a.positions[off + row0 + r], w, &c, &s);
-        angles[r * half + f] = c * a.amplitude;
-        angles[ps * half + r * half + f] = s * a.amplitude;
-      }
-    }
-    __syncthreads();
-  }
-
-  const int wpp = ps >> 4;               // warps of a page
+  float* ct = reinterpret_cast<float*>(angle_table);
+  const int width = angle_width(half);
+  float* st = ct + ps * width;
+  const int wpp = ps / ROWS;  // warps of a page
   const int team = warp / wpp, slice = warp - team * wpp;
-  const int hp = kPagedWriteWarps / wpp;  // heads at a time
-  const int j = lane % LPR, rl = lane / LPR;
+  const int hp = (threads >> 5) / wpp;  // heads at a time
+  const int j = lane % LPR, r = slice * ROWS + lane / LPR;  // its lane's row of the page
   // The lane's chunks: adjacent ones; for K under the half layout with whole
   // chunks on both sides a rotated chunk and its partner.
   const bool pairs = turn && !a.interleaved && a.rot % 16 == 0;
@@ -175,71 +172,112 @@ __global__ void __launch_bounds__(kWriteThreads) paged_write_kernel(const PagedW
   const int k0 = !pairs ? v0 : j < rc ? 8 * j : v0;
   const int k1 = !pairs ? v1 : j < rc ? 8 * j + half : v1;
 
-  for (int it = 0; it < a.head_loop; ++it) {
-    const int g0 = (blockIdx.z * a.head_loop + it) * hp;
-    if (g0 >= C.Hkv) break;  // the same in every thread
-    const int g = g0 + team;
-    const bool on = g < C.Hkv;
-    uint8_t* kp = static_cast<uint8_t*>(C.k_d) + page * C.stride_page + (int64_t)g * C.stride_head;
-    uint8_t* vp = static_cast<uint8_t*>(C.v_d) + page * C.stride_page + (int64_t)g * C.stride_head;
-    float* ksp = C.k_scale_d + page * C.Hkv + g;
-    float* vsp = C.v_scale_d + page * C.Hkv + g;
-    Chunk<T> kc[PASSES][2], vc[PASSES][2];
-    float kf[PASSES], vf[PASSES];  // source scales (commit)
-#pragma unroll
-    for (int p = 0; p < PASSES; ++p) {
-      const int r = slice * 16 + p * RPP + rl;
-      kf[p] = vf[p] = 1.f;
-      if (on && r >= kept && r < end) {
+  Chunk<T> kc[2], vc[2];
+  float kf, vf;  // source scales (commit)
+  int parity = 0;
+  for (int round = 0;; ++round) {
+    const int pi = first + blockIdx.x + round * gridDim.x;
+    const bool work = pi <= last;                      // the same in every thread
+    const int row0 = pi * ps - start;                  // new row held by the page's row 0 (negative: kept rows)
+    const int kept = max(-row0, 0), end = min(ps, n - row0);  // new rows: page rows kept .. end - 1
+    // The lane's part of a row of head group `it`: K's, then V's.
+    auto load = [&](int it, bool is_v) {
+      const int g = (blockIdx.z * a.head_loop + it) * hp + team;
+      Chunk<T>* c = is_v ? vc : kc;
+      float& f = is_v ? vf : kf;
+      f = 1.f;
+      c[0].clear();
+      c[1].clear();
+      if (it < a.head_loop && g < C.Hkv && r >= kept && r < end) {
         const int i = row0 + r;
         if constexpr (kCommit) {
           const int src = spath[i];
           const int64_t sp = src / ps;
-          const int64_t o = sp * C.stride_page + (int64_t)(src - (int)sp * ps) * C.stride_row + (int64_t)g * C.stride_head;
-          const uint8_t* ks = static_cast<const uint8_t*>(C.k_d) + o;
-          const uint8_t* vs = static_cast<const uint8_t*>(C.v_d) + o;
-          kc[p][0].load(ks + k0);
-          kc[p][1].load(ks + k1);
-          vc[p][0].load(vs + v0);
-          vc[p][1].load(vs + v1);
-          kf[p] = C.k_scale_d[sp * C.Hkv + g];
-          vf[p] = C.v_scale_d[sp * C.Hkv + g];
+          const uint8_t* row = static_cast<const uint8_t*>(is_v ? C.v_d : C.k_d) + sp * C.stride_page +
+                               (int64_t)(src - (int)sp * ps) * C.stride_row + (int64_t)g * C.stride_head;
+          c[0].load(row + (is_v ? v0 : k0));
+          c[1].load(row + (is_v ? v1 : k1));
+          f = (is_v ? C.v_scale_d : C.k_scale_d)[sp * C.Hkv + g];
         } else {
-          const T* ks = static_cast<const T*>(a.k) + (int64_t)(off + i) * a.ks_n + (int64_t)g * a.ks_h;
-          const T* vs = static_cast<const T*>(a.v) + (int64_t)(off + i) * a.vs_n + (int64_t)g * a.vs_h;
-          kc[p][0].load(ks + k0);
-          kc[p][1].load(ks + k1);
-          vc[p][0].load(vs + v0);
-          vc[p][1].load(vs + v1);
+          const T* row = is_v ? static_cast<const T*>(a.v) + (int64_t)(off + i) * a.vs_n + (int64_t)g * a.vs_h
+                              : static_cast<const T*>(a.k) + (int64_t)(off + i) * a.ks_n + (int64_t)g * a.ks_h;
+          c[0].load(row + (is_v ? v0 : k0));
+          c[1].load(row + (is_v ? v1 : k1));
         }
-      } else {
-        kc[p][0].clear();
-        kc[p][1].clear();
-        vc[p][0].clear();
-        vc[p][1].clear();
+      }
+    };
+    if (round > 0) __syncthreads();  // the previous page's angles have been read
+    if (!kCommit && work) {  // (a commit's rows come from pages that are checked first)
+      load(0, false);
+      load(0, true);
+    }
+    if (work && turn) {
+      const int per = threads / half, f = tid % half;
+      if (tid < per * half) {
+        const uint64_t w = rope_turns(a.inv_freq[f]);
+        for (int r = kept + tid / half; r < end; r += per) {
+          float c, s;
+          rope_cos_sin(a.positions[off + row0 + r], w, &c, &s);
+          const int at = r * width + angle_at(f);
+          ct[at] = c * a.amplitude;
+          st[at] = s * a.amplitude;
+        }
       }
     }
-    const float k_old = on && kept > 0 ? *ksp : 0.f, v_old = on && kept > 0 ? *vsp : 0.f;
+    if (round == 0) {
+      bad = __syncthreads_or(bad);
+      if (blockIdx.x == 0 && blockIdx.z == 0 && tid == 0) {
+        a.status[b] = bad ? TSV_ERR_INVALID_ARG : TSV_OK;
+        if (kCommit && a.new_len) a.new_len[b] = bad ? -1 : start + n;
+      }
+      if (bad) return;
+    } else {
+      __syncthreads();
+    }
+    if (!work) return;
+    if (kCommit) {
+      load(0, false);
+      load(0, true);
+    }
+    const int64_t page = ids[pi];
 
-    float kx[PASSES][16];
-    float km = 0.f, vm = 0.f;
-#pragma unroll
-    for (int p = 0; p < PASSES; ++p) {
-      const int r = slice * 16 + p * RPP + rl;
-      kc[p][0].get(kx[p], kf[p]);
-      kc[p][1].get(kx[p] + 8, kf[p]);
+    for (int it = 0; it < a.head_loop; ++it) {
+      const int g0 = (blockIdx.z * a.head_loop + it) * hp;
+      if (g0 >= C.Hkv) break;  // the same in every thread
+      const int g = g0 + team;
+      const bool on = g < C.Hkv;
+      uint8_t* kp = static_cast<uint8_t*>(C.k_d) + page * C.stride_page + (int64_t)g * C.stride_head;
+      uint8_t* vp = static_cast<uint8_t*>(C.v_d) + page * C.stride_page + (int64_t)g * C.stride_head;
+      float* ksp = C.k_scale_d + page * C.Hkv + g;
+      float* vsp = C.v_scale_d + page * C.Hkv + g;
+      const float k_old = on && kept > 0 ? *ksp : 0.f, v_old = on && kept > 0 ? *vsp : 0.f;
+
+      float kx[16];
+      float km = 0.f, vm = 0.f;
+      kc[0].get(kx, kf);
+      kc[1].get(kx + 8, kf);
+      load(it + 1, false);  // the next head's K goes while this one is turned and rounded
       if (turn && on && r >= kept && r < end) {
-        const float* c = ct + r * half;
-        const float* s = st + r * half;
-        if (pairs) {
-          if (j < rc) {
+        const float* c = ct + r * width;
+        const float* s = st + r * width;
+        if (pairs || a.interleaved) {
+          // The lane's pairs have the angles 8 j .. 8 j + 7.
+          if (pairs ? j < rc : v0 < a.rot) {
+            float cs[8], sn[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) rope_pair(kx[p][e], kx[p][8 + e], c[k0 + e], s[k0 + e]);
+            for (int e = 0; e < 8; e += 4) {
+              *reinterpret_cast<float4*>(cs + e) = *reinterpret_cast<const float4*>(c + angle_at(8 * j + e));
+              *reinterpret_cast<float4*>(sn + e) = *reinterpret_cast<const float4*>(s + angle_at(8 * j + e));
+            }
+            if (pairs) {
+#pragma unroll
+              for (int e = 0; e < 8; ++e) rope_pair(kx[e], kx[8 + e], cs[e], sn[e]);
+            } else {
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                if (v0 + 2 * e < a.rot) rope_pair(kx[2 * e], kx[2 * e + 1], cs[e], sn[e]);
+            }
           }
-        } else if (a.interleaved) {
-#pragma unroll
-          for (int e = 0; e < 16; e += 2)
-            if (k0 + e < a.rot) rope_pair(kx[p][e], kx[p][e + 1], c[(k0 + e) >> 1], s[(k0 + e) >> 1]);
         } else if constexpr (!kCommit) {
           // Half layout that cuts a chunk: the partner is read again.
           const T* ks = static_cast<const T*>(a.k) + (int64_t)(off + row0 + r) * a.ks_n + (int64_t)g * a.ks_h;
@@ -249,60 +287,57 @@ __global__ void __launch_bounds__(kWriteThreads) paged_write_kernel(const PagedW
             if (d < a.rot) {
               const bool low = d < half;
               const float q = scalar_f32<T>(ks[low ? d + half : d - half]);
-              const int f = low ? d : d - half;
-              float x = kx[p][e], y = q;
+              const int f = angle_at(low ? d : d - half);
+              float x = kx[e], y = q;
               if (low) {
                 rope_pair(x, y, c[f], s[f]);
-                kx[p][e] = x;
+                kx[e] = x;
               } else {
                 rope_pair(y, x, c[f], s[f]);
-                kx[p][e] = x;
+                kx[e] = x;
               }
             }
           }
         }
       }
-#pragma unroll
-      for (int e = 0; e < 16; ++e) km = fmaxf(km, finite_abs(kx[p][e]));
+      km = finite_amax(kx);
       float vx[16];
-      vc[p][0].get(vx, vf[p]);
-      vc[p][1].get(vx + 8, vf[p]);
-#pragma unroll
-      for (int e = 0; e < 16; ++e) vm = fmaxf(vm, finite_abs(vx[e]));
-    }
-    km = warp_max(km);
-    vm = warp_max(vm);
-    if (it > 0) __syncthreads();  // the previous group's maxima have been read
-    if (lane == 0) {
-      amax[0][warp] = km;
-      amax[1][warp] = vm;
-    }
-    __syncthreads();  // also: every thread has read the old scales
-    if (!on) continue;
-    km = vm = 0.f;
-    for (int w = 0; w < wpp; ++w) {
-      km = fmaxf(km, amax[0][team * wpp + w]);
-      vm = fmaxf(vm, amax[1][team * wpp + w]);
-    }
-    const float k_scale = fmaxf(k_old, pow2_scale(km)), v_scale = fmaxf(v_old, pow2_scale(vm));
-    const float k_inv = 1.f / k_scale, v_inv = 1.f / v_scale;
-    if (slice == 0 && lane == 0) {
-      *ksp = k_scale;
-      *vsp = v_scale;
-    }
-    const float k_again = k_old * k_inv, v_again = v_old * v_inv;
-#pragma unroll
-    for (int p = 0; p < PASSES; ++p) {
-      const int r = slice * 16 + p * RPP + rl;
+      vc[0].get(vx, vf);
+      vc[1].get(vx + 8, vf);
+      vm = finite_amax(vx);
+      km = warp_max(km);
+      vm = warp_max(vm);
+      // Two sets of maxima in turn: a set is written again behind the next one's barrier.
+      float(*most)[kPagedWriteMaxWarps] = amax[parity];
+      parity ^= 1;
+      if (lane == 0) {
+        most[0][warp] = km;
+        most[1][warp] = vm;
+      }
+      __syncthreads();  // also: every thread has read the old scales
+      if (!on) continue;  // (no later group of this team is on either)
+      km = vm = 0.f;
+      for (int w = 0; w < wpp; ++w) {
+        km = fmaxf(km, most[0][team * wpp + w]);
+        vm = fmaxf(vm, most[1][team * wpp + w]);
+      }
+      const float k_scale = fmaxf(k_old, pow2_scale(km)), v_scale = fmaxf(v_old, pow2_scale(vm));
+      const float k_inv = 1.f / k_scale, v_inv = 1.f / v_scale;
+      if (slice == 0 && lane == 0) {
+        *ksp = k_scale;
+        *vsp = v_scale;
+      }
+      const float k_again = k_old * k_inv, v_again = v_old * v_inv;
       uint8_t* kr = kp + (int64_t)r * C.stride_row;
       uint8_t* vr = vp + (int64_t)r * C.stride_row;
       if (r >= kept && r < end) {
         float vx[16];
-        vc[p][0].get(vx, vf[p]);
-        vc[p][1].get(vx + 8, vf[p]);
+        vc[0].get(vx, vf);
+        vc[1].get(vx + 8, vf);
         const uint2 va = pack8(vx, v_inv), vb = pack8(vx + 8, v_inv);
-        *reinterpret_cast<uint2*>(kr + k0) = pack8(kx[p], k_inv);
-        *reinterpret_cast<uint2*>(kr + k1) = pack8(kx[p] + 8, k_inv);
+        load(it + 1, true);
+        *reinterpret_cast<uint2*>(kr + k0) = pack8(kx, k_inv);
+        *reinterpret_cast<uint2*>(kr + k1) = pack8(kx + 8, k_inv);
         *reinterpret_cast<uint4*>(vr + v0) = make_uint4(va.x, va.y, vb.x, vb.y);
       } else if (r < kept) {
 #pragma unroll
@@ -332,16 +367,23 @@ int32_t most_pages(const PagedWriteArgs& a) {
 }
 
 template <typename T, int D>
-cudaError_t launch_typed(const PagedWriteArgs& a, size_t smem, cudaStream_t st) {
-  const int hp = kPagedWriteWarps / (a.cache.page_size / 16);
-  const int groups = (a.cache.Hkv + hp - 1) / hp;
-  const dim3 grid(max(1, most_pages(a)), a.B, (groups + a.head_loop - 1) / a.head_loop);
-  return launch_pdl(paged_write_kernel<T, D>, grid, dim3(kWriteThreads), smem, st, 0u, a);
+cudaError_t launch_typed(const PagedWriteArgs& a, size_t smem, int num_sms, cudaStream_t st) {
+  const int warps = paged_write_warps(a.cache.page_size, D);
+  const int hp = paged_write_heads(a.cache.page_size, D);
+  const int groups = (a.cache.Hkv + hp - 1) / hp, gz = (groups + a.head_loop - 1) / a.head_loop;
+  // CTAs for every page that a request could touch, up to 8 per SM: lengths are
+  // read on the device, most requests touch far fewer pages (a commit one or
+  // two), and the rest of a long one is walked.
+  const int most = (int)max((int64_t)1, 8 * num_sms / ((int64_t)a.B * gz));
+  const dim3 grid(min(max(1, most_pages(a)), most), a.B, gz);
+  return launch_pdl(paged_write_kernel<T, D>, grid, dim3(32 * warps), smem, st, 0u, a);
 }
 
 }  // namespace
 
-size_t paged_append_smem_bytes(int32_t page_size, int32_t rot) { return (size_t)page_size * rot * sizeof(float); }
+size_t paged_append_smem_bytes(int32_t page_size, int32_t rot) {
+  return (size_t)page_size * 2 * angle_width(rot / 2) * sizeof(float);
+}
 
 cudaError_t paged_append_set_attributes(bool bf16, int32_t D) {
   const int most = (int)paged_append_smem_bytes(128, D);
@@ -353,15 +395,15 @@ cudaError_t paged_append_set_attributes(bool bf16, int32_t D) {
                  : cudaFuncSetAttribute(paged_write_kernel<float, 128>, what, most);
 }
 
-cudaError_t launch_paged_append(const PagedWriteArgs& a, bool bf16, cudaStream_t st) {
+cudaError_t launch_paged_append(const PagedWriteArgs& a, bool bf16, int num_sms, cudaStream_t st) {
   const size_t smem = a.inv_freq ? paged_append_smem_bytes(a.cache.page_size, a.rot) : 0;
   if (bf16)
-    return a.cache.D == 64 ? launch_typed<__nv_bfloat16, 64>(a, smem, st) : launch_typed<__nv_bfloat16, 128>(a, smem, st);
-  return a.cache.D == 64 ? launch_typed<float, 64>(a, smem, st) : launch_typed<float, 128>(a, smem, st);
+    return a.cache.D == 64 ? launch_typed<__nv_bfloat16, 64>(a, smem, num_sms, st) : launch_typed<__nv_bfloat16, 128>(a, smem, num_sms, st);
+  return a.cache.D == 64 ? launch_typed<float, 64>(a, smem, num_sms, st) : launch_typed<float, 128>(a, smem, num_sms, st);
 }
 
-cudaError_t launch_paged_commit(const PagedWriteArgs& a, cudaStream_t st) {
-  return a.cache.D == 64 ? launch_typed<FromCodes, 64>(a, 0, st) : launch_typed<FromCodes, 128>(a, 0, st);
+cudaError_t launch_paged_commit(const PagedWriteArgs& a, int num_sms, cudaStream_t st) {
+  return a.cache.D == 64 ? launch_typed<FromCodes, 64>(a, 0, num_sms, st) : launch_typed<FromCodes, 128>(a, 0, num_sms, st);
 }
 
 }  // namespace tsv
