@@ -52,7 +52,9 @@ typedef struct {
 } tsv_paged_cache;
 
 /* Page lists of B requests: entry i of request b is ids_d[b * stride + i],
- * i < pages.  Entries that a call does not need are not read. */
+ * i < pages; pages x page_size is TSV_PAGED_MAX_ROWS at most.  Entries that a
+ * call does not need are not read. */
+#define TSV_PAGED_MAX_ROWS (1 << 30)
 typedef struct {
   const int32_t* ids_d;
   int64_t stride;

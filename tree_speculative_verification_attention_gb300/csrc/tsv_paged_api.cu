@@ -52,9 +52,10 @@ tsv_status check_cache(const tsv_paged_cache* in, tsv_paged_cache* c) {
   return TSV_OK;
 }
 
-tsv_status check_table(const tsv_page_table* t, int32_t B) {
+tsv_status check_table(const tsv_page_table* t, int32_t B, const tsv_paged_cache& c) {
   if (!t || !t->ids_d || t->pages < 1) return TSV_ERR_INVALID_ARG;
   if (B > 1 && t->stride < t->pages) return TSV_ERR_INVALID_ARG;
+  if ((int64_t)t->pages * c.page_size > TSV_PAGED_MAX_ROWS) return TSV_ERR_UNSUPPORTED;
   return TSV_OK;
 }
 
@@ -88,16 +89,23 @@ tsv_status encode_pages(tsv_handle h, CUtensorMap* map, const void* base, const 
 
 bool paged_uses_tc(tsv_dtype dtype, uint32_t flags) { return dtype == TSV_BF16 && !(flags & TSV_ATTN_SIMT); }
 
-// Head groups that one CTA of an append takes in turn: as many as leave every
-// SM its 32 warps.  A CTA computes its page's angles once and loads the next
-// group's rows under the current one's arithmetic, so fewer, longer CTAs save
-// work as soon as the grid fills the machine.
-int32_t head_loop(const PagedWriteArgs& a, int64_t rows, int num_sms) {
+// Head groups that one CTA of an append or commit takes in turn, of about
+// `pages` pages to write.  What it does once (the angles, or the chain of loads
+// from the lengths to the path's pages) costs as much as `once` groups, and the
+// next group's rows are loaded under the current one's arithmetic: the grid is
+// split over the heads as finely as does not cost another wave of 32 warps per
+// SM.
+int32_t head_loop(const PagedWriteArgs& a, int64_t pages, int once, int num_sms) {
   const int64_t groups = cdiv(a.cache.Hkv, paged_write_heads(a.cache.page_size, a.cache.D));
-  const int64_t pages = cdiv(rows, a.cache.page_size) + a.B / 2;
-  const int64_t warps = pages * groups * paged_write_warps(a.cache.page_size, a.cache.D);
-  const int64_t loop = std::max<int64_t>(1, std::min(groups, warps / (32 * (int64_t)num_sms)));
-  return (int32_t)cdiv(groups, cdiv(groups, loop));  // the same number for each CTA
+  const int64_t slots = num_sms * std::max(1, 32 / paged_write_warps(a.cache.page_size, a.cache.D));
+  int64_t loop = groups, least = INT64_MAX;
+  for (int64_t z = 1; z <= std::min<int64_t>(groups, 256); ++z) {
+    const int64_t cost = cdiv(pages * z, slots) * (once + cdiv(groups, z));
+    if (cost > least) continue;
+    least = cost;
+    loop = cdiv(groups, z);
+  }
+  return (int32_t)loop;
 }
 
 }  // namespace
@@ -181,7 +189,7 @@ tsv_status tsv_paged_append(tsv_handle h, tsv_dtype dtype, const tsv_paged_cache
   if (B < 1 || B > TSV_MAX_BATCH || N < 0 || max_rows < 0 || !row_offsets_d || !status_d) return TSV_ERR_INVALID_ARG;
   PagedWriteArgs a{};
   tsv_status st = check_cache(cache, &a.cache);
-  if (st == TSV_OK) st = check_table(table, B);
+  if (st == TSV_OK) st = check_table(table, B, a.cache);
   if (st != TSV_OK) return st;
   if (inv_freq_d && (rotary_dim < 2 || rotary_dim % 2 || rotary_dim > a.cache.D)) return TSV_ERR_INVALID_ARG;
   const int64_t esz = dtype == TSV_BF16 ? 2 : 4;
@@ -210,7 +218,7 @@ tsv_status tsv_paged_append(tsv_handle h, tsv_dtype dtype, const tsv_paged_cache
   a.rot = inv_freq_d ? rotary_dim : 0;
   a.interleaved = (flags & TSV_ROPE_INTERLEAVED) ? 1 : 0;
   a.amplitude = amplitude;
-  a.head_loop = head_loop(a, N, h->num_sms);
+  a.head_loop = head_loop(a, std::max<int64_t>(1, cdiv(N, a.cache.page_size) + B / 2), inv_freq_d ? 2 : 0, h->num_sms);
   const uint32_t bit = 1u << ((dtype == TSV_BF16 ? 2 : 0) + (a.cache.D == 128 ? 1 : 0));
   if (!(h->append_attr_mask & bit)) {
     if (paged_append_set_attributes(dtype == TSV_BF16, a.cache.D) != cudaSuccess) return TSV_ERR_CUDA;
@@ -241,8 +249,8 @@ tsv_status tsv_paged_tree_attention(tsv_handle h, tsv_dtype dtype, const void* q
                                     void* stream) {
   PagedAttnArgs a{};
   tsv_status st = check_attention(h, dtype, cache, &a.cache, B, max_nodes, Hq, flags);
-  if (st == TSV_OK) st = check_table(table, B);
-  if (st == TSV_OK && tree_table) st = check_table(tree_table, B);
+  if (st == TSV_OK) st = check_table(table, B, a.cache);
+  if (st == TSV_OK && tree_table) st = check_table(tree_table, B, a.cache);
   if (st != TSV_OK) return st;
   if (!prefix_len_d || !node_offsets_d || !status_d || N < 0) return TSV_ERR_INVALID_ARG;
   if (!(scale >= 0.f) || isinf(scale) || (anc_d && !aligned16(anc_d))) return TSV_ERR_INVALID_ARG;
@@ -298,8 +306,8 @@ tsv_status tsv_paged_commit(tsv_handle h, const tsv_paged_cache* cache, const ts
   if (new_len_d == prefix_len_d) return TSV_ERR_INVALID_ARG;
   PagedWriteArgs a{};
   tsv_status st = check_cache(cache, &a.cache);
-  if (st == TSV_OK) st = check_table(table, B);
-  if (st == TSV_OK) st = check_table(tree_table, B);
+  if (st == TSV_OK) st = check_table(table, B, a.cache);
+  if (st == TSV_OK) st = check_table(tree_table, B, a.cache);
   if (st != TSV_OK) return st;
   const DeviceScope scope(h->device);
   if (!scope.ok) return TSV_ERR_CUDA;
@@ -314,7 +322,7 @@ tsv_status tsv_paged_commit(tsv_handle h, const tsv_paged_cache* cache, const ts
   a.path = path_d;
   a.accept_len = accept_len_d;
   a.new_len = new_len_d;
-  a.head_loop = 1;
+  a.head_loop = head_loop(a, B + B / 2, 4, h->num_sms);  // (an accepted path ends in one or two pages)
   return cuda_status(launch_paged_commit(a, h->num_sms, static_cast<cudaStream_t>(stream)));
 }
 

@@ -86,11 +86,12 @@ __device__ __forceinline__ void rope_cos_sin(int32_t position, uint64_t turns, f
   sincospif((float)frac * 4.656612873077392578125e-10f, s, c);                             // 2^-31: half turns
 }
 
-// One rotated pair.
+// One rotated pair.  The roundings are spelled out: every kernel and vector
+// width gives the same bits.
 __device__ __forceinline__ void rope_pair(float& a, float& b, float c, float s) {
   const float x = a, y = b;
-  a = x * c - y * s;
-  b = y * c + x * s;
+  a = __fmaf_rn(x, c, -__fmul_rn(y, s));
+  b = __fmaf_rn(y, c, __fmul_rn(x, s));
 }
 
 // Lengths of request b of an attention call; false when they do not fit the

@@ -21,6 +21,8 @@
 // a pair never leaves its thread.
 #include <cuda_runtime.h>
 
+#include <type_traits>
+
 #include "tsv_paged_common.cuh"
 
 namespace tsv {
@@ -36,7 +38,7 @@ template <>
 struct Chunk<__nv_bfloat16> {
   uint4 w;
   __device__ __forceinline__ void clear() { w = make_uint4(0u, 0u, 0u, 0u); }
-  __device__ __forceinline__ void load(const __nv_bfloat16* p) { w = __ldg(reinterpret_cast<const uint4*>(p)); }
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) { w = __ldcs(reinterpret_cast<const uint4*>(p)); }
   __device__ __forceinline__ void get(float* f, float) const {
     const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
@@ -51,8 +53,8 @@ struct Chunk<float> {
   float4 a, b;
   __device__ __forceinline__ void clear() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
   __device__ __forceinline__ void load(const float* p) {
-    a = __ldg(reinterpret_cast<const float4*>(p));
-    b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+    a = __ldcs(reinterpret_cast<const float4*>(p));
+    b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
   }
   __device__ __forceinline__ void get(float* f, float) const {
     f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w;
@@ -77,10 +79,9 @@ __device__ __forceinline__ uint2 pack8(const float* f, float inv) {
   return r;
 }
 
+// Of values >= 0: their bits order them.
 __device__ __forceinline__ float warp_max(float v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-  return v;
+  return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(v)));
 }
 
 // The largest finite |x|.  A maximum leaves NaN out by itself; only an infinity
@@ -94,6 +95,23 @@ __device__ __forceinline__ float finite_amax(const float (&x)[16]) {
     for (int e = 0; e < 16; ++e) m = fmaxf(m, finite_abs(x[e]));
   }
   return m;
+}
+
+// The largest finite |value| of two chunks; of bf16 in pairs, as they are.
+template <typename T>
+__device__ __forceinline__ float source_amax(const Chunk<T> (&c)[2], float s) {
+  float x[16];
+  if constexpr (std::is_same_v<T, __nv_bfloat16>) {
+    const uint32_t w[8] = {c[0].w.x, c[0].w.y, c[0].w.z, c[0].w.w, c[1].w.x, c[1].w.y, c[1].w.z, c[1].w.w};
+    uint32_t m = 0u;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) asm("max.bf16x2 %0, %0, %1;" : "+r"(m) : "r"(w[i] & 0x7FFF7FFFu));
+    const float best = fmaxf(__uint_as_float(m << 16), __uint_as_float(m & 0xFFFF0000u));
+    if (best < INFINITY) return best;
+  }
+  c[0].get(x, s);
+  c[1].get(x + 8, s);
+  return finite_amax(x);
 }
 
 // The table of angles: rows of `width` floats, their 16-byte blocks 2i and
@@ -113,6 +131,7 @@ __device__ __forceinline__ float scalar_f32<__nv_bfloat16>(__nv_bfloat16 v) { re
 template <typename T, int D>
 __global__ void __launch_bounds__(32 * kPagedWriteMaxWarps) paged_write_kernel(const PagedWriteArgs a) {
   constexpr bool kCommit = sizeof(Chunk<T>) == sizeof(uint2);
+  using S = std::conditional_t<kCommit, uint8_t, T>;  // element of a source row
   constexpr int LPR = D / 16;                      // lanes of a row
   constexpr int ROWS = paged_write_rows(D);        // rows of a warp
   static_assert(LPR * ROWS == 32, "a lane holds a part of one row");
@@ -180,36 +199,52 @@ __global__ void __launch_bounds__(32 * kPagedWriteMaxWarps) paged_write_kernel(c
     const bool work = pi <= last;                      // the same in every thread
     const int row0 = pi * ps - start;                  // new row held by the page's row 0 (negative: kept rows)
     const int kept = max(-row0, 0), end = min(ps, n - row0);  // new rows: page rows kept .. end - 1
-    // The lane's part of a row of head group `it`: K's, then V's.
-    auto load = [&](int it, bool is_v) {
-      const int g = (blockIdx.z * a.head_loop + it) * hp + team;
-      Chunk<T>* c = is_v ? vc : kc;
-      float& f = is_v ? vf : kf;
-      f = 1.f;
-      c[0].clear();
-      c[1].clear();
-      if (it < a.head_loop && g < C.Hkv && r >= kept && r < end) {
-        const int i = row0 + r;
-        if constexpr (kCommit) {
-          const int src = spath[i];
-          const int64_t sp = src / ps;
-          const uint8_t* row = static_cast<const uint8_t*>(is_v ? C.v_d : C.k_d) + sp * C.stride_page +
-                               (int64_t)(src - (int)sp * ps) * C.stride_row + (int64_t)g * C.stride_head;
-          c[0].load(row + (is_v ? v0 : k0));
-          c[1].load(row + (is_v ? v1 : k1));
-          f = (is_v ? C.v_scale_d : C.k_scale_d)[sp * C.Hkv + g];
-        } else {
-          const T* row = is_v ? static_cast<const T*>(a.v) + (int64_t)(off + i) * a.vs_n + (int64_t)g * a.vs_h
-                              : static_cast<const T*>(a.k) + (int64_t)(off + i) * a.ks_n + (int64_t)g * a.ks_h;
-          c[0].load(row + (is_v ? v0 : k0));
-          c[1].load(row + (is_v ? v1 : k1));
-        }
+    const bool row_on = work && r >= kept && r < end;  // the lane's row is a new one
+    const int g0 = blockIdx.z * a.head_loop * hp, gn = min(C.Hkv, g0 + a.head_loop * hp);
+    // The lane's part of the row at head g0 + team, then hp heads on at each load.
+    const S *ks = nullptr, *vs = nullptr;
+    int64_t sp = 0;  // page of the source (commit)
+    int gk = g0 + team, gv = gk;
+    auto source = [&]() {
+      if constexpr (kCommit) {
+        const int src = row_on ? spath[row0 + r] : 0;
+        sp = src / ps;
+        const int64_t at = sp * C.stride_page + (int64_t)(src - (int)sp * ps) * C.stride_row + (int64_t)gk * C.stride_head;
+        ks = static_cast<const uint8_t*>(C.k_d) + at + k0;
+        vs = static_cast<const uint8_t*>(C.v_d) + at + v0;
+      } else {
+        ks = static_cast<const T*>(a.k) + (int64_t)(off + row0 + r) * a.ks_n + (int64_t)gk * a.ks_h + k0;
+        vs = static_cast<const T*>(a.v) + (int64_t)(off + row0 + r) * a.vs_n + (int64_t)gv * a.vs_h + v0;
       }
     };
+    auto load_k = [&]() {
+      if (row_on && gk < gn) {
+        kc[0].load(ks);
+        kc[1].load(ks + (k1 - k0));
+        if (kCommit) kf = C.k_scale_d[sp * C.Hkv + gk];
+      }
+      gk += hp;
+      ks += hp * (kCommit ? C.stride_head : a.ks_h);
+    };
+    auto load_v = [&]() {
+      if (row_on && gv < gn) {
+        vc[0].load(vs);
+        vc[1].load(vs + 8);
+        if (kCommit) vf = C.v_scale_d[sp * C.Hkv + gv];
+      }
+      gv += hp;
+      vs += hp * (kCommit ? C.stride_head : a.vs_h);
+    };
+    kf = vf = 1.f;
+    kc[0].clear();
+    kc[1].clear();
+    vc[0].clear();
+    vc[1].clear();
     if (round > 0) __syncthreads();  // the previous page's angles have been read
-    if (!kCommit && work) {  // (a commit's rows come from pages that are checked first)
-      load(0, false);
-      load(0, true);
+    if (!kCommit) {  // (a commit's rows come from pages that are checked first)
+      source();
+      load_k();
+      load_v();
     }
     if (work && turn) {
       const int per = threads / half, f = tid % half;
@@ -236,18 +271,18 @@ __global__ void __launch_bounds__(32 * kPagedWriteMaxWarps) paged_write_kernel(c
     }
     if (!work) return;
     if (kCommit) {
-      load(0, false);
-      load(0, true);
+      source();
+      load_k();
+      load_v();
     }
     const int64_t page = ids[pi];
+    const int64_t to = page * C.stride_page + (int64_t)r * C.stride_row + (int64_t)(g0 + team) * C.stride_head;
+    uint8_t* kr = static_cast<uint8_t*>(C.k_d) + to;
+    uint8_t* vr = static_cast<uint8_t*>(C.v_d) + to;
 
-    for (int it = 0; it < a.head_loop; ++it) {
-      const int g0 = (blockIdx.z * a.head_loop + it) * hp;
-      if (g0 >= C.Hkv) break;  // the same in every thread
-      const int g = g0 + team;
-      const bool on = g < C.Hkv;
-      uint8_t* kp = static_cast<uint8_t*>(C.k_d) + page * C.stride_page + (int64_t)g * C.stride_head;
-      uint8_t* vp = static_cast<uint8_t*>(C.v_d) + page * C.stride_page + (int64_t)g * C.stride_head;
+    for (int h0 = g0; h0 < gn; h0 += hp) {  // the same in every thread
+      const int g = h0 + team;
+      const bool on = g < gn;
       float* ksp = C.k_scale_d + page * C.Hkv + g;
       float* vsp = C.v_scale_d + page * C.Hkv + g;
       const float k_old = on && kept > 0 ? *ksp : 0.f, v_old = on && kept > 0 ? *vsp : 0.f;
@@ -256,8 +291,8 @@ __global__ void __launch_bounds__(32 * kPagedWriteMaxWarps) paged_write_kernel(c
       float km = 0.f, vm = 0.f;
       kc[0].get(kx, kf);
       kc[1].get(kx + 8, kf);
-      load(it + 1, false);  // the next head's K goes while this one is turned and rounded
-      if (turn && on && r >= kept && r < end) {
+      load_k();  // the next head's K goes while this one is turned and rounded
+      if (turn && on && row_on) {
         const float* c = ct + r * width;
         const float* s = st + r * width;
         if (pairs || a.interleaved) {
@@ -280,13 +315,13 @@ __global__ void __launch_bounds__(32 * kPagedWriteMaxWarps) paged_write_kernel(c
           }
         } else if constexpr (!kCommit) {
           // Half layout that cuts a chunk: the partner is read again.
-          const T* ks = static_cast<const T*>(a.k) + (int64_t)(off + row0 + r) * a.ks_n + (int64_t)g * a.ks_h;
+          const T* row = static_cast<const T*>(a.k) + (int64_t)(off + row0 + r) * a.ks_n + (int64_t)g * a.ks_h;
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
             const int d = k0 + e;
             if (d < a.rot) {
               const bool low = d < half;
-              const float q = scalar_f32<T>(ks[low ? d + half : d - half]);
+              const float q = scalar_f32<T>(row[low ? d + half : d - half]);
               const int f = angle_at(low ? d : d - half);
               float x = kx[e], y = q;
               if (low) {
@@ -300,13 +335,8 @@ __global__ void __launch_bounds__(32 * kPagedWriteMaxWarps) paged_write_kernel(c
           }
         }
       }
-      km = finite_amax(kx);
-      float vx[16];
-      vc[0].get(vx, vf);
-      vc[1].get(vx + 8, vf);
-      vm = finite_amax(vx);
-      km = warp_max(km);
-      vm = warp_max(vm);
+      km = warp_max(finite_amax(kx));
+      vm = warp_max(source_amax(vc, vf));
       // Two sets of maxima in turn: a set is written again behind the next one's barrier.
       float(*most)[kPagedWriteMaxWarps] = amax[parity];
       parity ^= 1;
@@ -316,26 +346,23 @@ __global__ void __launch_bounds__(32 * kPagedWriteMaxWarps) paged_write_kernel(c
       }
       __syncthreads();  // also: every thread has read the old scales
       if (!on) continue;  // (no later group of this team is on either)
-      km = vm = 0.f;
-      for (int w = 0; w < wpp; ++w) {
-        km = fmaxf(km, most[0][team * wpp + w]);
-        vm = fmaxf(vm, most[1][team * wpp + w]);
-      }
+      km = warp_max(lane < wpp ? most[0][team * wpp + lane] : 0.f);
+      vm = warp_max(lane < wpp ? most[1][team * wpp + lane] : 0.f);
       const float k_scale = fmaxf(k_old, pow2_scale(km)), v_scale = fmaxf(v_old, pow2_scale(vm));
-      const float k_inv = 1.f / k_scale, v_inv = 1.f / v_scale;
+      // (A kept scale is the caller's, the others are powers of two.)
+      const float k_inv = kept > 0 ? 1.f / k_scale : pow2_inverse(k_scale);
+      const float v_inv = kept > 0 ? 1.f / v_scale : pow2_inverse(v_scale);
       if (slice == 0 && lane == 0) {
         *ksp = k_scale;
         *vsp = v_scale;
       }
       const float k_again = k_old * k_inv, v_again = v_old * v_inv;
-      uint8_t* kr = kp + (int64_t)r * C.stride_row;
-      uint8_t* vr = vp + (int64_t)r * C.stride_row;
-      if (r >= kept && r < end) {
+      if (row_on) {
         float vx[16];
         vc[0].get(vx, vf);
         vc[1].get(vx + 8, vf);
         const uint2 va = pack8(vx, v_inv), vb = pack8(vx + 8, v_inv);
-        load(it + 1, true);
+        load_v();
         *reinterpret_cast<uint2*>(kr + k0) = pack8(kx, k_inv);
         *reinterpret_cast<uint2*>(kr + k1) = pack8(kx + 8, k_inv);
         *reinterpret_cast<uint4*>(vr + v0) = make_uint4(va.x, va.y, vb.x, vb.y);
@@ -356,6 +383,8 @@ __global__ void __launch_bounds__(32 * kPagedWriteMaxWarps) paged_write_kernel(c
           *at = make_uint4(lo.x, lo.y, hi.x, hi.y);
         }
       }
+      kr += hp * C.stride_head;
+      vr += hp * C.stride_head;
     }
   }
 }

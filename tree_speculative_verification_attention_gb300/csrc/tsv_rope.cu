@@ -6,11 +6,16 @@
 // the rest is copied.  Every value is read and written once, so the bound is
 // HBM: a CTA takes a few rows, issues the loads of its first vectors, computes
 // the rows' rot/2 cosines and sines into shared memory meanwhile (they are the
-// same for every head) and then streams the heads in vectors of up to 16 bytes,
-// four of them in flight per thread.  A vector of the half layout goes with
-// its partner rot/2 elements on, both in one thread's registers; where rot/2 is
-// no multiple of 16 bytes the vectors shrink to what divides it.
+// same for every head) and then streams the heads in vectors of up to 16 bytes.
+// A thread keeps its place in the row (head and element, worked out once) and
+// goes down the rows, four vectors in flight: what is left per vector is its
+// load, its arithmetic and its store, so that issue stays below the copy's
+// time.  A vector of the half layout goes with its partner rot/2 elements on,
+// both in one thread's registers; where rot/2 is no multiple of 16 bytes the
+// vectors shrink to what divides it.
 #include <cuda_runtime.h>
+
+#include <type_traits>
 
 #include "tsv_paged_common.cuh"
 
@@ -19,7 +24,7 @@ namespace tsv {
 namespace {
 
 constexpr int kRopeThreads = 256;
-constexpr int kRopeTableFloats = 2 * 2048;  // cosines and sines of one CTA's rows
+constexpr int kRopePairs = 2048;  // angles of one CTA's rows
 
 template <typename T>
 __device__ __forceinline__ float to_f32(T v);
@@ -38,10 +43,12 @@ template <typename T, int E>
 struct alignas(sizeof(T) * E) Vec {
   T v[E];
 };
+template <int BYTES>
+using Raw = std::conditional_t<BYTES == 16, uint4,
+                               std::conditional_t<BYTES == 8, uint2, std::conditional_t<BYTES == 4, uint32_t, unsigned short>>>;
 
-// n / d of 0 <= n < 2^31 by a multiplication: q = (umulhi(n, m) + n) >> s with
-// s = ceil(log2 d), m = floor(2^32 (2^s - d) / d) + 1 (a division each for row,
-// head and vector would cost as much issue time as the vector's own work).
+// n / d of 0 <= n < 2^31 by a multiplication: (umulhi(n, m) + n) >> s with
+// s = ceil(log2 d), m = floor(2^32 (2^s - d) / d) + 1.
 struct FastDiv {
   uint32_t d, m;
   int s;
@@ -52,106 +59,140 @@ struct FastDiv {
   __device__ __forceinline__ int div(int n) const { return (int)((__umulhi((uint32_t)n, m) + (uint32_t)n) >> s); }
 };
 
+// Each value is read once and written once: streaming accesses leave the L2 to
+// others, and keep the written lines from waiting there (16384 rows x 64 heads x
+// 128: 82 us with them, 108 us without; a copy of the same bytes takes 82).
+template <typename T, int E>
+__device__ __forceinline__ Vec<T, E> load_vec(const T* p) {
+  union {
+    Raw<sizeof(T) * E> raw;
+    Vec<T, E> v;
+  } w;
+  w.raw = __ldcs(reinterpret_cast<const Raw<sizeof(T) * E>*>(p));
+  return w.v;
+}
+template <typename T, int E>
+__device__ __forceinline__ void store_vec(T* p, const Vec<T, E>& v) {
+  __stcs(reinterpret_cast<Raw<sizeof(T) * E>*>(p), *reinterpret_cast<const Raw<sizeof(T) * E>*>(&v));
+}
+
 constexpr int kVectors = 4;  // vectors of a thread in flight
 
-// E elements per access.  Items of one head: rotated ones, then copied ones.  A
-// rotated item is a vector of pairs, or (half layout, and single elements) a
-// vector and its partner.
+// E elements per access.  Items of one row: per head, rotated ones, then copied
+// ones.  A rotated item is a vector of pairs, or (half layout, and single
+// elements) a vector and its partner.
 template <typename T, int E, bool INTERLEAVED>
-__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs a, int rows_per_cta, const FastDiv by_row,
-                                                            const FastDiv by_head) {
+__global__ void __launch_bounds__(kRopeThreads, 5) rope_kernel(const RopeArgs a, int rows_per_cta, const FastDiv by_row,
+                                                            const FastDiv by_items, const FastDiv by_half) {
   pdl_trigger();
   pdl_wait();
-  __shared__ float table[kRopeTableFloats];
   constexpr bool SPLIT = !INTERLEAVED || E == 1;
-  constexpr int PARTS = SPLIT ? 2 : 1, kBatch = kVectors / PARTS;
+  constexpr int PARTS = SPLIT ? 2 : 1, BATCH = kVectors / PARTS;
   constexpr int STEP = INTERLEAVED && SPLIT ? 2 : E;  // from one rotated item to the next
-  const int half = a.rot >> 1;
+  constexpr int PAIRS = SPLIT ? E : E / 2;            // of an item (even, or one)
+  __shared__ alignas(16) float2 table[kRopePairs];    // (cosine, sine) [rows][width]
+  const int half = a.rot >> 1, width = (half + 1) & ~1;
   const int n0 = blockIdx.x * rows_per_cta;
   const int rows = min(rows_per_cta, a.N - n0);
-  float* tc = table;
-  float* ts = table + rows_per_cta * half;
   const int partner = INTERLEAVED ? 1 : half;
-  const int turn_items = (SPLIT ? half : a.rot) / E;
-  const T* x = static_cast<const T*>(a.x) + (int64_t)n0 * a.xs_n;
-  T* y = static_cast<T*>(a.y) + (int64_t)n0 * a.ys_n;
-  const int total = rows * (int)by_row.d;
-  Vec<T, E> v[kBatch][PARTS];
-  struct Item {
-    int r, h, it, d;  // row, head, item, first element
+  const int turn_items = half / PAIRS, items = (int)by_items.d, per_row = (int)by_row.d;
+  // The thread's items of a row (one, or every blockDim.x-th), and its rows.
+  const int tid = threadIdx.x, threads = blockDim.x;
+  const int r0 = by_row.div(tid), at_once = max(1, by_row.div(threads));
+  const int i0 = at_once > 1 ? tid - r0 * per_row : tid;
+  const int first_row = at_once > 1 ? (r0 < at_once ? r0 : rows) : 0;
+
+  Vec<T, E> v[BATCH][PARTS];
+  const T* x;
+  T* y;
+  bool turn;
+  int pair;
+  auto place = [&](int i) {
+    const int h = by_items.div(i), it = i - h * items;
+    turn = it < turn_items;
+    pair = it * PAIRS;
+    const int d = turn ? it * STEP : a.rot + (it - turn_items) * E;
+    x = static_cast<const T*>(a.x) + (int64_t)n0 * a.xs_n + (int64_t)h * a.xs_h + d;
+    y = static_cast<T*>(a.y) + (int64_t)n0 * a.ys_n + (int64_t)h * a.ys_h + d;
   };
-  auto item = [&](int i) {
-    Item k;
-    k.r = by_row.div(i);
-    const int in_row = i - k.r * (int)by_row.d;
-    k.h = by_head.div(in_row);
-    k.it = in_row - k.h * (int)by_head.d;
-    k.d = k.it < turn_items ? k.it * STEP : a.rot + (k.it - turn_items) * E;
-    return k;
-  };
-  auto load = [&](int i0) {
+  auto load = [&](int row) {
 #pragma unroll
-    for (int u = 0; u < kBatch; ++u) {
-      const int i = i0 + u * kRopeThreads;
-      if (i >= total) break;
-      const Item k = item(i);
-      const T* xr = x + k.r * a.xs_n + k.h * a.xs_h + k.d;
-      v[u][0] = *reinterpret_cast<const Vec<T, E>*>(xr);
-      if (SPLIT && k.it < turn_items) v[u][PARTS - 1] = *reinterpret_cast<const Vec<T, E>*>(xr + partner);
+    for (int u = 0; u < BATCH; ++u) {
+      const int r = row + u * at_once;
+      if (r >= rows) break;
+      const T* xr = x + r * a.xs_n;
+      v[u][0] = load_vec<T, E>(xr);
+      if (SPLIT && turn) v[u][PARTS - 1] = load_vec<T, E>(xr + partner);
     }
   };
-  load(threadIdx.x);
-  for (int i = threadIdx.x; i < rows * half; i += kRopeThreads) {
-    const int r = i / half, f = i - r * half;
+  if (i0 < per_row) {
+    place(i0);
+    load(first_row);
+  }
+  for (int i = tid; i < rows * half; i += threads) {
+    const int r = by_half.div(i), f = i - r * half;
     float c, s;
     rope_cos_sin(a.positions[n0 + r], rope_turns(a.inv_freq[f]), &c, &s);
-    tc[i] = c * a.amplitude;
-    ts[i] = (a.inverse ? -s : s) * a.amplitude;
+    table[r * width + f] = make_float2(c * a.amplitude, (a.inverse ? -s : s) * a.amplitude);
   }
   __syncthreads();
-  for (int i0 = threadIdx.x; i0 < total; i0 += kBatch * kRopeThreads) {
-    if (i0 != (int)threadIdx.x) load(i0);
+  for (int i = i0; i < per_row; i += threads) {
+    if (i != i0) {
+      place(i);
+      load(first_row);
+    }
+    for (int row = first_row; row < rows; row += BATCH * at_once) {
+      if (row != first_row) load(row);
 #pragma unroll
-    for (int u = 0; u < kBatch; ++u) {
-      const int i = i0 + u * kRopeThreads;
-      if (i >= total) break;
-      const Item k = item(i);
-      T* yr = y + k.r * a.ys_n + k.h * a.ys_h + k.d;
-      if (k.it < turn_items) {
-        const float* c = tc + k.r * half;
-        const float* s = ts + k.r * half;
-        if constexpr (!SPLIT) {
+      for (int u = 0; u < BATCH; ++u) {
+        const int r = row + u * at_once;
+        if (r >= rows) break;
+        T* yr = y + r * a.ys_n;
+        if (turn) {
+          float cs[2 * PAIRS];
+          const float2* t = table + r * width + pair;
+          if constexpr (PAIRS == 1) {
+            *reinterpret_cast<float2*>(cs) = *t;
+          } else {
 #pragma unroll
-          for (int e = 0; e < E; e += 2) {
-            float p = to_f32(v[u][0].v[e]), q = to_f32(v[u][0].v[e + 1]);
-            rope_pair(p, q, c[(k.d + e) >> 1], s[(k.d + e) >> 1]);
-            v[u][0].v[e] = from_f32<T>(p);
-            v[u][0].v[e + 1] = from_f32<T>(q);
+            for (int e = 0; e < PAIRS; e += 2)
+              *reinterpret_cast<float4*>(cs + 2 * e) = *reinterpret_cast<const float4*>(t + e);
           }
-        } else {
 #pragma unroll
-          for (int e = 0; e < E; ++e) {
-            float p = to_f32(v[u][0].v[e]), q = to_f32(v[u][1].v[e]);
-            const int f = INTERLEAVED ? k.it : k.d + e;
-            rope_pair(p, q, c[f], s[f]);
-            v[u][0].v[e] = from_f32<T>(p);
-            v[u][1].v[e] = from_f32<T>(q);
+          for (int e = 0; e < PAIRS; ++e) {
+            T& first = SPLIT ? v[u][0].v[e] : v[u][0].v[2 * e];
+            T& second = SPLIT ? v[u][PARTS - 1].v[e] : v[u][0].v[(2 * e + 1) % E];
+            float p = to_f32(first), q = to_f32(second);
+            rope_pair(p, q, cs[2 * e], cs[2 * e + 1]);
+            first = from_f32<T>(p);
+            second = from_f32<T>(q);
           }
-          *reinterpret_cast<Vec<T, E>*>(yr + partner) = v[u][1];
+          if constexpr (SPLIT) store_vec<T, E>(yr + partner, v[u][1]);
         }
+        store_vec<T, E>(yr, v[u][0]);
       }
-      *reinterpret_cast<Vec<T, E>*>(yr) = v[u][0];
     }
   }
 }
 
 template <typename T, int E>
-cudaError_t launch_rope_vec(const RopeArgs& a, int rows, cudaStream_t st) {
-  const int items = (a.interleaved && E > 1 ? a.rot / E : a.rot / 2 / E) + (a.D - a.rot) / E;
-  const FastDiv by_head((uint32_t)items), by_row((uint32_t)items * (uint32_t)a.H);
-  const dim3 grid((a.N + rows - 1) / rows), block(kRopeThreads);
-  if (a.interleaved) return launch_pdl(rope_kernel<T, E, true>, grid, block, 0, st, 0u, a, rows, by_row, by_head);
-  return launch_pdl(rope_kernel<T, E, false>, grid, block, 0, st, 0u, a, rows, by_row, by_head);
+cudaError_t launch_rope_vec(const RopeArgs& a, int num_sms, cudaStream_t st) {
+  const int half = a.rot / 2, parts = a.interleaved && E > 1 ? 1 : 2;
+  const int items = a.rot / (E * parts) + (a.D - a.rot) / E, per_row = items * a.H;
+  // Threads: of 256 at most, those that whole rows or equal shares of one use.
+  const int share = per_row > kRopeThreads ? (per_row + kRopeThreads - 1) / kRopeThreads : 1;
+  const int used = share > 1 ? (per_row + share - 1) / share : kRopeThreads / per_row * per_row;
+  const int threads = (used + 31) / 32 * 32;
+  // Rows per CTA: as many as leave one wave of 40 warps per SM (48 registers a
+  // thread), up to 8: beyond it more CTAs are better than longer ones (16384
+  // rows x 64 heads x 128: 82 us at 8 rows, 90 in one wave of 22, 113 at 1).
+  // The table holds their angles.
+  const int64_t resident = (int64_t)num_sms * (40 * 32 / threads);
+  const int rows = (int)min(min((a.N + resident - 1) / resident, (int64_t)8), (int64_t)(kRopePairs / ((half + 1) & ~1)));
+  const dim3 grid((a.N + rows - 1) / rows), block(threads);
+  const FastDiv by_row((uint32_t)per_row), by_items((uint32_t)items), by_half((uint32_t)half);
+  if (a.interleaved) return launch_pdl(rope_kernel<T, E, true>, grid, block, 0, st, 0u, a, rows, by_row, by_items, by_half);
+  return launch_pdl(rope_kernel<T, E, false>, grid, block, 0, st, 0u, a, rows, by_row, by_items, by_half);
 }
 
 template <typename T>
@@ -162,20 +203,11 @@ cudaError_t launch_typed(const RopeArgs& a, int num_sms, cudaStream_t st) {
   const int64_t whole = (int64_t)bits | a.xs_n | a.xs_h | a.ys_n | a.ys_h | a.D | (a.interleaved ? a.rot : a.rot / 2);
   int E = 16 / (int)sizeof(T);
   while (E > 1 && whole % E) E >>= 1;
-  const int half = a.rot / 2;
-  // Rows per CTA: enough for kVectors a thread, as far as the table holds
-  // their angles and every SM keeps a CTA.
-  const int64_t row_items = (int64_t)a.H * a.D / E;
-  int rows = (int)((kVectors * kRopeThreads + row_items - 1) / row_items);
-  // A few more where the angles would leave threads idle, as long as 8 CTAs per SM remain.
-  rows = max(rows, min((kRopeThreads + half - 1) / half, a.N / (8 * num_sms)));
-  rows = min(rows, (kRopeTableFloats / 2) / half);
-  rows = max(1, min(rows, a.N / num_sms));
   if constexpr (sizeof(T) == 2)
-    if (E == 8) return launch_rope_vec<T, 8>(a, rows, st);
-  if (E == 4) return launch_rope_vec<T, 4>(a, rows, st);
-  if (E == 2) return launch_rope_vec<T, 2>(a, rows, st);
-  return launch_rope_vec<T, 1>(a, rows, st);
+    if (E == 8) return launch_rope_vec<T, 8>(a, num_sms, st);
+  if (E == 4) return launch_rope_vec<T, 4>(a, num_sms, st);
+  if (E == 2) return launch_rope_vec<T, 2>(a, num_sms, st);
+  return launch_rope_vec<T, 1>(a, num_sms, st);
 }
 
 }  // namespace
