@@ -156,6 +156,8 @@ __global__ void __launch_bounds__(32 * kPagedWriteMaxWarps) paged_write_kernel(c
   const int first = bad ? 0 : start / ps;
   const int last = bad || n == 0 ? first - 1 : (start + n - 1) / ps;
   const int32_t* ids = a.table.ids_d + (int64_t)b * a.table.stride;
+  const bool reports = blockIdx.x == 0 && blockIdx.z == 0;
+  if (!reports && (int)blockIdx.x > last - first) return;  // no page (or a bad request)
   if (!bad) {
     for (int i = first + tid; i <= last; i += threads) {
       const int id = ids[i];
@@ -261,7 +263,7 @@ __global__ void __launch_bounds__(32 * kPagedWriteMaxWarps) paged_write_kernel(c
     }
     if (round == 0) {
       bad = __syncthreads_or(bad);
-      if (blockIdx.x == 0 && blockIdx.z == 0 && tid == 0) {
+      if (reports && tid == 0) {
         a.status[b] = bad ? TSV_ERR_INVALID_ARG : TSV_OK;
         if (kCommit && a.new_len) a.new_len[b] = bad ? -1 : start + n;
       }
