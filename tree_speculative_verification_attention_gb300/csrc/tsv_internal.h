@@ -300,7 +300,8 @@ struct PagedAttnArgs {
 // Tensor-core kernel: row tiles of R = 16, 32 or 64 query rows; its workspace
 // holds one completion counter per CTA, then two partial results per CTA (O
 // [R][D], then maxima and sums [2][R]).
-inline int32_t paged_attn_rows(int64_t rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
+constexpr int32_t kPagedWideRows = 256;
+inline int32_t paged_attn_rows(int64_t rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : kPagedWideRows; }
 struct PagedAttnLayout {
   size_t part_o, part_ml, total;
 };
@@ -314,6 +315,8 @@ inline PagedAttnLayout paged_attn_layout(int grid, int32_t R, int32_t D) {
 cudaError_t paged_attention_set_attributes(int32_t D, int32_t R);
 cudaError_t launch_paged_attention(const CUtensorMap& tk, const CUtensorMap& tv, const PagedAttnArgs& a, int32_t R, int grid,
                                    void* ws, cudaStream_t st);
+cudaError_t paged_attention_wide_set_attributes(int32_t D);
+cudaError_t launch_paged_attention_wide(const PagedAttnArgs& a, int grid, void* ws, cudaStream_t st);
 cudaError_t launch_paged_attention_simt(const PagedAttnArgs& a, bool bf16, cudaStream_t st);
 
 }  // namespace tsv

@@ -282,15 +282,18 @@ tsv_status tsv_paged_tree_attention(tsv_handle h, tsv_dtype dtype, const void* q
   a.G = Hq / a.cache.Hkv;
   a.scale = scale == 0.f ? 1.f / sqrtf((float)a.cache.D) : scale;
   if (use_tc) {
+    const bool wide = R == kPagedWideRows;
+    const uint32_t bit = 1u << ((wide ? 3 : R == 16 ? 0 : R == 32 ? 1 : 2) + (a.cache.D == 128 ? 4 : 0));
+    if (!(h->paged_attr_mask & bit)) {
+      if ((wide ? paged_attention_wide_set_attributes(a.cache.D) : paged_attention_set_attributes(a.cache.D, R)) != cudaSuccess)
+        return TSV_ERR_CUDA;
+      h->paged_attr_mask |= bit;
+    }
+    if (wide) return cuda_status(launch_paged_attention_wide(a, h->num_sms, workspace_d, static_cast<cudaStream_t>(stream)));
     CUtensorMap tk, tv;
     st = encode_pages(h, &tk, a.cache.k_d, a.cache);
     if (st == TSV_OK) st = encode_pages(h, &tv, a.cache.v_d, a.cache);
     if (st != TSV_OK) return st;
-    const uint32_t bit = 1u << ((R == 16 ? 0 : R == 32 ? 1 : 2) + (a.cache.D == 128 ? 3 : 0));
-    if (!(h->paged_attr_mask & bit)) {
-      if (paged_attention_set_attributes(a.cache.D, R) != cudaSuccess) return TSV_ERR_CUDA;
-      h->paged_attr_mask |= bit;
-    }
     return cuda_status(launch_paged_attention(tk, tv, a, R, h->num_sms, workspace_d, static_cast<cudaStream_t>(stream)));
   }
   return cuda_status(launch_paged_attention_simt(a, dtype == TSV_BF16, static_cast<cudaStream_t>(stream)));

@@ -1,0 +1,747 @@
+// tsv_paged_attention_wide.cu — tree attention over a paged 8-bit cache for many
+// query rows per KV head, query rows on the TMEM lanes.
+//
+//   S = Q K^T         M = 128 rows, N = 128 keys, K = D       (A = Q, B = K, shared memory)
+//   O += P V          M = 128 rows, N = D, K = 128 keys       (A = P, TMEM; B = V, shared memory)
+//
+// Both products are fp16 with fp32 sums.  An e4m3 code is an fp16 value, so K
+// and V are widened without a rounding (one conversion per two codes); a row of
+// Q is a bf16 row times a power of two that moves its largest value to
+// [2^14, 2^15): exact down to 2^-31 of it.  P is 2^7 p with p <= 2^8, rounded to
+// fp16's 11 bits.  The scale of a key's page multiplies S in fp32; the scale of
+// its V page, relative to the largest one so far, multiplies P.
+//
+// Why another kernel: with rows on N (the kernel for few rows) a block of 128
+// keys costs the MMA's issue time whatever N is, and two e4m3 terms of Q and of
+// P.  From some 33 rows on that is more than what the widening costs, which
+// here is paid once for 256 rows: 128 rows x 64 heads, 32768 keys: see the
+// figures at the launch.
+//
+// One CTA per SM walks its share of the list of blocks (as the other kernel
+// does; a unit is up to 256 rows, two tiles).  Roles (20 warps):
+//   0-7    softmax: warps 0-3 tile 0, 4-7 tile 1; a thread owns a row.  The
+//          reference maximum moves only when a score passes it by 2^8, and with
+//          it the row of O in TMEM.
+//   8-15   widening: K and V codes go from global memory into registers a block
+//          ahead (a page row is 128 or 64 contiguous bytes, whatever the
+//          strides around it), and from there as fp16 into the swizzled tiles:
+//          TMA would bring them no closer than a second pass through shared
+//          memory, which Q (64 KB) and the two fp16 rings (128 KB) leave no
+//          room for.
+//   16     MMA issuer: PV_0(j), S_0(j+1), PV_1(j), S_1(j+1): one tile's softmax
+//          runs under the other's products.
+// Bound: the tensor cores (four 128^3 products a block of 256 rows) and, close
+// behind, the exponentials.
+//
+// Masks: the keys of tree blocks by the ancestor words of the row's node, keys
+// past the end by their number.  V rows past the last key are zeros, and NaN
+// codes of tree rows are kept out of the product and put back only into the
+// rows that see them.
+#include <type_traits>
+
+#include "tsv_paged_tc.cuh"
+
+namespace tsv {
+
+namespace {
+
+constexpr int kWThreads = 640;
+constexpr int kWConvWarp = 8, kWMmaWarp = 16;
+// Registers a thread: 640 x 96 at launch = 256 x 144 + 256 x 72 + 128 x 48.
+constexpr int kWRegs = 96, kWSoftRegs = 144, kWConvRegs = 72, kWRestRegs = 48;
+static_assert(256 * kWSoftRegs + 256 * kWConvRegs + 128 * kWRestRegs <= kWThreads * kWRegs, "register split");
+constexpr int kWRows = kPagedWideRows, kWTile = 128;
+constexpr float kWThreshold = 8.f;  // log2: how far a score may pass the reference maximum
+constexpr int kBarWSoft = 1;
+
+template <int D>
+struct WCfg {
+  static constexpr int kTileBytes = kPBlock * D * 2;  // fp16 K or V block, or a Q tile
+  static constexpr int kStages = 2;
+  static constexpr int kOffQ = 0;                                    // [2 tiles]
+  static constexpr int kOffK = kOffQ + 2 * kTileBytes;
+  static constexpr int kOffV = kOffK + kStages * kTileBytes;
+  static constexpr int kOffAnc = kOffV + kStages * kTileBytes;       // u32 [256 rows][9]: ancestors (odd stride: no bank conflicts)
+  static constexpr int kOffCum = kOffAnc + kWRows * 9 * 4;           // i64 [TSV_MAX_BATCH + 2]
+  static constexpr int kOffReq = kOffCum + 8 * (TSV_MAX_BATCH + 2);  // int4 [TSV_MAX_BATCH]
+  static constexpr int kOffFr = kOffReq + 16 * TSV_MAX_BATCH;        // f32 [256]: score factor of a row
+  static constexpr int kOffRow = kOffFr + 4 * kWRows;                // i32 [256]: output row
+  static constexpr int kOffScale = kOffRow + 4 * kWRows;             // f32 [4][16]: K's factors of 8 x 16 keys, V's
+  static constexpr int kOffNan = kOffScale + 4 * 64;                 // u32 [8]: tree keys whose V row holds a NaN
+  static constexpr int kOffUnit = kOffNan + 32;                      // PUnit
+  static constexpr int kOffFirst = kOffUnit + 64;                    // PUnit, then i64 [4]
+  static constexpr int kOffBar = kOffFirst + 96;
+  // k_full[2], k_empty[2], v_full[2], v_empty[2], sc_full[4], s_full[2], p_full[2], pv_done[2], mma_done
+  static constexpr int kBars = 19;
+  static constexpr int kOffMisc = kOffBar + 8 * kBars + 8;
+  static constexpr int kSmem = kOffMisc + 32 + 1024;
+  static constexpr uint32_t kColO = 2 * kPBlock;  // S0 | S1 | O0 | O1
+  static_assert(kSmem <= 227 * 1024, "shared memory");
+  static_assert(kOffAnc % 1024 == 0 && kOffCum % 16 == 0 && kOffScale % 16 == 0 && kOffUnit % 16 == 0 && kOffBar % 8 == 0, "alignment");
+};
+
+// fp16 A and B, fp32 D; A K-major, B K-major (0) or N-major (1).
+__host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, int b_mn) {
+  return (1u << 4) | ((uint32_t)b_mn << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+// Issued by the whole warp, so that the operands stay uniform: the one lane
+// with `lead` set issues the MMA.  A from shared memory, then A from TMEM.
+__device__ __forceinline__ void umma_f16(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accumulate,
+                                         uint32_t lead) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(lead)
+      : "memory");
+}
+__device__ __forceinline__ void umma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc, uint32_t accumulate,
+                                            uint32_t lead) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(lead)
+      : "memory");
+}
+
+// 16 bytes at p, or zeros: no branch, so that several are in flight.
+__device__ __forceinline__ uint4 load_if(const uint8_t* p, bool on) {
+  uint4 v = make_uint4(0u, 0u, 0u, 0u);
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];\n\t}\n"
+      : "+r"(v.x), "+r"(v.y), "+r"(v.z), "+r"(v.w)
+      : "l"(p), "r"((uint32_t)on));
+  return v;
+}
+
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// 16 codes as 16 fp16 values.
+__device__ __forceinline__ void widen(const uint4& w, uint4& a, uint4& b) {
+  a = make_uint4(f16x2_of_e4m3x2(w.x & 0xFFFFu), f16x2_of_e4m3x2(w.x >> 16), f16x2_of_e4m3x2(w.y & 0xFFFFu), f16x2_of_e4m3x2(w.y >> 16));
+  b = make_uint4(f16x2_of_e4m3x2(w.z & 0xFFFFu), f16x2_of_e4m3x2(w.z >> 16), f16x2_of_e4m3x2(w.w & 0xFFFFu), f16x2_of_e4m3x2(w.w >> 16));
+}
+// Bytes that are NaN codes, as their top bits.
+__device__ __forceinline__ uint32_t nan_codes(uint32_t w) { return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u; }
+
+// What a role keeps of the unit.
+struct WUnit {
+  int n, P, g, off, row0, j, blocks, nmain, rows, ntiles, ntree;
+  // Block j + i: its first key, how many it has.
+  __device__ __forceinline__ int base(int i) const { return (j + i < nmain ? j + i : j + i - nmain) * kPBlock; }
+  __device__ __forceinline__ int valid(int i) const { return max(0, min(kPBlock, (j + i < nmain ? P : ntree) - base(i))); }
+};
+
+template <int D>
+__global__ void __launch_bounds__(kWThreads, 1)
+    paged_attn_wide_kernel(const __grid_constant__ PagedAttnArgs a, int32_t* __restrict__ counters, float* __restrict__ part_o,
+                           float* __restrict__ part_ml) {
+  using C = WCfg<D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sQ = smem + C::kOffQ;
+  uint8_t* sK = smem + C::kOffK;
+  uint8_t* sV = smem + C::kOffV;
+  uint32_t* sAnc = reinterpret_cast<uint32_t*>(smem + C::kOffAnc);
+  int64_t* sCum = reinterpret_cast<int64_t*>(smem + C::kOffCum);
+  int4* sReq = reinterpret_cast<int4*>(smem + C::kOffReq);
+  float* sFr = reinterpret_cast<float*>(smem + C::kOffFr);
+  int32_t* sRow = reinterpret_cast<int32_t*>(smem + C::kOffRow);
+  float* sScale = reinterpret_cast<float*>(smem + C::kOffScale);
+  uint32_t* sNan = reinterpret_cast<uint32_t*>(smem + C::kOffNan);
+  PUnit* sUnit = reinterpret_cast<PUnit*>(smem + C::kOffUnit);
+  PUnit* sFirst = reinterpret_cast<PUnit*>(smem + C::kOffFirst);
+  int64_t* sRange = reinterpret_cast<int64_t*>(smem + C::kOffFirst + 64);
+  uint64_t* k_full = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
+  uint64_t* k_empty = k_full + 2;
+  uint64_t* v_full = k_empty + 2;
+  uint64_t* v_empty = v_full + 2;
+  uint64_t* sc_full = v_empty + 2;
+  uint64_t* s_full = sc_full + 4;   // [tile]
+  uint64_t* p_full = s_full + 2;    // [tile]
+  uint64_t* pv_done = p_full + 2;   // [tile]
+  uint64_t* mma_done = pv_done + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
+  int* abort_flag = reinterpret_cast<int*>(smem + C::kOffMisc + 4);
+  int* sJoin = reinterpret_cast<int*>(smem + C::kOffMisc + 8);
+  volatile int* abort_v = abort_flag;
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int lps = __ffs(a.cache.page_size) - 1;
+  const bool tree = a.tree_table.ids_d != nullptr;
+  bool dead = false;
+
+  if (tid == 0) {
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&k_full[s], 8);   // the widening warps
+      mbar_init(&k_empty[s], 1);
+      mbar_init(&v_full[s], 8);
+      mbar_init(&v_empty[s], 1);
+      mbar_init(&s_full[s], 1);
+      mbar_init(&p_full[s], 128);
+      mbar_init(&pv_done[s], 1);
+    }
+    for (int s = 0; s < 4; ++s) mbar_init(&sc_full[s], 1);
+    mbar_init(mma_done, 1);
+    *abort_flag = 0;
+    mbar_fence_init();
+  }
+  if (warp == kWMmaWarp) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  pdl_wait();  // the previous kernel's results are visible from here on
+  pdl_trigger();
+  if (warp == 0) plist_setup(a, kWRows, sCum, sReq, sFirst, sRange);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const PList list{sCum, sReq, a.B, a.G, a.cache.Hkv, kWRows, tree, sRange[1]};
+
+  // Every role walks the units together: a barrier before each, one when its
+  // rows are in, and one behind it.
+  if (tid == 0) *sUnit = *sFirst;
+  int t = 0;            // blocks so far
+  int cnt[2] = {0, 0};  // and those of each tile
+  auto begin = [&](WUnit& u) {
+    __syncthreads();
+    if (!sUnit->valid) return false;
+    u.n = sUnit->n;
+    u.P = sUnit->P;
+    u.g = sUnit->g;
+    u.off = sUnit->off;
+    u.row0 = sUnit->tile * kWRows;
+    u.j = sUnit->j;
+    u.blocks = sUnit->j1 - u.j;
+    u.nmain = sUnit->nmain;
+    u.rows = min(kWRows, u.n * a.G - u.row0);
+    u.ntiles = u.rows > kWTile ? 2 : 1;
+    u.ntree = tree ? u.n : 0;
+    return true;
+  };
+  auto end = [&](const WUnit& u) {
+    t += u.blocks;
+    cnt[0] += u.blocks;
+    if (u.ntiles > 1) cnt[1] += u.blocks;
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+  };
+  WUnit u;
+
+  if (warp >= kWConvWarp && warp < kWMmaWarp) {
+    // ---------------------------------------------------------- Q, then K and V, widened
+    setmaxnreg_dec<kWConvRegs>();
+    while (begin(u)) {
+      const int w = warp - kWConvWarp, ct = tid - kWConvWarp * 32;
+      const tsv_paged_cache& c = a.cache;
+      // A lane's part of a block: 16 codes of u.rows row_of, row_of + kStep, ...
+      constexpr int kLanes = D / 16, kStep = 256 / kLanes, kParts = kPBlock / kStep;  // lanes of a row; 4 or 2 rows of a thread
+      const int chunk = ct % kLanes, first_row = ct / kLanes;
+      uint4 kb[kParts], vb[kParts];
+      float sk = 0.f, sv = 0.f;  // warp 0, lanes 0 .. 7: scales of 16 keys each
+      const int64_t head_at = (int64_t)u.g * c.stride_head + 16 * chunk;
+      // Page ids of the lane's rows of block i (-1: none), a block before the
+      // rows are loaded; warp 0's lanes 0 .. 7: those of 16 keys each.
+      int ids[kParts], sid = -1;
+      auto look = [&](int i) {
+        const bool main = u.j + i < u.nmain;
+        const int base = u.base(i), valid = u.valid(i);
+        const tsv_page_table& pt = main ? a.table : a.tree_table;
+        const int32_t* list_b = pt.ids_d + (int64_t)sUnit->b * pt.stride;
+#pragma unroll
+        for (int q = 0; q < kParts; ++q) {
+          const int key = first_row + q * kStep;
+          ids[q] = -1;
+          if (key < valid) ids[q] = __ldg(list_b + ((base + key) >> lps));
+        }
+        sid = -1;
+        if (w == 0 && lane < 8 && lane * 16 < valid) sid = __ldg(list_b + ((base + lane * 16) >> lps));
+      };
+      auto load = [&](int i) {
+        const int base = u.base(i);
+#pragma unroll
+        for (int q = 0; q < kParts; ++q) {
+          const int row = (base + first_row + q * kStep) & ((1 << lps) - 1);
+          const bool on = (uint32_t)ids[q] < (uint32_t)c.num_pages;
+          const int64_t at = (int64_t)ids[q] * c.stride_page + (int64_t)row * c.stride_row + head_at;
+          kb[q] = load_if(static_cast<const uint8_t*>(c.k_d) + at, on);
+          vb[q] = load_if(static_cast<const uint8_t*>(c.v_d) + at, on);
+        }
+        sk = sv = 0.f;
+        if ((uint32_t)sid < (uint32_t)c.num_pages) {
+          sk = __ldg(c.k_scale_d + (int64_t)sid * c.Hkv + u.g);
+          sv = __ldg(c.v_scale_d + (int64_t)sid * c.Hkv + u.g);
+        }
+      };
+      auto put = [&](uint8_t* tile, int key, const uint4& codes) {
+        uint4 x, y;
+        widen(codes, x, y);
+        // Chunks 2 c and 2 c + 1 of 8 values; the upper lanes of a 128-wide row
+        // (the other column group) start with the second, so that 8 lanes meet
+        // 32 banks.
+        const int c0 = (2 * chunk) & 7;
+        uint8_t* row = tile + (chunk >> 2) * (kPBlock * 128) + key * 128;
+        const int s = D == 128 ? chunk >> 2 : 0;
+        *reinterpret_cast<uint4*>(row + (((c0 + s) ^ (key & 7)) << 4)) = s ? y : x;
+        *reinterpret_cast<uint4*>(row + (((c0 + (s ^ 1)) ^ (key & 7)) << 4)) = s ? x : y;
+      };
+      look(0);
+      load(0);
+      if (u.blocks > 1) look(1);
+      {
+        constexpr int E = D / 32;
+#pragma unroll 1
+        for (int r = w * 32; r < w * 32 + 32; ++r) {
+          if (r >= u.ntiles * kWTile) break;
+          const int gr = u.row0 + r, node = gr / a.G, head = u.g * a.G + (gr - node * a.G);
+          uint32_t raw[E / 2];
+#pragma unroll
+          for (int e = 0; e < E / 2; ++e) raw[e] = 0u;
+          if (r < u.rows) {
+            const __nv_bfloat16* src =
+                static_cast<const __nv_bfloat16*>(a.q) + (int64_t)(u.off + node) * a.qs_n + (int64_t)head * a.qs_h + lane * E;
+            if constexpr (E == 4) {
+              const uint2 v = __ldg(reinterpret_cast<const uint2*>(src));
+              raw[0] = v.x;
+              raw[1] = v.y;
+            } else {
+              raw[0] = __ldg(reinterpret_cast<const uint32_t*>(src));
+            }
+          }
+          uint32_t top = 0u;
+#pragma unroll
+          for (int e = 0; e < E / 2; ++e) top = max(top, max((raw[e] << 16) & 0x7FFF0000u, raw[e] & 0x7FFF0000u));
+          top = __reduce_max_sync(0xffffffffu, top);
+          const bool fine = top < 0x7F800000u;  // a row with an infinity or a NaN is NaN throughout (its scores are)
+          const int up = top == 0u ? 0 : max(-120, min(120, 141 - (int)(top >> 23)));
+          const float mul = __uint_as_float((uint32_t)(127 + up) << 23);
+          if (lane == 0) {
+            sFr[r] = __uint_as_float((uint32_t)(127 - up) << 23) * (a.scale * 1.4426950408889634f);
+            sRow[r] = r < u.rows ? (u.off + node) * a.Hq + head : -1;
+          }
+          uint32_t h[E / 2];
+#pragma unroll
+          for (int e = 0; e < E / 2; ++e)
+            h[e] = fine ? pack_f16x2(__uint_as_float(raw[e] << 16) * mul, __uint_as_float(raw[e] & 0xFFFF0000u) * mul) : 0x7FFF7FFFu;
+          const int d = lane * E, rt = r & (kWTile - 1);
+          uint8_t* at = sQ + (r >> 7) * C::kTileBytes + (d >> 6) * (kWTile * 128) + rt * 128 +
+                        ((((d & 63) >> 3) ^ (rt & 7)) << 4) + (d & 7) * 2;
+          if constexpr (E == 4) *reinterpret_cast<uint2*>(at) = make_uint2(h[0], h[1]);
+          else *reinterpret_cast<uint32_t*>(at) = h[0];
+        }
+        if (ct < 8) sNan[ct] = 0u;
+        fence_proxy_async_smem();
+      }
+      __syncthreads();  // the unit's u.rows are in
+#pragma unroll 1
+      for (int i = 0; i < u.blocks; ++i) {
+        const int x = t + i, st = x & 1;
+        if (x >= 2) TSV_PWAIT(&k_empty[st], (x >> 1) - 1);
+        if (__any_sync(0xffffffffu, dead)) break;
+        if (w == 0) {
+          if (lane < 8) {
+            sScale[(x & 3) * 16 + lane] = sk;
+            sScale[(x & 3) * 16 + 8 + lane] = sv;
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sc_full[x & 3]);
+        }
+#pragma unroll
+        for (int q = 0; q < kParts; ++q) put(sK + st * C::kTileBytes, first_row + q * kStep, kb[q]);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&k_full[st]);
+        if (x >= 2) TSV_PWAIT(&v_empty[st], (x >> 1) - 1);
+        if (__any_sync(0xffffffffu, dead)) break;
+        if (u.j + i >= u.nmain) {
+#pragma unroll
+          for (int q = 0; q < kParts; ++q) {
+            uint32_t* v = reinterpret_cast<uint32_t*>(&vb[q]);
+            uint32_t any = 0u;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const uint32_t bad = nan_codes(v[e]);
+              any |= bad;
+              v[e] &= ~((bad >> 7) * 0xFFu);
+            }
+            const int key = u.base(i) + first_row + q * kStep;
+            if (any) atomicOr(&sNan[key >> 5], 1u << (key & 31));
+          }
+        }
+#pragma unroll
+        for (int q = 0; q < kParts; ++q) put(sV + st * C::kTileBytes, first_row + q * kStep, vb[q]);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&v_full[st]);
+        if (i + 1 < u.blocks) load(i + 1);
+        if (i + 2 < u.blocks) look(i + 2);
+      }
+      end(u);
+    }
+  } else if (warp >= kWMmaWarp) {
+    // ---------------------------------------------------------- issuer
+    setmaxnreg_dec<kWRestRegs>();
+    while (begin(u)) {
+      __syncthreads();  // the unit's rows are in
+      if (warp == kWMmaWarp) {
+        constexpr uint32_t idS = idesc_f16_f32(kWTile, kPBlock, 0), idPV = idesc_f16_f32(kWTile, D, 1);
+        const uint64_t dq = sdesc_sw128(smem_u32(sQ), 16, 1024);
+        const uint64_t dk = sdesc_sw128(smem_u32(sK), 16, 1024);
+        const uint64_t dv = sdesc_sw128(smem_u32(sV), kPBlock * 128, 1024);
+        auto issue_s = [&](int tile, int x) {
+          const uint32_t da = (uint32_t)dq + (uint32_t)((tile * C::kTileBytes) >> 4);
+          const uint32_t db = (uint32_t)dk + (uint32_t)(((x & 1) * C::kTileBytes) >> 4);
+          const bool lead = elect_one();
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t o = ((kk >> 2) * (kPBlock * 128) + (kk & 3) * 32) >> 4;
+            umma_f16(tmem + (uint32_t)(tile * kPBlock), desc_at(dq, da + o), desc_at(dk, db + o), idS, kk > 0 ? 1u : 0u, lead);
+          }
+          if (lead) umma_commit(&s_full[tile]);
+          __syncwarp();
+        };
+        auto issue_pv = [&](int tile, int x, bool more) {
+          const uint32_t db = (uint32_t)dv + (uint32_t)(((x & 1) * C::kTileBytes) >> 4);
+          const bool lead = elect_one();
+#pragma unroll
+          for (int kk = 0; kk < kPBlock / 16; ++kk)
+            umma_f16_ts(tmem + C::kColO + tile * D, tmem + (uint32_t)(tile * kPBlock + kPBlock / 2) + kk * 8,
+                        desc_at(dv, db + ((kk * 16 * 128) >> 4)), idPV, more || kk > 0 ? 1u : 0u, lead);
+          if (lead) umma_commit(&pv_done[tile]);
+          __syncwarp();
+        };
+        TSV_PWAIT(&k_full[t & 1], t >> 1);
+        tc_fence_after();
+        if (!__any_sync(0xffffffffu, dead)) {
+          for (int q = 0; q < u.ntiles; ++q) issue_s(q, t);
+          if (elect_one()) umma_commit(&k_empty[t & 1]);
+        }
+        for (int i = 0; i < u.blocks; ++i) {
+          const int x = t + i;
+          const bool more = i + 1 < u.blocks;
+          TSV_PWAIT(&v_full[x & 1], x >> 1);
+          TSV_PWAIT(&p_full[0], cnt[0] + i);
+          if (__any_sync(0xffffffffu, dead)) break;
+          tc_fence_after();
+          issue_pv(0, x, i > 0);
+          if (more) {
+            TSV_PWAIT(&k_full[(x + 1) & 1], (x + 1) >> 1);
+            if (__any_sync(0xffffffffu, dead)) break;
+            tc_fence_after();
+            issue_s(0, x + 1);
+          }
+          if (u.ntiles > 1) {
+            TSV_PWAIT(&p_full[1], cnt[1] + i);
+            if (__any_sync(0xffffffffu, dead)) break;
+            tc_fence_after();
+            issue_pv(1, x, i > 0);
+          }
+          if (elect_one()) umma_commit(&v_empty[x & 1]);
+          if (more) {
+            if (u.ntiles > 1) issue_s(1, x + 1);
+            if (elect_one()) umma_commit(&k_empty[(x + 1) & 1]);
+          }
+          __syncwarp();
+        }
+      }
+      end(u);
+    }
+  } else {
+    // ---------------------------------------------------------- softmax: a thread owns a row
+    setmaxnreg_inc<kWSoftRegs>();
+    for (int k = 0; begin(u); ++k) {
+      const int tile = warp >> 2, r = tid & (kWTile - 1), row = tile * kWTile + r;
+      const bool active = tile < u.ntiles;
+      uint32_t* anc = sAnc + row * 9;
+      if (tree) {  // the row's ancestors
+        const int node = (u.row0 + row) / a.G;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          uint32_t bits = 0u;
+          if (row < u.rows) {
+            const int left = node + 1 - 32 * q;
+            bits = a.anc ? __ldg(a.anc + (int64_t)(u.off + node) * TSV_ANC_WORDS + q)
+                         : left >= 32 ? 0xFFFFFFFFu : left > 0 ? (1u << left) - 1u : 0u;
+          }
+          anc[q] = bits;
+        }
+      }
+      __syncthreads();  // the unit's u.rows are in
+      const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
+      const uint32_t s_col = tmem + lane_base + (uint32_t)(tile * kPBlock);
+      const uint32_t o_col = tmem + lane_base + C::kColO + (uint32_t)(tile * D);
+      const float fr = sFr[row];
+      float m_ref = -INFINITY, l = 0.f, v_ref = 0.f, to_v = 0.f;
+      auto block_step = [&](int i, auto masked_c) {
+        constexpr bool MASKED = decltype(masked_c)::value;
+        const int x = t + i;
+        TSV_PWAIT(&s_full[tile], cnt[tile] + i);
+        TSV_PWAIT(&sc_full[x & 3], x >> 2);
+        if (__any_sync(0xffffffffu, dead)) return;
+        tc_fence_after();
+        const float4* sc = reinterpret_cast<const float4*>(sScale + (x & 3) * 16);
+        uint64_t vis[2] = {~0ull, ~0ull};
+        if (MASKED) {
+          const int valid = u.valid(i);
+          vis[0] = valid >= 64 ? ~0ull : (1ull << valid) - 1ull;
+          vis[1] = valid >= 128 ? ~0ull : valid > 64 ? (1ull << (valid - 64)) - 1ull : 0ull;
+          if (u.j + i >= u.nmain) {
+            const uint32_t* m = anc + 4 * (u.j + i - u.nmain);
+            vis[0] &= (uint64_t)m[0] | ((uint64_t)m[1] << 32);
+            vis[1] &= (uint64_t)m[2] | ((uint64_t)m[3] << 32);
+          }
+        }
+        // The largest score, 32 keys at a time (all 128 would not fit in
+        // registers: they are read again below).
+        float hmax = -INFINITY;
+        uint32_t s[2][32];
+        float f[8];  // the row's factor of 16 keys each
+        {
+          const float4 f0 = sc[0], f1 = sc[1];
+          f[0] = f0.x * fr, f[1] = f0.y * fr, f[2] = f0.z * fr, f[3] = f0.w * fr;
+          f[4] = f1.x * fr, f[5] = f1.y * fr, f[6] = f1.z * fr, f[7] = f1.w * fr;
+        }
+        tmem_ld32_nowait(s_col, s[0]);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t(&z)[32] = s[c & 1];
+          tmem_wait_ld_tie32(z);
+          if (c < 3) tmem_ld32_nowait(s_col + 32 * (c + 1), s[(c + 1) & 1]);
+          else tmem_ld32_nowait(s_col + 96, s[0]);  // the last keys, for the second pass
+          if (MASKED) {
+            const uint32_t see = (uint32_t)(vis[c >> 1] >> (32 * (c & 1)));
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (!((see >> e) & 1u)) z[e] = 0xFF800000u;
+          }
+#pragma unroll
+          for (int q = 0; q < 32; q += 16) {
+            float b0 = fmaxf(__uint_as_float(z[q]), __uint_as_float(z[q + 1]));
+            float b1 = fmaxf(__uint_as_float(z[q + 2]), __uint_as_float(z[q + 3]));
+#pragma unroll
+            for (int e = q + 4; e < q + 16; e += 4) {
+              b0 = fmax3(b0, __uint_as_float(z[e]), __uint_as_float(z[e + 1]));
+              b1 = fmax3(b1, __uint_as_float(z[e + 2]), __uint_as_float(z[e + 3]));
+            }
+            hmax = fmaxf(hmax, fmaxf(b0, b1) * f[2 * c + (q >> 4)]);
+          }
+        }
+        float alpha = 1.f;
+        if (hmax > m_ref + kWThreshold) {
+          alpha = fast_exp2(m_ref - hmax);  // 0 when m_ref = -inf
+          m_ref = hmax;
+        }
+        l *= alpha;
+        const float4 g0 = sc[2], g1 = sc[3];
+        const float v_top = fmaxf(fmaxf(fmaxf(g0.x, g0.y), fmaxf(g0.z, g0.w)), fmaxf(fmaxf(g1.x, g1.y), fmaxf(g1.z, g1.w)));
+        if (v_top > v_ref) {  // the same in every thread
+          alpha *= v_ref / v_top;
+          v_ref = v_top;
+          to_v = 128.f / v_top;
+        }
+        if (i > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+          TSV_PWAIT(&pv_done[tile], cnt[tile] + i - 1);
+          tc_fence_after();
+#pragma unroll 1
+          for (int cc = 0; cc < D; cc += 16) {
+            float o[16];
+            tmem_ld16(o_col + cc, o);
+            uint32_t z16[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) z16[e] = __float_as_uint(o[e] * alpha);
+            tmem_st16u_nowait(o_col + cc, z16);
+          }
+        }
+        const float neg_ref = m_ref == -INFINITY ? 0.f : -m_ref;
+        const uint64_t ref2 = f2_pack(neg_ref, neg_ref);
+        uint64_t sum[2] = {0ull, 0ull};
+        // P from the last keys to the first over the upper half of S, two keys a
+        // column: what a store overwrites has been read.
+        const float fv[8] = {g0.x * to_v, g0.y * to_v, g0.z * to_v, g0.w * to_v, g1.x * to_v, g1.y * to_v, g1.z * to_v, g1.w * to_v};
+#pragma unroll
+        for (int c = 3; c >= 0; --c) {
+          uint32_t(&z)[32] = s[(c + 1) & 1];
+          tmem_wait_ld_tie32(z);
+          if (c > 0) tmem_ld32_nowait(s_col + 32 * (c - 1), s[c & 1]);
+          const uint32_t see = MASKED ? (uint32_t)(vis[c >> 1] >> (32 * (c & 1))) : 0u;
+          uint32_t h[16];
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) {
+            const int q = 2 * c + (e >> 4);
+            const uint64_t x2 = ffma2((uint64_t)z[e] | ((uint64_t)z[e + 1] << 32), f2_pack(f[q], f[q]), ref2);
+            float p0 = fast_exp2(f2_lo(x2)), p1 = fast_exp2(f2_hi(x2));
+            if (MASKED) {
+              if (!((see >> e) & 1u)) p0 = 0.f;
+              if (!((see >> (e + 1)) & 1u)) p1 = 0.f;
+            }
+            const uint64_t p2 = f2_pack(p0, p1);
+            sum[(e >> 1) & 1] = fadd2(sum[(e >> 1) & 1], p2);
+            const uint64_t y2 = fmul2(p2, f2_pack(fv[q], fv[q]));
+            h[e >> 1] = pack_f16x2(f2_lo(y2), f2_hi(y2));
+          }
+          tmem_st16u_nowait(s_col + kPBlock / 2 + 16 * c, h);
+        }
+        tmem_wait_st();
+        const uint64_t both = fadd2(sum[0], sum[1]);
+        l += f2_lo(both) + f2_hi(both);
+        tc_fence_before();
+        parrive(&p_full[tile], dead);
+      };
+      // Blocks of 128 prefix keys need no mask.
+      const int whole_main = max(0, min(u.blocks, u.P / kPBlock - u.j));
+      if (active) {
+#pragma unroll 1
+        for (int i = 0; i < whole_main; ++i) block_step(i, std::false_type{});
+#pragma unroll 1
+        for (int i = whole_main; i < u.blocks; ++i) block_step(i, std::true_type{});
+        TSV_PWAIT(&pv_done[tile], cnt[tile] + u.blocks - 1);
+      }
+      const bool stop = named_bar_or(kBarWSoft, 256, dead);  // the same in every softmax thread
+      if (!stop) {
+        tc_fence_after();
+        // Columns of a row whose NaN codes were kept out of the product.
+        uint32_t bad[D / 32];
+#pragma unroll
+        for (int q = 0; q < D / 32; ++q) bad[q] = 0u;
+        if (tree && active && row < u.rows) {
+#pragma unroll 1
+          for (int q = 0; q < 8; ++q) {
+#pragma unroll 1
+            for (uint32_t seen = sNan[q] & anc[q]; seen; seen &= seen - 1) {
+              const int key = 32 * q + __ffs(seen) - 1;
+              const int id = __ldg(a.tree_table.ids_d + (int64_t)sUnit->b * a.tree_table.stride + (key >> lps));
+              if ((uint32_t)id >= (uint32_t)a.cache.num_pages) continue;
+              const uint32_t* v = reinterpret_cast<const uint32_t*>(
+                  static_cast<const uint8_t*>(a.cache.v_d) + (int64_t)id * a.cache.stride_page +
+                  (int64_t)(key & ((1 << lps) - 1)) * a.cache.stride_row + (int64_t)u.g * a.cache.stride_head);
+#pragma unroll
+              for (int e = 0; e < D / 4; ++e) {
+                const uint32_t m = nan_codes(__ldg(v + e)) >> 7;  // bits 0, 8, 16, 24
+                bad[e >> 3] |= ((m | (m >> 7) | (m >> 14) | (m >> 21)) & 15u) << (4 * (e & 7));
+              }
+            }
+          }
+        }
+        const float unit = v_ref * (1.f / 128.f);
+        const float inv = l == 0.f ? 0.f : unit / l;  // (0 for a row that sees nothing)
+        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out);
+        const bool whole = sUnit->whole();
+        const int slot = 2 * (int)blockIdx.x + (k == 0 ? 0 : 1);
+        if (active) {
+          __nv_bfloat16* to = out + (int64_t)(row < u.rows ? sRow[row] : 0) * D;
+          float* po = part_o + ((int64_t)slot * kWRows + row) * D;
+#pragma unroll
+          for (int cc = 0; cc < D; cc += 32) {
+            float o[32];
+            tmem_ld32(o_col + cc, o);
+            if (row < u.rows) {
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] = l == 0.f ? 0.f : (bad[cc / 32] >> e) & 1u ? NAN : o[e] * inv;
+              if (whole) {
+#pragma unroll
+                for (int e = 0; e < 32; e += 8)
+                  *reinterpret_cast<uint4*>(to + cc + e) = make_uint4(pack_bf16x2(o[e], o[e + 1]), pack_bf16x2(o[e + 2], o[e + 3]),
+                                                                      pack_bf16x2(o[e + 4], o[e + 5]), pack_bf16x2(o[e + 6], o[e + 7]));
+              } else {
+#pragma unroll
+                for (int e = 0; e < 32; e += 4) *reinterpret_cast<float4*>(po + cc + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+              }
+            }
+          }
+          if (!whole && row < u.rows) {  // normalised: its sum is 1
+            float* pm = part_ml + (int64_t)slot * 2 * kWRows;
+            const bool sees = l != 0.f;
+            pm[row] = l > 0.f ? m_ref + log2f(l) : sees ? m_ref : -INFINITY;
+            pm[kWRows + row] = l > 0.f ? 1.f : l;
+          }
+        }
+        if (!whole) {
+          // CTAs cf .. cl share the group; the last to arrive joins.
+          const int64_t W = sRange[2], ctas = sRange[3], gx = sUnit->gx;
+          const int cf = (int)(((gx + 1) * ctas - 1) / W), cl = (int)(((gx + sUnit->T) * ctas - 1) / W);
+          named_bar_sync(kBarWSoft, 256);
+          if (tid == 0) {
+            const int before = atom_add_acq_rel_gpu(counters + cf, 1);
+            const bool last = before == cl - cf;
+            if (last) counters[cf] = 0;
+            *sJoin = last ? 1 : 0;
+          }
+          named_bar_sync(kBarWSoft, 256);
+          if (*sJoin) {
+            const int first_slot = (int64_t)cf * W / ctas >= gx ? 0 : 1;  // the group is its first unit, or its last
+            join_partials<D, kWRows>(part_o, part_ml, cf, cl, first_slot, u.rows, sRow, out, warp, 8, lane);
+          }
+        }
+      }
+      end(u);
+      if (tid == 0) {
+        PUnit next = *sUnit;
+        list.next(next);
+        *sUnit = next;
+      }
+    }
+  }
+  if (warp == kWMmaWarp) {
+    if (elect_one()) umma_commit(mma_done);  // every MMA has finished before TMEM is freed
+    __syncwarp();
+    mbar_wait(mma_done, 0, nullptr);
+  } else if (warp == kWMmaWarp + 1) {
+    // Every request's lengths and page ids are checked by one CTA.
+    for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
+      PagedRequest r;
+      bool bad = !paged_request(a, b, &r);
+      if (!bad) bad = paged_bad_page(a, b, r, lane, 32);
+      bad = __any_sync(0xffffffffu, bad);
+      if (lane == 0) a.status[b] = bad ? TSV_ERR_INVALID_ARG : TSV_OK;
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (tid == 0 && *abort_v)
+    for (PUnit u = *sFirst; u.valid; list.next(u)) a.status[u.b] = TSV_ERR_TIMEOUT;
+  if (warp == kWMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+template <int D>
+cudaError_t launch_typed(const PagedAttnArgs& a, int grid, void* ws, cudaStream_t st) {
+  char* w = static_cast<char*>(ws);
+  const PagedAttnLayout lay = paged_attn_layout(grid, kWRows, D);
+  return launch_pdl(paged_attn_wide_kernel<D>, dim3(grid), dim3(kWThreads), (size_t)WCfg<D>::kSmem, st, 0u, a,
+                    reinterpret_cast<int32_t*>(w), reinterpret_cast<float*>(w + lay.part_o), reinterpret_cast<float*>(w + lay.part_ml));
+}
+
+template <int D>
+cudaError_t set_typed() {
+  // The register split draws on what the block is launched with.
+  cudaFuncAttributes attr;
+  const cudaError_t e = cudaFuncGetAttributes(&attr, paged_attn_wide_kernel<D>);
+  if (e != cudaSuccess) return e;
+  if (attr.numRegs < kWRegs) return cudaErrorInvalidConfiguration;
+  return cudaFuncSetAttribute(paged_attn_wide_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, WCfg<D>::kSmem);
+}
+
+}  // namespace
+
+cudaError_t paged_attention_wide_set_attributes(int32_t D) { return D == 64 ? set_typed<64>() : set_typed<128>(); }
+
+cudaError_t launch_paged_attention_wide(const PagedAttnArgs& a, int grid, void* ws, cudaStream_t st) {
+  return a.cache.D == 64 ? launch_typed<64>(a, grid, ws, st) : launch_typed<128>(a, grid, ws, st);
+}
+
+}  // namespace tsv
