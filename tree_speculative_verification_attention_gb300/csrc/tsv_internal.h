@@ -301,6 +301,7 @@ struct PagedAttnArgs {
 // holds one completion counter per CTA, then two partial results per CTA (O
 // [R][D], then maxima and sums [2][R]).
 constexpr int32_t kPagedWideRows = 256;
+constexpr int32_t kPagedWideCtas = 160;  // at most: shared memory holds the weights of so many parts
 inline int32_t paged_attn_rows(int64_t rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : kPagedWideRows; }
 struct PagedAttnLayout {
   size_t part_o, part_ml, total;

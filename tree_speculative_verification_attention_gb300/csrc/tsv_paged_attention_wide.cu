@@ -47,8 +47,8 @@ namespace {
 
 constexpr int kWThreads = 640;
 constexpr int kWConvWarp = 8, kWMmaWarp = 16;
-// Registers a thread: 640 x 96 at launch = 256 x 144 + 256 x 72 + 128 x 48.
-constexpr int kWRegs = 96, kWSoftRegs = 144, kWConvRegs = 72, kWRestRegs = 48;
+// Registers a thread: 640 x 96 at launch = 256 x 128 + 256 x 72 + 128 x 80.
+constexpr int kWRegs = 96, kWSoftRegs = 128, kWConvRegs = 72, kWRestRegs = 80;
 static_assert(256 * kWSoftRegs + 256 * kWConvRegs + 128 * kWRestRegs <= kWThreads * kWRegs, "register split");
 constexpr int kWRows = kPagedWideRows, kWTile = 128;
 constexpr float kWThreshold = 8.f;  // log2: how far a score may pass the reference maximum
@@ -61,13 +61,14 @@ struct WCfg {
   static constexpr int kOffQ = 0;                                    // [2 tiles]
   static constexpr int kOffK = kOffQ + 2 * kTileBytes;
   static constexpr int kOffV = kOffK + kStages * kTileBytes;
-  static constexpr int kOffAnc = kOffV + kStages * kTileBytes;       // u32 [256 rows][9]: ancestors (odd stride: no bank conflicts)
+  static constexpr int kTiles = kOffV + kStages * kTileBytes, kWeights = kPagedWideCtas * kWRows * 4;
+  static constexpr int kOffAnc = kTiles > kWeights ? kTiles : kWeights;       // u32 [256 rows][9]: ancestors (odd stride: no bank conflicts)
   static constexpr int kOffCum = kOffAnc + kWRows * 9 * 4;           // i64 [TSV_MAX_BATCH + 2]
   static constexpr int kOffReq = kOffCum + 8 * (TSV_MAX_BATCH + 2);  // int4 [TSV_MAX_BATCH]
   static constexpr int kOffFr = kOffReq + 16 * TSV_MAX_BATCH;        // f32 [256]: score factor of a row
   static constexpr int kOffRow = kOffFr + 4 * kWRows;                // i32 [256]: output row
-  static constexpr int kOffScale = kOffRow + 4 * kWRows;             // f32 [4][16]: K's factors of 8 x 16 keys, V's
-  static constexpr int kOffNan = kOffScale + 4 * 64;                 // u32 [8]: tree keys whose V row holds a NaN
+  static constexpr int kOffScale = kOffRow + 4 * kWRows;             // f32 [4][20]: K's scales of 8 x 16 keys, V's, V's largest
+  static constexpr int kOffNan = kOffScale + 4 * 80;                 // u32 [8]: tree keys whose V row holds a NaN
   static constexpr int kOffUnit = kOffNan + 32;                      // PUnit
   static constexpr int kOffFirst = kOffUnit + 64;                    // PUnit, then i64 [4]
   static constexpr int kOffBar = kOffFirst + 96;
@@ -77,6 +78,8 @@ struct WCfg {
   static constexpr int kSmem = kOffMisc + 32 + 1024;
   static constexpr uint32_t kColO = 2 * kPBlock;  // S0 | S1 | O0 | O1
   static_assert(kSmem <= 227 * 1024, "shared memory");
+  static_assert(kWRows * (D + 4) * 4 <= kOffAnc, "a partial's rows fit in the tiles");
+
   static_assert(kOffAnc % 1024 == 0 && kOffCum % 16 == 0 && kOffScale % 16 == 0 && kOffUnit % 16 == 0 && kOffBar % 8 == 0, "alignment");
 };
 
@@ -248,7 +251,9 @@ __global__ void __launch_bounds__(kWThreads, 1)
       const tsv_paged_cache& c = a.cache;
       // A lane's part of a block: 16 codes of u.rows row_of, row_of + kStep, ...
       constexpr int kLanes = D / 16, kStep = 256 / kLanes, kParts = kPBlock / kStep;  // lanes of a row; 4 or 2 rows of a thread
-      const int chunk = ct % kLanes, first_row = ct / kLanes;
+      // Eight lanes take four 16-code chunks of two rows: their stores meet 32 banks.
+      const int chunk = D == 128 ? (ct & 3) | ((ct >> 1) & 4) : ct & 3;
+      const int first_row = D == 128 ? ((ct >> 2) & 1) | ((ct >> 4) << 1) : ct >> 2;
       uint4 kb[kParts], vb[kParts];
       float sk = 0.f, sv = 0.f;  // warp 0, lanes 0 .. 7: scales of 16 keys each
       const int64_t head_at = (int64_t)u.g * c.stride_head + 16 * chunk;
@@ -288,14 +293,10 @@ __global__ void __launch_bounds__(kWThreads, 1)
       auto put = [&](uint8_t* tile, int key, const uint4& codes) {
         uint4 x, y;
         widen(codes, x, y);
-        // Chunks 2 c and 2 c + 1 of 8 values; the upper lanes of a 128-wide row
-        // (the other column group) start with the second, so that 8 lanes meet
-        // 32 banks.
-        const int c0 = (2 * chunk) & 7;
         uint8_t* row = tile + (chunk >> 2) * (kPBlock * 128) + key * 128;
-        const int s = D == 128 ? chunk >> 2 : 0;
-        *reinterpret_cast<uint4*>(row + (((c0 + s) ^ (key & 7)) << 4)) = s ? y : x;
-        *reinterpret_cast<uint4*>(row + (((c0 + (s ^ 1)) ^ (key & 7)) << 4)) = s ? x : y;
+        const int at = (((2 * chunk) & 7) ^ (key & 7)) << 4;  // chunk 2 c of 8 values, and its neighbour
+        *reinterpret_cast<uint4*>(row + at) = x;
+        *reinterpret_cast<uint4*>(row + (at ^ 16)) = y;
       };
       look(0);
       load(0);
@@ -351,10 +352,12 @@ __global__ void __launch_bounds__(kWThreads, 1)
         if (x >= 2) TSV_PWAIT(&k_empty[st], (x >> 1) - 1);
         if (__any_sync(0xffffffffu, dead)) break;
         if (w == 0) {
+          const float top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(sv)));  // (scales are >= 0)
           if (lane < 8) {
-            sScale[(x & 3) * 16 + lane] = sk;
-            sScale[(x & 3) * 16 + 8 + lane] = sv;
+            sScale[(x & 3) * 20 + lane] = sk;
+            sScale[(x & 3) * 20 + 8 + lane] = sv;
           }
+          if (lane == 0) sScale[(x & 3) * 20 + 16] = top;
           __syncwarp();
           if (lane == 0) mbar_arrive(&sc_full[x & 3]);
         }
@@ -400,9 +403,10 @@ __global__ void __launch_bounds__(kWThreads, 1)
         const uint64_t dq = sdesc_sw128(smem_u32(sQ), 16, 1024);
         const uint64_t dk = sdesc_sw128(smem_u32(sK), 16, 1024);
         const uint64_t dv = sdesc_sw128(smem_u32(sV), kPBlock * 128, 1024);
-        auto issue_s = [&](int tile, int x) {
+        auto issue_s = [&](int tile, auto stage_c) {
+          constexpr int stage = decltype(stage_c)::value;
           const uint32_t da = (uint32_t)dq + (uint32_t)((tile * C::kTileBytes) >> 4);
-          const uint32_t db = (uint32_t)dk + (uint32_t)(((x & 1) * C::kTileBytes) >> 4);
+          const uint32_t db = (uint32_t)dk + (uint32_t)((stage * C::kTileBytes) >> 4);
           const bool lead = elect_one();
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
@@ -412,8 +416,9 @@ __global__ void __launch_bounds__(kWThreads, 1)
           if (lead) umma_commit(&s_full[tile]);
           __syncwarp();
         };
-        auto issue_pv = [&](int tile, int x, bool more) {
-          const uint32_t db = (uint32_t)dv + (uint32_t)(((x & 1) * C::kTileBytes) >> 4);
+        auto issue_pv = [&](int tile, auto stage_c, bool more) {
+          constexpr int stage = decltype(stage_c)::value;
+          const uint32_t db = (uint32_t)dv + (uint32_t)((stage * C::kTileBytes) >> 4);
           const bool lead = elect_one();
 #pragma unroll
           for (int kk = 0; kk < kPBlock / 16; ++kk)
@@ -422,38 +427,54 @@ __global__ void __launch_bounds__(kWThreads, 1)
           if (lead) umma_commit(&pv_done[tile]);
           __syncwarp();
         };
-        TSV_PWAIT(&k_full[t & 1], t >> 1);
-        tc_fence_after();
-        if (!__any_sync(0xffffffffu, dead)) {
-          for (int q = 0; q < u.ntiles; ++q) issue_s(q, t);
-          if (elect_one()) umma_commit(&k_empty[t & 1]);
-        }
-        for (int i = 0; i < u.blocks; ++i) {
+        using Even = std::integral_constant<int, 0>;
+        using Odd = std::integral_constant<int, 1>;
+        // PV of block i (stage_c: its ring stage), then S of the next one.
+        auto block = [&](int i, auto stage_c) {
+          constexpr int stage = decltype(stage_c)::value;
+          using Next = std::integral_constant<int, stage ^ 1>;
           const int x = t + i;
           const bool more = i + 1 < u.blocks;
-          TSV_PWAIT(&v_full[x & 1], x >> 1);
+          TSV_PWAIT(&v_full[stage], x >> 1);
           TSV_PWAIT(&p_full[0], cnt[0] + i);
-          if (__any_sync(0xffffffffu, dead)) break;
+          if (__any_sync(0xffffffffu, dead)) return;
           tc_fence_after();
-          issue_pv(0, x, i > 0);
+          issue_pv(0, stage_c, i > 0);
           if (more) {
-            TSV_PWAIT(&k_full[(x + 1) & 1], (x + 1) >> 1);
-            if (__any_sync(0xffffffffu, dead)) break;
+            TSV_PWAIT(&k_full[stage ^ 1], (x + 1) >> 1);
+            if (__any_sync(0xffffffffu, dead)) return;
             tc_fence_after();
-            issue_s(0, x + 1);
+            issue_s(0, Next{});
           }
           if (u.ntiles > 1) {
             TSV_PWAIT(&p_full[1], cnt[1] + i);
-            if (__any_sync(0xffffffffu, dead)) break;
+            if (__any_sync(0xffffffffu, dead)) return;
             tc_fence_after();
-            issue_pv(1, x, i > 0);
+            issue_pv(1, stage_c, i > 0);
           }
-          if (elect_one()) umma_commit(&v_empty[x & 1]);
+          if (elect_one()) umma_commit(&v_empty[stage]);
           if (more) {
-            if (u.ntiles > 1) issue_s(1, x + 1);
-            if (elect_one()) umma_commit(&k_empty[(x + 1) & 1]);
+            if (u.ntiles > 1) issue_s(1, Next{});
+            if (elect_one()) umma_commit(&k_empty[stage ^ 1]);
           }
           __syncwarp();
+        };
+        auto first = [&](auto stage_c) {
+          constexpr int stage = decltype(stage_c)::value;
+          TSV_PWAIT(&k_full[stage], t >> 1);
+          if (__any_sync(0xffffffffu, dead)) return;
+          tc_fence_after();
+          for (int q = 0; q < u.ntiles; ++q) issue_s(q, stage_c);
+          if (elect_one()) umma_commit(&k_empty[stage]);
+          __syncwarp();
+        };
+        if (t & 1) first(Odd{});
+        else first(Even{});
+#pragma unroll 1
+        for (int i = 0; i < u.blocks; ++i) {
+          if ((t + i) & 1) block(i, Odd{});
+          else block(i, Even{});
+          if (__any_sync(0xffffffffu, dead)) break;
         }
       }
       end(u);
@@ -491,7 +512,7 @@ __global__ void __launch_bounds__(kWThreads, 1)
         TSV_PWAIT(&sc_full[x & 3], x >> 2);
         if (__any_sync(0xffffffffu, dead)) return;
         tc_fence_after();
-        const float4* sc = reinterpret_cast<const float4*>(sScale + (x & 3) * 16);
+        const float* sc = sScale + (x & 3) * 20;
         uint64_t vis[2] = {~0ull, ~0ull};
         if (MASKED) {
           const int valid = u.valid(i);
@@ -503,23 +524,16 @@ __global__ void __launch_bounds__(kWThreads, 1)
             vis[1] &= (uint64_t)m[2] | ((uint64_t)m[3] << 32);
           }
         }
-        // The largest score, 32 keys at a time (all 128 would not fit in
-        // registers: they are read again below).
+        // The largest score, 32 keys at a time (128 would not fit in registers:
+        // the first 64 are read again below).
         float hmax = -INFINITY;
         uint32_t s[2][32];
-        float f[8];  // the row's factor of 16 keys each
-        {
-          const float4 f0 = sc[0], f1 = sc[1];
-          f[0] = f0.x * fr, f[1] = f0.y * fr, f[2] = f0.z * fr, f[3] = f0.w * fr;
-          f[4] = f1.x * fr, f[5] = f1.y * fr, f[6] = f1.z * fr, f[7] = f1.w * fr;
-        }
         tmem_ld32_nowait(s_col, s[0]);
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           uint32_t(&z)[32] = s[c & 1];
           tmem_wait_ld_tie32(z);
           if (c < 3) tmem_ld32_nowait(s_col + 32 * (c + 1), s[(c + 1) & 1]);
-          else tmem_ld32_nowait(s_col + 96, s[0]);  // the last keys, for the second pass
           if (MASKED) {
             const uint32_t see = (uint32_t)(vis[c >> 1] >> (32 * (c & 1)));
 #pragma unroll
@@ -535,7 +549,7 @@ __global__ void __launch_bounds__(kWThreads, 1)
               b0 = fmax3(b0, __uint_as_float(z[e]), __uint_as_float(z[e + 1]));
               b1 = fmax3(b1, __uint_as_float(z[e + 2]), __uint_as_float(z[e + 3]));
             }
-            hmax = fmaxf(hmax, fmaxf(b0, b1) * f[2 * c + (q >> 4)]);
+            hmax = fmaxf(hmax, fmaxf(b0, b1) * (sc[2 * c + (q >> 4)] * fr));
           }
         }
         float alpha = 1.f;
@@ -544,8 +558,7 @@ __global__ void __launch_bounds__(kWThreads, 1)
           m_ref = hmax;
         }
         l *= alpha;
-        const float4 g0 = sc[2], g1 = sc[3];
-        const float v_top = fmaxf(fmaxf(fmaxf(g0.x, g0.y), fmaxf(g0.z, g0.w)), fmaxf(fmaxf(g1.x, g1.y), fmaxf(g1.z, g1.w)));
+        const float v_top = sc[16];
         if (v_top > v_ref) {  // the same in every thread
           alpha *= v_ref / v_top;
           v_ref = v_top;
@@ -569,18 +582,19 @@ __global__ void __launch_bounds__(kWThreads, 1)
         uint64_t sum[2] = {0ull, 0ull};
         // P from the last keys to the first over the upper half of S, two keys a
         // column: what a store overwrites has been read.
-        const float fv[8] = {g0.x * to_v, g0.y * to_v, g0.z * to_v, g0.w * to_v, g1.x * to_v, g1.y * to_v, g1.z * to_v, g1.w * to_v};
 #pragma unroll
         for (int c = 3; c >= 0; --c) {
-          uint32_t(&z)[32] = s[(c + 1) & 1];
-          tmem_wait_ld_tie32(z);
-          if (c > 0) tmem_ld32_nowait(s_col + 32 * (c - 1), s[c & 1]);
+          uint32_t(&z)[32] = s[c & 1];
+          if (c < 2) tmem_wait_ld_tie32(z);
+          if (c == 1) tmem_ld32_nowait(s_col, s[0]);
           const uint32_t see = MASKED ? (uint32_t)(vis[c >> 1] >> (32 * (c & 1))) : 0u;
+          const float2 k2 = *reinterpret_cast<const float2*>(sc + 2 * c), v2 = *reinterpret_cast<const float2*>(sc + 8 + 2 * c);
+          const float f0 = k2.x * fr, f1 = k2.y * fr, fv0 = v2.x * to_v, fv1 = v2.y * to_v;
           uint32_t h[16];
 #pragma unroll
           for (int e = 0; e < 32; e += 2) {
-            const int q = 2 * c + (e >> 4);
-            const uint64_t x2 = ffma2((uint64_t)z[e] | ((uint64_t)z[e + 1] << 32), f2_pack(f[q], f[q]), ref2);
+            const float f = e < 16 ? f0 : f1, fv = e < 16 ? fv0 : fv1;
+            const uint64_t x2 = ffma2((uint64_t)z[e] | ((uint64_t)z[e + 1] << 32), f2_pack(f, f), ref2);
             float p0 = fast_exp2(f2_lo(x2)), p1 = fast_exp2(f2_hi(x2));
             if (MASKED) {
               if (!((see >> e) & 1u)) p0 = 0.f;
@@ -588,10 +602,11 @@ __global__ void __launch_bounds__(kWThreads, 1)
             }
             const uint64_t p2 = f2_pack(p0, p1);
             sum[(e >> 1) & 1] = fadd2(sum[(e >> 1) & 1], p2);
-            const uint64_t y2 = fmul2(p2, f2_pack(fv[q], fv[q]));
+            const uint64_t y2 = fmul2(p2, f2_pack(fv, fv));
             h[e >> 1] = pack_f16x2(f2_lo(y2), f2_hi(y2));
           }
           tmem_st16u_nowait(s_col + kPBlock / 2 + 16 * c, h);
+          if (c == 3) tmem_ld32_nowait(s_col + 32, s[1]);
         }
         tmem_wait_st();
         const uint64_t both = fadd2(sum[0], sum[1]);
@@ -641,7 +656,10 @@ __global__ void __launch_bounds__(kWThreads, 1)
         const int slot = 2 * (int)blockIdx.x + (k == 0 ? 0 : 1);
         if (active) {
           __nv_bfloat16* to = out + (int64_t)(row < u.rows ? sRow[row] : 0) * D;
-          float* po = part_o + ((int64_t)slot * kWRows + row) * D;
+          // A partial's rows go through shared memory (the tiles are idle), a
+          // warp its own 32, so that a store covers a whole row.
+          float* po = part_o + ((int64_t)slot * kWRows + (row & ~31)) * D;
+          float* mine = reinterpret_cast<float*>(smem) + row * (D + 4);
 #pragma unroll
           for (int cc = 0; cc < D; cc += 32) {
             float o[32];
@@ -656,9 +674,19 @@ __global__ void __launch_bounds__(kWThreads, 1)
                                                                       pack_bf16x2(o[e + 4], o[e + 5]), pack_bf16x2(o[e + 6], o[e + 7]));
               } else {
 #pragma unroll
-                for (int e = 0; e < 32; e += 4) *reinterpret_cast<float4*>(po + cc + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                for (int e = 0; e < 32; e += 4) *reinterpret_cast<float4*>(mine + cc + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
               }
             }
+          }
+          if (!whole) {
+            __syncwarp();
+            constexpr int kOnce = 128 / D;  // rows of a store
+            const int rl = lane / (D / 4), d4 = (lane % (D / 4)) * 4;
+#pragma unroll 4
+            for (int q = rl; q < 32; q += kOnce)
+              if ((row & ~31) + q < u.rows)
+                *reinterpret_cast<float4*>(po + q * D + d4) =
+                    *reinterpret_cast<const float4*>(reinterpret_cast<float*>(smem) + ((row & ~31) + q) * (D + 4) + d4);
           }
           if (!whole && row < u.rows) {  // normalised: its sum is 1
             float* pm = part_ml + (int64_t)slot * 2 * kWRows;
@@ -681,7 +709,63 @@ __global__ void __launch_bounds__(kWThreads, 1)
           named_bar_sync(kBarWSoft, 256);
           if (*sJoin) {
             const int first_slot = (int64_t)cf * W / ctas >= gx ? 0 : 1;  // the group is its first unit, or its last
-            join_partials<D, kWRows>(part_o, part_ml, cf, cl, first_slot, u.rows, sRow, out, warp, 8, lane);
+            // Weights of the parts of every row (a thread each), then the rows,
+            // 16 bytes at a time: four of a thread with six parts each in flight.
+            float* weight = reinterpret_cast<float*>(smem);  // [part][row]
+            const int parts = cl - cf + 1;
+            auto slot_of = [&](int c) { return (int64_t)(2 * (cf + c) + (c == 0 ? first_slot : 0)); };
+            if (tid < u.rows) {
+              float top = -INFINITY, all = 0.f;
+#pragma unroll 4
+              for (int c = 0; c < parts; ++c) top = fmaxf(top, __ldcg(part_ml + slot_of(c) * 2 * kWRows + tid));
+#pragma unroll 4
+              for (int c = 0; c < parts; ++c) {
+                const float* ml = part_ml + slot_of(c) * 2 * kWRows + tid;
+                const float m = __ldcg(ml), w = m == -INFINITY ? 0.f : fast_exp2(m - top);
+                all += w * __ldcg(ml + kWRows);
+                weight[c * kWRows + tid] = w;
+              }
+              const float scale = all == 0.f ? 0.f : 1.f / all;
+              for (int c = 0; c < parts; ++c) weight[c * kWRows + tid] *= scale;
+            }
+            named_bar_sync(kBarWSoft, 256);
+            constexpr int kItems = 4, kParts = 6, L4 = D / 4;
+            for (int i0 = tid; i0 < u.rows * L4; i0 += kItems * 256) {
+              float4 o[kItems];
+#pragma unroll
+              for (int x = 0; x < kItems; ++x) o[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+              for (int c0 = 0; c0 < parts; c0 += kParts) {
+                float4 v[kParts][kItems];
+#pragma unroll
+                for (int c = 0; c < kParts; ++c)
+#pragma unroll
+                  for (int x = 0; x < kItems; ++x) {
+                    const int i = i0 + x * 256;
+                    v[c][x] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (c0 + c < parts && i < u.rows * L4)
+                      v[c][x] = __ldcg(reinterpret_cast<const float4*>(part_o + slot_of(c0 + c) * kWRows * D) + i);
+                  }
+#pragma unroll
+                for (int c = 0; c < kParts; ++c)
+#pragma unroll
+                  for (int x = 0; x < kItems; ++x) {
+                    const int i = i0 + x * 256;
+                    if (c0 + c >= parts || i >= u.rows * L4) continue;
+                    const float w = weight[(c0 + c) * kWRows + i / L4];
+                    o[x].x += w * v[c][x].x;
+                    o[x].y += w * v[c][x].y;
+                    o[x].z += w * v[c][x].z;
+                    o[x].w += w * v[c][x].w;
+                  }
+              }
+#pragma unroll
+              for (int x = 0; x < kItems; ++x) {
+                const int i = i0 + x * 256;
+                if (i < u.rows * L4)
+                  *reinterpret_cast<uint2*>(out + (int64_t)sRow[i / L4] * D + (i % L4) * 4) =
+                      make_uint2(pack_bf16x2(o[x].x, o[x].y), pack_bf16x2(o[x].z, o[x].w));
+              }
+            }
           }
         }
       }
@@ -719,7 +803,8 @@ __global__ void __launch_bounds__(kWThreads, 1)
 }
 
 template <int D>
-cudaError_t launch_typed(const PagedAttnArgs& a, int grid, void* ws, cudaStream_t st) {
+cudaError_t launch_typed(const PagedAttnArgs& a, int num_sms, void* ws, cudaStream_t st) {
+  const int grid = min(num_sms, kPagedWideCtas);
   char* w = static_cast<char*>(ws);
   const PagedAttnLayout lay = paged_attn_layout(grid, kWRows, D);
   return launch_pdl(paged_attn_wide_kernel<D>, dim3(grid), dim3(kWThreads), (size_t)WCfg<D>::kSmem, st, 0u, a,
