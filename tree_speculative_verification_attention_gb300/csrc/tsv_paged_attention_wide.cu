@@ -52,7 +52,8 @@ constexpr int kWRegs = 96, kWSoftRegs = 128, kWConvRegs = 72, kWRestRegs = 80;
 static_assert(256 * kWSoftRegs + 256 * kWConvRegs + 128 * kWRestRegs <= kWThreads * kWRegs, "register split");
 constexpr int kWRows = kPagedWideRows, kWTile = 128;
 constexpr float kWThreshold = 8.f;  // log2: how far a score may pass the reference maximum
-constexpr int kBarWSoft = 1;
+constexpr int kHalf = 64;  // keys of a softmax step
+constexpr int kBarWSoft = 1, kBarWJoin = 2;
 
 template <int D>
 struct WCfg {
@@ -72,8 +73,8 @@ struct WCfg {
   static constexpr int kOffUnit = kOffNan + 32;                      // PUnit
   static constexpr int kOffFirst = kOffUnit + 64;                    // PUnit, then i64 [4]
   static constexpr int kOffBar = kOffFirst + 96;
-  // k_full[2], k_empty[2], v_full[2], v_empty[2], sc_full[4], s_full[2], p_full[2], pv_done[2], mma_done
-  static constexpr int kBars = 19;
+  // k_full[2], k_empty[2], v_full[2], v_empty[2], sc_full[4], s_full[4], p_full[4], pv_done[2], mma_done
+  static constexpr int kBars = 23;
   static constexpr int kOffMisc = kOffBar + 8 * kBars + 8;
   static constexpr int kSmem = kOffMisc + 32 + 1024;
   static constexpr uint32_t kColO = 2 * kPBlock;  // S0 | S1 | O0 | O1
@@ -120,6 +121,19 @@ __device__ __forceinline__ uint4 load_if(const uint8_t* p, bool on) {
       "@q ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];\n\t}\n"
       : "+r"(v.x), "+r"(v.y), "+r"(v.z), "+r"(v.w)
       : "l"(p), "r"((uint32_t)on));
+  return v;
+}
+
+// The same of a partial (through L2: another CTA wrote it).
+__device__ __forceinline__ float4 load_part(const float* p, bool on) {
+  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q ld.global.cg.v4.f32 {%0, %1, %2, %3}, [%4];\n\t}\n"
+      : "+f"(v.x), "+f"(v.y), "+f"(v.z), "+f"(v.w)
+      : "l"(p), "r"((uint32_t)on)
+      : "memory");
   return v;
 }
 
@@ -170,9 +184,9 @@ __global__ void __launch_bounds__(kWThreads, 1)
   uint64_t* v_full = k_empty + 2;
   uint64_t* v_empty = v_full + 2;
   uint64_t* sc_full = v_empty + 2;
-  uint64_t* s_full = sc_full + 4;   // [tile]
-  uint64_t* p_full = s_full + 2;    // [tile]
-  uint64_t* pv_done = p_full + 2;   // [tile]
+  uint64_t* s_full = sc_full + 4;   // [tile][half]
+  uint64_t* p_full = s_full + 4;    // [tile][half]
+  uint64_t* pv_done = p_full + 4;   // [tile]
   uint64_t* mma_done = pv_done + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
   int* abort_flag = reinterpret_cast<int*>(smem + C::kOffMisc + 4);
@@ -187,15 +201,17 @@ __global__ void __launch_bounds__(kWThreads, 1)
   if (tid == 0) {
     for (int s = 0; s < 2; ++s) {
       mbar_init(&k_full[s], 8);   // the widening warps
-      mbar_init(&k_empty[s], 1);
+      mbar_init(&k_empty[s], 2);  // both tiles' issuers (the first for both when there is one)
       mbar_init(&v_full[s], 8);
-      mbar_init(&v_empty[s], 1);
-      mbar_init(&s_full[s], 1);
-      mbar_init(&p_full[s], 128);
+      mbar_init(&v_empty[s], 2);
       mbar_init(&pv_done[s], 1);
     }
-    for (int s = 0; s < 4; ++s) mbar_init(&sc_full[s], 1);
-    mbar_init(mma_done, 1);
+    for (int s = 0; s < 4; ++s) {
+      mbar_init(&sc_full[s], 1);
+      mbar_init(&s_full[s], 1);
+      mbar_init(&p_full[s], 128);
+    }
+    mbar_init(mma_done, 2);
     *abort_flag = 0;
     mbar_fence_init();
   }
@@ -214,7 +230,10 @@ __global__ void __launch_bounds__(kWThreads, 1)
 
   // Every role walks the units together: a barrier before each, one when its
   // rows are in, and one behind it.
-  if (tid == 0) *sUnit = *sFirst;
+  if (tid == 0) {
+    *sUnit = *sFirst;
+    *sJoin = 0;
+  }
   int t = 0;            // blocks so far
   int cnt[2] = {0, 0};  // and those of each tile
   auto begin = [&](WUnit& u) {
@@ -242,6 +261,65 @@ __global__ void __launch_bounds__(kWThreads, 1)
     tc_fence_after();
   };
   WUnit u;
+  // CTAs cf .. cf + parts - 1 share the unit's group; part c is in slot(c).
+  struct Group {
+    int cf, parts, first;  // first: the group is the first unit of CTA cf, or its last
+    __device__ __forceinline__ int64_t slot(int c) const { return 2 * (cf + c) + (c == 0 ? first : 0); }
+  };
+  auto group = [&]() {
+    const int64_t W = sRange[2], ctas = sRange[3], gx = sUnit->gx;
+    Group z;
+    z.cf = (int)(((gx + 1) * ctas - 1) / W);
+    z.parts = (int)(((gx + sUnit->T) * ctas - 1) / W) - z.cf + 1;
+    z.first = (int64_t)z.cf * W / ctas >= gx ? 0 : 1;
+    return z;
+  };
+  float* weight = reinterpret_cast<float*>(smem);  // [part][row], over the idle tiles
+  // The group's rows from its parts (threads 0 .. 511): 16 bytes at a time, two
+  // of a thread with four parts each in flight.
+  auto join = [&](int i_first) {
+    const Group z = group();
+    constexpr int kItems = 2, kParts = 4, L4 = D / 4;
+    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out);
+#pragma unroll 1
+    for (int i0 = i_first; i0 < u.rows * L4; i0 += kItems * 512) {
+      float4 o[kItems];
+#pragma unroll
+      for (int x = 0; x < kItems; ++x) o[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+      for (int c0 = 0; c0 < z.parts; c0 += kParts) {
+        float4 v[kParts][kItems];
+#pragma unroll
+        for (int c = 0; c < kParts; ++c) {
+          const float* part = part_o + z.slot(c0 + c) * kWRows * D;
+#pragma unroll
+          for (int x = 0; x < kItems; ++x) {
+            const int i = i0 + x * 512;
+            v[c][x] = load_part(part + 4 * i, c0 + c < z.parts && i < u.rows * L4);
+          }
+        }
+#pragma unroll
+        for (int c = 0; c < kParts; ++c)
+#pragma unroll
+          for (int x = 0; x < kItems; ++x) {
+            const int i = i0 + x * 512;
+            if (c0 + c >= z.parts || i >= u.rows * L4) continue;
+            const float w = weight[(c0 + c) * kWRows + i / L4];
+            o[x].x += w * v[c][x].x;
+            o[x].y += w * v[c][x].y;
+            o[x].z += w * v[c][x].z;
+            o[x].w += w * v[c][x].w;
+          }
+      }
+#pragma unroll
+      for (int x = 0; x < kItems; ++x) {
+        const int i = i0 + x * 512;
+        if (i < u.rows * L4)
+          *reinterpret_cast<uint2*>(out + (int64_t)sRow[i / L4] * D + (i % L4) * 4) =
+              make_uint2(pack_bf16x2(o[x].x, o[x].y), pack_bf16x2(o[x].z, o[x].w));
+      }
+    }
+  };
 
   if (warp >= kWConvWarp && warp < kWMmaWarp) {
     // ---------------------------------------------------------- Q, then K and V, widened
@@ -391,6 +469,10 @@ __global__ void __launch_bounds__(kWThreads, 1)
         if (i + 1 < u.blocks) load(i + 1);
         if (i + 2 < u.blocks) look(i + 2);
       }
+      if (!sUnit->whole()) {
+        named_bar_sync(kBarWJoin, 512);
+        if (*sJoin) join(tid);
+      }
       end(u);
     }
   } else if (warp >= kWMmaWarp) {
@@ -398,83 +480,68 @@ __global__ void __launch_bounds__(kWThreads, 1)
     setmaxnreg_dec<kWRestRegs>();
     while (begin(u)) {
       __syncthreads();  // the unit's rows are in
-      if (warp == kWMmaWarp) {
-        constexpr uint32_t idS = idesc_f16_f32(kWTile, kPBlock, 0), idPV = idesc_f16_f32(kWTile, D, 1);
+      const int q = warp - kWMmaWarp;  // the issuer's tile
+      if (q < u.ntiles) {
+        constexpr uint32_t idS = idesc_f16_f32(kWTile, kHalf, 0), idPV = idesc_f16_f32(kWTile, D, 1);
         const uint64_t dq = sdesc_sw128(smem_u32(sQ), 16, 1024);
         const uint64_t dk = sdesc_sw128(smem_u32(sK), 16, 1024);
         const uint64_t dv = sdesc_sw128(smem_u32(sV), kPBlock * 128, 1024);
-        auto issue_s = [&](int tile, auto stage_c) {
-          constexpr int stage = decltype(stage_c)::value;
+        // S of tile and half block: 64 keys, so that a tile has two buffers and
+        // the next half's scores are there when its softmax gets to them.
+        auto issue_s = [&](int tile, int x, int half) {
           const uint32_t da = (uint32_t)dq + (uint32_t)((tile * C::kTileBytes) >> 4);
-          const uint32_t db = (uint32_t)dk + (uint32_t)((stage * C::kTileBytes) >> 4);
+          const uint32_t db = (uint32_t)dk + (uint32_t)(((x & 1) * C::kTileBytes + half * (kHalf * 128)) >> 4);
+          const uint32_t dst = tmem + (uint32_t)(tile * kPBlock + half * kHalf);
           const bool lead = elect_one();
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
             const uint32_t o = ((kk >> 2) * (kPBlock * 128) + (kk & 3) * 32) >> 4;
-            umma_f16(tmem + (uint32_t)(tile * kPBlock), desc_at(dq, da + o), desc_at(dk, db + o), idS, kk > 0 ? 1u : 0u, lead);
+            umma_f16(dst, desc_at(dq, da + o), desc_at(dk, db + o), idS, kk > 0 ? 1u : 0u, lead);
           }
-          if (lead) umma_commit(&s_full[tile]);
+          if (lead) umma_commit(&s_full[2 * tile + half]);
           __syncwarp();
         };
-        auto issue_pv = [&](int tile, auto stage_c, bool more) {
-          constexpr int stage = decltype(stage_c)::value;
-          const uint32_t db = (uint32_t)dv + (uint32_t)((stage * C::kTileBytes) >> 4);
+        // O += P V over those keys; P, two keys a column, lies over its S.
+        auto issue_pv = [&](int tile, int x, int half, bool more) {
+          const uint32_t db = (uint32_t)dv + (uint32_t)(((x & 1) * C::kTileBytes + half * (kHalf * 128)) >> 4);
+          const uint32_t pa = tmem + (uint32_t)(tile * kPBlock + half * kHalf), dst = tmem + C::kColO + (uint32_t)(tile * D);
           const bool lead = elect_one();
 #pragma unroll
-          for (int kk = 0; kk < kPBlock / 16; ++kk)
-            umma_f16_ts(tmem + C::kColO + tile * D, tmem + (uint32_t)(tile * kPBlock + kPBlock / 2) + kk * 8,
-                        desc_at(dv, db + ((kk * 16 * 128) >> 4)), idPV, more || kk > 0 ? 1u : 0u, lead);
+          for (int kk = 0; kk < kHalf / 16; ++kk)
+            umma_f16_ts(dst, pa + kk * 8, desc_at(dv, db + ((kk * 16 * 128) >> 4)), idPV, more || kk > 0 ? 1u : 0u, lead);
           if (lead) umma_commit(&pv_done[tile]);
           __syncwarp();
         };
-        using Even = std::integral_constant<int, 0>;
-        using Odd = std::integral_constant<int, 1>;
-        // PV of block i (stage_c: its ring stage), then S of the next one.
-        auto block = [&](int i, auto stage_c) {
-          constexpr int stage = decltype(stage_c)::value;
-          using Next = std::integral_constant<int, stage ^ 1>;
-          const int x = t + i;
-          const bool more = i + 1 < u.blocks;
-          TSV_PWAIT(&v_full[stage], x >> 1);
-          TSV_PWAIT(&p_full[0], cnt[0] + i);
-          if (__any_sync(0xffffffffu, dead)) return;
+        const int both = u.ntiles == 1 ? 2 : 1;  // arrivals at the rings' barriers
+        TSV_PWAIT(&k_full[t & 1], t >> 1);
+        if (!__any_sync(0xffffffffu, dead)) {
           tc_fence_after();
-          issue_pv(0, stage_c, i > 0);
-          if (more) {
-            TSV_PWAIT(&k_full[stage ^ 1], (x + 1) >> 1);
-            if (__any_sync(0xffffffffu, dead)) return;
-            tc_fence_after();
-            issue_s(0, Next{});
-          }
-          if (u.ntiles > 1) {
-            TSV_PWAIT(&p_full[1], cnt[1] + i);
-            if (__any_sync(0xffffffffu, dead)) return;
-            tc_fence_after();
-            issue_pv(1, stage_c, i > 0);
-          }
-          if (elect_one()) umma_commit(&v_empty[stage]);
-          if (more) {
-            if (u.ntiles > 1) issue_s(1, Next{});
-            if (elect_one()) umma_commit(&k_empty[stage ^ 1]);
-          }
+          issue_s(q, t, 0);
+          issue_s(q, t, 1);
+          if (elect_one())
+            for (int n = 0; n < both; ++n) umma_commit(&k_empty[t & 1]);
           __syncwarp();
-        };
-        auto first = [&](auto stage_c) {
-          constexpr int stage = decltype(stage_c)::value;
-          TSV_PWAIT(&k_full[stage], t >> 1);
-          if (__any_sync(0xffffffffu, dead)) return;
-          tc_fence_after();
-          for (int q = 0; q < u.ntiles; ++q) issue_s(q, stage_c);
-          if (elect_one()) umma_commit(&k_empty[stage]);
-          __syncwarp();
-        };
-        if (t & 1) first(Odd{});
-        else first(Even{});
+        }
 #pragma unroll 1
-        for (int i = 0; i < u.blocks; ++i) {
-          if ((t + i) & 1) block(i, Odd{});
-          else block(i, Even{});
+        for (int h = 0; h < 2 * u.blocks; ++h) {
+          const int i = h >> 1, half = h & 1, x = t + i;
+          const bool more = i + 1 < u.blocks;
+          if (half == 0) TSV_PWAIT(&v_full[x & 1], x >> 1);
+          TSV_PWAIT(&p_full[2 * q + half], cnt[q] + i);
           if (__any_sync(0xffffffffu, dead)) break;
+          tc_fence_after();
+          issue_pv(q, x, half, h > 0);
+          if (half == 1 && elect_one())
+            for (int n = 0; n < both; ++n) umma_commit(&v_empty[x & 1]);
+          if (more) {
+            if (half == 0) TSV_PWAIT(&k_full[(x + 1) & 1], (x + 1) >> 1);
+            if (__any_sync(0xffffffffu, dead)) break;
+            tc_fence_after();
+            issue_s(q, x + 1, half);
+            if (half == 1 && elect_one())
+              for (int n = 0; n < both; ++n) umma_commit(&k_empty[(x + 1) & 1]);
+          }
+          __syncwarp();
         }
       }
       end(u);
@@ -501,56 +568,54 @@ __global__ void __launch_bounds__(kWThreads, 1)
       }
       __syncthreads();  // the unit's u.rows are in
       const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
-      const uint32_t s_col = tmem + lane_base + (uint32_t)(tile * kPBlock);
       const uint32_t o_col = tmem + lane_base + C::kColO + (uint32_t)(tile * D);
       const float fr = sFr[row];
       float m_ref = -INFINITY, l = 0.f, v_ref = 0.f, to_v = 0.f;
-      auto block_step = [&](int i, auto masked_c) {
+      auto half_step = [&](int h, auto masked_c) {
         constexpr bool MASKED = decltype(masked_c)::value;
-        const int x = t + i;
-        TSV_PWAIT(&s_full[tile], cnt[tile] + i);
-        TSV_PWAIT(&sc_full[x & 3], x >> 2);
+        const int i = h >> 1, half = h & 1, x = t + i;
+        TSV_PWAIT(&s_full[2 * tile + half], cnt[tile] + i);
+        if (half == 0) TSV_PWAIT(&sc_full[x & 3], x >> 2);
         if (__any_sync(0xffffffffu, dead)) return;
         tc_fence_after();
-        const float* sc = sScale + (x & 3) * 20;
-        uint64_t vis[2] = {~0ull, ~0ull};
-        if (MASKED) {
-          const int valid = u.valid(i);
-          vis[0] = valid >= 64 ? ~0ull : (1ull << valid) - 1ull;
-          vis[1] = valid >= 128 ? ~0ull : valid > 64 ? (1ull << (valid - 64)) - 1ull : 0ull;
-          if (u.j + i >= u.nmain) {
-            const uint32_t* m = anc + 4 * (u.j + i - u.nmain);
-            vis[0] &= (uint64_t)m[0] | ((uint64_t)m[1] << 32);
-            vis[1] &= (uint64_t)m[2] | ((uint64_t)m[3] << 32);
-          }
-        }
-        // The largest score, 32 keys at a time (128 would not fit in registers:
-        // the first 64 are read again below).
-        float hmax = -INFINITY;
+        const uint32_t s_col = tmem + lane_base + (uint32_t)(tile * kPBlock + half * kHalf);
         uint32_t s[2][32];
         tmem_ld32_nowait(s_col, s[0]);
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t(&z)[32] = s[c & 1];
-          tmem_wait_ld_tie32(z);
-          if (c < 3) tmem_ld32_nowait(s_col + 32 * (c + 1), s[(c + 1) & 1]);
-          if (MASKED) {
-            const uint32_t see = (uint32_t)(vis[c >> 1] >> (32 * (c & 1)));
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (!((see >> e) & 1u)) z[e] = 0xFF800000u;
+        tmem_ld32_nowait(s_col + 32, s[1]);
+        const float* sc = sScale + (x & 3) * 20;
+        const float4 k4 = *reinterpret_cast<const float4*>(sc + 4 * half), v4 = *reinterpret_cast<const float4*>(sc + 8 + 4 * half);
+        const float v_top = sc[16];
+        const float f[4] = {k4.x * fr, k4.y * fr, k4.z * fr, k4.w * fr};  // the row's factor of 16 keys each
+        uint32_t see[2] = {~0u, ~0u};
+        if (MASKED) {
+          const int valid = u.valid(i) - half * kHalf;
+          see[0] = valid >= 32 ? ~0u : valid > 0 ? (1u << valid) - 1u : 0u;
+          see[1] = valid >= 64 ? ~0u : valid > 32 ? (1u << (valid - 32)) - 1u : 0u;
+          if (u.j + i >= u.nmain) {
+            const uint32_t* m = anc + 4 * (u.j + i - u.nmain) + 2 * half;
+            see[0] &= m[0];
+            see[1] &= m[1];
           }
+        }
+        tmem_wait_ld_tie32(s[0]);
+        reg_tie32(s[1]);
+        if (MASKED) {
 #pragma unroll
-          for (int q = 0; q < 32; q += 16) {
-            float b0 = fmaxf(__uint_as_float(z[q]), __uint_as_float(z[q + 1]));
-            float b1 = fmaxf(__uint_as_float(z[q + 2]), __uint_as_float(z[q + 3]));
+          for (int e = 0; e < 64; ++e)
+            if (!((see[e >> 5] >> (e & 31)) & 1u)) s[e >> 5][e & 31] = 0xFF800000u;
+        }
+        float hmax = -INFINITY;
 #pragma unroll
-            for (int e = q + 4; e < q + 16; e += 4) {
-              b0 = fmax3(b0, __uint_as_float(z[e]), __uint_as_float(z[e + 1]));
-              b1 = fmax3(b1, __uint_as_float(z[e + 2]), __uint_as_float(z[e + 3]));
-            }
-            hmax = fmaxf(hmax, fmaxf(b0, b1) * (sc[2 * c + (q >> 4)] * fr));
+        for (int q = 0; q < 4; ++q) {
+          const uint32_t* z = &s[q >> 1][(q & 1) * 16];
+          float b0 = fmaxf(__uint_as_float(z[0]), __uint_as_float(z[1]));
+          float b1 = fmaxf(__uint_as_float(z[2]), __uint_as_float(z[3]));
+#pragma unroll
+          for (int e = 4; e < 16; e += 4) {
+            b0 = fmax3(b0, __uint_as_float(z[e]), __uint_as_float(z[e + 1]));
+            b1 = fmax3(b1, __uint_as_float(z[e + 2]), __uint_as_float(z[e + 3]));
           }
+          hmax = fmaxf(hmax, fmaxf(b0, b1) * f[q]);
         }
         float alpha = 1.f;
         if (hmax > m_ref + kWThreshold) {
@@ -558,14 +623,13 @@ __global__ void __launch_bounds__(kWThreads, 1)
           m_ref = hmax;
         }
         l *= alpha;
-        const float v_top = sc[16];
         if (v_top > v_ref) {  // the same in every thread
           alpha *= v_ref / v_top;
           v_ref = v_top;
           to_v = 128.f / v_top;
         }
-        if (i > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
-          TSV_PWAIT(&pv_done[tile], cnt[tile] + i - 1);
+        if (h > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+          TSV_PWAIT(&pv_done[tile], 2 * cnt[tile] + h - 1);
           tc_fence_after();
 #pragma unroll 1
           for (int cc = 0; cc < D; cc += 16) {
@@ -580,48 +644,40 @@ __global__ void __launch_bounds__(kWThreads, 1)
         const float neg_ref = m_ref == -INFINITY ? 0.f : -m_ref;
         const uint64_t ref2 = f2_pack(neg_ref, neg_ref);
         uint64_t sum[2] = {0ull, 0ull};
-        // P from the last keys to the first over the upper half of S, two keys a
-        // column: what a store overwrites has been read.
+        const float fv[4] = {v4.x * to_v, v4.y * to_v, v4.z * to_v, v4.w * to_v};
 #pragma unroll
-        for (int c = 3; c >= 0; --c) {
-          uint32_t(&z)[32] = s[c & 1];
-          if (c < 2) tmem_wait_ld_tie32(z);
-          if (c == 1) tmem_ld32_nowait(s_col, s[0]);
-          const uint32_t see = MASKED ? (uint32_t)(vis[c >> 1] >> (32 * (c & 1))) : 0u;
-          const float2 k2 = *reinterpret_cast<const float2*>(sc + 2 * c), v2 = *reinterpret_cast<const float2*>(sc + 8 + 2 * c);
-          const float f0 = k2.x * fr, f1 = k2.y * fr, fv0 = v2.x * to_v, fv1 = v2.y * to_v;
-          uint32_t h[16];
+        for (int c = 0; c < 2; ++c) {
+          uint32_t p[16];
 #pragma unroll
           for (int e = 0; e < 32; e += 2) {
-            const float f = e < 16 ? f0 : f1, fv = e < 16 ? fv0 : fv1;
-            const uint64_t x2 = ffma2((uint64_t)z[e] | ((uint64_t)z[e + 1] << 32), f2_pack(f, f), ref2);
+            const int q = 2 * c + (e >> 4);
+            const uint64_t x2 = ffma2((uint64_t)s[c][e] | ((uint64_t)s[c][e + 1] << 32), f2_pack(f[q], f[q]), ref2);
             float p0 = fast_exp2(f2_lo(x2)), p1 = fast_exp2(f2_hi(x2));
             if (MASKED) {
-              if (!((see >> e) & 1u)) p0 = 0.f;
-              if (!((see >> (e + 1)) & 1u)) p1 = 0.f;
+              if (!((see[c] >> e) & 1u)) p0 = 0.f;
+              if (!((see[c] >> (e + 1)) & 1u)) p1 = 0.f;
             }
             const uint64_t p2 = f2_pack(p0, p1);
             sum[(e >> 1) & 1] = fadd2(sum[(e >> 1) & 1], p2);
-            const uint64_t y2 = fmul2(p2, f2_pack(fv, fv));
-            h[e >> 1] = pack_f16x2(f2_lo(y2), f2_hi(y2));
+            const uint64_t y2 = fmul2(p2, f2_pack(fv[q], fv[q]));
+            p[e >> 1] = pack_f16x2(f2_lo(y2), f2_hi(y2));
           }
-          tmem_st16u_nowait(s_col + kPBlock / 2 + 16 * c, h);
-          if (c == 3) tmem_ld32_nowait(s_col + 32, s[1]);
+          tmem_st16u_nowait(s_col + 16 * c, p);
         }
         tmem_wait_st();
         const uint64_t both = fadd2(sum[0], sum[1]);
         l += f2_lo(both) + f2_hi(both);
         tc_fence_before();
-        parrive(&p_full[tile], dead);
+        parrive(&p_full[2 * tile + half], dead);
       };
       // Blocks of 128 prefix keys need no mask.
       const int whole_main = max(0, min(u.blocks, u.P / kPBlock - u.j));
       if (active) {
 #pragma unroll 1
-        for (int i = 0; i < whole_main; ++i) block_step(i, std::false_type{});
+        for (int h = 0; h < 2 * whole_main; ++h) half_step(h, std::false_type{});
 #pragma unroll 1
-        for (int i = whole_main; i < u.blocks; ++i) block_step(i, std::true_type{});
-        TSV_PWAIT(&pv_done[tile], cnt[tile] + u.blocks - 1);
+        for (int h = 2 * whole_main; h < 2 * u.blocks; ++h) half_step(h, std::true_type{});
+        TSV_PWAIT(&pv_done[tile], 2 * (cnt[tile] + u.blocks) - 1);
       }
       const bool stop = named_bar_or(kBarWSoft, 256, dead);  // the same in every softmax thread
       if (!stop) {
@@ -696,92 +752,53 @@ __global__ void __launch_bounds__(kWThreads, 1)
           }
         }
         if (!whole) {
-          // CTAs cf .. cl share the group; the last to arrive joins.
-          const int64_t W = sRange[2], ctas = sRange[3], gx = sUnit->gx;
-          const int cf = (int)(((gx + 1) * ctas - 1) / W), cl = (int)(((gx + sUnit->T) * ctas - 1) / W);
+          // The last CTA of the group to arrive joins.
+          const Group z = group();
           named_bar_sync(kBarWSoft, 256);
           if (tid == 0) {
-            const int before = atom_add_acq_rel_gpu(counters + cf, 1);
-            const bool last = before == cl - cf;
-            if (last) counters[cf] = 0;
+            const int before = atom_add_acq_rel_gpu(counters + z.cf, 1);
+            const bool last = before == z.parts - 1;
+            if (last) counters[z.cf] = 0;
             *sJoin = last ? 1 : 0;
           }
           named_bar_sync(kBarWSoft, 256);
           if (*sJoin) {
-            const int first_slot = (int64_t)cf * W / ctas >= gx ? 0 : 1;  // the group is its first unit, or its last
-            // Weights of the parts of every row (a thread each), then the rows,
-            // 16 bytes at a time: four of a thread with six parts each in flight.
-            float* weight = reinterpret_cast<float*>(smem);  // [part][row]
-            const int parts = cl - cf + 1;
-            auto slot_of = [&](int c) { return (int64_t)(2 * (cf + c) + (c == 0 ? first_slot : 0)); };
+            // Weights of the parts of every row (a thread each); the rows follow.
             if (tid < u.rows) {
               float top = -INFINITY, all = 0.f;
 #pragma unroll 4
-              for (int c = 0; c < parts; ++c) top = fmaxf(top, __ldcg(part_ml + slot_of(c) * 2 * kWRows + tid));
+              for (int c = 0; c < z.parts; ++c) top = fmaxf(top, __ldcg(part_ml + z.slot(c) * 2 * kWRows + tid));
 #pragma unroll 4
-              for (int c = 0; c < parts; ++c) {
-                const float* ml = part_ml + slot_of(c) * 2 * kWRows + tid;
+              for (int c = 0; c < z.parts; ++c) {
+                const float* ml = part_ml + z.slot(c) * 2 * kWRows + tid;
                 const float m = __ldcg(ml), w = m == -INFINITY ? 0.f : fast_exp2(m - top);
                 all += w * __ldcg(ml + kWRows);
                 weight[c * kWRows + tid] = w;
               }
               const float scale = all == 0.f ? 0.f : 1.f / all;
-              for (int c = 0; c < parts; ++c) weight[c * kWRows + tid] *= scale;
-            }
-            named_bar_sync(kBarWSoft, 256);
-            constexpr int kItems = 4, kParts = 6, L4 = D / 4;
-            for (int i0 = tid; i0 < u.rows * L4; i0 += kItems * 256) {
-              float4 o[kItems];
-#pragma unroll
-              for (int x = 0; x < kItems; ++x) o[x] = make_float4(0.f, 0.f, 0.f, 0.f);
-              for (int c0 = 0; c0 < parts; c0 += kParts) {
-                float4 v[kParts][kItems];
-#pragma unroll
-                for (int c = 0; c < kParts; ++c)
-#pragma unroll
-                  for (int x = 0; x < kItems; ++x) {
-                    const int i = i0 + x * 256;
-                    v[c][x] = make_float4(0.f, 0.f, 0.f, 0.f);
-                    if (c0 + c < parts && i < u.rows * L4)
-                      v[c][x] = __ldcg(reinterpret_cast<const float4*>(part_o + slot_of(c0 + c) * kWRows * D) + i);
-                  }
-#pragma unroll
-                for (int c = 0; c < kParts; ++c)
-#pragma unroll
-                  for (int x = 0; x < kItems; ++x) {
-                    const int i = i0 + x * 256;
-                    if (c0 + c >= parts || i >= u.rows * L4) continue;
-                    const float w = weight[(c0 + c) * kWRows + i / L4];
-                    o[x].x += w * v[c][x].x;
-                    o[x].y += w * v[c][x].y;
-                    o[x].z += w * v[c][x].z;
-                    o[x].w += w * v[c][x].w;
-                  }
-              }
-#pragma unroll
-              for (int x = 0; x < kItems; ++x) {
-                const int i = i0 + x * 256;
-                if (i < u.rows * L4)
-                  *reinterpret_cast<uint2*>(out + (int64_t)sRow[i / L4] * D + (i % L4) * 4) =
-                      make_uint2(pack_bf16x2(o[x].x, o[x].y), pack_bf16x2(o[x].z, o[x].w));
-              }
+              for (int c = 0; c < z.parts; ++c) weight[c * kWRows + tid] *= scale;
             }
           }
         }
+      }
+      if (!sUnit->whole()) {
+        named_bar_sync(kBarWJoin, 512);
+        if (*sJoin) join(tid);
       }
       end(u);
       if (tid == 0) {
         PUnit next = *sUnit;
         list.next(next);
         *sUnit = next;
+        *sJoin = 0;
       }
     }
   }
-  if (warp == kWMmaWarp) {
+  if (warp == kWMmaWarp || warp == kWMmaWarp + 1) {
     if (elect_one()) umma_commit(mma_done);  // every MMA has finished before TMEM is freed
     __syncwarp();
     mbar_wait(mma_done, 0, nullptr);
-  } else if (warp == kWMmaWarp + 1) {
+  } else if (warp == kWMmaWarp + 2) {
     // Every request's lengths and page ids are checked by one CTA.
     for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
       PagedRequest r;
