@@ -317,7 +317,8 @@ cudaError_t paged_attention_set_attributes(int32_t D, int32_t R);
 cudaError_t launch_paged_attention(const CUtensorMap& tk, const CUtensorMap& tv, const PagedAttnArgs& a, int32_t R, int grid,
                                    void* ws, cudaStream_t st);
 cudaError_t paged_attention_wide_set_attributes(int32_t D);
-cudaError_t launch_paged_attention_wide(const PagedAttnArgs& a, int grid, void* ws, cudaStream_t st);
+cudaError_t launch_paged_attention_wide(const CUtensorMap& tk, const CUtensorMap& tv, const PagedAttnArgs& a, int num_sms, void* ws,
+                                        cudaStream_t st);
 cudaError_t launch_paged_attention_simt(const PagedAttnArgs& a, bool bf16, cudaStream_t st);
 
 }  // namespace tsv

@@ -289,11 +289,11 @@ tsv_status tsv_paged_tree_attention(tsv_handle h, tsv_dtype dtype, const void* q
         return TSV_ERR_CUDA;
       h->paged_attr_mask |= bit;
     }
-    if (wide) return cuda_status(launch_paged_attention_wide(a, h->num_sms, workspace_d, static_cast<cudaStream_t>(stream)));
     CUtensorMap tk, tv;
     st = encode_pages(h, &tk, a.cache.k_d, a.cache);
     if (st == TSV_OK) st = encode_pages(h, &tv, a.cache.v_d, a.cache);
     if (st != TSV_OK) return st;
+    if (wide) return cuda_status(launch_paged_attention_wide(tk, tv, a, h->num_sms, workspace_d, static_cast<cudaStream_t>(stream)));
     return cuda_status(launch_paged_attention(tk, tv, a, R, h->num_sms, workspace_d, static_cast<cudaStream_t>(stream)));
   }
   return cuda_status(launch_paged_attention_simt(a, dtype == TSV_BF16, static_cast<cudaStream_t>(stream)));

@@ -22,14 +22,14 @@
 //   0-7    softmax: warps 0-3 tile 0, 4-7 tile 1; a thread owns a row.  The
 //          reference maximum moves only when a score passes it by 2^8, and with
 //          it the row of O in TMEM.
-//   8-15   widening: K and V codes go from global memory into registers a block
-//          ahead (a page row is 128 or 64 contiguous bytes, whatever the
-//          strides around it), and from there as fp16 into the swizzled tiles:
-//          TMA would bring them no closer than a second pass through shared
-//          memory, which Q (64 KB) and the two fp16 rings (128 KB) leave no
-//          room for.
-//   16     MMA issuer: PV_0(j), S_0(j+1), PV_1(j), S_1(j+1): one tile's softmax
-//          runs under the other's products.
+//   8-15   widening: a block's codes lie in the upper half of the tile that
+//          takes them as fp16 (Q and the two fp16 rings leave no room beside
+//          them): everyone reads his part into registers, then writes.
+//   16, 17 MMA issuers, one per tile.  S comes in halves of 64 keys, two
+//          buffers a tile: PV of one half, then S of the half a block on, which
+//          runs under the softmax of the half between them.
+//   18, 19 producers of K and of V: a page's rows of the head are one TMA box,
+//          asked for a block ahead of their tile's release through L2.
 // Bound: the tensor cores (four 128^3 products a block of 256 rows) and, close
 // behind, the exponentials.
 //
@@ -53,7 +53,7 @@ static_assert(256 * kWSoftRegs + 256 * kWConvRegs + 128 * kWRestRegs <= kWThread
 constexpr int kWRows = kPagedWideRows, kWTile = 128;
 constexpr float kWThreshold = 8.f;  // log2: how far a score may pass the reference maximum
 constexpr int kHalf = 64;  // keys of a softmax step
-constexpr int kBarWSoft = 1, kBarWJoin = 2;
+constexpr int kBarWSoft = 1, kBarWJoin = 2, kBarWConv = 3;
 
 template <int D>
 struct WCfg {
@@ -73,8 +73,8 @@ struct WCfg {
   static constexpr int kOffUnit = kOffNan + 32;                      // PUnit
   static constexpr int kOffFirst = kOffUnit + 64;                    // PUnit, then i64 [4]
   static constexpr int kOffBar = kOffFirst + 96;
-  // k_full[2], k_empty[2], v_full[2], v_empty[2], sc_full[4], s_full[4], p_full[4], pv_done[2], mma_done
-  static constexpr int kBars = 23;
+  // k_full[2], k_empty[2], v_full[2], v_empty[2], sc_full[4], s_full[4], p_full[4], pv_done[2], mma_done, kc_full[2], vc_full[2]
+  static constexpr int kBars = 27;
   static constexpr int kOffMisc = kOffBar + 8 * kBars + 8;
   static constexpr int kSmem = kOffMisc + 32 + 1024;
   static constexpr uint32_t kColO = 2 * kPBlock;  // S0 | S1 | O0 | O1
@@ -112,19 +112,8 @@ __device__ __forceinline__ void umma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, ui
       : "memory");
 }
 
-// 16 bytes at p, or zeros: no branch, so that several are in flight.
-__device__ __forceinline__ uint4 load_if(const uint8_t* p, bool on) {
-  uint4 v = make_uint4(0u, 0u, 0u, 0u);
-  asm volatile(
-      "{\n\t.reg .pred q;\n\t"
-      "setp.ne.b32 q, %5, 0;\n\t"
-      "@q ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];\n\t}\n"
-      : "+r"(v.x), "+r"(v.y), "+r"(v.z), "+r"(v.w)
-      : "l"(p), "r"((uint32_t)on));
-  return v;
-}
-
-// The same of a partial (through L2: another CTA wrote it).
+// 16 bytes of a partial (through L2: another CTA wrote it), or zeros: no branch,
+// so that several are in flight.
 __device__ __forceinline__ float4 load_part(const float* p, bool on) {
   float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
   asm volatile(
@@ -161,7 +150,8 @@ struct WUnit {
 
 template <int D>
 __global__ void __launch_bounds__(kWThreads, 1)
-    paged_attn_wide_kernel(const __grid_constant__ PagedAttnArgs a, int32_t* __restrict__ counters, float* __restrict__ part_o,
+    paged_attn_wide_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
+                           const __grid_constant__ PagedAttnArgs a, int32_t* __restrict__ counters, float* __restrict__ part_o,
                            float* __restrict__ part_ml) {
   using C = WCfg<D>;
   extern __shared__ uint8_t smem_raw[];
@@ -188,13 +178,15 @@ __global__ void __launch_bounds__(kWThreads, 1)
   uint64_t* p_full = s_full + 4;    // [tile][half]
   uint64_t* pv_done = p_full + 4;   // [tile]
   uint64_t* mma_done = pv_done + 2;
+  uint64_t* kc_full = mma_done + 1;  // a block's codes are in
+  uint64_t* vc_full = kc_full + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
   int* abort_flag = reinterpret_cast<int*>(smem + C::kOffMisc + 4);
   int* sJoin = reinterpret_cast<int*>(smem + C::kOffMisc + 8);
   volatile int* abort_v = abort_flag;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int lps = __ffs(a.cache.page_size) - 1;
+  const int lps = __ffs(a.cache.page_size) - 1;  // pages are powers of two
   const bool tree = a.tree_table.ids_d != nullptr;
   bool dead = false;
 
@@ -205,6 +197,8 @@ __global__ void __launch_bounds__(kWThreads, 1)
       mbar_init(&v_full[s], 8);
       mbar_init(&v_empty[s], 2);
       mbar_init(&pv_done[s], 1);
+      mbar_init(&kc_full[s], 1);
+      mbar_init(&vc_full[s], 1);
     }
     for (int s = 0; s < 4; ++s) {
       mbar_init(&sc_full[s], 1);
@@ -332,40 +326,30 @@ __global__ void __launch_bounds__(kWThreads, 1)
       // Eight lanes take four 16-code chunks of two rows: their stores meet 32 banks.
       const int chunk = D == 128 ? (ct & 3) | ((ct >> 1) & 4) : ct & 3;
       const int first_row = D == 128 ? ((ct >> 2) & 1) | ((ct >> 4) << 1) : ct >> 2;
-      uint4 kb[kParts], vb[kParts];
-      float sk = 0.f, sv = 0.f;  // warp 0, lanes 0 .. 7: scales of 16 keys each
-      const int64_t head_at = (int64_t)u.g * c.stride_head + 16 * chunk;
-      // Page ids of the lane's rows of block i (-1: none), a block before the
-      // rows are loaded; warp 0's lanes 0 .. 7: those of 16 keys each.
-      int ids[kParts], sid = -1;
+      // Warp 0, lanes 0 .. 7: pages and scales of 16 keys each, two blocks and one ahead.
+      int sid = -1;
+      float sk = 0.f, sv = 0.f;
       auto look = [&](int i) {
-        const bool main = u.j + i < u.nmain;
-        const int base = u.base(i), valid = u.valid(i);
-        const tsv_page_table& pt = main ? a.table : a.tree_table;
-        const int32_t* list_b = pt.ids_d + (int64_t)sUnit->b * pt.stride;
-#pragma unroll
-        for (int q = 0; q < kParts; ++q) {
-          const int key = first_row + q * kStep;
-          ids[q] = -1;
-          if (key < valid) ids[q] = __ldg(list_b + ((base + key) >> lps));
-        }
         sid = -1;
-        if (w == 0 && lane < 8 && lane * 16 < valid) sid = __ldg(list_b + ((base + lane * 16) >> lps));
+        if (w != 0 || lane >= 8 || lane * 16 >= u.valid(i)) return;
+        const tsv_page_table& pt = u.j + i < u.nmain ? a.table : a.tree_table;
+        sid = __ldg(pt.ids_d + (int64_t)sUnit->b * pt.stride + ((u.base(i) + lane * 16) >> lps));
       };
-      auto load = [&](int i) {
-        const int base = u.base(i);
-#pragma unroll
-        for (int q = 0; q < kParts; ++q) {
-          const int row = (base + first_row + q * kStep) & ((1 << lps) - 1);
-          const bool on = (uint32_t)ids[q] < (uint32_t)c.num_pages;
-          const int64_t at = (int64_t)ids[q] * c.stride_page + (int64_t)row * c.stride_row + head_at;
-          kb[q] = load_if(static_cast<const uint8_t*>(c.k_d) + at, on);
-          vb[q] = load_if(static_cast<const uint8_t*>(c.v_d) + at, on);
-        }
+      auto scales = [&]() {
         sk = sv = 0.f;
         if ((uint32_t)sid < (uint32_t)c.num_pages) {
           sk = __ldg(c.k_scale_d + (int64_t)sid * c.Hkv + u.g);
           sv = __ldg(c.v_scale_d + (int64_t)sid * c.Hkv + u.g);
+        }
+      };
+      // The lane's codes of a block, out of the tile's upper half.
+      auto take = [&](const uint8_t* tile, int valid, uint4 (&codes)[kParts]) {
+#pragma unroll
+        for (int q = 0; q < kParts; ++q) {
+          const int key = first_row + q * kStep;
+          const int at = D == 128 ? key * 128 + ((chunk ^ (key & 7)) << 4) : key * 64 + ((chunk ^ ((key >> 1) & 3)) << 4);
+          codes[q] = make_uint4(0u, 0u, 0u, 0u);
+          if (key < valid) codes[q] = *reinterpret_cast<const uint4*>(tile + C::kTileBytes / 2 + at);
         }
       };
       auto put = [&](uint8_t* tile, int key, const uint4& codes) {
@@ -377,7 +361,7 @@ __global__ void __launch_bounds__(kWThreads, 1)
         *reinterpret_cast<uint4*>(row + (at ^ 16)) = y;
       };
       look(0);
-      load(0);
+      scales();
       if (u.blocks > 1) look(1);
       {
         constexpr int E = D / 32;
@@ -427,8 +411,12 @@ __global__ void __launch_bounds__(kWThreads, 1)
 #pragma unroll 1
       for (int i = 0; i < u.blocks; ++i) {
         const int x = t + i, st = x & 1;
-        if (x >= 2) TSV_PWAIT(&k_empty[st], (x >> 1) - 1);
-        if (__any_sync(0xffffffffu, dead)) break;
+        const int valid = u.valid(i);
+        uint4 codes[kParts];
+        TSV_PWAIT(&kc_full[st], x >> 1);
+        take(sK + st * C::kTileBytes, valid, codes);
+        dead = named_bar_or(kBarWConv, 256, dead);  // everyone has read, or gives up
+        if (dead) break;
         if (w == 0) {
           const float top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(sv)));  // (scales are >= 0)
           if (lane < 8) {
@@ -440,16 +428,20 @@ __global__ void __launch_bounds__(kWThreads, 1)
           if (lane == 0) mbar_arrive(&sc_full[x & 3]);
         }
 #pragma unroll
-        for (int q = 0; q < kParts; ++q) put(sK + st * C::kTileBytes, first_row + q * kStep, kb[q]);
+        for (int q = 0; q < kParts; ++q) put(sK + st * C::kTileBytes, first_row + q * kStep, codes[q]);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&k_full[st]);
-        if (x >= 2) TSV_PWAIT(&v_empty[st], (x >> 1) - 1);
-        if (__any_sync(0xffffffffu, dead)) break;
+        if (i + 1 < u.blocks) scales();
+        if (i + 2 < u.blocks) look(i + 2);
+        TSV_PWAIT(&vc_full[st], x >> 1);
+        take(sV + st * C::kTileBytes, valid, codes);
+        dead = named_bar_or(kBarWConv, 256, dead);
+        if (dead) break;
         if (u.j + i >= u.nmain) {
 #pragma unroll
           for (int q = 0; q < kParts; ++q) {
-            uint32_t* v = reinterpret_cast<uint32_t*>(&vb[q]);
+            uint32_t* v = reinterpret_cast<uint32_t*>(&codes[q]);
             uint32_t any = 0u;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
@@ -462,12 +454,10 @@ __global__ void __launch_bounds__(kWThreads, 1)
           }
         }
 #pragma unroll
-        for (int q = 0; q < kParts; ++q) put(sV + st * C::kTileBytes, first_row + q * kStep, vb[q]);
+        for (int q = 0; q < kParts; ++q) put(sV + st * C::kTileBytes, first_row + q * kStep, codes[q]);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&v_full[st]);
-        if (i + 1 < u.blocks) load(i + 1);
-        if (i + 2 < u.blocks) look(i + 2);
       }
       if (!sUnit->whole()) {
         named_bar_sync(kBarWJoin, 512);
@@ -478,6 +468,7 @@ __global__ void __launch_bounds__(kWThreads, 1)
   } else if (warp >= kWMmaWarp) {
     // ---------------------------------------------------------- issuer
     setmaxnreg_dec<kWRestRegs>();
+    int asked = 0;  // blocks that the producer has asked for
     while (begin(u)) {
       __syncthreads();  // the unit's rows are in
       const int q = warp - kWMmaWarp;  // the issuer's tile
@@ -543,9 +534,46 @@ __global__ void __launch_bounds__(kWThreads, 1)
           }
           __syncwarp();
         }
+      } else if (q >= 2) {
+        // ------------------------------------------------------ producers of K and of V
+        const bool is_v = q == 3;
+        const CUtensorMap* tmap = is_v ? &tmap_v : &tmap_k;
+        uint64_t* full = is_v ? vc_full : kc_full;
+        uint64_t* empty = is_v ? v_empty : k_empty;
+        const uint64_t pol = sUnit->tiles > 1 ? l2_policy_evict_last() : l2_policy_evict_first();
+        // Lane p holds page p of the next block.
+        auto page_of = [&](int i) {
+          if (i >= u.blocks || (lane << lps) >= u.valid(i)) return -1;
+          const tsv_page_table& pt = u.j + i < u.nmain ? a.table : a.tree_table;
+          return __ldg(pt.ids_d + (int64_t)sUnit->b * pt.stride + (u.base(i) >> lps) + lane);
+        };
+        int next = page_of(0);
+#pragma unroll 1
+        for (int i = 0; i < u.blocks; ++i) {
+          const int x = t + i, st = x & 1, ids = next;
+          next = page_of(i + 1);
+          const uint32_t pages = (uint32_t)(u.valid(i) + (1 << lps) - 1) >> lps;
+          if (x >= 2) TSV_PWAIT(&empty[st], (x >> 1) - 1);
+          if (__any_sync(0xffffffffu, dead)) break;
+          const uint32_t at = smem_u32(is_v ? sV : sK) + (uint32_t)(st * C::kTileBytes + C::kTileBytes / 2);
+          const bool lead = elect_one();
+          if (pages > 0 && lead) mbar_expect_tx(&full[st], (pages << lps) * D);
+#pragma unroll 1
+          for (uint32_t p = 0; p < pages; ++p)
+            tma_load_page(at + (p << lps) * D, tmap, smem_u32(&full[st]), (uint32_t)u.g,
+                          (uint32_t)__shfl_sync(0xffffffffu, ids, (int)p), pol, lead);
+          __syncwarp();
+          if (lead) mbar_arrive(&full[st]);
+          if ((uint32_t)next < (uint32_t)a.cache.num_pages) tma_prefetch_4d(tmap, 0, u.g, 0, next);
+          asked = x + 1;
+        }
       }
       end(u);
     }
+    // Every copy has landed before the CTA leaves (whatever the other roles did).
+    if (warp >= kWMmaWarp + 2)
+      for (int x = max(0, asked - 2); x < asked; ++x)
+        mbar_wait(warp == kWMmaWarp + 3 ? &vc_full[x & 1] : &kc_full[x & 1], (x >> 1) & 1, nullptr);
   } else {
     // ---------------------------------------------------------- softmax: a thread owns a row
     setmaxnreg_inc<kWSoftRegs>();
@@ -820,11 +848,11 @@ __global__ void __launch_bounds__(kWThreads, 1)
 }
 
 template <int D>
-cudaError_t launch_typed(const PagedAttnArgs& a, int num_sms, void* ws, cudaStream_t st) {
+cudaError_t launch_typed(const CUtensorMap& tk, const CUtensorMap& tv, const PagedAttnArgs& a, int num_sms, void* ws, cudaStream_t st) {
   const int grid = min(num_sms, kPagedWideCtas);
   char* w = static_cast<char*>(ws);
   const PagedAttnLayout lay = paged_attn_layout(grid, kWRows, D);
-  return launch_pdl(paged_attn_wide_kernel<D>, dim3(grid), dim3(kWThreads), (size_t)WCfg<D>::kSmem, st, 0u, a,
+  return launch_pdl(paged_attn_wide_kernel<D>, dim3(grid), dim3(kWThreads), (size_t)WCfg<D>::kSmem, st, 0u, tk, tv, a,
                     reinterpret_cast<int32_t*>(w), reinterpret_cast<float*>(w + lay.part_o), reinterpret_cast<float*>(w + lay.part_ml));
 }
 
@@ -842,8 +870,9 @@ cudaError_t set_typed() {
 
 cudaError_t paged_attention_wide_set_attributes(int32_t D) { return D == 64 ? set_typed<64>() : set_typed<128>(); }
 
-cudaError_t launch_paged_attention_wide(const PagedAttnArgs& a, int grid, void* ws, cudaStream_t st) {
-  return a.cache.D == 64 ? launch_typed<64>(a, grid, ws, st) : launch_typed<128>(a, grid, ws, st);
+cudaError_t launch_paged_attention_wide(const CUtensorMap& tk, const CUtensorMap& tv, const PagedAttnArgs& a, int num_sms, void* ws,
+                                        cudaStream_t st) {
+  return a.cache.D == 64 ? launch_typed<64>(tk, tv, a, num_sms, ws, st) : launch_typed<128>(tk, tv, a, num_sms, ws, st);
 }
 
 }  // namespace tsv

@@ -41,6 +41,23 @@ __device__ __forceinline__ uint64_t fmul2(uint64_t a, uint64_t b) {
   return d;
 }
 
+// tma_load_4d of one KV head's rows of a page, issued by the lane with `lead`
+// set (the whole warp calls it, so the operands stay uniform).
+__device__ __forceinline__ void tma_load_page(uint32_t dst, const CUtensorMap* tmap, uint32_t bar, uint32_t head, uint32_t page,
+                                              uint64_t policy, bool lead) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "setp.ne.b32 q, %7, 0;\n\t"
+      "@q cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%2, %3, %2, %4}], [%5], %6;\n\t}\n" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(0), "r"(head), "r"(page), "r"(bar), "l"(policy), "r"((uint32_t)lead)
+      : "memory");
+}
+
+__device__ __forceinline__ void mbar_expect_tx(uint64_t* bar, uint32_t bytes) {
+  asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes) : "memory");
+}
+
 // One unit of a CTA's range: blocks j .. j1 - 1 of a (request, KV head, row
 // tile) group of T blocks, nmain of them over prefix rows.  gx is the place of
 // the group's block 0 in the list of all blocks.
