@@ -500,6 +500,174 @@ def test_attention_sink_and_flat_tail(tsv, kind):
     assert (out.double() - want).abs().max().item() <= tol
 
 
+# Many rows per KV head in enough (request, head) pairs: query rows on the TMEM lanes, up to 256 of them a unit.
+WIDE = [  # page, Hq, Hkv, D, head_major, lengths (prefix, nodes)
+    (16, 64, 8, 128, True, [(0, 1), (1, 20), (127, 33), (128, 16), (129, 9), (300, 32), (77, 12), (513, 17)]),
+    (128, 12, 4, 64, True, [(500, 90), (128, 64), (0, 3), (127, 1), (1, 86), (256, 0), (30, 43), (700, 5)]),
+    (32, 32, 32, 128, False, [(70, 256), (33, 1)]),
+    (64, 20, 4, 128, False, [(64 * i, 13 + i) for i in range(8)]),
+    (16, 34, 2, 64, True, [(40 + i, 3 + i % 6) for i in range(16)]),
+    (128, 16, 8, 128, True, [(9000, 40), (20, 129), (1500, 256), (4000, 1)]),
+]
+
+
+def wide_workspace(tsv, b, max_nodes=None):
+    ws = tsv.paged_tree_attention_workspace(b.q, b.cache, len(b.lens), max_nodes or max(n for _, n in b.lens))
+    assert ws.numel() * ws.element_size() > 256 * 2 * 64 * b.D * 4  # 256 rows a part: the kernel that is meant
+    return ws
+
+
+@pytest.mark.parametrize("case", WIDE, ids=lambda c: "-".join(str(x) for x in c[:5]))
+def test_attention_of_many_rows(tsv, case):
+    page, Hq, Hkv, D, head_major, lens = case
+    b = Batch(tsv, np.random.default_rng(page + Hq), lens, Hq, Hkv, D, page, head_major=head_major)
+    ws = wide_workspace(tsv, b)
+    out, st = b.run(tsv, workspace=ws)
+    b.check(out, st, True)
+    again, st = b.run(tsv, workspace=ws)
+    assert torch.equal(again, out) and (st == 0).all()
+
+
+def test_attention_of_many_rows_chain_scale_and_any_scales(tsv):
+    """anc None; a softmax scale of the caller's; page scales that are no powers of two; without a tree; a strided q."""
+    b = Batch(tsv, np.random.default_rng(21), [(50, 40), (0, 7), (140, 1), (1300, 150)], 24, 8, 128, 32, power=False)
+    ws = wide_workspace(tsv, b)
+    out, st = b.run(tsv, anc=False, scale=0.2, workspace=ws)
+    b.check(out, st, True, anc=False, scale=0.2)
+    q = torch.zeros(b.q.shape[0], b.Hq + 3, b.D + 16, dtype=b.q.dtype, device="cuda")
+    q[:, 2:-1, :b.D] = b.q
+    plain, b.q = b.q, q[:, 2:-1, :b.D]
+    again, _ = b.run(tsv, anc=False, scale=0.2, workspace=ws)
+    assert torch.equal(again, out)
+    b.q, b.tree = plain, False
+    out, st = b.run(tsv, workspace=ws)
+    b.check(out, st, True)
+    assert (out[40:47] == 0).all()
+
+
+@pytest.mark.parametrize("long", [0, 6000])
+@pytest.mark.parametrize("D", [64, 128])
+def test_attention_of_many_rows_ignores_what_it_may_not_see(tsv, D, long):
+    """As above, with units that end in one CTA and units that are cut: NaN behind the last rows and in tree rows."""
+    rng = np.random.default_rng(22)
+    lens = [(37 + long, 6), (128, 5), (0, 3), (700, 140)]
+    G, Hkv = 4, 8
+    b = Batch(tsv, rng, lens, G * Hkv, Hkv, D, 16)
+    ws = wide_workspace(tsv, b)
+    clean, st = b.run(tsv, workspace=ws)
+    b.check(clean, st, True)
+    k, v = b.cache.k.view(torch.uint8), b.cache.v.view(torch.uint8)
+    used = torch.zeros(b.cache.num_pages, 16, dtype=torch.bool)
+    for i, (p, n) in enumerate(lens):
+        for t, m in ((b.table[i], p), (b.tree_table[i], n)):
+            for r in range(m):
+                used[t[r // 16], r % 16] = True
+    k[~used.cuda()] = 0x7F
+    v[~used.cuda()] = 0xFF
+    out, st = b.run(tsv, workspace=ws)
+    assert torch.equal(out, clean) and (st == 0).all()
+    # NaN in V: nodes 2 of request 0 and 3, 130 of request 3; in K: node 3 of request 1
+    marks = [(0, 2, 1, 5), (3, 3, 0, D - 1), (3, 130, 7, 33)]
+    for i, node, head, d in marks:
+        v[b.tree_table[i][node // 16], node % 16, head, d] = 0x7F
+    k[b.tree_table[1][0], 3, 0, 7] = 0xFF
+    out, st = b.run(tsv, workspace=ws)
+    want = torch.zeros_like(out, dtype=torch.bool)
+    for i, node, head, d in marks:
+        for x in range(lens[i][1]):
+            if b.sees[b.offs[i] + x, node]:
+                want[b.offs[i] + x, G * head:G * (head + 1), d] = True
+    for x in range(5):
+        if b.sees[6 + x, 3]:
+            want[6 + x, 0:G] = True
+    assert torch.equal(torch.isnan(out), want)
+    assert torch.equal(out[~want], clean[~want])
+    v[b.table[1][0], 0, 0, 1] = 0x7F  # in a prefix row: every node of the request, the heads that share it
+    out, _ = b.run(tsv, workspace=ws)
+    assert torch.isnan(out[6:11, 0:G, 1]).all() and not torch.isnan(out[11:14]).any()
+
+
+def test_attention_of_many_rows_extreme_scores(tsv):
+    """Rows whose scores reach thousands of either sign, rows of zeros, of tiny values and of infinities, and V scales that
+    differ by 2^24 from page to page: rows do not touch each other."""
+    rng = np.random.default_rng(23)
+    lens = [(700, 4), (260, 20), (0, 17), (1100, 30)]
+    b = Batch(tsv, rng, lens, 64, 8, 128, 32)
+    pages = torch.arange(b.cache.num_pages, device="cuda")
+    b.cache.v_scale.mul_((2.0 ** ((pages * 7) % 25 - 24.0)).unsqueeze(1))
+    b.q[0] *= 60.0
+    b.q[1] = 0.0
+    b.q[2] *= 1e-6
+    b.q[30] *= 1e-30
+    ws = wide_workspace(tsv, b)
+    out, st = b.run(tsv, workspace=ws)
+    ref, spread, size = R.attention(b.q.double().cpu().numpy(), values(b.cache), b.table, b.prefix, b.offs, b.tree_table, b.sees)
+    tol = _attention_bound(ref, spread, size, b.q.dtype, 1130, 128, True)
+    assert (np.abs(out.double().cpu().numpy() - ref) <= tol).all()
+    b.q[3] = math.inf
+    b.q[45] = math.nan
+    out2, _ = b.run(tsv, workspace=ws)
+    keep = [i for i in range(71) if i not in (3, 45)]
+    assert torch.equal(out2[keep], out[keep]) and torch.isnan(out2[3]).all() and torch.isnan(out2[45]).all()
+
+
+def test_attention_of_many_rows_sink_and_flat_tail(tsv):
+    """Weights 8192 : 6000 again, for every row."""
+    b = Batch(tsv, np.random.default_rng(24), [(6001, 12)], 256, 32, 64, 128, tree=False)
+    k, v = b.cache.k.view(torch.uint8), b.cache.v.view(torch.uint8)
+    k.zero_()
+    v.fill_(0x38)  # 1.0
+    b.cache.k_scale.fill_(1.0)
+    b.cache.v_scale.fill_(1.0)
+    k[b.table[0][3], 77, :, 0] = 0x38
+    v[b.table[0][3], 77] = 0xB8  # -1.0
+    b.q.zero_()
+    b.q[:, :, 0] = 13 * math.log(2.0)
+    out, _ = b.run(tsv, scale=1.0, workspace=wide_workspace(tsv, b))
+    w = math.exp(float(b.q[0, 0, 0].double()))
+    want = (6000 - w) / (6000 + w)
+    tol = 2.0 ** -8 * 1.01 + HALF_STEP[torch.bfloat16] * abs(want)
+    assert (out.double() - want).abs().max().item() <= tol
+
+
+def test_attention_of_many_rows_follows_the_lengths(tsv):
+    """A captured call replayed with other lengths on the device, a request rejected, outputs of rejected rows left."""
+    b = Batch(tsv, np.random.default_rng(25), [(500, 40), (900, 30), (100, 17), (64, 33)], 32, 8, 128, 64)
+    ws = wide_workspace(tsv, b)
+    q, table, tree, anc = b.q, dev(b.table), dev(b.tree_table), dev(b.words)
+    prefix, offs = i32(b.prefix), i32(b.offs)
+    out, st = torch.empty_like(q), torch.empty(4, dtype=torch.int32, device="cuda")
+
+    def call(o, s, w):
+        tsv.paged_tree_attention(q, b.cache, table, prefix, offs, tree_table=tree, anc=anc, max_nodes=40, out=o, status=s, workspace=w)
+
+    call(out, st, ws)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call(out, st, ws)
+    for lens in ([500, 900, 100, 64], [3, 900, 0, 1], [499, 128, 99, 64], [512, 0, 64, -1]):
+        prefix.copy_(i32(lens))
+        out.fill_(7.0)
+        graph.replay()
+        other, st2 = torch.full_like(out, 7.0), torch.empty_like(st)
+        call(other, st2, wide_workspace(tsv, b))
+        assert torch.equal(out, other) and torch.equal(st, st2)
+        assert st.tolist() == [0, 0, 0, 1 if lens[3] < 0 else 0]
+        if lens[3] < 0:
+            assert (out[87:] == 7).all()
+
+
+def test_page_tables_beyond_the_limit_are_refused(tsv):
+    b = Batch(tsv, np.random.default_rng(26), [(16, 2)], 2, 2, 64, 16)
+    b.table = np.zeros((1, 1), np.int32)
+    big = torch.empty((1, (1 << 26) + 1), dtype=torch.int32, device="cuda")
+    with pytest.raises(tsv.TSVError):
+        tsv.paged_tree_attention(b.q, b.cache, big, i32(b.prefix), i32(b.offs), tree_table=dev(b.tree_table), max_nodes=2)
+    with pytest.raises(tsv.TSVError):
+        tsv.paged_append(b.cache, big, b.q, b.q, i32(b.offs))
+
+
 def test_attention_rejects_requests_one_by_one(tsv):
     for flags, dtype in ((0, torch.bfloat16), (1, torch.bfloat16), (0, torch.float32)):
         b = Batch(tsv, np.random.default_rng(14), [(40, 3), (50, 2), (33, 4), (20, 5)], 4, 2, 64, 16, dtype=dtype)

@@ -302,7 +302,20 @@ struct PagedAttnArgs {
 // [R][D], then maxima and sums [2][R]).
 constexpr int32_t kPagedWideRows = 256;
 constexpr int32_t kPagedWideCtas = 160;  // at most: shared memory holds the weights of so many parts
-inline int32_t paged_attn_rows(int64_t rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : kPagedWideRows; }
+// Rows of a unit of the tensor-core kernels: 16, 32, 64 (keys on the TMEM lanes)
+// or 256 (rows on them), of `rows` query rows in each of `groups` (request, KV
+// head) pairs.  More rows share a block's cost, but units that are few are cut
+// into many parts, which costs more the more rows they have.  Measured (us; 64
+// heads on 8 KV heads, D = 128), 32 / 64 / 256 rows a unit:
+//   16 requests x 2048 keys:  40 rows 62 / 48 / 75, 96 rows 88 / 81 / 77, 256 rows 207 / 145 / 103
+//   1 request x 16384 keys:   64 rows 31 / 45 / 53, 256 rows 69 / 66 / 90, 512 rows 121 / 103 / 102
+//   1 request x 1024 keys:    64 rows 18 / 25 / 31, 512 rows 32 / 35 / 50
+inline int32_t paged_attn_rows(int64_t rows, int64_t groups) {
+  if (rows <= 32) return rows <= 16 ? 16 : 32;
+  const int64_t few = 32;
+  if (rows > 64 && groups * ((rows + kPagedWideRows - 1) / kPagedWideRows) >= few) return kPagedWideRows;
+  return groups * ((rows + 63) / 64) >= few ? 64 : 32;
+}
 struct PagedAttnLayout {
   size_t part_o, part_ml, total;
 };

@@ -73,8 +73,8 @@ struct WCfg {
   static constexpr int kOffUnit = kOffNan + 32;                      // PUnit
   static constexpr int kOffFirst = kOffUnit + 64;                    // PUnit, then i64 [4]
   static constexpr int kOffBar = kOffFirst + 96;
-  // k_full[2], k_empty[2], v_full[2], v_empty[2], sc_full[4], s_full[4], p_full[4], pv_done[2], mma_done, kc_full[2], vc_full[2]
-  static constexpr int kBars = 27;
+  // k_full[2], k_empty[2], v_full[2], v_empty[2], sc_full[4], s_full[4], p_full[4], pv_done[4], mma_done, kc_full[2], vc_full[2]
+  static constexpr int kBars = 29;
   static constexpr int kOffMisc = kOffBar + 8 * kBars + 8;
   static constexpr int kSmem = kOffMisc + 32 + 1024;
   static constexpr uint32_t kColO = 2 * kPBlock;  // S0 | S1 | O0 | O1
@@ -176,8 +176,10 @@ __global__ void __launch_bounds__(kWThreads, 1)
   uint64_t* sc_full = v_empty + 2;
   uint64_t* s_full = sc_full + 4;   // [tile][half]
   uint64_t* p_full = s_full + 4;    // [tile][half]
-  uint64_t* pv_done = p_full + 4;   // [tile]
-  uint64_t* mma_done = pv_done + 2;
+  // A wait must be for the current phase or the one just past, so a barrier
+  // whose phases could run two ahead of a waiter is split: here by half.
+  uint64_t* pv_done = p_full + 4;   // [tile][half]
+  uint64_t* mma_done = pv_done + 4;
   uint64_t* kc_full = mma_done + 1;  // a block's codes are in
   uint64_t* vc_full = kc_full + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
@@ -196,7 +198,6 @@ __global__ void __launch_bounds__(kWThreads, 1)
       mbar_init(&k_empty[s], 2);  // both tiles' issuers (the first for both when there is one)
       mbar_init(&v_full[s], 8);
       mbar_init(&v_empty[s], 2);
-      mbar_init(&pv_done[s], 1);
       mbar_init(&kc_full[s], 1);
       mbar_init(&vc_full[s], 1);
     }
@@ -204,6 +205,7 @@ __global__ void __launch_bounds__(kWThreads, 1)
       mbar_init(&sc_full[s], 1);
       mbar_init(&s_full[s], 1);
       mbar_init(&p_full[s], 128);
+      mbar_init(&pv_done[s], 1);
     }
     mbar_init(mma_done, 2);
     *abort_flag = 0;
@@ -462,6 +464,7 @@ __global__ void __launch_bounds__(kWThreads, 1)
       if (!sUnit->whole()) {
         named_bar_sync(kBarWJoin, 512);
         if (*sJoin) join(tid);
+        fence_proxy_async_smem();
       }
       end(u);
     }
@@ -500,7 +503,7 @@ __global__ void __launch_bounds__(kWThreads, 1)
 #pragma unroll
           for (int kk = 0; kk < kHalf / 16; ++kk)
             umma_f16_ts(dst, pa + kk * 8, desc_at(dv, db + ((kk * 16 * 128) >> 4)), idPV, more || kk > 0 ? 1u : 0u, lead);
-          if (lead) umma_commit(&pv_done[tile]);
+          if (lead) umma_commit(&pv_done[2 * tile + half]);
           __syncwarp();
         };
         const int both = u.ntiles == 1 ? 2 : 1;  // arrivals at the rings' barriers
@@ -657,7 +660,7 @@ __global__ void __launch_bounds__(kWThreads, 1)
           to_v = 128.f / v_top;
         }
         if (h > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
-          TSV_PWAIT(&pv_done[tile], 2 * cnt[tile] + h - 1);
+          TSV_PWAIT(&pv_done[2 * tile + (1 - half)], cnt[tile] + ((h - 1) >> 1));
           tc_fence_after();
 #pragma unroll 1
           for (int cc = 0; cc < D; cc += 16) {
@@ -705,7 +708,8 @@ __global__ void __launch_bounds__(kWThreads, 1)
         for (int h = 0; h < 2 * whole_main; ++h) half_step(h, std::false_type{});
 #pragma unroll 1
         for (int h = 2 * whole_main; h < 2 * u.blocks; ++h) half_step(h, std::true_type{});
-        TSV_PWAIT(&pv_done[tile], 2 * (cnt[tile] + u.blocks) - 1);
+        TSV_PWAIT(&pv_done[2 * tile], cnt[tile] + u.blocks - 1);
+        TSV_PWAIT(&pv_done[2 * tile + 1], cnt[tile] + u.blocks - 1);
       }
       const bool stop = named_bar_or(kBarWSoft, 256, dead);  // the same in every softmax thread
       if (!stop) {
@@ -812,6 +816,7 @@ __global__ void __launch_bounds__(kWThreads, 1)
       if (!sUnit->whole()) {
         named_bar_sync(kBarWJoin, 512);
         if (*sJoin) join(tid);
+        fence_proxy_async_smem();  // the next unit's copies come after these accesses of the tiles
       }
       end(u);
       if (tid == 0) {
