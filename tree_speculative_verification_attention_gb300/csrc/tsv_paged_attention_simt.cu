@@ -21,6 +21,7 @@ namespace {
 
 constexpr int kSimtWarps = 8;
 constexpr int kSimtHeads = 8;  // query heads of one pass
+constexpr int kBatch = 8;      // V rows of a warp in flight
 
 template <typename T>
 __device__ __forceinline__ float in_f32(T v);
@@ -121,9 +122,12 @@ __global__ void __launch_bounds__(32 * kSimtWarps) paged_attn_simt_kernel(const 
       for (int h = 0; h < kSimtHeads; ++h) s[h] = 0.f;
       if (see) {
         const uint4* kr = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(C.k_d) + row);
-#pragma unroll 1
+        uint4 kw[D / 16];
+#pragma unroll
+        for (int c = 0; c < D / 16; ++c) kw[c] = kr[c];
+#pragma unroll
         for (int c = 0; c < D / 16; ++c) {
-          const uint4 w = kr[c];
+          const uint4 w = kw[c];
           float f[16];
           e4m3x4_to_f32(w.x, 1.f, f);
           e4m3x4_to_f32(w.y, 1.f, f + 4);
@@ -156,24 +160,35 @@ __global__ void __launch_bounds__(32 * kSimtWarps) paged_attn_simt_kernel(const 
 #pragma unroll
         for (int e = 0; e < E; ++e) o[h][e] *= keep;
       }
-      for (uint32_t left = seen; left; left &= left - 1) {
-        const int src = __ffs(left) - 1;
-        const int64_t vr = __shfl_sync(0xffffffffu, row, src);
-        const uint8_t* vp = static_cast<const uint8_t*>(C.v_d) + vr + lane * E;
-        float f[4];
-        if constexpr (E == 4) {
-          e4m3x4_to_f32(*reinterpret_cast<const uint32_t*>(vp), 1.f, f);
-        } else {
-          const uint32_t two = f16x2_of_e4m3x2(*reinterpret_cast<const uint16_t*>(vp));
-          f[0] = f16_lo(two);
-          f[1] = f16_hi(two);
+      // The rows of V, kBatch in flight (a row that is not seen is not read).
+#pragma unroll 1
+      for (int k1 = 0; k1 < 32; k1 += kBatch) {
+        if (((seen >> k1) & ((1u << kBatch) - 1u)) == 0u) continue;
+        uint32_t vw[kBatch];
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+          const uint8_t* vp = static_cast<const uint8_t*>(C.v_d) + __shfl_sync(0xffffffffu, row, k1 + u) + lane * E;
+          vw[u] = 0u;
+          if ((seen >> (k1 + u)) & 1u)
+            vw[u] = E == 4 ? *reinterpret_cast<const uint32_t*>(vp) : *reinterpret_cast<const uint16_t*>(vp);
         }
 #pragma unroll
-        for (int h = 0; h < kSimtHeads; ++h) {
-          if (h >= heads) break;
-          const float ph = __shfl_sync(0xffffffffu, p[h], src);
+        for (int u = 0; u < kBatch; ++u) {
+          float f[4];
+          if constexpr (E == 4) {
+            e4m3x4_to_f32(vw[u], 1.f, f);
+          } else {
+            const uint32_t two = f16x2_of_e4m3x2(vw[u]);
+            f[0] = f16_lo(two);
+            f[1] = f16_hi(two);
+          }
 #pragma unroll
-          for (int e = 0; e < E; ++e) o[h][e] = fmaf(ph, f[e], o[h][e]);
+          for (int h = 0; h < kSimtHeads; ++h) {
+            if (h >= heads) break;
+            const float ph = __shfl_sync(0xffffffffu, p[h], k1 + u);
+#pragma unroll
+            for (int e = 0; e < E; ++e) o[h][e] = fmaf(ph, f[e], o[h][e]);
+          }
         }
       }
     }
