@@ -3,7 +3,7 @@
 //
 //   out[i,h] = sum_j p_j v_j / sum_j p_j,  p_j = exp(scale <q[i,h], k_j>)
 //
-// One CTA per (node, KV head): its 8 warps take 32 keys each in turn, a lane
+// One CTA per (node, KV head): its 8 or 16 warps take 32 keys each in turn, a lane
 // per key for the scores (its own K row, the query broadcast from shared
 // memory) and a lane per D / 32 elements for the sums over V, with a running
 // maximum and sum per query head; the warps' partial results are joined in
@@ -19,7 +19,10 @@ namespace tsv {
 
 namespace {
 
-constexpr int kSimtWarps = 8;
+// Warps of a CTA: keys of a node go 32 to a warp, so more warps mean a shorter
+// chain (16 is what the joined results leave room for at D = 64).
+template <int D>
+constexpr int simt_warps() { return D == 64 ? 16 : 8; }
 constexpr int kSimtHeads = 8;  // query heads of one pass
 constexpr int kBatch = 8;      // V rows of a warp in flight
 
@@ -37,7 +40,8 @@ template <>
 __device__ __forceinline__ __nv_bfloat16 out_of_f32<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 
 template <typename T, int D>
-__global__ void __launch_bounds__(32 * kSimtWarps) paged_attn_simt_kernel(const PagedAttnArgs a) {
+__global__ void __launch_bounds__(32 * simt_warps<D>()) paged_attn_simt_kernel(const PagedAttnArgs a) {
+  constexpr int kSimtWarps = simt_warps<D>();
   constexpr int E = D / 32;  // elements of V per lane
   pdl_trigger();
   pdl_wait();
@@ -224,7 +228,7 @@ __global__ void __launch_bounds__(32 * kSimtWarps) paged_attn_simt_kernel(const 
 }  // namespace
 
 cudaError_t launch_paged_attention_simt(const PagedAttnArgs& a, bool bf16, cudaStream_t st) {
-  const dim3 grid(a.N + a.B, a.cache.Hkv), block(32 * kSimtWarps);
+  const dim3 grid(a.N + a.B, a.cache.Hkv), block(32 * (a.cache.D == 64 ? simt_warps<64>() : simt_warps<128>()));
   if (bf16)
     return a.cache.D == 64 ? launch_pdl(paged_attn_simt_kernel<__nv_bfloat16, 64>, grid, block, 0, st, 0u, a)
                            : launch_pdl(paged_attn_simt_kernel<__nv_bfloat16, 128>, grid, block, 0, st, 0u, a);
