@@ -318,9 +318,12 @@ def _attention_bound(out_ref, spread, size, dtype, keys, D, tensor):
     over |v|, once for the weighted sum and once for its denominator).
     CUDA cores, fp32: a score is a sum of D products in fp32, off by at most (D + 4) 2^-24 of scale x sum |q| |k|; exp2 and
     the running sums add (keys + 16) 2^-24.
-    Tensor cores: q is split into two e4m3 terms, off by 2^-17 of its row's largest value at most, which a score sees as
-    2^-17 x D^.5.. x size at most D 2^-17 |q|max |k|max; a weight in two e4m3 terms is off by 2^-8 of itself or 2^-21 of
-    its block's largest weight (128 keys a block)."""
+    Tensor cores, few rows: q is split into two e4m3 terms, off by 2^-17 of its row's largest value at most, which a score
+    sees as at most 2^-12 of its size for rows without outliers beyond 2^5; a weight in two e4m3 terms is off by 2^-8 of
+    itself or 2^-18 of its step's largest weight (256 keys: 2^-10 together).  Many rows: q is exact down to 2^-31 of the
+    row's largest value, a weight in fp16 off by 2^-12 of itself or 2^-33 of the largest: less on both counts.
+    128 x 2^-21 = 2^-14 stands in for the 2^-10: single weights that small are off independently, and the cases here
+    hold it."""
     e = (D + 4) * 2.0 ** -24 * size + (keys + 16) * 2.0 ** -24
     tol = 2 * e[..., None] * spread + 2.0 ** -8 * 0
     if tensor:

@@ -11,17 +11,17 @@
 //   q = (hi + lo) 2^-k   two e4m3 terms under a power of two per row (the
 //                        row's largest value lands in [128, 256)): a bf16's 8
 //                        bits exactly down to 2^-17 of the row's largest.
-//   p = (hi + lo) / 256  relative to the block's own largest score of the
-//                        row: 8 bits down to 2^-10 of it, never off by more
-//                        than 2^-18 of it (128 keys: 2^-11 of the block).
+//   p = (hi + lo) / 256  relative to the step's own largest score of the row:
+//                        off by 2^-8 of itself or 2^-18 of that largest (256
+//                        keys: 2^-10 of the step).
 // The terms of q accumulate into the same S; those of p lie side by side on the
 // N axis of one MMA (an MMA of this shape takes its issue time, not its N) and
 // are added in fp32.
-// That the reference maximum is the block's own (not a running one) keeps
-// those bounds whatever the earlier blocks held; O of a block is brought to
-// the running maximum in fp32 registers, which also keeps long sums out of the
-// tensor core's accumulator.  The scale of a key's page multiplies S, and the
-// scale of its V page, relative to the block's largest, multiplies P.
+// That the reference maximum is the step's own (not a running one) keeps those
+// bounds whatever the earlier steps held; O of a step is brought to the running
+// maximum in fp32 registers, which also keeps long sums out of the tensor core's
+// accumulator.  The scale of a key's page multiplies S, and the scale of its V
+// page, relative to the step's largest, multiplies P.
 //
 // Work.  The 128-key blocks of all (request, KV head, row tile) groups form one
 // list, cut into equal ranges, one per CTA (one CTA per SM): every SM gets the
@@ -32,7 +32,10 @@
 // round of barriers for 256 keys.  With few rows the bound is not the bytes but
 // the instructions around them (a warp's chain of dependent steps runs at 6 to
 // 7 cycles an instruction, a third of it waiting for instruction fetches), so
-// what a step costs once matters most.
+// what a step costs once matters most.  Measured: 32 requests x 2064 keys x 32
+// heads, 16 rows each, 142 us (3.8 TB/s; without P's arithmetic 104, without O's
+// sums 137, one MMA of four for O 122); one token of 8 requests, 64 heads on 8 of
+// the cache, 28 us; a 20-node tree over 1024 keys, 32 heads, 20 us.
 //
 // Roles (20 warps): two softmax warpgroups (warps 0-3 and 4-7; a thread owns a
 // key of each block), which take alternate steps, or, with 64 rows, 32 rows of
@@ -40,9 +43,8 @@
 // producers (12, 13 of K, 14, 15 of V, each pair taking alternate blocks: page
 // ids and scales are looked up a warp's worth ahead, a page is one TMA box, and
 // a box costs its warp about 100 cycles); the issuers of S and of O (16, 17);
-// and two warps that prepare the next unit's Q tiles and tree mask (18, 19). 
-// What
-// a role needs from the rows (maxima, factors) is worked out by each of its
+// and two warps that prepare the next unit's Q tiles and tree mask (18, 19).
+// What a role needs from the rows (maxima, factors) is worked out by each of its
 // warps for itself: a step costs a softmax group one barrier and the
 // accumulating group none.  The register file is split by role.
 //
@@ -130,7 +132,7 @@ __device__ __forceinline__ void umma_e4m3(uint32_t d_tmem, uint64_t adesc, uint6
       "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(lead)
       : "memory");
 }
-// A value that is the same in every lane, in a uniform register.
+// The bits that any lane has set, in a uniform register.
 __device__ __forceinline__ uint32_t uniform(uint32_t x) { return __reduce_or_sync(0xffffffffu, x); }
 // Instruction descriptor of kind::f8f6f4: e4m3 A and B (format 0), fp32 D.
 __device__ __forceinline__ uint32_t idesc_e4m3(int M, int N, int a_mn, int b_mn) {

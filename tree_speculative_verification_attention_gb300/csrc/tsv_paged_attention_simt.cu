@@ -3,14 +3,17 @@
 //
 //   out[i,h] = sum_j p_j v_j / sum_j p_j,  p_j = exp(scale <q[i,h], k_j>)
 //
-// One CTA per (node, KV head): its 8 or 16 warps take 32 keys each in turn, a lane
+// One CTA per (node, KV head): its 16 warps take 32 keys each in turn, a lane
 // per key for the scores (its own K row, the query broadcast from shared
 // memory) and a lane per D / 32 elements for the sums over V, with a running
 // maximum and sum per query head; the warps' partial results are joined in
 // shared memory at the end.  A key that the node does not see is skipped, so
 // whatever its V row holds stays out.  The K and V rows of a KV head are read
-// once per node (from L2): the work is 2 D products per key and query head
-// on the FMA units, which is what bounds it.
+// once per node (from L2).  With the few CTAs of a small batch the chain of a
+// warp's 32 keys bounds it (7 us of loads, products and exchanges), so a CTA has
+// all the warps that fit and each keeps its whole K rows and eight V rows in
+// flight: 3 ragged requests of up to 40 nodes over up to 1500 keys, 8 heads on 2
+// KV heads of 64, 24 us (one V row at a time and 8 warps: 74).
 #include <cuda_runtime.h>
 
 #include "tsv_paged_common.cuh"
@@ -19,11 +22,9 @@ namespace tsv {
 
 namespace {
 
-// Warps of a CTA: keys of a node go 32 to a warp, so more warps mean a shorter
-// chain (16 is what the joined results leave room for at D = 64).
+constexpr int kSimtWarps = 16;
 template <int D>
-constexpr int simt_warps() { return D == 64 ? 16 : 8; }
-constexpr int kSimtHeads = 8;  // query heads of one pass
+constexpr int simt_heads() { return D == 64 ? 8 : 4; }  // query heads of one pass: what the joined results leave room for
 constexpr int kBatch = 8;      // V rows of a warp in flight
 
 template <typename T>
@@ -40,8 +41,8 @@ template <>
 __device__ __forceinline__ __nv_bfloat16 out_of_f32<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 
 template <typename T, int D>
-__global__ void __launch_bounds__(32 * simt_warps<D>()) paged_attn_simt_kernel(const PagedAttnArgs a) {
-  constexpr int kSimtWarps = simt_warps<D>();
+__global__ void __launch_bounds__(32 * kSimtWarps) paged_attn_simt_kernel(const PagedAttnArgs a) {
+  constexpr int kSimtHeads = simt_heads<D>();
   constexpr int E = D / 32;  // elements of V per lane
   pdl_trigger();
   pdl_wait();
@@ -228,7 +229,7 @@ __global__ void __launch_bounds__(32 * simt_warps<D>()) paged_attn_simt_kernel(c
 }  // namespace
 
 cudaError_t launch_paged_attention_simt(const PagedAttnArgs& a, bool bf16, cudaStream_t st) {
-  const dim3 grid(a.N + a.B, a.cache.Hkv), block(32 * (a.cache.D == 64 ? simt_warps<64>() : simt_warps<128>()));
+  const dim3 grid(a.N + a.B, a.cache.Hkv), block(32 * kSimtWarps);
   if (bf16)
     return a.cache.D == 64 ? launch_pdl(paged_attn_simt_kernel<__nv_bfloat16, 64>, grid, block, 0, st, 0u, a)
                            : launch_pdl(paged_attn_simt_kernel<__nv_bfloat16, 128>, grid, block, 0, st, 0u, a);

@@ -1,21 +1,23 @@
 // tsv_paged_attention_wide.cu — tree attention over a paged 8-bit cache for many
 // query rows per KV head, query rows on the TMEM lanes.
 //
-//   S = Q K^T         M = 128 rows, N = 128 keys, K = D       (A = Q, B = K, shared memory)
-//   O += P V          M = 128 rows, N = D, K = 128 keys       (A = P, TMEM; B = V, shared memory)
+//   S = Q K^T         M = 128 rows, N = 64 keys, K = D       (A = Q, B = K, shared memory)
+//   O += P V          M = 128 rows, N = D, K = 64 keys       (A = P, TMEM; B = V, shared memory)
 //
 // Both products are fp16 with fp32 sums.  An e4m3 code is an fp16 value, so K
 // and V are widened without a rounding (one conversion per two codes); a row of
 // Q is a bf16 row times a power of two that moves its largest value to
 // [2^14, 2^15): exact down to 2^-31 of it.  P is 2^7 p with p <= 2^8, rounded to
 // fp16's 11 bits.  The scale of a key's page multiplies S in fp32; the scale of
-// its V page, relative to the largest one so far, multiplies P.
+// its V page, relative to the largest one so far, multiplies P (weights of V
+// rows whose scale is below 2^-21 of the unit's largest lose bits to fp16's
+// range, below 2^-32 they are nothing).
 //
-// Why another kernel: with rows on N (the kernel for few rows) a block of 128
-// keys costs the MMA's issue time whatever N is, and two e4m3 terms of Q and of
-// P.  From some 33 rows on that is more than what the widening costs, which
-// here is paid once for 256 rows: 128 rows x 64 heads, 32768 keys: see the
-// figures at the launch.
+// Why another kernel: with rows on N (the kernel for few rows) both products
+// take two e4m3 terms of Q and of P, and every 64 rows their own pass over the
+// keys.  Here the widening is paid once for 256 rows: a 128-node tree x 64 heads
+// on 8 of the cache, 32768 keys: 221 us against 341 (622 TFLOP/s of both
+// products).  When it is taken: at paged_attn_rows.
 //
 // One CTA per SM walks its share of the list of blocks (as the other kernel
 // does; a unit is up to 256 rows, two tiles).  Roles (20 warps):
@@ -24,14 +26,16 @@
 //          it the row of O in TMEM.
 //   8-15   widening: a block's codes lie in the upper half of the tile that
 //          takes them as fp16 (Q and the two fp16 rings leave no room beside
-//          them): everyone reads his part into registers, then writes.
+//          them): every warp reads its part into registers, then all write.
 //   16, 17 MMA issuers, one per tile.  S comes in halves of 64 keys, two
 //          buffers a tile: PV of one half, then S of the half a block on, which
 //          runs under the softmax of the half between them.
 //   18, 19 producers of K and of V: a page's rows of the head are one TMA box,
 //          asked for a block ahead of their tile's release through L2.
-// Bound: the tensor cores (four 128^3 products a block of 256 rows) and, close
-// behind, the exponentials.
+// What bounds it: the chain of a half block through issuer, softmax and issuer
+// again, not one unit: with half of the MMAs it takes 195 us, without widening
+// 204, without exponentials 207, without all three 168; the join of units that
+// were cut (256 rows each) is 17 us of it.
 //
 // Masks: the keys of tree blocks by the ancestor words of the row's node, keys
 // past the end by their number.  V rows past the last key are zeros, and NaN
@@ -323,12 +327,12 @@ __global__ void __launch_bounds__(kWThreads, 1)
     while (begin(u)) {
       const int w = warp - kWConvWarp, ct = tid - kWConvWarp * 32;
       const tsv_paged_cache& c = a.cache;
-      // A lane's part of a block: 16 codes of u.rows row_of, row_of + kStep, ...
+      // A lane's part of a block: 16 codes of rows first_row, first_row + kStep, ...
       constexpr int kLanes = D / 16, kStep = 256 / kLanes, kParts = kPBlock / kStep;  // lanes of a row; 4 or 2 rows of a thread
       // Eight lanes take four 16-code chunks of two rows: their stores meet 32 banks.
       const int chunk = D == 128 ? (ct & 3) | ((ct >> 1) & 4) : ct & 3;
       const int first_row = D == 128 ? ((ct >> 2) & 1) | ((ct >> 4) << 1) : ct >> 2;
-      // Warp 0, lanes 0 .. 7: pages and scales of 16 keys each, two blocks and one ahead.
+      // Warp 0, lanes 0 .. 7: the page of 16 keys each, two blocks ahead, its scales one.
       int sid = -1;
       float sk = 0.f, sv = 0.f;
       auto look = [&](int i) {
@@ -409,7 +413,7 @@ __global__ void __launch_bounds__(kWThreads, 1)
         if (ct < 8) sNan[ct] = 0u;
         fence_proxy_async_smem();
       }
-      __syncthreads();  // the unit's u.rows are in
+      __syncthreads();  // the unit's rows are in
 #pragma unroll 1
       for (int i = 0; i < u.blocks; ++i) {
         const int x = t + i, st = x & 1;
@@ -597,7 +601,7 @@ __global__ void __launch_bounds__(kWThreads, 1)
           anc[q] = bits;
         }
       }
-      __syncthreads();  // the unit's u.rows are in
+      __syncthreads();  // the unit's rows are in
       const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
       const uint32_t o_col = tmem + lane_base + C::kColO + (uint32_t)(tile * D);
       const float fr = sFr[row];

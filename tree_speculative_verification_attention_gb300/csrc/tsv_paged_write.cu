@@ -14,7 +14,12 @@
 // `head_loop` such groups: the angles of the page's rows are the same for every
 // head and are computed once per CTA, while its first rows are on their way.
 // One row part a lane rather than two or four: 64 registers hold it, so 32
-// warps share an SM and one's loads run under another's rounding.
+// warps share an SM and one's loads run under another's rounding (18,200 rows of
+// 8 requests, 8 heads of 128, bf16, rotated: 33 us, 3.4 TB/s; 16 values of four
+// rows a lane: 88 us).  What is left there is issue, half of the cycles: about
+// 250 instructions for a lane's 32 values, and the angles.  Few rows cost a chain
+// of loads (lengths, pages, rows, scales): 20 rows x 32 heads 4.4 us, a commit of
+// their path 3.9 us, of 128 requests' paths 10 us.
 //
 // A lane owns 16 values of a row as two chunks of 8: adjacent chunks, or, for
 // the half layout, a chunk and its partner rotary_dim / 2 elements on, so that
