@@ -503,21 +503,26 @@ def test_attention_sink_and_flat_tail(tsv, kind):
     assert (out.double() - want).abs().max().item() <= tol
 
 
-# Many rows per KV head in enough (request, head) pairs: query rows on the TMEM lanes, up to 256 of them a unit.
+# Many rows per KV head over many keys: query rows on the TMEM lanes, up to 256 of them a unit.
 WIDE = [  # page, Hq, Hkv, D, head_major, lengths (prefix, nodes)
     (16, 64, 8, 128, True, [(0, 1), (1, 20), (127, 33), (128, 16), (129, 9), (300, 32), (77, 12), (513, 17)]),
     (128, 12, 4, 64, True, [(500, 90), (128, 64), (0, 3), (127, 1), (1, 86), (256, 0), (30, 43), (700, 5)]),
     (32, 32, 32, 128, False, [(70, 256), (33, 1)]),
-    (64, 20, 4, 128, False, [(64 * i, 13 + i) for i in range(8)]),
+    (64, 32, 4, 128, False, [(64 * i, 13 + i) for i in range(8)]),
     (16, 34, 2, 64, True, [(40 + i, 3 + i % 6) for i in range(16)]),
     (128, 16, 8, 128, True, [(9000, 40), (20, 129), (1500, 256), (4000, 1)]),
 ]
 
 
-def wide_workspace(tsv, b, max_nodes=None):
-    ws = tsv.paged_tree_attention_workspace(b.q, b.cache, len(b.lens), max_nodes or max(n for _, n in b.lens))
-    assert ws.numel() * ws.element_size() > 256 * 2 * 64 * b.D * 4  # 256 rows a part: the kernel that is meant
-    return ws
+def wide_workspace(tsv, b):
+    """Makes room in the page table for as many keys as the kernel of many rows is taken for (entries that no length needs
+    are not read); returns a workspace."""
+    if b.table.shape[1] * b.page < 1 << 19:
+        more = np.full((len(b.lens), (1 << 19) // b.page), -1, dtype=np.int32)
+        b.table = np.concatenate([b.table, more], axis=1)
+    rows = max(n for _, n in b.lens) * (b.Hq // b.Hkv)
+    assert rows > 128 and len(b.lens) * b.Hkv * -(-rows // 256) * (b.table.shape[1] * b.page // 128) >= 4096
+    return tsv.paged_tree_attention_workspace(b.q, b.cache, len(b.lens), max(n for _, n in b.lens))
 
 
 @pytest.mark.parametrize("case", WIDE, ids=lambda c: "-".join(str(x) for x in c[:5]))
@@ -616,7 +621,7 @@ def test_attention_of_many_rows_extreme_scores(tsv):
 
 def test_attention_of_many_rows_sink_and_flat_tail(tsv):
     """Weights 8192 : 6000 again, for every row."""
-    b = Batch(tsv, np.random.default_rng(24), [(6001, 12)], 256, 32, 64, 128, tree=False)
+    b = Batch(tsv, np.random.default_rng(24), [(6001, 17)], 256, 32, 64, 128, tree=False)
     k, v = b.cache.k.view(torch.uint8), b.cache.v.view(torch.uint8)
     k.zero_()
     v.fill_(0x38)  # 1.0

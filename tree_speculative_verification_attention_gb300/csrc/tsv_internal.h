@@ -304,17 +304,20 @@ constexpr int32_t kPagedWideRows = 256;
 constexpr int32_t kPagedWideCtas = 160;  // at most: shared memory holds the weights of so many parts
 // Rows of a unit of the tensor-core kernels: 16, 32, 64 (keys on the TMEM lanes)
 // or 256 (rows on them), of `rows` query rows in each of `groups` (request, KV
-// head) pairs.  More rows share a block's cost, but units that are few are cut
-// into many parts, which costs more the more rows they have.  Measured (us; 64
-// heads on 8 KV heads, D = 128), 32 / 64 / 256 rows a unit:
-//   16 requests x 2048 keys:  40 rows 62 / 48 / 75, 96 rows 88 / 81 / 77, 256 rows 207 / 145 / 103
-//   1 request x 16384 keys:   64 rows 31 / 45 / 53, 256 rows 69 / 66 / 90, 512 rows 121 / 103 / 102
-//   1 request x 1024 keys:    64 rows 18 / 25 / 31, 512 rows 32 / 35 / 50
-inline int32_t paged_attn_rows(int64_t rows, int64_t groups) {
+// head) pairs, over up to `keys` keys (what the page tables hold).  More rows
+// share a block's cost, but units that are few are cut into many parts, and
+// parts cost more the more rows they have.  Measured (us; 8 query heads a KV
+// head, D = 128), 32 / 64 / 256 rows a unit:
+//   1 request x 16384 keys x 8 KV heads:   64 rows 31 / 45 / 53, 256 rows 69 / 66 / 90, 512 rows 121 / 103 / 102
+//   1 request x 32768 keys x 8 KV heads:   1024 rows - / 341 / 221
+//   4 requests x 4096 keys x 8 KV heads:   128 rows 50 / 45 / 64, 256 rows 85 / 68 / 79
+//   13 requests x 256 keys x 8 KV heads:   256 rows 73 / 56 / 58; 2048 keys 168 / 117 / 94
+//   32 requests x 4096 keys x 8 KV heads:  40 rows 164 / 113 / 199, 128 rows 311 / 221 / 207, 256 rows 600 / 418 / 249
+inline int32_t paged_attn_rows(int64_t rows, int64_t groups, int64_t keys) {
   if (rows <= 32) return rows <= 16 ? 16 : 32;
-  const int64_t few = 32;
-  if (rows > 64 && groups * ((rows + kPagedWideRows - 1) / kPagedWideRows) >= few) return kPagedWideRows;
-  return groups * ((rows + 63) / 64) >= few ? 64 : 32;
+  const int64_t wide = groups * ((rows + kPagedWideRows - 1) / kPagedWideRows);
+  if (rows > 128 && wide * (keys / 128 + 1) >= (wide >= 96 ? 1024 : 4096)) return kPagedWideRows;
+  return groups * ((rows + 63) / 64) >= 32 ? 64 : 32;
 }
 struct PagedAttnLayout {
   size_t part_o, part_ml, total;

@@ -234,7 +234,7 @@ tsv_status tsv_paged_tree_attention_workspace_size(tsv_handle h, tsv_dtype dtype
   if (!bytes) return TSV_ERR_INVALID_ARG;
   const tsv_status st = check_attention(h, dtype, cache, &c, B, max_nodes, Hq, flags);
   if (st != TSV_OK) return st;
-  const int32_t R = paged_attn_rows((int64_t)max_nodes * (Hq / c.Hkv), (int64_t)B * c.Hkv);
+  const int32_t R = paged_attn_rows((int64_t)max_nodes * (Hq / c.Hkv), (int64_t)B * c.Hkv, TSV_PAGED_MAX_ROWS);  // for every table
   *bytes = paged_uses_tc(dtype, flags) ? paged_attn_layout(h->num_sms, R, c.D).total : 0;
   return TSV_OK;
 }
@@ -259,7 +259,8 @@ tsv_status tsv_paged_tree_attention(tsv_handle h, tsv_dtype dtype, const void* q
     return TSV_ERR_INVALID_ARG;
   if ((int64_t)N * Hq > INT32_MAX) return TSV_ERR_UNSUPPORTED;
   const bool use_tc = paged_uses_tc(dtype, flags);
-  const int32_t R = paged_attn_rows((int64_t)max_nodes * (Hq / a.cache.Hkv), (int64_t)B * a.cache.Hkv);
+  const int32_t R = paged_attn_rows((int64_t)max_nodes * (Hq / a.cache.Hkv), (int64_t)B * a.cache.Hkv,
+                                    (int64_t)table->pages * a.cache.page_size);
   if (use_tc && (!workspace_d || !aligned16(workspace_d) ||
                  workspace_bytes < paged_attn_layout(h->num_sms, R, a.cache.D).total))
     return TSV_ERR_INVALID_ARG;
