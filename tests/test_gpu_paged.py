@@ -994,3 +994,48 @@ def test_scales_stay_apart_in_a_long_pool(tsv):
         a, s1 = tsv.paged_tree_attention(q, c, i32(last), i32([n]), i32([0, 1]), flags=flags)
         b, s2 = tsv.paged_tree_attention(q, small, i32([[1, 2, 0]]), i32([n]), i32([0, 1]), flags=flags)
         assert torch.equal(a, b) and s1.tolist() == s2.tolist() == [0]
+
+
+def test_rope_refuses_pointers_between_elements(tsv):
+    """Through the C entry: x, y, positions and frequencies on their types' boundaries."""
+    x = torch.zeros(4 * 2 * 8 + 8, device="cuda")
+    pos, freq = i32([0, 1, 2, 3]), tsv.rope_frequencies(8, device="cuda")[0]
+    h = tsv.handle(x.device.index)
+
+    def call(dx=0, dy=0, dp=0, df=0):
+        return tsv._lib.tsv_rope(h, tsv.TSV_F32, x.data_ptr() + dx, 16, 8, x.data_ptr() + dy, 16, 8, 4, 2, 8, pos.data_ptr() + dp,
+                                 freq.data_ptr() + df, 8, 1.0, 0, 0)
+
+    assert call() == 0
+    for bad in (dict(dx=2), dict(dy=1), dict(dp=2), dict(df=4)):
+        assert call(**bad) == 1
+    torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("kind", KINDS, ids=lambda k: k[0])
+def test_the_largest_batch(tsv, kind):
+    """128 requests of every small length through append, attention, commit and attention again, few and many rows."""
+    rng = np.random.default_rng(31)
+    B, Hkv, D, page = 128, 2, 64, 16
+    lens = [(int(rng.integers(0, 70)), int(rng.integers(0, 10))) for _ in range(B)]
+    b = Batch(tsv, rng, lens, 4, Hkv, D, page, dtype=kind[1])
+    out, st = b.run(tsv, flags=kind[2])
+    b.check(out, st, kind[0] == "bf16")
+    N = int(b.offs[-1])
+    k, v = (dev(rng.normal(size=(N, Hkv, D)), kind[1]) for _ in range(2))
+    st = tsv.paged_append(b.cache, dev(b.tree_table), k, v, i32(b.offs))
+    assert (st == 0).all()
+    out, st = b.run(tsv, flags=kind[2])
+    b.check(out, st, kind[0] == "bf16")
+    path, accept = np.zeros(N, np.int32), np.zeros(B, np.int32)
+    for i, (_, n) in enumerate(lens):
+        path[b.offs[i]:b.offs[i + 1]] = np.arange(n)
+        accept[i] = max(n - 1, 0)
+    room = np.full((B, b.table.shape[1] + 1), -1, np.int32)  # pages behind each prefix to commit into
+    room[:, :-1] = b.table
+    r = tsv.paged_commit(b.cache, dev(room), dev(b.tree_table), i32(b.prefix), i32(b.offs), i32(path), i32(accept))
+    fits = np.array([n > 0 and (p + n - 1) // page < -(-p // page) for p, n in lens])  # the others lack a page, or rows
+    got = r["status"].cpu().numpy()
+    assert (got[fits] == 0).all()
+    assert (got[[n == 0 for _, n in lens]] == 1).all()
+    assert np.array_equal(r["new_len"].cpu().numpy()[fits], np.array([p + n for p, n in lens])[fits])

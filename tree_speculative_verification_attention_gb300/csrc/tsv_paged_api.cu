@@ -155,6 +155,10 @@ tsv_status tsv_rope(tsv_handle h, tsv_dtype dtype, const void* x_d, int64_t x_st
   if (D > 1024 || (int64_t)H * D > (1 << 30)) return TSV_ERR_UNSUPPORTED;
   if (N == 0) return TSV_OK;
   if (!x_d || !y_d || !positions_d || !inv_freq_d) return TSV_ERR_INVALID_ARG;
+  const uintptr_t esz = dtype == TSV_BF16 ? 2 : 4;
+  if ((reinterpret_cast<uintptr_t>(x_d) | reinterpret_cast<uintptr_t>(y_d)) % esz || reinterpret_cast<uintptr_t>(positions_d) % 4 ||
+      reinterpret_cast<uintptr_t>(inv_freq_d) % 8)
+    return TSV_ERR_INVALID_ARG;
   if (x_d == y_d && ((N > 1 && x_stride_n != y_stride_n) || (H > 1 && x_stride_h != y_stride_h)))
     return TSV_ERR_INVALID_ARG;
   const DeviceScope scope(h->device);

@@ -189,7 +189,7 @@ cudaError_t launch_rope_vec(const RopeArgs& a, int num_sms, cudaStream_t st) {
   // The table holds their angles.
   const int64_t resident = (int64_t)num_sms * (40 * 32 / threads);
   const int rows = (int)min(min((a.N + resident - 1) / resident, (int64_t)8), (int64_t)(kRopePairs / ((half + 1) & ~1)));
-  const dim3 grid((a.N + rows - 1) / rows), block(threads);
+  const dim3 grid((uint32_t)(((int64_t)a.N + rows - 1) / rows)), block(threads);
   const FastDiv by_row((uint32_t)per_row), by_items((uint32_t)items), by_half((uint32_t)half);
   if (a.interleaved) return launch_pdl(rope_kernel<T, E, true>, grid, block, 0, st, 0u, a, rows, by_row, by_items, by_half);
   return launch_pdl(rope_kernel<T, E, false>, grid, block, 0, st, 0u, a, rows, by_row, by_items, by_half);
