@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import struct
 
 import torch
 
@@ -163,19 +164,24 @@ def _want(ok, what):
 
 def _ints(name, t, size, index):
     """The address of an int32 vector of `size` values on the call's device."""
-    if t.dtype is not _INT or t.get_device() != index or t.dim() != 1 or t.numel() != size or not t.is_contiguous():
+    if t.dtype is not _INT or t.get_device() != index or t.shape != (size,) or not t.is_contiguous():
         raise ValueError("%s: a contiguous int32 tensor of %d values on cuda:%d is wanted" % (name, size, index))
     return t.data_ptr()
 
 
+_pack_table = struct.Struct("@Pqi4x").pack  # CPageTable's bytes: made in a third of the structure's time
+assert struct.calcsize("@Pqi4x") == ctypes.sizeof(CPageTable)
+
+
 def _table(name, t, B, index):
+    """A tsv_page_table, as its bytes."""
     if t.dtype is not _INT or t.get_device() != index or t.dim() != 2:
         raise ValueError("%s: an int32 tensor [%d, pages] on cuda:%d is wanted" % (name, B, index))
     rows, pages = t.shape
     stride, inner = t.stride()
-    if rows != B or (pages > 1 and inner != 1):
+    if rows != B or (pages > 1 and inner != 1) or pages >= 1 << 31:
         raise ValueError("%s: an int32 tensor [%d, pages] on cuda:%d is wanted" % (name, B, index))
-    return CPageTable(t.data_ptr(), stride, pages)
+    return _pack_table(t.data_ptr(), stride, pages)
 
 
 def _heads(name, t, index, D=None):
@@ -289,7 +295,7 @@ def paged_append(cache, page_table, k, v, row_offsets, start=None, positions=Non
         with _allocating(stream, cache.device):
             status = torch.empty(B, dtype=_INT, device=cache.device)
     st = _ints("status", status, B, index)
-    _check(_lib.tsv_paged_append(_handle(index), code, cache.at, ctypes.addressof(table), first, k.data_ptr(), ks[0], ks[1],
+    _check(_lib.tsv_paged_append(_handle(index), code, cache.at, table, first, k.data_ptr(), ks[0], ks[1],
                                  v.data_ptr(), vs[0], vs[1], offs, B, N, N if max_rows is None else max_rows, pos, freq, rot,
                                  amplitude, TSV_ROPE_INTERLEAVED if interleaved else 0, st, _on(stream, index)),
            "tsv_paged_append")
@@ -336,8 +342,8 @@ def paged_tree_attention(q, cache, page_table, prefix_len, node_offsets, tree_ta
           "out: a contiguous tensor of q's shape and type is wanted")
     _want(workspace.get_device() == index and workspace.is_contiguous(), "workspace: a contiguous tensor beside the cache is wanted")
     st = _ints("status", status, B, index)
-    _check(_lib.tsv_paged_tree_attention(h, code, q.data_ptr(), qs[0], qs[1], cache.at, ctypes.addressof(main), plen,
-                                         None if tree is None else ctypes.addressof(tree), offs, words, out.data_ptr(), B, N,
+    _check(_lib.tsv_paged_tree_attention(h, code, q.data_ptr(), qs[0], qs[1], cache.at, main, plen,
+                                         tree, offs, words, out.data_ptr(), B, N,
                                          max_nodes, Hq, scale, workspace.data_ptr(),
                                          workspace.numel() * workspace.element_size(), st, flags, _on(stream, index)),
            "tsv_paged_tree_attention")
@@ -361,7 +367,7 @@ def paged_commit(cache, page_table, tree_table, prefix_len, node_offsets, path, 
             out = dict(new_len=torch.empty(B, dtype=_INT, device=cache.device),
                        status=torch.empty(B, dtype=_INT, device=cache.device))
     new, st = _ints("new_len", out["new_len"], B, index), _ints("status", out["status"], B, index)
-    _check(_lib.tsv_paged_commit(_handle(index), cache.at, ctypes.addressof(main), ctypes.addressof(tree), plen, offs, way, acc,
+    _check(_lib.tsv_paged_commit(_handle(index), cache.at, main, tree, plen, offs, way, acc,
                                  B, N, max(1, min(N, TSV_MAX_NODES)) if max_nodes is None else max_nodes, new, st,
                                  _on(stream, index)), "tsv_paged_commit")
     return out
