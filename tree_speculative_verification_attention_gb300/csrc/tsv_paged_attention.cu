@@ -33,9 +33,9 @@
 // the instructions around them (a warp's chain of dependent steps runs at 6 to
 // 7 cycles an instruction, a third of it waiting for instruction fetches), so
 // what a step costs once matters most.  Measured: 32 requests x 2064 keys x 32
-// heads, 16 rows each, 142 us (3.8 TB/s; without P's arithmetic 104, without O's
+// heads, 16 rows each, 144 us (3.8 TB/s; without P's arithmetic 104, without O's
 // sums 137, one MMA of four for O 122); one token of 8 requests, 64 heads on 8 of
-// the cache, 28 us; a 20-node tree over 1024 keys, 32 heads, 20 us.
+// the cache, 26 us; a 20-node tree over 1024 keys, 32 heads, 15.6 us.
 //
 // Roles (20 warps): two softmax warpgroups (warps 0-3 and 4-7; a thread owns a
 // key of each block), which take alternate steps, or, with 64 rows, 32 rows of
@@ -64,6 +64,13 @@ constexpr int kPProducerWarp = 12, kPSWarp = 16, kPOWarp = 17, kPPrepWarp = 18;
 // Registers a thread: 640 x 96 at launch = 256 x 120 + 128 x 112 + 256 x 64.
 constexpr int kPRegs = 96, kPSoftRegs = 120, kPAccRegs = 112, kPRestRegs = 64;
 static_assert(256 * kPSoftRegs + 128 * kPAccRegs + 256 * kPRestRegs <= kPThreads * kPRegs, "register split");
+// What a unit costs beside its blocks, in blocks (us at 0, 2, 4, 6: a 20-node
+// tree x 32 heads over 1024 keys 20.1, 16.1, 16.1, 16.9; 64 requests of one
+// token, 64 heads on 8, up to 3000 keys 81.7, 80.5, 78.6, 76.8; 32 requests x 16
+// nodes x 32 heads over 2048 keys 141, 144, 143, 142).
+// Groups of two or three blocks cost more cut than whole: 13 requests of up to 45
+// nodes over up to 144 keys 22 us without, 26 with.
+constexpr PPad kPPad{4, 4};
 constexpr int kBarSoft = 1;       // and 2: one per softmax warpgroup
 constexpr int kBarAcc = 3, kBarFirst = 4;
 
@@ -299,12 +306,12 @@ __global__ void __launch_bounds__(kPThreads, 1)
   pdl_wait();  // the previous kernel's results are visible from here on
   pdl_trigger();
 
-  if (warp == 0) plist_setup(a, R, sCum, sReq, sFirst, sRange);
+  if (warp == 0) plist_setup(a, R, kPPad, sCum, sReq, sFirst, sRange);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  const PList list{sCum, sReq, a.B, a.G, a.cache.Hkv, R, tree, sRange[1]};
+  const PList list{sCum, sReq, a.B, a.G, a.cache.Hkv, R, kPPad, tree, sRange[1]};
 
   // Rows r_lo .. r_lo + count - 1 of a unit's tile (one warp): their output
   // rows, score factors and two e4m3 terms.
@@ -446,7 +453,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
     Look c0{-1, 0, 0, 0}, c1;
     float2 sc0 = make_float2(0.f, 0.f), sc1 = sc0;
     float top = 0.f;  // of the lane's block: V's largest scale
-    const int blocks = __shfl_sync(0xffffffffu, (int)(sRange[1] - sRange[0]), 0);
+    const int blocks = __shfl_sync(0xffffffffu, (int)sRange[0], 0);
     int st = odd, ph = 0;  // of this warp's next block: ring stage and phase
     // Chunk t is issued (c0) while the ids of the next one (c1) are looked up,
     // at its first block, and its scales, at its second.
@@ -1049,7 +1056,8 @@ __global__ void __launch_bounds__(kPThreads, 1)
         if (d < R) pm[R + d] = fin[d];
         // CTAs cf .. cl share the group; the last to arrive joins.
         const int64_t W = sRange[2], ctas = sRange[3];
-        const int cf = (int)(((u.gx + 1) * ctas - 1) / W), cl = (int)(((u.gx + u.T) * ctas - 1) / W);
+        const int64_t g0 = u.gx + list.pad.of(u.T);  // the place of its first block
+        const int cf = (int)(((g0 + 1) * ctas - 1) / W), cl = (int)(((g0 + u.T) * ctas - 1) / W);
         named_bar_sync(kBarAcc, 128);
         if (d == 0) {
           const int n = atom_add_acq_rel_gpu(counters + cf, 1);

@@ -7,22 +7,22 @@
 // Both products are fp16 with fp32 sums.  An e4m3 code is an fp16 value, so K
 // and V are widened without a rounding (one conversion per two codes); a row of
 // Q is a bf16 row times a power of two that moves its largest value to
-// [2^14, 2^15): exact down to 2^-31 of it.  P is 2^7 p with p <= 2^8, rounded to
+// [2^14, 2^15): exact down to 2^-31 of it.  P is 2^11 p with p <= 2^4, rounded to
 // fp16's 11 bits.  The scale of a key's page multiplies S in fp32; the scale of
 // its V page, relative to the largest one so far, multiplies P (weights of V
-// rows whose scale is below 2^-21 of the unit's largest lose bits to fp16's
-// range, below 2^-32 they are nothing).
+// rows whose scale is below 2^-25 of the unit's largest lose bits to fp16's
+// range, below 2^-36 they are nothing).
 //
 // Why another kernel: with rows on N (the kernel for few rows) both products
 // take two e4m3 terms of Q and of P, and every 64 rows their own pass over the
 // keys.  Here the widening is paid once for 256 rows: a 128-node tree x 64 heads
-// on 8 of the cache, 32768 keys: 221 us against 341 (622 TFLOP/s of both
+// on 8 of the cache, 32768 keys: 204 us against 341 (674 TFLOP/s of both
 // products).  When it is taken: at paged_attn_rows.
 //
 // One CTA per SM walks its share of the list of blocks (as the other kernel
 // does; a unit is up to 256 rows, two tiles).  Roles (20 warps):
 //   0-7    softmax: warps 0-3 tile 0, 4-7 tile 1; a thread owns a row.  The
-//          reference maximum moves only when a score passes it by 2^8, and with
+//          reference maximum moves only when a score passes it by 2^4, and with
 //          it the row of O in TMEM.
 //   8-15   widening: a block's codes lie in the upper half of the tile that
 //          takes them as fp16 (Q and the two fp16 rings leave no room beside
@@ -33,9 +33,9 @@
 //   18, 19 producers of K and of V: a page's rows of the head are one TMA box,
 //          asked for a block ahead of their tile's release through L2.
 // What bounds it: the chain of a half block through issuer, softmax and issuer
-// again, not one unit: with half of the MMAs it takes 195 us, without widening
-// 204, without exponentials 207, without all three 168; the join of units that
-// were cut (256 rows each) is 17 us of it.
+// again, not one unit.  Measured when that case took 219 us: with half of the
+// MMAs 195, without widening 204, without exponentials 207, without all three
+// 168; without the join of units that were cut (256 rows each) 202.
 //
 // Masks: the keys of tree blocks by the ancestor words of the row's node, keys
 // past the end by their number.  V rows past the last key are zeros, and NaN
@@ -55,8 +55,14 @@ constexpr int kWConvWarp = 8, kWMmaWarp = 16;
 constexpr int kWRegs = 96, kWSoftRegs = 128, kWConvRegs = 72, kWRestRegs = 80;
 static_assert(256 * kWSoftRegs + 256 * kWConvRegs + 128 * kWRestRegs <= kWThreads * kWRegs, "register split");
 constexpr int kWRows = kPagedWideRows, kWTile = 128;
-constexpr float kWThreshold = 8.f;  // log2: how far a score may pass the reference maximum
+constexpr float kWThreshold = 4.f;  // log2: how far a score may pass the reference maximum
+constexpr float kWScale = 2048.f;   // of P: 2^4 x it is within fp16
 constexpr int kHalf = 64;  // keys of a softmax step
+// What a unit costs beside its blocks (Q, the pipeline's start and end, its
+// results, the join), in blocks.  128 nodes x 64 heads over 32768 keys: 222 us
+// at 0, 202 at 8 and 12, 206 at 20; 64 ragged requests of up to 64 nodes over up
+// to 700 keys 330, 260, 252, 259.
+constexpr PPad kWPad{12, 0};
 constexpr int kBarWSoft = 1, kBarWJoin = 2, kBarWConv = 3;
 
 template <int D>
@@ -221,12 +227,12 @@ __global__ void __launch_bounds__(kWThreads, 1)
   }
   pdl_wait();  // the previous kernel's results are visible from here on
   pdl_trigger();
-  if (warp == 0) plist_setup(a, kWRows, sCum, sReq, sFirst, sRange);
+  if (warp == 0) plist_setup(a, kWRows, kWPad, sCum, sReq, sFirst, sRange);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  const PList list{sCum, sReq, a.B, a.G, a.cache.Hkv, kWRows, tree, sRange[1]};
+  const PList list{sCum, sReq, a.B, a.G, a.cache.Hkv, kWRows, kWPad, tree, sRange[1]};
 
   // Every role walks the units together: a barrier before each, one when its
   // rows are in, and one behind it.
@@ -267,10 +273,10 @@ __global__ void __launch_bounds__(kWThreads, 1)
     __device__ __forceinline__ int64_t slot(int c) const { return 2 * (cf + c) + (c == 0 ? first : 0); }
   };
   auto group = [&]() {
-    const int64_t W = sRange[2], ctas = sRange[3], gx = sUnit->gx;
+    const int64_t W = sRange[2], ctas = sRange[3], gx = sUnit->gx, g0 = gx + list.pad.of(sUnit->T);  // g0: of its first block
     Group z;
-    z.cf = (int)(((gx + 1) * ctas - 1) / W);
-    z.parts = (int)(((gx + sUnit->T) * ctas - 1) / W) - z.cf + 1;
+    z.cf = (int)(((g0 + 1) * ctas - 1) / W);
+    z.parts = (int)(((g0 + sUnit->T) * ctas - 1) / W) - z.cf + 1;
     z.first = (int64_t)z.cf * W / ctas >= gx ? 0 : 1;
     return z;
   };
@@ -661,7 +667,7 @@ __global__ void __launch_bounds__(kWThreads, 1)
         if (v_top > v_ref) {  // the same in every thread
           alpha *= v_ref / v_top;
           v_ref = v_top;
-          to_v = 128.f / v_top;
+          to_v = kWScale / v_top;
         }
         if (h > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
           TSV_PWAIT(&pv_done[2 * tile + (1 - half)], cnt[tile] + ((h - 1) >> 1));
@@ -741,7 +747,7 @@ __global__ void __launch_bounds__(kWThreads, 1)
             }
           }
         }
-        const float unit = v_ref * (1.f / 128.f);
+        const float unit = v_ref * (1.f / kWScale);
         const float inv = l == 0.f ? 0.f : unit / l;  // (0 for a row that sees nothing)
         __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out);
         const bool whole = sUnit->whole();

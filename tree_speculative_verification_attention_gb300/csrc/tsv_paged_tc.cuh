@@ -60,17 +60,25 @@ __device__ __forceinline__ void mbar_expect_tx(uint64_t* bar, uint32_t bytes) {
 
 // One unit of a CTA's range: blocks j .. j1 - 1 of a (request, KV head, row
 // tile) group of T blocks, nmain of them over prefix rows.  gx is the place of
-// the group's block 0 in the list of all blocks.
+// the group in the list of all blocks: it begins with a few places that hold no
+// block and stand for what a unit costs beside its blocks, so that a CTA with a
+// group's end and another's beginning gets as many blocks fewer.
 struct alignas(16) PUnit {
   int b, g, tile, tiles, off, n, P, nmain, T, j, j1, valid;
   int64_t gx;
   __device__ __forceinline__ bool whole() const { return j == 0 && j1 == T; }
 };
 
+struct PPad {
+  int blocks, least;  // of groups of `least` blocks at least
+  __device__ __forceinline__ int of(int T) const { return T >= least ? blocks : 0; }
+};
+
 struct PList {
   const int64_t* cum;
   const int4* req;
   int B, G, Hkv, R;
+  PPad pad;
   bool tree;
   int64_t x1;  // end of this CTA's range
 
@@ -93,16 +101,19 @@ struct PList {
     for (int q = 0; q < TSV_MAX_BATCH / 32; ++q) u.b += __popc(__ballot_sync(0xffffffffu, cum[32 * q + lane + 1] <= x0));
     request(u);
     const int64_t rel = x0 - cum[u.b];
-    const int group = rel <= 0xFFFFFFFFll ? (int)((uint32_t)rel / (uint32_t)u.T) : (int)(rel / u.T);
-    u.j = (int)(rel - (int64_t)group * u.T);
+    const int none = pad.of(u.T), len = u.T + none;
+    const int group = rel <= 0xFFFFFFFFll ? (int)((uint32_t)rel / (uint32_t)len) : (int)(rel / len);
+    const int at = (int)(rel - (int64_t)group * len);
+    u.j = max(0, at - none);
     u.g = group / u.tiles;
     u.tile = group - u.g * u.tiles;
-    u.gx = x0 - u.j;
-    u.j1 = (int)min((int64_t)u.T, x1 - u.gx);
+    u.gx = x0 - at;
+    u.j1 = (int)min((int64_t)u.T, x1 - u.gx - none);
+    u.valid = u.j < u.j1;  // (else the range ends before the group's first block)
     return u;
   }
   __device__ __forceinline__ void next(PUnit& u) const {
-    u.gx += u.T;
+    u.gx += u.T + pad.of(u.T);
     u.valid = u.gx < x1;
     if (!u.valid) return;
     if (++u.tile == u.tiles) {
@@ -115,7 +126,8 @@ struct PList {
       }
     }
     u.j = 0;
-    u.j1 = (int)min((int64_t)u.T, x1 - u.gx);
+    u.j1 = (int)min((int64_t)u.T, x1 - u.gx - pad.of(u.T));
+    u.valid = u.j1 > 0;
   }
 };
 
@@ -158,9 +170,9 @@ __device__ __forceinline__ void parrive(uint64_t* bar, bool dead) {
 
 // The list of blocks: request b holds T_b x Hkv x tiles of them.  A request
 // with nothing to see still gets one (empty) block, which writes its zeros.
-// One warp works it out, and the CTA's range (range: x0, x1, blocks, CTAs) and
-// first unit.
-__device__ __forceinline__ void plist_setup(const PagedAttnArgs& a, int R, int64_t* sCum, int4* sReq, PUnit* sFirst,
+// One warp works it out, and the CTA's range (sRange: its blocks, its end, all
+// places, CTAs) and first unit.
+__device__ __forceinline__ void plist_setup(const PagedAttnArgs& a, int R, PPad pad, int64_t* sCum, int4* sReq, PUnit* sFirst,
                                             int64_t* sRange) {
   const int lane = threadIdx.x & 31;
   const bool tree = a.tree_table.ids_d != nullptr;
@@ -174,7 +186,7 @@ __device__ __forceinline__ void plist_setup(const PagedAttnArgs& a, int R, int64
       PagedRequest r;
       if (b < a.B && paged_request(a, b, &r) && r.n > 0) {
         const int T = max(1, (r.P + kPBlock - 1) / kPBlock + (tree ? (r.n + kPBlock - 1) / kPBlock : 0));
-        upto = (int64_t)T * a.cache.Hkv * ((r.n * a.G + R - 1) / R);
+        upto = (int64_t)(T + pad.of(T)) * a.cache.Hkv * ((r.n * a.G + R - 1) / R);
         sReq[b] = make_int4(r.off, r.n, r.P, T);
       }
 #pragma unroll
@@ -198,11 +210,16 @@ __device__ __forceinline__ void plist_setup(const PagedAttnArgs& a, int R, int64
       x1 = ((int64_t)blockIdx.x + 1) * W / ctas;
     }
   }
-  const PList mine{sCum, sReq, a.B, a.G, a.cache.Hkv, R, tree, x1};
+  const PList mine{sCum, sReq, a.B, a.G, a.cache.Hkv, R, pad, tree, x1};
   const PUnit u = mine.first(x0);
+  int64_t blocks = x1 - x0;
+  if (pad.blocks > 0) {
+    blocks = 0;
+    for (PUnit w = u; w.valid; mine.next(w)) blocks += w.j1 - w.j;
+  }
   if (lane == 0) {
     *sFirst = u;
-    sRange[0] = x0;
+    sRange[0] = blocks;
     sRange[1] = x1;
     sRange[2] = W;
     sRange[3] = ctas;
