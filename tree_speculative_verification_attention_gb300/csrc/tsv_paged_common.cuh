@@ -83,7 +83,14 @@ __device__ __forceinline__ uint64_t rope_turns(double w) {
 
 __device__ __forceinline__ void rope_cos_sin(int32_t position, uint64_t turns, float* c, float* s) {
   const int32_t frac = (int32_t)(uint32_t)((turns * (uint64_t)(int64_t)position) >> 32);  // [-1/2, 1/2) turn x 2^32
-  sincospif((float)frac * 4.656612873077392578125e-10f, s, c);                             // 2^-31: half turns
+  // The fraction's 32 bits as a float and what that left (up to 2^6 units, 1.5
+  // fp32 steps of the angle), which turns the result on.
+  const float f = (float)frac;
+  const float rest = (float)(frac - (int32_t)f) * 1.4629180792671596e-9f;  // pi 2^-31
+  float s0, c0;
+  sincospif(f * 4.656612873077392578125e-10f, &s0, &c0);  // 2^-31: half turns
+  *c = fmaf(-s0, rest, c0);
+  *s = fmaf(c0, rest, s0);
 }
 
 // One rotated pair.  The roundings are spelled out: every kernel and vector
