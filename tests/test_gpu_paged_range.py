@@ -1,0 +1,70 @@
+"""Ranges of the paged 8-bit cache's operators on the GPU: scales far from one another, the smallest and largest ones, full
+batches.  Against the 64-bit forms of tests/_paged_ref.py under the bounds of test_gpu_paged.py."""
+import numpy as np
+import pytest
+import torch
+
+from test_gpu_paged import Batch, values, wide_workspace
+
+pytestmark = pytest.mark.gpu
+
+LENS = [(37, 5), (300, 3), (0, 8), (256, 1), (700, 4)]  # prefix, nodes (8 at most)
+ROWS = [(16, 4, 2), (32, 8, 2), (64, 64, 8)]  # query rows a unit, Hq, Hkv: 8 nodes times Hq / Hkv
+
+
+def run_of(tsv, b, rows, flags=0):
+    """The call that takes units of so many rows (256: the kernel of many rows)."""
+    return b.run(tsv, flags=flags, workspace=wide_workspace(tsv, b) if rows == 256 else None)
+
+
+# ------------------------------------------------------------------ values of zero
+
+
+def zero_values(b, where, head=0):
+    """V of one head zero in some of the pages, under the scale that append and commit write for zeros."""
+    pages = []
+    for i, (p, n) in enumerate(b.lens):
+        main = b.table[i][:-(-p // b.page)].tolist()
+        tree = b.tree_table[i][:-(-n // b.page)].tolist()
+        front = 256 // b.page
+        pages += {"all": main + tree, "front": main[:front], "back": main[front:] + tree, "tree": tree}[where]
+    ids = torch.tensor(pages, device="cuda")
+    b.cache.v.view(torch.uint8)[ids, :, head] = 0
+    b.cache.v_scale[ids, head] = 2.0 ** -126
+
+
+ZERO = ["all", "front", "back", "tree"]
+
+
+@pytest.mark.parametrize("where", ZERO)
+@pytest.mark.parametrize("page,D", [(16, 128), (64, 64)])
+@pytest.mark.parametrize("rows,Hq,Hkv", ROWS)
+def test_zero_values(tsv, rows, Hq, Hkv, page, D, where):
+    """Weights times zeros are zeros, whatever is masked, and ordinary values beside them are as exact as alone."""
+    b = Batch(tsv, np.random.default_rng(101), LENS, Hq, Hkv, D, page)
+    zero_values(b, where)
+    out, st = run_of(tsv, b, rows)
+    b.check(out, st, True)
+    if where == "all":
+        assert (out[:, :Hq // Hkv] == 0).all()
+
+
+@pytest.mark.parametrize("rows", [0, 16, 32, 64])
+@pytest.mark.parametrize("power", [-110, 100, 127])
+def test_a_scale_is_a_factor(tsv, rows, power):
+    """V scales of 2^power give 2^power times what scales of one give, from the smallest to the largest fp32 holds (2^127:
+    with values of 2^-6 at most).  Powers of two change no rounding, but results below 2^-126 have bf16's step of 2^-133."""
+    Hq, Hkv = {0: (4, 2), 16: (4, 2), 32: (8, 2), 64: (64, 8)}[rows]
+    b = Batch(tsv, np.random.default_rng(104), LENS, Hq, Hkv, 128, 16)
+    if power == 127:
+        v = b.cache.v.view(torch.uint8)
+        v.copy_((v & 0x80) | (v & 0x07))
+    flags = 1 if rows == 0 else 0
+    b.cache.v_scale.fill_(1.0)
+    one = run_of(tsv, b, rows, flags)[0].double()
+    b.cache.v_scale.fill_(2.0 ** power)
+    out, st = run_of(tsv, b, rows, flags)
+    assert (st == 0).all() and torch.isfinite(out).all()
+    err = (out.double() * 2.0 ** -power - one).abs()
+    # (results of 2^-126 and more are one of 2^-16 and more, of which none here is less but zeros)
+    assert (err <= 2.0 ** (-133 - power)).all()

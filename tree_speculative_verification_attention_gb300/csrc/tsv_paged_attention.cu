@@ -771,8 +771,10 @@ __global__ void __launch_bounds__(kPThreads, 1)
           }
           // V's scales, relative to the step's largest, go to P with its 256.
           const float top0 = sScale[st0 * 20 + 16];
-          const float top = nh == 2 ? fmaxf(top0, sScale[st1 * 20 + 16]) : top0;
-          const float inv_top = top > 0.f ? __fdividef(256.f, top) : 0.f;
+          // (2^-118 at least: a page of zeros has the scale 2^-126, and 256 over
+          // that is no fp32 number.  Values that small lose bits of their weights.)
+          const float top = fmaxf(nh == 2 ? fmaxf(top0, sScale[st1 * 20 + 16]) : top0, 0x1p-118f);
+          const float inv_top = __fdividef(1.f, top * 0x1p-8f);
           named_bar_sync(kBarSoft + wg, 128);
           // Every warp works out the rows' maxima and factors for itself.
           float m = 0.f;
