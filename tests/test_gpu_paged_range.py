@@ -4,7 +4,7 @@ import numpy as np
 import pytest
 import torch
 
-from test_gpu_paged import Batch, values, wide_workspace
+from test_gpu_paged import Batch, dev, i32, values, wide_workspace
 
 pytestmark = pytest.mark.gpu
 
@@ -49,12 +49,43 @@ def test_zero_values(tsv, rows, Hq, Hkv, page, D, where):
         assert (out[:, :Hq // Hkv] == 0).all()
 
 
-@pytest.mark.parametrize("rows", [0, 16, 32, 64])
+@pytest.mark.parametrize("where", ZERO)
+@pytest.mark.parametrize("long", [0, 6000])
+@pytest.mark.parametrize("page,D", [(16, 128), (64, 64)])
+def test_zero_values_of_many_rows(tsv, page, D, long, where):
+    """The same in units of 256 rows, whole and cut."""
+    lens = [(p + long * (i == 1), n) for i, (p, n) in enumerate(LENS)]
+    b = Batch(tsv, np.random.default_rng(102), lens, 256, 8, D, page)
+    zero_values(b, where)
+    out, st = run_of(tsv, b, 256)
+    b.check(out, st, True)
+    if where == "all":
+        assert (out[:, :32] == 0).all()
+
+
+@pytest.mark.parametrize("rows", [0, 16, 32, 64, 256])
+def test_zero_values_written_by_append(tsv, rows):
+    """A KV head whose V is zero throughout, prefix and tree written by append (rows 0: on CUDA cores)."""
+    Hq, Hkv = {0: (4, 2), 16: (4, 2), 32: (8, 2), 64: (64, 8), 256: (256, 8)}[rows]
+    rng = np.random.default_rng(103)
+    b = Batch(tsv, rng, LENS, Hq, Hkv, 128, 32)
+    for table, sizes in ((b.table, [p for p, _ in LENS]), (b.tree_table, [n for _, n in LENS])):
+        offs = np.concatenate([[0], np.cumsum(sizes)])
+        k, v = (dev(rng.normal(size=(int(offs[-1]), Hkv, 128)), torch.bfloat16) for _ in range(2))
+        v[:, 1] = 0
+        assert (tsv.paged_append(b.cache, dev(table), k, v, i32(offs)) == 0).all()
+    out, st = run_of(tsv, b, rows, flags=1 if rows == 0 else 0)
+    b.check(out, st, rows > 0)
+    G = Hq // Hkv
+    assert (out[:, G:2 * G] == 0).all()
+
+
+@pytest.mark.parametrize("rows", [0, 16, 32, 64, 256])
 @pytest.mark.parametrize("power", [-110, 100, 127])
 def test_a_scale_is_a_factor(tsv, rows, power):
     """V scales of 2^power give 2^power times what scales of one give, from the smallest to the largest fp32 holds (2^127:
     with values of 2^-6 at most).  Powers of two change no rounding, but results below 2^-126 have bf16's step of 2^-133."""
-    Hq, Hkv = {0: (4, 2), 16: (4, 2), 32: (8, 2), 64: (64, 8)}[rows]
+    Hq, Hkv = {0: (4, 2), 16: (4, 2), 32: (8, 2), 64: (64, 8), 256: (256, 8)}[rows]
     b = Batch(tsv, np.random.default_rng(104), LENS, Hq, Hkv, 128, 16)
     if power == 127:
         v = b.cache.v.view(torch.uint8)

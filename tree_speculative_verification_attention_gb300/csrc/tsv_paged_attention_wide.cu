@@ -78,7 +78,7 @@ struct WCfg {
   static constexpr int kOffReq = kOffCum + 8 * (TSV_MAX_BATCH + 2);  // int4 [TSV_MAX_BATCH]
   static constexpr int kOffFr = kOffReq + 16 * TSV_MAX_BATCH;        // f32 [256]: score factor of a row
   static constexpr int kOffRow = kOffFr + 4 * kWRows;                // i32 [256]: output row
-  static constexpr int kOffScale = kOffRow + 4 * kWRows;             // f32 [4][20]: K's scales of 8 x 16 keys, V's, V's largest
+  static constexpr int kOffScale = kOffRow + 4 * kWRows;             // f32 [4][20]: K's scales of 8 x 16 keys, V's relative ones, V's largest
   static constexpr int kOffNan = kOffScale + 4 * 80;                 // u32 [8]: tree keys whose V row holds a NaN
   static constexpr int kOffUnit = kOffNan + 32;                      // PUnit
   static constexpr int kOffFirst = kOffUnit + 64;                    // PUnit, then i64 [4]
@@ -340,7 +340,7 @@ __global__ void __launch_bounds__(kWThreads, 1)
       const int first_row = D == 128 ? ((ct >> 2) & 1) | ((ct >> 4) << 1) : ct >> 2;
       // Warp 0, lanes 0 .. 7: the page of 16 keys each, two blocks ahead, its scales one.
       int sid = -1;
-      float sk = 0.f, sv = 0.f;
+      float sk = 0.f, sv = 0.f, top = 0.f;
       auto look = [&](int i) {
         sid = -1;
         if (w != 0 || lane >= 8 || lane * 16 >= u.valid(i)) return;
@@ -425,15 +425,22 @@ __global__ void __launch_bounds__(kWThreads, 1)
         const int x = t + i, st = x & 1;
         const int valid = u.valid(i);
         uint4 codes[kParts];
+        float rv = 0.f;
+        if (w == 0) {
+          // The unit's largest V scale so far, and the block's relative to it (the
+          // ratio first: of zeros' 2^-126 the reciprocal times kWScale is no fp32
+          // number), worked out while the codes are on their way.
+          top = fmaxf(top, __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(sv))));  // (scales are >= 0)
+          rv = top > 0.f ? sv / top * kWScale : 0.f;
+        }
         TSV_PWAIT(&kc_full[st], x >> 1);
         take(sK + st * C::kTileBytes, valid, codes);
         dead = named_bar_or(kBarWConv, 256, dead);  // everyone has read, or gives up
         if (dead) break;
         if (w == 0) {
-          const float top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(sv)));  // (scales are >= 0)
           if (lane < 8) {
             sScale[(x & 3) * 20 + lane] = sk;
-            sScale[(x & 3) * 20 + 8 + lane] = sv;
+            sScale[(x & 3) * 20 + 8 + lane] = rv;
           }
           if (lane == 0) sScale[(x & 3) * 20 + 16] = top;
           __syncwarp();
@@ -611,7 +618,7 @@ __global__ void __launch_bounds__(kWThreads, 1)
       const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
       const uint32_t o_col = tmem + lane_base + C::kColO + (uint32_t)(tile * D);
       const float fr = sFr[row];
-      float m_ref = -INFINITY, l = 0.f, v_ref = 0.f, to_v = 0.f;
+      float m_ref = -INFINITY, l = 0.f, v_ref = 0.f;
       auto half_step = [&](int h, auto masked_c) {
         constexpr bool MASKED = decltype(masked_c)::value;
         const int i = h >> 1, half = h & 1, x = t + i;
@@ -624,8 +631,9 @@ __global__ void __launch_bounds__(kWThreads, 1)
         tmem_ld32_nowait(s_col, s[0]);
         tmem_ld32_nowait(s_col + 32, s[1]);
         const float* sc = sScale + (x & 3) * 20;
-        const float4 k4 = *reinterpret_cast<const float4*>(sc + 4 * half), v4 = *reinterpret_cast<const float4*>(sc + 8 + 4 * half);
-        const float v_top = sc[16];
+        const float4 k4 = *reinterpret_cast<const float4*>(sc + 4 * half);
+        const float4 v4 = *reinterpret_cast<const float4*>(sc + 8 + 4 * half);  // times kWScale, relative to v_top
+        const float v_top = sc[16];  // V's largest scale so far
         const float f[4] = {k4.x * fr, k4.y * fr, k4.z * fr, k4.w * fr};  // the row's factor of 16 keys each
         uint32_t see[2] = {~0u, ~0u};
         if (MASKED) {
@@ -667,7 +675,6 @@ __global__ void __launch_bounds__(kWThreads, 1)
         if (v_top > v_ref) {  // the same in every thread
           alpha *= v_ref / v_top;
           v_ref = v_top;
-          to_v = kWScale / v_top;
         }
         if (h > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
           TSV_PWAIT(&pv_done[2 * tile + (1 - half)], cnt[tile] + ((h - 1) >> 1));
@@ -685,7 +692,7 @@ __global__ void __launch_bounds__(kWThreads, 1)
         const float neg_ref = m_ref == -INFINITY ? 0.f : -m_ref;
         const uint64_t ref2 = f2_pack(neg_ref, neg_ref);
         uint64_t sum[2] = {0ull, 0ull};
-        const float fv[4] = {v4.x * to_v, v4.y * to_v, v4.z * to_v, v4.w * to_v};
+        const float fv[4] = {v4.x, v4.y, v4.z, v4.w};
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           uint32_t p[16];
@@ -747,8 +754,9 @@ __global__ void __launch_bounds__(kWThreads, 1)
             }
           }
         }
-        const float unit = v_ref * (1.f / kWScale);
-        const float inv = l == 0.f ? 0.f : unit / l;  // (0 for a row that sees nothing)
+        // (0 for a row that sees nothing.  v_ref may be 2^-126, a page of zeros': a
+        // factor of its own.)
+        const float inv = l == 0.f ? 0.f : (1.f / kWScale) / l;
         __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out);
         const bool whole = sUnit->whole();
         const int slot = 2 * (int)blockIdx.x + (k == 0 ? 0 : 1);
@@ -764,7 +772,7 @@ __global__ void __launch_bounds__(kWThreads, 1)
             tmem_ld32(o_col + cc, o);
             if (row < u.rows) {
 #pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] = l == 0.f ? 0.f : (bad[cc / 32] >> e) & 1u ? NAN : o[e] * inv;
+              for (int e = 0; e < 32; ++e) o[e] = l == 0.f ? 0.f : (bad[cc / 32] >> e) & 1u ? NAN : o[e] * inv * v_ref;
               if (whole) {
 #pragma unroll
                 for (int e = 0; e < 32; e += 8)
