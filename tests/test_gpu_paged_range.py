@@ -1,10 +1,13 @@
 """Ranges of the paged 8-bit cache's operators on the GPU: scales far from one another, the smallest and largest ones, full
 batches.  Against the 64-bit forms of tests/_paged_ref.py under the bounds of test_gpu_paged.py."""
+import math
+
 import numpy as np
 import pytest
 import torch
 
-from test_gpu_paged import Batch, dev, i32, values, wide_workspace
+import _paged_ref as R
+from test_gpu_paged import Batch, _attention_bound, dev, i32, values, wide_workspace
 
 pytestmark = pytest.mark.gpu
 
@@ -81,10 +84,11 @@ def test_zero_values_written_by_append(tsv, rows):
 
 
 @pytest.mark.parametrize("rows", [0, 16, 32, 64, 256])
-@pytest.mark.parametrize("power", [-110, 100, 127])
+@pytest.mark.parametrize("power", [-126, -120, -110, 100, 127])
 def test_a_scale_is_a_factor(tsv, rows, power):
     """V scales of 2^power give 2^power times what scales of one give, from the smallest to the largest fp32 holds (2^127:
-    with values of 2^-6 at most).  Powers of two change no rounding, but results below 2^-126 have bf16's step of 2^-133."""
+    with values of 2^-6 at most).  Powers of two change no rounding, but results below 2^-126 have bf16's step of 2^-133,
+    and products of weights and scales below it fp32's of 2^-149, which is 2^-23 of the largest."""
     Hq, Hkv = {0: (4, 2), 16: (4, 2), 32: (8, 2), 64: (64, 8), 256: (256, 8)}[rows]
     b = Batch(tsv, np.random.default_rng(104), LENS, Hq, Hkv, 128, 16)
     if power == 127:
@@ -97,5 +101,60 @@ def test_a_scale_is_a_factor(tsv, rows, power):
     out, st = run_of(tsv, b, rows, flags)
     assert (st == 0).all() and torch.isfinite(out).all()
     err = (out.double() * 2.0 ** -power - one).abs()
-    # (results of 2^-126 and more are one of 2^-16 and more, of which none here is less but zeros)
-    assert (err <= 2.0 ** (-133 - power)).all()
+    if power >= -110:  # (results of 2^-126 and more are one of 2^-16, of which none here is less but zeros)
+        assert (err <= 2.0 ** (-133 - power)).all()
+    else:
+        # one bf16 step where 2^-21 moves a value over the border between two
+        top = b.cache.v.float().abs().amax().item()
+        assert (err <= 2.0 ** -7 * one.abs() + 2.0 ** -20 * top + 2.0 ** (-133 - power)).all()
+
+
+# ------------------------------------------------------------------ V scales far apart
+
+
+def lost(b, floor):
+    """How far outputs may be off beyond _attention_bound because a weight (p times its V scale) is off by at most `floor` of
+    its row's largest, or, next to nothing, lost: the sums of min(weight, floor x largest) |code| [N, Hq, D]."""
+    c, G = values(b.cache), b.Hq // b.Hkv
+    out = np.zeros((len(b.q), b.Hq, b.D))
+    q = b.q.double().cpu().numpy()
+    for r, (P, n) in enumerate(b.lens):
+        ids = np.concatenate([b.table[r][np.arange(P) // b.page], b.tree_table[r][np.arange(n) // b.page]])
+        rows = np.concatenate([np.arange(P), np.arange(n)]) % b.page
+        k, codes = c.k[ids, rows] * c.k_scale[ids][:, :, None], np.abs(c.v[ids, rows])
+        for i in range(n):
+            see = np.concatenate([np.ones(P, bool), b.sees[b.offs[r] + i, :n]])
+            for h in range(b.Hq):
+                s = k[see, h // G] @ q[b.offs[r] + i, h] / math.sqrt(b.D)
+                p = np.exp(s - s.max())
+                w = p / p.sum() * c.v_scale[ids[see], h // G]
+                out[b.offs[r] + i, h] = np.minimum(w, floor * w.max()) @ codes[see, h // G]
+    return out
+
+
+@pytest.mark.parametrize("rows", [0, 16, 32, 64])
+@pytest.mark.parametrize("page,D", [(16, 128), (128, 64), (32, 128)])
+def test_pages_whose_values_lie_far_apart(tsv, rows, page, D):
+    """V scales 2^30 apart from page to page and rows that attend to hardly more than one key: the weights of a page of
+    small values are held as well as those of a page of large ones beside it."""
+    Hq, Hkv = {0: (4, 2), 16: (4, 2), 32: (8, 2), 64: (64, 8)}[rows]
+    rng = np.random.default_rng(105)
+    lens = [(p + 256 * i, n) for i, (p, n) in enumerate(LENS)]
+    b = Batch(tsv, rng, lens, Hq, Hkv, D, page)
+    pages = torch.arange(b.cache.num_pages, device="cuda")
+    b.cache.v_scale.mul_((2.0 ** ((pages * 7) % 31 - 30.0)).unsqueeze(1))
+    b.q[::2] *= 60.0  # rows of one key, and flat ones
+    out, st = run_of(tsv, b, rows, flags=1 if rows == 0 else 0)
+    assert (st == 0).all()
+    ref, spread, size = R.attention(b.q.double().cpu().numpy(), values(b.cache), b.table, b.prefix, b.offs, b.tree_table, b.sees)
+    tol = _attention_bound(ref, spread, size, b.q.dtype, max(p + n for p, n in lens), D, rows > 0)
+    # Few rows: a weight is two e4m3 terms whose smallest step is 2^-9, the second off by half of it: 2^-10, of 256 for the
+    # step's largest p times scale, or of 2^4 less where the step's scales are no further apart than that: 2^-14 of the row's
+    # largest at most.  Many rows: fp16 of 2^11 or more for the largest, off by 2^-25: 2^-36.  The reference takes p times the
+    # scale in fp32, whose own rounding _attention_bound has.
+    if rows > 0:
+        tol += lost(b, 2.0 ** -36 if rows == 256 else 2.0 ** -14) * (1 + 2.0 ** -7)
+    err = np.abs(out.double().cpu().numpy() - ref)
+    assert (err <= tol).all(), ((err / tol).max(), np.argwhere(err > tol)[:4])
+    # the rows of one key do reach pages of small values
+    assert (np.abs(ref).max(axis=-1) < 2.0 ** -12 * np.abs(ref).max()).any()

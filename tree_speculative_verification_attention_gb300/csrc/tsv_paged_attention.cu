@@ -13,7 +13,8 @@
 //                        bits exactly down to 2^-17 of the row's largest.
 //   p = (hi + lo) / 256  relative to the step's own largest score of the row:
 //                        off by 2^-8 of itself or 2^-18 of that largest (256
-//                        keys: 2^-10 of the step).
+//                        keys: 2^-10 of the step; of weights times V's scale
+//                        2^-14 where scales lie up to 2^4 apart, see below).
 // The terms of q accumulate into the same S; those of p lie side by side on the
 // N axis of one MMA (an MMA of this shape takes its issue time, not its N) and
 // are added in fp32.
@@ -21,7 +22,11 @@
 // bounds whatever the earlier steps held; O of a step is brought to the running
 // maximum in fp32 registers, which also keeps long sums out of the tensor core's
 // accumulator.  The scale of a key's page multiplies S, and the scale of its V
-// page, relative to the step's largest, multiplies P.
+// page, relative to the step's largest, multiplies P.  Where V's scales in a step
+// lie more than 2^4 apart (a page of zeros has 2^-126), the reference is instead
+// the row's largest score plus the logarithm of that ratio, so that a row whose
+// weight lies on pages of small values keeps its bits: a second look at S, taken
+// by such steps alone.
 //
 // Work.  The 128-key blocks of all (request, KV head, row tile) groups form one
 // list, cut into equal ranges, one per CTA (one CTA per SM): every SM gets the
@@ -33,9 +38,10 @@
 // the instructions around them (a warp's chain of dependent steps runs at 6 to
 // 7 cycles an instruction, a third of it waiting for instruction fetches), so
 // what a step costs once matters most.  Measured: 32 requests x 2064 keys x 32
-// heads, 16 rows each, 144 us (3.8 TB/s; without P's arithmetic 104, without O's
-// sums 137, one MMA of four for O 122); one token of 8 requests, 64 heads on 8 of
-// the cache, 26 us; a 20-node tree over 1024 keys, 32 heads, 15.6 us.
+// heads, 16 rows each, 122 us (4.5 TB/s; at 144 us it took 104 without P's
+// arithmetic, 137 without O's sums, 122 with one MMA of four for O); one token of
+// 8 requests, 64 heads on 8 of the cache, 25 us; a 20-node tree over 1024 keys, 32
+// heads, 15.9 us.
 //
 // Roles (20 warps): two softmax warpgroups (warps 0-3 and 4-7; a thread owns a
 // key of each block), which take alternate steps, or, with 64 rows, 32 rows of
@@ -71,6 +77,7 @@ static_assert(256 * kPSoftRegs + 128 * kPAccRegs + 256 * kPRestRegs <= kPThreads
 // Groups of two or three blocks cost more cut than whole: 13 requests of up to 45
 // nodes over up to 144 keys 22 us without, 26 with.
 constexpr PPad kPPad{4, 4};
+constexpr float kPEven = 16.f, kPApart = 40.f;  // of V's scales: see the softmax
 constexpr int kBarSoft = 1;       // and 2: one per softmax warpgroup
 constexpr int kBarAcc = 3, kBarFirst = 4;
 
@@ -108,7 +115,7 @@ struct PCfg {
   static constexpr int kOffFin = kOffMw + 16 * RW;                 // f32 [2][R]: sums of a unit
   static constexpr int kOffUnit = kOffFin + 8 * R;                 // PUnit [2]
   static constexpr int kOffFirst = kOffUnit + 128;                 // PUnit, then i64 [4]: x0, x1, blocks, CTAs
-  static constexpr int kOffScale = kOffFirst + 96;                 // f32 [V stages][20]: (K, V) of 8 pages, V's largest
+  static constexpr int kOffScale = kOffFirst + 96;                 // f32 [V stages][20]: (K, V) of 8 pages, V's largest and smallest
   static constexpr int kOffSv = kOffScale + kVStages * 80;         // f32 [4]
   static constexpr int kOffBar = kOffSv + 16;
   // k_full, k_empty, v_full, v_empty, sc_full (per stage), s_full[4], p_full[4], o_full[2], o_free[2], q_full[2], unit_free[2],
@@ -452,7 +459,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
     };
     Look c0{-1, 0, 0, 0}, c1;
     float2 sc0 = make_float2(0.f, 0.f), sc1 = sc0;
-    float top = 0.f;  // of the lane's block: V's largest scale
+    float top = 0.f, low = 0.f;  // of the lane's block: V's largest scale, and the smallest
     const int blocks = __shfl_sync(0xffffffffu, (int)sRange[0], 0);
     int st = odd, ph = 0;  // of this warp's next block: ring stage and phase
     // Chunk t is issued (c0) while the ids of the next one (c1) are looked up,
@@ -481,12 +488,16 @@ __global__ void __launch_bounds__(kPThreads, 1)
         }
         if (is_v && i == odd) {  // (the copies of the first block go before the wait for its scales)
           top = sc0.y;
-          for (int o = per >> 1; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+          low = c0.id >= 0 ? sc0.y : INFINITY;
+          for (int o = per >> 1; o > 0; o >>= 1) {
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+            low = fminf(low, __shfl_xor_sync(0xffffffffu, low, o));
+          }
         }
         if (is_v && mine_now) {
           float* sc = sScale + st * 20;
           *reinterpret_cast<float2*>(sc + 2 * pg) = sc0;
-          if (pg == 0) sc[16] = top;
+          if (pg == 0) *reinterpret_cast<float2*>(sc + 16) = make_float2(top, low);
         }
         __syncwarp();
         if (lead) {
@@ -697,7 +708,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
         tc_fence_after();
 
         auto step = [&](auto all_c) {
-          constexpr bool ALL = decltype(all_c)::value;
+          constexpr bool ALL = decltype(all_c)::value;  // no masks, and V's scales near each other (else: false)
           if (!ALL && j + halves > nmain) TSV_PWAIT(&d_full[buf], k >> 1);
           const int nh = ALL ? 2 : halves;
           // Rows (of this group) that see a key, one bit each.
@@ -710,81 +721,111 @@ __global__ void __launch_bounds__(kPThreads, 1)
           // thread holds 2 in 2 columns of 8; then three halving exchanges over
           // the 8 thread rows.  best[2 i + c] is column 8 i + 2 (lane % 4) + c.
           constexpr int N0 = RW / 4;
-          float best[N0];
+          float* wmax = sWmax + ((wg * 2 + (nth & 1)) * 4) * RW;
+          auto maxima = [&](auto apart_c, float inv_top) {
+            constexpr bool APART = decltype(apart_c)::value;
+            float best[N0];
 #pragma unroll
-          for (int i = 0; i < N0; ++i) best[i] = -INFINITY;
+            for (int i = 0; i < N0; ++i) best[i] = -INFINITY;
 #pragma unroll 1
-          for (int h = 0; h < nh; ++h) {
-            uint32_t sa[RW / 2], sb[RW / 2];  // the warp's keys 0-15 and 16-31
-            tmem_ld_16x256(s_col + h * R, sa);
-            tmem_ld_16x256(s_col + h * R + (16u << 16), sb);
-            TSV_PWAIT(&sc_full[h ? st1 : st0], h ? ph1 : ph0);
-            const float2* sc = reinterpret_cast<const float2*>(sScale + (h ? st1 : st0) * 20);
-            const float fa = sc[(lg * 32) >> lps].x, fb = sc[(lg * 32 + 16) >> lps].x;
-            tmem_wait_tie(sa);
-            tmem_tie(sb);
-            if (!ALL) {
-              const int key = lg * 32 + (lane >> 2);
-              const int sh = 2 * (lane & 3);
-              const uint32_t v0 = sees(h, key) >> sh, v1 = sees(h, key + 8) >> sh;
-              const uint32_t v2 = sees(h, key + 16) >> sh, v3 = sees(h, key + 24) >> sh;
+            for (int h = 0; h < nh; ++h) {
+              uint32_t sa[RW / 2], sb[RW / 2];  // the warp's keys 0-15 and 16-31
+              tmem_ld_16x256(s_col + h * R, sa);
+              tmem_ld_16x256(s_col + h * R + (16u << 16), sb);
+              TSV_PWAIT(&sc_full[h ? st1 : st0], h ? ph1 : ph0);
+              const float2* sc = reinterpret_cast<const float2*>(sScale + (h ? st1 : st0) * 20);
+              const float fa = sc[(lg * 32) >> lps].x, fb = sc[(lg * 32 + 16) >> lps].x;
+              tmem_wait_tie(sa);
+              tmem_tie(sb);
+              if (!ALL) {
+                const int key = lg * 32 + (lane >> 2);
+                const int sh = 2 * (lane & 3);
+                const uint32_t v0 = sees(h, key) >> sh, v1 = sees(h, key + 8) >> sh;
+                const uint32_t v2 = sees(h, key + 16) >> sh, v3 = sees(h, key + 24) >> sh;
+#pragma unroll
+                for (int i = 0; i < RW / 8; ++i)
+#pragma unroll
+                  for (int c = 0; c < 2; ++c) {
+                    if (!((v0 >> (8 * i + c)) & 1u)) sa[4 * i + c] = 0xFF800000u;
+                    if (!((v1 >> (8 * i + c)) & 1u)) sa[4 * i + 2 + c] = 0xFF800000u;
+                    if (!((v2 >> (8 * i + c)) & 1u)) sb[4 * i + c] = 0xFF800000u;
+                    if (!((v3 >> (8 * i + c)) & 1u)) sb[4 * i + 2 + c] = 0xFF800000u;
+                  }
+              }
+              if constexpr (APART) {
+                const float la = fmaxf(__log2f(sc[(lg * 32) >> lps].y * inv_top), -kPApart);
+                const float lb = fmaxf(__log2f(sc[(lg * 32 + 16) >> lps].y * inv_top), -kPApart);
+#pragma unroll
+                for (int i = 0; i < RW / 8; ++i) {
+                  const float2 f2 = *reinterpret_cast<const float2*>(sFr + buf * R + col0 + 8 * i + 2 * (lane & 3));
+#pragma unroll
+                  for (int c = 0; c < 2; ++c) {
+                    const float xa = fmaxf(__uint_as_float(sa[4 * i + c]), __uint_as_float(sa[4 * i + 2 + c])) * fa;
+                    const float xb = fmaxf(__uint_as_float(sb[4 * i + c]), __uint_as_float(sb[4 * i + 2 + c])) * fb;
+                    const float f = c ? f2.y : f2.x;
+                    best[2 * i + c] = fmaxf(best[2 * i + c], fmaxf(fmaf(xa, f, la), fmaf(xb, f, lb)));
+                  }
+                }
+                continue;
+              }
 #pragma unroll
               for (int i = 0; i < RW / 8; ++i)
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
-                  if (!((v0 >> (8 * i + c)) & 1u)) sa[4 * i + c] = 0xFF800000u;
-                  if (!((v1 >> (8 * i + c)) & 1u)) sa[4 * i + 2 + c] = 0xFF800000u;
-                  if (!((v2 >> (8 * i + c)) & 1u)) sb[4 * i + c] = 0xFF800000u;
-                  if (!((v3 >> (8 * i + c)) & 1u)) sb[4 * i + 2 + c] = 0xFF800000u;
+                  const float x = fmaxf(fmaxf(__uint_as_float(sa[4 * i + c]), __uint_as_float(sa[4 * i + 2 + c])) * fa,
+                                        fmaxf(__uint_as_float(sb[4 * i + c]), __uint_as_float(sb[4 * i + 2 + c])) * fb);
+                  best[2 * i + c] = fmaxf(best[2 * i + c], x);
                 }
             }
+            {
+              int at = 0;  // first index that this thread is left with: the halvings pick its bits from the top
 #pragma unroll
-            for (int i = 0; i < RW / 8; ++i)
+              for (int s = 0; s < 3; ++s) {
+                const int half = (N0 >> s) / 2;  // values kept
+                const int bit = 16 >> s;
+                const bool up = lane & bit;
+                if (half >= 1) {
 #pragma unroll
-              for (int c = 0; c < 2; ++c) {
-                const float x = fmaxf(fmaxf(__uint_as_float(sa[4 * i + c]), __uint_as_float(sa[4 * i + 2 + c])) * fa,
-                                      fmaxf(__uint_as_float(sb[4 * i + c]), __uint_as_float(sb[4 * i + 2 + c])) * fb);
-                best[2 * i + c] = fmaxf(best[2 * i + c], x);
-              }
-          }
-          float* wmax = sWmax + ((wg * 2 + (nth & 1)) * 4) * RW;
-          {
-            int at = 0;  // first index that this thread is left with: the halvings pick its bits from the top
-#pragma unroll
-            for (int s = 0; s < 3; ++s) {
-              const int half = (N0 >> s) / 2;  // values kept
-              const int bit = 16 >> s;
-              const bool up = lane & bit;
-              if (half >= 1) {
-#pragma unroll
-                for (int i = 0; i < (half > 0 ? half : 1); ++i) {
-                  const float send = up ? best[i] : best[i + half];
-                  const float keep = up ? best[i + half] : best[i];
-                  best[i] = fmaxf(keep, __shfl_xor_sync(0xffffffffu, send, bit));
+                  for (int i = 0; i < (half > 0 ? half : 1); ++i) {
+                    const float send = up ? best[i] : best[i + half];
+                    const float keep = up ? best[i + half] : best[i];
+                    best[i] = fmaxf(keep, __shfl_xor_sync(0xffffffffu, send, bit));
+                  }
+                  at += up ? half : 0;
+                } else {
+                  best[0] = fmaxf(best[0], __shfl_xor_sync(0xffffffffu, best[0], bit));
                 }
-                at += up ? half : 0;
-              } else {
-                best[0] = fmaxf(best[0], __shfl_xor_sync(0xffffffffu, best[0], bit));
               }
+              wmax[lg * RW + (at >> 1) * 8 + 2 * (lane & 3) + (at & 1)] = best[0];
             }
-            wmax[lg * RW + (at >> 1) * 8 + 2 * (lane & 3) + (at & 1)] = best[0];
+          };
+          maxima(std::false_type{}, 0.f);
+          // V's scales go to P relative to the step's largest (2^-126 at least: there
+          // is none above 0 that the library writes below it).  Scales further apart
+          // than kPEven: the rows' references are those of p times the scale (as far
+          // as 2^-kPApart), so that a row which attends to a page of small values has
+          // its bits there.
+          const float2 v0 = *reinterpret_cast<const float2*>(sScale + st0 * 20 + 16);
+          const float2 v1 = nh == 2 ? *reinterpret_cast<const float2*>(sScale + st1 * 20 + 16) : v0;
+          const float top = fmaxf(fmaxf(v0.x, v1.x), 0x1p-126f);
+          const float inv_top = __frcp_rn(top);
+          const bool apart = fminf(v0.y, v1.y) * kPEven < top;
+          if (apart) {
+            if (ALL) return false;
+            maxima(std::true_type{}, inv_top);
           }
-          // V's scales, relative to the step's largest, go to P with its 256.
-          const float top0 = sScale[st0 * 20 + 16];
-          // (2^-118 at least: a page of zeros has the scale 2^-126, and 256 over
-          // that is no fp32 number.  Values that small lose bits of their weights.)
-          const float top = fmaxf(nh == 2 ? fmaxf(top0, sScale[st1 * 20 + 16]) : top0, 0x1p-118f);
-          const float inv_top = __fdividef(1.f, top * 0x1p-8f);
           named_bar_sync(kBarSoft + wg, 128);
           // Every warp works out the rows' maxima and factors for itself.
           float m = 0.f;
           bool moved = false;
           if (lane < RW) {
-            m = fmaxf(fmaxf(wmax[lane], wmax[RW + lane]), fmaxf(wmax[2 * RW + lane], wmax[3 * RW + lane])) * fr;
+            m = fmaxf(fmaxf(wmax[lane], wmax[RW + lane]), fmaxf(wmax[2 * RW + lane], wmax[3 * RW + lane])) * (!ALL && apart ? 1.f : fr);
             if (!(m > -INFINITY)) m = -INFINITY;  // nothing seen, or NaN scores only: P is 0 or NaN
             const float mn = fmaxf(mw, m);
-            pw[lane] = m == -INFINITY ? 0.f : -m;
-            pw[RW + lane] = m == -INFINITY ? 1.f : fast_exp2(m - mn);
+            // P takes 2^8 p (256 over the scale of a page of zeros, 2^-126, would be no
+            // fp32 number), the sums p.
+            pw[lane] = m == -INFINITY ? 0.f : 8.f - m;
+            pw[RW + lane] = m == -INFINITY ? 1.f : fast_exp2(m - mn) * (1.f / 256.f);
             pw[2 * RW + lane] = mn == -INFINITY ? 1.f : mw == -INFINITY ? 0.f : fast_exp2(mw - mn);
             moved = mn != mw;
             mw = mn;
@@ -891,9 +932,9 @@ __global__ void __launch_bounds__(kPThreads, 1)
               }
             }
           }
+          return true;
         };
-        if (all) step(std::true_type{});
-        else step(std::false_type{});
+        if (!all || !step(std::true_type{})) step(std::false_type{});
         fence_proxy_async_smem();
         tc_fence_before();
         parrive(&p_full[t & 3], dead);
