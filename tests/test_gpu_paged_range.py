@@ -132,12 +132,12 @@ def lost(b, floor):
     return out
 
 
-@pytest.mark.parametrize("rows", [0, 16, 32, 64])
+@pytest.mark.parametrize("rows", [0, 16, 32, 64, 256])
 @pytest.mark.parametrize("page,D", [(16, 128), (128, 64), (32, 128)])
 def test_pages_whose_values_lie_far_apart(tsv, rows, page, D):
     """V scales 2^30 apart from page to page and rows that attend to hardly more than one key: the weights of a page of
     small values are held as well as those of a page of large ones beside it."""
-    Hq, Hkv = {0: (4, 2), 16: (4, 2), 32: (8, 2), 64: (64, 8)}[rows]
+    Hq, Hkv = {0: (4, 2), 16: (4, 2), 32: (8, 2), 64: (64, 8), 256: (256, 8)}[rows]
     rng = np.random.default_rng(105)
     lens = [(p + 256 * i, n) for i, (p, n) in enumerate(LENS)]
     b = Batch(tsv, rng, lens, Hq, Hkv, D, page)

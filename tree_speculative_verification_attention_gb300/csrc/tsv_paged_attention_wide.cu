@@ -9,21 +9,23 @@
 // Q is a bf16 row times a power of two that moves its largest value to
 // [2^14, 2^15): exact down to 2^-31 of it.  P is 2^11 p with p <= 2^4, rounded to
 // fp16's 11 bits.  The scale of a key's page multiplies S in fp32; the scale of
-// its V page, relative to the largest one so far, multiplies P (weights of V
-// rows whose scale is below 2^-25 of the unit's largest lose bits to fp16's
-// range, below 2^-36 they are nothing).
+// its V page, relative to the largest one so far, multiplies P, and its logarithm
+// counts in the row's reference maximum: the largest p times scale of a row has
+// its 11 bits however small the row's pages are beside others (as far as 2^-40),
+// and a weight 2^-25 below that loses bits to fp16's range, 2^-36 below is nothing.
 //
 // Why another kernel: with rows on N (the kernel for few rows) both products
 // take two e4m3 terms of Q and of P, and every 64 rows their own pass over the
 // keys.  Here the widening is paid once for 256 rows: a 128-node tree x 64 heads
-// on 8 of the cache, 32768 keys: 204 us against 341 (674 TFLOP/s of both
+// on 8 of the cache, 32768 keys: 209 us against 341 (658 TFLOP/s of both
 // products).  When it is taken: at paged_attn_rows.
 //
 // One CTA per SM walks its share of the list of blocks (as the other kernel
 // does; a unit is up to 256 rows, two tiles).  Roles (20 warps):
 //   0-7    softmax: warps 0-3 tile 0, 4-7 tile 1; a thread owns a row.  The
 //          reference maximum moves only when a score passes it by 2^4, and with
-//          it the row of O in TMEM.
+//          it the row of O in TMEM; it falls where a larger V scale comes up (O
+//          then stays as it is).
 //   8-15   widening: a block's codes lie in the upper half of the tile that
 //          takes them as fp16 (Q and the two fp16 rings leave no room beside
 //          them): every warp reads its part into registers, then all write.
@@ -57,6 +59,7 @@ static_assert(256 * kWSoftRegs + 256 * kWConvRegs + 128 * kWRestRegs <= kWThread
 constexpr int kWRows = kPagedWideRows, kWTile = 128;
 constexpr float kWThreshold = 4.f;  // log2: how far a score may pass the reference maximum
 constexpr float kWScale = 2048.f;   // of P: 2^4 x it is within fp16
+constexpr int kWApart = 40;         // log2: V scales that far apart leave a row's weights their bits
 constexpr int kHalf = 64;  // keys of a softmax step
 // What a unit costs beside its blocks (Q, the pipeline's start and end, its
 // results, the join), in blocks.  128 nodes x 64 heads over 32768 keys: 222 us
@@ -78,8 +81,8 @@ struct WCfg {
   static constexpr int kOffReq = kOffCum + 8 * (TSV_MAX_BATCH + 2);  // int4 [TSV_MAX_BATCH]
   static constexpr int kOffFr = kOffReq + 16 * TSV_MAX_BATCH;        // f32 [256]: score factor of a row
   static constexpr int kOffRow = kOffFr + 4 * kWRows;                // i32 [256]: output row
-  static constexpr int kOffScale = kOffRow + 4 * kWRows;             // f32 [4][20]: K's scales of 8 x 16 keys, V's relative ones, V's largest
-  static constexpr int kOffNan = kOffScale + 4 * 80;                 // u32 [8]: tree keys whose V row holds a NaN
+  static constexpr int kOffScale = kOffRow + 4 * kWRows;             // f32 [4][28]: K's scales of 8 x 16 keys, V's relative ones, V's largest, [20..] logarithms
+  static constexpr int kOffNan = kOffScale + 4 * 112;                // u32 [8]: tree keys whose V row holds a NaN
   static constexpr int kOffUnit = kOffNan + 32;                      // PUnit
   static constexpr int kOffFirst = kOffUnit + 64;                    // PUnit, then i64 [4]
   static constexpr int kOffBar = kOffFirst + 96;
@@ -431,7 +434,8 @@ __global__ void __launch_bounds__(kWThreads, 1)
           // ratio first: of zeros' 2^-126 the reciprocal times kWScale is no fp32
           // number), worked out while the codes are on their way.
           top = fmaxf(top, __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(sv))));  // (scales are >= 0)
-          rv = top > 0.f ? sv / top * kWScale : 0.f;
+          const float even = top > 1.f ? 0x1p-64f : 0x1p64f;  // (the division wants an ordinary divisor)
+          rv = top > 0.f ? __fdividef(sv * even, top * even) : 0.f;
         }
         TSV_PWAIT(&kc_full[st], x >> 1);
         take(sK + st * C::kTileBytes, valid, codes);
@@ -439,10 +443,11 @@ __global__ void __launch_bounds__(kWThreads, 1)
         if (dead) break;
         if (w == 0) {
           if (lane < 8) {
-            sScale[(x & 3) * 20 + lane] = sk;
-            sScale[(x & 3) * 20 + 8 + lane] = rv;
+            sScale[(x & 3) * 28 + lane] = sk;
+            sScale[(x & 3) * 28 + 8 + lane] = rv * kWScale;
+            sScale[(x & 3) * 28 + 20 + lane] = fmaxf(__log2f(rv), -(float)kWApart);
           }
-          if (lane == 0) sScale[(x & 3) * 20 + 16] = top;
+          if (lane == 0) sScale[(x & 3) * 28 + 16] = top;
           __syncwarp();
           if (lane == 0) mbar_arrive(&sc_full[x & 3]);
         }
@@ -619,6 +624,7 @@ __global__ void __launch_bounds__(kWThreads, 1)
       const uint32_t o_col = tmem + lane_base + C::kColO + (uint32_t)(tile * D);
       const float fr = sFr[row];
       float m_ref = -INFINITY, l = 0.f, v_ref = 0.f;
+      int room = kWApart;  // how far the reference may still be lowered
       auto half_step = [&](int h, auto masked_c) {
         constexpr bool MASKED = decltype(masked_c)::value;
         const int i = h >> 1, half = h & 1, x = t + i;
@@ -630,9 +636,10 @@ __global__ void __launch_bounds__(kWThreads, 1)
         uint32_t s[2][32];
         tmem_ld32_nowait(s_col, s[0]);
         tmem_ld32_nowait(s_col + 32, s[1]);
-        const float* sc = sScale + (x & 3) * 20;
+        const float* sc = sScale + (x & 3) * 28;
         const float4 k4 = *reinterpret_cast<const float4*>(sc + 4 * half);
         const float4 v4 = *reinterpret_cast<const float4*>(sc + 8 + 4 * half);  // times kWScale, relative to v_top
+        const float4 g4 = *reinterpret_cast<const float4*>(sc + 20 + 4 * half);  // log2 of that
         const float v_top = sc[16];  // V's largest scale so far
         const float f[4] = {k4.x * fr, k4.y * fr, k4.z * fr, k4.w * fr};  // the row's factor of 16 keys each
         uint32_t see[2] = {~0u, ~0u};
@@ -653,6 +660,22 @@ __global__ void __launch_bounds__(kWThreads, 1)
           for (int e = 0; e < 64; ++e)
             if (!((see[e >> 5] >> (e & 31)) & 1u)) s[e >> 5][e & 31] = 0xFF800000u;
         }
+        float alpha = 1.f;
+        if (v_top > v_ref) {  // the same in every thread
+          // What was summed up stays, under a reference that is lower by as much as
+          // the relative scales of its keys now are (powers of two: l goes with it).
+          if (v_ref > 0.f) {
+            const float c = v_ref / v_top;
+            const int down = min(127 - (int)(__float_as_uint(c) >> 23), room);
+            const float up = __uint_as_float((uint32_t)(127 + down) << 23);
+            room -= down;
+            m_ref -= (float)down;
+            l *= up;
+            alpha = c * up;  // 1 for scales that are powers of two
+          }
+          v_ref = v_top;
+        }
+        const float g[4] = {g4.x, g4.y, g4.z, g4.w};
         float hmax = -INFINITY;
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
@@ -664,17 +687,13 @@ __global__ void __launch_bounds__(kWThreads, 1)
             b0 = fmax3(b0, __uint_as_float(z[e]), __uint_as_float(z[e + 1]));
             b1 = fmax3(b1, __uint_as_float(z[e + 2]), __uint_as_float(z[e + 3]));
           }
-          hmax = fmaxf(hmax, fmaxf(b0, b1) * f[q]);
+          hmax = fmaxf(hmax, fmaf(fmaxf(b0, b1), f[q], g[q]));
         }
-        float alpha = 1.f;
         if (hmax > m_ref + kWThreshold) {
-          alpha = fast_exp2(m_ref - hmax);  // 0 when m_ref = -inf
+          const float a = fast_exp2(m_ref - hmax);  // 0 when m_ref = -inf
           m_ref = hmax;
-        }
-        l *= alpha;
-        if (v_top > v_ref) {  // the same in every thread
-          alpha *= v_ref / v_top;
-          v_ref = v_top;
+          l *= a;
+          alpha *= a;
         }
         if (h > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
           TSV_PWAIT(&pv_done[2 * tile + (1 - half)], cnt[tile] + ((h - 1) >> 1));
