@@ -174,7 +174,8 @@ tsv_status tsv_paged_tree_attention_workspace_size(tsv_handle h, tsv_dtype dtype
  *   status_d (out) int32 [B]: TSV_OK; TSV_ERR_INVALID_ARG when the request's
  *                 lengths do not fit N, max_nodes or its page lists, or a page id
  *                 is out of range (its outputs are undefined, nothing out of
- *                 range is read); TSV_ERR_TIMEOUT on a device-side timeout
+ *                 range is read); TSV_ERR_TIMEOUT on a device-side timeout, and
+ *                 from later calls until the workspace is zeroed again
  *   flags         TSV_ATTN_DEFAULT or TSV_ATTN_SIMT (CUDA cores for bf16 too)
  * Rows past a request's lengths may hold anything.  A NaN in a V row reaches
  * only the nodes that see the row.

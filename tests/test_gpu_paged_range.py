@@ -158,3 +158,26 @@ def test_pages_whose_values_lie_far_apart(tsv, rows, page, D):
     assert (err <= tol).all(), ((err / tol).max(), np.argwhere(err > tol)[:4])
     # the rows of one key do reach pages of small values
     assert (np.abs(ref).max(axis=-1) < 2.0 ** -12 * np.abs(ref).max()).any()
+
+
+# ------------------------------------------------------------------ workspaces
+
+
+@pytest.mark.parametrize("rows", [16, 32, 64, 256])
+def test_a_timeout_is_not_overwritten(tsv, rows):
+    """Words of a workspace that are set stand for CTAs that gave up a wait before the requests were checked: the checks do
+    not report success over them, in this call or a later one.  Zeroed again, the workspace is as good as new."""
+    Hq, Hkv = {16: (4, 2), 32: (8, 2), 64: (64, 8), 256: (256, 8)}[rows]
+    b = Batch(tsv, np.random.default_rng(106), LENS, Hq, Hkv, 128, 16)
+    if rows == 256:
+        wide_workspace(tsv, b)
+    ws = tsv.paged_tree_attention_workspace(b.q, b.cache, len(LENS), 8)
+    good, st = b.run(tsv, workspace=ws)
+    assert (st == 0).all()
+    ws.fill_(1)
+    for _ in range(2):
+        _, st = b.run(tsv, workspace=ws)
+        assert (st == tsv.TSV_ERR_TIMEOUT).all()
+    ws.zero_()
+    out, st = b.run(tsv, workspace=ws)
+    assert torch.equal(out, good) and (st == 0).all()

@@ -298,8 +298,9 @@ struct PagedAttnArgs {
   float scale;
 };
 // Tensor-core kernel: row tiles of R = 16, 32 or 64 query rows; its workspace
-// holds one completion counter per CTA, then two partial results per CTA (O
-// [R][D], then maxima and sums [2][R]).
+// holds one word per request (set by a CTA that gave up a wait for it), one
+// completion counter per CTA, then two partial results per CTA (O [R][D], then
+// maxima and sums [2][R]).
 constexpr int32_t kPagedWideRows = 256;
 constexpr int32_t kPagedWideCtas = 160;  // at most: shared memory holds the weights of so many parts
 // Rows of a unit of the tensor-core kernels: 16, 32, 64 (keys on the TMEM lanes)
@@ -324,7 +325,7 @@ struct PagedAttnLayout {
 };
 inline PagedAttnLayout paged_attn_layout(int grid, int32_t R, int32_t D) {
   PagedAttnLayout l;
-  l.part_o = ((size_t)grid * 4 + 255) & ~(size_t)255;
+  l.part_o = ((size_t)(TSV_MAX_BATCH + grid) * 4 + 255) & ~(size_t)255;
   l.part_ml = l.part_o + (size_t)grid * 2 * R * D * 4;
   l.total = l.part_ml + (size_t)grid * 2 * 2 * R * 4;
   return l;

@@ -213,10 +213,11 @@ __device__ __forceinline__ void tmem_ld8_nowait(uint32_t taddr, uint32_t (&r)[8]
 template <int D, int R>
 __global__ void __launch_bounds__(kPThreads, 1)
     paged_attn_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
-                      const __grid_constant__ PagedAttnArgs a, int32_t* __restrict__ counters,
+                      const __grid_constant__ PagedAttnArgs a, int32_t* words,
                       float* __restrict__ part_o, float* __restrict__ part_ml) {
   using C = PCfg<D, R>;
   constexpr int SK = C::kKStages, SV = C::kVStages, NS = C::kNS;
+  int32_t* counters = words + TSV_MAX_BATCH;  // (the first words: requests that a wait was given up for)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sK = smem + C::kOffK;
@@ -662,7 +663,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
       bool bad = !paged_request(a, b, &r);
       if (!bad) bad = paged_bad_page(a, b, r, lane, 32);
       bad = __any_sync(0xffffffffu, bad);
-      if (lane == 0) a.status[b] = bad ? TSV_ERR_INVALID_ARG : TSV_OK;
+      if (lane == 0) report_check(a, words, b, bad);
     }
   } else if (warp < 8) {
     // ------------------------------------------------------------ softmax: a thread owns a key
@@ -1122,7 +1123,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
   tc_fence_before();
   __syncthreads();
   if (tid == 0 && *abort_v)
-    for (PUnit u = *sFirst; u.valid; list.next(u)) a.status[u.b] = TSV_ERR_TIMEOUT;
+    for (PUnit u = *sFirst; u.valid; list.next(u)) report_timeout(a, words, u.b);
   if (warp == kPSWarp) {
     tc_fence_after();
     tmem_dealloc(tmem, C::kTmem);

@@ -164,9 +164,10 @@ struct WUnit {
 template <int D>
 __global__ void __launch_bounds__(kWThreads, 1)
     paged_attn_wide_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
-                           const __grid_constant__ PagedAttnArgs a, int32_t* __restrict__ counters, float* __restrict__ part_o,
+                           const __grid_constant__ PagedAttnArgs a, int32_t* words, float* __restrict__ part_o,
                            float* __restrict__ part_ml) {
   using C = WCfg<D>;
+  int32_t* counters = words + TSV_MAX_BATCH;  // (the first words: requests that a wait was given up for)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sQ = smem + C::kOffQ;
@@ -875,14 +876,14 @@ __global__ void __launch_bounds__(kWThreads, 1)
       bool bad = !paged_request(a, b, &r);
       if (!bad) bad = paged_bad_page(a, b, r, lane, 32);
       bad = __any_sync(0xffffffffu, bad);
-      if (lane == 0) a.status[b] = bad ? TSV_ERR_INVALID_ARG : TSV_OK;
+      if (lane == 0) report_check(a, words, b, bad);
     }
   }
   __syncwarp();
   tc_fence_before();
   __syncthreads();
   if (tid == 0 && *abort_v)
-    for (PUnit u = *sFirst; u.valid; list.next(u)) a.status[u.b] = TSV_ERR_TIMEOUT;
+    for (PUnit u = *sFirst; u.valid; list.next(u)) report_timeout(a, words, u.b);
   if (warp == kWMmaWarp) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);

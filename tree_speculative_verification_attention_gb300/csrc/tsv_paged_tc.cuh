@@ -226,6 +226,21 @@ __device__ __forceinline__ void plist_setup(const PagedAttnArgs& a, int R, PPad 
   }
 }
 
+// Status of a request.  One CTA checks it, others may give up a wait for it, in any
+// order: a word of the workspace makes the timeout win.  Each side writes its own
+// word, then looks at (or overwrites) the other's, with a fence between: whichever
+// fence comes first, the last store to the status is the timeout's.
+__device__ __forceinline__ void report_timeout(const PagedAttnArgs& a, int32_t* timeouts, int b) {
+  *static_cast<volatile int32_t*>(timeouts + b) = 1;
+  __threadfence();
+  *static_cast<volatile int32_t*>(a.status + b) = TSV_ERR_TIMEOUT;
+}
+__device__ __forceinline__ void report_check(const PagedAttnArgs& a, const int32_t* timeouts, int b, bool bad) {
+  *static_cast<volatile int32_t*>(a.status + b) = bad ? TSV_ERR_INVALID_ARG : TSV_OK;
+  __threadfence();
+  if (*static_cast<const volatile int32_t*>(timeouts + b)) *static_cast<volatile int32_t*>(a.status + b) = TSV_ERR_TIMEOUT;
+}
+
 // Joins the partials of CTAs cf .. cl of a group (slots of R rows: part_ml holds
 // maxima, then sums; part_o unscaled rows) into `rows` output rows.
 template <int D, int R>
