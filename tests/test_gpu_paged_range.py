@@ -7,7 +7,7 @@ import pytest
 import torch
 
 import _paged_ref as R
-from test_gpu_paged import Batch, _attention_bound, dev, i32, values, wide_workspace
+from test_gpu_paged import Batch, _attention_bound, accepted, dev, i32, values, wide_workspace
 
 pytestmark = pytest.mark.gpu
 
@@ -181,3 +181,51 @@ def test_a_timeout_is_not_overwritten(tsv, rows):
     ws.zero_()
     out, st = b.run(tsv, workspace=ws)
     assert torch.equal(out, good) and (st == 0).all()
+
+
+# ------------------------------------------------------------------ order of launches
+
+
+@pytest.mark.parametrize("between", ["rope", "append", "attention", "commit"])
+def test_overlapped_verification_behind_a_paged_call(tsv, between):
+    """A verification that may run beside the call before it still comes behind the one before that: here a rotation by 0 that
+    writes its logits in one long wave of blocks."""
+    rng = np.random.default_rng(107)
+    B, n, V = 19, 128, 65536
+    N = B * n
+    want = torch.randn(N, V, generator=torch.Generator("cuda").manual_seed(1), device="cuda")
+    logits = torch.empty_like(want)
+    parent = i32(np.tile(np.arange(-1, n - 1), B))
+    offs = i32(np.arange(B + 1) * n)
+    tokens = torch.cat([want[:1].argmax(-1), want.argmax(-1)[:-1]]).int()  # every node accepted
+    zeros, freq = i32(np.zeros(N)), tsv.rope_frequencies(1024, device="cuda")[0]
+    b = Batch(tsv, rng, [(20, 3)], 2, 2, 64, 16, spare=4)
+    kv = b.q.clone()
+    small = tsv.rope_frequencies(64, device="cuda")[0]
+    ws = torch.zeros(tsv.tsv_tree_verify_greedy_workspace_size(tsv.handle(), B, N, V), dtype=torch.uint8, device="cuda")
+    g = tsv.tree_verify_greedy(want, tokens, parent, offs, workspace=ws)
+    assert (g["accept_len"] == n - 1).all()
+    d = dict(table=dev(b.table), tree=dev(b.tree_table), plen=i32(b.prefix), offs=i32(b.offs), anc=dev(b.words), path=i32([0, 1, 2]), last=i32([2]))
+    out, st = torch.empty_like(b.q), torch.empty(1, dtype=torch.int32, device="cuda")
+    res = dict(new_len=torch.empty_like(st), status=torch.empty_like(st))
+    calls = {
+        "rope": lambda: tsv.rope(kv, d["path"], small, out=out),
+        "append": lambda: tsv.paged_append(b.cache, d["tree"], kv, kv, d["offs"], status=st),
+        "attention": lambda: tsv.paged_tree_attention(b.q, b.cache, d["table"], d["plen"], d["offs"], tree_table=d["tree"], anc=d["anc"],
+                                                      max_nodes=3, flags=1, out=out, status=st),
+        "commit": lambda: tsv.paged_commit(b.cache, d["table"], d["tree"], d["plen"], d["offs"], d["path"], d["last"], out=res),
+    }
+    for _ in range(3):
+        logits.fill_(-1.0)
+        logits[:, 0] = 0.0
+        for r in g.values():
+            r.fill_(-1)
+        torch.cuda.synchronize()
+        with tsv.verify_overlap(tsv.TSV_OVERLAP_GREEDY):
+            tsv.rope(want.view(N, 64, 1024), zeros, freq, out=logits.view(N, 64, 1024))
+            calls[between]()
+            tsv.tree_verify_greedy(logits, tokens, parent, offs, workspace=ws, out=g)  # (nothing else is launched)
+        torch.cuda.synchronize()
+        assert torch.equal(logits, want)
+        assert (g["status"] == 0).all() and (g["accept_len"] == n - 1).all()
+        assert torch.equal(g["bonus"].long(), want.argmax(-1)[n - 1::n])

@@ -95,8 +95,11 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volati
 // and its memory operations are visible, so every kernel calls it before its
 // first global-memory access: results are those of plain serialised launches,
 // only launch latency overlaps.  pdl_trigger() lets the next kernel be
-// scheduled (once every CTA of this one has called it or exited).  Both are
-// no-ops for a kernel launched without the attribute.
+// scheduled (once every CTA of this one has called it or exited).  It comes
+// behind pdl_wait(): a verification that may run beside the kernel before it
+// does not wait for that kernel, so that kernel must not let it start before
+// the one in front of it has completed.  Both are no-ops for a kernel launched
+// without the attribute.
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 

@@ -44,8 +44,8 @@ template <typename T, int D>
 __global__ void __launch_bounds__(32 * kSimtWarps) paged_attn_simt_kernel(const PagedAttnArgs a) {
   constexpr int kSimtHeads = simt_heads<D>();
   constexpr int E = D / 32;  // elements of V per lane
+  pdl_wait();  // the previous kernel's results are visible from here on
   pdl_trigger();
-  pdl_wait();
   __shared__ float sq[kSimtHeads][D];
   __shared__ float so[kSimtWarps][kSimtHeads][D];
   __shared__ float sm[kSimtWarps][kSimtHeads], sl[kSimtWarps][kSimtHeads];

@@ -140,8 +140,8 @@ __global__ void __launch_bounds__(32 * kPagedWriteMaxWarps) paged_write_kernel(c
   constexpr int LPR = D / 16;                      // lanes of a row
   constexpr int ROWS = paged_write_rows(D);        // rows of a warp
   static_assert(LPR * ROWS == 32, "a lane holds a part of one row");
-  pdl_trigger();
   pdl_wait();  // the previous kernel's results are visible from here on
+  pdl_trigger();
   extern __shared__ float4 angle_table[];  // cosines [page_size][width], then sines
   __shared__ float amax[2][2][kPagedWriteMaxWarps];
   __shared__ int32_t spath[kCommit ? TSV_MAX_NODES : 1];

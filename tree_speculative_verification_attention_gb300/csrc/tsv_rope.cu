@@ -84,8 +84,8 @@ constexpr int kVectors = 4;  // vectors of a thread in flight
 template <typename T, int E, bool INTERLEAVED>
 __global__ void __launch_bounds__(kRopeThreads, 5) rope_kernel(const RopeArgs a, int rows_per_cta, const FastDiv by_row,
                                                             const FastDiv by_items, const FastDiv by_half) {
+  pdl_wait();  // the previous kernel's results are visible from here on
   pdl_trigger();
-  pdl_wait();
   constexpr bool SPLIT = !INTERLEAVED || E == 1;
   constexpr int PARTS = SPLIT ? 2 : 1, BATCH = kVectors / PARTS;
   constexpr int STEP = INTERLEAVED && SPLIT ? 2 : E;  // from one rotated item to the next
