@@ -1,6 +1,7 @@
 """Ranges of the paged 8-bit cache's operators on the GPU: scales far from one another, the smallest and largest ones, full
 batches.  Against the 64-bit forms of tests/_paged_ref.py under the bounds of test_gpu_paged.py."""
 import math
+from fractions import Fraction
 
 import numpy as np
 import pytest
@@ -229,3 +230,29 @@ def test_overlapped_verification_behind_a_paged_call(tsv, between):
         assert torch.equal(logits, want)
         assert (g["status"] == 0).all() and (g["accept_len"] == n - 1).all()
         assert torch.equal(g["bonus"].long(), want.argmax(-1)[n - 1::n])
+
+
+# ------------------------------------------------------------------ angles
+
+
+def test_rope_angles_to_the_last_bit(tsv):
+    """Pairs (1, 0) turn into (cosine, sine) of the angle.  A frequency is kept to half of 2^-64 turns, and nothing of its
+    product with the position is dropped: the angle is off by |position| 2^-65 turns.  Then cosine and sine of its upper part
+    (2^-22 of each), turned on by the rest r of at most 64 x 2^-32 turns: 2^-22 more for the rounding, r^2 / 2 < 2^-47 for the
+    second order, and 2^-22 r < 2^-45 where sine and rest cancel."""
+    two_pi = Fraction("6.283185307179586476925286766559005768394338798750211641949889")
+    steps = [k + f for k in (0, 1, 2, 3, 63, 64, 65, 127, 128, 1000) for f in (0.5, 0.9, 0.99)]
+    w = [2 * math.pi * s / 2 ** 32 for s in steps] + [2 * math.pi * s / 2 ** 64 for s in steps]
+    w += [math.pi - x for x in w[:30]] + [math.pi * (1 - 2.0 ** -k) for k in range(2, 40)] + [10000.0 ** (-i / 64) for i in range(64)]
+    half = len(w)
+    pos = [1, -1, 3, 1 << 20, 2 ** 31 - 1, -2 ** 31]
+    x = torch.zeros(len(pos), 1, 2 * half, device="cuda")
+    x[..., :half] = 1.0
+    got = tsv.rope(x, i32(pos), torch.tensor(w, dtype=torch.float64, device="cuda")).double().cpu().numpy()[:, 0]
+    for n, p in enumerate(pos):
+        for i, f in enumerate(w):
+            t = Fraction(f) * p / two_pi
+            t = float((t - round(t)) * two_pi)
+            for have, ref in ((got[n, i], math.cos(t)), (got[n, half + i], math.sin(t))):
+                tol = 2.0 ** -21 * abs(ref) + 2.0 ** -44 + 2 * math.pi * abs(p) * 2.0 ** -65
+                assert abs(have - ref) <= tol, (p, f, have, ref, abs(have - ref) / tol)

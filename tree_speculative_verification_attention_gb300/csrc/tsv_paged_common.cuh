@@ -60,9 +60,8 @@ __device__ __forceinline__ float finite_abs(float x) {
 }
 
 // Rotary angles.  A frequency is kept as a fraction of a turn per position in
-// 64-bit fixed point, so that position x frequency modulo one turn is an
-// integer product: its error is |position| x 2^-65 turns, below fp32's for
-// every int32 position.
+// 64-bit fixed point, rounded to nearest, so that position x frequency modulo one
+// turn is an integer product: its error is |position| x 2^-65 turns.
 __device__ __forceinline__ uint64_t rope_turns(double w) {
   // w = m 2^(e - 1075) with a 53-bit integer m; 2^64 w / (2 pi) = m C 2^(e - 1077)
   // with C = 2^66 / (2 pi).  Integers throughout: fp64 runs at a small fraction
@@ -73,20 +72,22 @@ __device__ __forceinline__ uint64_t rope_turns(double w) {
   const uint64_t m = (u & 0xFFFFFFFFFFFFFull) | (1ull << 52);
   const uint64_t hi = __umul64hi(m, C), lo = m * C;
   const int sh = 1077 - e;
-  uint64_t t;
-  if (e == 0 || sh >= 128) t = 0;
-  else if (sh >= 64) t = hi >> (sh - 64);
-  else if (sh > 0) t = (lo >> sh) | (hi << (64 - sh));
+  uint64_t t;  // the product's bits from bit sh on, and the one below them
+  if (e == 0 || sh > 128) t = 0;
+  else if (sh > 64) t = (sh < 128 ? hi >> (sh - 64) : 0ull) + ((hi >> (sh - 65)) & 1ull);
+  else if (sh == 64) t = hi + (lo >> 63);
+  else if (sh > 0) t = ((lo >> sh) | (hi << (64 - sh))) + ((lo >> (sh - 1)) & 1ull);
   else t = sh > -64 ? lo << -sh : 0;
   return (u >> 63) ? 0ull - t : t;
 }
 
 __device__ __forceinline__ void rope_cos_sin(int32_t position, uint64_t turns, float* c, float* s) {
-  const int32_t frac = (int32_t)(uint32_t)((turns * (uint64_t)(int64_t)position) >> 32);  // [-1/2, 1/2) turn x 2^32
-  // The fraction's 32 bits as a float and what that left (up to 2^6 units, 1.5
-  // fp32 steps of the angle), which turns the result on.
-  const float f = (float)frac;
-  const float rest = (float)(frac - (int32_t)f) * 1.4629180792671596e-9f;  // pi 2^-31
+  const uint64_t t = turns * (uint64_t)(int64_t)position;  // fraction of a turn x 2^64, as a signed number in [-1/2, 1/2)
+  // Its upper 25 bits are a float; cosine and sine of them are turned on by the
+  // rest (64 x 2^-32 turns at most, so that its square, 2^-46, does not count).
+  const uint32_t hi = (uint32_t)(t >> 32), top = (hi + 64u) & ~127u;
+  const float f = (float)(int32_t)top;
+  const float rest = fmaf((float)(uint32_t)t, 0x1p-32f, (float)(int32_t)(hi - top)) * 1.4629180792671596e-9f;  // pi 2^-31
   float s0, c0;
   sincospif(f * 4.656612873077392578125e-10f, &s0, &c0);  // 2^-31: half turns
   *c = fmaf(-s0, rest, c0);
