@@ -197,3 +197,36 @@ def test_frequencies_refusals(paged):
         bad = list(good)
         bad[i] = x
         assert f(*bad) == 1, (i, x)
+
+
+# ------------------------------------------------------------------ devices
+
+
+def test_the_first_call_on_a_device_leaves_the_current_one(paged, monkeypatch):
+    """A handle that a call makes (tsv_create makes its device current) does not change the caller's device."""
+    from types import SimpleNamespace
+
+    now = [0]
+
+    class Device:
+        def __init__(self, index):
+            self.index = index
+
+        def __enter__(self):
+            self.before, now[0] = now[0], self.index
+
+        def __exit__(self, *error):
+            now[0] = self.before
+
+    def create(index):
+        now[0] = index
+        return 7
+
+    monkeypatch.setattr(paged.torch.cuda, "device", Device)
+    monkeypatch.setattr(paged, "_HANDLES", {})
+    monkeypatch.setattr(paged, "handle", create)
+    assert paged._handle(1) == 7 and now == [0]
+    monkeypatch.setattr(paged, "tsv_paged_tree_attention_workspace_size", lambda h, *shape: 16 if h == 7 else None)
+    monkeypatch.setattr(paged, "_workspace", lambda nbytes, device: (nbytes, device.index))
+    q = SimpleNamespace(device=SimpleNamespace(index=1), dtype=paged.torch.bfloat16, shape=(1, 2, 64))
+    assert paged.paged_tree_attention_workspace(q, SimpleNamespace(c=None), 1, 1) == (16, 1) and now == [0]

@@ -154,7 +154,11 @@ def _code(dt):
 
 
 def _handle(index):
-    return _HANDLES.get(index) or handle(index)
+    h = _HANDLES.get(index)
+    if h is None:
+        with torch.cuda.device(index):  # (tsv_create makes the device current)
+            h = handle(index)
+    return h
 
 
 def _want(ok, what):
@@ -304,7 +308,7 @@ def paged_append(cache, page_table, k, v, row_offsets, start=None, positions=Non
 
 def paged_tree_attention_workspace(q, cache, B, max_nodes, flags=TSV_ATTN_DEFAULT):
     """A zero-filled workspace for calls of this shape, one at a time."""
-    need = tsv_paged_tree_attention_workspace_size(handle(q.device.index), _code(q.dtype), cache.c, B, max_nodes, q.shape[1], flags)
+    need = tsv_paged_tree_attention_workspace_size(_handle(q.device.index), _code(q.dtype), cache.c, B, max_nodes, q.shape[1], flags)
     return _workspace(need, q.device)
 
 
