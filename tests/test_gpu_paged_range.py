@@ -8,7 +8,7 @@ import pytest
 import torch
 
 import _paged_ref as R
-from test_gpu_paged import Batch, _attention_bound, accepted, dev, i32, values, wide_workspace
+from test_gpu_paged import Batch, _attention_bound, accepted, dev, i32, same_codes, values, wide_workspace
 
 pytestmark = pytest.mark.gpu
 
@@ -256,3 +256,14 @@ def test_rope_angles_to_the_last_bit(tsv):
             for have, ref in ((got[n, i], math.cos(t)), (got[n, half + i], math.sin(t))):
                 tol = 2.0 ** -21 * abs(ref) + 2.0 ** -44 + 2 * math.pi * abs(p) * 2.0 ** -65
                 assert abs(have - ref) <= tol, (p, f, have, ref, abs(have - ref) / tol)
+
+
+def test_commit_rejects_the_largest_accept_len(tsv):
+    """accept_len + 1 does not overflow."""
+    b = Batch(tsv, np.random.default_rng(108), [(5, 3), (7, 4)], 2, 2, 64, 16)
+    before = values(b.cache)
+    for big in (2 ** 31 - 1, 2 ** 31 - 2, -2 ** 31):
+        o = tsv.paged_commit(b.cache, dev(b.table), dev(b.tree_table), i32(b.prefix), i32(b.offs), i32([0, 1, 2, 0, 1, 2, 3]),
+                             i32([big, big]))
+        assert o["status"].tolist() == [1, 1] and o["new_len"].tolist() == [-1, -1]
+    same_codes(b.cache, before)

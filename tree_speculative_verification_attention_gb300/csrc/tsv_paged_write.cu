@@ -152,7 +152,7 @@ __global__ void __launch_bounds__(32 * kPagedWriteMaxWarps) paged_write_kernel(c
   const int ps = C.page_size;
   const int off = a.offsets[b], n_rows = a.offsets[b + 1] - off;
   const int start = a.start ? a.start[b] : 0;
-  const int n = kCommit ? a.accept_len[b] + 1 : n_rows;
+  const int n = kCommit ? min(a.accept_len[b], TSV_MAX_NODES) + 1 : n_rows;  // (accept_len may be anything)
   // The request's lengths, then every page id (and path entry) that it needs:
   // one that is wrong rejects the whole request.
   bool bad = off < 0 || n_rows < 0 || n_rows > a.max_rows || (int64_t)off + n_rows > a.N || start < 0 ||
