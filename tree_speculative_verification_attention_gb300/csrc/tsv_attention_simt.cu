@@ -51,8 +51,8 @@ __global__ void __launch_bounds__(kSimtWarps * 32)
                           const int32_t* __restrict__ node_offsets,
                           const uint32_t* __restrict__ anc, int32_t B, int32_t Hq, int32_t Hkv,
                           float scale_log2) {
-  pdl_trigger();
   pdl_wait();  // the previous kernel's results are visible from here on
+  pdl_trigger();
   constexpr int E = D / 32;
   const int h = blockIdx.x;
   const int gi = blockIdx.y;

@@ -29,8 +29,8 @@ __global__ void __launch_bounds__(kCommitThreads)
                      const int32_t* __restrict__ node_offsets, const int32_t* __restrict__ path,
                      const int32_t* __restrict__ accept_len, int32_t* __restrict__ new_len,
                      int32_t* __restrict__ status) {
-  pdl_trigger();
   pdl_wait();  // the previous kernel's results are visible from here on
+  pdl_trigger();
   __shared__ int32_t spath[TSV_MAX_NODES];
   __shared__ int bad;
   const int b = blockIdx.x;

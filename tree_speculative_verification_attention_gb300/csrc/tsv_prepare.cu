@@ -16,8 +16,8 @@ __global__ void __launch_bounds__(TSV_MAX_NODES)
     tree_prepare_kernel(const int32_t* __restrict__ parent, const int32_t* __restrict__ node_offsets,
                         uint32_t* __restrict__ anc, int32_t* __restrict__ depth,
                         int32_t* __restrict__ status) {
-  pdl_trigger();
   pdl_wait();  // the previous kernel's results are visible from here on
+  pdl_trigger();
   __shared__ uint32_t A[2][TSV_MAX_NODES][TSV_ANC_WORDS];
   __shared__ int32_t J[2][TSV_MAX_NODES];
   __shared__ int bad;

@@ -212,8 +212,8 @@ __global__ void __launch_bounds__(kArgmaxThreads)
                        const int32_t* __restrict__ parent, const int32_t* __restrict__ node_offsets,
                        int32_t* __restrict__ path, int32_t* __restrict__ accept_len,
                        int32_t* __restrict__ bonus, int32_t* __restrict__ status) {
-  pdl_trigger();
   pdl_wait();  // the previous kernel's results are visible from here on
+  pdl_trigger();
   __shared__ WalkSmem w;
   const int b = blockIdx.x;
   const int off = node_offsets[b], n = node_offsets[b + 1] - off;
@@ -1656,8 +1656,8 @@ __device__ void expand_small(const float* __restrict__ row, int64_t lo, int64_t 
 __global__ void __launch_bounds__(kSelThreads)
     tree_expand_kernel(const float* __restrict__ logits, int64_t V, int k, int ncl,
                        int32_t* __restrict__ tokens) {
-  pdl_trigger();
   pdl_wait();  // the previous kernel's results are visible from here on
+  pdl_trigger();
   __shared__ __align__(16) float pub[2][4];
   __shared__ SelSmem sel;
   __shared__ float red[128];
@@ -1754,8 +1754,8 @@ __global__ void __launch_bounds__(256)
                       int32_t* __restrict__ out_parent, int32_t* __restrict__ out_tokens,
                       int32_t* __restrict__ out_source, int32_t* __restrict__ out_count,
                       int32_t* __restrict__ status) {
-  pdl_trigger();
   pdl_wait();  // the previous kernel's results are visible from here on
+  pdl_trigger();
   __shared__ int32_t up[TSV_MAX_NODES], ut[TSV_MAX_NODES], usrc[TSV_MAX_NODES];
   __shared__ int32_t ipar[kMergeMaxInput], itok[kMergeMaxInput], imap[kMergeMaxInput];
   __shared__ int bad, ucount_s;
