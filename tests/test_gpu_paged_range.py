@@ -267,3 +267,42 @@ def test_commit_rejects_the_largest_accept_len(tsv):
                              i32([big, big]))
         assert o["status"].tolist() == [1, 1] and o["new_len"].tolist() == [-1, -1]
     same_codes(b.cache, before)
+
+
+# ------------------------------------------------------------------ full batches
+
+
+@pytest.mark.parametrize("rows", [0, 16, 32, 64, 256])
+def test_full_batches_through_a_step(tsv, rows):
+    """128 requests, where the lists of a call are full: attention, the commit of a path whose rows end in the next page (the
+    cache against the 64-bit form), and attention over the longer prefixes."""
+    Hq, Hkv, most = {0: (4, 2, 8), 16: (4, 2, 8), 32: (8, 2, 8), 64: (32, 4, 8), 256: (64, 2, 8)}[rows]
+    rng = np.random.default_rng(109)
+    lens = [(int(rng.integers(0, 300)), int(rng.integers(1, most + 1))) for _ in range(128)]
+    lens[5] = (15, most)
+    b = Batch(tsv, rng, lens, Hq, Hkv, 64, 16, spare=130)
+    kw = dict(flags=1 if rows == 0 else 0)
+    if rows == 256:
+        kw["workspace"] = wide_workspace(tsv, b)
+    out, st = b.run(tsv, **kw)
+    b.check(out, st, rows > 0)
+    used = set(b.table[b.table >= 0]) | set(b.tree_table[b.tree_table >= 0])
+    free = [i for i in range(b.cache.num_pages) if i not in used]
+    path, acc, ref = np.full(int(b.offs[-1]), -1), [], values(b.cache)
+    b.table = np.concatenate([b.table, np.full((128, 1), -1, dtype=np.int32)], axis=1)
+    for i, (p, n) in enumerate(lens):
+        way = accepted(rng, b.parent[b.offs[i]:b.offs[i] + n], n)
+        path[b.offs[i]:b.offs[i] + len(way)] = way
+        acc.append(len(way) - 1)
+        if -(-(p + len(way)) // 16) > -(-p // 16):
+            b.table[i, -(-p // 16)] = free.pop()
+        k, v = ref.rows(b.tree_table[i], n)
+        ref.write(b.table[i], p, k[way], v[way])
+    o = tsv.paged_commit(b.cache, dev(b.table), dev(b.tree_table), i32(b.prefix), i32(b.offs), i32(path), i32(acc))
+    assert (o["status"] == 0).all()
+    same_codes(b.cache, ref)
+    b.lens = [(p + a + 1, n) for (p, n), a in zip(lens, acc)]
+    b.prefix = np.array([p for p, _ in b.lens])
+    assert o["new_len"].tolist() == b.prefix.tolist()
+    out, st = b.run(tsv, **kw)
+    b.check(out, st, rows > 0)
