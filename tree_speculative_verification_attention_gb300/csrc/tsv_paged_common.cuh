@@ -83,11 +83,12 @@ __device__ __forceinline__ uint64_t rope_turns(double w) {
 
 __device__ __forceinline__ void rope_cos_sin(int32_t position, uint64_t turns, float* c, float* s) {
   const uint64_t t = turns * (uint64_t)(int64_t)position;  // fraction of a turn x 2^64, as a signed number in [-1/2, 1/2)
-  // Its upper 25 bits are a float; cosine and sine of them are turned on by the
-  // rest (64 x 2^-32 turns at most, so that its square, 2^-46, does not count).
-  const uint32_t hi = (uint32_t)(t >> 32), top = (hi + 64u) & ~127u;
-  const float f = (float)(int32_t)top;
-  const float rest = fmaf((float)(uint32_t)t, 0x1p-32f, (float)(int32_t)(hi - top)) * 1.4629180792671596e-9f;  // pi 2^-31
+  // Its upper half rounded to a float; cosine and sine of that are turned on by
+  // the rest (64 x 2^-32 turns at most, so that its square, 2^-46, does not count;
+  // an upper half that rounds to 2^31 comes back as one less).
+  const int32_t hi = (int32_t)(uint32_t)(t >> 32);
+  const float f = (float)hi;
+  const float rest = fmaf((float)(uint32_t)t, 0x1p-32f, (float)(hi - (int32_t)f - (f == 0x1p31f ? 1 : 0))) * 1.4629180792671596e-9f;  // pi 2^-31
   float s0, c0;
   sincospif(f * 4.656612873077392578125e-10f, &s0, &c0);  // 2^-31: half turns
   *c = fmaf(-s0, rest, c0);
