@@ -309,11 +309,13 @@ constexpr int32_t kPagedWideCtas = 160;  // at most: shared memory holds the wei
 // share a block's cost, but units that are few are cut into many parts, and
 // parts cost more the more rows they have.  Measured (us; 8 query heads a KV
 // head, D = 128), 32 / 64 / 256 rows a unit:
-//   1 request x 16384 keys x 8 KV heads:   64 rows 31 / 45 / 53, 256 rows 69 / 66 / 90, 512 rows 121 / 103 / 102
-//   1 request x 32768 keys x 8 KV heads:   1024 rows - / 341 / 204
-//   4 requests x 4096 keys x 8 KV heads:   128 rows 50 / 45 / 64, 256 rows 85 / 68 / 79
-//   13 requests x 256 keys x 8 KV heads:   256 rows 73 / 56 / 58; 2048 keys 168 / 117 / 78
-//   32 requests x 4096 keys x 8 KV heads:  40 rows 164 / 113 / 199, 128 rows 311 / 221 / 207, 256 rows 600 / 418 / 244
+//   1 request x 16384 keys x 8 KV heads:   64 rows 32 / 46 / 62, 256 rows 67 / 63 / 99, 512 rows 118 / 100 / 93
+//   1 request x 32768 keys x 8 KV heads:   1024 rows - / 333 / 199
+//   4 requests x 4096 keys x 8 KV heads:   128 rows 50 / 44 / 60, 256 rows 88 / 66 / 70
+//   13 requests x 256 keys x 8 KV heads:   256 rows 77 / 55 / 45; 2048 keys 178 / 117 / 84
+//   32 requests x 4096 keys x 8 KV heads:  40 rows 169 / 111 / 200, 128 rows 318 / 215 / 203, 256 rows 612 / 399 / 241
+// (128 rows over long prefixes of many requests stay with 64 a unit: 6 % there,
+// against 36 % the other way with few requests.)
 inline int32_t paged_attn_rows(int64_t rows, int64_t groups, int64_t keys) {
   if (rows <= 32) return rows <= 16 ? 16 : 32;
   const int64_t wide = groups * ((rows + kPagedWideRows - 1) / kPagedWideRows);

@@ -17,7 +17,7 @@
 // Why another kernel: with rows on N (the kernel for few rows) both products
 // take two e4m3 terms of Q and of P, and every 64 rows their own pass over the
 // keys.  Here the widening is paid once for 256 rows: a 128-node tree x 64 heads
-// on 8 of the cache, 32768 keys: 209 us against 341 (658 TFLOP/s of both
+// on 8 of the cache, 32768 keys: 205 us against 333 (670 TFLOP/s of both
 // products).  When it is taken: at paged_attn_rows.
 //
 // One CTA per SM walks its share of the list of blocks (as the other kernel
@@ -774,9 +774,10 @@ __global__ void __launch_bounds__(kWThreads, 1)
             }
           }
         }
-        // (0 for a row that sees nothing.  v_ref may be 2^-126, a page of zeros': a
-        // factor of its own.)
-        const float inv = l == 0.f ? 0.f : (1.f / kWScale) / l;
+        // (0 for a row that sees nothing.  v_ref may be 2^-126, a page of zeros', or
+        // little more: then it is a factor of its own.)
+        const bool tiny = v_ref < 0x1p-60f;
+        const float inv = l == 0.f ? 0.f : (1.f / kWScale) / l * (tiny ? 1.f : v_ref);
         __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out);
         const bool whole = sUnit->whole();
         const int slot = 2 * (int)blockIdx.x + (k == 0 ? 0 : 1);
@@ -792,7 +793,11 @@ __global__ void __launch_bounds__(kWThreads, 1)
             tmem_ld32(o_col + cc, o);
             if (row < u.rows) {
 #pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] = l == 0.f ? 0.f : (bad[cc / 32] >> e) & 1u ? NAN : o[e] * inv * v_ref;
+              for (int e = 0; e < 32; ++e) o[e] = l == 0.f ? 0.f : (bad[cc / 32] >> e) & 1u ? NAN : o[e] * inv;
+              if (tiny) {
+#pragma unroll
+                for (int e = 0; e < 32; ++e) o[e] *= v_ref;
+              }
               if (whole) {
 #pragma unroll
                 for (int e = 0; e < 32; e += 8)
