@@ -809,7 +809,8 @@ __global__ void __launch_bounds__(kPThreads, 1)
           const float2 v0 = *reinterpret_cast<const float2*>(sScale + st0 * 20 + 16);
           const float2 v1 = nh == 2 ? *reinterpret_cast<const float2*>(sScale + st1 * 20 + 16) : v0;
           const float top = fmaxf(fmaxf(v0.x, v1.x), 0x1p-126f);
-          const float inv_top = __frcp_rn(top);
+          float inv_top;
+          asm("rcp.approx.f32 %0, %1;" : "=f"(inv_top) : "f"(top));  // (of 2^127 too, unlike __fdividef)
           const bool apart = fminf(v0.y, v1.y) * kPEven < top;
           if (apart) {
             if (ALL) return false;
