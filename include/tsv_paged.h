@@ -18,7 +18,7 @@
  * page holds one fp32 scale per KV head for K and one for V: value = code x
  * scale.  The library writes scales that are powers of two, so a change of
  * scale moves a code's exponent and loses nothing until values fall below
- * 2^-6 x scale; it reads any finite scale >= 0.
+ * 2^-6 x scale; it reads any finite scale >= 0.  (A page of zeros has 2^-126.)
  *
  * A request has two lists of pages, each a row of a page table: its verified
  * rows 0 .. prefix_len - 1 lie in its prefix pages (row r in page r /
@@ -179,6 +179,16 @@ tsv_status tsv_paged_tree_attention_workspace_size(tsv_handle h, tsv_dtype dtype
  *   flags         TSV_ATTN_DEFAULT or TSV_ATTN_SIMT (CUDA cores for bf16 too)
  * Rows past a request's lengths may hold anything.  A NaN in a V row reaches
  * only the nodes that see the row.
+ *   Which kernel runs follows from the shapes alone: rows per KV head (max_nodes
+ * x Hq / Hkv), requests, KV heads, and the keys that `table` has room for.  The
+ * same call gives the same bits again; a wider table can change the last ones.
+ *   Accuracy.  Scores and sums are fp32.  On the tensor cores a weight (its
+ * softmax term times the V scale of its page) is rounded: with few rows to
+ * 2^-8 of itself (two e4m3 terms) or 2^-18 of the largest among 256 keys (2^-14
+ * where their V scales lie up to 2^4 apart), with many to 2^-12 of itself
+ * (fp16) or 2^-36 of the row's largest; V scales further apart count in what a
+ * row's weights are relative to, up to 2^40.  q is held to 2^-17 of its row's
+ * largest value with few rows, 2^-31 with many.
  */
 tsv_status tsv_paged_tree_attention(tsv_handle h, tsv_dtype dtype, const void* q_d, int64_t q_stride_n,
                                     int64_t q_stride_h, const tsv_paged_cache* cache,

@@ -270,7 +270,7 @@ __global__ void __launch_bounds__(kWThreads, 1)
     __syncthreads();
     tc_fence_after();
   };
-  WUnit u;
+  WUnit u{};
   // CTAs cf .. cf + parts - 1 share the unit's group; part c is in slot(c).
   struct Group {
     int cf, parts, first;  // first: the group is the first unit of CTA cf, or its last

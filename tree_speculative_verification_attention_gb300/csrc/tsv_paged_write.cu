@@ -16,8 +16,10 @@
 // One row part a lane rather than two or four: 64 registers hold it, so 32
 // warps share an SM and one's loads run under another's rounding (18,200 rows of
 // 8 requests, 8 heads of 128, bf16, rotated: 33 us, 3.4 TB/s; 16 values of four
-// rows a lane: 88 us).  What is left there is issue, half of the cycles: about
-// 250 instructions for a lane's 32 values, and the angles.  Few rows cost a chain
+// rows a lane: 88 us).  Nothing is saturated there (issue 57 %, DRAM 29 % of their
+// peaks): a lane's 32 values take about 250 instructions and the angles, behind two
+// barriers a head, and 64 registers, all that the 1024 threads of a 128-row page
+// leave, spill 88 to 184 bytes.  Few rows cost a chain
 // of loads (lengths, pages, rows, scales): 20 rows x 32 heads 4.4 us, a commit of
 // their path 3.9 us, of 128 requests' paths 10 us.
 //

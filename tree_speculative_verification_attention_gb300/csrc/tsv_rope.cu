@@ -47,8 +47,9 @@ template <int BYTES>
 using Raw = std::conditional_t<BYTES == 16, uint4,
                                std::conditional_t<BYTES == 8, uint2, std::conditional_t<BYTES == 4, uint32_t, unsigned short>>>;
 
-// n / d of 0 <= n < 2^31 by a multiplication: (umulhi(n, m) + n) >> s with
-// s = ceil(log2 d), m = floor(2^32 (2^s - d) / d) + 1.
+// n / d of 0 <= n < 2^31 by a multiplication (Granlund and Montgomery's division by
+// an invariant): (umulhi(n, m) + n) >> s with s = ceil(log2 d), m = floor(2^32
+// (2^s - d) / d) + 1.
 struct FastDiv {
   uint32_t d, m;
   int s;
