@@ -8,7 +8,7 @@ import pytest
 import torch
 
 import _paged_ref as R
-from test_gpu_paged import Batch, _attention_bound, accepted, dev, i32, same_codes, values, wide_workspace
+from test_gpu_paged import KINDS, Batch, _attention_bound, accepted, dev, i32, same_codes, values, wide_workspace
 
 pytestmark = pytest.mark.gpu
 
@@ -306,3 +306,81 @@ def test_full_batches_through_a_step(tsv, rows):
     assert o["new_len"].tolist() == b.prefix.tolist()
     out, st = b.run(tsv, **kw)
     b.check(out, st, rows > 0)
+
+
+# ------------------------------------------------------------------ captured steps
+
+
+@pytest.mark.parametrize("kind", KINDS, ids=lambda k: k[0])
+def test_a_captured_step_gives_what_eager_calls_give(tsv, kind):
+    """Rotation, append, attention and commit in one graph, replayed with other positions, lengths and paths on the device:
+    results and cache bit for bit as from single calls, those on a stream of their own too."""
+    rng = np.random.default_rng(110)
+    dtype, flags = kind[1], kind[2]
+    b = Batch(tsv, rng, [(100, 9), (31, 3), (0, 6)], 8, 2, 128, 16, dtype=dtype, spare=20)
+    N, B = len(b.q), 3
+    used = set(b.table[b.table >= 0]) | set(b.tree_table[b.tree_table >= 0])
+    free = [i for i in range(b.cache.num_pages) if i not in used]
+    table = np.concatenate([b.table, np.full((B, 2), -1, dtype=np.int32)], axis=1)
+    for i in range(B):
+        for x in range(table.shape[1]):
+            if table[i, x] < 0 and free:
+                table[i, x] = free.pop()
+    freq = tsv.rope_frequencies(128, device="cuda")[0]
+    d = dict(table=dev(table), tree=dev(b.tree_table), plen=i32(b.prefix), offs=i32(b.offs), anc=dev(b.words), pos=i32(np.zeros(N)),
+             path=i32(np.full(N, -1)), acc=i32(np.zeros(B)))
+    kv = dev(rng.normal(size=(N, 2, 2, 128)), dtype)
+    start = [t.clone() for t in (b.cache.k.view(torch.uint8), b.cache.v.view(torch.uint8), b.cache.k_scale, b.cache.v_scale)]
+
+    def restore():
+        for to, was in zip((b.cache.k.view(torch.uint8), b.cache.v.view(torch.uint8), b.cache.k_scale, b.cache.v_scale), start):
+            to.copy_(was)
+
+    def buffers():
+        return dict(q=torch.empty_like(b.q), out=torch.full_like(b.q, 7.0), s1=i32([7] * B), s2=i32([7] * B),
+                    res=dict(new_len=i32([7] * B), status=i32([7] * B)),
+                    ws=tsv.paged_tree_attention_workspace(b.q, b.cache, B, 9, flags=flags))
+
+    def step(o, stream=None):
+        tsv.rope(b.q, d["pos"], freq, out=o["q"], stream=stream)
+        tsv.paged_append(b.cache, d["tree"], kv[:, 0], kv[:, 1], d["offs"], positions=d["pos"], inv_freq=freq, status=o["s1"], stream=stream)
+        tsv.paged_tree_attention(o["q"], b.cache, d["table"], d["plen"], d["offs"], tree_table=d["tree"], anc=d["anc"], max_nodes=9,
+                                 flags=flags, out=o["out"], workspace=o["ws"], status=o["s2"], stream=stream)
+        tsv.paged_commit(b.cache, d["table"], d["tree"], d["plen"], d["offs"], d["path"], d["acc"], max_nodes=9, out=o["res"], stream=stream)
+
+    def results(o):
+        torch.cuda.synchronize()
+        c = b.cache
+        return [t.clone() for t in (o["q"], o["out"], o["s1"], o["s2"], o["res"]["new_len"], o["res"]["status"],
+                                    c.k.view(torch.uint8), c.v.view(torch.uint8), c.k_scale, c.v_scale)]
+
+    o, graph, side = buffers(), torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    step(o)
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        step(o)
+    for lens in ([100, 31, 0], [17, 0, 5], [64, 16, 1], [3, -1, 2]):
+        path, acc = np.full(N, -1), []
+        for i in range(B):
+            lo, hi = b.offs[i], b.offs[i + 1]
+            way = accepted(rng, b.parent[lo:hi], hi - lo)
+            path[lo:lo + len(way)] = way
+            acc.append(len(way) - 1)
+        for name, x in (("plen", lens), ("path", path), ("acc", acc), ("pos", rng.integers(0, 5000, N))):
+            d[name].copy_(i32(x))
+        restore()
+        o["out"].fill_(7.0)  # (the rows of a rejected request stay)
+        graph.replay()
+        got = results(o)
+        restore()
+        e = buffers()
+        step(e)
+        for n, (x, y) in enumerate(zip(got, results(e))):
+            assert torch.equal(x, y), (lens, n)
+        restore()
+        e = buffers()
+        side.wait_stream(torch.cuda.current_stream())
+        step(e, side)
+        for n, (x, y) in enumerate(zip(got, results(e))):
+            assert torch.equal(x, y), (lens, n)
+        assert got[3].tolist() == got[5].tolist() == [1 if p < 0 else 0 for p in lens]
