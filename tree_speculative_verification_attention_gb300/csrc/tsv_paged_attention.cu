@@ -767,16 +767,16 @@ __global__ void __launch_bounds__(kPThreads, 1)
                     best[2 * i + c] = fmaxf(best[2 * i + c], fmaxf(fmaf(xa, f, la), fmaf(xb, f, lb)));
                   }
                 }
-                continue;
+              } else {
+#pragma unroll
+                for (int i = 0; i < RW / 8; ++i)
+#pragma unroll
+                  for (int c = 0; c < 2; ++c) {
+                    const float x = fmaxf(fmaxf(__uint_as_float(sa[4 * i + c]), __uint_as_float(sa[4 * i + 2 + c])) * fa,
+                                          fmaxf(__uint_as_float(sb[4 * i + c]), __uint_as_float(sb[4 * i + 2 + c])) * fb);
+                    best[2 * i + c] = fmaxf(best[2 * i + c], x);
+                  }
               }
-#pragma unroll
-              for (int i = 0; i < RW / 8; ++i)
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                  const float x = fmaxf(fmaxf(__uint_as_float(sa[4 * i + c]), __uint_as_float(sa[4 * i + 2 + c])) * fa,
-                                        fmaxf(__uint_as_float(sb[4 * i + c]), __uint_as_float(sb[4 * i + 2 + c])) * fb);
-                  best[2 * i + c] = fmaxf(best[2 * i + c], x);
-                }
             }
             {
               int at = 0;  // first index that this thread is left with: the halvings pick its bits from the top
