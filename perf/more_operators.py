@@ -291,7 +291,7 @@ def prepare(case, seed):
             s["out"] = dict(copy_src=ints(B), copy_dst=ints(B), status=ints(B))
         else:
             s["out"] = dict(refs=ints(case["pool"]), tables=[torch.full_like(s["table"], -1)], new_id=ints(case["pool"]),
-                            move_src=ints(case["pool"]), move_dst=ints(case["pool"]), moved=ints(1))
+                            move_src=torch.full_like(s["refs"], -1), move_dst=torch.full_like(s["refs"], -1), moved=ints(1), status=ints(1))
     return s
 
 
