@@ -75,7 +75,8 @@ typedef enum {
   TSV_ERR_UNSUPPORTED = 3,
   TSV_ERR_CUDA = 4,
   TSV_ERR_TIMEOUT = 5,
-  TSV_ERR_SCRATCH_LIMIT = 6  /* the call needs more than the fixed scratch of a _noalloc entry point */
+  TSV_ERR_SCRATCH_LIMIT = 6, /* the call needs more than the fixed scratch of a _noalloc entry point */
+  TSV_ERR_NO_PAGES = 7       /* the pool has too few free pages left (tsv_pages.h) */
 } tsv_status;
 
 typedef enum { TSV_F32 = 0, TSV_BF16 = 1 } tsv_dtype;

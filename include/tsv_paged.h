@@ -8,6 +8,7 @@
  *   tsv_paged_append          rotates, quantises and writes new K/V rows
  *   tsv_paged_tree_attention  tsv_tree_attention over prefix and tree pages
  *   tsv_paged_commit          the accepted path's rows, moved behind the prefix
+ *   tsv_paged_chunk_attention causal attention of new tokens in the prefix pages
  *
  * The conventions of tsv.h hold for every call here (handles, streams,
  * ownership, status arrays, the zero-filled workspace).  In addition a call may
@@ -220,6 +221,45 @@ tsv_status tsv_paged_commit(tsv_handle h, const tsv_paged_cache* cache, const ts
                             const int32_t* node_offsets_d, const int32_t* path_d,
                             const int32_t* accept_len_d, int32_t B, int32_t N, int32_t max_nodes,
                             int32_t* new_len_d, int32_t* status_d, void* stream);
+
+/* Workspace bytes of tsv_paged_chunk_attention (zero-fill once, as in tsv.h),
+ * for calls with these B, N and max_rows at most, with and without a window. */
+tsv_status tsv_paged_chunk_attention_workspace_size(tsv_handle h, tsv_dtype dtype, const tsv_paged_cache* cache, int32_t B,
+                                                    int32_t N, int32_t max_rows, int32_t Hq, uint32_t flags, size_t* bytes);
+
+/*
+ * tsv_paged_chunk_attention — causal attention of a chunk of new tokens over the
+ * pages that hold them already: request b's new rows are rows start[b] ..
+ * start[b] + n_b - 1 of its prefix pages (tsv_paged_append wrote them there),
+ * n_b = row_offsets[b+1] - row_offsets[b], and the i-th of them sees rows
+ * 0 .. start[b] + i, or, under a window, the last `window` of those,
+ *   out[i,h] = sum_j softmax_j(scale * <q[i,h], k_j>) v_j.
+ * A prompt in one piece (start 0) or in several, prompts of some requests beside
+ * single tokens of others, or single tokens alone.  The lengths are read on the
+ * device, so a captured call follows them.
+ *   dtype         TSV_BF16 or TSV_F32: q and out
+ *   q_d           element (n, h, d) at n * q_stride_n + h * q_stride_h + d;
+ *                 16-byte aligned pointer and strides (in bytes)
+ *   start_d       int32 [B] rows in front of the new ones
+ *   row_offsets_d int32 [B+1]: rows of q and out of each request; rows of q in
+ *                 no request are not read, and those of out keep what they hold
+ *   out_d   (out) [N, Hq, D] contiguous, 16-byte aligned
+ *   max_rows      >= 1; no request has more new rows
+ *   window        >= 0; 0: no window
+ *   scale         softmax scale; 0 means 1/sqrt(D)
+ *   status_d (out) int32 [B]: as in tsv_paged_tree_attention
+ *   flags         TSV_ATTN_DEFAULT or TSV_ATTN_SIMT (CUDA cores; a check rather
+ *                 than a way to run long chunks)
+ * Rows past a request's lengths may hold anything.  A NaN in a V row reaches
+ * only the rows that see it.  Values of V (code x scale) are 2^127 at most over
+ * the number of keys that a row sees, so that sums before the division are
+ * finite.
+ */
+tsv_status tsv_paged_chunk_attention(tsv_handle h, tsv_dtype dtype, const void* q_d, int64_t q_stride_n, int64_t q_stride_h,
+                                     const tsv_paged_cache* cache, const tsv_page_table* table, const int32_t* start_d,
+                                     const int32_t* row_offsets_d, void* out_d, int32_t B, int32_t N, int32_t max_rows,
+                                     int32_t Hq, int32_t window, float scale, void* workspace_d, size_t workspace_bytes,
+                                     int32_t* status_d, uint32_t flags, void* stream);
 
 #ifdef __cplusplus
 }

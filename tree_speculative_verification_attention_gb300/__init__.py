@@ -27,7 +27,7 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libtsv.so")
 
 (TSV_OK, TSV_ERR_INVALID_ARG, TSV_ERR_BAD_TREE, TSV_ERR_UNSUPPORTED, TSV_ERR_CUDA, TSV_ERR_TIMEOUT,
- TSV_ERR_SCRATCH_LIMIT) = range(7)
+ TSV_ERR_SCRATCH_LIMIT, TSV_ERR_NO_PAGES) = range(8)
 TSV_F32, TSV_BF16 = 0, 1
 TSV_ATTN_DEFAULT, TSV_ATTN_SIMT = 0, 1
 TSV_MAX_NODES, TSV_MAX_BATCH, TSV_ANC_WORDS = 256, 128, 8
@@ -434,6 +434,11 @@ def selftest_bounded_wait(arrive, device=None, stream=None):
 
 
 # The paged 8-bit cache (include/tsv_paged.h).
-from .paged import (PAGED_EXPORTED, PagedCache, paged_append, paged_commit, paged_tree_attention,  # noqa: E402,F401
+from .paged import (PAGED_EXPORTED, PagedCache, paged_append, paged_chunk_attention,  # noqa: E402,F401
+                    paged_chunk_attention_workspace, paged_commit, paged_tree_attention,
                     paged_tree_attention_workspace, rope, rope_frequencies)
 from . import paged  # noqa: E402,F401
+
+# Page management (include/tsv_pages.h).
+from .pages import PAGES_EXPORTED, PagePool, pages_compact, pages_copy, pages_fork, pages_resize  # noqa: E402,F401
+from . import pages  # noqa: E402,F401

@@ -266,6 +266,7 @@ const char* tsv_status_string(int status) {
     case TSV_ERR_CUDA: return "CUDA error";
     case TSV_ERR_TIMEOUT: return "device-side wait timed out";
     case TSV_ERR_SCRATCH_LIMIT: return "shape needs more than the fixed scratch of the no-allocation entry point";
+    case TSV_ERR_NO_PAGES: return "too few free pages in the pool";
     default: return "unknown status";
   }
 }

@@ -8,7 +8,7 @@
 #include <stdint.h>
 
 #include "../../include/tsv.h"
-#include "../../include/tsv_paged.h"
+#include "../../include/tsv_pages.h"
 
 typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
                                   const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
@@ -296,6 +296,10 @@ struct PagedAttnArgs {
   int32_t* status;
   int32_t B, N, max_nodes, Hq, G;
   float scale;
+  // tsv_paged_chunk_attention: the nodes are the prefix pages' rows prefix_len ..
+  // prefix_len + n - 1 themselves, and each sees the rows up to its own
+  // (window > 0: the last `window` of them).
+  int32_t chunk, window;
 };
 // Tensor-core kernel: row tiles of R = 16, 32 or 64 query rows; its workspace
 // holds one word per request (set by a CTA that gave up a wait for it), one
@@ -339,5 +343,60 @@ cudaError_t paged_attention_wide_set_attributes(int32_t D);
 cudaError_t launch_paged_attention_wide(const CUtensorMap& tk, const CUtensorMap& tv, const PagedAttnArgs& a, int num_sms, void* ws,
                                         cudaStream_t st);
 cudaError_t launch_paged_attention_simt(const PagedAttnArgs& a, bool bf16, cudaStream_t st);
+
+// Page lists and the pool they draw on (tsv_pages.h).
+struct PagesResizeArgs {
+  tsv_page_pool pool;
+  tsv_page_table table;
+  int32_t* pages;
+  const int32_t* rows;
+  int32_t B, page_size;
+  int32_t* status;
+};
+struct PagesForkArgs {
+  tsv_page_pool pool;
+  tsv_page_table from, to;
+  const int32_t* from_pages;
+  int32_t* to_pages;
+  const int32_t* source;
+  const int32_t* rows;
+  int32_t F, B, page_size;
+  int32_t* copy_src;
+  int32_t* copy_dst;
+  int32_t* status;
+};
+struct PagesCompactArgs {
+  tsv_page_pool pool;
+  int32_t* refs_out;
+  tsv_page_lists lists[TSV_PAGES_MAX_LISTS];
+  int32_t n;
+  int32_t* new_id;
+  int32_t* move_src;
+  int32_t* move_dst;
+  int32_t* moved;
+  int32_t* status;
+};
+struct PagesCopyArgs {
+  tsv_paged_cache cache;
+  const int32_t* src;
+  const int32_t* dst;
+  int32_t n;
+  const int32_t* count;  // NULL: n
+  int32_t* status;
+};
+cudaError_t launch_pages_resize(const PagesResizeArgs& a, cudaStream_t st);
+cudaError_t launch_pages_fork(const PagesForkArgs& a, cudaStream_t st);
+cudaError_t launch_pages_compact(const PagesCompactArgs& a, cudaStream_t st);
+cudaError_t launch_pages_copy(const PagesCopyArgs& a, int num_sms, cudaStream_t st);
+
+// Host-side checks that the paged entries share (tsv_paged_api.cu).
+struct DeviceScope {  // makes the handle's device current for the length of a call
+  int before = -1;
+  bool ok = true;
+  explicit DeviceScope(int device);
+  ~DeviceScope();
+};
+// A cache's fields; fills in the strides of dimensions of size 1.
+tsv_status check_paged_cache(const tsv_paged_cache* in, tsv_paged_cache* c);
 
 }  // namespace tsv

@@ -10,31 +10,23 @@
 
 using namespace tsv;
 
-namespace {
+namespace tsv {
 
-inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
-inline int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
-tsv_status cuda_status(cudaError_t e) { return e == cudaSuccess ? TSV_OK : TSV_ERR_CUDA; }
-
-// Makes the handle's device current for the length of a call.
-struct DeviceScope {
-  int before = -1;
-  bool ok = true;
-  explicit DeviceScope(int device) {
-    int now = -1;
-    ok = cudaGetDevice(&now) == cudaSuccess;
-    if (ok && now != device) {
-      ok = cudaSetDevice(device) == cudaSuccess;
-      if (ok) before = now;
-    }
+DeviceScope::DeviceScope(int device) {
+  int now = -1;
+  ok = cudaGetDevice(&now) == cudaSuccess;
+  if (ok && now != device) {
+    ok = cudaSetDevice(device) == cudaSuccess;
+    if (ok) before = now;
   }
-  ~DeviceScope() {
-    if (before >= 0) cudaSetDevice(before);
-  }
-};
+}
+DeviceScope::~DeviceScope() {
+  if (before >= 0) cudaSetDevice(before);
+}
 
-// Checks a cache and fills in the strides of dimensions of size 1.
-tsv_status check_cache(const tsv_paged_cache* in, tsv_paged_cache* c) {
+static inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+
+tsv_status check_paged_cache(const tsv_paged_cache* in, tsv_paged_cache* c) {
   if (!in) return TSV_ERR_INVALID_ARG;
   *c = *in;
   if (!c->k_d || !c->v_d || !c->k_scale_d || !c->v_scale_d || !aligned16(c->k_d) || !aligned16(c->v_d))
@@ -52,6 +44,13 @@ tsv_status check_cache(const tsv_paged_cache* in, tsv_paged_cache* c) {
   return TSV_OK;
 }
 
+}  // namespace tsv
+
+namespace {
+
+inline int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+tsv_status cuda_status(cudaError_t e) { return e == cudaSuccess ? TSV_OK : TSV_ERR_CUDA; }
+
 tsv_status check_table(const tsv_page_table* t, int32_t B, const tsv_paged_cache& c) {
   if (!t || !t->ids_d || t->pages < 1) return TSV_ERR_INVALID_ARG;
   if (B > 1 && t->stride < t->pages) return TSV_ERR_INVALID_ARG;
@@ -65,10 +64,10 @@ bool rows_aligned(const void* p, int64_t sn, int64_t sh, int64_t esz) {
 }
 
 tsv_status check_attention(tsv_handle h, tsv_dtype dtype, const tsv_paged_cache* cache, tsv_paged_cache* c, int32_t B,
-                           int32_t max_nodes, int32_t Hq, uint32_t flags) {
+                           int32_t max_nodes, int32_t most, int32_t Hq, uint32_t flags) {
   if (!h || (dtype != TSV_F32 && dtype != TSV_BF16) || (flags & ~TSV_ATTN_SIMT)) return TSV_ERR_INVALID_ARG;
-  if (B < 1 || B > TSV_MAX_BATCH || max_nodes < 1 || max_nodes > TSV_MAX_NODES) return TSV_ERR_INVALID_ARG;
-  const tsv_status st = check_cache(cache, c);
+  if (B < 1 || B > TSV_MAX_BATCH || max_nodes < 1 || max_nodes > most) return TSV_ERR_INVALID_ARG;
+  const tsv_status st = check_paged_cache(cache, c);
   if (st != TSV_OK) return st;
   if (Hq < 1 || Hq % c->Hkv) return TSV_ERR_INVALID_ARG;
   if (c->Hkv > 65535) return TSV_ERR_UNSUPPORTED;
@@ -88,6 +87,23 @@ tsv_status encode_pages(tsv_handle h, CUtensorMap* map, const void* base, const 
 }
 
 bool paged_uses_tc(tsv_dtype dtype, uint32_t flags) { return dtype == TSV_BF16 && !(flags & TSV_ATTN_SIMT); }
+
+// The tensor-core kernel of R query rows a unit.
+tsv_status launch_tree_kernels(tsv_handle h, const PagedAttnArgs& a, int32_t R, void* workspace_d, cudaStream_t stream) {
+  const bool wide = R == kPagedWideRows;
+  const uint32_t bit = 1u << ((wide ? 3 : R == 16 ? 0 : R == 32 ? 1 : 2) + (a.cache.D == 128 ? 4 : 0));
+  if (!(h->paged_attr_mask & bit)) {
+    if ((wide ? paged_attention_wide_set_attributes(a.cache.D) : paged_attention_set_attributes(a.cache.D, R)) != cudaSuccess)
+      return TSV_ERR_CUDA;
+    h->paged_attr_mask |= bit;
+  }
+  CUtensorMap tk, tv;
+  tsv_status st = encode_pages(h, &tk, a.cache.k_d, a.cache);
+  if (st == TSV_OK) st = encode_pages(h, &tv, a.cache.v_d, a.cache);
+  if (st != TSV_OK) return st;
+  if (wide) return cuda_status(launch_paged_attention_wide(tk, tv, a, h->num_sms, workspace_d, stream));
+  return cuda_status(launch_paged_attention(tk, tv, a, R, h->num_sms, workspace_d, stream));
+}
 
 // Head groups that one CTA of an append or commit takes in turn, of about
 // `pages` pages to write.  What it does once (the angles, or the chain of loads
@@ -192,7 +208,7 @@ tsv_status tsv_paged_append(tsv_handle h, tsv_dtype dtype, const tsv_paged_cache
   if (!h || (dtype != TSV_F32 && dtype != TSV_BF16) || (flags & ~TSV_ROPE_INTERLEAVED)) return TSV_ERR_INVALID_ARG;
   if (B < 1 || B > TSV_MAX_BATCH || N < 0 || max_rows < 0 || !row_offsets_d || !status_d) return TSV_ERR_INVALID_ARG;
   PagedWriteArgs a{};
-  tsv_status st = check_cache(cache, &a.cache);
+  tsv_status st = check_paged_cache(cache, &a.cache);
   if (st == TSV_OK) st = check_table(table, B, a.cache);
   if (st != TSV_OK) return st;
   if (inv_freq_d && (rotary_dim < 2 || rotary_dim % 2 || rotary_dim > a.cache.D)) return TSV_ERR_INVALID_ARG;
@@ -236,7 +252,7 @@ tsv_status tsv_paged_tree_attention_workspace_size(tsv_handle h, tsv_dtype dtype
                                                    size_t* bytes) {
   tsv_paged_cache c;
   if (!bytes) return TSV_ERR_INVALID_ARG;
-  const tsv_status st = check_attention(h, dtype, cache, &c, B, max_nodes, Hq, flags);
+  const tsv_status st = check_attention(h, dtype, cache, &c, B, max_nodes, TSV_MAX_NODES, Hq, flags);
   if (st != TSV_OK) return st;
   const int32_t R = paged_attn_rows((int64_t)max_nodes * (Hq / c.Hkv), (int64_t)B * c.Hkv, TSV_PAGED_MAX_ROWS);  // for every table
   *bytes = paged_uses_tc(dtype, flags) ? paged_attn_layout(h->num_sms, R, c.D).total : 0;
@@ -252,7 +268,7 @@ tsv_status tsv_paged_tree_attention(tsv_handle h, tsv_dtype dtype, const void* q
                                     size_t workspace_bytes, int32_t* status_d, uint32_t flags,
                                     void* stream) {
   PagedAttnArgs a{};
-  tsv_status st = check_attention(h, dtype, cache, &a.cache, B, max_nodes, Hq, flags);
+  tsv_status st = check_attention(h, dtype, cache, &a.cache, B, max_nodes, TSV_MAX_NODES, Hq, flags);
   if (st == TSV_OK) st = check_table(table, B, a.cache);
   if (st == TSV_OK && tree_table) st = check_table(tree_table, B, a.cache);
   if (st != TSV_OK) return st;
@@ -286,21 +302,7 @@ tsv_status tsv_paged_tree_attention(tsv_handle h, tsv_dtype dtype, const void* q
   a.Hq = Hq;
   a.G = Hq / a.cache.Hkv;
   a.scale = scale == 0.f ? 1.f / sqrtf((float)a.cache.D) : scale;
-  if (use_tc) {
-    const bool wide = R == kPagedWideRows;
-    const uint32_t bit = 1u << ((wide ? 3 : R == 16 ? 0 : R == 32 ? 1 : 2) + (a.cache.D == 128 ? 4 : 0));
-    if (!(h->paged_attr_mask & bit)) {
-      if ((wide ? paged_attention_wide_set_attributes(a.cache.D) : paged_attention_set_attributes(a.cache.D, R)) != cudaSuccess)
-        return TSV_ERR_CUDA;
-      h->paged_attr_mask |= bit;
-    }
-    CUtensorMap tk, tv;
-    st = encode_pages(h, &tk, a.cache.k_d, a.cache);
-    if (st == TSV_OK) st = encode_pages(h, &tv, a.cache.v_d, a.cache);
-    if (st != TSV_OK) return st;
-    if (wide) return cuda_status(launch_paged_attention_wide(tk, tv, a, h->num_sms, workspace_d, static_cast<cudaStream_t>(stream)));
-    return cuda_status(launch_paged_attention(tk, tv, a, R, h->num_sms, workspace_d, static_cast<cudaStream_t>(stream)));
-  }
+  if (use_tc) return launch_tree_kernels(h, a, R, workspace_d, static_cast<cudaStream_t>(stream));
   return cuda_status(launch_paged_attention_simt(a, dtype == TSV_BF16, static_cast<cudaStream_t>(stream)));
 }
 
@@ -313,7 +315,7 @@ tsv_status tsv_paged_commit(tsv_handle h, const tsv_paged_cache* cache, const ts
   if (!prefix_len_d || !node_offsets_d || !accept_len_d || !status_d || (N > 0 && !path_d)) return TSV_ERR_INVALID_ARG;
   if (new_len_d == prefix_len_d) return TSV_ERR_INVALID_ARG;
   PagedWriteArgs a{};
-  tsv_status st = check_cache(cache, &a.cache);
+  tsv_status st = check_paged_cache(cache, &a.cache);
   if (st == TSV_OK) st = check_table(table, B, a.cache);
   if (st == TSV_OK) st = check_table(tree_table, B, a.cache);
   if (st != TSV_OK) return st;
@@ -332,6 +334,54 @@ tsv_status tsv_paged_commit(tsv_handle h, const tsv_paged_cache* cache, const ts
   a.new_len = new_len_d;
   a.head_loop = head_loop(a, B + B / 2, 4, h->num_sms);  // (an accepted path ends in one or two pages)
   return cuda_status(launch_paged_commit(a, h->num_sms, static_cast<cudaStream_t>(stream)));
+}
+
+tsv_status tsv_paged_chunk_attention_workspace_size(tsv_handle h, tsv_dtype dtype, const tsv_paged_cache* cache, int32_t B,
+                                                    int32_t N, int32_t max_rows, int32_t Hq, uint32_t flags, size_t* bytes) {
+  tsv_paged_cache c;
+  if (!bytes || N < 0) return TSV_ERR_INVALID_ARG;
+  const tsv_status st = check_attention(h, dtype, cache, &c, B, max_rows, INT32_MAX, Hq, flags);
+  if (st != TSV_OK) return st;
+  *bytes = 0;
+  return TSV_OK;
+}
+
+tsv_status tsv_paged_chunk_attention(tsv_handle h, tsv_dtype dtype, const void* q_d, int64_t q_stride_n, int64_t q_stride_h,
+                                     const tsv_paged_cache* cache, const tsv_page_table* table, const int32_t* start_d,
+                                     const int32_t* row_offsets_d, void* out_d, int32_t B, int32_t N, int32_t max_rows,
+                                     int32_t Hq, int32_t window, float scale, void* workspace_d, size_t workspace_bytes,
+                                     int32_t* status_d, uint32_t flags, void* stream) {
+  PagedAttnArgs a{};
+  tsv_status st = check_attention(h, dtype, cache, &a.cache, B, max_rows, INT32_MAX, Hq, flags);
+  if (st == TSV_OK) st = check_table(table, B, a.cache);
+  if (st != TSV_OK) return st;
+  if (!start_d || !row_offsets_d || !status_d || N < 0 || window < 0) return TSV_ERR_INVALID_ARG;
+  if (!(scale >= 0.f) || isinf(scale)) return TSV_ERR_INVALID_ARG;
+  const int64_t esz = dtype == TSV_BF16 ? 2 : 4;
+  if (N > 0 && (!q_d || !out_d || !aligned16(out_d) || !rows_aligned(q_d, q_stride_n, q_stride_h, esz)))
+    return TSV_ERR_INVALID_ARG;
+  if ((int64_t)N * Hq > INT32_MAX) return TSV_ERR_UNSUPPORTED;
+  const DeviceScope scope(h->device);
+  if (!scope.ok) return TSV_ERR_CUDA;
+  a.q = q_d;
+  a.qs_n = q_stride_n;
+  a.qs_h = q_stride_h;
+  a.table = *table;
+  a.prefix_len = start_d;
+  a.offsets = row_offsets_d;
+  a.out = out_d;
+  a.status = status_d;
+  a.B = B;
+  a.N = N;
+  a.max_nodes = max_rows;
+  a.Hq = Hq;
+  a.G = Hq / a.cache.Hkv;
+  a.scale = scale == 0.f ? 1.f / sqrtf((float)a.cache.D) : scale;
+  a.chunk = 1;
+  a.window = window;
+  (void)workspace_d;
+  (void)workspace_bytes;
+  return cuda_status(launch_paged_attention_simt(a, dtype == TSV_BF16, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

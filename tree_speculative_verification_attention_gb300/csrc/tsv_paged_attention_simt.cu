@@ -75,9 +75,12 @@ __global__ void __launch_bounds__(32 * kSimtWarps) paged_attn_simt_kernel(const 
   if (b < 0) return;
   PagedRequest r;
   if (!paged_request(a, b, &r)) return;
-  const int off = r.off, n = r.n, P = r.P, ps = C.page_size;
+  const int off = r.off, n = r.n, ps = C.page_size;
   const bool tree = a.tree_table.ids_d != nullptr;
   const int i = node - off;
+  // The prefix rows that the node sees: lo .. P - 1.
+  const int P = a.chunk ? r.P - n + i + 1 : r.P;
+  const int lo = a.window > 0 ? max(0, P - a.window) : 0;
   if (tid < TSV_ANC_WORDS) {
     const int left = i + 1 - 32 * tid;  // chain: bits 0 .. i
     sanc[tid] = !tree ? 0u
@@ -104,10 +107,10 @@ __global__ void __launch_bounds__(32 * kSimtWarps) paged_attn_simt_kernel(const 
 #pragma unroll
       for (int e = 0; e < E; ++e) o[h][e] = 0.f;
     }
-    for (int k0 = warp * 32; k0 < keys; k0 += kSimtWarps * 32) {
+    for (int k0 = (lo & ~31) + warp * 32; k0 < keys; k0 += kSimtWarps * 32) {
       const int key = k0 + lane;
-      bool see = key < P;
-      if (!see && key < keys) see = (sanc[(key - P) >> 5] >> ((key - P) & 31)) & 1u;
+      bool see = key < P && key >= lo;
+      if (tree && key >= P && key < keys) see = (sanc[(key - P) >> 5] >> ((key - P) & 31)) & 1u;
       int64_t row = 0;   // byte offset of the key's row of this head
       float ks = 0.f, vs = 0.f;
       if (see) {

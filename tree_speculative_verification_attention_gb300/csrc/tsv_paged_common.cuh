@@ -104,7 +104,8 @@ __device__ __forceinline__ void rope_pair(float& a, float& b, float c, float s) 
 }
 
 // Lengths of request b of an attention call; false when they do not fit the
-// call (the request is then skipped by every kernel).
+// call (the request is then skipped by every kernel).  Of a chunk, P counts the
+// new rows too.
 struct PagedRequest {
   int off, n, P;
 };
@@ -114,6 +115,7 @@ __device__ __forceinline__ bool paged_request(const PagedAttnArgs& a, int b, Pag
   const int end = __ldg(a.offsets + b + 1);
   r->P = __ldg(a.prefix_len + b);
   r->n = end - r->off;
+  if (a.chunk && r->P >= 0 && r->n >= 0) r->P = (int)min((int64_t)r->P + r->n, (int64_t)INT32_MAX);
   return r->off >= 0 && end >= r->off && end <= a.N && r->n <= a.max_nodes && r->P >= 0 &&
          (int64_t)r->P <= (int64_t)a.table.pages * ps &&
          (a.tree_table.ids_d == nullptr || (int64_t)r->n <= (int64_t)a.tree_table.pages * ps);

@@ -1,0 +1,556 @@
+// tsv_pages.cu — page lists against a pool of reference counts: resize, fork,
+// compact.
+//
+// The pool is the counts alone: a free page is one whose count is 0, and pages
+// are handed out by rising id, so a call's result is a function of its
+// arguments.  Finding the k-th free page is a prefix sum over the counts.  One
+// cluster runs a whole call: its CTAs split the pool (a warp takes a contiguous
+// range, 128 counts at a time), exchange their totals through distributed
+// shared memory, and each then hands out, or moves, what lies in its own range;
+// cluster barriers stand between the phases, so a call is one launch and needs
+// no workspace.  What bounds a call is the chain of loads and barriers
+// (microseconds), and for pools of a million pages the counts' way through the
+// cluster's SMs.
+#include <cuda_runtime.h>
+
+#include "tsv_device.cuh"
+#include "tsv_internal.h"
+
+namespace tsv {
+
+namespace {
+
+constexpr int kPoolThreads = 1024, kPoolWarps = 32;
+constexpr int kPoolCtas = 8;  // of a cluster, at most
+
+__device__ __forceinline__ int ld_dsmem_i32(uint32_t addr) {
+  int v;
+  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+// The counterpart of `p` in CTA `rank` of the cluster.
+__device__ __forceinline__ int remote_i32(const int* p, int rank) { return ld_dsmem_i32(mapa_shared(smem_u32(p), (uint32_t)rank)); }
+
+// Barrier of the cluster behind which earlier writes to global memory are seen too.
+__device__ __forceinline__ void cluster_sync_global() {
+  __threadfence();
+  cluster_sync_all();
+}
+
+// Four counts from page `at` on (a multiple of 4); pages past the end count as `none`.
+__device__ __forceinline__ int4 load_counts(const int32_t* refs, int at, int pages, int none) {
+  if (at + 4 <= pages) return __ldcg(reinterpret_cast<const int4*>(refs + at));
+  int4 v = make_int4(none, none, none, none);
+  if (at < pages) v.x = __ldcg(refs + at);
+  if (at + 1 < pages) v.y = __ldcg(refs + at + 1);
+  if (at + 2 < pages) v.z = __ldcg(refs + at + 2);
+  return v;
+}
+
+// The range of pages of a warp: `steps` x 128 from `first` on.
+struct PoolShare {
+  int first, end;
+  __device__ __forceinline__ PoolShare(int pages, int warp) {
+    const int warps = gridDim.x * kPoolWarps, chunks = (pages + 127) >> 7;
+    const int w = blockIdx.x * kPoolWarps + warp;
+    first = (int)((int64_t)chunks * w / warps) << 7;
+    end = min(pages, (int)((int64_t)chunks * (w + 1) / warps) << 7);
+  }
+};
+
+// Pages with count 0 (LIVE: above 0) from `first` up to `end`.
+template <bool LIVE>
+__device__ __forceinline__ int count_pages(const int32_t* refs, int first, int end, int lane) {
+  int n = 0;
+#pragma unroll 8
+  for (int at = first + 4 * lane; at < end; at += 128) {
+    const int4 v = load_counts(refs, at, end, LIVE ? 0 : 1);
+    n += LIVE ? (v.x > 0) + (v.y > 0) + (v.z > 0) + (v.w > 0) : (v.x == 0) + (v.y == 0) + (v.z == 0) + (v.w == 0);
+  }
+  return (int)__reduce_add_sync(0xffffffffu, (unsigned)n);
+}
+
+// Every warp's count -> what lies before its range, and the whole pool's: the
+// warps' sums in shared memory, the CTAs' through the cluster.
+struct PoolScan {
+  int warp_sum[kPoolWarps];
+  int total;
+};
+__device__ __forceinline__ int scan_counts(PoolScan& s, int mine, int warp, int lane, int* all) {
+  if (lane == 0) s.warp_sum[warp] = mine;
+  __syncthreads();
+  int v = s.warp_sum[lane];
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += y;
+  }
+  const int inside = __shfl_sync(0xffffffffu, v, warp) - mine;
+  if (warp == 0 && lane == 31) s.total = v;
+  cluster_sync_all();
+  int t = lane < gridDim.x ? remote_i32(&s.total, lane) : 0;
+  int before = lane < blockIdx.x ? t : 0;
+  *all = (int)__reduce_add_sync(0xffffffffu, (unsigned)t);
+  before = (int)__reduce_add_sync(0xffffffffu, (unsigned)before);
+  return before + inside;
+}
+
+// What the requests of a call want, the same in every CTA.
+struct PoolRequests {
+  int32_t held[TSV_MAX_BATCH], want[TSV_MAX_BATCH], need[TSV_MAX_BATCH], upto[TSV_MAX_BATCH];
+  int32_t bad[TSV_MAX_BATCH];  // (of the CTA's own requests)
+  PoolScan scan;
+  int32_t needed;              // by all requests
+  int32_t granted;
+};
+
+// upto[b]: pages needed up to and with request b (one warp).
+__device__ __forceinline__ void sum_needs(PoolRequests& r, int B, int lane) {
+  int64_t before = 0;
+  for (int b0 = 0; b0 < B; b0 += 32) {
+    int64_t v = b0 + lane < B ? r.need[b0 + lane] : 0;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, v, o);
+      if (lane >= o) v += y;
+    }
+    if (b0 + lane < B) r.upto[b0 + lane] = (int32_t)min(before + v, (int64_t)INT32_MAX);  // (more than any pool holds)
+    before += __shfl_sync(0xffffffffu, v, 31);
+  }
+  if (lane == 0) r.needed = (int32_t)min(before, (int64_t)INT32_MAX);
+}
+
+// Whether request b gets what it needs out of `free` pages.
+__device__ __forceinline__ bool is_served(const PoolRequests& r, int b, int free) { return r.need[b] == 0 || r.upto[b] <= free; }
+
+// Hands out the free pages of the warp's range, the first of which is the pool's
+// `rank`-th: give(b, k, id) for page k of request b's need.
+template <typename Give>
+__device__ __forceinline__ void hand_out(PoolRequests& r, const tsv_page_pool& pool, const PoolShare& share, int rank, int granted, int B,
+                                         int lane, Give give) {
+#pragma unroll 1
+  for (int at = share.first; at < share.end && rank < granted; at += 128) {
+    const int page = at + 4 * lane;
+    const int4 v = load_counts(pool.refs_d, page, share.end, 1);
+    const int f[4] = {v.x == 0, v.y == 0, v.z == 0, v.w == 0};
+    const int n = f[0] + f[1] + f[2] + f[3];
+    int upto = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += y;
+    }
+    int k = rank + upto - n;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if (!f[e]) continue;
+      if (k < granted) {
+        int lo = 0, hi = B - 1;  // the first request with upto > k
+        while (lo < hi) {
+          const int mid = (lo + hi) >> 1;
+          if (r.upto[mid] > k) hi = mid;
+          else lo = mid + 1;
+        }
+        pool.refs_d[page + e] = 1;
+        give(lo, k - (r.upto[lo] - r.need[lo]), page + e);
+      }
+      ++k;
+    }
+    rank += __shfl_sync(0xffffffffu, upto, 31);
+  }
+}
+
+// One reference less of a page that is held; false when it is not.
+__device__ __forceinline__ bool drop_page(int32_t* refs, int32_t id) {
+  if (atomicSub(refs + id, 1) > 0) return true;
+  atomicAdd(refs + id, 1);
+  return false;
+}
+__device__ __forceinline__ bool is_held(const tsv_page_pool& p, int32_t id) {
+  return (uint32_t)id < (uint32_t)p.num_pages && __ldcg(p.refs_d + id) > 0;
+}
+
+// The cluster's requests are shared out: request b belongs to CTA b % CTAs, and
+// there to a group of warps.  for_own(b, t, threads) runs on each of them.
+template <typename F>
+__device__ __forceinline__ void for_own(int B, int warp, int lane, F f) {
+  const int own = (B - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x;  // requests of this CTA
+  if (own <= 0) return;
+  const int group = max(1, kPoolWarps / own);  // warps of a request
+  for (int i = warp / group; i < own; i += kPoolWarps / group)
+    f((int)blockIdx.x + i * (int)gridDim.x, (warp % group) * 32 + lane, group * 32);
+}
+
+__global__ void __launch_bounds__(kPoolThreads, 1) pages_resize_kernel(const PagesResizeArgs a) {
+  __shared__ PoolRequests r;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  pdl_wait();  // the previous kernel's results are visible from here on
+  pdl_trigger();
+  bool shrinks = false;
+  if (tid < a.B) {
+    const int held = __ldcg(a.pages + tid), rows = __ldg(a.rows + tid);
+    const int want = rows / a.page_size + (rows % a.page_size > 0 ? 1 : 0);
+    const bool bad = held < 0 || held > a.table.pages || rows < 0 || want > a.table.pages;
+    r.held[tid] = held;
+    r.want[tid] = want;
+    r.need[tid] = bad ? 0 : max(0, want - held);
+    r.bad[tid] = bad;
+    shrinks = !bad && want < held;
+  }
+  shrinks = __syncthreads_or(shrinks);  // the same in every CTA
+  if (warp == 0) sum_needs(r, a.B, lane);
+  if (shrinks) {
+    for_own(a.B, warp, lane, [&](int b, int t, int threads) {
+      if (r.bad[b] || r.want[b] >= r.held[b]) return;
+      const int32_t* ids = a.table.ids_d + (int64_t)b * a.table.stride;
+      bool bad = false;
+      for (int i = r.want[b] + t; i < r.held[b]; i += threads) bad |= !is_held(a.pool, __ldcg(ids + i));
+      if (t == 0 && __ldg(a.rows + b) % a.page_size > 0) {  // new rows would go to the last page
+        const int32_t id = __ldcg(ids + r.want[b] - 1);
+        bad |= !is_held(a.pool, id) || __ldcg(a.pool.refs_d + id) > 1;
+      }
+      if (bad) atomicOr(&r.bad[b], 2);
+    });
+    cluster_sync_all();  // every look at the counts comes before the first change
+    for_own(a.B, warp, lane, [&](int b, int t, int threads) {
+      if (r.bad[b] & 3 || r.want[b] >= r.held[b]) return;
+      const int32_t* ids = a.table.ids_d + (int64_t)b * a.table.stride;
+      bool bad = false;
+      for (int i = r.want[b] + t; i < r.held[b]; i += threads) bad |= !drop_page(a.pool.refs_d, __ldcg(ids + i));
+      if (bad) atomicOr(&r.bad[b], 4);  // (listed more often than counted)
+    });
+    cluster_sync_global();
+  } else {
+    __syncthreads();
+  }
+  int free = 0;
+  if (r.needed > 0) {
+    const PoolShare share(a.pool.num_pages, warp);
+    const int mine = count_pages<false>(a.pool.refs_d, share.first, share.end, lane);
+    const int rank = scan_counts(r.scan, mine, warp, lane, &free);
+    if (tid == 0) r.granted = 0;
+    __syncthreads();
+    if (tid < a.B && is_served(r, tid, free)) atomicMax(&r.granted, r.need[tid] ? r.upto[tid] : 0);
+    __syncthreads();
+    hand_out(r, a.pool, share, rank, r.granted, a.B, lane, [&](int b, int k, int id) {
+      const_cast<int32_t*>(a.table.ids_d)[(int64_t)b * a.table.stride + r.held[b] + k] = id;
+    });
+  }
+  if (tid < a.B && tid % gridDim.x == blockIdx.x) {
+    const bool bad = r.bad[tid] & 3, served = is_served(r, tid, free);
+    if (!bad && served) a.pages[tid] = r.want[tid];
+    a.status[tid] = r.bad[tid] ? TSV_ERR_INVALID_ARG : served ? TSV_OK : TSV_ERR_NO_PAGES;
+  }
+  cluster_sync_all();  // the others have read this CTA's total
+}
+
+__global__ void __launch_bounds__(kPoolThreads, 1) pages_fork_kernel(const PagesForkArgs a) {
+  __shared__ PoolRequests r;
+  __shared__ int32_t source[TSV_MAX_BATCH], full[TSV_MAX_BATCH];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  pdl_wait();  // the previous kernel's results are visible from here on
+  pdl_trigger();
+  if (tid < a.B) {
+    const int held = __ldcg(a.to_pages + tid), rows = __ldg(a.rows + tid), src = __ldg(a.source + tid);
+    const int whole = rows / a.page_size, part = rows % a.page_size > 0 ? 1 : 0;
+    bool bad = src < -1 || src >= a.F || (src >= 0 && (rows < 0 || held < 0 || held > a.to.pages));
+    if (src >= 0 && !bad) {
+      const int has = __ldg(a.from_pages + src);
+      bad = has < 0 || has > a.from.pages || whole + part > has || whole + part > a.to.pages;
+    }
+    r.held[tid] = held;
+    r.want[tid] = whole + part;
+    full[tid] = whole;
+    source[tid] = bad ? -1 : src;
+    r.need[tid] = bad || src < 0 ? 0 : part;
+    r.bad[tid] = bad;
+  }
+  __syncthreads();
+  for_own(a.B, warp, lane, [&](int b, int t, int threads) {
+    if (source[b] < 0) return;
+    const int32_t* old = a.to.ids_d + (int64_t)b * a.to.stride;
+    const int32_t* ids = a.from.ids_d + (int64_t)source[b] * a.from.stride;
+    bool bad = false;
+    for (int i = t; i < r.held[b]; i += threads) bad |= !is_held(a.pool, __ldcg(old + i));
+    for (int i = t; i < r.want[b]; i += threads) bad |= !is_held(a.pool, __ldg(ids + i));
+    if (bad) atomicOr(&r.bad[b], 2);
+  });
+  cluster_sync_all();  // every look at the counts comes before the first change
+  // What the owners found: the needs are the same in every CTA.
+  if (tid < a.B) {
+    const int bad = remote_i32(&r.bad[tid], tid % gridDim.x) & 3;
+    if (bad) {
+      source[tid] = -1;
+      r.need[tid] = 0;
+    }
+  }
+  __syncthreads();
+  if (warp == 0) sum_needs(r, a.B, lane);
+  for_own(a.B, warp, lane, [&](int b, int t, int threads) {
+    if (source[b] < 0) return;
+    const int32_t* old = a.to.ids_d + (int64_t)b * a.to.stride;
+    bool bad = false;
+    for (int i = t; i < r.held[b]; i += threads) bad |= !drop_page(a.pool.refs_d, __ldcg(old + i));
+    if (bad) atomicOr(&r.bad[b], 4);  // (listed more often than counted)
+  });
+  cluster_sync_global();
+  int free = 0;
+  const PoolShare share(a.pool.num_pages, warp);
+  int rank = 0;
+  if (r.needed > 0) {
+    const int mine = count_pages<false>(a.pool.refs_d, share.first, share.end, lane);
+    rank = scan_counts(r.scan, mine, warp, lane, &free);  // (a barrier of the cluster: counts are read before pages are shared)
+    if (tid == 0) r.granted = 0;
+    __syncthreads();
+    if (tid < a.B && is_served(r, tid, free)) atomicMax(&r.granted, r.need[tid] ? r.upto[tid] : 0);
+    __syncthreads();
+    // (A page that becomes shared below has another holder: its count is never 0.)
+    hand_out(r, a.pool, share, rank, r.granted, a.B, lane, [&](int b, int, int id) {
+      const_cast<int32_t*>(a.to.ids_d)[(int64_t)b * a.to.stride + full[b]] = id;
+      a.copy_src[b] = __ldg(a.from.ids_d + (int64_t)source[b] * a.from.stride + full[b]);
+      a.copy_dst[b] = id;
+    });
+  }
+  for_own(a.B, warp, lane, [&](int b, int t, int threads) {
+    if (source[b] < 0 || !is_served(r, b, free)) return;
+    int32_t* list = const_cast<int32_t*>(a.to.ids_d) + (int64_t)b * a.to.stride;
+    const int32_t* ids = a.from.ids_d + (int64_t)source[b] * a.from.stride;
+    for (int i = t; i < full[b]; i += threads) {
+      const int32_t id = __ldg(ids + i);
+      list[i] = id;
+      atomicAdd(a.pool.refs_d + id, 1);
+    }
+  });
+  if (tid < a.B && tid % gridDim.x == blockIdx.x) {
+    const bool served = is_served(r, tid, free);
+    if (source[tid] >= 0) a.to_pages[tid] = served ? r.want[tid] : 0;
+    if (source[tid] < 0 || !served || r.need[tid] == 0) {
+      a.copy_src[tid] = -1;
+      a.copy_dst[tid] = -1;
+    }
+    a.status[tid] = r.bad[tid] ? TSV_ERR_INVALID_ARG : served ? TSV_OK : TSV_ERR_NO_PAGES;
+  }
+  cluster_sync_all();  // the others have read this CTA's flags and total
+}
+
+__global__ void __launch_bounds__(kPoolThreads, 1) pages_compact_kernel(const PagesCompactArgs a) {
+  __shared__ PoolScan scan;
+  __shared__ int below;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  pdl_wait();  // the previous kernel's results are visible from here on
+  pdl_trigger();
+  const int pages = a.pool.num_pages;
+  const PoolShare share(pages, warp);
+  int L = 0;
+  const int before = scan_counts(scan, count_pages<true>(a.pool.refs_d, share.first, share.end, lane), warp, lane, &L);
+  // Pages in use below L: the warp whose range holds page L knows (the last one
+  // when every page is in use), and tells every CTA.
+  const bool last = blockIdx.x == gridDim.x - 1 && warp == kPoolWarps - 1;
+  if ((share.first <= L && L < share.end) || (last && L == pages)) {
+    const int n = before + count_pages<true>(a.pool.refs_d, share.first, min(L, share.end), lane);
+    if (lane < gridDim.x)
+      asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(mapa_shared(smem_u32(&below), (uint32_t)lane)), "r"(n) : "memory");
+  }
+  cluster_sync_all();
+  const int kept = below, moved = L - kept;
+  if (blockIdx.x == 0 && tid == 0) *a.moved = moved;
+  if (blockIdx.x == 0 && tid < a.n) a.status[tid] = TSV_OK;
+  // The holes below L and the pages in use from L on, by rising id.
+  int live = before;  // pages in use before the current one
+#pragma unroll 1
+  for (int at = share.first; at < share.end; at += 128) {
+    const int page = at + 4 * lane;
+    const int4 v = load_counts(a.pool.refs_d, page, share.end, 0);
+    const int c[4] = {v.x, v.y, v.z, v.w};
+    const int n = (c[0] > 0) + (c[1] > 0) + (c[2] > 0) + (c[3] > 0);
+    int upto = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += y;
+    }
+    int k = live + upto - n;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int id = page + e;
+      if (id >= share.end) break;
+      const bool used = c[e] > 0;
+      if (id < L) {
+        a.new_id[id] = used ? id : -1;
+        if (used) a.refs_out[id] = c[e];
+        else a.move_dst[id - k] = id;  // (its count comes with its new page)
+      } else if (used) {
+        a.move_src[k - kept] = id;
+      } else {
+        a.new_id[id] = -1;
+        a.refs_out[id] = 0;
+      }
+      k += used;
+    }
+    live += __shfl_sync(0xffffffffu, upto, 31);
+  }
+  cluster_sync_global();
+  for (int i = blockIdx.x * kPoolThreads + tid; i < moved; i += gridDim.x * kPoolThreads) {
+    const int src = __ldcg(a.move_src + i), dst = __ldcg(a.move_dst + i);
+    const int count = __ldcg(a.pool.refs_d + src);
+    a.new_id[src] = dst;
+    a.refs_out[src] = 0;
+    a.refs_out[dst] = count;
+  }
+}
+
+// Entries of the lists under their new ids: a CTA per row and 4096 entries.
+constexpr int kRemapThreads = 512, kRemapEntries = 4096;
+__global__ void __launch_bounds__(kRemapThreads) pages_remap_kernel(const PagesCompactArgs a, int chunks) {
+  pdl_wait();  // the previous kernel's results are visible from here on
+  pdl_trigger();
+  int row = blockIdx.x / chunks, t = 0;
+  const int first = (blockIdx.x - row * chunks) * kRemapEntries;
+  while (row >= a.lists[t].B) row -= a.lists[t++].B;
+  const tsv_page_lists& l = a.lists[t];
+  const int held = __ldg(l.pages_d + row);
+  bool bad = held < 0 || held > l.table.pages;
+  if (!bad) {
+    const int32_t* from = l.table.ids_d + (int64_t)row * l.table.stride;
+    int32_t* to = l.out_d + (int64_t)row * l.out_stride;
+    const int end = min(held, first + kRemapEntries);
+#pragma unroll 4
+    for (int i = first + threadIdx.x; i < end; i += kRemapThreads) {
+      const int32_t id = from[i];
+      const int32_t now = (uint32_t)id < (uint32_t)a.pool.num_pages ? __ldg(a.new_id + id) : -1;
+      bad |= now < 0;
+      to[i] = now;
+    }
+  }
+  if (bad) a.status[t] = TSV_ERR_INVALID_ARG;
+}
+
+int pool_ctas(int32_t num_pages) {
+  // A CTA's 32 warps take 4096 counts a step.
+  int n = 1;
+  while (n < kPoolCtas && num_pages > n * 4096) n *= 2;
+  return n;
+}
+
+}  // namespace
+
+cudaError_t launch_pages_resize(const PagesResizeArgs& a, cudaStream_t st) {
+  const int n = pool_ctas(a.pool.num_pages);
+  return launch_pdl(pages_resize_kernel, dim3(n), dim3(kPoolThreads), 0, st, (unsigned)n, a);
+}
+
+cudaError_t launch_pages_fork(const PagesForkArgs& a, cudaStream_t st) {
+  const int n = pool_ctas(a.pool.num_pages);
+  return launch_pdl(pages_fork_kernel, dim3(n), dim3(kPoolThreads), 0, st, (unsigned)n, a);
+}
+
+cudaError_t launch_pages_compact(const PagesCompactArgs& a, cudaStream_t st) {
+  const int n = pool_ctas(a.pool.num_pages);
+  const cudaError_t e = launch_pdl(pages_compact_kernel, dim3(n), dim3(kPoolThreads), 0, st, (unsigned)n, a);
+  if (e != cudaSuccess || a.n == 0) return e;
+  int64_t rows = 0;
+  int32_t width = 1;
+  for (int t = 0; t < a.n; ++t) {
+    rows += a.lists[t].B;
+    width = width > a.lists[t].table.pages ? width : a.lists[t].table.pages;
+  }
+  const int64_t chunks = ((int64_t)width + kRemapEntries - 1) / kRemapEntries;
+  if (rows * chunks > INT32_MAX) return cudaErrorInvalidValue;
+  return launch_pdl(pages_remap_kernel, dim3((unsigned)(rows * chunks)), dim3(kRemapThreads), 0, st, 0u, a, (int)chunks);
+}
+
+// ---------------------------------------------------------------- contents
+
+namespace {
+
+// Address of 16-byte vector v of a page: runs of run16 vectors, n1 of them s1
+// apart, and those s0 apart.
+struct PageShape {
+  int32_t run16, n1;
+  int64_t s1, s0;
+  int32_t vectors;
+};
+
+constexpr int kCopyThreads = 256, kCopyBatch = 8;
+
+__global__ void __launch_bounds__(kCopyThreads) pages_copy_kernel(const PagesCopyArgs a, const PageShape shape) {
+  pdl_wait();  // the previous kernel's results are visible from here on
+  pdl_trigger();
+  const tsv_paged_cache& c = a.cache;
+  const int tid = threadIdx.x;
+  int n = a.n;
+  if (a.count) n = max(0, min(n, __ldg(a.count)));
+  if (blockIdx.x == gridDim.x - 1) {  // the ids are checked once
+    bool bad = false;
+#pragma unroll 8
+    for (int i = tid; i < n; i += kCopyThreads) {
+      const int32_t s = __ldg(a.src + i), d = __ldg(a.dst + i);
+      bad |= (s != -1 && (uint32_t)s >= (uint32_t)c.num_pages) || (d != -1 && (uint32_t)d >= (uint32_t)c.num_pages);
+    }
+    bad = __syncthreads_or(bad);
+    if (tid == 0) *a.status = bad ? TSV_ERR_INVALID_ARG : TSV_OK;
+  }
+  constexpr int kPart = kCopyThreads * kCopyBatch;  // vectors of a part
+  const int parts = (shape.vectors + kPart - 1) / kPart;
+  const int64_t units = 2ll * n * parts;
+  for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
+    const int64_t pk = u / parts;
+    const int part = (int)(u - pk * parts), pair = (int)(pk >> 1);
+    const bool is_v = pk & 1;
+    const int32_t s = __ldg(a.src + pair), d = __ldg(a.dst + pair);
+    if ((uint32_t)s >= (uint32_t)c.num_pages || (uint32_t)d >= (uint32_t)c.num_pages) continue;
+    const uint8_t* base = static_cast<const uint8_t*>(is_v ? c.v_d : c.k_d);
+    const uint8_t* from = base + (int64_t)s * c.stride_page;
+    uint8_t* to = const_cast<uint8_t*>(base) + (int64_t)d * c.stride_page;
+    uint4 x[kCopyBatch];
+    int64_t at[kCopyBatch];
+#pragma unroll
+    for (int q = 0; q < kCopyBatch; ++q) {
+      const int v = part * kPart + q * kCopyThreads + tid;
+      at[q] = -1;
+      if (v >= shape.vectors) continue;
+      const int run = v / shape.run16, row = run / shape.n1;
+      at[q] = 16ll * (v - run * shape.run16) + (run - row * shape.n1) * shape.s1 + row * shape.s0;
+      x[q] = __ldcs(reinterpret_cast<const uint4*>(from + at[q]));
+    }
+#pragma unroll
+    for (int q = 0; q < kCopyBatch; ++q)
+      if (at[q] >= 0) __stcs(reinterpret_cast<uint4*>(to + at[q]), x[q]);
+    if (part == 0) {
+      float* scale = is_v ? c.v_scale_d : c.k_scale_d;
+      for (int g = tid; g < c.Hkv; g += kCopyThreads) scale[(int64_t)d * c.Hkv + g] = scale[(int64_t)s * c.Hkv + g];
+    }
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_pages_copy(const PagesCopyArgs& a, int num_sms, cudaStream_t st) {
+  const tsv_paged_cache& c = a.cache;
+  // Rows and heads by rising stride; neighbours that lie next to each other are one run.
+  PageShape s{};
+  const bool heads_inside = c.stride_head <= c.stride_row;
+  int64_t run = c.D, n1 = heads_inside ? c.Hkv : c.page_size, n0 = heads_inside ? c.page_size : c.Hkv;
+  s.s1 = heads_inside ? c.stride_head : c.stride_row;
+  s.s0 = heads_inside ? c.stride_row : c.stride_head;
+  if (s.s1 == run || n1 == 1) {
+    run *= n1;
+    n1 = n0;
+    s.s1 = s.s0;
+    s.s0 = 0;
+    n0 = 1;
+    if (s.s1 == run || n1 == 1) {
+      run *= n1;
+      n1 = 1;
+    }
+  }
+  s.run16 = (int32_t)(run / 16);
+  s.n1 = (int32_t)n1;
+  s.vectors = (int32_t)((int64_t)c.page_size * c.Hkv * c.D / 16);
+  const int64_t parts = (s.vectors + kCopyThreads * kCopyBatch - 1) / (kCopyThreads * kCopyBatch);
+  const int64_t units = 2ll * a.n * parts, most = (int64_t)num_sms * 8;
+  const int grid = (int)(units < 1 ? 1 : units < most ? units : most);
+  return launch_pdl(pages_copy_kernel, dim3(grid), dim3(kCopyThreads), 0, st, 0u, a, s);
+}
+
+}  // namespace tsv

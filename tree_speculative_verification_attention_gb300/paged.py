@@ -2,8 +2,7 @@
 
 Two layers, as in the package's main module: ``tsv_*`` functions mirror the C
 ABI one to one; ``rope_frequencies``, ``rope``, ``PagedCache``, ``paged_append``,
-``paged_tree_attention`` and ``paged_commit`` check shapes and types, allocate
-what the caller did not pass, and call them.  The launches go to the current
+``paged_tree_attention``, ``paged_commit`` and ``paged_chunk_attention`` check shapes and types, allocate what the caller did not pass, and call them.  The launches go to the current
 stream of the tensors' device, or to ``stream``; what these helpers allocate
 belongs to that stream.
 """
@@ -19,7 +18,7 @@ from . import TSV_ATTN_DEFAULT, TSV_BF16, TSV_F32, TSV_MAX_NODES, _HANDLES, _che
 
 PAGED_EXPORTED = (
     "tsv_rope_frequencies", "tsv_rope", "tsv_paged_append", "tsv_paged_tree_attention_workspace_size",
-    "tsv_paged_tree_attention", "tsv_paged_commit",
+    "tsv_paged_tree_attention", "tsv_paged_commit", "tsv_paged_chunk_attention_workspace_size", "tsv_paged_chunk_attention",
 )
 
 TSV_ROPE_INTERLEAVED, TSV_ROPE_INVERSE = 1, 2
@@ -56,6 +55,9 @@ def _declare():
         "tsv_paged_tree_attention": [vp, e, vp, i64, i64, cache, table, vp, table, vp, vp, vp, i32, i32, i32, i32, f32,
                                      vp, sz, vp, u32, vp],
         "tsv_paged_commit": [vp, cache, table, table, vp, vp, vp, vp, i32, i32, i32, vp, vp, vp],
+        "tsv_paged_chunk_attention_workspace_size": [vp, e, cache, i32, i32, i32, i32, u32, ctypes.POINTER(sz)],
+        "tsv_paged_chunk_attention": [vp, e, vp, i64, i64, cache, table, vp, vp, vp, i32, i32, i32, i32, i32, f32, vp, sz, vp,
+                                      u32, vp],
     }
     for name, args in sig.items():
         f = getattr(_lib, name)
@@ -119,6 +121,21 @@ def tsv_paged_commit(h, cache, table, tree_table, prefix_len, node_offsets, path
     _check(_lib.tsv_paged_commit(h, _at(cache), _at(table), _at(tree_table), _ptr(prefix_len), _ptr(node_offsets), _ptr(path),
                                  _ptr(accept_len), B, N, max_nodes, _ptr(new_len), _ptr(status), stream),
            "tsv_paged_commit")
+
+
+def tsv_paged_chunk_attention_workspace_size(h, dtype_code, cache, B, N, max_rows, Hq, flags=TSV_ATTN_DEFAULT) -> int:
+    out = ctypes.c_size_t()
+    _check(_lib.tsv_paged_chunk_attention_workspace_size(h, dtype_code, _at(cache), int(B), int(N), int(max_rows), int(Hq),
+                                                         int(flags), ctypes.byref(out)),
+           "tsv_paged_chunk_attention_workspace_size")
+    return out.value
+
+
+def tsv_paged_chunk_attention(h, dtype_code, q, q_stride_n, q_stride_h, cache, table, start, row_offsets, out, B, N, max_rows, Hq,
+                              window, scale, workspace, workspace_bytes, status, flags, stream):
+    _check(_lib.tsv_paged_chunk_attention(h, dtype_code, _ptr(q), q_stride_n, q_stride_h, _at(cache), _at(table), _ptr(start),
+                                          _ptr(row_offsets), _ptr(out), B, N, max_rows, Hq, window, scale, _ptr(workspace),
+                                          workspace_bytes, _ptr(status), flags, stream), "tsv_paged_chunk_attention")
 
 
 # ----------------------------------------------------------------- convenience layer
@@ -375,3 +392,46 @@ def paged_commit(cache, page_table, tree_table, prefix_len, node_offsets, path, 
                                  B, N, max(1, min(N, TSV_MAX_NODES)) if max_nodes is None else max_nodes, new, st,
                                  _on(stream, index)), "tsv_paged_commit")
     return out
+
+
+def paged_chunk_attention_workspace(q, cache, B, max_rows, flags=TSV_ATTN_DEFAULT):
+    """A zero-filled workspace for calls of this shape (or a smaller one), one at a time."""
+    need = tsv_paged_chunk_attention_workspace_size(_handle(q.device.index), _code(q.dtype), cache.c, B, q.shape[0], max_rows,
+                                                    q.shape[1], flags)
+    return _workspace(need, q.device)
+
+
+def paged_chunk_attention(q, cache, page_table, start, row_offsets, window=0, max_rows=None, scale=0.0, flags=TSV_ATTN_DEFAULT,
+                          out=None, workspace=None, status=None, stream=None):
+    """Causal attention of new tokens over the pages that hold them: rows row_offsets[b] .. row_offsets[b+1]-1 of q [N, Hq, D] are
+    request b's tokens, whose K/V rows start[b] .. paged_append wrote; each sees the rows up to its own (`window`: the last so
+    many of them).  `max_rows`: the most new rows of one request (default N; 1 for single tokens is faster when it is given).
+    Returns out [N, Hq, D] and status [B]."""
+    index = cache.index
+    B = row_offsets.shape[0] - 1
+    shape, qs = _heads("q", q, index, cache.D)
+    N, Hq, D = shape
+    first = _ints("start", start, B, index)
+    offs = _ints("row_offsets", row_offsets, B + 1, index)
+    if max_rows is None:
+        max_rows = max(1, N)
+    table = _table("page_table", page_table, B, index)
+    h, code = _handle(index), _code(q.dtype)
+    if out is None or status is None or workspace is None:
+        with _allocating(stream, cache.device):
+            if out is None:
+                out = torch.empty((N, Hq, D), dtype=q.dtype, device=cache.device)
+            if status is None:
+                status = torch.empty(B, dtype=_INT, device=cache.device)
+            if workspace is None:
+                workspace = _workspace(tsv_paged_chunk_attention_workspace_size(h, code, cache.c, B, N, max_rows, Hq, flags),
+                                       cache.device)
+    _want(out.shape == shape and out.dtype is q.dtype and out.is_contiguous() and out.get_device() == index,
+          "out: a contiguous tensor of q's shape and type is wanted")
+    _want(workspace.get_device() == index and workspace.is_contiguous(), "workspace: a contiguous tensor beside the cache is wanted")
+    st = _ints("status", status, B, index)
+    _check(_lib.tsv_paged_chunk_attention(h, code, q.data_ptr(), qs[0], qs[1], cache.at, table, first, offs, out.data_ptr(), B, N,
+                                          max_rows, Hq, window, scale, workspace.data_ptr(),
+                                          workspace.numel() * workspace.element_size(), st, flags, _on(stream, index)),
+           "tsv_paged_chunk_attention")
+    return out, status
