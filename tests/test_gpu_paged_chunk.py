@@ -345,7 +345,7 @@ def test_captured_chunks_follow_the_lengths(tsv, kind):
                 call()
         graphs.append((g, s))
         outs.append((out, st))
-        state.append(a)
+        state.append(dict(a, ws=ws))  # (a graph's workspace lives as long as the graph)
     for starts, offs in (([300, 20], [0, 90, 220]), ([5, 0], [0, 1, 130]), ([170, 100], [0, 220, 220]), ([0, 149], [0, 0, 1])):
         for a in state:
             a["start"].copy_(i32(starts)), a["offs"].copy_(i32(offs))
@@ -393,6 +393,37 @@ def test_chunks_over_many_blocks(tsv, case):
     b.check(out, st, 0, window=window)
     again, _ = b.run(tsv, window=window)
     assert torch.equal(again, out)
+
+
+MANY = [  # page, Hq, Hkv, D, lengths, window: more units of 256 rows than SMs
+    (16, 32, 16, 128, [(300, 1), (0, 257), (9, 1), (200, 400), (0, 1), (1000, 1), (0, 300), (700, 129), (50, 65), (3, 1), (129, 128)], 0),
+    (128, 32, 16, 64, [(0, 1)] * 40 + [(5, 700)] + [(600, 1)] * 40 + [(250, 600)], 0),
+    (32, 24, 24, 128, [(40, 300), (0, 1), (100, 500), (0, 1), (0, 1), (513, 257), (0, 700)], 150),
+    (64, 48, 24, 64, [(1500, 33)] * 20 + [(1000, 200)], 1200),
+]
+
+
+@pytest.mark.parametrize("case", MANY, ids=lambda c: "-".join(str(x) for x in c[:4]))
+def test_many_units_of_one_and_two_tiles(tsv, case):
+    page, Hq, Hkv, D, lens, window = case
+    b = Chunk(tsv, np.random.default_rng(52), lens, Hq, Hkv, D, page)
+    assert -(-len(b.q) * (Hq // Hkv) // 256) * Hkv >= 152
+    out, st = b.run(tsv, window=window)
+    b.check(out, st, 0, window=window)
+    again, _ = b.run(tsv, window=window)
+    assert torch.equal(again, out)
+    # NaN in V, in masked blocks and others
+    v = b.cache.v.view(torch.uint8)
+    want = torch.zeros_like(out, dtype=torch.bool)
+    G = Hq // Hkv
+    for i, (p, n) in enumerate(lens):
+        for row, g, d in ((p + n // 2, 1, 3), (p + n - 1, 0, D - 1), (p // 2, Hkv - 1, 0)):
+            v[b.table[i][row // page], row % page, g, d] = 0x7F
+            for x in range(n):
+                if row <= p + x and (not window or row > p + x - window):
+                    want[int(b.offs[i]) + x, g * G:(g + 1) * G, d] = True
+    got, _ = b.run(tsv, window=window)
+    assert torch.equal(torch.isnan(got), want) and torch.equal(got[~want], out[~want])
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])

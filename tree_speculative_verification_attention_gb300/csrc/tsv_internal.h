@@ -29,6 +29,7 @@ struct tsv_handle_s {
   int mss_max_clusters[kMssClusterSizeEntries];  // resident MSS clusters of each size
   uint32_t verify_overlap;  // tsv_set_verify_overlap: TSV_OVERLAP_* flags
   uint32_t paged_attr_mask;   // paged attention kernels whose attributes are set, one bit per (D, tile rows)
+  uint32_t chunk_attr_mask;   // chunk attention kernels, one bit per D
   uint32_t append_attr_mask;  // paged append kernels, one bit per (type, D)
 };
 
@@ -343,6 +344,27 @@ cudaError_t paged_attention_wide_set_attributes(int32_t D);
 cudaError_t launch_paged_attention_wide(const CUtensorMap& tk, const CUtensorMap& tv, const PagedAttnArgs& a, int num_sms, void* ws,
                                         cudaStream_t st);
 cudaError_t launch_paged_attention_simt(const PagedAttnArgs& a, bool bf16, cudaStream_t st);
+
+// Attention of chunks on the tensor cores.  Its workspace holds one word per
+// request (set by a CTA that gave up a wait for it), room for the counters of the
+// kernels above (which take single tokens, in the same workspace, and find them
+// zero), what each CTA left to join,
+// then two partial results per CTA (O [256][D], then maxima and sums [2][256]).
+constexpr size_t kPagedChunkPartBytes = 32;
+struct PagedChunkLayout {
+  size_t parts, part_o, part_ml, total;
+};
+inline PagedChunkLayout paged_chunk_layout(int grid, int32_t D) {
+  PagedChunkLayout l;
+  l.parts = ((size_t)(TSV_MAX_BATCH + grid) * 4 + 255) & ~(size_t)255;
+  l.part_o = (l.parts + (size_t)grid * kPagedChunkPartBytes + 255) & ~(size_t)255;
+  l.part_ml = l.part_o + (size_t)grid * 2 * kPagedWideRows * D * 4;
+  l.total = l.part_ml + (size_t)grid * 2 * 2 * kPagedWideRows * 4;
+  return l;
+}
+cudaError_t paged_chunk_set_attributes(int32_t D);
+cudaError_t launch_paged_chunk(const CUtensorMap& tk, const CUtensorMap& tv, const PagedAttnArgs& a, int num_sms, void* ws,
+                               cudaStream_t st);
 
 // Page lists and the pool they draw on (tsv_pages.h).
 struct PagesResizeArgs {

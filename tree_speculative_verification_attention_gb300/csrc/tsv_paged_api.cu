@@ -105,6 +105,11 @@ tsv_status launch_tree_kernels(tsv_handle h, const PagedAttnArgs& a, int32_t R, 
   return cuda_status(launch_paged_attention(tk, tv, a, R, h->num_sms, workspace_d, stream));
 }
 
+// Rows a unit of the tree attention's kernel when each request has one token.
+int32_t chunk_token_rows(int32_t G, int32_t B, const tsv_paged_cache& c) {
+  return paged_attn_rows(G, (int64_t)B * c.Hkv, TSV_PAGED_MAX_ROWS);
+}
+
 // Head groups that one CTA of an append or commit takes in turn, of about
 // `pages` pages to write.  What it does once (the angles, or the chain of loads
 // from the lengths to the path's pages) costs as much as `once` groups, and the
@@ -342,7 +347,10 @@ tsv_status tsv_paged_chunk_attention_workspace_size(tsv_handle h, tsv_dtype dtyp
   if (!bytes || N < 0) return TSV_ERR_INVALID_ARG;
   const tsv_status st = check_attention(h, dtype, cache, &c, B, max_rows, INT32_MAX, Hq, flags);
   if (st != TSV_OK) return st;
-  *bytes = 0;
+  const bool one = max_rows == 1;  // (without a window a kernel of the tree attention takes single tokens)
+  *bytes = !paged_uses_tc(dtype, flags) ? 0
+           : std::max(paged_chunk_layout(h->num_sms, c.D).total,
+                      one ? paged_attn_layout(h->num_sms, chunk_token_rows(Hq / c.Hkv, B, c), c.D).total : 0);
   return TSV_OK;
 }
 
@@ -361,6 +369,12 @@ tsv_status tsv_paged_chunk_attention(tsv_handle h, tsv_dtype dtype, const void* 
   if (N > 0 && (!q_d || !out_d || !aligned16(out_d) || !rows_aligned(q_d, q_stride_n, q_stride_h, esz)))
     return TSV_ERR_INVALID_ARG;
   if ((int64_t)N * Hq > INT32_MAX) return TSV_ERR_UNSUPPORTED;
+  const bool use_tc = paged_uses_tc(dtype, flags), by_chunks = use_tc && (max_rows > 1 || window > 0);
+  const int32_t R = by_chunks ? 0 : chunk_token_rows(Hq / a.cache.Hkv, B, a.cache);
+  if (use_tc && (!workspace_d || !aligned16(workspace_d) ||
+                 workspace_bytes < (by_chunks ? paged_chunk_layout(h->num_sms, a.cache.D).total
+                                              : paged_attn_layout(h->num_sms, R, a.cache.D).total)))
+    return TSV_ERR_INVALID_ARG;
   const DeviceScope scope(h->device);
   if (!scope.ok) return TSV_ERR_CUDA;
   a.q = q_d;
@@ -379,8 +393,19 @@ tsv_status tsv_paged_chunk_attention(tsv_handle h, tsv_dtype dtype, const void* 
   a.scale = scale == 0.f ? 1.f / sqrtf((float)a.cache.D) : scale;
   a.chunk = 1;
   a.window = window;
-  (void)workspace_d;
-  (void)workspace_bytes;
+  if (use_tc && !by_chunks) return launch_tree_kernels(h, a, R, workspace_d, static_cast<cudaStream_t>(stream));
+  if (by_chunks) {
+    const uint32_t bit = a.cache.D == 128 ? 2u : 1u;
+    if (!(h->chunk_attr_mask & bit)) {
+      if (paged_chunk_set_attributes(a.cache.D) != cudaSuccess) return TSV_ERR_CUDA;
+      h->chunk_attr_mask |= bit;
+    }
+    CUtensorMap tk, tv;
+    st = encode_pages(h, &tk, a.cache.k_d, a.cache);
+    if (st == TSV_OK) st = encode_pages(h, &tv, a.cache.v_d, a.cache);
+    if (st != TSV_OK) return st;
+    return cuda_status(launch_paged_chunk(tk, tv, a, h->num_sms, workspace_d, static_cast<cudaStream_t>(stream)));
+  }
   return cuda_status(launch_paged_attention_simt(a, dtype == TSV_BF16, static_cast<cudaStream_t>(stream)));
 }
 

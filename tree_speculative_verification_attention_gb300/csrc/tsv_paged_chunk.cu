@@ -1,0 +1,1073 @@
+// tsv_paged_chunk.cu — causal attention of chunks of new tokens over a paged
+// 8-bit cache, bf16 rows on the tensor cores.
+//
+//   S = (Qh + Ql) K^T   M = 128 rows, N = 128 keys, K = D   (e4m3; A = Q, B = K, shared memory)
+//   O += P V            M = 128 rows, N = D, K = 128 keys   (fp16; A = P, TMEM; B = V, shared memory)
+//
+// Rows of a tile are (token, query head of the KV head) pairs, token by token, so
+// a KV head's codes are read once for all heads that share it.  K's codes are an
+// operand as they lie in the cache: TMA brings a page's rows of a head into the
+// swizzled tile.  A row of q is two e4m3 terms under a power of two that moves
+// its largest value to [128, 256): a bf16's 8 bits exactly down to 2^-17 of it,
+// at the price of one fp16 product, since e4m3 products run at twice the rate.
+// V is widened to fp16 (exactly) so that P keeps fp16's 11 bits: P is 2^11 p
+// times the V scale of its page relative to the unit's largest so far, p <= 2^4
+// below a reference maximum that moves only when a score passes it by that much.
+// A V scale that is a power of two goes into the exponent of p and out of the
+// row's sum again (a factor per 16 keys), others are a product of their own.
+//
+// Work.  Units of up to 256 rows (two tiles) of a KV head and the 128-key blocks
+// that any of their rows sees form one list, which is cut into equal ranges, one
+// per CTA (one CTA per SM); the lengths are read from the device.  A unit that a
+// cut goes through leaves fp32 partials, which a second launch joins.
+// Roles (16 warps) run on their own through all units of the range, tied by
+// barriers on the buffers alone, so that a unit's end overlaps the next one's
+// beginning:
+//   0-7    softmax, a thread per row (0-3 tile 0, 4-7 tile 1): they bring their
+//          tile's next Q in before they wait for the last product
+//   8-11   widening of V, and NaN codes of blocks with masked keys taken out
+//   12, 13 MMA issuers of the tiles: S of a block goes out behind PV of the one
+//          before it, so one tile's products run under the other's softmax
+//   14, 15 producers of K and of V with the pages' scales
+#include <type_traits>
+
+#include "tsv_paged_tc.cuh"
+
+namespace tsv {
+
+namespace {
+
+constexpr int kCThreads = 512;
+constexpr int kCConvWarp = 8, kCMmaWarp = 12, kCKWarp = 14, kCVWarp = 15;
+// Registers a thread: 512 x 128 at launch = 256 x 192 + 256 x 64.
+constexpr int kCSoftRegs = 192, kCRestRegs = 64;
+static_assert(256 * kCSoftRegs + 256 * kCRestRegs <= kCThreads * 128, "register split");
+constexpr int kTileRows = 128;
+constexpr int kKStages = 3;
+constexpr float kRise = 4.f;    // log2: how far a score may pass the reference maximum
+constexpr float kUp = 11.f;     // log2 of P's factor: 2^4 x 2^11 is within fp16
+constexpr int kFarApart = 40;   // log2: V scales that far apart leave a row's weights their bits
+// What a unit costs beside its blocks, in blocks; and how near to a unit's end a cut may come.
+constexpr int kUnitCost = 3, kLeastCut = 8, kNearEnd = 3;
+constexpr int kBarConv = 1;
+constexpr int kNanSlots = 6;    // blocks of a unit with masked keys: 3 at each end
+
+// A row's last key, its unit and its part.
+struct CUnit {
+  int b, tile, g;
+  int off, n, start, tiles;  // of the request
+  int row0, rows;
+  int first, end;            // blocks of the unit
+  int j, j1;                 // and those of this part
+  __device__ __forceinline__ bool whole() const { return j == first && j1 == end; }
+};
+
+struct ChunkGeometry {
+  int G, R, window;
+  // Blocks that rows r0 .. r1 of request (start) see: first, end.
+  __device__ __forceinline__ int2 blocks(int start, int r0, int r1) const {
+    const int p0 = start + r0 / G, p1 = start + r1 / G;
+    const int lo = window > 0 ? max(0, p0 - window + 1) : 0;
+    return make_int2(lo / kPBlock, p1 / kPBlock + 1);
+  }
+};
+
+template <int D>
+struct CCfg {
+  static constexpr int kQTile = kTileRows * D;       // one term of a Q tile
+  static constexpr int kKTile = kPBlock * D;         // codes of a block
+  static constexpr int kVTile = kPBlock * D * 2;
+  static constexpr int kOffQ = 0;                                   // [tile][hi, lo]
+  static constexpr int kOffK = kOffQ + 4 * kQTile;                  // ring of codes
+  static constexpr int kOffRaw = kOffK + kKStages * kKTile;         // V's codes
+  static constexpr int kOffV = kOffRaw + 2 * kKTile;                // V in fp16
+  static constexpr int kOffReq = kOffV + 2 * kVTile;                // int4 [TSV_MAX_BATCH]: off, n, start, tiles
+  static constexpr int kOffTiles = kOffReq + 16 * TSV_MAX_BATCH;    // i32 [TSV_MAX_BATCH + 4]: tiles of the requests before
+  static constexpr int kOffPre = kOffTiles + 4 * (TSV_MAX_BATCH + 4);  // i64 [17 + 3]
+  static constexpr int kOffFr = kOffPre + 8 * 20;                   // f32 [256]: score factor of a row
+  static constexpr int kOffScale = kOffFr + 4 * 256;                // f32 [4][36]
+  static constexpr int kOffNan = kOffScale + 4 * 144;               // u32 [2][kNanSlots][4]
+  static constexpr int kOffCut = kOffNan + 2 * kNanSlots * 16;      // i32 [2][4]: f, g, j of the range's ends
+  // k_full[3], k_empty[3], raw_full[2], raw_empty[2], v_full[2], v_empty[2], sc_full[4], s_full[2], p_full[4], pv_done[2],
+  // q_full[2], mma_done
+  static constexpr int kOffBar = kOffCut + 32;
+  static constexpr int kBars = 2 * kKStages + 23;
+  static constexpr int kOffMisc = kOffBar + 8 * kBars + 8;
+  static constexpr int kSmem = kOffMisc + 64 + 1024;
+  static constexpr uint32_t kColO = 2 * kPBlock;  // S0 | S1 | O0 | O1
+  static_assert(kSmem <= 227 * 1024, "shared memory");
+  static_assert(kOffPre % 16 == 0 && kOffScale % 16 == 0 && kOffBar % 8 == 0, "alignment");
+};
+
+// What a CTA did of groups that others share, for the launch that joins them.
+struct alignas(16) ChunkPart {
+  int empty, cont, through, lead;  // first unit continues a group (and goes on in the next CTA); the last one begins a cut group
+  int off, row0, rows, g;          // of the group that is begun
+};
+
+__device__ __forceinline__ void umma_e4m3(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accumulate,
+                                          uint32_t lead) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(lead)
+      : "memory");
+}
+__device__ __forceinline__ void umma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc, uint32_t accumulate,
+                                            uint32_t lead) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(lead)
+      : "memory");
+}
+// e4m3 (kind::f8f6f4) or fp16 (kind::f16) A and B, fp32 D; A K-major, B K-major (0) or N-major (1).
+__host__ __device__ constexpr uint32_t idesc_mn(int M, int N, int b_mn) {
+  return (1u << 4) | ((uint32_t)b_mn << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+template <int ROW>
+__device__ __forceinline__ uint64_t sdesc_row(uint32_t saddr, uint32_t lbo) {
+  uint64_t d = sdesc_sw128(saddr, lbo, 8 * ROW);
+  if (ROW == 64) d = (d & ~(7ull << 61)) | (4ull << 61);
+  return d;
+}
+// Position of 16-byte chunk c of row r in a swizzled tile of ROW-byte rows.
+template <int ROW>
+__device__ __forceinline__ int swizzled(int r, int c) {
+  return ROW == 128 ? r * 128 + ((c ^ (r & 7)) << 4) : r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+// Bytes that are NaN codes, as their top bits.
+__device__ __forceinline__ uint32_t nan_bytes(uint32_t w) { return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u; }
+__device__ __forceinline__ uint32_t bits_below(int n) { return n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1u; }
+
+// A wait after which the whole warp knows whether it is dead.
+#define TSV_CWAIT(bar, parity)                                    \
+  do {                                                            \
+    pwait((bar), (uint32_t)(parity), abort_v, dead);              \
+    dead = __any_sync(0xffffffffu, dead);                         \
+  } while (0)
+
+template <int D>
+__global__ void __launch_bounds__(kCThreads, 1)
+    paged_chunk_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
+                       const __grid_constant__ PagedAttnArgs a, int R, int32_t* timeouts, ChunkPart* __restrict__ parts,
+                       float* __restrict__ part_o, float* __restrict__ part_ml) {
+  using C = CCfg<D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sQ = smem + C::kOffQ;
+  uint8_t* sK = smem + C::kOffK;
+  uint8_t* sRaw = smem + C::kOffRaw;
+  uint8_t* sV = smem + C::kOffV;
+  int4* sReq = reinterpret_cast<int4*>(smem + C::kOffReq);
+  int32_t* sTiles = reinterpret_cast<int32_t*>(smem + C::kOffTiles);
+  int64_t* sPre = reinterpret_cast<int64_t*>(smem + C::kOffPre);
+  float* sFr = reinterpret_cast<float*>(smem + C::kOffFr);
+  float* sScale = reinterpret_cast<float*>(smem + C::kOffScale);
+  uint32_t* sNan = reinterpret_cast<uint32_t*>(smem + C::kOffNan);
+  int32_t* sCut = reinterpret_cast<int32_t*>(smem + C::kOffCut);
+  uint64_t* k_full = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
+  uint64_t* k_empty = k_full + kKStages;
+  uint64_t* raw_full = k_empty + kKStages;
+  uint64_t* raw_empty = raw_full + 2;
+  uint64_t* v_full = raw_empty + 2;
+  uint64_t* v_empty = v_full + 2;
+  uint64_t* sc_full = v_empty + 2;   // scales of a block
+  uint64_t* s_full = sc_full + 4;    // [tile]
+  uint64_t* p_full = s_full + 2;     // [tile][half]
+  uint64_t* pv_done = p_full + 4;    // [tile]
+  uint64_t* q_full = pv_done + 2;    // [tile]
+  uint64_t* mma_done = q_full + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
+  int* abort_flag = reinterpret_cast<int*>(smem + C::kOffMisc + 4);
+  volatile int* abort_v = abort_flag;
+  volatile int* units_done = reinterpret_cast<int*>(smem + C::kOffMisc + 16);  // [8]: of the softmax warps
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int lps = __ffs(a.cache.page_size) - 1;  // pages are powers of two
+  const ChunkGeometry geo{a.G, R, a.window};
+  const int Hkv = a.cache.Hkv;
+  bool dead = false;
+
+  if (tid == 0) {
+    for (int s = 0; s < kKStages; ++s) {
+      mbar_init(&k_full[s], 1);
+      mbar_init(&k_empty[s], 2);  // both tiles' issuers
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&raw_full[s], 1);
+      mbar_init(&raw_empty[s], 4);  // the widening warps
+      mbar_init(&v_full[s], 4);
+      mbar_init(&v_empty[s], 2);
+      mbar_init(&s_full[s], 1);
+      mbar_init(&pv_done[s], 1);
+      mbar_init(&q_full[s], 4);
+    }
+    for (int s = 0; s < 4; ++s) {
+      mbar_init(&sc_full[s], 1);
+      mbar_init(&p_full[s], 128);
+    }
+    mbar_init(mma_done, 2);
+    *abort_flag = 0;
+    for (int w = 0; w < 8; ++w) units_done[w] = 0;
+    mbar_fence_init();
+  }
+  if (warp == kCMmaWarp) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  pdl_wait();  // the previous kernel's results are visible from here on
+  pdl_trigger();
+
+  // ------------------------------------------------------------ the list and this CTA's range
+  if (warp == 0) {
+    int before = 0;
+    if (lane == 0) sTiles[0] = 0;
+#pragma unroll 1
+    for (int b0 = 0; b0 < TSV_MAX_BATCH; b0 += 32) {
+      const int b = b0 + lane;
+      int tiles = 0;
+      PagedRequest r;
+      if (b < a.B && paged_request(a, b, &r) && r.n > 0) {
+        tiles = (int)(((int64_t)r.n * a.G + R - 1) / R);
+        sReq[b] = make_int4(r.off, r.n, r.P - r.n, tiles);
+      }
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, tiles, o);
+        if (lane >= o) tiles += y;
+      }
+      sTiles[b + 1] = before + tiles;
+      before += __shfl_sync(0xffffffffu, tiles, 31);
+    }
+  }
+  if (tid < 8) sCut[tid] = -1;
+  __syncthreads();
+  auto request_of = [&](int f) {  // the request that owns tile f of all
+    int lo = 0, hi = a.B - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (sTiles[mid + 1] > f) hi = mid;
+      else lo = mid + 1;
+    }
+    return lo;
+  };
+  auto tile_blocks = [&](int b, int tile) {
+    const int4 q = sReq[b];
+    const int r0 = tile * R, r1 = (int)(min((int64_t)r0 + R, (int64_t)q.y * a.G) - 1);
+    return geo.blocks(q.z, r0, r1);
+  };
+  const int all_tiles = sTiles[TSV_MAX_BATCH];
+  const int share = (all_tiles + kCThreads - 1) / kCThreads, f_lo = min(all_tiles, tid * share), f_hi = min(all_tiles, f_lo + share);
+  int64_t mine = 0;
+  for (int f = f_lo, b = f < f_hi ? request_of(f) : 0; f < f_hi; ++f) {
+    while (sTiles[b + 1] <= f) ++b;
+    const int2 t = tile_blocks(b, f - sTiles[b]);
+    mine += t.y - t.x + kUnitCost;
+  }
+  int64_t upto = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto += y;
+  }
+  if (lane == 31) sPre[warp + 1] = upto;
+  __syncthreads();
+  int64_t begin = upto - mine, total = 0;
+#pragma unroll 1
+  for (int w = 0; w < kCThreads / 32; ++w) {
+    if (w < warp) begin += sPre[w + 1];
+    total += sPre[w + 1];
+  }
+  begin *= Hkv;
+  total *= Hkv;
+  {
+    const int64_t ctas = gridDim.x;
+    const int64_t x[2] = {total * blockIdx.x / ctas, total * (blockIdx.x + 1) / ctas};
+#pragma unroll 1
+    for (int e = 0; e < 2; ++e) {
+      if (mine == 0 || x[e] < begin || x[e] >= begin + mine * Hkv) continue;
+      int64_t at = begin;
+      int f = f_lo, b = request_of(f);
+      int2 t = tile_blocks(b, f - sTiles[b]);
+      while (x[e] >= at + (int64_t)(t.y - t.x + kUnitCost) * Hkv) {
+        at += (int64_t)(t.y - t.x + kUnitCost) * Hkv;
+        ++f;
+        while (sTiles[b + 1] <= f) ++b;
+        t = tile_blocks(b, f - sTiles[b]);
+      }
+      const int T = t.y - t.x;
+      int g = (int)((x[e] - at) / (T + kUnitCost));
+      int j = max(0, (int)(x[e] - at - (int64_t)g * (T + kUnitCost)) - kUnitCost);
+      // Short units stay whole, and no part is short.
+      if (T < kLeastCut) j = 2 * j < T ? 0 : T;
+      else if (j < kNearEnd) j = 0;
+      else if (T - j < kNearEnd) j = T;
+      if (j == T) {
+        j = 0;
+        if (++g == Hkv) {
+          g = 0;
+          ++f;
+        }
+      }
+      sCut[4 * e] = f;
+      sCut[4 * e + 1] = g;
+      sCut[4 * e + 2] = j;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  // The units of the range, for every role by itself.
+  struct Cut {
+    int f, g, j;
+  };
+  const Cut from{sCut[0] < 0 ? all_tiles : sCut[0], sCut[0] < 0 ? 0 : sCut[1], sCut[0] < 0 ? 0 : sCut[2]};
+  const Cut to{sCut[4] < 0 ? all_tiles : sCut[4], sCut[4] < 0 ? 0 : sCut[5], sCut[4] < 0 ? 0 : sCut[6]};
+  auto load_unit = [&](CUnit& u, int f) {  // g, tile and b are set
+    const int4 q = sReq[u.b];
+    u.off = q.x;
+    u.n = q.y;
+    u.start = q.z;
+    u.tiles = q.w;
+    u.row0 = u.tile * R;
+    u.rows = (int)min((int64_t)R, (int64_t)u.n * a.G - u.row0);
+    const int2 t = geo.blocks(u.start, u.row0, u.row0 + u.rows - 1);
+    u.first = t.x;
+    u.end = t.y;
+    u.j = u.first;
+    u.j1 = f == to.f && u.g == to.g ? u.first + to.j : u.end;
+  };
+  auto first_unit = [&](CUnit& u) {
+    if (from.f >= all_tiles || (from.f == to.f && from.g == to.g && from.j == to.j)) return false;
+    u.b = request_of(from.f);
+    u.tile = from.f - sTiles[u.b];
+    u.g = from.g;
+    load_unit(u, from.f);
+    u.j = u.first + from.j;
+    return true;
+  };
+  auto next_unit = [&](CUnit& u) {
+    if (++u.g == Hkv) {
+      u.g = 0;
+      if (++u.tile == u.tiles) {
+        u.tile = 0;
+        do ++u.b;
+        while (u.b < a.B && sTiles[u.b + 1] == sTiles[u.b]);
+      }
+    }
+    const int f = u.b < a.B ? sTiles[u.b] + u.tile : all_tiles;
+    if (f > to.f || (f == to.f && (u.g > to.g || (u.g == to.g && to.j == 0))) || f >= all_tiles) return false;
+    load_unit(u, f);
+    return true;
+  };
+  // Blocks of a tile among those of the part (none: both at its end).
+  auto tile_range = [&](const CUnit& u, int q) {
+    const int r0 = q * kTileRows, r1 = min(u.rows, r0 + kTileRows) - 1;
+    int2 t = make_int2(u.j1, u.j1);
+    if (r0 < u.rows) {
+      const int2 x = geo.blocks(u.start, u.row0 + r0, u.row0 + r1);
+      const int lo = max(u.j, x.x), hi = min(u.j1, x.y);
+      if (lo < hi) t = make_int2(lo, hi);
+    }
+    return t;
+  };
+  // Whether all rows r0 .. r1 of the unit see all keys of block j.
+  auto seen_by_all = [&](const CUnit& u, int r0, int r1, int j) {
+    const int p0 = u.start + (u.row0 + r0) / a.G, p1 = u.start + (u.row0 + r1) / a.G;
+    return j * kPBlock + kPBlock - 1 <= p0 && (a.window == 0 || j * kPBlock > p1 - a.window);
+  };
+  CUnit u{};
+
+  if (warp == 0) {  // what the joining launch has to know
+    CUnit v{};
+    const bool any = first_unit(v);
+    ChunkPart p{};
+    p.empty = any ? 0 : 1;
+    if (any) {
+      p.cont = v.j > v.first;
+      p.through = p.cont && v.j1 < v.end;
+      if (to.j > 0 && !(from.f == to.f && from.g == to.g && from.j > 0)) {  // the last unit begins a group
+        p.lead = 1;
+        v.b = request_of(to.f);
+        v.tile = to.f - sTiles[v.b];
+        v.g = to.g;
+        load_unit(v, to.f);
+        p.off = v.off;
+        p.row0 = v.row0;
+        p.rows = v.rows;
+        p.g = v.g;
+      }
+    }
+    if (lane == 0) parts[blockIdx.x] = p;
+  }
+
+  if (warp < kCConvWarp) {
+    // ---------------------------------------------------------- softmax: a thread owns a row
+    setmaxnreg_inc<kCSoftRegs>();
+    const int tile = warp >> 2, r = tid & (kTileRows - 1), row = tile * kTileRows + r;
+    const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t s_col = tmem + lane_base + (uint32_t)(tile * kPBlock);
+    const uint32_t o_col = tmem + lane_base + C::kColO + (uint32_t)(tile * D);
+    // The warp's rows of q, as two e4m3 terms each.
+    auto bring_q = [&](const CUnit& v) {
+      constexpr int kLanes = D / 8, kRows = 32 / kLanes, kPasses = 32 / kRows, kBatch = 8;
+      int64_t at = -1;
+      if (row < v.rows) {
+        const int gr = v.row0 + row, token = gr / a.G;
+        at = (int64_t)(v.off + token) * a.qs_n + (int64_t)(v.g * a.G + (gr - token * a.G)) * a.qs_h;
+      }
+      const int part = lane % kLanes, sub = lane / kLanes;
+#pragma unroll 1
+      for (int p0 = 0; p0 < kPasses; p0 += kBatch) {
+        uint4 raw[kBatch];
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+          const int64_t x = __shfl_sync(0xffffffffu, at, (p0 + i) * kRows + sub);
+          raw[i] = make_uint4(0u, 0u, 0u, 0u);
+          if (x >= 0) raw[i] = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + x + part * 8));
+        }
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+          const int rr = (p0 + i) * kRows + sub;  // of the warp
+          const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+          uint32_t top = 0u;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) top = max(top, max((w[e] << 16) & 0x7FFF0000u, w[e] & 0x7FFF0000u));
+#pragma unroll
+          for (int o = 1; o < kLanes; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+          const bool fine = top < 0x7F800000u;  // a row with an infinity or a NaN is NaN throughout (its scores are)
+          const int up = top == 0u ? 0 : max(-120, min(120, 134 - (int)(top >> 23)));
+          const float mul = __uint_as_float((uint32_t)(127 + up) << 23);
+          uint32_t hi[2], lo[2];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float x0 = __uint_as_float(w[e] << 16) * mul, x1 = __uint_as_float(w[e] & 0xFFFF0000u) * mul;
+            const uint32_t h = e4m3x2(x0, x1), b2 = f16x2_of_e4m3x2(h);
+            const uint32_t l = e4m3x2(x0 - f16_lo(b2), x1 - f16_hi(b2));
+            if (e & 1) {
+              hi[e >> 1] |= h << 16;
+              lo[e >> 1] |= l << 16;
+            } else {
+              hi[e >> 1] = h;
+              lo[e >> 1] = l;
+            }
+          }
+          if (!fine) hi[0] = hi[1] = lo[0] = lo[1] = 0x7F7F7F7Fu;
+          const int tr = (warp & 3) * 32 + rr;
+          uint8_t* to_hi = sQ + tile * 2 * C::kQTile + swizzled<D>(tr, part >> 1) + 8 * (part & 1);
+          *reinterpret_cast<uint2*>(to_hi) = make_uint2(hi[0], hi[1]);
+          *reinterpret_cast<uint2*>(to_hi + C::kQTile) = make_uint2(lo[0], lo[1]);
+          if (part == 0) sFr[tile * kTileRows + tr] = __uint_as_float((uint32_t)(127 - up) << 23) * (a.scale * 1.4426950408889634f);
+        }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&q_full[tile]);
+    };
+    int t = 0, cnt = 0, units = 0;  // blocks and units of all roles, blocks of the tile
+    auto takes_part = [&](const CUnit& v) {
+      const int2 x = tile_range(v, tile);
+      return x.x < x.y;
+    };
+    bool going = first_unit(u);
+    if (going && takes_part(u)) bring_q(u);
+    while (going) {
+      const int2 range = tile_range(u, tile);
+      const bool active = tile * kTileRows < u.rows;
+      const float fr = sFr[row];
+      const int pos = u.start + (u.row0 + min(row, u.rows - 1)) / a.G;
+      float m_ref = -INFINITY, l = 0.f, v_ref = 0.f;
+      int room = kFarApart;  // how far the reference may still be lowered
+      auto step = [&](int j, auto masked_c) {
+        constexpr bool MASKED = decltype(masked_c)::value;
+        const int x = t + j - u.j;
+        TSV_CWAIT(&s_full[tile], cnt);
+        TSV_CWAIT(&sc_full[x & 3], x >> 2);
+        if (dead) return;
+        tc_fence_after();
+        uint32_t s[4][32];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld32_nowait(s_col + 32 * c, s[c]);
+        const float* sc = sScale + (x & 3) * 36;
+        // Per 16 keys: the factor of the scores, the logarithm of V's scale for the maximum.
+        float f[8], g[8];
+#pragma unroll
+        for (int q = 0; q < 8; q += 4) {
+          *reinterpret_cast<float4*>(f + q) = *reinterpret_cast<const float4*>(sc + q);
+          *reinterpret_cast<float4*>(g + q) = *reinterpret_cast<const float4*>(sc + 8 + q);
+        }
+#pragma unroll
+        for (int q = 0; q < 8; ++q) f[q] *= fr;
+        const float v_top = sc[32];
+        const bool even = sc[33] != 0.f;  // every scale goes into the exponent
+        uint32_t see[4] = {~0u, ~0u, ~0u, ~0u};
+        if (MASKED) {
+          const int hi = pos - j * kPBlock + 1, lo = a.window > 0 ? hi - a.window : 0;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) see[c] = bits_below(hi - 32 * c) & ~bits_below(lo - 32 * c);
+        }
+        tmem_wait_ld_tie32(s[0]);
+        reg_tie32(s[1]);
+        reg_tie32(s[2]);
+        reg_tie32(s[3]);
+        if (MASKED) {
+#pragma unroll
+          for (int e = 0; e < 128; ++e)
+            if (!((see[e >> 5] >> (e & 31)) & 1u)) s[e >> 5][e & 31] = 0xFF800000u;
+        }
+        float alpha = 1.f;
+        if (v_top > v_ref) {  // the same in every thread
+          // What was summed up stays, under a reference that is lower by as much as
+          // the relative scales of its keys now are (powers of two: l goes with it).
+          if (v_ref > 0.f) {
+            const float c = v_ref / v_top;
+            const int down = min(127 - (int)(__float_as_uint(c) >> 23), room);
+            const float up = __uint_as_float((uint32_t)(127 + down) << 23);
+            room -= down;
+            m_ref -= (float)down;
+            l *= up;
+            alpha = c * up;  // 1 for scales that are powers of two
+          }
+          v_ref = v_top;
+        }
+        float top = -INFINITY;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          const uint32_t* z = &s[q >> 1][(q & 1) * 16];
+          float b0 = fmaxf(__uint_as_float(z[0]), __uint_as_float(z[1]));
+          float b1 = fmaxf(__uint_as_float(z[2]), __uint_as_float(z[3]));
+#pragma unroll
+          for (int e = 4; e < 16; e += 4) {
+            b0 = fmax3(b0, __uint_as_float(z[e]), __uint_as_float(z[e + 1]));
+            b1 = fmax3(b1, __uint_as_float(z[e + 2]), __uint_as_float(z[e + 3]));
+          }
+          top = fmaxf(top, fmaf(fmaxf(b0, b1), f[q], g[q]));
+        }
+        if (top > m_ref + kRise) {
+          const float c = fast_exp2(m_ref - top);  // 0 when m_ref = -inf
+          m_ref = top;
+          l *= c;
+          alpha *= c;
+        }
+        if (j > range.x && __any_sync(0xffffffffu, alpha != 1.f)) {
+          TSV_CWAIT(&pv_done[tile], cnt - 1);
+          tc_fence_after();
+#pragma unroll 1
+          for (int cc = 0; cc < D; cc += 16) {
+            float o[16];
+            tmem_ld16(o_col + cc, o);
+            uint32_t z16[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) z16[e] = __float_as_uint(o[e] * alpha);
+            tmem_st16u_nowait(o_col + cc, z16);
+          }
+        }
+        const float base = m_ref == -INFINITY ? kUp : kUp - m_ref;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t p[16];
+#pragma unroll
+          for (int q = 2 * c; q < 2 * c + 2; ++q) {
+            const float in_exp = even ? g[q] : sc[16 + q];  // logarithm of V's scale, 0 when it is a factor of its own
+            const uint64_t ref2 = f2_pack(base + in_exp, base + in_exp), f2 = f2_pack(f[q], f[q]);
+            uint64_t sum = 0ull;
+            float w[16];
+#pragma unroll
+            for (int e = 0; e < 16; e += 2) {
+              const int k = (q & 1) * 16 + e;
+              const uint64_t x2 = ffma2((uint64_t)s[c][k] | ((uint64_t)s[c][k + 1] << 32), f2, ref2);
+              w[e] = fast_exp2(f2_lo(x2));
+              w[e + 1] = fast_exp2(f2_hi(x2));
+              if (MASKED) {
+                if (!((see[c] >> k) & 1u)) w[e] = 0.f;
+                if (!((see[c] >> (k + 1)) & 1u)) w[e + 1] = 0.f;
+              }
+              sum = fadd2(sum, f2_pack(w[e], w[e + 1]));
+            }
+            l = fmaf(f2_lo(sum) + f2_hi(sum), fast_exp2(-in_exp), l);
+            if (!even) {
+              const float own = sc[24 + q];
+#pragma unroll
+              for (int e = 0; e < 16; ++e) w[e] *= own;
+            }
+#pragma unroll
+            for (int e = 0; e < 16; e += 2) p[(q & 1) * 8 + (e >> 1)] = pack_f16(w[e], w[e + 1]);
+          }
+          tmem_st16u_nowait(s_col + 16 * c, p);
+          if (c & 1) {  // the keys of half a block
+            tmem_wait_st();
+            tc_fence_before();
+            parrive(&p_full[2 * tile + (c >> 1)], dead);
+          }
+        }
+        ++cnt;
+      };
+      // The blocks that every row sees whole lie together.
+      int j = range.x;
+      if (active) {
+        const int r0 = tile * kTileRows, r1 = min(u.rows, r0 + kTileRows) - 1;
+#pragma unroll 1
+        for (; j < range.y && !seen_by_all(u, r0, r1, j) && !dead; ++j) step(j, std::true_type{});
+#pragma unroll 1
+        for (; j < range.y && seen_by_all(u, r0, r1, j) && !dead; ++j) step(j, std::false_type{});
+#pragma unroll 1
+        for (; j < range.y && !dead; ++j) step(j, std::true_type{});
+      }
+      const CUnit now = u;
+      going = next_unit(u);
+      if (dead) break;
+      if (going && takes_part(u)) bring_q(u);  // (the tile's last S is there: Q is free)
+      if (active) {
+        if (range.x < range.y) TSV_CWAIT(&pv_done[tile], cnt - 1);
+        if (dead) break;
+        tc_fence_after();
+        const int gr = now.row0 + row, token = gr / a.G;
+        // Columns of a row whose NaN codes were kept out of the product.
+        uint32_t bad[D / 32];
+#pragma unroll
+        for (int q = 0; q < D / 32; ++q) bad[q] = 0u;
+        if (row < now.rows) {
+          const uint32_t* nan = sNan + (units & 1) * (kNanSlots * 4);
+#pragma unroll 1
+          for (int w = 0; w < kNanSlots * 4; ++w) {
+            const int slot = w >> 2, jb = slot < 3 ? now.first + slot : now.end - 1 - (slot - 3);
+            uint32_t seen = nan[w];
+            if (seen == 0u) continue;
+            const int base = jb * kPBlock + 32 * (w & 3);
+            seen &= bits_below(pos - base + 1) & (a.window > 0 ? ~bits_below(pos - base + 1 - a.window) : ~0u);
+#pragma unroll 1
+            for (; seen; seen &= seen - 1) {
+              const int key = base + __ffs(seen) - 1;
+              const int id = __ldg(a.table.ids_d + (int64_t)now.b * a.table.stride + (key >> lps));
+              if ((uint32_t)id >= (uint32_t)a.cache.num_pages) continue;
+              const uint32_t* v = reinterpret_cast<const uint32_t*>(
+                  static_cast<const uint8_t*>(a.cache.v_d) + (int64_t)id * a.cache.stride_page +
+                  (int64_t)(key & ((1 << lps) - 1)) * a.cache.stride_row + (int64_t)now.g * a.cache.stride_head);
+#pragma unroll
+              for (int e = 0; e < D / 4; ++e) {
+                const uint32_t m = nan_bytes(__ldg(v + e)) >> 7;  // bits 0, 8, 16, 24
+                bad[e >> 3] |= ((m | (m >> 7) | (m >> 14) | (m >> 21)) & 15u) << (4 * (e & 7));
+              }
+            }
+          }
+        }
+        // (v_ref may be 2^-126, a page of zeros', or little more: then it is a factor of its own.)
+        const bool none = range.x >= range.y || l == 0.f, tiny = v_ref < 0x1p-60f;
+        const float inv = none ? 0.f : 1.f / l * (tiny ? 1.f : v_ref);
+        const bool whole = now.whole();
+        const int slot = 2 * (int)blockIdx.x + (now.j > now.first ? 0 : 1);
+        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) +
+                             ((int64_t)(now.off + token) * a.Hq + now.g * a.G + (gr - token * a.G)) * D;
+        float* po = part_o + ((int64_t)slot * kPagedWideRows + row) * D;
+#pragma unroll 1
+        for (int cc = 0; cc < D; cc += 32) {
+          float o[32];
+          tmem_ld32(o_col + cc, o);
+          if (row >= now.rows) continue;
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = none ? 0.f : o[e] * inv;
+          if (tiny) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] *= v_ref;
+          }
+          uint32_t nans = bad[0];
+#pragma unroll
+          for (int q = 1; q < D / 32; ++q)
+            if (cc == 32 * q) nans = bad[q];
+          if (nans) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if ((nans >> e) & 1u) o[e] = NAN;
+          }
+          if (whole) {
+#pragma unroll
+            for (int e = 0; e < 32; e += 8)
+              *reinterpret_cast<uint4*>(out + cc + e) = make_uint4(pack_bf16x2(o[e], o[e + 1]), pack_bf16x2(o[e + 2], o[e + 3]),
+                                                                   pack_bf16x2(o[e + 4], o[e + 5]), pack_bf16x2(o[e + 6], o[e + 7]));
+          } else {
+#pragma unroll
+            for (int e = 0; e < 32; e += 4) *reinterpret_cast<float4*>(po + cc + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+          }
+        }
+        if (!whole && row < now.rows) {  // normalised: its sum is 1
+          float* pm = part_ml + (int64_t)slot * 2 * kPagedWideRows;
+          pm[row] = none ? -INFINITY : l > 0.f ? m_ref + log2f(l) : m_ref;
+          pm[kPagedWideRows + row] = none ? 0.f : l > 0.f ? 1.f : l;
+        }
+        tc_fence_before();
+      }
+      t += now.j1 - now.j;
+      ++units;
+      __syncwarp();
+      if (lane == 0) units_done[warp] = units;  // (a warp whose tile sits units out may be far ahead)
+    }
+  } else {
+    setmaxnreg_dec<kCRestRegs>();
+    if (warp < kCMmaWarp) {
+      // -------------------------------------------------------- V, widened
+      const int ct = tid - kCConvWarp * 32;
+      constexpr int kLanes = D / 16, kStep = 128 / kLanes, kParts = kPBlock / kStep;  // lanes of a row; rows of a thread
+      // Eight lanes take four 16-code chunks of two rows: their stores meet 32 banks.
+      const int chunk = D == 128 ? (ct & 3) | ((ct >> 1) & 4) : ct & 3;
+      const int first_row = D == 128 ? ((ct >> 2) & 1) | ((ct >> 4) << 1) : ct >> 2;
+      int t = 0, units = 0;
+      for (bool going = first_unit(u); going; going = next_unit(u)) {
+        const int par = units & 1;
+        // The rows of the unit before last, which had these words, are done with them.
+        for (uint64_t t0 = 0; !__all_sync(0xffffffffu, lane >= 8 || units_done[lane & 7] >= units - 1);) {
+          const uint64_t now = global_timer_ns();
+          if (t0 == 0) t0 = now;
+          if (__any_sync(0xffffffffu, *abort_v != 0 || now - t0 > kWaitLimitNs)) {
+            *abort_v = 1;
+            dead = true;
+            break;
+          }
+        }
+        if (ct < kNanSlots * 4) sNan[par * (kNanSlots * 4) + ct] = 0u;
+        dead = named_bar_or(kBarConv, 128, dead);
+        if (dead) break;
+        const int keys = u.start + min(u.n, (u.row0 + u.rows - 1) / a.G + 1);  // behind the last one that a row sees
+#pragma unroll 1
+        for (int j = u.j; j < u.j1; ++j) {
+          const int x = t + j - u.j, st = x & 1, valid = keys - j * kPBlock;
+          TSV_CWAIT(&raw_full[st], x >> 1);
+          if (x >= 2) TSV_CWAIT(&v_empty[st], (x >> 1) - 1);
+          if (dead) break;
+          const bool masked = !seen_by_all(u, 0, u.rows - 1, j);
+          const int slot = j - u.first < 3 ? j - u.first : u.end - 1 - j < 3 ? 3 + u.end - 1 - j : 0;
+#pragma unroll
+          for (int h = 0; h < kParts; h += 4) {
+            uint4 codes[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const int key = first_row + (h + q) * kStep;
+              codes[q] = make_uint4(0u, 0u, 0u, 0u);
+              if (key < valid) codes[q] = *reinterpret_cast<const uint4*>(sRaw + st * C::kKTile + swizzled<D>(key, chunk));
+            }
+            if (masked) {
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                uint32_t* v = reinterpret_cast<uint32_t*>(&codes[q]);
+                uint32_t any = 0u;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  const uint32_t bad = nan_bytes(v[e]);
+                  any |= bad;
+                  v[e] &= ~((bad >> 7) * 0xFFu);
+                }
+                const int key = first_row + (h + q) * kStep;
+                if (any) atomicOr(&sNan[par * (kNanSlots * 4) + slot * 4 + (key >> 5)], 1u << (key & 31));
+              }
+            }
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const int key = first_row + (h + q) * kStep;
+              const uint4 c = codes[q];
+              uint8_t* to_row = sV + st * C::kVTile + (chunk >> 2) * (kPBlock * 128) + key * 128;
+              const int at = (((2 * chunk) & 7) ^ (key & 7)) << 4;  // chunk 2 c of 8 values, and its neighbour
+              *reinterpret_cast<uint4*>(to_row + at) = make_uint4(f16x2_of_e4m3x2(c.x & 0xFFFFu), f16x2_of_e4m3x2(c.x >> 16),
+                                                                  f16x2_of_e4m3x2(c.y & 0xFFFFu), f16x2_of_e4m3x2(c.y >> 16));
+              *reinterpret_cast<uint4*>(to_row + (at ^ 16)) = make_uint4(f16x2_of_e4m3x2(c.z & 0xFFFFu), f16x2_of_e4m3x2(c.z >> 16),
+                                                                         f16x2_of_e4m3x2(c.w & 0xFFFFu), f16x2_of_e4m3x2(c.w >> 16));
+            }
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&v_full[st]);
+            mbar_arrive(&raw_empty[st]);
+          }
+        }
+        t += u.j1 - u.j;
+        ++units;
+      }
+    } else if (warp < kCKWarp) {
+      // -------------------------------------------------------- issuer of a tile
+      const int q = warp - kCMmaWarp;
+      constexpr uint32_t idS = idesc_mn(kTileRows, kPBlock, 0), idPV = idesc_mn(kTileRows, D, 1);
+      const uint64_t dq = sdesc_row<D>(smem_u32(sQ + q * 2 * C::kQTile), 16);
+      const uint64_t dk = sdesc_row<D>(smem_u32(sK), 16);
+      const uint64_t dv = sdesc_sw128(smem_u32(sV), kPBlock * 128, 1024);
+      const uint32_t s_at = tmem + (uint32_t)(q * kPBlock), o_at = tmem + C::kColO + (uint32_t)(q * D);
+      int t = 0, cnt = 0, mine_units = 0;
+      for (bool going = first_unit(u); going && !dead; going = next_unit(u)) {
+        const int2 range = tile_range(u, q);
+        // A block that no row of the tile sees (or a unit without the tile): the issuer
+        // keeps step with the rings, so that no wait is for a phase further on.
+        auto skip = [&](int j) {
+          const int x = t + j - u.j;
+          TSV_CWAIT(&k_full[x % kKStages], x / kKStages);
+          TSV_CWAIT(&v_full[x & 1], x >> 1);
+          if (dead) return;
+          if (elect_one()) {
+            mbar_arrive(&k_empty[x % kKStages]);
+            mbar_arrive(&v_empty[x & 1]);
+          }
+          __syncwarp();
+        };
+        auto issue_s = [&](int j) {
+          const int x = t + j - u.j, st = x % kKStages;
+          TSV_CWAIT(&k_full[st], x / kKStages);
+          if (dead) return;
+          tc_fence_after();
+          const uint32_t db = (uint32_t)dk + (uint32_t)((st * C::kKTile) >> 4);
+          const bool lead = elect_one();
+#pragma unroll
+          for (int term = 0; term < 2; ++term)
+#pragma unroll
+            for (int kk = 0; kk < D / 32; ++kk)
+              umma_e4m3(s_at, desc_at(dq, (uint32_t)dq + (uint32_t)((term * C::kQTile) >> 4) + kk * 2), desc_at(dk, db + kk * 2), idS,
+                        term + kk > 0 ? 1u : 0u, lead);
+          if (lead) {
+            umma_commit(&s_full[q]);
+            umma_commit(&k_empty[st]);
+          }
+          __syncwarp();
+        };
+        if (range.x < range.y) {
+          TSV_CWAIT(&q_full[q], mine_units);
+          ++mine_units;
+        }
+#pragma unroll 1
+        for (int j = u.j; j < range.x && !dead; ++j) skip(j);
+        if (range.x < range.y && !dead) issue_s(range.x);
+#pragma unroll 1
+        for (int j = range.x; j < range.y && !dead; ++j) {
+          const int x = t + j - u.j;
+          TSV_CWAIT(&v_full[x & 1], x >> 1);
+          const uint32_t db = (uint32_t)dv + (uint32_t)(((x & 1) * C::kVTile) >> 4);
+#pragma unroll 1
+          for (int half = 0; half < 2; ++half) {
+            TSV_CWAIT(&p_full[2 * q + half], cnt);
+            if (dead) break;
+            tc_fence_after();
+            const bool lead = elect_one();
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)  // 16 keys each; P, two keys a column, lies over its S
+              umma_f16_ts(o_at, s_at + half * 32 + kk * 8, desc_at(dv, db + (uint32_t)((half * 64 * 128 + kk * 16 * 128) >> 4)), idPV,
+                          j > range.x || half + kk > 0 ? 1u : 0u, lead);
+            __syncwarp();
+          }
+          if (dead) break;
+          if (elect_one()) {
+            umma_commit(&pv_done[q]);
+            umma_commit(&v_empty[x & 1]);
+          }
+          __syncwarp();
+          ++cnt;
+          if (j + 1 < range.y) issue_s(j + 1);
+        }
+        if (range.x < range.y) {
+#pragma unroll 1
+          for (int j = range.y; j < u.j1 && !dead; ++j) skip(j);
+        }
+        t += u.j1 - u.j;
+      }
+      __syncwarp();
+      if (elect_one()) umma_commit(mma_done);  // every MMA has finished before TMEM is freed
+      __syncwarp();
+      mbar_wait(mma_done, 0, nullptr);
+    } else {
+      // -------------------------------------------------------- producers
+      const bool is_v = warp == kCVWarp;
+      const CUtensorMap* tmap = is_v ? &tmap_v : &tmap_k;
+      const tsv_paged_cache& c = a.cache;
+      const uint64_t pol = l2_policy_evict_last();
+      int t = 0, asked = 0;
+      for (bool going = first_unit(u); going && !dead; going = next_unit(u)) {
+        const int32_t* ids = a.table.ids_d + (int64_t)u.b * a.table.stride;
+        const int keys = u.start + min(u.n, (u.row0 + u.rows - 1) / a.G + 1);
+        const int page_end = (keys + (1 << lps) - 1) >> lps;
+        // Lane p holds page p of the next block.
+        auto page_of = [&](int j) {
+          const int p = ((j * kPBlock) >> lps) + lane;
+          return j < u.j1 && (lane << lps) < kPBlock && p < page_end ? __ldg(ids + p) : -1;
+        };
+        // Lanes 0 .. 7 (V's producer): the scales of 16 keys each.
+        float top = 0.f;
+        int next = page_of(u.j);
+#pragma unroll 1
+        for (int j = u.j; j < u.j1; ++j) {
+          const int x = t + j - u.j, now = next;
+          next = page_of(j + 1);
+          const int valid = min(kPBlock, keys - j * kPBlock);
+          const uint32_t pages = (uint32_t)(valid + (1 << lps) - 1) >> lps;
+          float sk = 0.f, sv = 0.f;
+          if (is_v) {
+            const int sid = __shfl_sync(0xffffffffu, now, (lane * 16) >> lps & 31);
+            if (lane < 8 && lane * 16 < valid && (uint32_t)sid < (uint32_t)c.num_pages) {
+              sk = __ldg(c.k_scale_d + (int64_t)sid * c.Hkv + u.g);
+              sv = __ldg(c.v_scale_d + (int64_t)sid * c.Hkv + u.g);
+            }
+          }
+          const int st = is_v ? x & 1 : x % kKStages;
+          uint64_t* full = is_v ? &raw_full[st] : &k_full[st];
+          if (is_v && x >= 2) TSV_CWAIT(&raw_empty[st], (x >> 1) - 1);
+          if (!is_v && x >= kKStages) TSV_CWAIT(&k_empty[st], x / kKStages - 1);
+          if (dead) break;
+          const uint32_t at = smem_u32(is_v ? sRaw : sK) + (uint32_t)(st * C::kKTile);
+          const bool lead = elect_one();
+          if (lead) mbar_expect_tx(full, (pages << lps) * D);
+          __syncwarp();
+#pragma unroll 1
+          for (uint32_t p = 0; p < pages; ++p)
+            tma_load_page(at + (p << lps) * D, tmap, smem_u32(full), (uint32_t)u.g, (uint32_t)__shfl_sync(0xffffffffu, now, (int)p), pol,
+                          lead);
+          __syncwarp();
+          if (lead) mbar_arrive(full);
+          asked = x + 1;
+          if (is_v) {
+            // The unit's largest V scale so far, and the block's relative to it.
+            top = fmaxf(top, __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(sv))));  // (scales are >= 0)
+            const float turn = top > 1.f ? 0x1p-64f : 0x1p64f;  // (the division wants an ordinary divisor)
+            const float rel = top > 0.f ? __fdiv_rn(sv * turn, top * turn) : 1.f;
+            const int e = (int)(__float_as_uint(rel) >> 23) - 127;
+            // A power of two not too far below goes into the exponent; keys past the end take part in nothing.
+            const bool past = lane * 16 >= valid;
+            const bool in_exp = past || ((__float_as_uint(rel) & 0x7FFFFFu) == 0u && e >= -kFarApart);
+            const bool all = __all_sync(0xffffffffu, lane >= 8 || in_exp);
+            float* sc = sScale + (x & 3) * 36;
+            if (lane < 8) {
+              sc[lane] = sk;
+              sc[8 + lane] = past ? 0.f : in_exp ? (float)e : fmaxf(__log2f(rel), -(float)kFarApart);
+              sc[16 + lane] = past || !in_exp ? 0.f : (float)e;
+              sc[24 + lane] = past || in_exp ? 1.f : rel;
+            }
+            if (lane == 0) {
+              sc[32] = top;
+              sc[33] = all ? 1.f : 0.f;
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sc_full[x & 3]);
+          }
+        }
+        t += u.j1 - u.j;
+      }
+      // Every copy has landed before the CTA leaves (whatever the other roles did).
+      const int stages = is_v ? 2 : kKStages;
+      for (int x = max(0, asked - stages); x < asked; ++x)
+        mbar_wait(is_v ? &raw_full[x & 1] : &k_full[x % kKStages], (x / stages) & 1, nullptr);
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (tid == 0 && *abort_v) {
+    CUnit v{};
+    for (bool on = first_unit(v); on; on = next_unit(v)) *static_cast<volatile int32_t*>(timeouts + v.b) = 1;
+  }
+  if (warp == kCMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// Joins the partials of a group (in the order of the CTAs) and checks the
+// requests: CTA c x kJoinParts + k takes rows k x 256 / kJoinParts .. of the group
+// that CTA c of the other launch began.
+constexpr int kJoinParts = 16, kJoinThreads = 256;
+template <int D>
+__global__ void __launch_bounds__(kJoinThreads) paged_chunk_join_kernel(const __grid_constant__ PagedAttnArgs a, int ctas,
+                                                                        const int32_t* timeouts, const ChunkPart* __restrict__ parts,
+                                                                        const float* __restrict__ part_o,
+                                                                        const float* __restrict__ part_ml) {
+  pdl_wait();  // the previous kernel's results are visible from here on
+  pdl_trigger();
+  const int tid = threadIdx.x;
+  if ((int)blockIdx.x < a.B) {
+    const int b = blockIdx.x;
+    PagedRequest r;
+    bool bad = !paged_request(a, b, &r);
+    if (!bad) bad = paged_bad_page(a, b, r, tid, kJoinThreads);
+    bad = __syncthreads_or(bad);
+    if (tid == 0) a.status[b] = timeouts[b] ? TSV_ERR_TIMEOUT : bad ? TSV_ERR_INVALID_ARG : TSV_OK;
+  }
+  const int c0 = blockIdx.x / kJoinParts, k = blockIdx.x % kJoinParts;
+  if (c0 >= ctas) return;
+  const ChunkPart p = parts[c0];
+  if (!p.lead) return;
+  constexpr int kRows = kPagedWideRows / kJoinParts, L4 = D / 4;  // 16 bytes a thread
+  for (int i = tid; i < kRows * L4; i += kJoinThreads) {
+    const int row = k * kRows + i / L4, d4 = (i % L4) * 4;
+    if (row >= p.rows) return;
+    float top = -INFINITY, sum = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    auto add = [&](int64_t slot) {
+      const float m = part_ml[slot * 2 * kPagedWideRows + row], l = part_ml[(slot * 2 + 1) * kPagedWideRows + row];
+      const float4 v = *reinterpret_cast<const float4*>(part_o + (slot * kPagedWideRows + row) * D + d4);
+      const float t2 = fmaxf(top, m);
+      const float f = top == -INFINITY ? 1.f : fast_exp2(top - t2);  // nothing yet: all zero (or NaN)
+      const float w = m == -INFINITY ? 1.f : fast_exp2(m - t2);
+      top = t2;
+      sum = sum * f + l * w;
+      o.x = o.x * f + v.x * w;
+      o.y = o.y * f + v.y * w;
+      o.z = o.z * f + v.z * w;
+      o.w = o.w * f + v.w * w;
+    };
+    add(2 * c0 + 1);
+    for (int c = c0 + 1; c < ctas; ++c) {
+      if (parts[c].empty) continue;
+      add(2 * c);
+      if (!parts[c].through) break;
+    }
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    const int gr = p.row0 + row, token = gr / a.G;
+    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) +
+                              ((int64_t)(p.off + token) * a.Hq + p.g * a.G + (gr - token * a.G)) * D + d4) =
+        make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+  }
+}
+
+template <int D>
+cudaError_t launch_typed(const CUtensorMap& tk, const CUtensorMap& tv, const PagedAttnArgs& a, int num_sms, void* ws, cudaStream_t st) {
+  char* w = static_cast<char*>(ws);
+  const PagedChunkLayout lay = paged_chunk_layout(num_sms, D);
+  int32_t* timeouts = reinterpret_cast<int32_t*>(w);
+  ChunkPart* parts = reinterpret_cast<ChunkPart*>(w + lay.parts);
+  float* po = reinterpret_cast<float*>(w + lay.part_o);
+  float* pm = reinterpret_cast<float*>(w + lay.part_ml);
+  // Units of 256 rows share a block's cost; with fewer of them than SMs, 128 each.
+  const int64_t tiles = ((int64_t)a.N * a.G + 255) / 256 * a.cache.Hkv;
+  const int R = tiles >= num_sms ? 256 : 128;
+  const cudaError_t e =
+      launch_pdl(paged_chunk_kernel<D>, dim3(num_sms), dim3(kCThreads), (size_t)CCfg<D>::kSmem, st, 0u, tk, tv, a, R, timeouts, parts, po, pm);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(paged_chunk_join_kernel<D>, dim3(num_sms * kJoinParts > a.B ? num_sms * kJoinParts : a.B), dim3(kJoinThreads), 0, st, 0u,
+                    a, num_sms, timeouts, parts, po, pm);
+}
+
+template <int D>
+cudaError_t set_typed() {
+  // The register split draws on what the block is launched with.
+  cudaFuncAttributes attr;
+  const cudaError_t e = cudaFuncGetAttributes(&attr, paged_chunk_kernel<D>);
+  if (e != cudaSuccess) return e;
+  if (attr.numRegs < 128) return cudaErrorInvalidConfiguration;
+  return cudaFuncSetAttribute(paged_chunk_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, CCfg<D>::kSmem);
+}
+
+}  // namespace
+
+static_assert(sizeof(ChunkPart) == kPagedChunkPartBytes, "workspace layout");
+
+cudaError_t paged_chunk_set_attributes(int32_t D) { return D == 64 ? set_typed<64>() : set_typed<128>(); }
+
+cudaError_t launch_paged_chunk(const CUtensorMap& tk, const CUtensorMap& tv, const PagedAttnArgs& a, int num_sms, void* ws,
+                               cudaStream_t st) {
+  return a.cache.D == 64 ? launch_typed<64>(tk, tv, a, num_sms, ws, st) : launch_typed<128>(tk, tv, a, num_sms, ws, st);
+}
+
+}  // namespace tsv
