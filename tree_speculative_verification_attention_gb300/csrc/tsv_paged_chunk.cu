@@ -49,7 +49,9 @@ constexpr float kUp = 11.f;     // log2 of P's factor: 2^4 x 2^11 is within fp16
 constexpr int kFarApart = 40;   // log2: V scales that far apart leave a row's weights their bits
 // What a unit costs beside its blocks, in blocks; and how near to a unit's end a cut may come.
 constexpr int kUnitCost = 3, kLeastCut = 8, kNearEnd = 3;
+constexpr uint32_t kCWaitTries = 1u << 22;  // (of a microsecond or less each)
 constexpr int kBarConv = 1;
+constexpr int kScaleRow = 44;   // of a block, per 16 keys: K's scale, V's logarithm for the maximum and in the exponent, its factor, 2^-; top, even
 constexpr int kNanSlots = 6;    // blocks of a unit with masked keys: 3 at each end
 
 // A row's last key, its unit and its part.
@@ -85,13 +87,13 @@ struct CCfg {
   static constexpr int kOffTiles = kOffReq + 16 * TSV_MAX_BATCH;    // i32 [TSV_MAX_BATCH + 4]: tiles of the requests before
   static constexpr int kOffPre = kOffTiles + 4 * (TSV_MAX_BATCH + 4);  // i64 [17 + 3]
   static constexpr int kOffFr = kOffPre + 8 * 20;                   // f32 [256]: score factor of a row
-  static constexpr int kOffScale = kOffFr + 4 * 256;                // f32 [4][36]
-  static constexpr int kOffNan = kOffScale + 4 * 144;               // u32 [2][kNanSlots][4]
+  static constexpr int kOffScale = kOffFr + 4 * 256;                // f32 [4][kScaleRow]
+  static constexpr int kOffNan = kOffScale + 16 * kScaleRow;               // u32 [2][kNanSlots][4]
   static constexpr int kOffCut = kOffNan + 2 * kNanSlots * 16;      // i32 [2][4]: f, g, j of the range's ends
-  // k_full[3], k_empty[3], raw_full[2], raw_empty[2], v_full[2], v_empty[2], sc_full[4], s_full[2], p_full[4], pv_done[2],
+  // k_full[3], k_empty[3], raw_full[2], raw_empty[2], v_full[2], v_empty[2], sc_full[4], s_full[4], p_full[4], pv_done[4],
   // q_full[2], mma_done
   static constexpr int kOffBar = kOffCut + 32;
-  static constexpr int kBars = 2 * kKStages + 23;
+  static constexpr int kBars = 2 * kKStages + 27;
   static constexpr int kOffMisc = kOffBar + 8 * kBars + 8;
   static constexpr int kSmem = kOffMisc + 64 + 1024;
   static constexpr uint32_t kColO = 2 * kPBlock;  // S0 | S1 | O0 | O1
@@ -149,10 +151,22 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
 __device__ __forceinline__ uint32_t nan_bytes(uint32_t w) { return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u; }
 __device__ __forceinline__ uint32_t bits_below(int n) { return n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1u; }
 
+// As pwait, without a time that the hardware holds the thread for: warps that
+// wait here wait shortly (2 % of a long chunk).
+__device__ __forceinline__ void cwait(uint64_t* bar, uint32_t parity, volatile int* abort, bool& dead) {
+#pragma unroll 1
+  for (uint32_t n = 0; !mbar_try_wait(bar, parity & 1u); ++n)
+    if (dead || *abort || n == kCWaitTries) {
+      *abort = 1;
+      dead = true;
+      break;
+    }
+  __syncwarp();
+}
 // A wait after which the whole warp knows whether it is dead.
 #define TSV_CWAIT(bar, parity)                                    \
   do {                                                            \
-    pwait((bar), (uint32_t)(parity), abort_v, dead);              \
+    cwait((bar), (uint32_t)(parity), abort_v, dead);              \
     dead = __any_sync(0xffffffffu, dead);                         \
   } while (0)
 
@@ -182,10 +196,10 @@ __global__ void __launch_bounds__(kCThreads, 1)
   uint64_t* v_full = raw_empty + 2;
   uint64_t* v_empty = v_full + 2;
   uint64_t* sc_full = v_empty + 2;   // scales of a block
-  uint64_t* s_full = sc_full + 4;    // [tile]
-  uint64_t* p_full = s_full + 2;     // [tile][half]
-  uint64_t* pv_done = p_full + 4;    // [tile]
-  uint64_t* q_full = pv_done + 2;    // [tile]
+  uint64_t* s_full = sc_full + 4;    // [tile][half]
+  uint64_t* p_full = s_full + 4;     // [tile][half]
+  uint64_t* pv_done = p_full + 4;   // [tile][half]
+  uint64_t* q_full = pv_done + 4;    // [tile]
   uint64_t* mma_done = q_full + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
   int* abort_flag = reinterpret_cast<int*>(smem + C::kOffMisc + 4);
@@ -208,13 +222,13 @@ __global__ void __launch_bounds__(kCThreads, 1)
       mbar_init(&raw_empty[s], 4);  // the widening warps
       mbar_init(&v_full[s], 4);
       mbar_init(&v_empty[s], 2);
-      mbar_init(&s_full[s], 1);
-      mbar_init(&pv_done[s], 1);
       mbar_init(&q_full[s], 4);
     }
     for (int s = 0; s < 4; ++s) {
       mbar_init(&sc_full[s], 1);
-      mbar_init(&p_full[s], 128);
+      mbar_init(&s_full[s], 1);
+      mbar_init(&p_full[s], 4);
+      mbar_init(&pv_done[s], 1);
     }
     mbar_init(mma_done, 2);
     *abort_flag = 0;
@@ -490,43 +504,103 @@ __global__ void __launch_bounds__(kCThreads, 1)
       const int pos = u.start + (u.row0 + min(row, u.rows - 1)) / a.G;
       float m_ref = -INFINITY, l = 0.f, v_ref = 0.f;
       int room = kFarApart;  // how far the reference may still be lowered
-      auto step = [&](int j, auto masked_c) {
-        constexpr bool MASKED = decltype(masked_c)::value;
-        const int x = t + j - u.j;
-        TSV_CWAIT(&s_full[tile], cnt);
-        TSV_CWAIT(&sc_full[x & 3], x >> 2);
+      // 64 keys of a block.
+      auto half_step = [&](int j, int h, bool masked, float alpha, const float* sc, auto even_c) {
+        constexpr bool EVEN = decltype(even_c)::value;
+        if (h == 1) TSV_CWAIT(&s_full[2 * tile + 1], cnt);
         if (dead) return;
         tc_fence_after();
-        uint32_t s[4][32];
+        uint32_t s[2][32];
+        tmem_ld32_nowait(s_col + 64 * h, s[0]);
+        tmem_ld32_nowait(s_col + 64 * h + 32, s[1]);
+        // Per 16 keys: the factor of the scores, the logarithm of V's scale in the exponent.
+        float f[4], ex[4];
+        *reinterpret_cast<float4*>(f) = *reinterpret_cast<const float4*>(sc + 4 * h);
+        *reinterpret_cast<float4*>(ex) = *reinterpret_cast<const float4*>(sc + 16 + 4 * h);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld32_nowait(s_col + 32 * c, s[c]);
-        const float* sc = sScale + (x & 3) * 36;
-        // Per 16 keys: the factor of the scores, the logarithm of V's scale for the maximum.
-        float f[8], g[8];
-#pragma unroll
-        for (int q = 0; q < 8; q += 4) {
-          *reinterpret_cast<float4*>(f + q) = *reinterpret_cast<const float4*>(sc + q);
-          *reinterpret_cast<float4*>(g + q) = *reinterpret_cast<const float4*>(sc + 8 + q);
-        }
-#pragma unroll
-        for (int q = 0; q < 8; ++q) f[q] *= fr;
-        const float v_top = sc[32];
-        const bool even = sc[33] != 0.f;  // every scale goes into the exponent
-        uint32_t see[4] = {~0u, ~0u, ~0u, ~0u};
-        if (MASKED) {
-          const int hi = pos - j * kPBlock + 1, lo = a.window > 0 ? hi - a.window : 0;
-#pragma unroll
-          for (int c = 0; c < 4; ++c) see[c] = bits_below(hi - 32 * c) & ~bits_below(lo - 32 * c);
-        }
+        for (int q = 0; q < 4; ++q) f[q] = fmaxf(f[q] * fr, 0x1p-126f);  // (above 0: a masked key's -inf stays one)
         tmem_wait_ld_tie32(s[0]);
         reg_tie32(s[1]);
-        reg_tie32(s[2]);
-        reg_tie32(s[3]);
-        if (MASKED) {
+        if (masked) {
+          const int hi = pos - j * kPBlock + 1 - 64 * h, lo = a.window > 0 ? hi - a.window : 0;
 #pragma unroll
-          for (int e = 0; e < 128; ++e)
-            if (!((see[e >> 5] >> (e & 31)) & 1u)) s[e >> 5][e & 31] = 0xFF800000u;
+          for (int c = 0; c < 2; ++c) {
+            const uint32_t see = bits_below(hi - 32 * c) & ~bits_below(lo - 32 * c);
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (!((see >> e) & 1u)) s[c][e] = 0xFF800000u;
+          }
         }
+        float top = -INFINITY;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const uint32_t* z = &s[q >> 1][(q & 1) * 16];
+          float b0 = fmaxf(__uint_as_float(z[0]), __uint_as_float(z[1]));
+          float b1 = fmaxf(__uint_as_float(z[2]), __uint_as_float(z[3]));
+#pragma unroll
+          for (int e = 4; e < 16; e += 4) {
+            b0 = fmax3(b0, __uint_as_float(z[e]), __uint_as_float(z[e + 1]));
+            b1 = fmax3(b1, __uint_as_float(z[e + 2]), __uint_as_float(z[e + 3]));
+          }
+          top = fmaxf(top, fmaf(fmaxf(b0, b1), f[q], EVEN ? ex[q] : sc[8 + 4 * h + q]));
+        }
+        if (top > m_ref + kRise) {
+          const float c = fast_exp2(m_ref - top);  // 0 when m_ref = -inf
+          m_ref = top;
+          l *= c;
+          alpha *= c;
+        }
+        if (j + h > range.x && __any_sync(0xffffffffu, alpha != 1.f)) {
+          if (h == 0) TSV_CWAIT(&pv_done[2 * tile + 1], cnt - 1);
+          else TSV_CWAIT(&pv_done[2 * tile], cnt);
+          if (dead) return;
+          tc_fence_after();
+#pragma unroll 1
+          for (int cc = 0; cc < D; cc += 16) {
+            float o[16];
+            tmem_ld16(o_col + cc, o);
+            uint32_t z16[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) z16[e] = __float_as_uint(o[e] * alpha);
+            tmem_st16u_nowait(o_col + cc, z16);
+          }
+        }
+        const float base = m_ref == -INFINITY ? kUp : kUp - m_ref;
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          uint32_t p[16];
+#pragma unroll
+          for (int q = 2 * c; q < 2 * c + 2; ++q) {
+            const uint64_t ref2 = f2_pack(base + ex[q], base + ex[q]), f2 = f2_pack(f[q], f[q]);
+            uint64_t sum[2] = {0ull, 0ull};
+#pragma unroll
+            for (int e = 0; e < 16; e += 2) {
+              const int k = (q & 1) * 16 + e;
+              const uint64_t x2 = ffma2((uint64_t)s[c][k] | ((uint64_t)s[c][k + 1] << 32), f2, ref2);
+              uint64_t w2 = f2_pack(fast_exp2(f2_lo(x2)), fast_exp2(f2_hi(x2)));
+              if (e < 4) sum[e >> 1] = w2;
+              else sum[(e >> 1) & 1] = fadd2(sum[(e >> 1) & 1], w2);
+              if (!EVEN) w2 = fmul2(w2, f2_pack(sc[24 + 4 * h + q], sc[24 + 4 * h + q]));
+              p[(q & 1) * 8 + (e >> 1)] = pack_f16(f2_lo(w2), f2_hi(w2));
+            }
+            const uint64_t both = fadd2(sum[0], sum[1]);
+            l = fmaf(f2_lo(both) + f2_hi(both), sc[32 + 4 * h + q], l);
+          }
+          tmem_st16u_nowait(s_col + 64 * h + 16 * c, p);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[2 * tile + h]);
+      };
+      auto step = [&](int j, bool masked) {
+        const int x = t + j - u.j;
+        TSV_CWAIT(&s_full[2 * tile], cnt);  // (first: a tile that sits units out is far ahead of the scales' phases)
+        TSV_CWAIT(&sc_full[x & 3], x >> 2);
+        if (dead) return;
+        const float* sc = sScale + (x & 3) * kScaleRow;
+        const float v_top = sc[40];
+        const bool even = sc[41] != 0.f;  // every scale goes into the exponent
         float alpha = 1.f;
         if (v_top > v_ref) {  // the same in every thread
           // What was summed up stays, under a reference that is lower by as much as
@@ -542,95 +616,24 @@ __global__ void __launch_bounds__(kCThreads, 1)
           }
           v_ref = v_top;
         }
-        float top = -INFINITY;
-#pragma unroll
-        for (int q = 0; q < 8; ++q) {
-          const uint32_t* z = &s[q >> 1][(q & 1) * 16];
-          float b0 = fmaxf(__uint_as_float(z[0]), __uint_as_float(z[1]));
-          float b1 = fmaxf(__uint_as_float(z[2]), __uint_as_float(z[3]));
-#pragma unroll
-          for (int e = 4; e < 16; e += 4) {
-            b0 = fmax3(b0, __uint_as_float(z[e]), __uint_as_float(z[e + 1]));
-            b1 = fmax3(b1, __uint_as_float(z[e + 2]), __uint_as_float(z[e + 3]));
-          }
-          top = fmaxf(top, fmaf(fmaxf(b0, b1), f[q], g[q]));
-        }
-        if (top > m_ref + kRise) {
-          const float c = fast_exp2(m_ref - top);  // 0 when m_ref = -inf
-          m_ref = top;
-          l *= c;
-          alpha *= c;
-        }
-        if (j > range.x && __any_sync(0xffffffffu, alpha != 1.f)) {
-          TSV_CWAIT(&pv_done[tile], cnt - 1);
-          tc_fence_after();
 #pragma unroll 1
-          for (int cc = 0; cc < D; cc += 16) {
-            float o[16];
-            tmem_ld16(o_col + cc, o);
-            uint32_t z16[16];
-#pragma unroll
-            for (int e = 0; e < 16; ++e) z16[e] = __float_as_uint(o[e] * alpha);
-            tmem_st16u_nowait(o_col + cc, z16);
-          }
-        }
-        const float base = m_ref == -INFINITY ? kUp : kUp - m_ref;
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t p[16];
-#pragma unroll
-          for (int q = 2 * c; q < 2 * c + 2; ++q) {
-            const float in_exp = even ? g[q] : sc[16 + q];  // logarithm of V's scale, 0 when it is a factor of its own
-            const uint64_t ref2 = f2_pack(base + in_exp, base + in_exp), f2 = f2_pack(f[q], f[q]);
-            uint64_t sum = 0ull;
-            float w[16];
-#pragma unroll
-            for (int e = 0; e < 16; e += 2) {
-              const int k = (q & 1) * 16 + e;
-              const uint64_t x2 = ffma2((uint64_t)s[c][k] | ((uint64_t)s[c][k + 1] << 32), f2, ref2);
-              w[e] = fast_exp2(f2_lo(x2));
-              w[e + 1] = fast_exp2(f2_hi(x2));
-              if (MASKED) {
-                if (!((see[c] >> k) & 1u)) w[e] = 0.f;
-                if (!((see[c] >> (k + 1)) & 1u)) w[e + 1] = 0.f;
-              }
-              sum = fadd2(sum, f2_pack(w[e], w[e + 1]));
-            }
-            l = fmaf(f2_lo(sum) + f2_hi(sum), fast_exp2(-in_exp), l);
-            if (!even) {
-              const float own = sc[24 + q];
-#pragma unroll
-              for (int e = 0; e < 16; ++e) w[e] *= own;
-            }
-#pragma unroll
-            for (int e = 0; e < 16; e += 2) p[(q & 1) * 8 + (e >> 1)] = pack_f16(w[e], w[e + 1]);
-          }
-          tmem_st16u_nowait(s_col + 16 * c, p);
-          if (c & 1) {  // the keys of half a block
-            tmem_wait_st();
-            tc_fence_before();
-            parrive(&p_full[2 * tile + (c >> 1)], dead);
-          }
+        for (int h = 0; h < 2 && !dead; ++h) {
+          if (even) half_step(j, h, masked, h == 0 ? alpha : 1.f, sc, std::true_type{});
+          else half_step(j, h, masked, h == 0 ? alpha : 1.f, sc, std::false_type{});
         }
         ++cnt;
       };
-      // The blocks that every row sees whole lie together.
-      int j = range.x;
       if (active) {
         const int r0 = tile * kTileRows, r1 = min(u.rows, r0 + kTileRows) - 1;
 #pragma unroll 1
-        for (; j < range.y && !seen_by_all(u, r0, r1, j) && !dead; ++j) step(j, std::true_type{});
-#pragma unroll 1
-        for (; j < range.y && seen_by_all(u, r0, r1, j) && !dead; ++j) step(j, std::false_type{});
-#pragma unroll 1
-        for (; j < range.y && !dead; ++j) step(j, std::true_type{});
+        for (int j = range.x; j < range.y && !dead; ++j) step(j, !seen_by_all(u, r0, r1, j));
       }
       const CUnit now = u;
       going = next_unit(u);
       if (dead) break;
       if (going && takes_part(u)) bring_q(u);  // (the tile's last S is there: Q is free)
       if (active) {
-        if (range.x < range.y) TSV_CWAIT(&pv_done[tile], cnt - 1);
+        if (range.x < range.y) TSV_CWAIT(&pv_done[2 * tile + 1], cnt - 1);
         if (dead) break;
         tc_fence_after();
         const int gr = now.row0 + row, token = gr / a.G;
@@ -796,7 +799,7 @@ __global__ void __launch_bounds__(kCThreads, 1)
     } else if (warp < kCKWarp) {
       // -------------------------------------------------------- issuer of a tile
       const int q = warp - kCMmaWarp;
-      constexpr uint32_t idS = idesc_mn(kTileRows, kPBlock, 0), idPV = idesc_mn(kTileRows, D, 1);
+      constexpr uint32_t idS = idesc_mn(kTileRows, 64, 0), idPV = idesc_mn(kTileRows, D, 1);
       const uint64_t dq = sdesc_row<D>(smem_u32(sQ + q * 2 * C::kQTile), 16);
       const uint64_t dk = sdesc_row<D>(smem_u32(sK), 16);
       const uint64_t dv = sdesc_sw128(smem_u32(sV), kPBlock * 128, 1024);
@@ -817,22 +820,23 @@ __global__ void __launch_bounds__(kCThreads, 1)
           }
           __syncwarp();
         };
-        auto issue_s = [&](int j) {
+        // S of half a block.
+        auto issue_s = [&](int j, int half) {
           const int x = t + j - u.j, st = x % kKStages;
-          TSV_CWAIT(&k_full[st], x / kKStages);
+          if (half == 0) TSV_CWAIT(&k_full[st], x / kKStages);
           if (dead) return;
           tc_fence_after();
-          const uint32_t db = (uint32_t)dk + (uint32_t)((st * C::kKTile) >> 4);
+          const uint32_t db = (uint32_t)dk + (uint32_t)((st * C::kKTile + half * 64 * D) >> 4);
           const bool lead = elect_one();
 #pragma unroll
           for (int term = 0; term < 2; ++term)
 #pragma unroll
             for (int kk = 0; kk < D / 32; ++kk)
-              umma_e4m3(s_at, desc_at(dq, (uint32_t)dq + (uint32_t)((term * C::kQTile) >> 4) + kk * 2), desc_at(dk, db + kk * 2), idS,
-                        term + kk > 0 ? 1u : 0u, lead);
+              umma_e4m3(s_at + half * 64, desc_at(dq, (uint32_t)dq + (uint32_t)((term * C::kQTile) >> 4) + kk * 2),
+                        desc_at(dk, db + kk * 2), idS, term + kk > 0 ? 1u : 0u, lead);
           if (lead) {
-            umma_commit(&s_full[q]);
-            umma_commit(&k_empty[st]);
+            umma_commit(&s_full[2 * q + half]);
+            if (half == 1) umma_commit(&k_empty[st]);
           }
           __syncwarp();
         };
@@ -842,32 +846,33 @@ __global__ void __launch_bounds__(kCThreads, 1)
         }
 #pragma unroll 1
         for (int j = u.j; j < range.x && !dead; ++j) skip(j);
-        if (range.x < range.y && !dead) issue_s(range.x);
+        if (range.x < range.y && !dead) {
+          issue_s(range.x, 0);
+          if (!dead) issue_s(range.x, 1);
+        }
 #pragma unroll 1
         for (int j = range.x; j < range.y && !dead; ++j) {
           const int x = t + j - u.j;
           TSV_CWAIT(&v_full[x & 1], x >> 1);
           const uint32_t db = (uint32_t)dv + (uint32_t)(((x & 1) * C::kVTile) >> 4);
 #pragma unroll 1
-          for (int half = 0; half < 2; ++half) {
+          for (int half = 0; half < 2 && !dead; ++half) {
             TSV_CWAIT(&p_full[2 * q + half], cnt);
             if (dead) break;
             tc_fence_after();
             const bool lead = elect_one();
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)  // 16 keys each; P, two keys a column, lies over its S
-              umma_f16_ts(o_at, s_at + half * 32 + kk * 8, desc_at(dv, db + (uint32_t)((half * 64 * 128 + kk * 16 * 128) >> 4)), idPV,
+              umma_f16_ts(o_at, s_at + half * 64 + kk * 8, desc_at(dv, db + (uint32_t)((half * 64 * 128 + kk * 16 * 128) >> 4)), idPV,
                           j > range.x || half + kk > 0 ? 1u : 0u, lead);
+            if (lead) {
+              umma_commit(&pv_done[2 * q + half]);
+              if (half == 1) umma_commit(&v_empty[x & 1]);
+            }
             __syncwarp();
+            if (j + 1 < range.y) issue_s(j + 1, half);
           }
-          if (dead) break;
-          if (elect_one()) {
-            umma_commit(&pv_done[q]);
-            umma_commit(&v_empty[x & 1]);
-          }
-          __syncwarp();
           ++cnt;
-          if (j + 1 < range.y) issue_s(j + 1);
         }
         if (range.x < range.y) {
 #pragma unroll 1
@@ -938,16 +943,17 @@ __global__ void __launch_bounds__(kCThreads, 1)
             const bool past = lane * 16 >= valid;
             const bool in_exp = past || ((__float_as_uint(rel) & 0x7FFFFFu) == 0u && e >= -kFarApart);
             const bool all = __all_sync(0xffffffffu, lane >= 8 || in_exp);
-            float* sc = sScale + (x & 3) * 36;
+            float* sc = sScale + (x & 3) * kScaleRow;
             if (lane < 8) {
               sc[lane] = sk;
               sc[8 + lane] = past ? 0.f : in_exp ? (float)e : fmaxf(__log2f(rel), -(float)kFarApart);
               sc[16 + lane] = past || !in_exp ? 0.f : (float)e;
               sc[24 + lane] = past || in_exp ? 1.f : rel;
+              sc[32 + lane] = past || !in_exp ? 1.f : __uint_as_float((uint32_t)(127 - e) << 23);
             }
             if (lane == 0) {
-              sc[32] = top;
-              sc[33] = all ? 1.f : 0.f;
+              sc[40] = top;
+              sc[41] = all ? 1.f : 0.f;
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&sc_full[x & 3]);
