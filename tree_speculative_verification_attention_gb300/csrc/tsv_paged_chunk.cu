@@ -39,8 +39,9 @@ namespace {
 
 constexpr int kCThreads = 512;
 constexpr int kCConvWarp = 8, kCMmaWarp = 12, kCKWarp = 14, kCVWarp = 15;
-// Registers a thread: 512 x 128 at launch = 256 x 192 + 256 x 64.
-constexpr int kCSoftRegs = 192, kCRestRegs = 64;
+// Registers a thread: 512 x 128 at launch = 256 x 144 + 256 x 112.  (Nothing may
+// spill: beside so much shared memory the L1 holds next to nothing.)
+constexpr int kCSoftRegs = 144, kCRestRegs = 112;
 static_assert(256 * kCSoftRegs + 256 * kCRestRegs <= kCThreads * 128, "register split");
 constexpr int kTileRows = 128;
 constexpr int kKStages = 3;
@@ -51,7 +52,7 @@ constexpr int kFarApart = 40;   // log2: V scales that far apart leave a row's w
 constexpr int kUnitCost = 3, kLeastCut = 8, kNearEnd = 3;
 constexpr uint32_t kCWaitTries = 1u << 22;  // (of a microsecond or less each)
 constexpr int kBarConv = 1;
-constexpr int kScaleRow = 44;   // of a block, per 16 keys: K's scale, V's logarithm for the maximum and in the exponent, its factor, 2^-; top, even
+constexpr int kScaleRow = 36;   // of a block, per 16 keys: K's scale, e and 2^-e and m of V's relative scale m 2^e; V's largest scale, whether every m is 1
 constexpr int kNanSlots = 6;    // blocks of a unit with masked keys: 3 at each end
 
 // A row's last key, its unit and its part.
@@ -107,24 +108,20 @@ struct alignas(16) ChunkPart {
   int off, row0, rows, g;          // of the group that is begun
 };
 
-__device__ __forceinline__ void umma_e4m3(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accumulate,
-                                          uint32_t lead) {
+__device__ __forceinline__ void umma_e4m3(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
+      "{\n\t.reg .pred p;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "setp.ne.b32 q, %5, 0;\n\t"
-      "@q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d_tmem),
-      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(lead)
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
-__device__ __forceinline__ void umma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc, uint32_t accumulate,
-                                            uint32_t lead) {
+__device__ __forceinline__ void umma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
+      "{\n\t.reg .pred p;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "setp.ne.b32 q, %5, 0;\n\t"
-      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(lead)
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
 // e4m3 (kind::f8f6f4) or fp16 (kind::f16) A and B, fp32 D; A K-major, B K-major (0) or N-major (1).
@@ -397,10 +394,10 @@ __global__ void __launch_bounds__(kCThreads, 1)
     }
     return t;
   };
-  // Whether all rows r0 .. r1 of the unit see all keys of block j.
-  auto seen_by_all = [&](const CUnit& u, int r0, int r1, int j) {
+  // The blocks whose keys rows r0 .. r1 of the unit see all: from .x up to .y.
+  auto full_range = [&](const CUnit& u, int r0, int r1) {
     const int p0 = u.start + (u.row0 + r0) / a.G, p1 = u.start + (u.row0 + r1) / a.G;
-    return j * kPBlock + kPBlock - 1 <= p0 && (a.window == 0 || j * kPBlock > p1 - a.window);
+    return make_int2(a.window > 0 ? (max(p1 - a.window, -1) + kPBlock) / kPBlock : 0, (p0 + 1) / kPBlock);
   };
   CUnit u{};
 
@@ -504,19 +501,16 @@ __global__ void __launch_bounds__(kCThreads, 1)
       const int pos = u.start + (u.row0 + min(row, u.rows - 1)) / a.G;
       float m_ref = -INFINITY, l = 0.f, v_ref = 0.f;
       int room = kFarApart;  // how far the reference may still be lowered
-      // 64 keys of a block.
-      auto half_step = [&](int j, int h, bool masked, float alpha, const float* sc, auto even_c) {
-        constexpr bool EVEN = decltype(even_c)::value;
-        if (h == 1) TSV_CWAIT(&s_full[2 * tile + 1], cnt);
-        if (dead) return;
-        tc_fence_after();
+      // P of 64 keys out of their scores.
+      auto half_step = [&](int j, int h, bool masked, float alpha, const float* sc) {
         uint32_t s[2][32];
+        tc_fence_after();
         tmem_ld32_nowait(s_col + 64 * h, s[0]);
         tmem_ld32_nowait(s_col + 64 * h + 32, s[1]);
-        // Per 16 keys: the factor of the scores, the logarithm of V's scale in the exponent.
+        // Per 16 keys: the factor of the scores, V's exponent.
         float f[4], ex[4];
         *reinterpret_cast<float4*>(f) = *reinterpret_cast<const float4*>(sc + 4 * h);
-        *reinterpret_cast<float4*>(ex) = *reinterpret_cast<const float4*>(sc + 16 + 4 * h);
+        *reinterpret_cast<float4*>(ex) = *reinterpret_cast<const float4*>(sc + 8 + 4 * h);
 #pragma unroll
         for (int q = 0; q < 4; ++q) f[q] = fmaxf(f[q] * fr, 0x1p-126f);  // (above 0: a masked key's -inf stays one)
         tmem_wait_ld_tie32(s[0]);
@@ -542,7 +536,7 @@ __global__ void __launch_bounds__(kCThreads, 1)
             b0 = fmax3(b0, __uint_as_float(z[e]), __uint_as_float(z[e + 1]));
             b1 = fmax3(b1, __uint_as_float(z[e + 2]), __uint_as_float(z[e + 3]));
           }
-          top = fmaxf(top, fmaf(fmaxf(b0, b1), f[q], EVEN ? ex[q] : sc[8 + 4 * h + q]));
+          top = fmaxf(top, fmaf(fmaxf(b0, b1), f[q], ex[q]));
         }
         if (top > m_ref + kRise) {
           const float c = fast_exp2(m_ref - top);  // 0 when m_ref = -inf
@@ -553,7 +547,6 @@ __global__ void __launch_bounds__(kCThreads, 1)
         if (j + h > range.x && __any_sync(0xffffffffu, alpha != 1.f)) {
           if (h == 0) TSV_CWAIT(&pv_done[2 * tile + 1], cnt - 1);
           else TSV_CWAIT(&pv_done[2 * tile], cnt);
-          if (dead) return;
           tc_fence_after();
 #pragma unroll 1
           for (int cc = 0; cc < D; cc += 16) {
@@ -566,6 +559,8 @@ __global__ void __launch_bounds__(kCThreads, 1)
           }
         }
         const float base = m_ref == -INFINITY ? kUp : kUp - m_ref;
+        const float4 back = *reinterpret_cast<const float4*>(sc + 16 + 4 * h);  // 2^-exponent
+        const float un[4] = {back.x, back.y, back.z, back.w};
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           uint32_t p[16];
@@ -577,56 +572,55 @@ __global__ void __launch_bounds__(kCThreads, 1)
             for (int e = 0; e < 16; e += 2) {
               const int k = (q & 1) * 16 + e;
               const uint64_t x2 = ffma2((uint64_t)s[c][k] | ((uint64_t)s[c][k + 1] << 32), f2, ref2);
-              uint64_t w2 = f2_pack(fast_exp2(f2_lo(x2)), fast_exp2(f2_hi(x2)));
+              const uint64_t w2 = f2_pack(fast_exp2(f2_lo(x2)), fast_exp2(f2_hi(x2)));
               if (e < 4) sum[e >> 1] = w2;
               else sum[(e >> 1) & 1] = fadd2(sum[(e >> 1) & 1], w2);
-              if (!EVEN) w2 = fmul2(w2, f2_pack(sc[24 + 4 * h + q], sc[24 + 4 * h + q]));
               p[(q & 1) * 8 + (e >> 1)] = pack_f16(f2_lo(w2), f2_hi(w2));
             }
             const uint64_t both = fadd2(sum[0], sum[1]);
-            l = fmaf(f2_lo(both) + f2_hi(both), sc[32 + 4 * h + q], l);
+            l = fmaf(f2_lo(both) + f2_hi(both), un[q], l);
           }
           tmem_st16u_nowait(s_col + 64 * h + 16 * c, p);
         }
         tmem_wait_st();
         tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[2 * tile + h]);
+        dead = __any_sync(0xffffffffu, dead);
+        if (lane == 0 && !dead) mbar_arrive(&p_full[2 * tile + h]);
       };
-      auto step = [&](int j, bool masked) {
-        const int x = t + j - u.j;
-        TSV_CWAIT(&s_full[2 * tile], cnt);  // (first: a tile that sits units out is far ahead of the scales' phases)
-        TSV_CWAIT(&sc_full[x & 3], x >> 2);
-        if (dead) return;
-        const float* sc = sScale + (x & 3) * kScaleRow;
-        const float v_top = sc[40];
-        const bool even = sc[41] != 0.f;  // every scale goes into the exponent
-        float alpha = 1.f;
-        if (v_top > v_ref) {  // the same in every thread
-          // What was summed up stays, under a reference that is lower by as much as
-          // the relative scales of its keys now are (powers of two: l goes with it).
-          if (v_ref > 0.f) {
-            const float c = v_ref / v_top;
-            const int down = min(127 - (int)(__float_as_uint(c) >> 23), room);
-            const float up = __uint_as_float((uint32_t)(127 + down) << 23);
-            room -= down;
-            m_ref -= (float)down;
-            l *= up;
-            alpha = c * up;  // 1 for scales that are powers of two
-          }
-          v_ref = v_top;
-        }
-#pragma unroll 1
-        for (int h = 0; h < 2 && !dead; ++h) {
-          if (even) half_step(j, h, masked, h == 0 ? alpha : 1.f, sc, std::true_type{});
-          else half_step(j, h, masked, h == 0 ? alpha : 1.f, sc, std::false_type{});
-        }
-        ++cnt;
-      };
-      if (active) {
+      if (range.x < range.y) {
         const int r0 = tile * kTileRows, r1 = min(u.rows, r0 + kTileRows) - 1;
+        const int2 full = full_range(u, r0, r1);
 #pragma unroll 1
-        for (int j = range.x; j < range.y && !dead; ++j) step(j, !seen_by_all(u, r0, r1, j));
+        for (int j = range.x; j < range.y && !dead; ++j) {
+          const int x = t + j - u.j;
+          const bool masked = j < full.x || j >= full.y;
+          cwait(&s_full[2 * tile], (uint32_t)cnt, abort_v, dead);
+          // (Behind s_full: a tile that sits units out is far ahead of the scales' phases.)
+          cwait(&sc_full[x & 3], (uint32_t)(x >> 2), abort_v, dead);
+          const float* sc = sScale + (x & 3) * kScaleRow;
+          const float v_top = sc[32];
+          float alpha = 1.f;
+          if (v_top > v_ref) {  // the same in every thread
+            // What was summed up stays, under a reference that is lower by as much as
+            // the relative scales of its keys now are (powers of two: l goes with it).
+            if (v_ref > 0.f) {
+              const float c = v_ref / v_top;
+              const int down = min(127 - (int)(__float_as_uint(c) >> 23), room);
+              const float up = __uint_as_float((uint32_t)(127 + down) << 23);
+              room -= down;
+              m_ref -= (float)down;
+              l *= up;
+              alpha = c * up;  // 1 for scales that are powers of two
+            }
+            v_ref = v_top;
+          }
+#pragma unroll 1
+          for (int h = 0; h < 2; ++h) {
+            if (h == 1) cwait(&s_full[2 * tile + 1], (uint32_t)cnt, abort_v, dead);
+            half_step(j, h, masked, h == 0 ? alpha : 1.f, sc);
+          }
+          ++cnt;
+        }
       }
       const CUnit now = u;
       going = next_unit(u);
@@ -741,14 +735,18 @@ __global__ void __launch_bounds__(kCThreads, 1)
         if (ct < kNanSlots * 4) sNan[par * (kNanSlots * 4) + ct] = 0u;
         dead = named_bar_or(kBarConv, 128, dead);
         if (dead) break;
+        const int2 full = full_range(u, 0, u.rows - 1);
         const int keys = u.start + min(u.n, (u.row0 + u.rows - 1) / a.G + 1);  // behind the last one that a row sees
 #pragma unroll 1
         for (int j = u.j; j < u.j1; ++j) {
           const int x = t + j - u.j, st = x & 1, valid = keys - j * kPBlock;
           TSV_CWAIT(&raw_full[st], x >> 1);
+          TSV_CWAIT(&sc_full[x & 3], x >> 2);
           if (x >= 2) TSV_CWAIT(&v_empty[st], (x >> 1) - 1);
           if (dead) break;
-          const bool masked = !seen_by_all(u, 0, u.rows - 1, j);
+          const float* sc = sScale + (x & 3) * kScaleRow;
+          const bool plain = sc[33] != 0.f;
+          const bool masked = j < full.x || j >= full.y;
           const int slot = j - u.first < 3 ? j - u.first : u.end - 1 - j < 3 ? 3 + u.end - 1 - j : 0;
 #pragma unroll
           for (int h = 0; h < kParts; h += 4) {
@@ -780,10 +778,16 @@ __global__ void __launch_bounds__(kCThreads, 1)
               const uint4 c = codes[q];
               uint8_t* to_row = sV + st * C::kVTile + (chunk >> 2) * (kPBlock * 128) + key * 128;
               const int at = (((2 * chunk) & 7) ^ (key & 7)) << 4;  // chunk 2 c of 8 values, and its neighbour
-              *reinterpret_cast<uint4*>(to_row + at) = make_uint4(f16x2_of_e4m3x2(c.x & 0xFFFFu), f16x2_of_e4m3x2(c.x >> 16),
-                                                                  f16x2_of_e4m3x2(c.y & 0xFFFFu), f16x2_of_e4m3x2(c.y >> 16));
-              *reinterpret_cast<uint4*>(to_row + (at ^ 16)) = make_uint4(f16x2_of_e4m3x2(c.z & 0xFFFFu), f16x2_of_e4m3x2(c.z >> 16),
-                                                                         f16x2_of_e4m3x2(c.w & 0xFFFFu), f16x2_of_e4m3x2(c.w >> 16));
+              uint32_t v[8] = {f16x2_of_e4m3x2(c.x & 0xFFFFu), f16x2_of_e4m3x2(c.x >> 16), f16x2_of_e4m3x2(c.y & 0xFFFFu),
+                               f16x2_of_e4m3x2(c.y >> 16),     f16x2_of_e4m3x2(c.z & 0xFFFFu), f16x2_of_e4m3x2(c.z >> 16),
+                               f16x2_of_e4m3x2(c.w & 0xFFFFu), f16x2_of_e4m3x2(c.w >> 16)};
+              if (!plain) {
+                const float m = sc[24 + (key >> 4)];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[e] = pack_f16(f16_lo(v[e]) * m, f16_hi(v[e]) * m);
+              }
+              *reinterpret_cast<uint4*>(to_row + at) = make_uint4(v[0], v[1], v[2], v[3]);
+              *reinterpret_cast<uint4*>(to_row + (at ^ 16)) = make_uint4(v[4], v[5], v[6], v[7]);
             }
           }
           fence_proxy_async_smem();
@@ -804,6 +808,9 @@ __global__ void __launch_bounds__(kCThreads, 1)
       const uint64_t dk = sdesc_row<D>(smem_u32(sK), 16);
       const uint64_t dv = sdesc_sw128(smem_u32(sV), kPBlock * 128, 1024);
       const uint32_t s_at = tmem + (uint32_t)(q * kPBlock), o_at = tmem + C::kColO + (uint32_t)(q * D);
+      // The whole warp waits, one thread issues: behind elect.sync the compiler knows
+      // that it is one, and the operands stay in uniform registers (behind a test of
+      // the lane a long chunk took 1.13 times as long).
       int t = 0, cnt = 0, mine_units = 0;
       for (bool going = first_unit(u); going && !dead; going = next_unit(u)) {
         const int2 range = tile_range(u, q);
@@ -813,8 +820,7 @@ __global__ void __launch_bounds__(kCThreads, 1)
           const int x = t + j - u.j;
           TSV_CWAIT(&k_full[x % kKStages], x / kKStages);
           TSV_CWAIT(&v_full[x & 1], x >> 1);
-          if (dead) return;
-          if (elect_one()) {
+          if (!dead && elect_one()) {
             mbar_arrive(&k_empty[x % kKStages]);
             mbar_arrive(&v_empty[x & 1]);
           }
@@ -827,14 +833,13 @@ __global__ void __launch_bounds__(kCThreads, 1)
           if (dead) return;
           tc_fence_after();
           const uint32_t db = (uint32_t)dk + (uint32_t)((st * C::kKTile + half * 64 * D) >> 4);
-          const bool lead = elect_one();
+          if (elect_one()) {
 #pragma unroll
-          for (int term = 0; term < 2; ++term)
+            for (int term = 0; term < 2; ++term)
 #pragma unroll
-            for (int kk = 0; kk < D / 32; ++kk)
-              umma_e4m3(s_at + half * 64, desc_at(dq, (uint32_t)dq + (uint32_t)((term * C::kQTile) >> 4) + kk * 2),
-                        desc_at(dk, db + kk * 2), idS, term + kk > 0 ? 1u : 0u, lead);
-          if (lead) {
+              for (int kk = 0; kk < D / 32; ++kk)
+                umma_e4m3(s_at + half * 64, desc_at(dq, (uint32_t)dq + (uint32_t)((term * C::kQTile) >> 4) + kk * 2),
+                          desc_at(dk, db + kk * 2), idS, term + kk > 0 ? 1u : 0u);
             umma_commit(&s_full[2 * q + half]);
             if (half == 1) umma_commit(&k_empty[st]);
           }
@@ -848,24 +853,23 @@ __global__ void __launch_bounds__(kCThreads, 1)
         for (int j = u.j; j < range.x && !dead; ++j) skip(j);
         if (range.x < range.y && !dead) {
           issue_s(range.x, 0);
-          if (!dead) issue_s(range.x, 1);
+          issue_s(range.x, 1);
         }
 #pragma unroll 1
         for (int j = range.x; j < range.y && !dead; ++j) {
           const int x = t + j - u.j;
           TSV_CWAIT(&v_full[x & 1], x >> 1);
-          const uint32_t db = (uint32_t)dv + (uint32_t)(((x & 1) * C::kVTile) >> 4);
-#pragma unroll 1
-          for (int half = 0; half < 2 && !dead; ++half) {
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
             TSV_CWAIT(&p_full[2 * q + half], cnt);
             if (dead) break;
             tc_fence_after();
-            const bool lead = elect_one();
+            const uint32_t db = (uint32_t)dv + (uint32_t)(((x & 1) * C::kVTile + half * 64 * 128) >> 4);
+            if (elect_one()) {
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk)  // 16 keys each; P, two keys a column, lies over its S
-              umma_f16_ts(o_at, s_at + half * 64 + kk * 8, desc_at(dv, db + (uint32_t)((half * 64 * 128 + kk * 16 * 128) >> 4)), idPV,
-                          j > range.x || half + kk > 0 ? 1u : 0u, lead);
-            if (lead) {
+              for (int kk = 0; kk < 4; ++kk)  // 16 keys each; P, two keys a column, lies over its S
+                umma_f16_ts(o_at, s_at + half * 64 + kk * 8, desc_at(dv, db + (uint32_t)((kk * 16 * 128) >> 4)), idPV,
+                            half + kk > 0 || j > range.x ? 1u : 0u);
               umma_commit(&pv_done[2 * q + half]);
               if (half == 1) umma_commit(&v_empty[x & 1]);
             }
@@ -880,7 +884,6 @@ __global__ void __launch_bounds__(kCThreads, 1)
         }
         t += u.j1 - u.j;
       }
-      __syncwarp();
       if (elect_one()) umma_commit(mma_done);  // every MMA has finished before TMEM is freed
       __syncwarp();
       mbar_wait(mma_done, 0, nullptr);
@@ -895,28 +898,31 @@ __global__ void __launch_bounds__(kCThreads, 1)
         const int32_t* ids = a.table.ids_d + (int64_t)u.b * a.table.stride;
         const int keys = u.start + min(u.n, (u.row0 + u.rows - 1) / a.G + 1);
         const int page_end = (keys + (1 << lps) - 1) >> lps;
-        // Lane p holds page p of the next block.
+        // Lane p holds page p of the next block (of V's producer: of the next two), lanes
+        // 0 .. 7 the next block's scales of 16 keys each: asked for a block ahead.
         auto page_of = [&](int j) {
           const int p = ((j * kPBlock) >> lps) + lane;
           return j < u.j1 && (lane << lps) < kPBlock && p < page_end ? __ldg(ids + p) : -1;
         };
-        // Lanes 0 .. 7 (V's producer): the scales of 16 keys each.
-        float top = 0.f;
-        int next = page_of(u.j);
+        float top = 0.f, sk = 0.f, sv = 0.f;
+        auto scales_of = [&](int pages, int j) {
+          const int sid = __shfl_sync(0xffffffffu, pages, ((lane * 16) >> lps) & 31);
+          const bool on = j < u.j1 && lane < 8 && lane * 16 < keys - j * kPBlock && (uint32_t)sid < (uint32_t)c.num_pages;
+          sk = on ? __ldg(c.k_scale_d + (int64_t)sid * c.Hkv + u.g) : 0.f;
+          sv = on ? __ldg(c.v_scale_d + (int64_t)sid * c.Hkv + u.g) : 0.f;
+        };
+        int now = page_of(u.j), next = page_of(u.j + 1);
+        if (is_v) scales_of(now, u.j);
 #pragma unroll 1
         for (int j = u.j; j < u.j1; ++j) {
-          const int x = t + j - u.j, now = next;
-          next = page_of(j + 1);
+          const int x = t + j - u.j;
           const int valid = min(kPBlock, keys - j * kPBlock);
           const uint32_t pages = (uint32_t)(valid + (1 << lps) - 1) >> lps;
-          float sk = 0.f, sv = 0.f;
-          if (is_v) {
-            const int sid = __shfl_sync(0xffffffffu, now, (lane * 16) >> lps & 31);
-            if (lane < 8 && lane * 16 < valid && (uint32_t)sid < (uint32_t)c.num_pages) {
-              sk = __ldg(c.k_scale_d + (int64_t)sid * c.Hkv + u.g);
-              sv = __ldg(c.v_scale_d + (int64_t)sid * c.Hkv + u.g);
-            }
-          }
+          const float sk_now = sk, sv_now = sv;
+          const int pages_now = now;
+          now = next;
+          next = page_of(j + 2);
+          if (is_v) scales_of(now, j + 1);
           const int st = is_v ? x & 1 : x % kKStages;
           uint64_t* full = is_v ? &raw_full[st] : &k_full[st];
           if (is_v && x >= 2) TSV_CWAIT(&raw_empty[st], (x >> 1) - 1);
@@ -928,32 +934,31 @@ __global__ void __launch_bounds__(kCThreads, 1)
           __syncwarp();
 #pragma unroll 1
           for (uint32_t p = 0; p < pages; ++p)
-            tma_load_page(at + (p << lps) * D, tmap, smem_u32(full), (uint32_t)u.g, (uint32_t)__shfl_sync(0xffffffffu, now, (int)p), pol,
+            tma_load_page(at + (p << lps) * D, tmap, smem_u32(full), (uint32_t)u.g, (uint32_t)__shfl_sync(0xffffffffu, pages_now, (int)p), pol,
                           lead);
           __syncwarp();
           if (lead) mbar_arrive(full);
           asked = x + 1;
           if (is_v) {
-            // The unit's largest V scale so far, and the block's relative to it.
-            top = fmaxf(top, __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(sv))));  // (scales are >= 0)
+            // The unit's largest V scale so far, and the block's relative to it as m 2^e:
+            // 2^e goes into the exponent of P and m, 1 as a rule, into V as it is widened.
+            top = fmaxf(top, __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(sv_now))));  // (scales are >= 0)
             const float turn = top > 1.f ? 0x1p-64f : 0x1p64f;  // (the division wants an ordinary divisor)
-            const float rel = top > 0.f ? __fdiv_rn(sv * turn, top * turn) : 1.f;
-            const int e = (int)(__float_as_uint(rel) >> 23) - 127;
-            // A power of two not too far below goes into the exponent; keys past the end take part in nothing.
-            const bool past = lane * 16 >= valid;
-            const bool in_exp = past || ((__float_as_uint(rel) & 0x7FFFFFu) == 0u && e >= -kFarApart);
-            const bool all = __all_sync(0xffffffffu, lane >= 8 || in_exp);
+            const bool past = lane * 16 >= valid;               // (such keys take part in nothing)
+            const float rel = top > 0.f && !past ? __fdiv_rn(sv_now * turn, top * turn) : 1.f;
+            const int e = max((int)(__float_as_uint(rel) >> 23) - 127, -kFarApart);
+            const float m = rel * __uint_as_float((uint32_t)(127 - e) << 23);
+            const bool all = __all_sync(0xffffffffu, lane >= 8 || m == 1.f);
             float* sc = sScale + (x & 3) * kScaleRow;
             if (lane < 8) {
-              sc[lane] = sk;
-              sc[8 + lane] = past ? 0.f : in_exp ? (float)e : fmaxf(__log2f(rel), -(float)kFarApart);
-              sc[16 + lane] = past || !in_exp ? 0.f : (float)e;
-              sc[24 + lane] = past || in_exp ? 1.f : rel;
-              sc[32 + lane] = past || !in_exp ? 1.f : __uint_as_float((uint32_t)(127 - e) << 23);
+              sc[lane] = sk_now;
+              sc[8 + lane] = (float)e;
+              sc[16 + lane] = __uint_as_float((uint32_t)(127 - e) << 23);
+              sc[24 + lane] = m;
             }
             if (lane == 0) {
-              sc[40] = top;
-              sc[41] = all ? 1.f : 0.f;
+              sc[32] = top;
+              sc[33] = all ? 1.f : 0.f;
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&sc_full[x & 3]);
