@@ -306,6 +306,7 @@ tsv_status tsv_create(tsv_handle* out, int device) {
   h->mss_staged_limit = 0;
   h->verify_overlap = 0u;
   h->paged_attr_mask = h->append_attr_mask = h->chunk_attr_mask = 0u;
+  h->pages_cluster = 0;
   *out = h;
   return TSV_OK;
 }

@@ -30,6 +30,7 @@ struct tsv_handle_s {
   uint32_t verify_overlap;  // tsv_set_verify_overlap: TSV_OVERLAP_* flags
   uint32_t paged_attr_mask;   // paged attention kernels whose attributes are set, one bit per (D, tile rows)
   uint32_t chunk_attr_mask;   // chunk attention kernels, one bit per D
+  int pages_cluster;          // most CTAs of a page-list call's cluster, 0: not asked yet
   uint32_t append_attr_mask;  // paged append kernels, one bit per (type, D)
 };
 
@@ -406,9 +407,11 @@ struct PagesCopyArgs {
   const int32_t* count;  // NULL: n
   int32_t* status;
 };
-cudaError_t launch_pages_resize(const PagesResizeArgs& a, cudaStream_t st);
-cudaError_t launch_pages_fork(const PagesForkArgs& a, cudaStream_t st);
-cudaError_t launch_pages_compact(const PagesCompactArgs& a, cudaStream_t st);
+// Most CTAs of a call's cluster on the current device (once per handle).
+int pages_cluster_limit();
+cudaError_t launch_pages_resize(const PagesResizeArgs& a, int most, cudaStream_t st);
+cudaError_t launch_pages_fork(const PagesForkArgs& a, int most, cudaStream_t st);
+cudaError_t launch_pages_compact(const PagesCompactArgs& a, int most, cudaStream_t st);
 cudaError_t launch_pages_copy(const PagesCopyArgs& a, int num_sms, cudaStream_t st);
 
 // Host-side checks that the paged entries share (tsv_paged_api.cu).

@@ -21,7 +21,7 @@ namespace tsv {
 namespace {
 
 constexpr int kPoolThreads = 1024, kPoolWarps = 32;
-constexpr int kPoolCtas = 8;  // of a cluster, at most
+constexpr int kPoolCtas = 16;  // of a cluster, at most (8 where the device holds no 16)
 
 __device__ __forceinline__ int ld_dsmem_i32(uint32_t addr) {
   int v;
@@ -47,14 +47,30 @@ __device__ __forceinline__ int4 load_counts(const int32_t* refs, int at, int pag
   return v;
 }
 
-// The range of pages of a warp: `steps` x 128 from `first` on.
+// Eight counts in a row, from page `at` on (a multiple of 8).
+struct EightCounts {
+  int c[8];
+  __device__ __forceinline__ EightCounts(const int32_t* refs, int at, int pages, int none) {
+    const int4 a = load_counts(refs, at, pages, none), b = load_counts(refs, at + 4, pages, none);
+    c[0] = a.x;
+    c[1] = a.y;
+    c[2] = a.z;
+    c[3] = a.w;
+    c[4] = b.x;
+    c[5] = b.y;
+    c[6] = b.z;
+    c[7] = b.w;
+  }
+};
+
+// The range of pages of a warp: whole chunks of 256.
 struct PoolShare {
   int first, end;
   __device__ __forceinline__ PoolShare(int pages, int warp) {
-    const int warps = gridDim.x * kPoolWarps, chunks = (pages + 127) >> 7;
+    const int warps = gridDim.x * kPoolWarps, chunks = (pages + 255) >> 8;
     const int w = blockIdx.x * kPoolWarps + warp;
-    first = (int)((int64_t)chunks * w / warps) << 7;
-    end = min(pages, (int)((int64_t)chunks * (w + 1) / warps) << 7);
+    first = (int)((int64_t)chunks * w / warps) << 8;
+    end = min(pages, (int)((int64_t)chunks * (w + 1) / warps) << 8);
   }
 };
 
@@ -128,12 +144,15 @@ __device__ __forceinline__ bool is_served(const PoolRequests& r, int b, int free
 template <typename Give>
 __device__ __forceinline__ void hand_out(PoolRequests& r, const tsv_page_pool& pool, const PoolShare& share, int rank, int granted, int B,
                                          int lane, Give give) {
+  EightCounts now(pool.refs_d, share.first + 8 * lane, share.end, 1);
 #pragma unroll 1
-  for (int at = share.first; at < share.end && rank < granted; at += 128) {
-    const int page = at + 4 * lane;
-    const int4 v = load_counts(pool.refs_d, page, share.end, 1);
-    const int f[4] = {v.x == 0, v.y == 0, v.z == 0, v.w == 0};
-    const int n = f[0] + f[1] + f[2] + f[3];
+  for (int at = share.first; at < share.end && rank < granted; at += 256) {
+    const int page = at + 8 * lane;
+    const EightCounts next(pool.refs_d, page + 256, share.end, 1);  // on its way meanwhile
+    uint32_t f = 0u;  // free pages of the lane
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f |= (now.c[e] == 0 ? 1u : 0u) << e;
+    const int n = __popc(f);
     int upto = n;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -141,22 +160,22 @@ __device__ __forceinline__ void hand_out(PoolRequests& r, const tsv_page_pool& p
       if (lane >= o) upto += y;
     }
     int k = rank + upto - n;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      if (!f[e]) continue;
-      if (k < granted) {
-        int lo = 0, hi = B - 1;  // the first request with upto > k
-        while (lo < hi) {
-          const int mid = (lo + hi) >> 1;
-          if (r.upto[mid] > k) hi = mid;
-          else lo = mid + 1;
-        }
-        pool.refs_d[page + e] = 1;
-        give(lo, k - (r.upto[lo] - r.need[lo]), page + e);
+    if (n > 0 && k < granted) {
+      int lo = 0, hi = B - 1;  // the first request with upto > k
+      while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (r.upto[mid] > k) hi = mid;
+        else lo = mid + 1;
       }
-      ++k;
+      for (; f && k < granted; f &= f - 1, ++k) {
+        while (r.upto[lo] <= k) ++lo;
+        const int id = page + __ffs(f) - 1;
+        pool.refs_d[id] = 1;
+        give(lo, k - (r.upto[lo] - r.need[lo]), id);
+      }
     }
     rank += __shfl_sync(0xffffffffu, upto, 31);
+    now = next;
   }
 }
 
@@ -168,6 +187,24 @@ __device__ __forceinline__ bool drop_page(int32_t* refs, int32_t id) {
 }
 __device__ __forceinline__ bool is_held(const tsv_page_pool& p, int32_t id) {
   return (uint32_t)id < (uint32_t)p.num_pages && __ldcg(p.refs_d + id) > 0;
+}
+
+// Entries from `first` up to `end` of a list by `threads` threads, eight of a
+// thread in flight: each(id), and whether any was false.
+template <typename F>
+__device__ __forceinline__ bool every_entry(const int32_t* ids, int first, int end, int t, int threads, F each) {
+  constexpr int U = 8;
+  bool fine = true;
+#pragma unroll 1
+  for (int i = first + t; i < end; i += U * threads) {
+    int32_t id[U];
+#pragma unroll
+    for (int q = 0; q < U; ++q) id[q] = i + q * threads < end ? __ldcg(ids + i + q * threads) : -1;
+#pragma unroll
+    for (int q = 0; q < U; ++q)
+      if (i + q * threads < end) fine &= each(id[q], i + q * threads);
+  }
+  return fine;
 }
 
 // The cluster's requests are shared out: request b belongs to CTA b % CTAs, and
@@ -204,7 +241,7 @@ __global__ void __launch_bounds__(kPoolThreads, 1) pages_resize_kernel(const Pag
       if (r.bad[b] || r.want[b] >= r.held[b]) return;
       const int32_t* ids = a.table.ids_d + (int64_t)b * a.table.stride;
       bool bad = false;
-      for (int i = r.want[b] + t; i < r.held[b]; i += threads) bad |= !is_held(a.pool, __ldcg(ids + i));
+      bad |= !every_entry(ids, r.want[b], r.held[b], t, threads, [&](int32_t id, int) { return is_held(a.pool, id); });
       if (t == 0 && __ldg(a.rows + b) % a.page_size > 0) {  // new rows would go to the last page
         const int32_t id = __ldcg(ids + r.want[b] - 1);
         bad |= !is_held(a.pool, id) || __ldcg(a.pool.refs_d + id) > 1;
@@ -215,9 +252,7 @@ __global__ void __launch_bounds__(kPoolThreads, 1) pages_resize_kernel(const Pag
     for_own(a.B, warp, lane, [&](int b, int t, int threads) {
       if (r.bad[b] & 3 || r.want[b] >= r.held[b]) return;
       const int32_t* ids = a.table.ids_d + (int64_t)b * a.table.stride;
-      bool bad = false;
-      for (int i = r.want[b] + t; i < r.held[b]; i += threads) bad |= !drop_page(a.pool.refs_d, __ldcg(ids + i));
-      if (bad) atomicOr(&r.bad[b], 4);  // (listed more often than counted)
+      if (!every_entry(ids, r.want[b], r.held[b], t, threads, [&](int32_t id, int) { return drop_page(a.pool.refs_d, id); })) atomicOr(&r.bad[b], 4);  // (listed more often than counted)
     });
     cluster_sync_global();
   } else {
@@ -270,10 +305,9 @@ __global__ void __launch_bounds__(kPoolThreads, 1) pages_fork_kernel(const Pages
     if (source[b] < 0) return;
     const int32_t* old = a.to.ids_d + (int64_t)b * a.to.stride;
     const int32_t* ids = a.from.ids_d + (int64_t)source[b] * a.from.stride;
-    bool bad = false;
-    for (int i = t; i < r.held[b]; i += threads) bad |= !is_held(a.pool, __ldcg(old + i));
-    for (int i = t; i < r.want[b]; i += threads) bad |= !is_held(a.pool, __ldg(ids + i));
-    if (bad) atomicOr(&r.bad[b], 2);
+    const auto held = [&](int32_t id, int) { return is_held(a.pool, id); };
+    const bool fine = every_entry(old, 0, r.held[b], t, threads, held) & every_entry(ids, 0, r.want[b], t, threads, held);
+    if (!fine) atomicOr(&r.bad[b], 2);
   });
   cluster_sync_all();  // every look at the counts comes before the first change
   // What the owners found: the needs are the same in every CTA.
@@ -289,9 +323,7 @@ __global__ void __launch_bounds__(kPoolThreads, 1) pages_fork_kernel(const Pages
   for_own(a.B, warp, lane, [&](int b, int t, int threads) {
     if (source[b] < 0) return;
     const int32_t* old = a.to.ids_d + (int64_t)b * a.to.stride;
-    bool bad = false;
-    for (int i = t; i < r.held[b]; i += threads) bad |= !drop_page(a.pool.refs_d, __ldcg(old + i));
-    if (bad) atomicOr(&r.bad[b], 4);  // (listed more often than counted)
+    if (!every_entry(old, 0, r.held[b], t, threads, [&](int32_t id, int) { return drop_page(a.pool.refs_d, id); })) atomicOr(&r.bad[b], 4);  // (listed more often than counted)
   });
   cluster_sync_global();
   int free = 0;
@@ -315,11 +347,11 @@ __global__ void __launch_bounds__(kPoolThreads, 1) pages_fork_kernel(const Pages
     if (source[b] < 0 || !is_served(r, b, free)) return;
     int32_t* list = const_cast<int32_t*>(a.to.ids_d) + (int64_t)b * a.to.stride;
     const int32_t* ids = a.from.ids_d + (int64_t)source[b] * a.from.stride;
-    for (int i = t; i < full[b]; i += threads) {
-      const int32_t id = __ldg(ids + i);
+    every_entry(ids, 0, full[b], t, threads, [&](int32_t id, int i) {
       list[i] = id;
       atomicAdd(a.pool.refs_d + id, 1);
-    }
+      return true;
+    });
   });
   if (tid < a.B && tid % gridDim.x == blockIdx.x) {
     const bool served = is_served(r, tid, free);
@@ -357,12 +389,15 @@ __global__ void __launch_bounds__(kPoolThreads, 1) pages_compact_kernel(const Pa
   if (blockIdx.x == 0 && tid < a.n) a.status[tid] = TSV_OK;
   // The holes below L and the pages in use from L on, by rising id.
   int live = before;  // pages in use before the current one
+  const bool aligned = ((reinterpret_cast<uintptr_t>(a.new_id) | reinterpret_cast<uintptr_t>(a.refs_out)) & 15) == 0;
+  EightCounts now(a.pool.refs_d, share.first + 8 * lane, share.end, 0);
 #pragma unroll 1
-  for (int at = share.first; at < share.end; at += 128) {
-    const int page = at + 4 * lane;
-    const int4 v = load_counts(a.pool.refs_d, page, share.end, 0);
-    const int c[4] = {v.x, v.y, v.z, v.w};
-    const int n = (c[0] > 0) + (c[1] > 0) + (c[2] > 0) + (c[3] > 0);
+  for (int at = share.first; at < share.end; at += 256) {
+    const int page = at + 8 * lane;
+    const EightCounts next(a.pool.refs_d, page + 256, share.end, 0);  // on its way meanwhile
+    int n = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) n += now.c[e] > 0;
     int upto = n;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -370,32 +405,74 @@ __global__ void __launch_bounds__(kPoolThreads, 1) pages_compact_kernel(const Pa
       if (lane >= o) upto += y;
     }
     int k = live + upto - n;
+    // New ids and counts that are known already; a hole's count and a moved page's id
+    // come below.
+    int id_out[8], count_out[8];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
+    for (int e = 0; e < 8; ++e) {
       const int id = page + e;
-      if (id >= share.end) break;
-      const bool used = c[e] > 0;
-      if (id < L) {
-        a.new_id[id] = used ? id : -1;
-        if (used) a.refs_out[id] = c[e];
-        else a.move_dst[id - k] = id;  // (its count comes with its new page)
-      } else if (used) {
-        a.move_src[k - kept] = id;
-      } else {
-        a.new_id[id] = -1;
-        a.refs_out[id] = 0;
+      const bool used = now.c[e] > 0, low = id < L;
+      id_out[e] = used && low ? id : -1;
+      count_out[e] = low || !used ? now.c[e] : 0;
+      if (id < share.end) {
+        if (low && !used) a.move_dst[id - k] = id;
+        if (!low && used) a.move_src[k - kept] = id;
       }
       k += used;
     }
+    // (A moved page's count is still to be read when the counts are written in place.)
+    const bool in_place = a.refs_out == a.pool.refs_d;
+    if (page + 8 <= share.end) {
+      int4* to_id = reinterpret_cast<int4*>(a.new_id + page);
+      if (aligned) {
+        to_id[0] = make_int4(id_out[0], id_out[1], id_out[2], id_out[3]);
+        to_id[1] = make_int4(id_out[4], id_out[5], id_out[6], id_out[7]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) a.new_id[page + e] = id_out[e];
+      }
+      if (!in_place) {
+        int4* to_count = reinterpret_cast<int4*>(a.refs_out + page);
+        if (aligned) {
+          to_count[0] = make_int4(count_out[0], count_out[1], count_out[2], count_out[3]);
+          to_count[1] = make_int4(count_out[4], count_out[5], count_out[6], count_out[7]);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) a.refs_out[page + e] = count_out[e];
+        }
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        if (page + e >= share.end) break;
+        a.new_id[page + e] = id_out[e];
+        if (!in_place) a.refs_out[page + e] = count_out[e];
+      }
+    }
     live += __shfl_sync(0xffffffffu, upto, 31);
+    now = next;
   }
   cluster_sync_global();
-  for (int i = blockIdx.x * kPoolThreads + tid; i < moved; i += gridDim.x * kPoolThreads) {
-    const int src = __ldcg(a.move_src + i), dst = __ldcg(a.move_dst + i);
-    const int count = __ldcg(a.pool.refs_d + src);
-    a.new_id[src] = dst;
-    a.refs_out[src] = 0;
-    a.refs_out[dst] = count;
+  constexpr int U = 4;
+  const int threads = gridDim.x * kPoolThreads;
+#pragma unroll 1
+  for (int i = blockIdx.x * kPoolThreads + tid; i < moved; i += U * threads) {
+    int src[U], dst[U], count[U];
+#pragma unroll
+    for (int q = 0; q < U; ++q) {
+      const bool on = i + q * threads < moved;
+      src[q] = on ? __ldcg(a.move_src + i + q * threads) : -1;
+      dst[q] = on ? __ldcg(a.move_dst + i + q * threads) : -1;
+    }
+#pragma unroll
+    for (int q = 0; q < U; ++q) count[q] = src[q] >= 0 ? __ldcg(a.pool.refs_d + src[q]) : 0;
+#pragma unroll
+    for (int q = 0; q < U; ++q) {
+      if (src[q] < 0) continue;
+      a.new_id[src[q]] = dst[q];
+      a.refs_out[src[q]] = 0;
+      a.refs_out[dst[q]] = count[q];
+    }
   }
 }
 
@@ -425,27 +502,55 @@ __global__ void __launch_bounds__(kRemapThreads) pages_remap_kernel(const PagesC
   if (bad) a.status[t] = TSV_ERR_INVALID_ARG;
 }
 
-int pool_ctas(int32_t num_pages) {
-  // A CTA's 32 warps take 4096 counts a step.
+// CTAs of a call's cluster: one per 4096 counts, a step of a CTA's 32 warps being
+// twice as many.
+int pool_ctas(int32_t num_pages, int most) {
   int n = 1;
-  while (n < kPoolCtas && num_pages > n * 4096) n *= 2;
+  while (n < most && num_pages > n * 4096) n *= 2;
   return n;
 }
 
 }  // namespace
 
-cudaError_t launch_pages_resize(const PagesResizeArgs& a, cudaStream_t st) {
-  const int n = pool_ctas(a.pool.num_pages);
+int pages_cluster_limit() {
+  // Clusters of 16 have to be asked for, kernel by kernel.
+  int most = kPoolCtas;
+  const void* kernels[3] = {reinterpret_cast<const void*>(pages_resize_kernel), reinterpret_cast<const void*>(pages_fork_kernel),
+                            reinterpret_cast<const void*>(pages_compact_kernel)};
+  for (const void* k : kernels) {
+    int fit = 0;
+    if (cudaFuncSetAttribute(k, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess) {
+      cudaLaunchConfig_t cfg = {};
+      cfg.gridDim = dim3(kPoolCtas);
+      cfg.blockDim = dim3(kPoolThreads);
+      cudaLaunchAttribute attr[1];
+      attr[0].id = cudaLaunchAttributeClusterDimension;
+      attr[0].val.clusterDim.x = kPoolCtas;
+      attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+      cfg.attrs = attr;
+      cfg.numAttrs = 1;
+      if (cudaOccupancyMaxActiveClusters(&fit, k, &cfg) != cudaSuccess) fit = 0;
+    }
+    if (fit < 1) {
+      cudaGetLastError();
+      most = 8;
+    }
+  }
+  return most;
+}
+
+cudaError_t launch_pages_resize(const PagesResizeArgs& a, int most, cudaStream_t st) {
+  const int n = pool_ctas(a.pool.num_pages, most);
   return launch_pdl(pages_resize_kernel, dim3(n), dim3(kPoolThreads), 0, st, (unsigned)n, a);
 }
 
-cudaError_t launch_pages_fork(const PagesForkArgs& a, cudaStream_t st) {
-  const int n = pool_ctas(a.pool.num_pages);
+cudaError_t launch_pages_fork(const PagesForkArgs& a, int most, cudaStream_t st) {
+  const int n = pool_ctas(a.pool.num_pages, most);
   return launch_pdl(pages_fork_kernel, dim3(n), dim3(kPoolThreads), 0, st, (unsigned)n, a);
 }
 
-cudaError_t launch_pages_compact(const PagesCompactArgs& a, cudaStream_t st) {
-  const int n = pool_ctas(a.pool.num_pages);
+cudaError_t launch_pages_compact(const PagesCompactArgs& a, int most, cudaStream_t st) {
+  const int n = pool_ctas(a.pool.num_pages, most);
   const cudaError_t e = launch_pdl(pages_compact_kernel, dim3(n), dim3(kPoolThreads), 0, st, (unsigned)n, a);
   if (e != cudaSuccess || a.n == 0) return e;
   int64_t rows = 0;

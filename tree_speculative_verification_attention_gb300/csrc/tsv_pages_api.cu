@@ -30,6 +30,11 @@ bool lists_meet(const tsv_page_table& a, int64_t ra, const tsv_page_table& b, in
   return a0 < b1 && b0 < a1;
 }
 
+int cluster_of(tsv_handle h) {  // (the handle's device is current)
+  if (h->pages_cluster == 0) h->pages_cluster = pages_cluster_limit();
+  return h->pages_cluster;
+}
+
 }  // namespace
 
 extern "C" {
@@ -50,7 +55,7 @@ tsv_status tsv_pages_resize(tsv_handle h, const tsv_page_pool* pool, const tsv_p
   a.B = B;
   a.page_size = page_size;
   a.status = status_d;
-  return cuda_status(launch_pages_resize(a, static_cast<cudaStream_t>(stream)));
+  return cuda_status(launch_pages_resize(a, cluster_of(h), static_cast<cudaStream_t>(stream)));
 }
 
 tsv_status tsv_pages_fork(tsv_handle h, const tsv_page_pool* pool, const tsv_page_table* from, const int32_t* from_pages_d,
@@ -80,7 +85,7 @@ tsv_status tsv_pages_fork(tsv_handle h, const tsv_page_pool* pool, const tsv_pag
   a.copy_src = copy_src_d;
   a.copy_dst = copy_dst_d;
   a.status = status_d;
-  return cuda_status(launch_pages_fork(a, static_cast<cudaStream_t>(stream)));
+  return cuda_status(launch_pages_fork(a, cluster_of(h), static_cast<cudaStream_t>(stream)));
 }
 
 tsv_status tsv_pages_compact(tsv_handle h, const tsv_page_pool* pool, int32_t* refs_out_d, const tsv_page_lists* lists,
@@ -115,7 +120,7 @@ tsv_status tsv_pages_compact(tsv_handle h, const tsv_page_pool* pool, int32_t* r
   a.move_dst = move_dst_d;
   a.moved = moved_d;
   a.status = status_d;
-  return cuda_status(launch_pages_compact(a, static_cast<cudaStream_t>(stream)));
+  return cuda_status(launch_pages_compact(a, cluster_of(h), static_cast<cudaStream_t>(stream)));
 }
 
 tsv_status tsv_pages_copy(tsv_handle h, const tsv_paged_cache* cache, const int32_t* src_d, const int32_t* dst_d, int32_t n,
