@@ -31,12 +31,6 @@ __device__ __forceinline__ int ld_dsmem_i32(uint32_t addr) {
 // The counterpart of `p` in CTA `rank` of the cluster.
 __device__ __forceinline__ int remote_i32(const int* p, int rank) { return ld_dsmem_i32(mapa_shared(smem_u32(p), (uint32_t)rank)); }
 
-// Barrier of the cluster behind which earlier writes to global memory are seen too.
-__device__ __forceinline__ void cluster_sync_global() {
-  __threadfence();
-  cluster_sync_all();
-}
-
 // Four counts from page `at` on (a multiple of 4); pages past the end count as `none`.
 __device__ __forceinline__ int4 load_counts(const int32_t* refs, int at, int pages, int none) {
   if (at + 4 <= pages) return __ldcg(reinterpret_cast<const int4*>(refs + at));
@@ -179,31 +173,50 @@ __device__ __forceinline__ void hand_out(PoolRequests& r, const tsv_page_pool& p
   }
 }
 
-// One reference less of a page that is held; false when it is not.
-__device__ __forceinline__ bool drop_page(int32_t* refs, int32_t id) {
-  if (atomicSub(refs + id, 1) > 0) return true;
-  atomicAdd(refs + id, 1);
-  return false;
-}
-__device__ __forceinline__ bool is_held(const tsv_page_pool& p, int32_t id) {
-  return (uint32_t)id < (uint32_t)p.num_pages && __ldcg(p.refs_d + id) > 0;
-}
-
-// Entries from `first` up to `end` of a list by `threads` threads, eight of a
-// thread in flight: each(id), and whether any was false.
+// Entries from `first` up to `end` of a list by `threads` threads, U of a thread
+// in flight: for_entries hands f the ids (-1: none) and their places.
+constexpr int kFlight = 8;
 template <typename F>
-__device__ __forceinline__ bool every_entry(const int32_t* ids, int first, int end, int t, int threads, F each) {
-  constexpr int U = 8;
-  bool fine = true;
+__device__ __forceinline__ void for_entries(const int32_t* ids, int first, int end, int t, int threads, F f) {
 #pragma unroll 1
-  for (int i = first + t; i < end; i += U * threads) {
-    int32_t id[U];
+  for (int i = first + t; i < end; i += kFlight * threads) {
+    int32_t id[kFlight];
+    bool on[kFlight];
 #pragma unroll
-    for (int q = 0; q < U; ++q) id[q] = i + q * threads < end ? __ldcg(ids + i + q * threads) : -1;
-#pragma unroll
-    for (int q = 0; q < U; ++q)
-      if (i + q * threads < end) fine &= each(id[q], i + q * threads);
+    for (int q = 0; q < kFlight; ++q) {
+      on[q] = i + q * threads < end;
+      id[q] = on[q] ? __ldcg(ids + i + q * threads) : -1;
+    }
+    f(id, on, i);
   }
+}
+// Whether all are pages that some list holds.
+__device__ __forceinline__ bool entries_held(const tsv_page_pool& p, const int32_t* ids, int first, int end, int t, int threads) {
+  bool fine = true;
+  for_entries(ids, first, end, t, threads, [&](const int32_t (&id)[kFlight], const bool (&on)[kFlight], int) {
+    int32_t count[kFlight];
+#pragma unroll
+    for (int q = 0; q < kFlight; ++q) count[q] = (uint32_t)id[q] < (uint32_t)p.num_pages ? __ldcg(p.refs_d + id[q]) : 0;
+#pragma unroll
+    for (int q = 0; q < kFlight; ++q) fine &= !on[q] || count[q] > 0;
+  });
+  return fine;
+}
+// One reference less of each (valid ids); false when one was not held, whose count
+// then stays what it was.
+__device__ __forceinline__ bool drop_entries(const tsv_page_pool& p, const int32_t* ids, int first, int end, int t, int threads) {
+  bool fine = true;
+  for_entries(ids, first, end, t, threads, [&](const int32_t (&id)[kFlight], const bool (&on)[kFlight], int) {
+    int32_t before[kFlight];
+#pragma unroll
+    for (int q = 0; q < kFlight; ++q) before[q] = on[q] ? atomicSub(p.refs_d + id[q], 1) : 1;
+#pragma unroll
+    for (int q = 0; q < kFlight; ++q)
+      if (before[q] <= 0) {
+        atomicAdd(p.refs_d + id[q], 1);
+        fine = false;
+      }
+  });
   return fine;
 }
 
@@ -241,10 +254,10 @@ __global__ void __launch_bounds__(kPoolThreads, 1) pages_resize_kernel(const Pag
       if (r.bad[b] || r.want[b] >= r.held[b]) return;
       const int32_t* ids = a.table.ids_d + (int64_t)b * a.table.stride;
       bool bad = false;
-      bad |= !every_entry(ids, r.want[b], r.held[b], t, threads, [&](int32_t id, int) { return is_held(a.pool, id); });
+      bad |= !entries_held(a.pool, ids, r.want[b], r.held[b], t, threads);
       if (t == 0 && __ldg(a.rows + b) % a.page_size > 0) {  // new rows would go to the last page
         const int32_t id = __ldcg(ids + r.want[b] - 1);
-        bad |= !is_held(a.pool, id) || __ldcg(a.pool.refs_d + id) > 1;
+        bad |= (uint32_t)id >= (uint32_t)a.pool.num_pages || __ldcg(a.pool.refs_d + id) != 1;
       }
       if (bad) atomicOr(&r.bad[b], 2);
     });
@@ -252,9 +265,9 @@ __global__ void __launch_bounds__(kPoolThreads, 1) pages_resize_kernel(const Pag
     for_own(a.B, warp, lane, [&](int b, int t, int threads) {
       if (r.bad[b] & 3 || r.want[b] >= r.held[b]) return;
       const int32_t* ids = a.table.ids_d + (int64_t)b * a.table.stride;
-      if (!every_entry(ids, r.want[b], r.held[b], t, threads, [&](int32_t id, int) { return drop_page(a.pool.refs_d, id); })) atomicOr(&r.bad[b], 4);  // (listed more often than counted)
+      if (!drop_entries(a.pool, ids, r.want[b], r.held[b], t, threads)) atomicOr(&r.bad[b], 4);  // (listed more often than counted)
     });
-    cluster_sync_global();
+    cluster_sync_all();  // (its release and acquire cover global memory among the cluster's threads)
   } else {
     __syncthreads();
   }
@@ -305,8 +318,7 @@ __global__ void __launch_bounds__(kPoolThreads, 1) pages_fork_kernel(const Pages
     if (source[b] < 0) return;
     const int32_t* old = a.to.ids_d + (int64_t)b * a.to.stride;
     const int32_t* ids = a.from.ids_d + (int64_t)source[b] * a.from.stride;
-    const auto held = [&](int32_t id, int) { return is_held(a.pool, id); };
-    const bool fine = every_entry(old, 0, r.held[b], t, threads, held) & every_entry(ids, 0, r.want[b], t, threads, held);
+    const bool fine = entries_held(a.pool, old, 0, r.held[b], t, threads) & entries_held(a.pool, ids, 0, r.want[b], t, threads);
     if (!fine) atomicOr(&r.bad[b], 2);
   });
   cluster_sync_all();  // every look at the counts comes before the first change
@@ -323,9 +335,9 @@ __global__ void __launch_bounds__(kPoolThreads, 1) pages_fork_kernel(const Pages
   for_own(a.B, warp, lane, [&](int b, int t, int threads) {
     if (source[b] < 0) return;
     const int32_t* old = a.to.ids_d + (int64_t)b * a.to.stride;
-    if (!every_entry(old, 0, r.held[b], t, threads, [&](int32_t id, int) { return drop_page(a.pool.refs_d, id); })) atomicOr(&r.bad[b], 4);  // (listed more often than counted)
+    if (!drop_entries(a.pool, old, 0, r.held[b], t, threads)) atomicOr(&r.bad[b], 4);  // (listed more often than counted)
   });
-  cluster_sync_global();
+  cluster_sync_all();  // (its release and acquire cover global memory among the cluster's threads)
   int free = 0;
   const PoolShare share(a.pool.num_pages, warp);
   int rank = 0;
@@ -347,10 +359,13 @@ __global__ void __launch_bounds__(kPoolThreads, 1) pages_fork_kernel(const Pages
     if (source[b] < 0 || !is_served(r, b, free)) return;
     int32_t* list = const_cast<int32_t*>(a.to.ids_d) + (int64_t)b * a.to.stride;
     const int32_t* ids = a.from.ids_d + (int64_t)source[b] * a.from.stride;
-    every_entry(ids, 0, full[b], t, threads, [&](int32_t id, int i) {
-      list[i] = id;
-      atomicAdd(a.pool.refs_d + id, 1);
-      return true;
+    for_entries(ids, 0, full[b], t, threads, [&](const int32_t (&id)[kFlight], const bool (&on)[kFlight], int i) {
+#pragma unroll
+      for (int q = 0; q < kFlight; ++q) {
+        if (!on[q]) continue;
+        list[i + q * threads] = id[q];
+        atomicAdd(a.pool.refs_d + id[q], 1);
+      }
     });
   });
   if (tid < a.B && tid % gridDim.x == blockIdx.x) {
@@ -452,7 +467,7 @@ __global__ void __launch_bounds__(kPoolThreads, 1) pages_compact_kernel(const Pa
     live += __shfl_sync(0xffffffffu, upto, 31);
     now = next;
   }
-  cluster_sync_global();
+  cluster_sync_all();  // (its release and acquire cover global memory among the cluster's threads)
   constexpr int U = 4;
   const int threads = gridDim.x * kPoolThreads;
 #pragma unroll 1
@@ -502,11 +517,11 @@ __global__ void __launch_bounds__(kRemapThreads) pages_remap_kernel(const PagesC
   if (bad) a.status[t] = TSV_ERR_INVALID_ARG;
 }
 
-// CTAs of a call's cluster: one per 4096 counts, a step of a CTA's 32 warps being
-// twice as many.
-int pool_ctas(int32_t num_pages, int most) {
+// CTAs of a call's cluster: one per two steps of 32 warps x 256 counts, or per
+// 8192 entries that the lists have room for.
+int pool_ctas(int32_t num_pages, int64_t entries, int most) {
   int n = 1;
-  while (n < most && num_pages > n * 4096) n *= 2;
+  while (n < most && (num_pages > n * 16384 || entries > n * (int64_t)8192)) n *= 2;
   return n;
 }
 
@@ -540,17 +555,17 @@ int pages_cluster_limit() {
 }
 
 cudaError_t launch_pages_resize(const PagesResizeArgs& a, int most, cudaStream_t st) {
-  const int n = pool_ctas(a.pool.num_pages, most);
+  const int n = pool_ctas(a.pool.num_pages, (int64_t)a.B * a.table.pages, most);
   return launch_pdl(pages_resize_kernel, dim3(n), dim3(kPoolThreads), 0, st, (unsigned)n, a);
 }
 
 cudaError_t launch_pages_fork(const PagesForkArgs& a, int most, cudaStream_t st) {
-  const int n = pool_ctas(a.pool.num_pages, most);
+  const int n = pool_ctas(a.pool.num_pages, (int64_t)a.B * a.to.pages, most);
   return launch_pdl(pages_fork_kernel, dim3(n), dim3(kPoolThreads), 0, st, (unsigned)n, a);
 }
 
 cudaError_t launch_pages_compact(const PagesCompactArgs& a, int most, cudaStream_t st) {
-  const int n = pool_ctas(a.pool.num_pages, most);
+  const int n = pool_ctas(a.pool.num_pages, 0, most);
   const cudaError_t e = launch_pdl(pages_compact_kernel, dim3(n), dim3(kPoolThreads), 0, st, (unsigned)n, a);
   if (e != cudaSuccess || a.n == 0) return e;
   int64_t rows = 0;
