@@ -29,7 +29,7 @@ struct tsv_handle_s {
   int mss_max_clusters[kMssClusterSizeEntries];  // resident MSS clusters of each size
   uint32_t verify_overlap;  // tsv_set_verify_overlap: TSV_OVERLAP_* flags
   uint32_t paged_attr_mask;   // paged attention kernels whose attributes are set, one bit per (D, tile rows)
-  uint32_t chunk_attr_mask;   // chunk attention kernels, one bit per D
+  uint32_t chunk_attr_mask;   // chunk attention kernels, one bit per (type, D)
   int pages_cluster;          // most CTAs of a page-list call's cluster, 0: not asked yet
   uint32_t append_attr_mask;  // paged append kernels, one bit per (type, D)
 };
@@ -366,6 +366,8 @@ inline PagedChunkLayout paged_chunk_layout(int grid, int32_t D) {
 cudaError_t paged_chunk_set_attributes(int32_t D);
 cudaError_t launch_paged_chunk(const CUtensorMap& tk, const CUtensorMap& tv, const PagedAttnArgs& a, int num_sms, void* ws,
                                cudaStream_t st);
+cudaError_t paged_chunk_f32_set_attributes(int32_t D);
+cudaError_t launch_paged_chunk_f32(const PagedAttnArgs& a, int num_sms, cudaStream_t st);
 
 // Page lists and the pool they draw on (tsv_pages.h).
 struct PagesResizeArgs {

@@ -406,6 +406,14 @@ tsv_status tsv_paged_chunk_attention(tsv_handle h, tsv_dtype dtype, const void* 
     if (st != TSV_OK) return st;
     return cuda_status(launch_paged_chunk(tk, tv, a, h->num_sms, workspace_d, static_cast<cudaStream_t>(stream)));
   }
+  if (dtype == TSV_F32 && !(flags & TSV_ATTN_SIMT) && max_rows > 1) {
+    const uint32_t bit = a.cache.D == 128 ? 8u : 4u;
+    if (!(h->chunk_attr_mask & bit)) {
+      if (paged_chunk_f32_set_attributes(a.cache.D) != cudaSuccess) return TSV_ERR_CUDA;
+      h->chunk_attr_mask |= bit;
+    }
+    return cuda_status(launch_paged_chunk_f32(a, h->num_sms, static_cast<cudaStream_t>(stream)));
+  }
   return cuda_status(launch_paged_attention_simt(a, dtype == TSV_BF16, static_cast<cudaStream_t>(stream)));
 }
 
