@@ -413,7 +413,7 @@ struct PagesCopyArgs {
 int pages_cluster_limit();
 cudaError_t launch_pages_resize(const PagesResizeArgs& a, int most, cudaStream_t st);
 cudaError_t launch_pages_fork(const PagesForkArgs& a, int most, cudaStream_t st);
-cudaError_t launch_pages_compact(const PagesCompactArgs& a, int most, cudaStream_t st);
+cudaError_t launch_pages_compact(const PagesCompactArgs& a, int most, int num_sms, cudaStream_t st);
 cudaError_t launch_pages_copy(const PagesCopyArgs& a, int num_sms, cudaStream_t st);
 
 // Host-side checks that the paged entries share (tsv_paged_api.cu).

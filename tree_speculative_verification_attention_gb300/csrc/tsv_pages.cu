@@ -220,6 +220,20 @@ __device__ __forceinline__ bool drop_entries(const tsv_page_pool& p, const int32
   return fine;
 }
 
+// Entries `first` up to `end` of list b become those of its source, shared.
+__device__ __forceinline__ void share_entries(const PagesForkArgs& a, int b, int source, int first, int end, int t, int threads) {
+  int32_t* list = const_cast<int32_t*>(a.to.ids_d) + (int64_t)b * a.to.stride;
+  for_entries(a.from.ids_d + (int64_t)source * a.from.stride, first, end, t, threads,
+              [&](const int32_t (&id)[kFlight], const bool (&on)[kFlight], int i) {
+#pragma unroll
+                for (int q = 0; q < kFlight; ++q) {
+                  if (!on[q]) continue;
+                  list[i + q * threads] = id[q];
+                  atomicAdd(a.pool.refs_d + id[q], 1);
+                }
+              });
+}
+
 // The cluster's requests are shared out: request b belongs to CTA b % CTAs, and
 // there to a group of warps.  for_own(b, t, threads) runs on each of them.
 template <typename F>
@@ -292,6 +306,52 @@ __global__ void __launch_bounds__(kPoolThreads, 1) pages_resize_kernel(const Pag
   cluster_sync_all();  // the others have read this CTA's total
 }
 
+// A fork of many entries is three launches, so that the lists' part of it runs on as
+// many SMs as there are lists: give back (kForkBack), the pages of the lists' own
+// (kForkTake), share (pages_share_kernel).  With few entries one cluster does it all.
+// (What a list gives back may be looked at while others are looked over: a page that
+// a list holds has a count above 0 whatever the others do.)
+enum { kForkAll = 0, kForkTake = 1 };
+
+// List b of a fork: what it wants; whether the numbers fit.
+struct ForkList {
+  int held, full, part, source;  // source -1: stays as it is
+  bool bad;
+  __device__ __forceinline__ ForkList(const PagesForkArgs& a, int b) {
+    const int rows = __ldg(a.rows + b);
+    held = __ldcg(a.to_pages + b);
+    source = __ldg(a.source + b);
+    full = rows / a.page_size;
+    part = rows % a.page_size > 0 ? 1 : 0;
+    bad = source < -1 || source >= a.F || (source >= 0 && (rows < 0 || held < 0 || held > a.to.pages));
+    if (source >= 0 && !bad) {
+      const int has = __ldg(a.from_pages + source);
+      bad = has < 0 || has > a.from.pages || full + part > has || full + part > a.to.pages;
+    }
+  }
+};
+
+__global__ void __launch_bounds__(kPoolThreads, 1) pages_give_back_kernel(const PagesForkArgs a) {
+  pdl_wait();  // the previous kernel's results are visible from here on
+  pdl_trigger();
+  const int b = blockIdx.x, t = threadIdx.x;
+  const ForkList l(a, b);
+  bool bad = l.bad;
+  if (!bad && l.source >= 0) {
+    const int32_t* old = a.to.ids_d + (int64_t)b * a.to.stride;
+    const int32_t* ids = a.from.ids_d + (int64_t)l.source * a.from.stride;
+    bool fine = entries_held(a.pool, old, 0, l.held, t, kPoolThreads) & entries_held(a.pool, ids, 0, l.full + l.part, t, kPoolThreads);
+    bad = __syncthreads_or(!fine);
+    if (!bad && !drop_entries(a.pool, old, 0, l.held, t, kPoolThreads)) bad = true;
+    // (2: listed more often than counted.  Its other pages went back: the list is empty.)
+    const bool over = __syncthreads_or(bad) && !__syncthreads_or(!fine);
+    if (t == 0) a.status[b] = over ? 2 : bad ? 1 : 0;
+    return;
+  }
+  if (t == 0) a.status[b] = bad ? 1 : 0;
+}
+
+template <int KIND>
 __global__ void __launch_bounds__(kPoolThreads, 1) pages_fork_kernel(const PagesForkArgs a) {
   __shared__ PoolRequests r;
   __shared__ int32_t source[TSV_MAX_BATCH], full[TSV_MAX_BATCH];
@@ -299,51 +359,50 @@ __global__ void __launch_bounds__(kPoolThreads, 1) pages_fork_kernel(const Pages
   pdl_wait();  // the previous kernel's results are visible from here on
   pdl_trigger();
   if (tid < a.B) {
-    const int held = __ldcg(a.to_pages + tid), rows = __ldg(a.rows + tid), src = __ldg(a.source + tid);
-    const int whole = rows / a.page_size, part = rows % a.page_size > 0 ? 1 : 0;
-    bool bad = src < -1 || src >= a.F || (src >= 0 && (rows < 0 || held < 0 || held > a.to.pages));
-    if (src >= 0 && !bad) {
-      const int has = __ldg(a.from_pages + src);
-      bad = has < 0 || has > a.from.pages || whole + part > has || whole + part > a.to.pages;
+    const ForkList l(a, tid);
+    int bad = l.bad ? 1 : 0;
+    if (KIND == kForkTake) {
+      const int found = __ldcg(a.status + tid);
+      bad = found == 2 ? 4 : found;
     }
-    r.held[tid] = held;
-    r.want[tid] = whole + part;
-    full[tid] = whole;
-    source[tid] = bad ? -1 : src;
-    r.need[tid] = bad || src < 0 ? 0 : part;
+    r.held[tid] = l.held;
+    r.want[tid] = l.full + l.part;
+    full[tid] = l.full;
+    source[tid] = bad & 3 ? -1 : l.source;
+    r.need[tid] = bad || l.source < 0 ? 0 : l.part;
     r.bad[tid] = bad;
   }
   __syncthreads();
-  for_own(a.B, warp, lane, [&](int b, int t, int threads) {
-    if (source[b] < 0) return;
-    const int32_t* old = a.to.ids_d + (int64_t)b * a.to.stride;
-    const int32_t* ids = a.from.ids_d + (int64_t)source[b] * a.from.stride;
-    const bool fine = entries_held(a.pool, old, 0, r.held[b], t, threads) & entries_held(a.pool, ids, 0, r.want[b], t, threads);
-    if (!fine) atomicOr(&r.bad[b], 2);
-  });
-  cluster_sync_all();  // every look at the counts comes before the first change
-  // What the owners found: the needs are the same in every CTA.
-  if (tid < a.B) {
-    const int bad = remote_i32(&r.bad[tid], tid % gridDim.x) & 3;
-    if (bad) {
-      source[tid] = -1;
-      r.need[tid] = 0;
+  if (KIND == kForkAll) {
+    for_own(a.B, warp, lane, [&](int b, int t, int threads) {
+      if (source[b] < 0) return;
+      const int32_t* old = a.to.ids_d + (int64_t)b * a.to.stride;
+      const int32_t* ids = a.from.ids_d + (int64_t)source[b] * a.from.stride;
+      const bool fine = entries_held(a.pool, old, 0, r.held[b], t, threads) & entries_held(a.pool, ids, 0, r.want[b], t, threads);
+      if (!fine) atomicOr(&r.bad[b], 2);
+    });
+    __syncthreads();
+    for_own(a.B, warp, lane, [&](int b, int t, int threads) {
+      if (source[b] < 0 || (r.bad[b] & 3)) return;
+      const int32_t* old = a.to.ids_d + (int64_t)b * a.to.stride;
+      if (!drop_entries(a.pool, old, 0, r.held[b], t, threads)) atomicOr(&r.bad[b], 4);  // (listed more often than counted)
+    });
+    cluster_sync_all();  // (its release and acquire cover global memory among the cluster's threads)
+    // What the owners found: the needs are the same in every CTA.
+    if (tid < a.B) {
+      const int bad = remote_i32(&r.bad[tid], tid % gridDim.x);
+      if (bad & 3) source[tid] = -1;
+      if (bad) r.need[tid] = 0;
     }
+    __syncthreads();
   }
-  __syncthreads();
   if (warp == 0) sum_needs(r, a.B, lane);
-  for_own(a.B, warp, lane, [&](int b, int t, int threads) {
-    if (source[b] < 0) return;
-    const int32_t* old = a.to.ids_d + (int64_t)b * a.to.stride;
-    if (!drop_entries(a.pool, old, 0, r.held[b], t, threads)) atomicOr(&r.bad[b], 4);  // (listed more often than counted)
-  });
-  cluster_sync_all();  // (its release and acquire cover global memory among the cluster's threads)
+  __syncthreads();
   int free = 0;
   const PoolShare share(a.pool.num_pages, warp);
-  int rank = 0;
   if (r.needed > 0) {
     const int mine = count_pages<false>(a.pool.refs_d, share.first, share.end, lane);
-    rank = scan_counts(r.scan, mine, warp, lane, &free);  // (a barrier of the cluster: counts are read before pages are shared)
+    const int rank = scan_counts(r.scan, mine, warp, lane, &free);  // (a barrier of the cluster: counts are read before pages are shared)
     if (tid == 0) r.granted = 0;
     __syncthreads();
     if (tid < a.B && is_served(r, tid, free)) atomicMax(&r.granted, r.need[tid] ? r.upto[tid] : 0);
@@ -355,31 +414,63 @@ __global__ void __launch_bounds__(kPoolThreads, 1) pages_fork_kernel(const Pages
       a.copy_dst[b] = id;
     });
   }
-  for_own(a.B, warp, lane, [&](int b, int t, int threads) {
-    if (source[b] < 0 || !is_served(r, b, free)) return;
-    int32_t* list = const_cast<int32_t*>(a.to.ids_d) + (int64_t)b * a.to.stride;
-    const int32_t* ids = a.from.ids_d + (int64_t)source[b] * a.from.stride;
-    for_entries(ids, 0, full[b], t, threads, [&](const int32_t (&id)[kFlight], const bool (&on)[kFlight], int i) {
-#pragma unroll
-      for (int q = 0; q < kFlight; ++q) {
-        if (!on[q]) continue;
-        list[i + q * threads] = id[q];
-        atomicAdd(a.pool.refs_d + id[q], 1);
-      }
+  if (KIND == kForkAll) {
+    for_own(a.B, warp, lane, [&](int b, int t, int threads) {
+      if (source[b] < 0 || r.bad[b] || !is_served(r, b, free)) return;
+      share_entries(a, b, source[b], 0, full[b], t, threads);
     });
-  });
+  }
   if (tid < a.B && tid % gridDim.x == blockIdx.x) {
+    const int bad = r.bad[tid];
     const bool served = is_served(r, tid, free);
-    if (source[tid] >= 0) a.to_pages[tid] = served ? r.want[tid] : 0;
+    if (source[tid] >= 0) a.to_pages[tid] = served && !bad ? r.want[tid] : 0;
     if (source[tid] < 0 || !served || r.need[tid] == 0) {
       a.copy_src[tid] = -1;
       a.copy_dst[tid] = -1;
     }
-    a.status[tid] = r.bad[tid] ? TSV_ERR_INVALID_ARG : served ? TSV_OK : TSV_ERR_NO_PAGES;
+    a.status[tid] = bad ? TSV_ERR_INVALID_ARG : served ? TSV_OK : TSV_ERR_NO_PAGES;
   }
   cluster_sync_all();  // the others have read this CTA's flags and total
 }
 
+// The whole pages of the lists that the launch before served, 8192 entries a CTA.
+constexpr int kShareEntries = kPoolThreads * kFlight;
+__global__ void __launch_bounds__(kPoolThreads, 1) pages_share_kernel(const PagesForkArgs a, int chunks) {
+  pdl_wait();  // the previous kernel's results are visible from here on
+  pdl_trigger();
+  const int b = blockIdx.x / chunks, first = (blockIdx.x - b * chunks) * kShareEntries;
+  if (__ldcg(a.status + b) != TSV_OK) return;
+  const ForkList l(a, b);
+  if (l.source >= 0) share_entries(a, b, l.source, first, min(l.full, first + kShareEntries), threadIdx.x, kPoolThreads);
+}
+
+// Counts and new ids of the pages that move, thread t of `threads`.
+constexpr int kMoveThreads = 256;
+__device__ __forceinline__ void move_counts(const PagesCompactArgs& a, int moved, int t, int threads) {
+  constexpr int U = 4;
+#pragma unroll 1
+  for (int i = t; i < moved; i += U * threads) {
+    int src[U], dst[U], count[U];
+#pragma unroll
+    for (int q = 0; q < U; ++q) {
+      const bool on = i + q * threads < moved;
+      src[q] = on ? __ldcg(a.move_src + i + q * threads) : -1;
+      dst[q] = on ? __ldcg(a.move_dst + i + q * threads) : -1;
+    }
+#pragma unroll
+    for (int q = 0; q < U; ++q) count[q] = src[q] >= 0 ? __ldcg(a.pool.refs_d + src[q]) : 0;
+#pragma unroll
+    for (int q = 0; q < U; ++q) {
+      if (src[q] < 0) continue;
+      a.new_id[src[q]] = dst[q];
+      a.refs_out[src[q]] = 0;
+      a.refs_out[dst[q]] = count[q];
+    }
+  }
+}
+
+// SPLIT: the counts of the pages that move are another launch's.
+template <bool SPLIT>
 __global__ void __launch_bounds__(kPoolThreads, 1) pages_compact_kernel(const PagesCompactArgs a) {
   __shared__ PoolScan scan;
   __shared__ int below;
@@ -467,28 +558,15 @@ __global__ void __launch_bounds__(kPoolThreads, 1) pages_compact_kernel(const Pa
     live += __shfl_sync(0xffffffffu, upto, 31);
     now = next;
   }
+  if (SPLIT) return;
   cluster_sync_all();  // (its release and acquire cover global memory among the cluster's threads)
-  constexpr int U = 4;
-  const int threads = gridDim.x * kPoolThreads;
-#pragma unroll 1
-  for (int i = blockIdx.x * kPoolThreads + tid; i < moved; i += U * threads) {
-    int src[U], dst[U], count[U];
-#pragma unroll
-    for (int q = 0; q < U; ++q) {
-      const bool on = i + q * threads < moved;
-      src[q] = on ? __ldcg(a.move_src + i + q * threads) : -1;
-      dst[q] = on ? __ldcg(a.move_dst + i + q * threads) : -1;
-    }
-#pragma unroll
-    for (int q = 0; q < U; ++q) count[q] = src[q] >= 0 ? __ldcg(a.pool.refs_d + src[q]) : 0;
-#pragma unroll
-    for (int q = 0; q < U; ++q) {
-      if (src[q] < 0) continue;
-      a.new_id[src[q]] = dst[q];
-      a.refs_out[src[q]] = 0;
-      a.refs_out[dst[q]] = count[q];
-    }
-  }
+  move_counts(a, moved, blockIdx.x * kPoolThreads + tid, gridDim.x * kPoolThreads);
+}
+
+__global__ void __launch_bounds__(kMoveThreads) pages_move_kernel(const PagesCompactArgs a) {
+  pdl_wait();  // the previous kernel's results are visible from here on
+  pdl_trigger();
+  move_counts(a, __ldg(a.moved), blockIdx.x * kMoveThreads + threadIdx.x, gridDim.x * kMoveThreads);
 }
 
 // Entries of the lists under their new ids: a CTA per row and 4096 entries.
@@ -525,13 +603,18 @@ int pool_ctas(int32_t num_pages, int64_t entries, int most) {
   return n;
 }
 
+constexpr int64_t kForkSplit = 32768;  // entries that the lists have room for
+constexpr int kCompactSplit = 131072;  // pages
+
 }  // namespace
 
 int pages_cluster_limit() {
   // Clusters of 16 have to be asked for, kernel by kernel.
   int most = kPoolCtas;
-  const void* kernels[3] = {reinterpret_cast<const void*>(pages_resize_kernel), reinterpret_cast<const void*>(pages_fork_kernel),
-                            reinterpret_cast<const void*>(pages_compact_kernel)};
+  const void* kernels[5] = {reinterpret_cast<const void*>(pages_resize_kernel), reinterpret_cast<const void*>(pages_fork_kernel<kForkAll>),
+                            reinterpret_cast<const void*>(pages_fork_kernel<kForkTake>),
+                            reinterpret_cast<const void*>(pages_compact_kernel<false>),
+                            reinterpret_cast<const void*>(pages_compact_kernel<true>)};
   for (const void* k : kernels) {
     int fit = 0;
     if (cudaFuncSetAttribute(k, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess) {
@@ -560,13 +643,26 @@ cudaError_t launch_pages_resize(const PagesResizeArgs& a, int most, cudaStream_t
 }
 
 cudaError_t launch_pages_fork(const PagesForkArgs& a, int most, cudaStream_t st) {
-  const int n = pool_ctas(a.pool.num_pages, (int64_t)a.B * a.to.pages, most);
-  return launch_pdl(pages_fork_kernel, dim3(n), dim3(kPoolThreads), 0, st, (unsigned)n, a);
+  const int64_t entries = (int64_t)a.B * a.to.pages;
+  if (entries <= kForkSplit) {
+    const int n = pool_ctas(a.pool.num_pages, entries, most);
+    return launch_pdl(pages_fork_kernel<kForkAll>, dim3(n), dim3(kPoolThreads), 0, st, (unsigned)n, a);
+  }
+  cudaError_t e = launch_pdl(pages_give_back_kernel, dim3(a.B), dim3(kPoolThreads), 0, st, 0u, a);
+  if (e != cudaSuccess) return e;
+  const int n = pool_ctas(a.pool.num_pages, 0, most);
+  e = launch_pdl(pages_fork_kernel<kForkTake>, dim3(n), dim3(kPoolThreads), 0, st, (unsigned)n, a);
+  if (e != cudaSuccess) return e;
+  const int chunks = (a.to.pages + kShareEntries - 1) / kShareEntries;
+  return launch_pdl(pages_share_kernel, dim3(a.B * chunks), dim3(kPoolThreads), 0, st, 0u, a, chunks);
 }
 
-cudaError_t launch_pages_compact(const PagesCompactArgs& a, int most, cudaStream_t st) {
+cudaError_t launch_pages_compact(const PagesCompactArgs& a, int most, int num_sms, cudaStream_t st) {
   const int n = pool_ctas(a.pool.num_pages, 0, most);
-  const cudaError_t e = launch_pdl(pages_compact_kernel, dim3(n), dim3(kPoolThreads), 0, st, (unsigned)n, a);
+  const bool split = a.pool.num_pages > kCompactSplit;
+  cudaError_t e = split ? launch_pdl(pages_compact_kernel<true>, dim3(n), dim3(kPoolThreads), 0, st, (unsigned)n, a)
+                        : launch_pdl(pages_compact_kernel<false>, dim3(n), dim3(kPoolThreads), 0, st, (unsigned)n, a);
+  if (e == cudaSuccess && split) e = launch_pdl(pages_move_kernel, dim3(2 * num_sms), dim3(kMoveThreads), 0, st, 0u, a);
   if (e != cudaSuccess || a.n == 0) return e;
   int64_t rows = 0;
   int32_t width = 1;

@@ -120,7 +120,7 @@ tsv_status tsv_pages_compact(tsv_handle h, const tsv_page_pool* pool, int32_t* r
   a.move_dst = move_dst_d;
   a.moved = moved_d;
   a.status = status_d;
-  return cuda_status(launch_pages_compact(a, cluster_of(h), static_cast<cudaStream_t>(stream)));
+  return cuda_status(launch_pages_compact(a, cluster_of(h), h->num_sms, static_cast<cudaStream_t>(stream)));
 }
 
 tsv_status tsv_pages_copy(tsv_handle h, const tsv_paged_cache* cache, const int32_t* src_d, const int32_t* dst_d, int32_t n,
