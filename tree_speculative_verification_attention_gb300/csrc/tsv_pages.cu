@@ -60,9 +60,9 @@ struct EightCounts {
 // The range of pages of a warp: whole chunks of 256.
 struct PoolShare {
   int first, end;
-  __device__ __forceinline__ PoolShare(int pages, int warp) {
-    const int warps = gridDim.x * kPoolWarps, chunks = (pages + 255) >> 8;
-    const int w = blockIdx.x * kPoolWarps + warp;
+  __device__ __forceinline__ PoolShare(int pages, int warp) : PoolShare(pages, blockIdx.x * kPoolWarps + warp, gridDim.x * kPoolWarps) {}
+  __device__ __forceinline__ PoolShare(int pages, int w, int warps) {
+    const int chunks = (pages + 255) >> 8;
     first = (int)((int64_t)chunks * w / warps) << 8;
     end = min(pages, (int)((int64_t)chunks * (w + 1) / warps) << 8);
   }
@@ -469,31 +469,9 @@ __device__ __forceinline__ void move_counts(const PagesCompactArgs& a, int moved
   }
 }
 
-// SPLIT: the counts of the pages that move are another launch's.
-template <bool SPLIT>
-__global__ void __launch_bounds__(kPoolThreads, 1) pages_compact_kernel(const PagesCompactArgs a) {
-  __shared__ PoolScan scan;
-  __shared__ int below;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  pdl_wait();  // the previous kernel's results are visible from here on
-  pdl_trigger();
-  const int pages = a.pool.num_pages;
-  const PoolShare share(pages, warp);
-  int L = 0;
-  const int before = scan_counts(scan, count_pages<true>(a.pool.refs_d, share.first, share.end, lane), warp, lane, &L);
-  // Pages in use below L: the warp whose range holds page L knows (the last one
-  // when every page is in use), and tells every CTA.
-  const bool last = blockIdx.x == gridDim.x - 1 && warp == kPoolWarps - 1;
-  if ((share.first <= L && L < share.end) || (last && L == pages)) {
-    const int n = before + count_pages<true>(a.pool.refs_d, share.first, min(L, share.end), lane);
-    if (lane < gridDim.x)
-      asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(mapa_shared(smem_u32(&below), (uint32_t)lane)), "r"(n) : "memory");
-  }
-  cluster_sync_all();
-  const int kept = below, moved = L - kept;
-  if (blockIdx.x == 0 && tid == 0) *a.moved = moved;
-  if (blockIdx.x == 0 && tid < a.n) a.status[tid] = TSV_OK;
-  // The holes below L and the pages in use from L on, by rising id.
+// The holes below L and the pages in use from L on, by rising id, and what does not
+// move, of a warp's share; `before` pages in use lie in front of it, `kept` below L.
+__device__ __forceinline__ void place_pages(const PagesCompactArgs& a, const PoolShare& share, int before, int L, int kept, int lane) {
   int live = before;  // pages in use before the current one
   const bool aligned = ((reinterpret_cast<uintptr_t>(a.new_id) | reinterpret_cast<uintptr_t>(a.refs_out)) & 15) == 0;
   EightCounts now(a.pool.refs_d, share.first + 8 * lane, share.end, 0);
@@ -558,7 +536,53 @@ __global__ void __launch_bounds__(kPoolThreads, 1) pages_compact_kernel(const Pa
     live += __shfl_sync(0xffffffffu, upto, 31);
     now = next;
   }
-  if (SPLIT) return;
+}
+
+// The same by as many CTAs as hold four warps each, of `warps` that shared the counts.
+constexpr int kPlaceWarps = 4;
+__global__ void __launch_bounds__(32 * kPlaceWarps) pages_place_kernel(const PagesCompactArgs a, int warps) {
+  pdl_wait();  // the previous kernel's results are visible from here on
+  pdl_trigger();
+  const int lane = threadIdx.x & 31;
+  const PoolShare share(a.pool.num_pages, blockIdx.x * kPlaceWarps + (threadIdx.x >> 5), warps);
+  if (share.first >= share.end) return;
+  const int before = __ldcg(a.new_id + share.first), L = __ldcg(a.new_id + share.first + 1), kept = L - __ldcg(a.moved);
+  __syncwarp();  // (read by every lane before they are written)
+  place_pages(a, share, before, L, kept, lane);
+}
+
+// SPLIT: counting alone; placing and moving are launches of their own.
+template <bool SPLIT>
+__global__ void __launch_bounds__(kPoolThreads, 1) pages_compact_kernel(const PagesCompactArgs a) {
+  __shared__ PoolScan scan;
+  __shared__ int below;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  pdl_wait();  // the previous kernel's results are visible from here on
+  pdl_trigger();
+  const int pages = a.pool.num_pages;
+  const PoolShare share(pages, warp);
+  int L = 0;
+  const int before = scan_counts(scan, count_pages<true>(a.pool.refs_d, share.first, share.end, lane), warp, lane, &L);
+  // Pages in use below L: the warp whose range holds page L knows (the last one
+  // when every page is in use), and tells every CTA.
+  const bool last = blockIdx.x == gridDim.x - 1 && warp == kPoolWarps - 1;
+  if ((share.first <= L && L < share.end) || (last && L == pages)) {
+    const int n = before + count_pages<true>(a.pool.refs_d, share.first, min(L, share.end), lane);
+    if (lane < gridDim.x)
+      asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(mapa_shared(smem_u32(&below), (uint32_t)lane)), "r"(n) : "memory");
+  }
+  cluster_sync_all();
+  const int kept = below, moved = L - kept;
+  if (blockIdx.x == 0 && tid == 0) *a.moved = moved;
+  if (blockIdx.x == 0 && tid < a.n) a.status[tid] = TSV_OK;
+  if (SPLIT) {  // on to pages_place_kernel, in the words that it writes
+    if (lane == 0 && share.first < share.end) {
+      a.new_id[share.first] = before;
+      a.new_id[share.first + 1] = L;  // (a share has 256 pages at least, but for a last one of two chunks at least)
+    }
+    return;
+  }
+  place_pages(a, share, before, L, kept, lane);
   cluster_sync_all();  // (its release and acquire cover global memory among the cluster's threads)
   move_counts(a, moved, blockIdx.x * kPoolThreads + tid, gridDim.x * kPoolThreads);
 }
@@ -662,6 +686,8 @@ cudaError_t launch_pages_compact(const PagesCompactArgs& a, int most, int num_sm
   const bool split = a.pool.num_pages > kCompactSplit;
   cudaError_t e = split ? launch_pdl(pages_compact_kernel<true>, dim3(n), dim3(kPoolThreads), 0, st, (unsigned)n, a)
                         : launch_pdl(pages_compact_kernel<false>, dim3(n), dim3(kPoolThreads), 0, st, (unsigned)n, a);
+  if (e == cudaSuccess && split)
+    e = launch_pdl(pages_place_kernel, dim3(n * kPoolWarps / kPlaceWarps), dim3(32 * kPlaceWarps), 0, st, 0u, a, n * kPoolWarps);
   if (e == cudaSuccess && split) e = launch_pdl(pages_move_kernel, dim3(2 * num_sms), dim3(kMoveThreads), 0, st, 0u, a);
   if (e != cudaSuccess || a.n == 0) return e;
   int64_t rows = 0;

@@ -158,15 +158,17 @@ def pages_compact(pool, tables, pages, out=None, in_place=False, stream=None):
     _want(len(out["tables"]) == n, "out: as many tables are wanted")
     packed = b""
     for i, (t, held, to) in enumerate(zip(tables, pages, out["tables"])):
-        B = t.shape[0]
-        _table("tables[%d]" % i, t, B, index), _table("out tables[%d]" % i, to, B, index)
-        _want(to.shape == t.shape, "out tables[%d]: the table's shape is wanted" % i)
-        packed += _pack_lists(t.data_ptr(), t.stride(0), t.shape[1], _ints("pages[%d]" % i, held, B, index), to.data_ptr(),
-                              to.stride(0), B)
+        shape, ts, os = t.shape, t.stride(), to.stride()
+        if (t.dtype is not _INT or to.dtype is not _INT or t.get_device() != index or to.get_device() != index or len(shape) != 2
+                or to.shape != shape or (shape[1] > 1 and not ts[1] == os[1] == 1)):
+            raise ValueError("tables[%d]: int32 tensors [B, pages] of one shape on cuda:%d are wanted, the new one too" % (i, index))
+        B, width = shape
+        packed += _pack_lists(t.data_ptr(), ts[0], width, _ints("pages", held, B, index), to.data_ptr(), os[0], B)
     refs, ids = _ints("refs", out["refs"], P, index), _ints("new_id", out["new_id"], P, index)
     src, dst = out["move_src"], out["move_dst"]
-    _want(src.shape[0] >= P // 2 and dst.shape[0] >= P // 2, "move_src and move_dst: half the pool's pages of room are wanted")
-    a, b = _ints("move_src", src, src.shape[0], index), _ints("move_dst", dst, dst.shape[0], index)
+    room, room_dst = src.numel(), dst.numel()
+    _want(room >= P // 2 and room_dst >= P // 2, "move_src and move_dst: half the pool's pages of room are wanted")
+    a, b = _ints("move_src", src, room, index), _ints("move_dst", dst, room_dst, index)
     count, st = _ints("moved", out["moved"], 1, index), _ints("status", out["status"], n, index)
     _check(_lib.tsv_pages_compact(_handle(index), pool.at, refs, packed or None, n, ids, a, b, count, st, _on(stream, index)),
            "tsv_pages_compact")
