@@ -65,11 +65,26 @@ struct CUnit {
   __device__ __forceinline__ bool whole() const { return j == first && j1 == end; }
 };
 
+// n / d of 0 <= n < 2^31 by a product: with 2^l >= d, m = 2^(31 + l) / d rounded up is
+// too large by less than d / d <= 2^l / d, which n x does not carry to the next quotient.
+struct Divisor {
+  uint32_t m;
+  int shift;
+  explicit Divisor(int d) {
+    int l = 0;
+    while (((int64_t)1 << l) < d) ++l;
+    shift = 31 + l;
+    m = (uint32_t)((((uint64_t)1 << shift) + d - 1) / d);
+  }
+  __device__ __forceinline__ int of(int n) const { return (int)(((uint64_t)(uint32_t)n * m) >> shift); }
+};
+
 struct ChunkGeometry {
-  int G, R, window;
+  Divisor by_heads;  // query heads of a KV head
+  int R, window;
   // Blocks that rows r0 .. r1 of request (start) see: first, end.
   __device__ __forceinline__ int2 blocks(int start, int r0, int r1) const {
-    const int p0 = start + r0 / G, p1 = start + r1 / G;
+    const int p0 = start + by_heads.of(r0), p1 = start + by_heads.of(r1);
     const int lo = window > 0 ? max(0, p0 - window + 1) : 0;
     return make_int2(lo / kPBlock, p1 / kPBlock + 1);
   }
@@ -144,6 +159,17 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
+// Two fp16 values -> two e4m3 codes, nearest even; the difference of fp16 pairs.
+__device__ __forceinline__ uint32_t e4m3x2_of_f16x2(uint32_t v) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(v));
+  return r;
+}
+__device__ __forceinline__ uint32_t f16x2_minus(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("sub.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
 // Bytes that are NaN codes, as their top bits.
 __device__ __forceinline__ uint32_t nan_bytes(uint32_t w) { return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u; }
 __device__ __forceinline__ uint32_t bits_below(int n) { return n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1u; }
@@ -170,7 +196,7 @@ __device__ __forceinline__ void cwait(uint64_t* bar, uint32_t parity, volatile i
 template <int D>
 __global__ void __launch_bounds__(kCThreads, 1)
     paged_chunk_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
-                       const __grid_constant__ PagedAttnArgs a, int R, int32_t* timeouts, ChunkPart* __restrict__ parts,
+                       const __grid_constant__ PagedAttnArgs a, const ChunkGeometry geo, int32_t* timeouts, ChunkPart* __restrict__ parts,
                        float* __restrict__ part_o, float* __restrict__ part_ml) {
   using C = CCfg<D>;
   extern __shared__ uint8_t smem_raw[];
@@ -205,7 +231,7 @@ __global__ void __launch_bounds__(kCThreads, 1)
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int lps = __ffs(a.cache.page_size) - 1;  // pages are powers of two
-  const ChunkGeometry geo{a.G, R, a.window};
+  const int R = geo.R;
   const int Hkv = a.cache.Hkv;
   bool dead = false;
 
@@ -244,7 +270,7 @@ __global__ void __launch_bounds__(kCThreads, 1)
     int before = 0;
     if (lane == 0) sTiles[0] = 0;
 #pragma unroll 1
-    for (int b0 = 0; b0 < TSV_MAX_BATCH; b0 += 32) {
+    for (int b0 = 0; b0 < a.B; b0 += 32) {
       const int b = b0 + lane;
       int tiles = 0;
       PagedRequest r;
@@ -277,7 +303,7 @@ __global__ void __launch_bounds__(kCThreads, 1)
     const int r0 = tile * R, r1 = (int)(min((int64_t)r0 + R, (int64_t)q.y * a.G) - 1);
     return geo.blocks(q.z, r0, r1);
   };
-  const int all_tiles = sTiles[TSV_MAX_BATCH];
+  const int all_tiles = sTiles[(a.B + 31) & ~31];
   const int share = (all_tiles + kCThreads - 1) / kCThreads, f_lo = min(all_tiles, tid * share), f_hi = min(all_tiles, f_lo + share);
   int64_t mine = 0;
   for (int f = f_lo, b = f < f_hi ? request_of(f) : 0; f < f_hi; ++f) {
@@ -293,17 +319,21 @@ __global__ void __launch_bounds__(kCThreads, 1)
   }
   if (lane == 31) sPre[warp + 1] = upto;
   __syncthreads();
-  int64_t begin = upto - mine, total = 0;
-#pragma unroll 1
-  for (int w = 0; w < kCThreads / 32; ++w) {
-    if (w < warp) begin += sPre[w + 1];
-    total += sPre[w + 1];
+  int64_t begin = upto - mine, total = lane < kCThreads / 32 ? sPre[lane + 1] : 0;
+#pragma unroll
+  for (int o = 1; o < kCThreads / 32; o <<= 1) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, total, o);
+    if (lane >= o) total += y;
   }
+  if (warp > 0) begin += __shfl_sync(0xffffffffu, total, warp - 1);
+  total = __shfl_sync(0xffffffffu, total, kCThreads / 32 - 1);
   begin *= Hkv;
   total *= Hkv;
   {
     const int64_t ctas = gridDim.x;
-    const int64_t x[2] = {total * blockIdx.x / ctas, total * (blockIdx.x + 1) / ctas};
+    const bool small = total < (1 << 21);  // 32-bit products and quotients (at most 1024 CTAs)
+    const int64_t x[2] = {small ? (uint32_t)total * blockIdx.x / gridDim.x : total * blockIdx.x / ctas,
+                          small ? (uint32_t)total * (blockIdx.x + 1) / gridDim.x : total * (blockIdx.x + 1) / ctas};
 #pragma unroll 1
     for (int e = 0; e < 2; ++e) {
       if (mine == 0 || x[e] < begin || x[e] >= begin + mine * Hkv) continue;
@@ -317,7 +347,7 @@ __global__ void __launch_bounds__(kCThreads, 1)
         t = tile_blocks(b, f - sTiles[b]);
       }
       const int T = t.y - t.x;
-      int g = (int)((x[e] - at) / (T + kUnitCost));
+      int g = small ? (int)((uint32_t)(x[e] - at) / (uint32_t)(T + kUnitCost)) : (int)((x[e] - at) / (T + kUnitCost));
       int j = max(0, (int)(x[e] - at - (int64_t)g * (T + kUnitCost)) - kUnitCost);
       // Short units stay whole, and no part is short.
       if (T < kLeastCut) j = 2 * j < T ? 0 : T;
@@ -396,33 +426,10 @@ __global__ void __launch_bounds__(kCThreads, 1)
   };
   // The blocks whose keys rows r0 .. r1 of the unit see all: from .x up to .y.
   auto full_range = [&](const CUnit& u, int r0, int r1) {
-    const int p0 = u.start + (u.row0 + r0) / a.G, p1 = u.start + (u.row0 + r1) / a.G;
+    const int p0 = u.start + geo.by_heads.of(u.row0 + r0), p1 = u.start + geo.by_heads.of(u.row0 + r1);
     return make_int2(a.window > 0 ? (max(p1 - a.window, -1) + kPBlock) / kPBlock : 0, (p0 + 1) / kPBlock);
   };
   CUnit u{};
-
-  if (warp == 0) {  // what the joining launch has to know
-    CUnit v{};
-    const bool any = first_unit(v);
-    ChunkPart p{};
-    p.empty = any ? 0 : 1;
-    if (any) {
-      p.cont = v.j > v.first;
-      p.through = p.cont && v.j1 < v.end;
-      if (to.j > 0 && !(from.f == to.f && from.g == to.g && from.j > 0)) {  // the last unit begins a group
-        p.lead = 1;
-        v.b = request_of(to.f);
-        v.tile = to.f - sTiles[v.b];
-        v.g = to.g;
-        load_unit(v, to.f);
-        p.off = v.off;
-        p.row0 = v.row0;
-        p.rows = v.rows;
-        p.g = v.g;
-      }
-    }
-    if (lane == 0) parts[blockIdx.x] = p;
-  }
 
   if (warp < kCConvWarp) {
     // ---------------------------------------------------------- softmax: a thread owns a row
@@ -433,10 +440,10 @@ __global__ void __launch_bounds__(kCThreads, 1)
     const uint32_t o_col = tmem + lane_base + C::kColO + (uint32_t)(tile * D);
     // The warp's rows of q, as two e4m3 terms each.
     auto bring_q = [&](const CUnit& v) {
-      constexpr int kLanes = D / 8, kRows = 32 / kLanes, kPasses = 32 / kRows, kBatch = 8;
+      constexpr int kLanes = D / 8, kRows = 32 / kLanes, kPasses = 32 / kRows, kBatch = 4;
       int64_t at = -1;
       if (row < v.rows) {
-        const int gr = v.row0 + row, token = gr / a.G;
+        const int gr = v.row0 + row, token = geo.by_heads.of(gr);
         at = (int64_t)(v.off + token) * a.qs_n + (int64_t)(v.g * a.G + (gr - token * a.G)) * a.qs_h;
       }
       const int part = lane % kLanes, sub = lane / kLanes;
@@ -453,20 +460,21 @@ __global__ void __launch_bounds__(kCThreads, 1)
         for (int i = 0; i < kBatch; ++i) {
           const int rr = (p0 + i) * kRows + sub;  // of the warp
           const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
-          uint32_t top = 0u;
+          // The row's largest value, two at a time: bf16 without sign as whole numbers.
+          uint32_t two = __vmaxu2(__vmaxu2(w[0] & 0x7FFF7FFFu, w[1] & 0x7FFF7FFFu), __vmaxu2(w[2] & 0x7FFF7FFFu, w[3] & 0x7FFF7FFFu));
 #pragma unroll
-          for (int e = 0; e < 4; ++e) top = max(top, max((w[e] << 16) & 0x7FFF0000u, w[e] & 0x7FFF0000u));
-#pragma unroll
-          for (int o = 1; o < kLanes; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+          for (int o = 1; o < kLanes; o <<= 1) two = __vmaxu2(two, __shfl_xor_sync(0xffffffffu, two, o));
+          const uint32_t top = max(two & 0xFFFFu, two >> 16) << 16;
           const bool fine = top < 0x7F800000u;  // a row with an infinity or a NaN is NaN throughout (its scores are)
           const int up = top == 0u ? 0 : max(-120, min(120, 134 - (int)(top >> 23)));
           const float mul = __uint_as_float((uint32_t)(127 + up) << 23);
           uint32_t hi[2], lo[2];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const float x0 = __uint_as_float(w[e] << 16) * mul, x1 = __uint_as_float(w[e] & 0xFFFF0000u) * mul;
-            const uint32_t h = e4m3x2(x0, x1), b2 = f16x2_of_e4m3x2(h);
-            const uint32_t l = e4m3x2(x0 - f16_lo(b2), x1 - f16_hi(b2));
+            // fp16 holds a bf16 under 2^8 down to 2^-17 of the row's largest, and what
+            // e4m3 leaves of it.
+            const uint32_t x2 = pack_f16(__uint_as_float(w[e] << 16) * mul, __uint_as_float(w[e] & 0xFFFF0000u) * mul);
+            const uint32_t h = e4m3x2_of_f16x2(x2), l = e4m3x2_of_f16x2(f16x2_minus(x2, f16x2_of_e4m3x2(h)));
             if (e & 1) {
               hi[e >> 1] |= h << 16;
               lo[e >> 1] |= l << 16;
@@ -498,7 +506,7 @@ __global__ void __launch_bounds__(kCThreads, 1)
       const int2 range = tile_range(u, tile);
       const bool active = tile * kTileRows < u.rows;
       const float fr = sFr[row];
-      const int pos = u.start + (u.row0 + min(row, u.rows - 1)) / a.G;
+      const int pos = u.start + geo.by_heads.of(u.row0 + min(row, u.rows - 1));
       float m_ref = -INFINITY, l = 0.f, v_ref = 0.f;
       int room = kFarApart;  // how far the reference may still be lowered
       // P of 64 keys out of their scores.
@@ -630,13 +638,13 @@ __global__ void __launch_bounds__(kCThreads, 1)
         if (range.x < range.y) TSV_CWAIT(&pv_done[2 * tile + 1], cnt - 1);
         if (dead) break;
         tc_fence_after();
-        const int gr = now.row0 + row, token = gr / a.G;
+        const int gr = now.row0 + row, token = geo.by_heads.of(gr);
         // Columns of a row whose NaN codes were kept out of the product.
         uint32_t bad[D / 32];
 #pragma unroll
         for (int q = 0; q < D / 32; ++q) bad[q] = 0u;
-        if (row < now.rows) {
-          const uint32_t* nan = sNan + (units & 1) * (kNanSlots * 4);
+        const uint32_t* nan = sNan + (units & 1) * (kNanSlots * 4);
+        if (__any_sync(0xffffffffu, lane < kNanSlots * 4 && nan[lane] != 0u) && row < now.rows) {
 #pragma unroll 1
           for (int w = 0; w < kNanSlots * 4; ++w) {
             const int slot = w >> 2, jb = slot < 3 ? now.first + slot : now.end - 1 - (slot - 3);
@@ -736,7 +744,7 @@ __global__ void __launch_bounds__(kCThreads, 1)
         dead = named_bar_or(kBarConv, 128, dead);
         if (dead) break;
         const int2 full = full_range(u, 0, u.rows - 1);
-        const int keys = u.start + min(u.n, (u.row0 + u.rows - 1) / a.G + 1);  // behind the last one that a row sees
+        const int keys = u.start + min(u.n, geo.by_heads.of(u.row0 + u.rows - 1) + 1);  // behind the last one that a row sees
 #pragma unroll 1
         for (int j = u.j; j < u.j1; ++j) {
           const int x = t + j - u.j, st = x & 1, valid = keys - j * kPBlock;
@@ -811,6 +819,28 @@ __global__ void __launch_bounds__(kCThreads, 1)
       // The whole warp waits, one thread issues: behind elect.sync the compiler knows
       // that it is one, and the operands stay in uniform registers (behind a test of
       // the lane a long chunk took 1.13 times as long).
+      if (q == 1) {  // what the joining launch has to know
+        CUnit v{};
+        const bool any = first_unit(v);
+        ChunkPart p{};
+        p.empty = any ? 0 : 1;
+        if (any) {
+          p.cont = v.j > v.first;
+          p.through = p.cont && v.j1 < v.end;
+          if (to.j > 0 && !(from.f == to.f && from.g == to.g && from.j > 0)) {  // the last unit begins a group
+            p.lead = 1;
+            v.b = request_of(to.f);
+            v.tile = to.f - sTiles[v.b];
+            v.g = to.g;
+            load_unit(v, to.f);
+            p.off = v.off;
+            p.row0 = v.row0;
+            p.rows = v.rows;
+            p.g = v.g;
+          }
+        }
+        if (lane == 0) parts[blockIdx.x] = p;
+      }
       int t = 0, cnt = 0, mine_units = 0;
       for (bool going = first_unit(u); going && !dead; going = next_unit(u)) {
         const int2 range = tile_range(u, q);
@@ -896,7 +926,7 @@ __global__ void __launch_bounds__(kCThreads, 1)
       int t = 0, asked = 0;
       for (bool going = first_unit(u); going && !dead; going = next_unit(u)) {
         const int32_t* ids = a.table.ids_d + (int64_t)u.b * a.table.stride;
-        const int keys = u.start + min(u.n, (u.row0 + u.rows - 1) / a.G + 1);
+        const int keys = u.start + min(u.n, geo.by_heads.of(u.row0 + u.rows - 1) + 1);
         const int page_end = (keys + (1 << lps) - 1) >> lps;
         // Lane p holds page p of the next block (of V's producer: of the next two), lanes
         // 0 .. 7 the next block's scales of 16 keys each: asked for a block ahead.
@@ -1054,7 +1084,8 @@ cudaError_t launch_typed(const CUtensorMap& tk, const CUtensorMap& tv, const Pag
   const int64_t tiles = ((int64_t)a.N * a.G + 255) / 256 * a.cache.Hkv;
   const int R = tiles >= num_sms ? 256 : 128;
   const cudaError_t e =
-      launch_pdl(paged_chunk_kernel<D>, dim3(num_sms), dim3(kCThreads), (size_t)CCfg<D>::kSmem, st, 0u, tk, tv, a, R, timeouts, parts, po, pm);
+      launch_pdl(paged_chunk_kernel<D>, dim3(num_sms), dim3(kCThreads), (size_t)CCfg<D>::kSmem, st, 0u, tk, tv, a,
+                 ChunkGeometry{Divisor(a.G), R, a.window}, timeouts, parts, po, pm);
   if (e != cudaSuccess) return e;
   return launch_pdl(paged_chunk_join_kernel<D>, dim3(num_sms * kJoinParts > a.B ? num_sms * kJoinParts : a.B), dim3(kJoinThreads), 0, st, 0u,
                     a, num_sms, timeouts, parts, po, pm);
