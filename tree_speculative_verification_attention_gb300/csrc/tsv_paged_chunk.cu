@@ -756,7 +756,7 @@ __global__ void __launch_bounds__(kCThreads, 1)
           const bool plain = sc[33] != 0.f;
           const bool masked = j < full.x || j >= full.y;
           const int slot = j - u.first < 3 ? j - u.first : u.end - 1 - j < 3 ? 3 + u.end - 1 - j : 0;
-#pragma unroll
+#pragma unroll 1
           for (int h = 0; h < kParts; h += 4) {
             uint4 codes[4];
 #pragma unroll
@@ -819,28 +819,6 @@ __global__ void __launch_bounds__(kCThreads, 1)
       // The whole warp waits, one thread issues: behind elect.sync the compiler knows
       // that it is one, and the operands stay in uniform registers (behind a test of
       // the lane a long chunk took 1.13 times as long).
-      if (q == 1) {  // what the joining launch has to know
-        CUnit v{};
-        const bool any = first_unit(v);
-        ChunkPart p{};
-        p.empty = any ? 0 : 1;
-        if (any) {
-          p.cont = v.j > v.first;
-          p.through = p.cont && v.j1 < v.end;
-          if (to.j > 0 && !(from.f == to.f && from.g == to.g && from.j > 0)) {  // the last unit begins a group
-            p.lead = 1;
-            v.b = request_of(to.f);
-            v.tile = to.f - sTiles[v.b];
-            v.g = to.g;
-            load_unit(v, to.f);
-            p.off = v.off;
-            p.row0 = v.row0;
-            p.rows = v.rows;
-            p.g = v.g;
-          }
-        }
-        if (lane == 0) parts[blockIdx.x] = p;
-      }
       int t = 0, cnt = 0, mine_units = 0;
       for (bool going = first_unit(u); going && !dead; going = next_unit(u)) {
         const int2 range = tile_range(u, q);
@@ -882,14 +860,14 @@ __global__ void __launch_bounds__(kCThreads, 1)
 #pragma unroll 1
         for (int j = u.j; j < range.x && !dead; ++j) skip(j);
         if (range.x < range.y && !dead) {
-          issue_s(range.x, 0);
-          issue_s(range.x, 1);
+#pragma unroll 1
+          for (int half = 0; half < 2; ++half) issue_s(range.x, half);
         }
 #pragma unroll 1
         for (int j = range.x; j < range.y && !dead; ++j) {
           const int x = t + j - u.j;
           TSV_CWAIT(&v_full[x & 1], x >> 1);
-#pragma unroll
+#pragma unroll 1
           for (int half = 0; half < 2; ++half) {
             TSV_CWAIT(&p_full[2 * q + half], cnt);
             if (dead) break;
@@ -1001,6 +979,28 @@ __global__ void __launch_bounds__(kCThreads, 1)
       for (int x = max(0, asked - stages); x < asked; ++x)
         mbar_wait(is_v ? &raw_full[x & 1] : &k_full[x % kKStages], (x / stages) & 1, nullptr);
     }
+  }
+  if (warp == kCMmaWarp + 1) {  // what the joining launch has to know
+    CUnit v{};
+    const bool any = first_unit(v);
+    ChunkPart p{};
+    p.empty = any ? 0 : 1;
+    if (any) {
+      p.cont = v.j > v.first;
+      p.through = p.cont && v.j1 < v.end;
+      if (to.j > 0 && !(from.f == to.f && from.g == to.g && from.j > 0)) {  // the last unit begins a group
+        p.lead = 1;
+        v.b = request_of(to.f);
+        v.tile = to.f - sTiles[v.b];
+        v.g = to.g;
+        load_unit(v, to.f);
+        p.off = v.off;
+        p.row0 = v.row0;
+        p.rows = v.rows;
+        p.g = v.g;
+      }
+    }
+    if (lane == 0) parts[blockIdx.x] = p;
   }
   __syncwarp();
   tc_fence_before();
