@@ -49,7 +49,7 @@ constexpr float kRise = 4.f;    // log2: how far a score may pass the reference 
 constexpr float kUp = 11.f;     // log2 of P's factor: 2^4 x 2^11 is within fp16
 constexpr int kFarApart = 40;   // log2: V scales that far apart leave a row's weights their bits
 // What a unit costs beside its blocks, in blocks; and how near to a unit's end a cut may come.
-constexpr int kUnitCost = 3, kLeastCut = 8, kNearEnd = 3;
+constexpr int kUnitCost = 5, kLeastCut = 6, kNearEnd = 2;
 constexpr uint32_t kCWaitTries = 1u << 22;  // (of a microsecond or less each)
 constexpr int kBarConv = 1;
 constexpr int kScaleRow = 36;   // of a block, per 16 keys: K's scale, e and 2^-e and m of V's relative scale m 2^e; V's largest scale, whether every m is 1
@@ -440,7 +440,7 @@ __global__ void __launch_bounds__(kCThreads, 1)
     const uint32_t o_col = tmem + lane_base + C::kColO + (uint32_t)(tile * D);
     // The warp's rows of q, as two e4m3 terms each.
     auto bring_q = [&](const CUnit& v) {
-      constexpr int kLanes = D / 8, kRows = 32 / kLanes, kPasses = 32 / kRows, kBatch = 4;
+      constexpr int kLanes = D / 8, kRows = 32 / kLanes, kPasses = 32 / kRows, kBatch = 8;
       int64_t at = -1;
       if (row < v.rows) {
         const int gr = v.row0 + row, token = geo.by_heads.of(gr);
@@ -757,17 +757,17 @@ __global__ void __launch_bounds__(kCThreads, 1)
           const bool masked = j < full.x || j >= full.y;
           const int slot = j - u.first < 3 ? j - u.first : u.end - 1 - j < 3 ? 3 + u.end - 1 - j : 0;
 #pragma unroll 1
-          for (int h = 0; h < kParts; h += 4) {
-            uint4 codes[4];
+          for (int h = 0; h < kParts; h += 2) {
+            uint4 codes[2];
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
+            for (int q = 0; q < 2; ++q) {
               const int key = first_row + (h + q) * kStep;
               codes[q] = make_uint4(0u, 0u, 0u, 0u);
               if (key < valid) codes[q] = *reinterpret_cast<const uint4*>(sRaw + st * C::kKTile + swizzled<D>(key, chunk));
             }
             if (masked) {
 #pragma unroll
-              for (int q = 0; q < 4; ++q) {
+              for (int q = 0; q < 2; ++q) {
                 uint32_t* v = reinterpret_cast<uint32_t*>(&codes[q]);
                 uint32_t any = 0u;
 #pragma unroll
@@ -781,7 +781,7 @@ __global__ void __launch_bounds__(kCThreads, 1)
               }
             }
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
+            for (int q = 0; q < 2; ++q) {
               const int key = first_row + (h + q) * kStep;
               const uint4 c = codes[q];
               uint8_t* to_row = sV + st * C::kVTile + (chunk >> 2) * (kPBlock * 128) + key * 128;
@@ -1080,9 +1080,14 @@ cudaError_t launch_typed(const CUtensorMap& tk, const CUtensorMap& tv, const Pag
   ChunkPart* parts = reinterpret_cast<ChunkPart*>(w + lay.parts);
   float* po = reinterpret_cast<float*>(w + lay.part_o);
   float* pm = reinterpret_cast<float*>(w + lay.part_ml);
-  // Units of 256 rows share a block's cost; with fewer of them than SMs, 128 each.
-  const int64_t tiles = ((int64_t)a.N * a.G + 255) / 256 * a.cache.Hkv;
-  const int R = tiles >= num_sms ? 256 : 128;
+  // Rows of a unit.  The second tile of 256 rows costs a block hardly more, but few
+  // units leave SMs idle, unless they are long enough to be cut.  Measured (us; 32
+  // query heads on 8, D = 128), 128 / 256 rows: 512 tokens from the start (64 units of
+  // 256) 23.6 / 26.5, 1024 (128 units) 51 / 38; behind 8000 tokens 64 tokens (8 units)
+  // 44 / 51, 128 54 / 51, 256 78 / 63.
+  const int64_t rows = (int64_t)a.max_nodes * a.G, tiles = ((int64_t)a.N * a.G + 255) / 256 * a.cache.Hkv;
+  const int64_t keys = (int64_t)a.table.pages * a.cache.page_size;
+  const int R = 2 * tiles >= num_sms || (rows > 512 && keys >= 4096) ? 256 : 128;
   const cudaError_t e =
       launch_pdl(paged_chunk_kernel<D>, dim3(num_sms), dim3(kCThreads), (size_t)CCfg<D>::kSmem, st, 0u, tk, tv, a,
                  ChunkGeometry{Divisor(a.G), R, a.window}, timeouts, parts, po, pm);
