@@ -300,8 +300,9 @@ struct PagedAttnArgs {
   float scale;
   // tsv_paged_chunk_attention: the nodes are the prefix pages' rows prefix_len ..
   // prefix_len + n - 1 themselves, and each sees the rows up to its own
-  // (window > 0: the last `window` of them).
-  int32_t chunk, window;
+  // (window > 0: the last `window` of them).  Requests of fewer than `least` new
+  // rows are another launch's.
+  int32_t chunk, window, least;
 };
 // Tensor-core kernel: row tiles of R = 16, 32 or 64 query rows; its workspace
 // holds one word per request (set by a CTA that gave up a wait for it), one
@@ -364,6 +365,14 @@ inline PagedChunkLayout paged_chunk_layout(int grid, int32_t D) {
   return l;
 }
 cudaError_t paged_chunk_set_attributes(int32_t D);
+// Whether requests of one token go to the tree attention's kernel, in a launch of
+// its own: 28 of them beside 4 prompts, 32 heads on 8, take 327 us in one launch and
+// 289 in two, but a batch without any pays 6 to 7 us for the second.  Far fewer rows
+// than as many requests of the longest would have tell that most are short.
+constexpr int32_t kChunkApart = 16;
+inline bool paged_chunk_apart(int32_t B, int32_t N, int32_t max_rows) {
+  return B >= kChunkApart && 3 * (int64_t)N <= (int64_t)B * max_rows;
+}
 cudaError_t launch_paged_chunk(const CUtensorMap& tk, const CUtensorMap& tv, const PagedAttnArgs& a, int num_sms, void* ws,
                                cudaStream_t st);
 cudaError_t paged_chunk_f32_set_attributes(int32_t D);

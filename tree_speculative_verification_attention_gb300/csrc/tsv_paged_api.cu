@@ -347,7 +347,7 @@ tsv_status tsv_paged_chunk_attention_workspace_size(tsv_handle h, tsv_dtype dtyp
   if (!bytes || N < 0) return TSV_ERR_INVALID_ARG;
   const tsv_status st = check_attention(h, dtype, cache, &c, B, max_rows, INT32_MAX, Hq, flags);
   if (st != TSV_OK) return st;
-  const bool one = max_rows == 1;  // (without a window a kernel of the tree attention takes single tokens)
+  const bool one = max_rows == 1 || B >= kChunkApart;  // (without a window a kernel of the tree attention takes single tokens)
   *bytes = !paged_uses_tc(dtype, flags) ? 0
            : std::max(paged_chunk_layout(h->num_sms, c.D).total,
                       one ? paged_attn_layout(h->num_sms, chunk_token_rows(Hq / c.Hkv, B, c), c.D).total : 0);
@@ -370,10 +370,11 @@ tsv_status tsv_paged_chunk_attention(tsv_handle h, tsv_dtype dtype, const void* 
     return TSV_ERR_INVALID_ARG;
   if ((int64_t)N * Hq > INT32_MAX) return TSV_ERR_UNSUPPORTED;
   const bool use_tc = paged_uses_tc(dtype, flags), by_chunks = use_tc && (max_rows > 1 || window > 0);
-  const int32_t R = by_chunks ? 0 : chunk_token_rows(Hq / a.cache.Hkv, B, a.cache);
+  const bool by_tokens = use_tc && (!by_chunks || (window == 0 && paged_chunk_apart(B, N, max_rows)));
+  const int32_t R = chunk_token_rows(Hq / a.cache.Hkv, B, a.cache);
   if (use_tc && (!workspace_d || !aligned16(workspace_d) ||
-                 workspace_bytes < (by_chunks ? paged_chunk_layout(h->num_sms, a.cache.D).total
-                                              : paged_attn_layout(h->num_sms, R, a.cache.D).total)))
+                 workspace_bytes < std::max(by_chunks ? paged_chunk_layout(h->num_sms, a.cache.D).total : 0,
+                                            by_tokens ? paged_attn_layout(h->num_sms, R, a.cache.D).total : 0)))
     return TSV_ERR_INVALID_ARG;
   const DeviceScope scope(h->device);
   if (!scope.ok) return TSV_ERR_CUDA;
@@ -393,7 +394,16 @@ tsv_status tsv_paged_chunk_attention(tsv_handle h, tsv_dtype dtype, const void* 
   a.scale = scale == 0.f ? 1.f / sqrtf((float)a.cache.D) : scale;
   a.chunk = 1;
   a.window = window;
-  if (use_tc && !by_chunks) return launch_tree_kernels(h, a, R, workspace_d, static_cast<cudaStream_t>(stream));
+  a.least = 1;
+  if (by_tokens) {
+    // Requests of more rows do not fit this launch's most: they are passed over, and
+    // their status is the joining launch's.
+    PagedAttnArgs tokens = a;
+    tokens.max_nodes = 1;
+    st = launch_tree_kernels(h, tokens, R, workspace_d, static_cast<cudaStream_t>(stream));
+    if (st != TSV_OK || !by_chunks) return st;
+    a.least = 2;
+  }
   if (by_chunks) {
     const uint32_t bit = a.cache.D == 128 ? 2u : 1u;
     if (!(h->chunk_attr_mask & bit)) {

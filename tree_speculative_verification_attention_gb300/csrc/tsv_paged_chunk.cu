@@ -274,7 +274,7 @@ __global__ void __launch_bounds__(kCThreads, 1)
       const int b = b0 + lane;
       int tiles = 0;
       PagedRequest r;
-      if (b < a.B && paged_request(a, b, &r) && r.n > 0) {
+      if (b < a.B && paged_request(a, b, &r) && r.n >= a.least) {
         tiles = (int)(((int64_t)r.n * a.G + R - 1) / R);
         sReq[b] = make_int4(r.off, r.n, r.P - r.n, tiles);
       }
