@@ -254,6 +254,17 @@ tsv_status tsv_paged_chunk_attention_workspace_size(tsv_handle h, tsv_dtype dtyp
  * only the rows that see it.  Values of V (code x scale) are 2^127 at most over
  * the number of keys that a row sees, so that sums before the division are
  * finite.
+ *   Which kernel runs follows from dtype, flags, the shapes and `window` alone
+ * (requests of one token may be a launch of their own beside longer ones).  The
+ * same call gives the same bits again; other requests in the batch, max_rows or a
+ * wider table can change the last ones.
+ *   Accuracy.  Scores and sums are fp32.  bf16: a weight is rounded to 2^-12 of
+ * itself (fp16) or 2^-36 of the row's largest, where V scales that lie apart count
+ * in what is largest, up to 2^40; V by a scale that is no power of two to 2^-12 of
+ * itself; q is held to 2^-17 of its row's largest value.  Requests of one token:
+ * as tsv_paged_tree_attention does few rows.  fp32: q and the weights are held to
+ * 2^-22 of themselves, 2^-38 of the largest of a row of q and of the weights of 16
+ * keys.
  */
 tsv_status tsv_paged_chunk_attention(tsv_handle h, tsv_dtype dtype, const void* q_d, int64_t q_stride_n, int64_t q_stride_h,
                                      const tsv_paged_cache* cache, const tsv_page_table* table, const int32_t* start_d,

@@ -21,7 +21,8 @@
  *
  * Counts that do not add up (a page on more lists than it counts) never reach a
  * page outside the pool, but some list that gives such a page back is reported
- * with TSV_ERR_INVALID_ARG after it was shortened.
+ * with TSV_ERR_INVALID_ARG after the fact: a resize has shortened it, a fork has
+ * left it empty (unchanged, if the page was free before the list was looked at).
  *
  * A list is a row of a page table with a count beside it: pages_d[b] entries of
  * row b are held.  Entries behind them are never read, and keep what they hold

@@ -332,8 +332,8 @@ inline int32_t paged_attn_rows(int64_t rows, int64_t groups, int64_t keys) {
 struct PagedAttnLayout {
   size_t part_o, part_ml, total;
 };
-inline PagedAttnLayout paged_attn_layout(int grid, int32_t R, int32_t D) {
-  PagedAttnLayout l;
+constexpr PagedAttnLayout paged_attn_layout(int grid, int32_t R, int32_t D) {
+  PagedAttnLayout l{};
   l.part_o = ((size_t)(TSV_MAX_BATCH + grid) * 4 + 255) & ~(size_t)255;
   l.part_ml = l.part_o + (size_t)grid * 2 * R * D * 4;
   l.total = l.part_ml + (size_t)grid * 2 * 2 * R * 4;
@@ -356,14 +356,15 @@ constexpr size_t kPagedChunkPartBytes = 32;
 struct PagedChunkLayout {
   size_t parts, part_o, part_ml, total;
 };
-inline PagedChunkLayout paged_chunk_layout(int grid, int32_t D) {
-  PagedChunkLayout l;
+constexpr PagedChunkLayout paged_chunk_layout(int grid, int32_t D) {
+  PagedChunkLayout l{};
   l.parts = ((size_t)(TSV_MAX_BATCH + grid) * 4 + 255) & ~(size_t)255;
   l.part_o = (l.parts + (size_t)grid * kPagedChunkPartBytes + 255) & ~(size_t)255;
   l.part_ml = l.part_o + (size_t)grid * 2 * kPagedWideRows * D * 4;
   l.total = l.part_ml + (size_t)grid * 2 * 2 * kPagedWideRows * 4;
   return l;
 }
+static_assert(paged_attn_layout(152, kPagedWideRows, 128).total <= paged_chunk_layout(152, 128).total, "one workspace serves both");
 cudaError_t paged_chunk_set_attributes(int32_t D);
 // Whether requests of one token go to the tree attention's kernel, in a launch of
 // its own: 28 of them beside 4 prompts, 32 heads on 8, take 327 us in one launch and

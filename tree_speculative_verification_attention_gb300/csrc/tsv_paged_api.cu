@@ -347,10 +347,7 @@ tsv_status tsv_paged_chunk_attention_workspace_size(tsv_handle h, tsv_dtype dtyp
   if (!bytes || N < 0) return TSV_ERR_INVALID_ARG;
   const tsv_status st = check_attention(h, dtype, cache, &c, B, max_rows, INT32_MAX, Hq, flags);
   if (st != TSV_OK) return st;
-  const bool one = max_rows == 1 || B >= kChunkApart;  // (without a window a kernel of the tree attention takes single tokens)
-  *bytes = !paged_uses_tc(dtype, flags) ? 0
-           : std::max(paged_chunk_layout(h->num_sms, c.D).total,
-                      one ? paged_attn_layout(h->num_sms, chunk_token_rows(Hq / c.Hkv, B, c), c.D).total : 0);
+  *bytes = paged_uses_tc(dtype, flags) ? paged_chunk_layout(h->num_sms, c.D).total : 0;  // (more than single tokens want)
   return TSV_OK;
 }
 

@@ -11,10 +11,11 @@
 // its largest value to [128, 256): a bf16's 8 bits exactly down to 2^-17 of it,
 // at the price of one fp16 product, since e4m3 products run at twice the rate.
 // V is widened to fp16 (exactly) so that P keeps fp16's 11 bits: P is 2^11 p
-// times the V scale of its page relative to the unit's largest so far, p <= 2^4
-// below a reference maximum that moves only when a score passes it by that much.
-// A V scale that is a power of two goes into the exponent of p and out of the
-// row's sum again (a factor per 16 keys), others are a product of their own.
+// times 2^e of the V scale of its page relative to the unit's largest so far,
+// m 2^e, p <= 2^4 below a reference maximum that moves only when a score passes it
+// by that much.  2^e is part of the exponent of p and goes out of the row's sum
+// again (a factor per 16 keys); m, 1 for scales that are powers of two, goes into V
+// as it is widened.
 //
 // Work.  Units of up to 256 rows (two tiles) of a KV head and the 128-key blocks
 // that any of their rows sees form one list, which is cut into equal ranges, one
@@ -26,9 +27,22 @@
 //   0-7    softmax, a thread per row (0-3 tile 0, 4-7 tile 1): they bring their
 //          tile's next Q in before they wait for the last product
 //   8-11   widening of V, and NaN codes of blocks with masked keys taken out
-//   12, 13 MMA issuers of the tiles: S of a block goes out behind PV of the one
-//          before it, so one tile's products run under the other's softmax
+//   12, 13 MMA issuers of the tiles.  A tile's scores are two buffers of 64 keys, and
+//          P lies over its scores: S of a half goes out behind PV of the same half of
+//          the block before, under the softmax of the other half and the other tile
 //   14, 15 producers of K and of V with the pages' scales
+//
+// What bounds it: the softmax warps.  A block of 256 rows takes the tensor cores
+// 2048 cycles (an e4m3 product of two terms and an fp16 one) and the softmax warps
+// some 4200 of waiting for the scores, loading them, their maximum, the exponentials
+// and the store of P, with two warps on a scheduler.  Measured: 4096 tokens behind
+// 28672, 64 query heads on 8, D = 128: 3.38 ms, 1.22 PFLOP/s (0.64 of a bf16
+// product's rate; 4.07 ms with whole blocks as buffers, 3.75 with issuers behind a
+// test of the lane and spills).  Short chunks are bound by the way to the first
+// score (2 us of list, 4 of Q and the first tiles) and back (1.5 of the unit's end,
+// 4 of the second launch): 512 tokens from the start, 32 heads on 8: 23 us.  A
+// softmax that looks at a block's sum and not at its maximum, two halves in
+// registers at once, and two warps on the halves of one tile were no faster.
 #include <type_traits>
 
 #include "tsv_paged_tc.cuh"
@@ -55,7 +69,7 @@ constexpr int kBarConv = 1;
 constexpr int kScaleRow = 36;   // of a block, per 16 keys: K's scale, e and 2^-e and m of V's relative scale m 2^e; V's largest scale, whether every m is 1
 constexpr int kNanSlots = 6;    // blocks of a unit with masked keys: 3 at each end
 
-// A row's last key, its unit and its part.
+// A unit, and the part of it in the CTA's range.
 struct CUnit {
   int b, tile, g;
   int off, n, start, tiles;  // of the request
@@ -789,7 +803,7 @@ __global__ void __launch_bounds__(kCThreads, 1)
               uint32_t v[8] = {f16x2_of_e4m3x2(c.x & 0xFFFFu), f16x2_of_e4m3x2(c.x >> 16), f16x2_of_e4m3x2(c.y & 0xFFFFu),
                                f16x2_of_e4m3x2(c.y >> 16),     f16x2_of_e4m3x2(c.z & 0xFFFFu), f16x2_of_e4m3x2(c.z >> 16),
                                f16x2_of_e4m3x2(c.w & 0xFFFFu), f16x2_of_e4m3x2(c.w >> 16)};
-              if (!plain) {
+              if (!plain) {  // rounded to fp16's 11 bits, as P is
                 const float m = sc[24 + (key >> 4)];
 #pragma unroll
                 for (int e = 0; e < 8; ++e) v[e] = pack_f16(f16_lo(v[e]) * m, f16_hi(v[e]) * m);

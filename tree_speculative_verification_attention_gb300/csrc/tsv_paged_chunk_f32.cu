@@ -7,10 +7,10 @@
 // not give; but an e4m3 code is an fp16 value, so only the other operand has to be
 // split: a row of q (under a power of two that moves its largest value to
 // [2^14, 2^15)) and the p of 16 keys (relative to their largest) are two fp16 terms
-// each, off by 2^-22 of themselves.  Products of such terms with codes are exact, and sums stay short
-// inside the tensor core (it truncates): S over D, O over the 16 keys of a step,
-// which are then added to fp32 registers, where the page's V scale is a factor of
-// that addition.
+// each, off by 2^-22 of themselves.  Products of such terms with codes are exact,
+// and sums stay short inside the tensor core (it truncates): S over D, O over the
+// 16 keys of a step, which are then added to fp32 registers, where the page's V
+// scale is a factor of that addition.
 //
 // That wants accumulators in registers after every step, so warp-level MMAs fit
 // better here than ones whose sums live in TMEM.  A CTA takes 64 rows ((token, head
@@ -18,6 +18,12 @@
 // next block wait in registers while the current one, widened once for all rows,
 // is worked on.  With few tiles a cluster shares a tile's keys and joins through
 // distributed shared memory.
+//
+// What bounds it: issue (four products where one would do, and each step's sums added
+// to registers), and with few rows a CTA's chain over its keys.  Measured: 2048
+// tokens from the start, 8 query heads on 2: 54 TFLOP/s at D = 64, 64 at D = 128
+// (fp32 on CUDA cores could be 80 at the very most).  Five ragged chunks under a
+// window of 500: 31 us (135 with a CTA a token on the CUDA cores).
 #include <cuda_runtime.h>
 
 #include "tsv_paged_common.cuh"

@@ -1,16 +1,27 @@
 // tsv_pages.cu — page lists against a pool of reference counts: resize, fork,
-// compact.
+// compact; and the contents of pages.
 //
 // The pool is the counts alone: a free page is one whose count is 0, and pages
 // are handed out by rising id, so a call's result is a function of its
 // arguments.  Finding the k-th free page is a prefix sum over the counts.  One
-// cluster runs a whole call: its CTAs split the pool (a warp takes a contiguous
-// range, 128 counts at a time), exchange their totals through distributed
-// shared memory, and each then hands out, or moves, what lies in its own range;
-// cluster barriers stand between the phases, so a call is one launch and needs
-// no workspace.  What bounds a call is the chain of loads and barriers
-// (microseconds), and for pools of a million pages the counts' way through the
-// cluster's SMs.
+// cluster does it: its CTAs split the pool (a warp takes a contiguous range, 256
+// counts at a time), exchange their totals through distributed shared memory,
+// and each then hands out, or moves, what lies in its own range.  Cluster
+// barriers stand between the phases, so there is no workspace.  The lists are the
+// other half of the work.  Where they, or the pool, are large, what needs no
+// common order is done by launches of its own, on all SMs; where they are small,
+// one launch does everything, since a call then takes as long as its chain of
+// loads and barriers (about 5 us of it the launch and the first two loads).
+//
+// Measured on the stream (a call alone, in a captured graph):
+//   resize  32 requests that take 1 to 4 entries and give them back, 8192 pages:
+//           11.5 us for the two calls; 128 requests that take up to 2048 entries
+//           each and give them back, 2^20 pages: 37 us for the two
+//   fork    8 lists of one of 69 entries 13 us; 128 lists of up to 2048 entries,
+//           2^17 pages: 19 us
+//   compact 4096 pages 8.8 us; 2^20 pages and 128 lists of up to 8192 entries 26 us
+//   copy    8 pages of 32 KB 2.9 us; 4096 of 128 KB 156 us, 6.9 TB/s (what a plain
+//           copy reaches)
 #include <cuda_runtime.h>
 
 #include "tsv_device.cuh"
@@ -21,6 +32,8 @@ namespace tsv {
 namespace {
 
 constexpr int kPoolThreads = 1024, kPoolWarps = 32;
+static_assert(kPoolWarps == 32, "scan_counts takes a warp's sum per lane");
+static_assert(TSV_MAX_BATCH <= kPoolThreads, "a thread per request");
 constexpr int kPoolCtas = 16;  // of a cluster, at most (8 where the device holds no 16)
 
 __device__ __forceinline__ int ld_dsmem_i32(uint32_t addr) {
@@ -414,6 +427,7 @@ __global__ void __launch_bounds__(kPoolThreads, 1) pages_fork_kernel(const Pages
       a.copy_dst[b] = id;
     });
   }
+  if (KIND == kForkTake && r.needed == 0) cluster_sync_all();  // every CTA has read the status words that are written below
   if (KIND == kForkAll) {
     for_own(a.B, warp, lane, [&](int b, int t, int threads) {
       if (source[b] < 0 || r.bad[b] || !is_served(r, b, free)) return;
@@ -627,6 +641,10 @@ int pool_ctas(int32_t num_pages, int64_t entries, int most) {
   return n;
 }
 
+// From where on a call is several launches.  128 lists with room for 2048 entries each
+// (262144): 40 us as one launch, 19 as three; 8 lists of 69: 12.9 us and 12.1, but 9.6
+// and 12.6 of the host's time.  A compaction of 2^20 pages: 52 us as one launch, 26 as
+// three; of 4096: 8.8 and 8.6, and 11.8 and 15.4 of the host's.
 constexpr int64_t kForkSplit = 32768;  // entries that the lists have room for
 constexpr int kCompactSplit = 131072;  // pages
 
@@ -790,7 +808,10 @@ cudaError_t launch_pages_copy(const PagesCopyArgs& a, int num_sms, cudaStream_t 
   s.n1 = (int32_t)n1;
   s.vectors = (int32_t)((int64_t)c.page_size * c.Hkv * c.D / 16);
   const int64_t parts = (s.vectors + kCopyThreads * kCopyBatch - 1) / (kCopyThreads * kCopyBatch);
-  const int64_t units = 2ll * a.n * parts, most = (int64_t)num_sms * 8;
+  // Few units a CTA, so that CTAs that start keep loads going while others store: 4096
+  // pages of 128 KB take 183 us with 8 CTAs an SM in the grid, 156 with 64.  (Not one a
+  // unit: a.n may be far above the count on the device.)
+  const int64_t units = 2ll * a.n * parts, most = (int64_t)num_sms * 64;
   const int grid = (int)(units < 1 ? 1 : units < most ? units : most);
   return launch_pdl(pages_copy_kernel, dim3(grid), dim3(kCopyThreads), 0, st, 0u, a, s);
 }
