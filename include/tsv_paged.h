@@ -259,7 +259,7 @@ tsv_status tsv_paged_chunk_attention_workspace_size(tsv_handle h, tsv_dtype dtyp
  * same call gives the same bits again; other requests in the batch, max_rows or a
  * wider table can change the last ones.
  *   Accuracy.  Scores and sums are fp32.  bf16: a weight is rounded to 2^-12 of
- * itself (fp16) or 2^-36 of the row's largest, where V scales that lie apart count
+ * itself (fp16) or 2^-33 of the row's largest, where V scales that lie apart count
  * in what is largest, up to 2^40; V by a scale that is no power of two to 2^-12 of
  * itself; q is held to 2^-17 of its row's largest value.  Requests of one token:
  * as tsv_paged_tree_attention does few rows.  fp32: q and the weights are held to

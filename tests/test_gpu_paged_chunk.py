@@ -262,7 +262,7 @@ def test_pages_whose_values_lie_far_apart(tsv, kind, page, D):
     assert (st == 0).all()
     ref, spread, size = b.ref()
     tol = bound(ref, spread, size, b.q.dtype, 1801, D, kind[2] == 0)
-    # a weight in fp16 is off by 2^-36 of the row's largest product of weight and scale at the least (codes up to 448); fp32 rows
+    # a weight in fp16 is off by 2^-33 of the row's largest product of weight and scale at the least (codes up to 448); fp32 rows
     # and CUDA cores hold more
     if kind[2] == 0:
         top = spread.max(axis=-1, keepdims=True)

@@ -10,12 +10,13 @@
 // swizzled tile.  A row of q is two e4m3 terms under a power of two that moves
 // its largest value to [128, 256): a bf16's 8 bits exactly down to 2^-17 of it,
 // at the price of one fp16 product, since e4m3 products run at twice the rate.
-// V is widened to fp16 (exactly) so that P keeps fp16's 11 bits: P is 2^11 p
+// V is widened to fp16 (exactly) so that P keeps fp16's 11 bits: P is 2^8 p
 // times 2^e of the V scale of its page relative to the unit's largest so far,
-// m 2^e, p <= 2^4 below a reference maximum that moves only when a score passes it
-// by that much.  2^e is part of the exponent of p and goes out of the row's sum
-// again (a factor per 16 keys); m, 1 for scales that are powers of two, goes into V
-// as it is widened.
+// m 2^e, where p is relative to a reference maximum that moves only when a score
+// passes it by 2^7 (moving costs a wait for the products and a pass over O: with 2^4
+// and 2^11 a chunk of 1024 tokens behind 8192 took 1.06 times as long).  2^e is part
+// of the exponent of p and goes out of the row's sum again (a factor per 16 keys); m,
+// 1 for scales that are powers of two, goes into V as it is widened.
 //
 // Work.  Units of up to 256 rows (two tiles) of a KV head and the 128-key blocks
 // that any of their rows sees form one list, which is cut into equal ranges, one
@@ -59,8 +60,8 @@ constexpr int kCSoftRegs = 144, kCRestRegs = 112;
 static_assert(256 * kCSoftRegs + 256 * kCRestRegs <= kCThreads * 128, "register split");
 constexpr int kTileRows = 128;
 constexpr int kKStages = 3;
-constexpr float kRise = 4.f;    // log2: how far a score may pass the reference maximum
-constexpr float kUp = 11.f;     // log2 of P's factor: 2^4 x 2^11 is within fp16
+constexpr float kRise = 7.f;    // log2: how far a score may pass the reference maximum
+constexpr float kUp = 8.f;      // log2 of P's factor: 2^7 x 2^8 is within fp16
 constexpr int kFarApart = 40;   // log2: V scales that far apart leave a row's weights their bits
 // What a unit costs beside its blocks, in blocks; and how near to a unit's end a cut may come.
 constexpr int kUnitCost = 5, kLeastCut = 6, kNearEnd = 2;
@@ -301,7 +302,7 @@ __global__ void __launch_bounds__(kCThreads, 1)
       before += __shfl_sync(0xffffffffu, tiles, 31);
     }
   }
-  if (tid < 8) sCut[tid] = -1;
+  if (tid < 8) sCut[tid] = tid & 3 ? 0 : INT32_MAX;  // behind all tiles
   __syncthreads();
   auto request_of = [&](int f) {  // the request that owns tile f of all
     int lo = 0, hi = a.B - 1;
@@ -388,9 +389,13 @@ __global__ void __launch_bounds__(kCThreads, 1)
   struct Cut {
     int f, g, j;
   };
-  const Cut from{sCut[0] < 0 ? all_tiles : sCut[0], sCut[0] < 0 ? 0 : sCut[1], sCut[0] < 0 ? 0 : sCut[2]};
-  const Cut to{sCut[4] < 0 ? all_tiles : sCut[4], sCut[4] < 0 ? 0 : sCut[5], sCut[4] < 0 ? 0 : sCut[6]};
-  auto load_unit = [&](CUnit& u, int f) {  // g, tile and b are set
+  // (Read where they are wanted: registers that lie idle through the blocks are better used.)
+  auto cut = [&](int e) {
+    const volatile int32_t* c = sCut + 4 * e;
+    return Cut{c[0], c[1], c[2]};
+  };
+  auto tiles_of_all = [&] { return *static_cast<const volatile int32_t*>(sTiles + ((a.B + 31) & ~31)); };
+  auto fill_unit = [&](CUnit& u) {  // g, tile and b are set
     const int4 q = sReq[u.b];
     u.off = q.x;
     u.n = q.y;
@@ -401,11 +406,16 @@ __global__ void __launch_bounds__(kCThreads, 1)
     const int2 t = geo.blocks(u.start, u.row0, u.row0 + u.rows - 1);
     u.first = t.x;
     u.end = t.y;
+  };
+  auto load_unit = [&](CUnit& u, int f) {
+    const Cut to = cut(1);
+    fill_unit(u);
     u.j = u.first;
     u.j1 = f == to.f && u.g == to.g ? u.first + to.j : u.end;
   };
   auto first_unit = [&](CUnit& u) {
-    if (from.f >= all_tiles || (from.f == to.f && from.g == to.g && from.j == to.j)) return false;
+    const Cut from = cut(0), to = cut(1);
+    if (from.f >= tiles_of_all() || (from.f == to.f && from.g == to.g && from.j == to.j)) return false;
     u.b = request_of(from.f);
     u.tile = from.f - sTiles[u.b];
     u.g = from.g;
@@ -414,6 +424,7 @@ __global__ void __launch_bounds__(kCThreads, 1)
     return true;
   };
   auto next_unit = [&](CUnit& u) {
+    const Cut to = cut(1);
     if (++u.g == Hkv) {
       u.g = 0;
       if (++u.tile == u.tiles) {
@@ -422,8 +433,8 @@ __global__ void __launch_bounds__(kCThreads, 1)
         while (u.b < a.B && sTiles[u.b + 1] == sTiles[u.b]);
       }
     }
-    const int f = u.b < a.B ? sTiles[u.b] + u.tile : all_tiles;
-    if (f > to.f || (f == to.f && (u.g > to.g || (u.g == to.g && to.j == 0))) || f >= all_tiles) return false;
+    const int all = tiles_of_all(), f = u.b < a.B ? sTiles[u.b] + u.tile : all;
+    if (f > to.f || (f == to.f && (u.g > to.g || (u.g == to.g && to.j == 0))) || f >= all) return false;
     load_unit(u, f);
     return true;
   };
@@ -537,7 +548,7 @@ __global__ void __launch_bounds__(kCThreads, 1)
         for (int q = 0; q < 4; ++q) f[q] = fmaxf(f[q] * fr, 0x1p-126f);  // (above 0: a masked key's -inf stays one)
         tmem_wait_ld_tie32(s[0]);
         reg_tie32(s[1]);
-        if (masked) {
+        if (__builtin_expect(masked, 0)) {
           const int hi = pos - j * kPBlock + 1 - 64 * h, lo = a.window > 0 ? hi - a.window : 0;
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
@@ -566,20 +577,6 @@ __global__ void __launch_bounds__(kCThreads, 1)
           l *= c;
           alpha *= c;
         }
-        if (j + h > range.x && __any_sync(0xffffffffu, alpha != 1.f)) {
-          if (h == 0) TSV_CWAIT(&pv_done[2 * tile + 1], cnt - 1);
-          else TSV_CWAIT(&pv_done[2 * tile], cnt);
-          tc_fence_after();
-#pragma unroll 1
-          for (int cc = 0; cc < D; cc += 16) {
-            float o[16];
-            tmem_ld16(o_col + cc, o);
-            uint32_t z16[16];
-#pragma unroll
-            for (int e = 0; e < 16; ++e) z16[e] = __float_as_uint(o[e] * alpha);
-            tmem_st16u_nowait(o_col + cc, z16);
-          }
-        }
         const float base = m_ref == -INFINITY ? kUp : kUp - m_ref;
         const float4 back = *reinterpret_cast<const float4*>(sc + 16 + 4 * h);  // 2^-exponent
         const float un[4] = {back.x, back.y, back.z, back.w};
@@ -604,17 +601,38 @@ __global__ void __launch_bounds__(kCThreads, 1)
           }
           tmem_st16u_nowait(s_col + 64 * h + 16 * c, p);
         }
+        // O moves only now, with the scores gone from registers: in front of P the copies
+        // that this block forced, run or not, cost a long chunk 12 %.
+        if (__builtin_expect(j + h > range.x && __any_sync(0xffffffffu, alpha != 1.f), 0)) {
+          if (h == 0) TSV_CWAIT(&pv_done[2 * tile + 1], cnt - 1);
+          else TSV_CWAIT(&pv_done[2 * tile], cnt);
+          tc_fence_after();
+#pragma unroll 1
+          for (int cc = 0; cc < D; cc += 32) {
+            float o[32];
+            tmem_ld32(o_col + cc, o);
+            uint32_t z16[2][16];
+#pragma unroll
+            for (int e = 0; e < 32; ++e) z16[e >> 4][e & 15] = __float_as_uint(o[e] * alpha);
+            tmem_st16u_nowait(o_col + cc, z16[0]);
+            tmem_st16u_nowait(o_col + cc + 16, z16[1]);
+          }
+        }
         tmem_wait_st();
         tc_fence_before();
         dead = __any_sync(0xffffffffu, dead);
         if (lane == 0 && !dead) mbar_arrive(&p_full[2 * tile + h]);
       };
+      // Across the blocks the unit is four registers; what follows from them comes again.
+      uint32_t who = (uint32_t)u.b | ((uint32_t)u.g << 8);
+      int who_tile = u.tile;
+      const int from_j = u.j, to_j = u.j1, x0 = t - from_j;
       if (range.x < range.y) {
         const int r0 = tile * kTileRows, r1 = min(u.rows, r0 + kTileRows) - 1;
         const int2 full = full_range(u, r0, r1);
 #pragma unroll 1
         for (int j = range.x; j < range.y && !dead; ++j) {
-          const int x = t + j - u.j;
+          const int x = x0 + j;
           const bool masked = j < full.x || j >= full.y;
           cwait(&s_full[2 * tile], (uint32_t)cnt, abort_v, dead);
           // (Behind s_full: a tile that sits units out is far ahead of the scales' phases.)
@@ -644,6 +662,13 @@ __global__ void __launch_bounds__(kCThreads, 1)
           ++cnt;
         }
       }
+      asm volatile("" : "+r"(who), "+r"(who_tile));
+      u.b = (int)(who & 255u);
+      u.g = (int)(who >> 8);
+      u.tile = who_tile;
+      fill_unit(u);
+      u.j = from_j;
+      u.j1 = to_j;
       const CUnit now = u;
       going = next_unit(u);
       if (dead) break;
@@ -997,6 +1022,7 @@ __global__ void __launch_bounds__(kCThreads, 1)
   if (warp == kCMmaWarp + 1) {  // what the joining launch has to know
     CUnit v{};
     const bool any = first_unit(v);
+    const Cut from = cut(0), to = cut(1);
     ChunkPart p{};
     p.empty = any ? 0 : 1;
     if (any) {
