@@ -367,8 +367,8 @@ constexpr PagedChunkLayout paged_chunk_layout(int grid, int32_t D) {
 static_assert(paged_attn_layout(152, kPagedWideRows, 128).total <= paged_chunk_layout(152, 128).total, "one workspace serves both");
 cudaError_t paged_chunk_set_attributes(int32_t D);
 // Whether requests of one token go to the tree attention's kernel, in a launch of
-// its own: 28 of them beside 4 prompts, 32 heads on 8, take 327 us in one launch and
-// 289 in two, but a batch without any pays 6 to 7 us for the second.  Far fewer rows
+// its own: 28 of them beside 4 prompts, 32 heads on 8, took 327 us in one launch and
+// 289 in two (250 now), but a batch without any pays 6 to 7 us for the second.  Far fewer rows
 // than as many requests of the longest would have tell that most are short.
 constexpr int32_t kChunkApart = 16;
 inline bool paged_chunk_apart(int32_t B, int32_t N, int32_t max_rows) {

@@ -33,16 +33,18 @@
 //          the block before, under the softmax of the other half and the other tile
 //   14, 15 producers of K and of V with the pages' scales
 //
-// What bounds it: the softmax warps.  A block of 256 rows takes the tensor cores
-// 2048 cycles (an e4m3 product of two terms and an fp16 one) and the softmax warps
-// some 4200 of waiting for the scores, loading them, their maximum, the exponentials
-// and the store of P, with two warps on a scheduler.  Measured: 4096 tokens behind
-// 28672, 64 query heads on 8, D = 128: 3.38 ms, 1.22 PFLOP/s (0.64 of a bf16
-// product's rate; 4.07 ms with whole blocks as buffers, 3.75 with issuers behind a
-// test of the lane and spills).  Short chunks are bound by the way to the first
-// score (2 us of list, 4 of Q and the first tiles) and back (1.5 of the unit's end,
-// 4 of the second launch): 512 tokens from the start, 32 heads on 8: 23 us.  A
-// softmax that looks at a block's sum and not at its maximum, two halves in
+// What bounds it: the chain softmax - issuer - tensor cores - softmax of a half, whose
+// links wait for one another more than any unit is busy.  A block of 256 rows takes
+// 3700 cycles; of those the tensor cores have 2048 to do (an e4m3 product of two
+// terms and an fp16 one), the softmax warps 2600 (two on a scheduler), and shared
+// memory moves 336 KB, 2700 at 128 bytes a cycle, 128 KB of it Q, which every product
+// of 64 keys reads again (TMEM is full of S and O).  Measured: 1024 tokens
+// behind 8192, 64 query heads on 8, D = 128: 244 us, 183 with the
+// arithmetic and most of the products taken out; 4096 behind 28672: 2.99 ms, 1.38
+// PFLOP/s, 0.72 of a large bf16 product's rate.  Short chunks are bound by the way to
+// the first score (2 us of list, 4 of Q and the first tiles) and back (1.5 of the
+// unit's end, 4 of the second launch): 512 tokens from the start, 32 heads on 8: 22 us.
+// A softmax that looks at a block's sum and not at its maximum, two halves in
 // registers at once, and two warps on the halves of one tile were no faster.
 #include <type_traits>
 
