@@ -128,7 +128,7 @@ tsv_status tsv_pages_compact(tsv_handle h, const tsv_page_pool* pool, int32_t* r
  * tsv_pages_copy — page dst[i] of the cache takes the codes and the scales of
  * page src[i], K and V.  Pairs with an id of -1 are left out.  No page may be
  * the destination of two pairs, or of one and the source of another (its
- * contents would be either's).
+ * contents would be either's).  A page has 2^33 bytes of codes at most.
  *   src_d, dst_d    int32 [n], n >= 0
  *   count_d         int32 [1], NULL: n.  Only the first count pairs are copied
  *                   (none when it is negative, n when it is more)

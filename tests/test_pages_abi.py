@@ -132,6 +132,8 @@ def test_bad_caches_are_refused(paged, name):  # noqa: F811
         for kw in (dict(ids_d=None), dict(pages=0), dict(stride=3)):
             assert _call(paged, name, table=_table(paged, **kw)) == 1, kw
         assert _call(paged, name, N=1 << 30, B=1, Hq=2) == 3
+    else:  # a page of more than 2^33 bytes
+        assert _call(paged, name, cache=_cache(paged, Hkv=(1 << 23) + 1)) == 3
 
 
 def test_chunk_workspace_size_refusals(paged):  # noqa: F811

@@ -626,8 +626,8 @@ __global__ void __launch_bounds__(kCThreads, 1)
         if (lane == 0 && !dead) mbar_arrive(&p_full[2 * tile + h]);
       };
       // Across the blocks the unit is four registers; what follows from them comes again.
-      uint32_t who = (uint32_t)u.b | ((uint32_t)u.g << 8);
-      int who_tile = u.tile;
+      uint32_t who = (uint32_t)u.b | ((uint32_t)u.tile << 8);  // (fewer than 2^24 tiles: 128 rows of 2^31)
+      int who_g = u.g;
       const int from_j = u.j, to_j = u.j1, x0 = t - from_j;
       if (range.x < range.y) {
         const int r0 = tile * kTileRows, r1 = min(u.rows, r0 + kTileRows) - 1;
@@ -664,10 +664,10 @@ __global__ void __launch_bounds__(kCThreads, 1)
           ++cnt;
         }
       }
-      asm volatile("" : "+r"(who), "+r"(who_tile));
+      asm volatile("" : "+r"(who), "+r"(who_g));
       u.b = (int)(who & 255u);
-      u.g = (int)(who >> 8);
-      u.tile = who_tile;
+      u.tile = (int)(who >> 8);
+      u.g = who_g;
       fill_unit(u);
       u.j = from_j;
       u.j1 = to_j;

@@ -129,6 +129,7 @@ tsv_status tsv_pages_copy(tsv_handle h, const tsv_paged_cache* cache, const int3
   PagesCopyArgs a{};
   const tsv_status st = check_paged_cache(cache, &a.cache);
   if (st != TSV_OK) return st;
+  if ((int64_t)a.cache.page_size * a.cache.Hkv * a.cache.D > ((int64_t)1 << 33)) return TSV_ERR_UNSUPPORTED;
   const DeviceScope scope(h->device);
   if (!scope.ok) return TSV_ERR_CUDA;
   a.src = src_d;
