@@ -1,0 +1,42 @@
+"""Chunk attention on the GPU where a page's scale, or what a page outside a row's sight holds, decides: values are code x scale, and
+nothing but the rows that a token sees counts.  Bounds as in test_gpu_paged_chunk.py unless a test derives its own."""
+import numpy as np
+import pytest
+import torch
+
+from test_gpu_paged_chunk import KINDS, Chunk
+
+pytestmark = pytest.mark.gpu
+
+
+ZERO_SCALES = [  # page, Hq, Hkv, D, lengths, window, pages of scale 0 (a request's i-th of m)
+    (16, 4, 2, 128, [(300, 140), (0, 130), (700, 1)], 0, lambda i, m: i < m // 2),
+    (128, 4, 2, 64, [(300, 140), (0, 130), (700, 1)], 0, lambda i, m: i < m // 2),
+    (32, 4, 2, 128, [(300, 140), (0, 130), (700, 1)], 0, lambda i, m: i >= m // 2),
+    (64, 4, 2, 128, [(300, 140), (0, 130), (700, 1)], 0, lambda i, m: True),
+    # a unit in many CTAs' ranges: parts that begin in, or lie wholly in, zeros
+    (64, 32, 4, 128, [(6000, 40)], 0, lambda i, m: i % 10 < 7),
+    (128, 32, 4, 64, [(6000, 40)], 0, lambda i, m: 10 <= i < 40),
+    # single tokens alone
+    (16, 8, 2, 128, [(700, 1), (1500, 1), (40, 1), (5000, 1)], 0, lambda i, m: i < 2 * m // 3),
+    (128, 48, 1, 64, [(700, 1), (1500, 1), (40, 1), (5000, 1)], 0, lambda i, m: i % 3 < 2),
+    # the window begins in zeros
+    (16, 4, 2, 128, [(1000, 200), (900, 3), (1200, 1)], 700, lambda i, m: i < 3 * m // 4),
+    (128, 6, 2, 64, [(1000, 200), (900, 3), (1200, 1)], 300, lambda i, m: i < m - 1),
+]
+
+
+@pytest.mark.parametrize("kind", KINDS, ids=lambda k: k[0])
+@pytest.mark.parametrize("case", ZERO_SCALES, ids=lambda c: "-".join(str(x) for x in c[:4]) + "-w%d" % c[5])
+def test_codes_under_a_scale_of_zero_are_zero(tsv, kind, case):
+    """Pages whose V scale is 0 and whose codes are not: they weigh, and add nothing.  Of the other KV heads the scale stays."""
+    page, Hq, Hkv, D, lens, window, zero = case
+    b = Chunk(tsv, np.random.default_rng(page + D), lens, Hq, Hkv, D, page, dtype=kind[1])
+    for i, (p, n) in enumerate(lens):
+        m = -(-(p + n) // page)
+        ids = torch.tensor([b.table[i][x] for x in range(m) if zero(x, m)], device="cuda", dtype=torch.int64)
+        assert (b.cache.v.view(torch.uint8)[ids, :, 0] & 0x7F != 0).any()
+        b.cache.v_scale[ids, 0] = 0.0
+    out, st = b.run(tsv, flags=kind[2], window=window)
+    b.check(out, st, kind[2], window=window)
+    assert Hkv == 1 or not (out[:, Hq // Hkv:] == 0).all()

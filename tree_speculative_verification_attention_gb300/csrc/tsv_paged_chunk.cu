@@ -994,7 +994,9 @@ __global__ void __launch_bounds__(kCThreads, 1)
             top = fmaxf(top, __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(sv_now))));  // (scales are >= 0)
             const float turn = top > 1.f ? 0x1p-64f : 0x1p64f;  // (the division wants an ordinary divisor)
             const bool past = lane * 16 >= valid;               // (such keys take part in nothing)
-            const float rel = top > 0.f && !past ? __fdiv_rn(sv_now * turn, top * turn) : 1.f;
+            // (While every scale so far is 0, values are 0 whatever their codes: m is 0 as for a
+            // scale of 0 beside others.)
+            const float rel = past ? 1.f : top > 0.f ? __fdiv_rn(sv_now * turn, top * turn) : 0.f;
             const int e = max((int)(__float_as_uint(rel) >> 23) - 127, -kFarApart);
             const float m = rel * __uint_as_float((uint32_t)(127 - e) << 23);
             const bool all = __all_sync(0xffffffffu, lane >= 8 || m == 1.f);
