@@ -40,3 +40,23 @@ def test_codes_under_a_scale_of_zero_are_zero(tsv, kind, case):
     out, st = b.run(tsv, flags=kind[2], window=window)
     b.check(out, st, kind[2], window=window)
     assert Hkv == 1 or not (out[:, Hq // Hkv:] == 0).all()
+
+
+@pytest.mark.parametrize("kind", KINDS, ids=lambda k: k[0])
+@pytest.mark.parametrize("case", [(16, 4, 2, 128, [(1000, 200), (900, 3), (1205, 1), (0, 150)], 100),
+                                  (16, 32, 4, 64, [(6000, 40), (3333, 1)], 3000), (32, 6, 1, 128, [(411, 1), (500, 60)], 77)],
+                         ids=lambda c: "-".join(str(x) for x in c[:4]))
+def test_scales_in_front_of_a_window_do_not_count(tsv, kind, case):
+    """Pages in front of every row's window may have any scales: no bit of a result changes, with V values 2^100 times as large
+    there."""
+    page, Hq, Hkv, D, lens, window = case
+    b = Chunk(tsv, np.random.default_rng(page + Hq), lens, Hq, Hkv, D, page, dtype=kind[1])
+    want, st = b.run(tsv, flags=kind[2], window=window)
+    b.check(want, st, kind[2], window=window)
+    for i, (p, n) in enumerate(lens):
+        front = max(0, p - window + 1) // page  # pages that no new row sees anything of
+        ids = torch.from_numpy(b.table[i][:front].astype(np.int64)).cuda()
+        b.cache.v_scale[ids] *= 2.0 ** 100
+        b.cache.k_scale[ids] *= 2.0 ** 100
+    out, st = b.run(tsv, flags=kind[2], window=window)
+    assert (st == 0).all() and torch.equal(out, want)

@@ -947,6 +947,9 @@ __global__ void __launch_bounds__(kCThreads, 1)
         const int32_t* ids = a.table.ids_d + (int64_t)u.b * a.table.stride;
         const int keys = u.start + min(u.n, geo.by_heads.of(u.row0 + u.rows - 1) + 1);
         const int page_end = (keys + (1 << lps) - 1) >> lps;
+        // Keys in front of the unit's first window, as far as they fill 16: their pages may
+        // hold anything, and have no say in V's largest scale.
+        const int front = a.window > 0 ? max(0, u.start + geo.by_heads.of(u.row0) - a.window + 1) & ~15 : 0;
         // Lane p holds page p of the next block (of V's producer: of the next two), lanes
         // 0 .. 7 the next block's scales of 16 keys each: asked for a block ahead.
         auto page_of = [&](int j) {
@@ -956,7 +959,8 @@ __global__ void __launch_bounds__(kCThreads, 1)
         float top = 0.f, sk = 0.f, sv = 0.f;
         auto scales_of = [&](int pages, int j) {
           const int sid = __shfl_sync(0xffffffffu, pages, ((lane * 16) >> lps) & 31);
-          const bool on = j < u.j1 && lane < 8 && lane * 16 < keys - j * kPBlock && (uint32_t)sid < (uint32_t)c.num_pages;
+          const bool on = j < u.j1 && lane < 8 && lane * 16 < keys - j * kPBlock && lane * 16 >= front - j * kPBlock &&
+                          (uint32_t)sid < (uint32_t)c.num_pages;
           sk = on ? __ldg(c.k_scale_d + (int64_t)sid * c.Hkv + u.g) : 0.f;
           sv = on ? __ldg(c.v_scale_d + (int64_t)sid * c.Hkv + u.g) : 0.f;
         };
@@ -993,7 +997,7 @@ __global__ void __launch_bounds__(kCThreads, 1)
             // 2^e goes into the exponent of P and m, 1 as a rule, into V as it is widened.
             top = fmaxf(top, __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(sv_now))));  // (scales are >= 0)
             const float turn = top > 1.f ? 0x1p-64f : 0x1p64f;  // (the division wants an ordinary divisor)
-            const bool past = lane * 16 >= valid;               // (such keys take part in nothing)
+            const bool past = lane * 16 >= valid || lane * 16 < front - j * kPBlock;  // (such keys take part in nothing)
             // (While every scale so far is 0, values are 0 whatever their codes: m is 0 as for a
             // scale of 0 beside others.)
             const float rel = past ? 1.f : top > 0.f ? __fdiv_rn(sv_now * turn, top * turn) : 0.f;
