@@ -245,9 +245,12 @@ tsv_status tsv_paged_chunk_attention_workspace_size(tsv_handle h, tsv_dtype dtyp
  *                 no request are not read, and those of out keep what they hold
  *   out_d   (out) [N, Hq, D] contiguous, 16-byte aligned
  *   max_rows      >= 1; no request has more new rows
- *   window        >= 0; 0: no window
+ *   window        >= 0; 0: no window.  Pages that lie in front of the window of a
+ *                 request's first new row may have been given away: their entries
+ *                 and they themselves may hold anything
  *   scale         softmax scale; 0 means 1/sqrt(D)
- *   status_d (out) int32 [B]: as in tsv_paged_tree_attention
+ *   status_d (out) int32 [B]: as in tsv_paged_tree_attention, of the pages that a
+ *                 row sees (none of a request without new rows)
  *   flags         TSV_ATTN_DEFAULT or TSV_ATTN_SIMT (CUDA cores; a check rather
  *                 than a way to run long chunks)
  * Rows past a request's lengths may hold anything.  A NaN in a V row reaches

@@ -60,3 +60,53 @@ def test_scales_in_front_of_a_window_do_not_count(tsv, kind, case):
         b.cache.k_scale[ids] *= 2.0 ** 100
     out, st = b.run(tsv, flags=kind[2], window=window)
     assert (st == 0).all() and torch.equal(out, want)
+
+
+@pytest.mark.parametrize("kind", KINDS, ids=lambda k: k[0])
+@pytest.mark.parametrize("case", [(16, 4, 2, 128, [(1000, 200), (900, 3), (1205, 1), (0, 150), (333, 0)], 100),
+                                  (16, 32, 4, 64, [(6000, 40), (3333, 1), (5, 0)], 3000), (128, 6, 1, 128, [(1411, 1), (500, 60)], 77)],
+                         ids=lambda c: "-".join(str(x) for x in c[:4]))
+def test_pages_in_front_of_a_window_may_be_given_away(tsv, kind, case):
+    """Entries of pages that no new row sees: out of range on either side, or other requests' pages of NaN codes under large
+    scales.  The request stays valid and no bit changes; an entry of the first page that a row sees has to be right."""
+    page, Hq, Hkv, D, lens, window = case
+    b = Chunk(tsv, np.random.default_rng(page + Hq), lens, Hq, Hkv, D, page, dtype=kind[1])
+    want, st = b.run(tsv, flags=kind[2], window=window)
+    b.check(want, st, kind[2], window=window)
+    unused = sorted(set(range(b.cache.num_pages)) - set(b.table[b.table >= 0].tolist()))
+    b.cache.k.view(torch.uint8)[unused] = 0x7F
+    b.cache.v.view(torch.uint8)[unused] = 0xFF
+    b.cache.k_scale[unused] = b.cache.v_scale[unused] = 2.0 ** 100
+    fronts = [max(0, p - window + 1) // page if n else -(-p // page) for p, n in lens]
+    table = b.table.copy()
+    for fill in (-1, b.cache.num_pages, 2 ** 31 - 1, unused[0]):
+        for i, front in enumerate(fronts):
+            b.table[i][:front] = fill
+        out, st = b.run(tsv, flags=kind[2], window=window)
+        assert st.tolist() == [0] * len(lens) and torch.equal(out, want)
+    for i, front in enumerate(fronts):
+        b.table = table.copy()
+        b.table[i][front] = -1
+        out, st = b.run(tsv, flags=kind[2], window=window)
+        assert st.tolist() == [int(x == i and lens[i][1] > 0) for x in range(len(lens))]
+        keep = torch.ones(len(out), dtype=torch.bool, device="cuda")
+        keep[int(b.offs[i]):int(b.offs[i + 1])] = False
+        assert torch.equal(out[keep], want[keep])
+    # without a window every page counts
+    b.table = table.copy()
+    b.table[0][0] = -1
+    _, st = b.run(tsv, flags=kind[2])
+    assert st.tolist() == [1] + [0] * (len(lens) - 1)
+
+
+@pytest.mark.parametrize("kind", KINDS, ids=lambda k: k[0])
+def test_requests_without_new_rows_need_no_pages(tsv, kind):
+    b = Chunk(tsv, np.random.default_rng(3), [(300, 20), (500, 0), (40, 1), (0, 0)], 4, 2, 64, 16, dtype=kind[1])
+    b.table[1] = -1
+    for kw in (dict(), dict(window=50)):
+        out, st = b.run(tsv, flags=kind[2], **kw)
+        b.check(out, st, kind[2], **kw)
+    b.offs, b.q = np.array([0, 1, 1, 2, 2]), b.q[:2].contiguous()  # single tokens
+    b.lens = [(300, 1), (500, 0), (40, 1), (0, 0)]
+    out, st = b.run(tsv, flags=kind[2], max_rows=1)
+    b.check(out, st, kind[2])

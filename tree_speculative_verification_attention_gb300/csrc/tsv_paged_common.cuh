@@ -122,12 +122,15 @@ __device__ __forceinline__ bool paged_request(const PagedAttnArgs& a, int b, Pag
 }
 
 // Whether a page id that the request needs is out of range, as far as the
-// calling thread's share (index t of `threads`) goes.
+// calling thread's share (index t of `threads`) goes.  A chunk needs the pages
+// from the first row's window on, and none without new rows.
 __device__ __forceinline__ bool paged_bad_page(const PagedAttnArgs& a, int b, const PagedRequest& r, int t, int threads) {
   const int ps = a.cache.page_size;
   bool bad = false;
   const int32_t* ids = a.table.ids_d + (int64_t)b * a.table.stride;
-  for (int i = t; i < (r.P + ps - 1) / ps; i += threads) bad |= (uint32_t)ids[i] >= (uint32_t)a.cache.num_pages;
+  const int first = a.window > 0 ? max(0, r.P - r.n + 1 - a.window) / ps : 0;
+  const int end = a.chunk && r.n == 0 ? 0 : (r.P + ps - 1) / ps;
+  for (int i = first + t; i < end; i += threads) bad |= (uint32_t)ids[i] >= (uint32_t)a.cache.num_pages;
   if (a.tree_table.ids_d) {
     ids = a.tree_table.ids_d + (int64_t)b * a.tree_table.stride;
     for (int i = t; i < (r.n + ps - 1) / ps; i += threads) bad |= (uint32_t)ids[i] >= (uint32_t)a.cache.num_pages;
