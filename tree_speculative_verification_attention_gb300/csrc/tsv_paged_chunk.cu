@@ -67,7 +67,7 @@ constexpr float kUp = 8.f;      // log2 of P's factor: 2^7 x 2^8 is within fp16
 constexpr int kFarApart = 40;   // log2: V scales that far apart leave a row's weights their bits
 // What a unit costs beside its blocks, in blocks; and how near to a unit's end a cut may come.
 constexpr int kUnitCost = 5, kLeastCut = 6, kNearEnd = 2;
-constexpr uint32_t kCWaitTries = 1u << 22;  // (of a microsecond or less each)
+constexpr uint32_t kCWaitTries = 1024;  // of a wait before it looks at the clock, too (0.3 to 1.4 us each)
 constexpr int kBarConv = 1;
 constexpr int kScaleRow = 36;   // of a block, per 16 keys: K's scale, e and 2^-e and m of V's relative scale m 2^e; V's largest scale, whether every m is 1
 constexpr int kNanSlots = 6;    // blocks of a unit with masked keys: 3 at each end
@@ -192,11 +192,14 @@ __device__ __forceinline__ uint32_t nan_bytes(uint32_t w) { return ((w & 0x7F7F7
 __device__ __forceinline__ uint32_t bits_below(int n) { return n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1u; }
 
 // As pwait, without a time that the hardware holds the thread for: warps that
-// wait here wait shortly (2 % of a long chunk).
+// wait here wait shortly (2 % of a long chunk).  But for the softmax warps of a tile that
+// sits units out, which wait for as long as those take: a wait is given up when for
+// kWaitLimitNs K's producer has asked for no block (abort[1]: the time when it last did,
+// the lower 32 bits of ns; it may be later than the clock that was read here).
 __device__ __forceinline__ void cwait(uint64_t* bar, uint32_t parity, volatile int* abort, bool& dead) {
 #pragma unroll 1
   for (uint32_t n = 0; !mbar_try_wait(bar, parity & 1u); ++n)
-    if (dead || *abort || n == kCWaitTries) {
+    if (dead || *abort || (n >= kCWaitTries && (int)((uint32_t)global_timer_ns() - (uint32_t)abort[1]) > (int)kWaitLimitNs)) {
       *abort = 1;
       dead = true;
       break;
@@ -382,6 +385,7 @@ __global__ void __launch_bounds__(kCThreads, 1)
       sCut[4 * e + 2] = j;
     }
   }
+  if (tid == 0) abort_v[1] = (int)(uint32_t)global_timer_ns();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -992,6 +996,7 @@ __global__ void __launch_bounds__(kCThreads, 1)
           __syncwarp();
           if (lead) mbar_arrive(full);
           asked = x + 1;
+          if (!is_v && lead) abort_v[1] = (int)(uint32_t)global_timer_ns();
           if (is_v) {
             // The unit's largest V scale so far, and the block's relative to it as m 2^e:
             // 2^e goes into the exponent of P and m, 1 as a rule, into V as it is widened.
