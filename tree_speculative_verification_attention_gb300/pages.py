@@ -154,7 +154,7 @@ def pages_compact(pool, tables, pages, out=None, in_place=False, stream=None):
             with _allocating(stream, pool.device):
                 out["tables"] = [torch.empty(t.shape, dtype=_INT, device=pool.device) for t in tables]
     elif "status" not in out:
-        out["status"], = _empty(pool, stream, n)
+        out = dict(out, status=_empty(pool, stream, n)[0])
     _want(len(out["tables"]) == n, "out: as many tables are wanted")
     packed = b""
     for i, (t, held, to) in enumerate(zip(tables, pages, out["tables"])):
