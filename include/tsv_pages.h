@@ -74,8 +74,8 @@ tsv_status tsv_pages_resize(tsv_handle h, const tsv_page_pool* pool, const tsv_p
  *   source_d        int32 [B]; -1 leaves list b as it is
  *   rows_d          int32 [B]
  *   to, to_pages_d  lists and their counts (both in / out), B of them; must not
- *                   overlap the source lists (of one table, rows apart from
- *                   each other will do)
+ *                   overlap the source lists (of one table, rows or columns
+ *                   apart from each other will do, also in turn)
  *   copy_src_d, copy_dst_d (out) int32 [B]: the page that list b's last page is
  *                   to be copied from, and that page; -1 when there is none
  *   status_d (out)  int32 [B]: TSV_OK; TSV_ERR_NO_PAGES, as in tsv_pages_resize,

@@ -22,12 +22,23 @@ tsv_status check_lists(const tsv_page_table* t, int64_t rows) {
   return t->pages > TSV_PAGED_MAX_ROWS ? TSV_ERR_UNSUPPORTED : TSV_OK;
 }
 
-// Whether the entries of two sets of lists lie in ranges that meet.
+// n / d of d > 0, rounded down.
+__int128 floor_div(__int128 n, int64_t d) { return n / d - (n % d < 0 ? 1 : 0); }
+
+// Whether two sets of lists have an entry in common (rows of one table may take turns, or
+// its columns be split): for each row of b, whether a row of a begins before its end and
+// ends behind its beginning.
 bool lists_meet(const tsv_page_table& a, int64_t ra, const tsv_page_table& b, int64_t rb) {
-  const uintptr_t a0 = addr(a.ids_d), b0 = addr(b.ids_d);
-  const uintptr_t a1 = a0 + 4 * (uintptr_t)((ra > 1 ? (ra - 1) * a.stride : 0) + a.pages);
-  const uintptr_t b1 = b0 + 4 * (uintptr_t)((rb > 1 ? (rb - 1) * b.stride : 0) + b.pages);
-  return a0 < b1 && b0 < a1;
+  const int64_t stride = ra > 1 ? a.stride : a.pages;
+  const __int128 first = ((__int128)addr(b.ids_d) - (__int128)addr(a.ids_d)) / 4;  // (both are multiples of 4)
+  if (first >= (__int128)(ra - 1) * stride + a.pages || (rb > 1 ? (__int128)(rb - 1) * b.stride : 0) + b.pages <= -first)
+    return false;  // one set ends before the other: as a rule
+  for (int64_t j = 0; j < rb; ++j) {
+    const __int128 at = first + (__int128)j * b.stride;
+    const __int128 lo = floor_div(at - a.pages, stride) + 1, hi = floor_div(at + b.pages - 1, stride);
+    if ((lo > 0 ? lo : 0) <= (hi < ra - 1 ? hi : ra - 1)) return true;
+  }
+  return false;
 }
 
 int cluster_of(tsv_handle h) {  // (the handle's device is current)
