@@ -5,6 +5,7 @@ import pytest
 import torch
 
 from test_gpu_paged_chunk import KINDS, Chunk
+from test_gpu_paged_chunk_range import MIXED
 
 pytestmark = pytest.mark.gpu
 
@@ -110,3 +111,85 @@ def test_requests_without_new_rows_need_no_pages(tsv, kind):
     b.lens = [(300, 1), (500, 0), (40, 1), (0, 0)]
     out, st = b.run(tsv, flags=kind[2], max_rows=1)
     b.check(out, st, kind[2])
+
+
+def _flat(tsv, dtype, lens, page=16, D=64):
+    """A batch of one head whose keys all score 0 but row 3, which scores q's first element; all V are 1, row 3's is 0."""
+    b = Chunk(tsv, np.random.default_rng(8), lens, 1, 1, D, page, dtype=dtype)
+    k, v = b.cache.k.view(torch.uint8), b.cache.v.view(torch.uint8)
+    k.zero_()
+    v.fill_(0x38)
+    b.cache.k_scale.fill_(1.0)
+    b.cache.v_scale.fill_(1.0)
+    b.q.zero_()
+    for i in range(len(lens)):
+        k[b.table[i][0], 3, 0, 0] = 0x38
+        v[b.table[i][0], 3] = 0
+    return b
+
+
+# What a weight is off by, at most: fp16's half step on the tensor cores (chunks in bf16), two terms of it (fp32: 2^-22), fp32's
+# exp2 and products otherwise.
+WEIGHT = {"f32": 2.0 ** -21, "f32-cuda-cores": 2.0 ** -22, "bf16-cuda-cores": 2.0 ** -22, "bf16": 2.0 ** -11}
+
+
+@pytest.mark.parametrize("kind", KINDS, ids=lambda k: k[0])
+def test_weights_hold_fp16s_bits(tsv, kind):
+    """n equal weights against one that is about as heavy as all of them (V 1 and -1): every weight is off the same way, so that a
+    single rounding shows, and the result is near 0, where its own rounding does not hide it.  One unit, not cut."""
+    b = _flat(tsv, kind[1], [(560, 40)])
+    b.cache.v.view(torch.uint8)[b.table[0][0], 3] = 0xB8
+    b.q[:, 0, 0] = 6.375
+    n = 560 + torch.arange(40, dtype=torch.float64)
+    worst = 0.0
+    for scale in np.linspace(0.985, 1.02, 36).astype(np.float32):
+        out, st = b.run(tsv, flags=kind[2], scale=float(scale))
+        assert (st == 0).all()
+        w = float(np.exp(6.375 * np.float64(scale)))
+        want = (n - w) / (n + w)
+        # the score (6.4, a few roundings of 2^-24 each: 2^-20), the weights, sums of 38 steps (2^-18), the result's half step
+        tol = (WEIGHT[kind[0]] * n + 2.0 ** -20 * w) / (n + w) + 2.0 ** -18 + (2.0 ** -8 if kind[1] == torch.bfloat16 else 2.0 ** -24) * want.abs()
+        err = (out[:, 0].double().cpu() - want[:, None]).abs()
+        worst = max(worst, (err / tol[:, None]).max().item())
+    assert worst <= 1.0, worst
+
+
+@pytest.mark.parametrize("kind", KINDS, ids=lambda k: k[0])
+@pytest.mark.parametrize("power", range(10, 38, 3))
+def test_light_weights_beside_a_heavy_one(tsv, kind, power):
+    """n weights 2^-power of another, whose V is 0: they are all of the result.  In fp16 a weight is off by 2^-33 of the row's
+    largest at the most beside its half step; fp32 rows hold theirs to 2^-38 of 16 keys' largest."""
+    b = _flat(tsv, kind[1], [(560, 40)])
+    b.q[:, 0, 0] = power * np.log(2.0)
+    out, st = b.run(tsv, flags=kind[2], scale=1.0)
+    assert (st == 0).all()
+    n = (560 + torch.arange(40, dtype=torch.float64))[:, None]
+    w = np.exp(float(b.q[0, 0, 0].double()))
+    want = n / (n + w)
+    floor = {"bf16": 2.0 ** -33, "f32": 2.0 ** -38}.get(kind[0], 0.0) * w
+    half = 2.0 ** -8 if kind[1] == torch.bfloat16 else 2.0 ** -24
+    # (a score of `power` bits, rounded a few times to 24: the weights move by power 2^-22 of themselves)
+    rel = WEIGHT[kind[0]] + power * 2.0 ** -22 + 2.0 ** -18
+    tol = want * rel + n * floor / (n + w)
+    tol = tol + half * (want + tol)
+    err = (out[:, 0].double().cpu() - want).abs()
+    assert (err <= tol).all(), (err / tol).max().item()
+
+
+@pytest.mark.parametrize("kind", KINDS, ids=lambda k: k[0])
+@pytest.mark.parametrize("D,Hq,Hkv", [(128, 8, 2), (64, 40, 1)])
+def test_single_tokens_beside_chunks_as_by_themselves(tsv, kind, D, Hq, Hkv):
+    """The single tokens of a mixed batch give the bits of a call of single tokens alone (the other requests bring no rows there)."""
+    b = Chunk(tsv, np.random.default_rng(Hq), MIXED, Hq, Hkv, D, 16, dtype=kind[1])
+    out, st = b.run(tsv, flags=kind[2])
+    assert (st == 0).all()
+    one = [i for i, (_, n) in enumerate(MIXED) if n == 1]
+    rows = torch.from_numpy(b.offs[one]).cuda()
+    b.q = b.q[rows].contiguous()
+    b.offs = np.concatenate([[0], np.cumsum([int(n == 1) for _, n in MIXED])])
+    alone, st = b.run(tsv, flags=kind[2], max_rows=1)
+    assert (st == 0).all()
+    if kind[0] == "f32":  # a kernel of its own
+        assert (alone.double() - out[rows].double()).abs().max().item() <= 2.0 ** -18 * out.abs().max().item()
+    else:
+        assert torch.equal(alone, out[rows])
