@@ -40,7 +40,9 @@ __device__ __forceinline__ float out_of_f32<float>(float v) { return v; }
 template <>
 __device__ __forceinline__ __nv_bfloat16 out_of_f32<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 
-template <typename T, int D>
+// CHUNK: the nodes are new rows of the prefix pages (a.chunk), of which each sees those up
+// to its own, or a window of them.
+template <typename T, int D, bool CHUNK>
 __global__ void __launch_bounds__(32 * kSimtWarps) paged_attn_simt_kernel(const PagedAttnArgs a) {
   constexpr int kSimtHeads = simt_heads<D>();
   constexpr int E = D / 32;  // elements of V per lane
@@ -58,7 +60,7 @@ __global__ void __launch_bounds__(32 * kSimtWarps) paged_attn_simt_kernel(const 
     if (g != 0) return;
     const int b = blockIdx.x;
     PagedRequest r;
-    bool bad = !paged_request(a, b, &r);
+    bool bad = !paged_request(a, b, &r, CHUNK);
     if (!bad) bad = paged_bad_page(a, b, r, tid, blockDim.x);
     bad = __syncthreads_or(bad);
     if (tid == 0) a.status[b] = bad ? TSV_ERR_INVALID_ARG : TSV_OK;
@@ -74,13 +76,13 @@ __global__ void __launch_bounds__(32 * kSimtWarps) paged_attn_simt_kernel(const 
   __syncthreads();
   if (b < 0) return;
   PagedRequest r;
-  if (!paged_request(a, b, &r)) return;
+  if (!paged_request(a, b, &r, CHUNK)) return;
   const int off = r.off, n = r.n, ps = C.page_size;
-  const bool tree = a.tree_table.ids_d != nullptr;
+  const bool tree = !CHUNK && a.tree_table.ids_d != nullptr;
   const int i = node - off;
   // The prefix rows that the node sees: lo .. P - 1.
-  const int P = a.chunk ? r.P - n + i + 1 : r.P;
-  const int lo = a.window > 0 ? max(0, P - a.window) : 0;
+  const int P = CHUNK ? r.P - n + i + 1 : r.P;
+  const int lo = CHUNK && a.window > 0 ? max(0, P - a.window) : 0;
   if (tid < TSV_ANC_WORDS) {
     const int left = i + 1 - 32 * tid;  // chain: bits 0 .. i
     sanc[tid] = !tree ? 0u
@@ -109,8 +111,9 @@ __global__ void __launch_bounds__(32 * kSimtWarps) paged_attn_simt_kernel(const 
     }
     for (int k0 = (lo & ~31) + warp * 32; k0 < keys; k0 += kSimtWarps * 32) {
       const int key = k0 + lane;
-      bool see = key < P && key >= lo;
-      if (tree && key >= P && key < keys) see = (sanc[(key - P) >> 5] >> ((key - P) & 31)) & 1u;
+      bool see = key < P;
+      if (CHUNK) see = see && key >= lo;
+      else if (!see && key < keys) see = (sanc[(key - P) >> 5] >> ((key - P) & 31)) & 1u;
       int64_t row = 0;   // byte offset of the key's row of this head
       float ks = 0.f, vs = 0.f;
       if (see) {
@@ -231,13 +234,16 @@ __global__ void __launch_bounds__(32 * kSimtWarps) paged_attn_simt_kernel(const 
 
 }  // namespace
 
-cudaError_t launch_paged_attention_simt(const PagedAttnArgs& a, bool bf16, cudaStream_t st) {
+template <typename T, int D>
+static cudaError_t launch_simt_typed(const PagedAttnArgs& a, cudaStream_t st) {
   const dim3 grid(a.N + a.B, a.cache.Hkv), block(32 * kSimtWarps);
-  if (bf16)
-    return a.cache.D == 64 ? launch_pdl(paged_attn_simt_kernel<__nv_bfloat16, 64>, grid, block, 0, st, 0u, a)
-                           : launch_pdl(paged_attn_simt_kernel<__nv_bfloat16, 128>, grid, block, 0, st, 0u, a);
-  return a.cache.D == 64 ? launch_pdl(paged_attn_simt_kernel<float, 64>, grid, block, 0, st, 0u, a)
-                         : launch_pdl(paged_attn_simt_kernel<float, 128>, grid, block, 0, st, 0u, a);
+  return a.chunk ? launch_pdl(paged_attn_simt_kernel<T, D, true>, grid, block, 0, st, 0u, a)
+                 : launch_pdl(paged_attn_simt_kernel<T, D, false>, grid, block, 0, st, 0u, a);
+}
+
+cudaError_t launch_paged_attention_simt(const PagedAttnArgs& a, bool bf16, cudaStream_t st) {
+  if (bf16) return a.cache.D == 64 ? launch_simt_typed<__nv_bfloat16, 64>(a, st) : launch_simt_typed<__nv_bfloat16, 128>(a, st);
+  return a.cache.D == 64 ? launch_simt_typed<float, 64>(a, st) : launch_simt_typed<float, 128>(a, st);
 }
 
 }  // namespace tsv

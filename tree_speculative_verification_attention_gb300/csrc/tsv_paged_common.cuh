@@ -109,17 +109,19 @@ __device__ __forceinline__ void rope_pair(float& a, float& b, float c, float s) 
 struct PagedRequest {
   int off, n, P;
 };
-__device__ __forceinline__ bool paged_request(const PagedAttnArgs& a, int b, PagedRequest* r) {
+__device__ __forceinline__ bool paged_request(const PagedAttnArgs& a, int b, PagedRequest* r, bool chunk) {
   const int ps = a.cache.page_size;
   r->off = __ldg(a.offsets + b);
   const int end = __ldg(a.offsets + b + 1);
   r->P = __ldg(a.prefix_len + b);
   r->n = end - r->off;
-  if (a.chunk && r->P >= 0 && r->n >= 0) r->P = (int)min((int64_t)r->P + r->n, (int64_t)INT32_MAX);
+  if (chunk && r->P >= 0 && r->n >= 0) r->P = (int)min((int64_t)r->P + r->n, (int64_t)INT32_MAX);
   return r->off >= 0 && end >= r->off && end <= a.N && r->n <= a.max_nodes && r->P >= 0 &&
          (int64_t)r->P <= (int64_t)a.table.pages * ps &&
          (a.tree_table.ids_d == nullptr || (int64_t)r->n <= (int64_t)a.tree_table.pages * ps);
 }
+
+__device__ __forceinline__ bool paged_request(const PagedAttnArgs& a, int b, PagedRequest* r) { return paged_request(a, b, r, a.chunk != 0); }
 
 // Whether a page id that the request needs is out of range, as far as the
 // calling thread's share (index t of `threads`) goes.  A chunk needs the pages
