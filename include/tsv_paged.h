@@ -186,7 +186,7 @@ tsv_status tsv_paged_tree_attention_workspace_size(tsv_handle h, tsv_dtype dtype
  *   Accuracy.  Scores and sums are fp32.  On the tensor cores a weight (its
  * softmax term times the V scale of its page) is rounded: with few rows to
  * 2^-8 of itself (two e4m3 terms) or 2^-18 of the largest among 256 keys (2^-14
- * where their V scales lie up to 2^4 apart), with many to 2^-12 of itself
+ * where their V scales lie up to 2^4 apart), with many to 2^-11 of itself
  * (fp16) or 2^-36 of the row's largest; V scales further apart count in what a
  * row's weights are relative to, up to 2^40.  q is held to 2^-17 of its row's
  * largest value with few rows, 2^-31 with many.
@@ -257,17 +257,22 @@ tsv_status tsv_paged_chunk_attention_workspace_size(tsv_handle h, tsv_dtype dtyp
  * only the rows that see it.  Values of V (code x scale) are 2^127 at most over
  * the number of keys that a row sees, so that sums before the division are
  * finite.
- *   Which kernel runs follows from dtype, flags, the shapes and `window` alone
- * (requests of one token may be a launch of their own beside longer ones).  The
- * same call gives the same bits again; other requests in the batch, max_rows or a
- * wider table can change the last ones.
- *   Accuracy.  Scores and sums are fp32.  bf16: a weight is rounded to 2^-12 of
- * itself (fp16) or 2^-33 of the row's largest, where V scales that lie apart count
- * in what is largest, up to 2^40; V by a scale that is no power of two to 2^-12 of
- * itself; q is held to 2^-17 of its row's largest value.  Requests of one token:
- * as tsv_paged_tree_attention does few rows.  fp32: q and the weights are held to
- * 2^-22 of themselves, 2^-38 of the largest of a row of q and of the weights of 16
- * keys.
+ *   Which kernel runs follows from dtype, flags, the shapes and `window` alone: a
+ * request of one token in bf16, without a window, is taken by the kernel of few
+ * rows of tsv_paged_tree_attention when max_rows is 1, and in batches of 16
+ * requests and more when N is at most a third of B x max_rows (a launch of its
+ * own, for which max_rows should be the most that there are); else as a chunk of
+ * one row.  The same call gives the same bits again; other requests in the batch,
+ * max_rows or a wider table can change the last ones.
+ *   Accuracy.  Scores and sums are fp32; on the tensor cores a sum loses 2^-23 of
+ * itself at most with every 16 keys (2^-10 over 2^17 keys that one CTA adds up).
+ * bf16: a weight is rounded to 2^-11 of itself (fp16) or 2^-33 of the row's
+ * largest, where V scales that lie apart count in what is largest, up to 2^40; V
+ * by a scale that is no power of two to 2^-11 of itself; q is held to 2^-17 of its
+ * row's largest value.  Single tokens in the kernel of few rows: weights as there
+ * (2^-8 of themselves).  fp32: q and the weights are held to 2^-22 of themselves,
+ * 2^-38 of the largest of a row of q and of the weights of 16 keys; sums over keys
+ * are added up 16 at a time, rounded to nearest.
  */
 tsv_status tsv_paged_chunk_attention(tsv_handle h, tsv_dtype dtype, const void* q_d, int64_t q_stride_n, int64_t q_stride_h,
                                      const tsv_paged_cache* cache, const tsv_page_table* table, const int32_t* start_d,

@@ -40,10 +40,10 @@
 // memory moves 336 KB, 2700 at 128 bytes a cycle, 128 KB of it Q, which every product
 // of 64 keys reads again (TMEM is full of S and O).  Measured: 1024 tokens
 // behind 8192, 64 query heads on 8, D = 128: 244 us, 183 with the
-// arithmetic and most of the products taken out; 4096 behind 28672: 2.99 ms, 1.38
-// PFLOP/s, 0.72 of a large bf16 product's rate.  Short chunks are bound by the way to
+// arithmetic and most of the products taken out; 4096 behind 28672: 3.0 ms, 1.37
+// PFLOP/s, 0.71 of a large bf16 product's rate.  Short chunks are bound by the way to
 // the first score (2 us of list, 4 of Q and the first tiles) and back (1.5 of the
-// unit's end, 4 of the second launch): 512 tokens from the start, 32 heads on 8: 22 us.
+// unit's end, 4 of the second launch): 512 tokens from the start, 32 heads on 8: 21 us.
 // A softmax that looks at a block's sum and not at its maximum, two halves in
 // registers at once, and two warps on the halves of one tile were no faster.
 #include <type_traits>

@@ -2,9 +2,10 @@
 
 Two layers, as in the package's main module: ``tsv_*`` functions mirror the C
 ABI one to one; ``rope_frequencies``, ``rope``, ``PagedCache``, ``paged_append``,
-``paged_tree_attention``, ``paged_commit`` and ``paged_chunk_attention`` check shapes and types, allocate what the caller did not pass, and call them.  The launches go to the current
-stream of the tensors' device, or to ``stream``; what these helpers allocate
-belongs to that stream.
+``paged_tree_attention``, ``paged_commit`` and ``paged_chunk_attention`` check
+shapes and types, allocate what the caller did not pass, and call them.  The
+launches go to the current stream of the tensors' device, or to ``stream``; what
+these helpers allocate belongs to that stream.
 """
 from __future__ import annotations
 
@@ -405,8 +406,9 @@ def paged_chunk_attention(q, cache, page_table, start, row_offsets, window=0, ma
                           out=None, workspace=None, status=None, stream=None):
     """Causal attention of new tokens over the pages that hold them: rows row_offsets[b] .. row_offsets[b+1]-1 of q [N, Hq, D] are
     request b's tokens, whose K/V rows start[b] .. paged_append wrote; each sees the rows up to its own (`window`: the last so
-    many of them).  `max_rows`: the most new rows of one request (default N; 1 for single tokens is faster when it is given).
-    Returns out [N, Hq, D] and status [B]."""
+    many of them).  `max_rows`: the most new rows of one request.  Give the true number: 1 for single tokens, and in batches of 16
+    requests or more, where the default, N, stands for a batch that is mostly single tokens and costs the others a launch (6 to
+    7 us); it also chooses between unit sizes.  Returns out [N, Hq, D] and status [B]."""
     index = cache.index
     B = row_offsets.shape[0] - 1
     shape, qs = _heads("q", q, index, cache.D)
