@@ -193,3 +193,18 @@ def test_single_tokens_beside_chunks_as_by_themselves(tsv, kind, D, Hq, Hkv):
         assert (alone.double() - out[rows].double()).abs().max().item() <= 2.0 ** -18 * out.abs().max().item()
     else:
         assert torch.equal(alone, out[rows])
+
+
+@pytest.mark.parametrize("kind", KINDS, ids=lambda k: k[0])
+@pytest.mark.parametrize("page,D,window", [(16, 128, 100), (16, 64, 37), (32, 64, 333)])
+def test_scales_of_pages_given_away_may_be_anything(tsv, kind, page, D, window):
+    """Pages in front of every window, as never written memory may have them: scales of NaN, infinity and below 0 change no bit."""
+    b = Chunk(tsv, np.random.default_rng(page + D), [(1000, 70), (900, 3), (1205, 1), (507, 150)], 4, 2, D, page, dtype=kind[1])
+    want, st = b.run(tsv, flags=kind[2], window=window)
+    b.check(want, st, kind[2], window=window)
+    front = np.concatenate([b.table[i][:max(0, p - window + 1) // page] for i, (p, _) in enumerate(b.lens)]).astype(np.int64)
+    ids = torch.from_numpy(front).cuda()
+    for scale in (float("nan"), float("inf"), -1.0):
+        b.cache.k_scale[ids] = b.cache.v_scale[ids] = scale
+        out, st = b.run(tsv, flags=kind[2], window=window)
+        assert (st == 0).all() and torch.equal(out, want)

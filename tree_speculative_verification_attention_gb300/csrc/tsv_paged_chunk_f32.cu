@@ -194,6 +194,9 @@ __global__ void __launch_bounds__(kFThreads) paged_chunk_f32_kernel(const __grid
   const int chunk = tid % kLanes, first_row = tid / kLanes;
   const int32_t* ids = a.table.ids_d + (int64_t)b * a.table.stride;
   const int keys = p_last + 1;
+  // Keys in front of the tile's first window, as far as they fill 16: no scale is read of
+  // what may be there (0 weights times a scale that is not finite would be NaN).
+  const int front = a.window > 0 ? max(0, p_first - a.window + 1) & ~15 : 0;
   uint4 kc[kPer], vc[kPer];
   float scale = 0.f;  // threads 0 .. 7: K's, then V's scales of 16 keys
   auto fetch = [&](int j) {
@@ -211,7 +214,7 @@ __global__ void __launch_bounds__(kFThreads) paged_chunk_f32_kernel(const __grid
     scale = 0.f;
     if (tid < 8) {
       const int key = j * kFKeys + 16 * (tid & 3);
-      const int id = key < keys ? __ldg(ids + (key >> lps)) : -1;
+      const int id = key < keys && key >= front ? __ldg(ids + (key >> lps)) : -1;
       if ((uint32_t)id < (uint32_t)c.num_pages) scale = __ldg((tid < 4 ? c.k_scale_d : c.v_scale_d) + (int64_t)id * c.Hkv + g);
     }
   };
